@@ -425,6 +425,124 @@ rz_status rz_swiglu_ffn_static(const float *x, const float *gamma, const void *w
                                int64_t hidden_pad, int64_t inter, float eps, rz_stream stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The paged KV cache in 4 bits.  Three calls serve requests of ragged lengths, any
+ * number of new tokens each (one token, drafted tokens, a prompt chunk):
+ *   rz_paged_plan          once a step: pages, slots, positions and row offsets
+ *   rz_qk_norm_rope        each layer: norm and rotate q and k, append k and v
+ *   rz_attention_paged_q4  each layer: attention over the pages
+ * The new tokens of all requests are packed into rows, request after request.  Lengths,
+ * positions, slots and tables are read from device memory, so that one captured
+ * graph serves every step.
+ *
+ * K and V are held as Q4_0 blocks of 32 values along the head: d = f16 of the value
+ * of largest magnitude (of +a and -a the positive one) divided by -8, clamped to f16's
+ * range; code = round-half-even(x / d) + 8 clamped to 0..15; value = d * (code - 8).
+ * d == 0 gives codes 8; a block with a NaN or an infinity gets d = NaN.  Bytes are laid
+ * out for the kernels (csrc/paged_q4.cuh), 16 tokens of one kv head in a record of
+ * 18 * head_dim bytes.
+ * ---------------------------------------------------------------------------
+ */
+
+/* The cache of one layer: pages holds n_pages * rz_kv_q4_page_bytes(...) bytes, 16-byte
+ * aligned; page_size 16, 32, 64 or 128 tokens; head_dim a multiple of 32 in [32, 256].
+ * Slot = page * page_size + offset names one token's place.  A page needs no
+ * initialisation: tokens beyond a request's length are never used. */
+typedef struct {
+    void *pages;
+    int64_t n_pages;
+    int32_t page_size, n_kv_heads, head_dim;
+} rz_kv_q4;
+
+/* Bytes of one page (0 for arguments outside their range). */
+size_t rz_kv_q4_page_bytes(int32_t page_size, int32_t n_kv_heads, int32_t head_dim);
+
+/*
+ * rz_paged_plan -- page table, slot map, positions and row offsets of one step from the
+ * requests' lengths, in one launch.
+ *   cached  int32 [n_seqs] tokens that each request holds in its pages
+ *   fresh   int32 [n_seqs] its new tokens of this step (0: none); negative: the request
+ *           has ended, and its pages go back to the pool before any are handed out
+ *   owned   int32 [n_seqs] pages each request has: block_table[i][0 .. owned[i])
+ *   free_pages, free_count  the pool: a stack of n_pages entries, the first *free_count of
+ *           them free.  Pages are taken from its top, in order of request and block.
+ *   block_table int32 [n_seqs][ld_table], max_blocks entries of a row in use; the new
+ *           pages are written behind the owned ones, nothing else is changed
+ *   owned_out, free_count_out  the state after the step; each may be its input
+ * Outputs:
+ *   cu_rows   int32 [n_seqs + 1]  rows of request i: cu_rows[i] .. cu_rows[i + 1]
+ *   kv_len    int32 [n_seqs]      cached + fresh; 0 for ended and refused requests (not
+ *             the buffer of cached or fresh).  The next step's cached.
+ *   row_seq, positions int32 [max_rows], slots int64 [max_rows]: the request, position and
+ *             cache slot of each row; -1 in the rows behind the last and, but for
+ *             row_seq, in those of a refused request
+ * Requests are served in order: the first whose new pages the pool does not have is
+ * refused, and so is every later one that needs a page; its rows stay in place, its state
+ * as it was (RZ_ERR_DEVICE from rz_check_device_error, code 0x204).  Refused with
+ * RZ_ERR_DEVICE too: negative lengths, owned outside [0, max_blocks], more tokens
+ * cached than its pages hold or in all than max_blocks pages do, and a request whose rows end
+ * beyond max_rows (it has none).  A page that an ended request returns beyond n_pages
+ * is dropped.
+ * 1 <= n_seqs <= 1024, page_size as above, max_blocks * page_size <= 2^30.
+ */
+rz_status rz_paged_plan(const int32_t *cached, const int32_t *fresh, int32_t n_seqs, const int32_t *owned,
+                        int32_t *owned_out, const int32_t *free_count, int32_t *free_count_out, int32_t *free_pages,
+                        int64_t n_pages, int32_t *block_table, int64_t ld_table, int32_t max_blocks, int32_t page_size,
+                        int64_t max_rows, int32_t *cu_rows, int32_t *kv_len, int32_t *row_seq, int32_t *positions,
+                        int64_t *slots, rz_stream stream);
+
+/*
+ * rz_qk_norm_rope -- for each row: RMSNorm of every head of q and k (q_gamma, k_gamma f32
+ * [head_dim], each NULL for none), rotation by the row's position (angles, theta and
+ * rope_mode as rz_layer_weights), and the append of k and v to the cache at the row's slot.
+ *   q, k, v    f32 rows of n_heads, n_kv_heads, n_kv_heads heads, row strides ld_*
+ *              (parts of one fused Q|K|V output, say); 4-byte aligned
+ *   positions  int32 [n_rows]; a negative one marks a padding row, whose outputs and
+ *              cache stay as they are
+ *   slots      int64 [n_rows]; negative: the row is not appended.  A slot beyond the cache
+ *              records RZ_ERR_DEVICE and is not written.  Slots of one call are distinct.
+ *   kv         the cache, or NULL: q_out and k_out only (v, slots unused, v_out NULL)
+ *   q_out      f32, row stride ld_qo; may be q (with ld_qo == ld_q)
+ *   k_out, v_out f32 [n_rows][n_kv_heads * head_dim] or NULL: with a cache the values as
+ *              it holds them, without one the rotated k
+ * The cache's codes and scales are those of the format evaluated in f64 (the kernel
+ * decides in f32 and works heads that lie next to a border again in f64).
+ */
+rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t ld_k, const float *v, int64_t ld_v,
+                          const float *q_gamma, const float *k_gamma, float eps, const int32_t *positions,
+                          const int64_t *slots, const rz_kv_q4 *kv, int64_t n_rows, int32_t n_heads, int32_t n_kv_heads,
+                          int32_t head_dim, float rope_theta, int32_t rope_mode, float *q_out, int64_t ld_qo,
+                          float *k_out, float *v_out, rz_stream stream);
+
+/*
+ * rz_attention_paged_q4 -- softmax(scale * q k^T) v of each request's new rows over its
+ * pages: row r of request i (r = 0 .. m - 1, m = cu_rows[i + 1] - cu_rows[i]) sees its first
+ * kv_len[i] - m + r + 1 tokens (the new ones are in the cache already); a row that sees
+ * none comes out as zeros.  Query head h reads kv head h / (n_heads / n_kv_heads).
+ *   q          f32 [n_rows] rows of n_heads * head_dim, stride ld_q (a multiple of 4),
+ *              16-byte aligned, |q| < 1e35; rows behind cu_rows[n_seqs] are not read and their outputs not
+ *              written
+ *   block_table int32 [n_seqs][ld_table], max_blocks entries of a row in use
+ *   scale      0 for 1 / sqrt(head_dim)
+ *   att        f32 [n_rows][n_heads * head_dim], or NULL
+ *   att_q8     Q8_1 of n_rows rows of q_pad (n_heads * head_dim rounded up to 256; the O
+ *              projection's input), or NULL
+ *   workspace  rz_attention_paged_q4_workspace_bytes bytes, 16-byte aligned, zero-filled
+ *              once after allocating it (a completed call leaves its counters zero); calls
+ *              that share it must not overlap on the GPU, captured ones among them
+ * Scores and sums are f32-accurate: q and the weights enter as two f16 pieces each, the
+ * codes exactly.  A length, row offset or page outside its range records RZ_ERR_DEVICE:
+ * the request counts as empty (lengths beyond its table, bad row offsets), or its
+ * rows are undefined (a bad page).  1 <= n_seqs <= 1024.
+ */
+size_t rz_attention_paged_q4_workspace_bytes(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+rz_status rz_attention_paged_q4(const float *q, int64_t ld_q, int64_t n_rows, const rz_kv_q4 *kv,
+                                const int32_t *block_table, int64_t ld_table, int32_t max_blocks,
+                                const int32_t *cu_rows, const int32_t *kv_len, int32_t n_seqs, int32_t n_heads,
+                                float scale, float *att, void *att_q8, void *workspace, size_t ws_bytes,
+                                rz_stream stream);
+
+/*
  * rz_check_device_error -- synchronise `stream`, read the device error word of the
  * current device and clear it.  *code_out (nullable) receives the raw code (0 = none).
  * Returns RZ_OK, RZ_ERR_TIMEOUT (a bounded wait ran out) or RZ_ERR_DEVICE (a

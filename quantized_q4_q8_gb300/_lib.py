@@ -62,6 +62,12 @@ class LayerWeightsQ40Struct(C.Structure):
     ]
 
 
+class KvQ4Struct(C.Structure):
+    """rz_kv_q4."""
+    _fields_ = [("pages", _vp), ("n_pages", _i64), ("page_size", _i32), ("n_kv_heads", _i32), ("head_dim", _i32)]
+
+
+_KQP = C.POINTER(KvQ4Struct)
 _LWP = C.POINTER(LayerWeightsStruct)
 _LQP = C.POINTER(LayerWeightsQ40Struct)
 _KVP = C.POINTER(KvCacheStruct)
@@ -98,6 +104,14 @@ SIGNATURES = {
     "rz_decode_layer_q4_0": [_vp, _LQP, _KVP, _vp, _i32, _i64, _vp, _vp, _sz, _vp],
     "rz_decode_layers": [_vp, _LWP, _KVP, _i32, _vp, _i32, _i64, _vp, _vp, _sz, _vp],
     "rz_decode_stack_launches": [_LWP, _i32, _i64, _i32, _i32, _i64],
+    "rz_kv_q4_page_bytes": [_i32, _i32, _i32],
+    "rz_paged_plan": [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _vp,
+                      _vp, _vp],
+    "rz_qk_norm_rope": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _KQP, _i64, _i32, _i32, _i32, _f32,
+                        _i32, _vp, _i64, _vp, _vp, _vp],
+    "rz_attention_paged_q4_workspace_bytes": [_i32, _i32, _i32],
+    "rz_attention_paged_q4": [_vp, _i64, _i64, _KQP, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _sz,
+                              _vp],
     "rz_check_device_error": [_vp, C.POINTER(C.c_uint32)],
     "rz_set_pdl": [C.c_int],
     "rz_debug_stall_next_gemv": [C.c_uint32],
@@ -108,6 +122,7 @@ _RESTYPES = {"rz_last_error": C.c_char_p, "rz_version": C.c_char_p,
              "rz_swiglu_ffn_workspace_bytes": _sz, "rz_attention_workspace_bytes": _sz,
              "rz_decode_layer_workspace_bytes": _sz, "rz_decode_stack_workspace_bytes": _sz,
              "rz_decode_layer_q4_0_workspace_bytes": _sz, "rz_q4k_q8_gemm_workspace_bytes": _sz,
+             "rz_kv_q4_page_bytes": _sz, "rz_attention_paged_q4_workspace_bytes": _sz,
              "rz_decode_stack_launches": C.c_int32}
 
 _lib = None

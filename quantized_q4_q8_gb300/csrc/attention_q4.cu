@@ -1,0 +1,820 @@
+// attention_q4.cu -- attention of each request's new tokens over its pages of the
+// 4-bit KV cache, read as they are held.
+//
+//   row i of a request with m new rows and n held tokens sees tokens j < n - m + i + 1:
+//   att = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j - max)
+//   k_j = d_jb (code - 8) for each block b of 32 values, v_j alike; a row that sees
+//   nothing comes out as zeros.
+//
+// Products.  Codes become f16 integers -8..7, exactly: a nibble ORed into the low bits of
+// 1024 is 1024 + code (high nibbles: 1024 + 16 code), and one packed subtraction or
+// multiply-add takes the rest off, two codes at a time.  (A code left in the low bits alone
+// is a subnormal, exact too and without the subtraction, but the tensor cores align a
+// product by its operands' exponents and not by its size: sums came out at 2^-17.)  q and the
+// weights p * d of V are two f16 pieces each (22 bits), the high pieces in rows 0..7 of an
+// m16n8k16 product and the low ones in rows 8..15, so that one product gives both
+// halves of 8 query rows; sums are f32.  q is scaled by a power of two for each row
+// (exact) so that its pieces fill f16's range.
+//
+// Softmax.  The running maximum M of a row is one of log2(p) + log2 |d of V|, so that the
+// weights p * d that are split stay within f16 (2^7 near the maximum, up to 2^15)
+// whatever the values' scale; the sums are rescaled when a weight would
+// leave that range, by 2^8 over the maximum, and not before.
+//
+// Work.  An item is (request, kv head, up to 8 W query rows: token-major, the group's
+// heads within a token); it reads tiles of W groups of 16 tokens.  All items' tiles,
+// weighted by their cost, are one line that the CTAs (one for each SM) share evenly, so
+// that one long request or many ragged ones load all SMs alike; a CTA whose share ends
+// within an item leaves its sums in the workspace and the CTA that finishes last adds them
+// up, in the order of the tiles (the result does not depend on which one it is).
+// Within a CTA the W consumer warps share a tile: with 8 query rows each takes one
+// group of 16 tokens, with 8 W each takes 8 rows; a producer warp copies records into a
+// ring of stages, a page at a time, with the bulk-copy engine.
+#include <math.h>
+
+#include <algorithm>
+
+#include "mma_f16.cuh"
+#include "paged_q4.cuh"
+#include "rz_common.cuh"
+#include "rz_kernels.h"
+
+namespace rz {
+namespace {
+
+// Consumer warps W: 11 and the producer are 3 warps a scheduler, 168 registers a thread;
+// heads of over 128 values need 255, and 8 warps.
+__host__ __device__ constexpr int consumers(int nb) { return nb <= 4 ? 11 : 7; }
+constexpr float kLazy = 8.0f;  // weights may grow by 2^8 over the running maximum
+constexpr float kBias = 7.0f;  // log2 of a weight p * |d| at the running maximum
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+__device__ __forceinline__ float quad_max(float v)
+{
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v)
+{
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+template <int W>
+__device__ __forceinline__ void consumer_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+}
+
+// Codes - 8 of a word's nibbles 0 and 4 (low) or 1 and 5 (high), as two f16.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w)
+{
+    return hsub2u(lop_and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u);
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w)
+{
+    return hfma2u(lop_and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // / 16 - 72
+}
+
+// ---------------------------------------------------------------- the line of work
+struct Seq {
+    int row0, m, n;  // first row, rows, held tokens
+    int rg;          // query row groups of 8 in an item
+    int items;       // items of one kv head
+};
+
+// Row groups of an item: as few as hold the request's rows, else one for each warp.
+template <int W>
+__device__ __forceinline__ int row_groups(int64_t rows)
+{
+    return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : W == 11 && rows <= 40 ? 5 : W;
+}
+
+template <int W>
+__device__ __forceinline__ Seq read_seq(const PagedAttnArgs &a, int s, bool &bad)
+{
+    const int c0 = a.cu_rows[s], c1 = a.cu_rows[s + 1];
+    const int64_t most = (int64_t)a.max_blocks << (a.kv.page_log + 4);
+    Seq q;
+    q.n = a.kv_len[s];
+    if (c0 < 0 || c1 < c0 || c1 > a.n_rows || q.n > most) bad = true;
+    const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.n_rows;
+    q.row0 = ok ? c0 : 0;
+    q.m = ok ? c1 - c0 : 0;
+    q.n = q.n > most ? 0 : max(q.n, 0);
+    const int64_t rows = (int64_t)q.m * (a.n_heads / a.kv.n_kv_heads);
+    q.rg = row_groups<W>(rows);
+    q.items = static_cast<int>((rows + 8 * q.rg - 1) / (8 * q.rg));
+    return q;
+}
+
+// Tokens that item it of a request sees (its last row's).
+__device__ __forceinline__ int item_tokens(const Seq &q, int group, int it)
+{
+    const int64_t last = min((int64_t)(it + 1) * 8 * q.rg - 1, (int64_t)q.m * group - 1) / group;
+    return max(q.n - q.m + static_cast<int>(last) + 1, 0);
+}
+template <int W>
+__device__ __forceinline__ int item_tiles(const Seq &q, int group, int it)
+{
+    return (item_tokens(q, group, it) + 16 * W - 1) / (16 * W);
+}
+// Cost of a tile and of an item's start and end, in units of a tile of 8 query rows.
+__device__ __forceinline__ int tile_cost(int rg) { return rg; }
+constexpr int kItemCost = 1;
+
+// Where CTA c's share of the line begins.
+__device__ __forceinline__ int64_t share(int64_t total, int c, int ctas) { return total * c / ctas; }
+
+// The parts of items that one CTA works, in order.  Every warp walks its own copy.
+struct Walk {
+    int64_t total, x0, x1;  // the line, this CTA's share of it
+    int64_t at;             // where the current item begins
+    Seq q;
+    int s, h, it;
+    int tokens, tiles, lo, hi;  // the current item's tokens and tiles, the part [lo, hi) of them
+};
+
+template <int W>
+__device__ __forceinline__ int64_t item_span(const Seq &q, int group, int it)
+{
+    return kItemCost + (int64_t)item_tiles<W>(q, group, it) * tile_cost(q.rg);
+}
+// The first tile at or after offset x of an item (kItemCost, then tiles).
+__device__ __forceinline__ int tile_at(int64_t x, int tiles, int cost)
+{
+    if (x <= kItemCost) return 0;
+    const int64_t t = (x - kItemCost + cost - 1) / cost;
+    return t < tiles ? static_cast<int>(t) : tiles;
+}
+
+template <int W>
+__device__ __forceinline__ void load_item(Walk &w, const PagedAttnArgs &a, int group)
+{
+    w.tokens = item_tokens(w.q, group, w.it);
+    w.tiles = (w.tokens + 16 * W - 1) / (16 * W);
+    const int cost = tile_cost(w.q.rg);
+    w.lo = tile_at(w.x0 - w.at, w.tiles, cost);
+    w.hi = tile_at(w.x1 - w.at, w.tiles, cost);
+}
+
+// To the first item of the share.  pre[s]: the line before request s.
+template <int W>
+__device__ __forceinline__ bool walk_begin(Walk &w, const PagedAttnArgs &a, const int64_t *pre, int group)
+{
+    w.total = pre[a.n_seqs];
+    w.x0 = share(w.total, blockIdx.x, gridDim.x);
+    w.x1 = share(w.total, blockIdx.x + 1, gridDim.x);
+    if (w.x0 >= w.x1) return false;
+    int lo = 0, hi = a.n_seqs;  // pre[lo] <= x0 < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= w.x0) lo = mid;
+        else hi = mid;
+    }
+    w.s = lo;
+    bool bad = false;
+    w.q = read_seq<W>(a, w.s, bad);
+    const int64_t head = (pre[lo + 1] - pre[lo]) / a.kv.n_kv_heads;
+    w.h = static_cast<int>((w.x0 - pre[lo]) / head);
+    w.at = pre[lo] + w.h * head;
+    w.it = 0;
+    for (; w.it + 1 < w.q.items; ++w.it) {
+        const int64_t span = item_span<W>(w.q, group, w.it);
+        if (w.at + span > w.x0) break;
+        w.at += span;
+    }
+    load_item<W>(w, a, group);
+    return true;
+}
+template <int W>
+__device__ __forceinline__ bool walk_next(Walk &w, const PagedAttnArgs &a, int group)
+{
+    w.at += item_span<W>(w.q, group, w.it);
+    if (w.at >= w.x1) return false;
+    if (++w.it == w.q.items) {
+        w.it = 0;
+        if (++w.h == a.kv.n_kv_heads) {
+            w.h = 0;
+            bool bad = false;
+            do {
+                if (++w.s >= a.n_seqs) return false;
+                w.q = read_seq<W>(a, w.s, bad);
+            } while (w.q.items == 0);
+        }
+    }
+    load_item<W>(w, a, group);
+    return true;
+}
+// Whether this CTA has something to do for the current item: tiles, or an item without
+// any that begins in its share.
+__device__ __forceinline__ bool walk_has(const Walk &w)
+{
+    return w.lo < w.hi || (w.tiles == 0 && w.at >= w.x0);
+}
+
+// ---------------------------------------------------------------- one warp's sums
+template <int NB>
+struct Warp {
+    uint32_t qa[NB][2][4];  // A fragments: block, low and high half, {a0..a3}
+    float unit;             // log2(e) * scale * the unit of the products
+    float o[NB][4][4];      // sums of V: block, tile (r, nibble), {c0..c3}
+    float m, l;             // running maximum (see the top), sum of p
+};
+
+// The query row of this lane's g: pieces in fragment order.  ptr == nullptr: a row of zeros.
+template <int NB>
+__device__ __forceinline__ void load_query(Warp<NB> &w, const float *ptr, float scale, int t)
+{
+    float4 v[NB][2];
+    float mx = 0.0f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            v[b][hf] = ptr ? __ldg(reinterpret_cast<const float4 *>(ptr + 32 * b + 16 * hf + 4 * t))
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v[b][hf].x), fabsf(v[b][hf].y)),
+                                 fmaxf(fabsf(v[b][hf].z), fabsf(v[b][hf].w))));
+        }
+    mx = quad_max(mx);
+    // 2^up brings the largest value to [2^14, 2^15); powers of two, so exact
+    const int ex = (__float_as_int(mx) >> 23) - 127;
+    const int up = mx == 0.0f ? 0 : min(14 - ex, 126);
+    const float sc = __int_as_float((up + 127) << 23);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const float x[4] = {v[b][hf].x * sc, v[b][hf].z * sc, v[b][hf].y * sc, v[b][hf].w * sc};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t hi = pack_f16(x[2 * k], x[2 * k + 1]);
+                const float2 h = unpack_f16(hi);
+                w.qa[b][hf][2 * k] = hi;                                                      // a0, a2: row g
+                w.qa[b][hf][2 * k + 1] = pack_f16(x[2 * k] - h.x, x[2 * k + 1] - h.y);  // a1, a3: row g + 8
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w.o[b][i][j] = 0.0f;
+    }
+    w.unit = scale * 1.4426950408889634f * __int_as_float((127 - up) << 23);
+    w.m = -1e37f;
+    w.l = 0.0f;
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&r)[N], const uint8_t *p)
+{
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            r[i] = v.x;
+            r[i + 1] = v.y;
+            r[i + 2] = v.z;
+            r[i + 3] = v.w;
+        }
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p + 4 * i);
+            r[i] = v.x;
+            r[i + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const uint32_t *>(p + 4 * i);
+    }
+}
+
+// f16 value i of a run of words
+template <int N>
+__device__ __forceinline__ float half_at(const uint32_t (&w)[N], int i)
+{
+    const float2 v = unpack_f16(w[i >> 1]);
+    return (i & 1) ? v.y : v.x;
+}
+
+// 16 tokens of a record for the warp's 8 query rows.  sees: how many of the 16 this lane's
+// row sees (kMasked), else all.
+template <int NB, bool kMasked>
+__device__ __forceinline__ void tokens16(Warp<NB> &w, const uint8_t *rec, int g, int t, int sees)
+{
+    constexpr int hd = 32 * NB;
+    // ---- scores of tokens 4 t .. 4 t + 3
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    {
+        uint32_t ks[2 * NB];
+        lds_words(ks, rec + q4_k_scale(NB, 4 * t));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            // column n of product j is token 4 (n / 2) + 2 j + n % 2
+            uint32_t kw[NB];
+            lds_words(kw, rec + (4 * (g >> 1) + 2 * j + (g & 1)) * (hd / 2) + t * 4 * NB);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const uint32_t u = kw[b] >> 8;
+                mma16816(c, w.qa[b][0], low_codes(kw[b]), low_codes(u), c);
+                mma16816(c, w.qa[b][1], high_codes(kw[b]), high_codes(u), c);
+                s[2 * j] = fmaf(half_at(ks, (2 * j) * NB + b), c[0] + c[2], s[2 * j]);
+                s[2 * j + 1] = fmaf(half_at(ks, (2 * j + 1) * NB + b), c[1] + c[3], s[2 * j + 1]);
+            }
+        }
+    }
+    uint32_t vs[2 * NB];
+    lds_words(vs, rec + q4_v_scale(NB, 4 * t));
+    if (kMasked) {
+        // what no row may see is whatever the page holds: its score and its scales are dropped
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * t + i >= sees) {
+                s[i] = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int k = i * NB + b;
+                    vs[k >> 1] &= (k & 1) ? 0x0000ffffu : 0xffff0000u;
+                }
+            }
+    }
+    // ---- running maximum of log2 p + log2 |d|
+    uint32_t dm = vs[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 2 * NB; ++i) {
+        const uint32_t v = vs[i] & 0x7fff7fffu;
+        asm("max.f16x2 %0, %0, %1;" : "+r"(dm) : "r"(v));
+    }
+    const float2 dm2 = unpack_f16(dm);
+    // the exponent above the largest |d| (d = 0: that of the smallest f16)
+    const float ev = static_cast<float>((__float_as_int(fmaxf(fmaxf(dm2.x, dm2.y), 0x1p-25f)) >> 23) - 126);
+    const float y = fmaf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), w.unit, ev);
+    if (__any_sync(0xffffffffu, y > w.m + kLazy)) {
+        const float top = quad_max(y);
+        const float m = top > w.m + kLazy ? top : w.m;
+        const float f = ex2(w.m - m);
+        w.m = m;
+        w.l *= f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w.o[b][i][j] *= f;
+        }
+    }
+    float p[4];
+    const float off = kBias - w.m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[i], w.unit, off));
+    w.l += (p[0] + p[1]) + (p[2] + p[3]);
+    // ---- sums of V
+    uint32_t vw[2 * NB];
+    constexpr int run = q4_v_run(NB);
+#pragma unroll
+    for (int r = 0; r < 2 * NB; r += run) {
+        uint32_t part[run];
+        lds_words(part, rec + 9 * hd + ((r / run) * 32 + 4 * g + t) * run * 4);
+#pragma unroll
+        for (int i = 0; i < run; ++i) vw[r + i] = part[i];
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        // weights p * d of tokens (0, 2) and (1, 3), in two pieces
+        const float d0 = half_at(vs, b), d1 = half_at(vs, NB + b), d2 = half_at(vs, 2 * NB + b),
+                    d3 = half_at(vs, 3 * NB + b);
+        const float x0 = p[0] * d0, x1 = p[1] * d1, x2 = p[2] * d2, x3 = p[3] * d3;
+        uint32_t pa[4];
+        pa[0] = pack_f16(x0, x2);
+        pa[2] = pack_f16(x1, x3);
+        const float2 h0 = unpack_f16(pa[0]), h1 = unpack_f16(pa[2]);
+        pa[1] = pack_f16(x0 - h0.x, x2 - h0.y);
+        pa[3] = pack_f16(x1 - h1.x, x3 - h1.y);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t v = vw[2 * b + k], u = v >> 8;
+            mma16816(w.o[b][2 * k], pa, low_codes(v), low_codes(u), w.o[b][2 * k]);
+            mma16816(w.o[b][2 * k + 1], pa, high_codes(v), high_codes(u), w.o[b][2 * k + 1]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- shared memory
+// stages of W records | the warps' sums, their (m, l) | mbarriers, flags (256 bytes) | the line's prefix
+constexpr int kPad = 8;  // floats after a row of sums: its 8 rows fall into other banks
+constexpr int kMaxStages = 10;
+template <int NB>
+struct Layout {
+    static constexpr int W = consumers(NB), hd = 32 * NB, rows = 8 * W;
+    static constexpr int stage = W * q4_record_bytes(hd);
+    static constexpr int sums = rows * (hd + kPad) * 4;
+    static constexpr int fixed = sums + rows * 8 + 256;  // and 8 bytes for each request and one
+    static constexpr int64_t part = (int64_t)rows * (hd + 2);  // floats of a partial record: sums, then (m, l)
+};
+
+// The warps' sums of one item to shared memory: row 8 slot + g of [8 W][hd + kPad].
+template <int NB>
+__device__ __forceinline__ void store_sums(const Warp<NB> &w, float *sums, float2 *ml, int slot, int g, int t)
+{
+    constexpr int ld = 32 * NB + kPad;
+    float *row = sums + (slot * 8 + g) * ld;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // tile k: values 16 (k & 1) + 8 (k >> 1) .. of the block
+            const float(&c)[4] = w.o[b][k];
+            *reinterpret_cast<float2 *>(row + 32 * b + 16 * (k & 1) + 8 * (k >> 1) + 2 * t) =
+                make_float2(c[0] + c[2], c[1] + c[3]);
+        }
+    }
+    const float l = quad_sum(w.l);
+    if (t == 0) ml[slot * 8 + g] = make_float2(w.m, l);
+}
+
+// Four values of one row, divided by its sum, to the outputs.  Every lane of the warp
+// calls it (8 lanes hold a block of 32 values); live: this lane's row exists.
+__device__ __forceinline__ void write_row4(const PagedAttnArgs &a, float4 v, bool live, int64_t row, int col, int q_pad)
+{
+    const int q_dim = a.n_heads * a.kv.head_dim;
+    if (a.att && live) *reinterpret_cast<float4 *>(a.att + row * q_dim + col) = v;
+    if (a.att_q8) {
+        float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float d = __fdiv_rn(mx, 127.0f);
+        const Q8Scale sc = q8_scale(d);
+        const int c0 = q8_code(v.x, sc), c1 = q8_code(v.y, sc), c2 = q8_code(v.z, sc), c3 = q8_code(v.w, sc);
+        int sum = c0 + c1 + c2 + c3;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (live) {
+            int8_t *q = static_cast<int8_t *>(a.att_q8);
+            float *qd = reinterpret_cast<float *>(q + a.n_rows * q_pad);
+            float *qs = qd + a.n_rows * (q_pad / 32);
+            *reinterpret_cast<char4 *>(q + row * q_pad + col) = make_char4(c0, c1, c2, c3);
+            if ((threadIdx.x & 7) == 0) {
+                qd[row * (q_pad / 32) + col / 32] = d;
+                qs[row * (q_pad / 32) + col / 32] = __fmul_rn(d, (float)sum);
+            }
+        }
+    }
+}
+
+template <int NB>
+__global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
+    paged_attention_kernel(const __grid_constant__ PagedAttnArgs a, int stages)
+{
+    using L = Layout<NB>;
+    constexpr int W = L::W, hd = L::hd, ld = hd + kPad, kStage = L::stage;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *ring = smem;
+    float *sums = reinterpret_cast<float *>(ring + (size_t)stages * kStage);
+    float2 *ml = reinterpret_cast<float2 *>(sums + L::sums / 4);
+    uint64_t *full = reinterpret_cast<uint64_t *>(ml + L::rows), *empty = full + kMaxStages;
+    int *flags = reinterpret_cast<int *>(empty + kMaxStages);  // [0] a wait ran out, [1] this CTA adds the parts up
+    int64_t *pre = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(full) + 256);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K = a.kv.n_kv_heads, group = a.n_heads / K;
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, W);
+        }
+        fence_mbar_init();
+        flags[0] = flags[1] = 0;
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // ---- the line: what comes before each request
+    {
+        int64_t *tmp = reinterpret_cast<int64_t *>(sums);
+        const int per = (a.n_seqs + W * 32 - 1) / (W * 32);
+        int64_t mine = 0;
+        bool bad = false;
+        if (tid < W * 32)
+            for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
+                const Seq q = read_seq<W>(a, i, bad);
+                int64_t span = 0;
+                for (int it = 0; it < q.items; ++it) span += item_span<W>(q, group, it);
+                pre[i + 1] = span * K;
+                mine += span * K;
+            }
+        if (bad && blockIdx.x == 0) set_error(a.err, DEV_BAD_LENGTH);
+        int64_t v = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) tmp[warp] = v;
+        __syncthreads();
+        if (tid < W * 32) {
+            for (int k = 0; k < warp; ++k) v += tmp[k];
+            v -= mine;
+            for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
+                v += pre[i + 1];
+                pre[i + 1] = v;
+            }
+        }
+        if (tid == 0) pre[0] = 0;
+        __syncthreads();
+    }
+
+    volatile int *gave_up = flags;
+    Walk w;
+    const bool any = walk_begin<W>(w, a, pre, group);
+    if (!any) return;  // the same for the whole CTA
+
+    if (warp == W) {
+        // ---------------------------------------------------------------- producer
+        const int lg = a.kv.page_log, per_page = 1 << lg;  // groups of 16 tokens in a page
+        const int64_t head_bytes = (int64_t)q4_record_bytes(hd) << lg;
+        RingPos pos{0, 0};
+        int issued = 0;
+        bool more = true;
+        // the step's keys and values were written by another kernel through the generic proxy
+        asm volatile("fence.proxy.async;" ::: "memory");
+        while (more && !*gave_up) {
+            const int32_t *row = a.table + (int64_t)w.s * a.table_ld;
+            for (int tile = w.lo; tile < w.hi; ++tile) {
+                const int t0 = tile * W * 16;
+                const int groups = min(W, (w.tokens - t0 + 15) >> 4);
+                // lane i copies the part of the tile that lies in its i-th page
+                const int first = (t0 >> 4) >> lg;  // page of the tile's first group
+                const int in = (t0 >> 4) & (per_page - 1);
+                const int g0 = lane == 0 ? 0 : (lane << lg) - in, g1 = min(groups, ((lane + 1) << lg) - in);
+                int32_t page = 0;
+                if (g0 < g1) {
+                    page = row[first + lane];
+                    if (page < 0 || page >= a.kv.n_pages) {
+                        set_error(a.err, DEV_BAD_PAGE);
+                        page = 0;  // a page there is; the request's rows are not to be used
+                    }
+                }
+                if (!mbar_wait(empty + pos.s, pos.par ^ 1u)) {
+                    *gave_up = 1;
+                    set_error(a.err, DEV_TIMEOUT_PAGED);
+                }
+                __syncwarp();
+                if (*gave_up) break;
+                uint8_t *dst = ring + (size_t)pos.s * kStage;
+                if (lane == 0) mbar_arrive_expect_tx(full + pos.s, groups * q4_record_bytes(hd));
+                __syncwarp();
+                if (g0 < g1)
+                    bulk_g2s(dst + g0 * q4_record_bytes(hd),
+                             a.kv.pages + ((int64_t)page * K + w.h) * head_bytes +
+                                 (int64_t)(lane == 0 ? in : 0) * q4_record_bytes(hd),
+                             (g1 - g0) * q4_record_bytes(hd), full + pos.s);
+                ++issued;
+                ring_next(pos, stages);
+            }
+            more = walk_next<W>(w, a, group);
+        }
+        // no copy outlives the CTA: after an abort, those that no consumer waits for any more are waited out
+        if (*gave_up) {
+            for (int k = max(0, issued - stages); k < issued; ++k) {
+                const RingPos p = ring_pos(k, stages);
+                if (!mbar_wait(full + p.s, p.par)) set_error(a.err, DEV_TIMEOUT_DRAIN);
+            }
+        }
+        return;
+    }
+
+    // -------------------------------------------------------------------- consumers
+    const int g = lane >> 2, t = lane & 3;
+    const int q_pad = (a.n_heads * hd + 255) / 256 * 256;
+    RingPos pos{0, 0};
+    bool more = true;
+    while (more) {
+        if (walk_has(w)) {
+            // rg row groups, copies warps for each, the others idle
+            const int rg = w.q.rg, copies = W / rg, row_it = w.it * 8 * rg;
+            const int qg = warp % rg, ks = warp / rg;
+            const int row8 = row_it + qg * 8;  // this warp's first query row
+            const int n_rows = w.q.m * group;  // of the request and kv head
+            // this lane's query row, and how many tokens it sees
+            const int my = row8 + g;
+            const int tok = my / group;
+            const bool live = my < n_rows;
+            const int64_t row = w.q.row0 + tok;
+            const int col0 = (w.h * group + (my - tok * group)) * hd;
+            // what it sees, what all of the warp's rows see and what any of them does (rows
+            // beyond the last see what the last sees, and are not written)
+            const int before = w.q.n - w.q.m + 1;
+            const int sees = max(before + min(my, n_rows - 1) / group, 0);
+            const int all_see = max(before + min(row8, n_rows - 1) / group, 0);
+            const int any_see = row8 < n_rows && ks < copies ? max(before + min(row8 + 7, n_rows - 1) / group, 0) : 0;
+            Warp<NB> acc;
+            load_query<NB>(acc, live ? a.q + row * a.ld_q + col0 : nullptr, a.scale, t);
+            for (int tile = w.lo; tile < w.hi; ++tile) {
+                bool ok = __all_sync(0xffffffffu, !*gave_up);
+                if (ok && !__all_sync(0xffffffffu, mbar_wait(full + pos.s, pos.par))) {
+                    ok = false;
+                    *gave_up = 1;
+                    set_error(a.err, DEV_TIMEOUT_PAGED);
+                }
+                if (ok) {
+                    const uint8_t *st = ring + (size_t)pos.s * kStage;
+                    // the first of the tile's groups whose number in the item falls to this warp
+                    const int g0 = tile * W;
+                    for (int gr = copies == W ? ks : (ks + copies - g0 % copies) % copies; gr < W; gr += copies) {
+                        const int t0 = (g0 + gr) * 16;
+                        if (t0 >= any_see) break;
+                        if (t0 + 16 <= all_see)
+                            tokens16<NB, false>(acc, st + gr * q4_record_bytes(hd), g, t, 16);
+                        else
+                            tokens16<NB, true>(acc, st + gr * q4_record_bytes(hd), g, t, sees - t0);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty + pos.s);
+                }
+                ring_next(pos, stages);
+            }
+            // ---- the warps' sums: copy ks of row group qg at slot ks * rg + qg
+            if (ks < copies) store_sums<NB>(acc, sums, ml, ks * rg + qg, g, t);
+            consumer_sync<W>();
+            const int rows_item = min(8 * rg, n_rows - row_it);
+            const bool whole = w.lo == 0 && w.hi == w.tiles;
+            const int quads = 8 * rg * (hd / 4);  // groups of 4 values of the item's rows
+            float *part = a.part + (2 * (int64_t)blockIdx.x + (w.lo == 0)) * L::part;
+            for (int i0 = 0; i0 < quads; i0 += W * 32) {
+                const int i = i0 + tid;
+                const int r = i / (hd / 4), c4 = i % (hd / 4) * 4;
+                const bool mine = i < quads && r < rows_item;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float m = -1e37f, l = 0.0f;
+                if (mine) {
+                    for (int k = 0; k < copies; ++k) m = fmaxf(m, ml[k * 8 * rg + r].x);
+                    for (int k = 0; k < copies; ++k) {
+                        const float2 x = ml[k * 8 * rg + r];
+                        const float f = ex2(x.x - m);
+                        const float4 u = *reinterpret_cast<const float4 *>(sums + (k * 8 * rg + r) * ld + c4);
+                        l = fmaf(x.y, f, l);
+                        v.x = fmaf(u.x, f, v.x);
+                        v.y = fmaf(u.y, f, v.y);
+                        v.z = fmaf(u.z, f, v.z);
+                        v.w = fmaf(u.w, f, v.w);
+                    }
+                }
+                if (whole) {
+                    // l == 0: the row sees nothing.  A NaN stays one.
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    const int my_row = row_it + r;
+                    write_row4(a, v, mine, w.q.row0 + my_row / group, (w.h * group + my_row % group) * hd + c4, q_pad);
+                } else if (mine) {
+                    *reinterpret_cast<float4 *>(part + r * hd + c4) = v;
+                    if (c4 == 0) *reinterpret_cast<float2 *>(part + L::rows * hd + 2 * r) = make_float2(m, l);
+                }
+            }
+            if (!whole) {
+                // ---- the CTAs whose shares hold the item's tiles: the last to arrive adds them up
+                const int cost = tile_cost(rg), ctas = gridDim.x;
+                int c = static_cast<int>(w.at * ctas / w.total);
+                while (c > 0 && share(w.total, c, ctas) > w.at) --c;
+                while (share(w.total, c + 1, ctas) <= w.at) ++c;
+                const int64_t end = w.at + kItemCost + (int64_t)w.tiles * cost;
+                auto tiles_of = [&](int k, int &lo, int &hi) {
+                    lo = tile_at(share(w.total, k, ctas) - w.at, w.tiles, cost);
+                    hi = tile_at(share(w.total, k + 1, ctas) - w.at, w.tiles, cost);
+                };
+                int lo, hi;
+                for (tiles_of(c, lo, hi); lo == hi; tiles_of(c, lo, hi)) ++c;  // the first with a tile
+                int parts = 0;
+                for (int k = c; k < ctas && share(w.total, k, ctas) < end; ++k) {
+                    tiles_of(k, lo, hi);
+                    parts += lo < hi;
+                }
+                __threadfence();
+                consumer_sync<W>();
+                if (tid == 0) {
+                    const int before = atomicAdd(a.counters + c, 1);
+                    flags[1] = before == parts - 1;
+                    if (before == parts - 1) a.counters[c] = 0;
+                }
+                consumer_sync<W>();
+                if (flags[1]) {
+                    __threadfence();
+                    for (int i0 = 0; i0 < quads; i0 += W * 32) {
+                        const int i = i0 + tid;
+                        const int r = i / (hd / 4), c4 = i % (hd / 4) * 4;
+                        const bool mine = i < quads && r < rows_item;
+                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        float m = -1e37f, l = 0.0f;
+                        if (mine) {
+                            for (int k = c, left = parts; left > 0; ++k) {
+                                tiles_of(k, lo, hi);
+                                if (lo == hi) continue;
+                                --left;
+                                const float *pk = a.part + (2 * (int64_t)k + (lo == 0)) * L::part;
+                                const float2 x = __ldcg(reinterpret_cast<const float2 *>(pk + L::rows * hd + 2 * r));
+                                const float4 u = __ldcg(reinterpret_cast<const float4 *>(pk + r * hd + c4));
+                                const float mn = fmaxf(m, x.x), f0 = ex2(m - mn), f1 = ex2(x.x - mn);
+                                m = mn;
+                                l = fmaf(l, f0, x.y * f1);
+                                v.x = fmaf(v.x, f0, u.x * f1);
+                                v.y = fmaf(v.y, f0, u.y * f1);
+                                v.z = fmaf(v.z, f0, u.z * f1);
+                                v.w = fmaf(v.w, f0, u.w * f1);
+                            }
+                        }
+                        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                        v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                        const int my_row = row_it + r;
+                        write_row4(a, v, mine, w.q.row0 + my_row / group, (w.h * group + my_row % group) * hd + c4,
+                                   q_pad);
+                    }
+                }
+            }
+            // the zero padding of the Q8_1 rows, with kv head 0
+            if (a.att_q8 && w.h == 0 && w.lo == 0) {
+                const int q_dim = a.n_heads * hd, pad = q_pad - q_dim;
+                if (pad) {
+                    int8_t *q8 = static_cast<int8_t *>(a.att_q8);
+                    float *qd = reinterpret_cast<float *>(q8 + a.n_rows * q_pad);
+                    float *qs = qd + a.n_rows * (q_pad / 32);
+                    const int r0 = row_it / group;
+                    const int r1 = min(w.q.m, (row_it + rows_item - 1) / group + 1);
+                    for (int i = tid; i < (r1 - r0) * pad; i += W * 32) {
+                        const int64_t rr = w.q.row0 + r0 + i / pad;
+                        const int cc = q_dim + i % pad;
+                        q8[rr * q_pad + cc] = 0;
+                        if (cc % 32 == 0) {
+                            qd[rr * (q_pad / 32) + cc / 32] = 0.0f;
+                            qs[rr * (q_pad / 32) + cc / 32] = 0.0f;
+                        }
+                    }
+                }
+            }
+            consumer_sync<W>();  // sums, ml and the flag are read
+        }
+        more = walk_next<W>(w, a, group);
+    }
+}
+
+template <int NB>
+cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
+{
+    using L = Layout<NB>;
+    const int smem_most = static_cast<int>(dev_info().smem_optin);
+    const int fixed = L::fixed + (a.n_seqs + 1) * 8;
+    const int stages = std::min(kMaxStages, (smem_most - fixed) / L::stage);
+    const int bytes = stages * L::stage + fixed;
+    cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)dev_info().sm_count);
+    cfg.blockDim = dim3((L::W + 1) * 32);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_use_pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, paged_attention_kernel<NB>, a, stages);
+}
+
+}  // namespace
+
+// counters (zero before the first call, zero again after each), then two partial records for each CTA
+size_t paged_attention_workspace_bytes(int head_dim)
+{
+    const size_t ctas = dev_info().sm_count;
+    return (ctas * 4 + 255) / 256 * 256 + 2 * ctas * 8 * consumers(head_dim / 32) * (head_dim + 2) * 4;
+}
+
+cudaError_t launch_paged_attention(const PagedAttnArgs &args, void *workspace, cudaStream_t s)
+{
+    PagedAttnArgs a = args;
+    a.counters = static_cast<int *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ((size_t)dev_info().sm_count * 4 + 255) / 256 * 256);
+    switch (a.kv.head_dim / 32) {
+        case 1: return launch<1>(a, s);
+        case 2: return launch<2>(a, s);
+        case 3: return launch<3>(a, s);
+        case 4: return launch<4>(a, s);
+        case 5: return launch<5>(a, s);
+        case 6: return launch<6>(a, s);
+        case 7: return launch<7>(a, s);
+        default: return launch<8>(a, s);
+    }
+}
+
+}  // namespace rz

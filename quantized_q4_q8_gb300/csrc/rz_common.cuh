@@ -20,9 +20,14 @@ enum DevErr : unsigned {
     DEV_TIMEOUT_Q40 = 0x102,
     DEV_TIMEOUT_ATTN = 0x104,   // the V-row copy wait of the attention kernel gave up
     DEV_TIMEOUT_GEMM = 0x108,   // a wait of the tensor-core many-token GEMM gave up
+    DEV_TIMEOUT_PAGED = 0x110,  // a page copy wait of the paged attention kernel gave up
     DEV_TIMEOUT_DRAIN = 0x1ff,  // draining outstanding copies gave up
     DEV_BAD_POSITION = 0x201,   // a device-resident position outside [0, max_seq)
     DEV_ATTN_GEOMETRY = 0x202,  // an attention work split outgrew its records or tables (skipped)
+    DEV_BAD_LENGTH = 0x203,     // a device-resident length, count or row offset outside its range
+    DEV_NO_PAGES = 0x204,       // the page pool ran out: requests were refused
+    DEV_BAD_SLOT = 0x205,       // a device-resident cache slot beyond the last page
+    DEV_BAD_PAGE = 0x206,       // a page table entry outside [0, n_pages)
 };
 
 __device__ __forceinline__ void set_error(unsigned *err, unsigned code)

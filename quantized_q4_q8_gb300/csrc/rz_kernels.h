@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "paged_q4.cuh"
+
 namespace rz {
 
 // A 2-D tiled tensor map (TMA descriptor) over a row-major array of `rows` rows
@@ -231,5 +233,61 @@ cudaError_t launch_decode_stack(const float *input, const LayerDesc *layers, int
 // vocab: rows of the LM head (with head only)
 int stack_kernel_launches(const LayerDesc *layers, int n_layers, int64_t m, int max_seq, bool head,
                           int64_t vocab);
+
+// ---------------------------------------------------------------- paged 4-bit KV cache
+// Page plan (paged_plan.cu): page table, slot map, positions and row offsets from
+// request lengths.
+struct PlanArgs {
+    const int32_t *cached, *fresh, *owned;
+    const int32_t *free_count;
+    int32_t *owned_out, *free_count_out;
+    int32_t *free_pages, *table;
+    int32_t *cu_rows, *kv_len, *row_seq, *positions;
+    int64_t *slots;
+    int64_t table_ld, n_pages, max_rows;
+    int n_seqs, max_blocks, page_size;
+    unsigned *err;
+};
+constexpr int kPlanMaxSeqs = 1024;
+cudaError_t launch_paged_plan(const PlanArgs &a, cudaStream_t s);
+
+// Norm, rotation and append (qk_norm_rope.cu).  freq and turn are filled by the launcher.
+struct HeadsArgs {
+    const float *q, *k, *v;
+    int64_t ld_q, ld_k, ld_v;
+    const float *q_gamma, *k_gamma;
+    const int32_t *positions;
+    const int64_t *slots;
+    PagedKv kv;  // pages == nullptr: no cache
+    float *q_out, *k_out, *v_out;
+    int64_t ld_qo;
+    int n_heads, n_kv_heads, rope_mode;
+    float eps;
+    unsigned *err;
+    double freq[128];    // theta^(-2i/head_dim)
+    uint64_t turn[128];  // the same as a fraction of a turn for each position, times 2^64
+};
+cudaError_t launch_qk_norm_rope(HeadsArgs &a, int64_t rows, int head_dim, float rope_theta, cudaStream_t s);
+
+// Attention over the pages (attention_q4.cu).
+struct PagedAttnArgs {
+    const float *q;
+    int64_t ld_q, n_rows;
+    PagedKv kv;
+    const int32_t *table;
+    int64_t table_ld;
+    int max_blocks;
+    const int32_t *cu_rows, *kv_len;
+    int n_seqs, n_heads;
+    float scale;
+    float *att;
+    void *att_q8;
+    float *part;
+    int *counters;
+    unsigned *err;
+};
+constexpr int kPagedMaxSeqs = 1024;
+size_t paged_attention_workspace_bytes(int head_dim);
+cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *workspace, cudaStream_t s);
 
 }  // namespace rz

@@ -19,6 +19,8 @@ __all__ = [
     "swiglu_ffn", "rz_swiglu_ffn_static", "attention_workspace_bytes", "attention_decode",
     "decode_layer_workspace_bytes", "decode_layer", "rz_decode_stack", "decode_stack",
     "rz_decode_layers", "decode_layers", "DeviceLayerQ40", "decode_layer_q4_0",
+    "kv_q4_page_bytes", "PagedKVQ4", "PagedPlan", "rz_paged_plan", "paged_plan", "rz_qk_norm_rope", "qk_norm_rope",
+    "rz_attention_paged_q4", "attention_paged_q4_workspace_bytes", "attention_paged_q4",
 ]
 
 
@@ -479,4 +481,214 @@ def decode_layer_q4_0(x, layer: DeviceLayerQ40, kv: "DeviceKV", position=0, posi
         ws = workspace(load().rz_decode_layer_q4_0_workspace_bytes(C.byref(layer.struct), m, kv.max_seq), x.device)
     call("rz_decode_layer_q4_0", _ptr(x), C.byref(layer.struct), C.byref(kv.struct), _ptr(positions), position, m,
          _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
+    return out
+
+
+# ------------------------------------------------------------------ paged 4-bit KV cache
+def kv_q4_page_bytes(page_size: int, n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page of the 4-bit cache."""
+    n = int(load().rz_kv_q4_page_bytes(page_size, n_kv_heads, head_dim))
+    if n == 0:
+        raise ValueError(load().rz_last_error().decode())
+    return n
+
+
+def _on_device(t, dtype, name, dim=None):
+    """A tensor of the current device, of this type (and number of dimensions)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if dim is not None and t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimension{'s' if dim > 1 else ''}, got {t.dim()}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return t
+
+
+def _vector(t, dtype, n, name):
+    _on_device(t, dtype, name, 1)
+    if t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be {n} contiguous values")
+    return t
+
+
+def _row_ld(t, cols, name):
+    """Row stride of a 2-D tensor of `cols` contiguous columns."""
+    if t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must have {cols} contiguous columns")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+
+
+def _new(shape, dtype, device, stream):
+    """An output allocated for the stream that the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class PagedKVQ4:
+    """The 4-bit K and V cache of one layer: a uint8 CUDA tensor of pages
+    [n_pages, n_kv_heads, page_size * head_dim * 9 / 8] and its C descriptor."""
+
+    def __init__(self, pages, page_size: int, head_dim: int):
+        import torch
+        from ._lib import KvQ4Struct
+        _on_device(pages, torch.uint8, "pages", 3)
+        n_pages, n_kv_heads, size = pages.shape
+        if not pages.is_contiguous() or n_pages < 1 or size * n_kv_heads != kv_q4_page_bytes(page_size, n_kv_heads, head_dim):
+            raise ValueError("pages must be contiguous [n_pages, n_kv_heads, page_size * head_dim * 9 / 8]")
+        self.pages, self.page_size, self.n_kv_heads, self.head_dim = pages, page_size, n_kv_heads, head_dim
+        self.struct = KvQ4Struct(pages.data_ptr(), n_pages, page_size, n_kv_heads, head_dim)
+        self.ref = C.byref(self.struct)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
+        import torch
+        size = kv_q4_page_bytes(page_size, n_kv_heads, head_dim) // n_kv_heads
+        return cls(torch.empty((n_pages, n_kv_heads, size), dtype=torch.uint8, device=device), page_size, head_dim)
+
+
+class PagedPlan:
+    """The outputs of paged_plan for n_seqs requests and up to max_rows new tokens: cu_rows,
+    kv_len, row_seq, positions (int32) and slots (int64), kept from step to step."""
+
+    def __init__(self, n_seqs: int, max_rows: int, device="cuda"):
+        import torch
+        self.n_seqs, self.max_rows = n_seqs, max_rows
+        self.cu_rows = torch.zeros(n_seqs + 1, dtype=torch.int32, device=device)
+        self.kv_len = torch.zeros(n_seqs, dtype=torch.int32, device=device)
+        self.row_seq = torch.full((max_rows,), -1, dtype=torch.int32, device=device)
+        self.positions = torch.full((max_rows,), -1, dtype=torch.int32, device=device)
+        self.slots = torch.full((max_rows,), -1, dtype=torch.int64, device=device)
+
+
+def rz_paged_plan(cached, fresh, n_seqs, owned, owned_out, free_count, free_count_out, free_pages, n_pages, block_table,
+                  ld_table, max_blocks, page_size, max_rows, cu_rows, kv_len, row_seq, positions, slots, stream=None):
+    return call("rz_paged_plan", _ptr(cached), _ptr(fresh), n_seqs, _ptr(owned), _ptr(owned_out), _ptr(free_count),
+                _ptr(free_count_out), _ptr(free_pages), n_pages, _ptr(block_table), ld_table, max_blocks, page_size,
+                max_rows, _ptr(cu_rows), _ptr(kv_len), _ptr(row_seq), _ptr(positions), _ptr(slots), _stream(stream))
+
+
+def paged_plan(cached, fresh, block_table, owned, free_pages, free_count, page_size: int, out: PagedPlan, owned_out=None,
+               free_count_out=None, stream=None) -> PagedPlan:
+    """Pages, slots, positions and row offsets of one step (see rz.h), into `out`.
+
+    cached, fresh, owned int32 [n]; block_table int32 [n, max_blocks]; free_pages int32
+    [n_pages] and free_count int32 [1]: the pool.  owned and free_count are updated in
+    place unless owned_out / free_count_out take the new state."""
+    import torch
+    i32 = torch.int32
+    n = out.n_seqs
+    _on_device(block_table, i32, "block_table", 2)
+    if block_table.shape[0] != n:
+        raise ValueError(f"block_table must have {n} rows")
+    _on_device(free_pages, i32, "free_pages", 1)
+    _on_device(out.slots, torch.int64, "out", 1)
+    owned_out = owned if owned_out is None else owned_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    for name, t, k in (("cached", cached, n), ("fresh", fresh, n), ("owned", owned, n), ("owned_out", owned_out, n),
+                       ("free_count", free_count, 1), ("free_count_out", free_count_out, 1),
+                       ("free_pages", free_pages, free_pages.shape[0])):
+        _vector(t, i32, k, name)
+    rz_paged_plan(cached, fresh, n, owned, owned_out, free_count, free_count_out, free_pages, free_pages.shape[0],
+                  block_table, _row_ld(block_table, block_table.shape[1], "block_table"), block_table.shape[1], page_size,
+                  out.max_rows, out.cu_rows, out.kv_len, out.row_seq, out.positions, out.slots, stream)
+    return out
+
+
+def rz_qk_norm_rope(q, ld_q, k, ld_k, v, ld_v, q_gamma, k_gamma, eps, positions, slots, kv, n_rows, n_heads, n_kv_heads,
+                    head_dim, rope_theta, rope_mode, q_out, ld_qo, k_out, v_out, stream=None):
+    return call("rz_qk_norm_rope", _ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, _ptr(q_gamma), _ptr(k_gamma), eps,
+                _ptr(positions), _ptr(slots), None if kv is None else kv.ref, n_rows, n_heads, n_kv_heads, head_dim,
+                rope_theta, rope_mode, _ptr(q_out), ld_qo, _ptr(k_out), _ptr(v_out), _stream(stream))
+
+
+def qk_norm_rope(q, k, v, positions, n_heads: int, n_kv_heads: int, head_dim: int, rope_theta: float, rope_mode: int,
+                 q_gamma=None, k_gamma=None, eps: float = 1e-6, kv: PagedKVQ4 = None, slots=None, q_out=None,
+                 want_k: bool = False, want_v: bool = False, stream=None):
+    """Norm each head of q and k (f32 [n, heads * head_dim], rows may be strided), rotate them,
+    and append k and v to the cache `kv` at `slots` (see rz.h).  Returns (q, k, v): k and
+    v as the cache holds them when asked for (else None); without a cache k is the rotated k."""
+    import torch
+    f32 = torch.float32
+    n = _on_device(q, f32, "q", 2).shape[0]
+    _on_device(k, f32, "k", 2)
+    q_dim, kv_dim = n_heads * head_dim, n_kv_heads * head_dim
+    ld_q, ld_k, ld_v = _row_ld(q, q_dim, "q"), _row_ld(k, kv_dim, "k"), kv_dim
+    if kv is None:
+        if want_v or slots is not None:
+            raise ValueError("slots and want_v need a cache")
+        v, want_k = None, True
+    else:
+        _on_device(v, f32, "v", 2)
+        ld_v = _row_ld(v, kv_dim, "v")
+        _vector(slots, torch.int64, slots.shape[0], "slots")
+        if v.shape[0] != n or slots.shape[0] < n:
+            raise ValueError("v and slots must have a row for each of q")
+        _on_device(kv.pages, torch.uint8, "kv")
+    _vector(positions, torch.int32, positions.shape[0], "positions")
+    if k.shape[0] != n or positions.shape[0] < n:
+        raise ValueError("k and positions must have a row for each of q")
+    for name, t in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+        if t is not None:
+            _vector(t, f32, head_dim, name)
+    if q_out is None:
+        q_out = _new((n, q_dim), f32, q.device, stream)
+    elif _on_device(q_out, f32, "q_out", 2).shape[0] != n:
+        raise ValueError("q_out must have a row for each of q")
+    k_out = _new((n, kv_dim), f32, q.device, stream) if want_k else None
+    v_out = _new((n, kv_dim), f32, q.device, stream) if want_v else None
+    rz_qk_norm_rope(q, ld_q, k, ld_k, v, ld_v, q_gamma, k_gamma, eps, positions, slots, kv, n, n_heads, n_kv_heads,
+                    head_dim, rope_theta, rope_mode, q_out, _row_ld(q_out, q_dim, "q_out"), k_out, v_out, stream)
+    return q_out, k_out, v_out
+
+
+def rz_attention_paged_q4(q, ld_q, n_rows, kv, block_table, ld_table, max_blocks, cu_rows, kv_len, n_seqs, n_heads, scale,
+                          att, att_q8, ws, ws_bytes, stream=None):
+    return call("rz_attention_paged_q4", _ptr(q), ld_q, n_rows, kv.ref, _ptr(block_table), ld_table, max_blocks,
+                _ptr(cu_rows), _ptr(kv_len), n_seqs, n_heads, scale, _ptr(att), _ptr(att_q8), _ptr(ws), ws_bytes,
+                _stream(stream))
+
+
+def attention_paged_q4_workspace_bytes(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(load().rz_attention_paged_q4_workspace_bytes(n_heads, n_kv_heads, head_dim))
+
+
+def attention_paged_q4(q, kv: PagedKVQ4, block_table, cu_rows, kv_len, n_heads: int, scale: float = 0.0, out=None, ws=None,
+                       att_q8=None, stream=None):
+    """Attention of each request's new rows of q (f32 [n_rows, n_heads * head_dim]) over its
+    pages (see rz.h); returns f32 [n_rows, n_heads * head_dim] (rows behind the last request's as
+    they were in `out`).  att_q8: a uint8 tensor of q8_1_size(n_rows, q_pad) for the Q8_1 form."""
+    import torch
+    i32 = torch.int32
+    n_rows = _on_device(q, torch.float32, "q", 2).shape[0]
+    q_dim = n_heads * kv.head_dim
+    ld_q = _row_ld(q, q_dim, "q")
+    _on_device(kv.pages, torch.uint8, "kv")
+    n = _on_device(block_table, i32, "block_table", 2).shape[0]
+    _vector(cu_rows, i32, n + 1, "cu_rows")
+    _vector(kv_len, i32, n, "kv_len")
+    if out is None:
+        out = _new((n_rows, q_dim), torch.float32, q.device, stream)
+    elif _on_device(out, torch.float32, "out", 2).shape != (n_rows, q_dim) or not out.is_contiguous():
+        raise ValueError("out must be contiguous, with the shape of q")
+    if att_q8 is not None and _on_device(att_q8, torch.uint8, "att_q8", 1).shape[0] < q8_1_size(n_rows, -(-q_dim // 256) * 256):
+        raise ValueError("att_q8 is too small")
+    if ws is None:
+        size = attention_paged_q4_workspace_bytes(n_heads, kv.n_kv_heads, kv.head_dim)
+        ws = _new((max(size, 16),), torch.uint8, q.device, stream)
+        if stream is None:
+            ws.zero_()
+        else:
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+                ws.zero_()
+    rz_attention_paged_q4(q, ld_q, n_rows, kv, block_table, _row_ld(block_table, block_table.shape[1], "block_table"),
+                          block_table.shape[1], cu_rows, kv_len, n, n_heads, scale, out, att_q8, _on_device(ws, torch.uint8, "ws", 1),
+                          ws.numel(), stream)
     return out
