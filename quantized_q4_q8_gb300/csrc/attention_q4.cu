@@ -23,7 +23,7 @@
 //
 // Work.  An item is (request, kv head, up to 8 W query rows: token-major, the group's
 // heads within a token); it reads tiles of W groups of 16 tokens.  All items' tiles,
-// weighted by their cost, are one line that the CTAs (one for each SM) share evenly, so
+// weighted by their cost, are one line that the CTAs (two for each SM) share evenly, so
 // that one long request or many ragged ones load all SMs alike; a CTA whose share ends
 // within an item leaves its sums in the workspace and the CTA that finishes last adds them
 // up, in the order of the tiles (the result does not depend on which one it is).
@@ -42,9 +42,10 @@
 namespace rz {
 namespace {
 
-// Consumer warps W: 11 and the producer are 3 warps a scheduler, 168 registers a thread;
-// heads of over 128 values need 255, and 8 warps.
-__host__ __device__ constexpr int consumers(int nb) { return nb <= 4 ? 11 : 7; }
+// Consumer warps W of a CTA, two CTAs on an SM: 5 and a producer are 3 warps a scheduler, 168
+// registers a thread; heads of over 128 values need 255, and 3 and a producer.
+__host__ __device__ constexpr int consumers(int nb) { return nb <= 4 ? 5 : 3; }
+constexpr int kFlush = 32;  // groups of 16 tokens summed in the tensor cores' accumulators at a time
 constexpr float kLazy = 8.0f;  // weights may grow by 2^8 over the running maximum
 constexpr float kBias = 7.0f;  // log2 of a weight p * |d| at the running maximum
 
@@ -100,7 +101,7 @@ struct Seq {
 template <int W>
 __device__ __forceinline__ int row_groups(int64_t rows)
 {
-    return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : W == 11 && rows <= 40 ? 5 : W;
+    return rows <= 8 ? 1 : rows <= 16 && W > 3 ? 2 : W;
 }
 
 template <int W>
@@ -132,17 +133,34 @@ __device__ __forceinline__ int item_tiles(const Seq &q, int group, int it)
 {
     return (item_tokens(q, group, it) + 16 * W - 1) / (16 * W);
 }
-// Cost of a tile and of an item's start and end, in units of a tile of 8 query rows.
-__device__ __forceinline__ int tile_cost(int rg) { return rg; }
-constexpr int kItemCost = 1;
+// Cost of a tile, and of an item's start and end, in halves of a tile of 8 query rows.
+__device__ __forceinline__ int tile_cost(int rg) { return rg == 1 ? 2 : rg == 2 ? 5 : 2 * rg; }
+constexpr int kItemCost = 4;
 
-// Where CTA c's share of the line begins.
-__device__ __forceinline__ int64_t share(int64_t total, int c, int ctas) { return total * c / ctas; }
+// The line, shared by as many CTAs as have a tile each: CTA c's share begins at
+// c * step + c * rest / ctas.
+struct Line {
+    int64_t total, step;
+    int ctas, rest;
+    __device__ __forceinline__ int64_t begin(int c) const
+    {
+        return c * step + static_cast<unsigned>(c * rest) / static_cast<unsigned>(ctas);
+    }
+};
+__device__ __forceinline__ Line make_line(int64_t total, int grid)
+{
+    Line l;
+    l.total = total;
+    l.ctas = total < 2 * (int64_t)grid ? max(1, static_cast<int>(total) / 2) : grid;
+    l.step = total < (1ll << 31) ? static_cast<unsigned>(total) / static_cast<unsigned>(l.ctas) : total / l.ctas;
+    l.rest = static_cast<int>(total - l.step * l.ctas);
+    return l;
+}
 
 // The parts of items that one CTA works, in order.  Every warp walks its own copy.
 struct Walk {
-    int64_t total, x0, x1;  // the line, this CTA's share of it
-    int64_t at;             // where the current item begins
+    int64_t x0, x1;  // this CTA's share of the line
+    int64_t at;      // where the current item begins
     Seq q;
     int s, h, it;
     int tokens, tiles, lo, hi;  // the current item's tokens and tiles, the part [lo, hi) of them
@@ -157,8 +175,8 @@ __device__ __forceinline__ int64_t item_span(const Seq &q, int group, int it)
 __device__ __forceinline__ int tile_at(int64_t x, int tiles, int cost)
 {
     if (x <= kItemCost) return 0;
-    const int64_t t = (x - kItemCost + cost - 1) / cost;
-    return t < tiles ? static_cast<int>(t) : tiles;
+    if (x >= kItemCost + (int64_t)tiles * cost) return tiles;
+    return static_cast<unsigned>(x - kItemCost + cost - 1) / static_cast<unsigned>(cost);
 }
 
 template <int W>
@@ -173,11 +191,11 @@ __device__ __forceinline__ void load_item(Walk &w, const PagedAttnArgs &a, int g
 
 // To the first item of the share.  pre[s]: the line before request s.
 template <int W>
-__device__ __forceinline__ bool walk_begin(Walk &w, const PagedAttnArgs &a, const int64_t *pre, int group)
+__device__ __forceinline__ bool walk_begin(Walk &w, const PagedAttnArgs &a, const Line &line, const int64_t *pre, int group)
 {
-    w.total = pre[a.n_seqs];
-    w.x0 = share(w.total, blockIdx.x, gridDim.x);
-    w.x1 = share(w.total, blockIdx.x + 1, gridDim.x);
+    if (line.total == 0 || blockIdx.x >= line.ctas) return false;
+    w.x0 = line.begin(blockIdx.x);
+    w.x1 = line.begin(blockIdx.x + 1);
     if (w.x0 >= w.x1) return false;
     int lo = 0, hi = a.n_seqs;  // pre[lo] <= x0 < pre[hi]
     while (hi - lo > 1) {
@@ -188,8 +206,15 @@ __device__ __forceinline__ bool walk_begin(Walk &w, const PagedAttnArgs &a, cons
     w.s = lo;
     bool bad = false;
     w.q = read_seq<W>(a, w.s, bad);
-    const int64_t head = (pre[lo + 1] - pre[lo]) / a.kv.n_kv_heads;
-    w.h = static_cast<int>((w.x0 - pre[lo]) / head);
+    const int64_t span = pre[lo + 1] - pre[lo], in = w.x0 - pre[lo];
+    int64_t head;
+    if (span < (1ll << 31)) {
+        head = static_cast<unsigned>(span) / static_cast<unsigned>(a.kv.n_kv_heads);
+        w.h = static_cast<unsigned>(in) / static_cast<unsigned>(head);
+    } else {
+        head = span / a.kv.n_kv_heads;
+        w.h = static_cast<int>(in / head);
+    }
     w.at = pre[lo] + w.h * head;
     w.it = 0;
     for (; w.it + 1 < w.q.items; ++w.it) {
@@ -233,7 +258,43 @@ struct Warp {
     float unit;             // log2(e) * scale * the unit of the products
     float o[NB][4][4];      // sums of V: block, tile (r, nibble), {c0..c3}
     float m, l;             // running maximum (see the top), sum of p
+    float *row;             // this lane's row of sums in shared memory
+    int since;              // groups of tokens in o
+    bool flushed;           // part of the sums is in row
 };
+
+// Visits the lane's sums: f(the two of a tile, their place in the row).
+template <int NB, typename F>
+__device__ __forceinline__ void each_sum(Warp<NB> &w, int t, F f)
+{
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // tile k: values 16 (k & 1) + 8 (k >> 1) .. of the block
+            f(w.o[b][k], reinterpret_cast<float2 *>(w.row + 32 * b + 16 * (k & 1) + 8 * (k >> 1) + 2 * t));
+}
+
+// The sums to shared memory, high and low pieces together.  The tensor cores cut what they
+// add to an accumulator instead of rounding it, so that a sum of n steps drifts towards zero by
+// up to n / 2 steps of 2^-24: 3.6e-6 after 4000 tokens.  Every kFlush groups the sums are
+// added to those in shared memory instead, rounded.
+template <int NB>
+__device__ __forceinline__ void flush(Warp<NB> &w, int t)
+{
+    const bool more = w.flushed;
+    each_sum(w, t, [&](float(&c)[4], float2 *p) {
+        float2 v = make_float2(c[0] + c[2], c[1] + c[3]);
+        if (more) {
+            const float2 u = *p;
+            v.x += u.x;
+            v.y += u.y;
+        }
+        *p = v;
+        c[0] = c[1] = c[2] = c[3] = 0.0f;
+    });
+    w.flushed = true;
+    w.since = 0;
+}
 
 // The query row of this lane's g: pieces in fragment order.  ptr == nullptr: a row of zeros.
 template <int NB>
@@ -276,6 +337,8 @@ __device__ __forceinline__ void load_query(Warp<NB> &w, const float *ptr, float 
     w.unit = scale * 1.4426950408889634f * __int_as_float((127 - up) << 23);
     w.m = -1e37f;
     w.l = 0.0f;
+    w.since = 0;
+    w.flushed = false;
 }
 
 template <int N>
@@ -377,6 +440,11 @@ __device__ __forceinline__ void tokens16(Warp<NB> &w, const uint8_t *rec, int g,
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w.o[b][i][j] *= f;
         }
+        if (w.flushed)
+            each_sum(w, t, [&](float(&)[4], float2 *p) {
+                const float2 u = *p;
+                *p = make_float2(u.x * f, u.y * f);
+            });
     }
     float p[4];
     const float off = kBias - w.m;
@@ -415,36 +483,19 @@ __device__ __forceinline__ void tokens16(Warp<NB> &w, const uint8_t *rec, int g,
 }
 
 // ---------------------------------------------------------------- shared memory
-// stages of W records | the warps' sums, their (m, l) | mbarriers, flags (256 bytes) | the line's prefix
+// stages of W records | the warps' sums, their (m, l) | mbarriers, flags, counts (256 bytes) |
+// the parts of an item | the line's prefix
 constexpr int kPad = 8;  // floats after a row of sums: its 8 rows fall into other banks
 constexpr int kMaxStages = 10;
+constexpr int kMaxCtas = 512;  // of the grid
 template <int NB>
 struct Layout {
     static constexpr int W = consumers(NB), hd = 32 * NB, rows = 8 * W;
     static constexpr int stage = W * q4_record_bytes(hd);
     static constexpr int sums = rows * (hd + kPad) * 4;
-    static constexpr int fixed = sums + rows * 8 + 256;  // and 8 bytes for each request and one
+    static constexpr int fixed = sums + rows * 8 + 256 + kMaxCtas * 2;  // and 8 bytes for each request and one
     static constexpr int64_t part = (int64_t)rows * (hd + 2);  // floats of a partial record: sums, then (m, l)
 };
-
-// The warps' sums of one item to shared memory: row 8 slot + g of [8 W][hd + kPad].
-template <int NB>
-__device__ __forceinline__ void store_sums(const Warp<NB> &w, float *sums, float2 *ml, int slot, int g, int t)
-{
-    constexpr int ld = 32 * NB + kPad;
-    float *row = sums + (slot * 8 + g) * ld;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // tile k: values 16 (k & 1) + 8 (k >> 1) .. of the block
-            const float(&c)[4] = w.o[b][k];
-            *reinterpret_cast<float2 *>(row + 32 * b + 16 * (k & 1) + 8 * (k >> 1) + 2 * t) =
-                make_float2(c[0] + c[2], c[1] + c[3]);
-        }
-    }
-    const float l = quad_sum(w.l);
-    if (t == 0) ml[slot * 8 + g] = make_float2(w.m, l);
-}
 
 // Four values of one row, divided by its sum, to the outputs.  Every lane of the warp
 // calls it (8 lanes hold a block of 32 values); live: this lane's row exists.
@@ -476,7 +527,7 @@ __device__ __forceinline__ void write_row4(const PagedAttnArgs &a, float4 v, boo
 }
 
 template <int NB>
-__global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
+__global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
     paged_attention_kernel(const __grid_constant__ PagedAttnArgs a, int stages)
 {
     using L = Layout<NB>;
@@ -487,7 +538,9 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
     float2 *ml = reinterpret_cast<float2 *>(sums + L::sums / 4);
     uint64_t *full = reinterpret_cast<uint64_t *>(ml + L::rows), *empty = full + kMaxStages;
     int *flags = reinterpret_cast<int *>(empty + kMaxStages);  // [0] a wait ran out, [1] this CTA adds the parts up
-    int64_t *pre = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(full) + 256);
+    int *part_count = flags + 2;  // W
+    int16_t *part_list = reinterpret_cast<int16_t *>(reinterpret_cast<uint8_t *>(full) + 256);
+    int64_t *pre = reinterpret_cast<int64_t *>(part_list + kMaxCtas);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = a.kv.n_kv_heads, group = a.n_heads / K;
     if (tid == 0) {
@@ -538,7 +591,8 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
 
     volatile int *gave_up = flags;
     Walk w;
-    const bool any = walk_begin<W>(w, a, pre, group);
+    const Line line = make_line(pre[a.n_seqs], gridDim.x);
+    const bool any = walk_begin<W>(w, a, line, pre, group);
     if (!any) return;  // the same for the whole CTA
 
     if (warp == W) {
@@ -621,6 +675,8 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
             const int all_see = max(before + min(row8, n_rows - 1) / group, 0);
             const int any_see = row8 < n_rows && ks < copies ? max(before + min(row8 + 7, n_rows - 1) / group, 0) : 0;
             Warp<NB> acc;
+            const int slot = (ks * rg + qg) * 8 + g;  // of this lane's row, copy ks
+            acc.row = sums + slot * ld;
             load_query<NB>(acc, live ? a.q + row * a.ld_q + col0 : nullptr, a.scale, t);
             for (int tile = w.lo; tile < w.hi; ++tile) {
                 bool ok = __all_sync(0xffffffffu, !*gave_up);
@@ -640,14 +696,19 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
                             tokens16<NB, false>(acc, st + gr * q4_record_bytes(hd), g, t, 16);
                         else
                             tokens16<NB, true>(acc, st + gr * q4_record_bytes(hd), g, t, sees - t0);
+                        if (++acc.since == kFlush) flush(acc, t);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(empty + pos.s);
                 }
                 ring_next(pos, stages);
             }
-            // ---- the warps' sums: copy ks of row group qg at slot ks * rg + qg
-            if (ks < copies) store_sums<NB>(acc, sums, ml, ks * rg + qg, g, t);
+            // ---- the warps' sums
+            if (ks < copies) {
+                flush(acc, t);
+                const float l = quad_sum(acc.l);
+                if (t == 0) ml[slot] = make_float2(acc.m, l);
+            }
             consumer_sync<W>();
             const int rows_item = min(8 * rg, n_rows - row_it);
             const bool whole = w.lo == 0 && w.hi == w.tiles;
@@ -684,29 +745,36 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
                 }
             }
             if (!whole) {
-                // ---- the CTAs whose shares hold the item's tiles: the last to arrive adds them up
-                const int cost = tile_cost(rg), ctas = gridDim.x;
-                int c = static_cast<int>(w.at * ctas / w.total);
-                while (c > 0 && share(w.total, c, ctas) > w.at) --c;
-                while (share(w.total, c + 1, ctas) <= w.at) ++c;
-                const int64_t end = w.at + kItemCost + (int64_t)w.tiles * cost;
-                auto tiles_of = [&](int k, int &lo, int &hi) {
-                    lo = tile_at(share(w.total, k, ctas) - w.at, w.tiles, cost);
-                    hi = tile_at(share(w.total, k + 1, ctas) - w.at, w.tiles, cost);
-                };
-                int lo, hi;
-                for (tiles_of(c, lo, hi); lo == hi; tiles_of(c, lo, hi)) ++c;  // the first with a tile
+                // ---- the CTAs whose shares hold the item's tiles, in order; the last to arrive adds them up
+                const int cost = tile_cost(rg);
+                int c = static_cast<int>(w.at / max(line.step, (int64_t)1));  // at or after the CTA that holds w.at
+                c = min(c, line.ctas - 1);
+                while (line.begin(c) > w.at) --c;
                 int parts = 0;
-                for (int k = c; k < ctas && share(w.total, k, ctas) < end; ++k) {
-                    tiles_of(k, lo, hi);
-                    parts += lo < hi;
+                for (int c0 = c; c0 < line.ctas; c0 += W * 32) {
+                    const int k = c0 + tid;
+                    const int lo = tile_at(line.begin(k) - w.at, w.tiles, cost), hi = tile_at(line.begin(k + 1) - w.at, w.tiles, cost);
+                    const unsigned has = __ballot_sync(0xffffffffu, k < line.ctas && lo < hi);
+                    consumer_sync<W>();  // the counts of the round before are read
+                    if (lane == 0) part_count[warp] = __popc(has);
+                    consumer_sync<W>();
+                    int before = parts;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        if (i < warp) before += part_count[i];
+                        parts += part_count[i];
+                    }
+                    // 2 k + 1: its part begins the item
+                    if (has >> lane & 1) part_list[before + __popc(has & ((1u << lane) - 1))] = static_cast<int16_t>(2 * k + (lo == 0));
+                    if (line.begin(min(c0 + W * 32, line.ctas)) >= w.at + kItemCost + (int64_t)w.tiles * cost) break;
                 }
                 __threadfence();
                 consumer_sync<W>();
                 if (tid == 0) {
-                    const int before = atomicAdd(a.counters + c, 1);
+                    int *counter = a.counters + (part_list[0] >> 1);
+                    const int before = atomicAdd(counter, 1);
                     flags[1] = before == parts - 1;
-                    if (before == parts - 1) a.counters[c] = 0;
+                    if (before == parts - 1) *counter = 0;
                 }
                 consumer_sync<W>();
                 if (flags[1]) {
@@ -718,11 +786,9 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
                         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         float m = -1e37f, l = 0.0f;
                         if (mine) {
-                            for (int k = c, left = parts; left > 0; ++k) {
-                                tiles_of(k, lo, hi);
-                                if (lo == hi) continue;
-                                --left;
-                                const float *pk = a.part + (2 * (int64_t)k + (lo == 0)) * L::part;
+#pragma unroll 4
+                            for (int k = 0; k < parts; ++k) {
+                                const float *pk = a.part + part_list[k] * L::part;
                                 const float2 x = __ldcg(reinterpret_cast<const float2 *>(pk + L::rows * hd + 2 * r));
                                 const float4 u = __ldcg(reinterpret_cast<const float4 *>(pk + r * hd + c4));
                                 const float mn = fmaxf(m, x.x), f0 = ex2(m - mn), f1 = ex2(x.x - mn);
@@ -737,8 +803,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
                         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                         v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
                         const int my_row = row_it + r;
-                        write_row4(a, v, mine, w.q.row0 + my_row / group, (w.h * group + my_row % group) * hd + c4,
-                                   q_pad);
+                        write_row4(a, v, mine, w.q.row0 + my_row / group, (w.h * group + my_row % group) * hd + c4, q_pad);
                     }
                 }
             }
@@ -768,18 +833,21 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 1)
     }
 }
 
+int grid_ctas() { return std::min(2 * dev_info().sm_count, kMaxCtas); }
+
 template <int NB>
 cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
 {
     using L = Layout<NB>;
-    const int smem_most = static_cast<int>(dev_info().smem_optin);
+    // half an SM's shared memory (228 KB, 1 KB of it for each CTA), as many stages as fit
+    const int most = 113 * 1024;
     const int fixed = L::fixed + (a.n_seqs + 1) * 8;
-    const int stages = std::min(kMaxStages, (smem_most - fixed) / L::stage);
+    const int stages = std::min(kMaxStages, (most - fixed) / L::stage);
     const int bytes = stages * L::stage + fixed;
-    cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most);
+    cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)dev_info().sm_count);
+    cfg.gridDim = dim3((unsigned)grid_ctas());
     cfg.blockDim = dim3((L::W + 1) * 32);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = s;
@@ -796,7 +864,7 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
 // counters (zero before the first call, zero again after each), then two partial records for each CTA
 size_t paged_attention_workspace_bytes(int head_dim)
 {
-    const size_t ctas = dev_info().sm_count;
+    const size_t ctas = grid_ctas();
     return (ctas * 4 + 255) / 256 * 256 + 2 * ctas * 8 * consumers(head_dim / 32) * (head_dim + 2) * 4;
 }
 
@@ -804,7 +872,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &args, void *workspace, c
 {
     PagedAttnArgs a = args;
     a.counters = static_cast<int *>(workspace);
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ((size_t)dev_info().sm_count * 4 + 255) / 256 * 256);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ((size_t)grid_ctas() * 4 + 255) / 256 * 256);
     switch (a.kv.head_dim / 32) {
         case 1: return launch<1>(a, s);
         case 2: return launch<2>(a, s);

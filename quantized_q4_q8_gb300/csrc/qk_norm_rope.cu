@@ -13,18 +13,18 @@
 // one token (several CTAs share a token's heads when there are few tokens) and forms
 // the token's cosines and sines once: the angle as a fraction of a turn is
 // position * F_i mod 2^64 with F_i = 2^64 theta^(-2i/head_dim) / (2 pi), a product of
-// integers, which drops whole turns exactly at any position and needs no f64.
+// integers, which drops whole turns exactly at any position.
 //
-// Codes of the definition: V is f32 and its codes are decided exactly (the sign of
-// |x| - h |d| at the border h is exact in one fused multiply-add, since h |d| has 16
-// significant bits).  K comes out of the norm and the rotation with an error below
-// 2^-20 (|y0| + |y1|) of its pair: (head_dim / 32 + 5) / 2 <= 6.5 roundings of the sum
-// of squares, 5 of the square root, quotient and products with gamma, 3.2 of a cosine
-// or sine near 1 with its argument, 1.5 of the rotation, each 2^-24.  A warp that finds a
-// value closer than that to the border of two codes, a scale as close to the border of
-// two f16 numbers, or two largest values as close to each other works the head again
-// in f64 (about one head in a hundred).  So the cache holds what the definition in 64
-// bits says, whatever the order of the sums.
+// The cache holds the codes that the definition gives in 64 bits, whatever the order of
+// the sums: a key that rounds to the other side of a border in f32 would be off by a
+// whole step, and in a long prompt some would.  V is f32, and its codes are decided exactly (the
+// sign of |x| - h |d| at a border h is exact in one fused multiply-add, since h |d| has 16
+// significant bits).  K is carried as sums of two floats from the load to the code: squares,
+// the inverse root (one Newton step), cosines and sines, rotation; each is good to about 2^-45, so
+// a key is off by 2^-40 of its pair, as far as the f64 form itself is at positions beyond
+// 10^4.  That costs some 250 more instructions for a key head.  f64 costs more here: working
+// only the doubtful heads (one in a hundred) in f64 took 12 us of 18 at 33 tokens of 32 + 64 heads of 128
+// and 23 us of 79 at 4096 tokens of 32 + 16.  Queries are f32.
 #include <math.h>
 
 #include <algorithm>
@@ -38,11 +38,82 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr float kKeyError = 0x1p-20f;
-constexpr double kTwoPiHi = 6.283185307179586476925286766559;
-constexpr double kTwoPiLo = 2.449293598294706e-16;  // 2 pi - kTwoPiHi
 constexpr double kInvTwoPi = 0.15915494309189533576888376337251;
 
+// cos(2 pi j / 64) as the sum of two floats; sin is the same from the other end
+__device__ const float2 kCos64[17] = {
+    {0x1p+0f, 0x0p+0f},          {0x1.fd88dap-1f, 0x1.e89292p-28f},  {0x1.f6297cp-1f, 0x1.feeb96p-26f},
+    {0x1.e9f416p-1f, -0x1.273a44p-26f}, {0x1.d906bcp-1f, 0x1.e651a8p-26f},  {0x1.c38b3p-1f, -0x1.cfe84ap-26f},
+    {0x1.a9b662p-1f, 0x1.21d434p-26f},  {0x1.8bc806p-1f, 0x1.62a2e8p-26f},  {0x1.6a09e6p-1f, 0x1.9fcef4p-27f},
+    {0x1.44cf32p-1f, 0x1.424776p-27f},  {0x1.1c73b4p-1f, -0x1.9465cep-27f}, {0x1.e2b5d4p-2f, -0x1.fe4272p-28f},
+    {0x1.87de2ap-2f, 0x1.abaa58p-28f},  {0x1.294062p-2f, 0x1.dab3ep-27f},   {0x1.8f8b84p-3f, -0x1.cb2cfap-30f},
+    {0x1.917a6cp-4f, -0x1.eb25eap-31f}, {0x0p+0f, 0x0p+0f}};
+
+// ---------------------------------------------------------------- sums of two floats
+// h + l, |l| at most half a step of h.  Products by __fmul_rn: a product whose error is
+// taken must not be fused into what uses it.
+struct Two {
+    float h, l;
+};
+
+__device__ __forceinline__ Two two_sum(float a, float b)
+{
+    const float s = a + b, bb = s - a;
+    return Two{s, (a - (s - bb)) + (b - bb)};
+}
+__device__ __forceinline__ Two quick_sum(float a, float b)  // |a| >= |b|
+{
+    const float s = a + b;
+    return Two{s, b - (s - a)};
+}
+__device__ __forceinline__ Two two_prod(float a, float b)
+{
+    const float p = __fmul_rn(a, b);
+    return Two{p, fmaf(a, b, -p)};
+}
+// a * b, not brought to |l| <= half a step
+__device__ __forceinline__ Two mul(Two a, float b)
+{
+    const Two p = two_prod(a.h, b);
+    return Two{p.h, fmaf(a.l, b, p.l)};
+}
+__device__ __forceinline__ Two mul(Two a, Two b)
+{
+    const Two p = two_prod(a.h, b.h);
+    return Two{p.h, p.l + fmaf(a.h, b.l, a.l * b.h)};
+}
+__device__ __forceinline__ Two add(Two a, Two b)
+{
+    const Two s = two_sum(a.h, b.h);
+    return quick_sum(s.h, s.l + (a.l + b.l));
+}
+
+// Cosine and sine of a fraction of a turn, turn / 2^64: the nearest 64th of a turn from
+// the table, the rest (at most 0.05) by its power series.
+__device__ __forceinline__ void turn_cos_sin(uint64_t turn, const float2 *cos64, Two &c, Two &s)
+{
+    const uint64_t k = (turn + (1ull << 57)) >> 58;
+    const int64_t r = static_cast<int64_t>(turn - (k << 58));
+    const float rh = static_cast<float>(r), rl = static_cast<float>(r - static_cast<int64_t>(rh));
+    // delta = 2 pi r / 2^64
+    Two d = two_prod(rh, 0x1.921fb6p-62f);
+    d.l += fmaf(rh, -0x1.777a5cp-87f, rl * 0x1.921fb6p-62f);
+    Two d2 = two_prod(d.h, d.h);
+    d2.l = fmaf(2.0f * d.h, d.l, d2.l);
+    const float u = d2.h;
+    const Two sd = {d.h, fmaf(d.h * u, fmaf(u, fmaf(u, -1.0f / 5040, 1.0f / 120), -1.0f / 6), d.l)};
+    const Two cm = {-0.5f * d2.h, fmaf(u * u, fmaf(u, -1.0f / 720, 1.0f / 24), -0.5f * d2.l)};  // cos(delta) - 1
+    const int j = static_cast<int>(k) & 15, quarter = static_cast<int>(k >> 4) & 3;
+    const float2 tc = cos64[j], ts = cos64[16 - j];
+    const Two C{tc.x, tc.y}, S{ts.x, ts.y};
+    // cos(a + delta) = C + C cm - S sd, sin(a + delta) = S + S cm + C sd
+    const Two ss = mul(S, sd), cs = mul(C, sd);
+    const Two co = add(C, add(mul(C, cm), Two{-ss.h, -ss.l})), si = add(S, add(mul(S, cm), cs));
+    c = quarter == 0 ? co : quarter == 1 ? Two{-si.h, -si.l} : quarter == 2 ? Two{-co.h, -co.l} : si;
+    s = quarter == 0 ? si : quarter == 1 ? co : quarter == 2 ? Two{-si.h, -si.l} : Two{-co.h, -co.l};
+}
+
+// ---------------------------------------------------------------- a head in a warp
 // NaN wins in both
 __device__ __forceinline__ float redux_max(float v)
 {
@@ -57,183 +128,163 @@ __device__ __forceinline__ float redux_min(float v)
     return r;
 }
 
-__device__ __forceinline__ double warp_sum_f64(double v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-__device__ __forceinline__ double warp_max_f64(double v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
+// Rotation of a head held as x[e] = value 32 e + lane: z[e] = x[e] cos + o[e] sin', o the
+// other value of the pair and sin' its sine, negative in the pair's first value.
+//   kMode 0: pairs (2i, 2i + 1), the neighbouring lane
+//   kMode 1: pairs (i, i + hd/2), another register of the lane where hd/2 is a multiple of
+//            32, else one of lane ^ 16: at e + NB/2 or e - NB/2 - 1 for lanes below 16, at
+//            e + NB/2 + 1 or e - NB/2 for the others
+template <int NB, int kMode>
+struct Pairs {
+    static constexpr bool same_lane = kMode == 1 && NB % 2 == 0;
+    static constexpr int n = same_lane ? NB / 2 : NB;  // pairs of a lane with angles of their own
 
-// One pair's turn, as the lane that holds x (the other value of the pair is o) sees it.
-template <typename T>
-__device__ __forceinline__ T turned(T x, T o, T cs, T sn, bool first)
-{
-    return first ? x * cs - o * sn : o * sn + x * cs;
-}
-
-// Rotates a head held as x[e] = value 32 e + lane; pair(i, cs, sn) gives pair i's cosine
-// and sine, mag[e] receives |x| + |o| of the value's pair.
-template <int NB, typename T, typename F>
-__device__ __forceinline__ void rotate(T (&x)[NB], T (&mag)[NB], int mode, int lane, F pair)
-{
-    constexpr int half = 16 * NB;
-    T cs, sn;
-    if (mode == 0) {  // pairs (2i, 2i + 1): the neighbouring lane
+    static __device__ __forceinline__ bool first(int e, int lane)
+    {
+        if (kMode == 0) return (lane & 1) == 0;
+        if (same_lane) return e < NB / 2;
+        return lane < 16 ? e + NB / 2 < NB : e + NB / 2 + 1 < NB;
+    }
+    static __device__ __forceinline__ int pair(int e, int lane)
+    {
+        if (kMode == 0) return 16 * e + (lane >> 1);
+        if (same_lane) return 32 * (e % n) + lane;
+        return 32 * e + lane - (first(e, lane) ? 0 : 16 * NB);
+    }
+    static __device__ __forceinline__ void other(const float (&x)[NB], float (&o)[NB], int lane)
+    {
+        if (kMode == 0) {
 #pragma unroll
-        for (int e = 0; e < NB; ++e) {
-            const T o = __shfl_xor_sync(0xffffffffu, x[e], 1);
-            pair(16 * e + (lane >> 1), cs, sn);
-            mag[e] = fabs(x[e]) + fabs(o);
-            x[e] = turned(x[e], o, cs, sn, (lane & 1) == 0);
-        }
-    } else if (NB % 2 == 0) {  // pairs (i, i + half): another register of the lane
+            for (int e = 0; e < NB; ++e) o[e] = __shfl_xor_sync(0xffffffffu, x[e], 1);
+        } else if (same_lane) {
 #pragma unroll
-        for (int e = 0; e < NB / 2; ++e) {
-            const T a = x[e], b = x[e + NB / 2];
-            pair(32 * e + lane, cs, sn);
-            mag[e] = mag[e + NB / 2] = fabs(a) + fabs(b);
-            x[e] = turned(a, b, cs, sn, true);
-            x[e + NB / 2] = turned(b, a, cs, sn, false);
-        }
-    } else {
-        // half is an odd multiple of 16: the partner of value 32 e + l lies in lane l ^ 16, at
-        // register e + h or e - h - 1 (lanes below 16) or e + h + 1 or e - h (the others)
-        constexpr int h = NB / 2;
-        T r[NB];
+            for (int e = 0; e < NB; ++e) o[e] = x[e < NB / 2 ? e + NB / 2 : e - NB / 2];
+        } else {
+            constexpr int h = NB / 2;
+            float r[NB];
 #pragma unroll
-        for (int e = 0; e < NB; ++e) r[e] = __shfl_xor_sync(0xffffffffu, x[e], 16);
-        const bool low = lane < 16;
+            for (int e = 0; e < NB; ++e) r[e] = __shfl_xor_sync(0xffffffffu, x[e], 16);
 #pragma unroll
-        for (int e = 0; e < NB; ++e) {
-            const T ol = r[e + h < NB ? e + h : e - h - 1], oh = r[e + h + 1 < NB ? e + h + 1 : e - h];
-            const T o = low ? ol : oh;
-            const bool first = low ? e + h < NB : e + h + 1 < NB;
-            const int d = 32 * e + lane;
-            pair(first ? d : d - half, cs, sn);
-            mag[e] = fabs(x[e]) + fabs(o);
-            x[e] = turned(x[e], o, cs, sn, first);
+            for (int e = 0; e < NB; ++e) {
+                const float low = r[e + h < NB ? e + h : e - h - 1], high = r[e + h + 1 < NB ? e + h + 1 : e - h];
+                o[e] = lane < 16 ? low : high;
+            }
         }
     }
+};
+
+// A head whose squares leave f32's range, scaled by a power of two (exact); returns eps
+// scaled alike, which leaves the norm's result as it is.
+template <int NB>
+__device__ __forceinline__ float into_range(float (&x)[NB], float eps)
+{
+    float mx = 0.0f;
+#pragma unroll
+    for (int e = 0; e < NB; ++e) mx = fmaxf(mx, fabsf(x[e]));
+    mx = redux_max(mx);
+    if (mx == 0.0f || !(mx < INFINITY)) return eps;
+    int up = 127 - (__float_as_int(mx) >> 23);
+    // eps may not leave the range either (where it counts, the squares need not)
+    if (eps > 0.0f) up = min(up, (127 + 40 - (__float_as_int(eps) >> 23)) / 2);
+    up = max(min(up, 126), -126);
+    const float f = __int_as_float((up + 127) << 23);
+#pragma unroll
+    for (int e = 0; e < NB; ++e) x[e] *= f;
+    return eps * f * f;
+}
+__device__ __forceinline__ bool in_range(float ss) { return ss > 1e-30f && ss < 1e37f; }
+
+// Sum of squares of a head.
+template <int NB>
+__device__ __forceinline__ Two squares(const float (&x)[NB])
+{
+    Two a{0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < NB; ++e) {
+        const Two p = two_prod(x[e], x[e]), t = two_sum(a.h, p.h);
+        a = Two{t.h, a.l + (t.l + p.l)};
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const Two t = two_sum(a.h, __shfl_xor_sync(0xffffffffu, a.h, o));
+        a = Two{t.h, (a.l + __shfl_xor_sync(0xffffffffu, a.l, o)) + t.l};
+    }
+    return a;
+}
+
+// 1 / sqrt(ss / n + eps)
+__device__ __forceinline__ Two inverse_rms(Two ss, int n, float eps)
+{
+    const float r = 1.0f / n, m = __fmul_rn(ss.h, r);
+    const float ml = (fmaf(-m, static_cast<float>(n), ss.h) + ss.l) * r;
+    const Two a = two_sum(m, eps);
+    const float al = a.l + ml, y = rsqrtf(a.h);
+    const Two y2 = two_prod(y, y), t = two_prod(a.h, y2.h);
+    const float e = (1.0f - t.h) - (t.l + fmaf(a.h, y2.l, al * y2.h));  // 1 - a y^2
+    // an infinite sum: 0, and no correction of it
+    return Two{y, a.h < INFINITY ? y * e * fmaf(0.375f, e, 0.5f) : 0.0f};
 }
 
 struct Block {
-    uint16_t d;  // f16 bits of the scale
-    int code;    // this lane's code
-    float value; // and what it stands for
+    uint16_t d;   // f16 bits of the scale
+    int code;     // this lane's code
+    float value;  // and what it stands for
 };
 
-__device__ __forceinline__ uint16_t scale_bits(float s8)
+// The block of 32 values z, one in each lane.
+__device__ __forceinline__ Block quantise(Two z)
 {
-    const uint16_t b = __half_as_ushort(__float2half_rn(fminf(fmaxf(s8, -65504.0f), 65504.0f)));
-    return (b & 0x7fffu) ? b : uint16_t(0);
-}
-
-__device__ __forceinline__ int signed_code(float mag, bool negative)
-{
-    const int m = static_cast<int>(mag);
-    return min(max(negative ? 8 - m : 8 + m, 0), 15);
-}
-
-// The block of 32 values z, one in each lane, with |z - true z| <= err.  Returns true
-// where the codes or the scale of the true values may be others.
-template <bool kExact>
-__device__ __forceinline__ bool quantise(float z, float err, Block &o)
-{
-    const float mx = redux_max(z), mn = redux_min(z);
-    if (!(mx < INFINITY && mn > -INFINITY)) {  // the same in every lane
-        o = Block{0x7e00, 8, __int_as_float(0x7fffffff)};
-        return !kExact;
+    const float mx = redux_max(z.h), mn = redux_min(z.h);
+    if (!(mx < INFINITY && mn > -INFINITY)) return Block{0x7e00, 8, __int_as_float(0x7fffffff)};
+    float s = mx >= -mn ? mx : mn;
+    if (mx == -mn) {  // the low parts tell which is larger
+        const float top = redux_max(z.h == mx ? z.l : -INFINITY), low = redux_min(z.h == mn ? z.l : INFINITY);
+        if (top < -low) s = mn;
     }
-    const float s = mx >= -mn ? mx : mn;
-    o.d = scale_bits(s * -0.125f);
-    bool unsure = false;
-    if (!kExact) {
-        const float eb = redux_max(err);
-        unsure = fabsf(mx + mn) < 2.0f * eb || scale_bits((s - eb) * -0.125f) != scale_bits((s + eb) * -0.125f);
-    }
-    const float d = h2f(o.d), ad = fabsf(d), az = fabsf(z);
-    if (ad == 0.0f) {
-        o.code = 8;
-        o.value = 0.0f;
-        return unsure;
-    }
+    Block o;
+    o.d = __half_as_ushort(__float2half_rn(fminf(fmaxf(s * -0.125f, -65504.0f), 65504.0f)));
+    if ((o.d & 0x7fffu) == 0) return Block{0, 8, 0.0f};
+    const float d = h2f(o.d), ad = fabsf(d), az = fabsf(z.h), al = z.h < 0.0f ? -z.l : z.l;
     const float k = floorf(fminf(az * rcp_approx(ad), 64.0f));
     const float t = __fmaf_rn(-(k + 0.5f), ad, az);
-    if (!kExact) unsure = unsure || fabsf(t) < err;
-    const bool up = t > 0.0f || (t == 0.0f && (static_cast<int>(k) & 1));
-    o.code = signed_code(up ? k + 1.0f : k, (z < 0.0f) != (d < 0.0f));
+    // beyond the border, or on it: then the low part tells, and of a tie the even code is taken
+    const bool up = t > 0.0f || (t == 0.0f && (al > 0.0f || (al == 0.0f && (static_cast<int>(k) & 1))));
+    const int m = static_cast<int>(up ? k + 1.0f : k);
+    o.code = min(max((z.h < 0.0f) != (d < 0.0f) ? 8 - m : 8 + m, 0), 15);
     o.value = static_cast<float>(o.code - 8) * d;
-    return unsure;
+    return o;
 }
 
-// The same for values in f64, as the definition has them.
-__device__ __forceinline__ void quantise_f64(double z, Block &o)
+// One block of a token's key or value: values to `out` (or nowhere), bytes into the record.
+template <int NB, bool kIsV>
+__device__ __forceinline__ void put_block(const Block &b, int e, int lane, float *out, uint8_t *rec, int tok)
 {
-    const bool fine = __all_sync(0xffffffffu, fabs(z) < (double)INFINITY);
-    if (!fine) {
-        o = Block{0x7e00, 8, __int_as_float(0x7fffffff)};
-        return;
-    }
-    const double mx = warp_max_f64(z), mn = -warp_max_f64(-z);
-    o.d = scale_bits(static_cast<float>((mx >= -mn ? mx : mn) * -0.125));
-    const float d = h2f(o.d);
-    if (d == 0.0f) {
-        o.code = 8;
-        o.value = 0.0f;
-        return;
-    }
-    const double m = fmin(rint(fabs(z) / fabs(static_cast<double>(d))), 64.0);
-    o.code = signed_code(static_cast<float>(m), (z < 0.0) != (d < 0.0f));
-    o.value = static_cast<float>(o.code - 8) * d;
+    if (out) out[32 * e + lane] = b.value;
+    if (!rec) return;
+    const int high = __shfl_down_sync(0xffffffffu, b.code, 16);
+    if (lane < 16)
+        rec[kIsV ? q4_v_byte(NB, tok, e, lane) : q4_k_byte(NB, tok, e, lane)] = static_cast<uint8_t>(b.code | (high << 4));
+    if (lane == e)
+        reinterpret_cast<uint16_t *>(rec + (kIsV ? q4_v_scale(NB, tok) : q4_k_scale(NB, tok)))[e] = b.d;
 }
 
-// A head normed and rotated in f64.
-template <int NB>
-__device__ __noinline__ void head_f64(const float *src, const float *gamma, float eps, int pos, const double *freq,
-                                      int mode, int lane, double (&z)[NB])
-{
-    double ss = 0.0, mag[NB];
-#pragma unroll
-    for (int e = 0; e < NB; ++e) {
-        z[e] = src[32 * e + lane];
-        ss = fma(z[e], z[e], ss);
-    }
-    if (gamma) {
-        const double inv = 1.0 / sqrt(warp_sum_f64(ss) / (32 * NB) + eps);
-#pragma unroll
-        for (int e = 0; e < NB; ++e) z[e] = z[e] * inv * gamma[32 * e + lane];
-    }
-    rotate<NB, double>(z, mag, mode, lane, [&](int i, double &cs, double &sn) {
-        const double ang = pos * freq[i], n = rint(ang * kInvTwoPi);
-        sincos(fma(-n, kTwoPiLo, fma(-n, kTwoPiHi, ang)), &sn, &cs);
-    });
-}
-
-// grid (tokens, splits): CTA (t, y) works heads y * per .. of token t's n_heads + 2
-// n_kv_heads rows, a warp at a time, the next row's values on their way meanwhile.
-template <int NB>
+// grid (tokens, splits): CTA (t, y) works rows y * per .. of token t's n_heads queries, then
+// n_kv_heads keys, then values, a row a warp; a row's values are on their way
+// while the warp works the one before.
+template <int NB, int kMode>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ HeadsArgs a)
 {
     constexpr int hd = 32 * NB;
-    __shared__ float2 tab[hd / 2];
+    using P = Pairs<NB, kMode>;
+    __shared__ float4 tab[hd / 2];  // cos h, sin h, cos l, sin l of each pair
+    __shared__ float2 cos64[17];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t t = blockIdx.x;
+    if (tid < 17) cos64[tid] = kCos64[tid];
     pdl_launch_dependents();
     pdl_wait();
     const int pos = a.positions[t];
     if (pos < 0) return;  // the same for the whole CTA: a padding row
-    for (int i = tid; i < hd / 2; i += kThreads) {
-        const int turn = static_cast<int>(static_cast<uint64_t>(pos) * a.turn[i] >> 32);
-        float2 cs;
-        sincospif(static_cast<float>(turn) * 0x1p-31f, &cs.y, &cs.x);
-        tab[i] = cs;
-    }
     const int H = a.n_heads, K = a.n_kv_heads;
     const int rows = a.kv.pages ? H + 2 * K : H + K;
     const int per = (rows + gridDim.y - 1) / gridDim.y;
@@ -242,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
     // where the token lies in the cache
     uint8_t *rec = nullptr;
     int tok = 0;
-    if (a.kv.pages && a.slots) {
+    if (a.kv.pages) {
         const int64_t slot = a.slots[t];
         const int lg = a.kv.page_log + 4;
         if (slot >= 0 && (slot >> lg) < a.kv.n_pages) {
@@ -253,102 +304,128 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
             set_error(a.err, DEV_BAD_SLOT);
         }
     }
-
-    auto row_ptr = [&](int r) {
-        return r < H ? a.q + t * a.ld_q + (int64_t)r * hd
-                     : r < H + K ? a.k + t * a.ld_k + (int64_t)(r - H) * hd : a.v + t * a.ld_v + (int64_t)(r - H - K) * hd;
+    auto load = [&](float (&x)[NB], int r) {
+        const float *p = r < H ? a.q + t * a.ld_q + (int64_t)r * hd
+                               : r < H + K ? a.k + t * a.ld_k + (int64_t)(r - H) * hd
+                                           : a.v + t * a.ld_v + (int64_t)(r - H - K) * hd;
+#pragma unroll
+        for (int e = 0; e < NB; ++e) x[e] = p[32 * e + lane];
     };
     float nx[NB];
-    if (r0 + warp < r1) {
-        const float *p = row_ptr(r0 + warp);
-#pragma unroll
-        for (int e = 0; e < NB; ++e) nx[e] = p[32 * e + lane];
+    if (r0 + warp < r1) load(nx, r0 + warp);
+    __syncthreads();  // cos64
+    for (int i = tid; i < hd / 2; i += kThreads) {
+        Two c, s;
+        turn_cos_sin(static_cast<uint64_t>(pos) * a.turn[i], cos64, c, s);
+        tab[i] = make_float4(c.h, s.h, c.l, s.l);
     }
     __syncthreads();
-    for (int r = r0 + warp; r < r1; r += kWarps) {
-        float x[NB], mag[NB];
+
+    int r = r0 + warp;
+    auto next = [&](float (&x)[NB]) {  // row r's values, and the next row's on their way
 #pragma unroll
         for (int e = 0; e < NB; ++e) x[e] = nx[e];
-        if (r + kWarps < r1) {
-            const float *p = row_ptr(r + kWarps);
+        if (r + kWarps < r1) load(nx, r + kWarps);
+    };
+    // ---- queries
+    if (r < min(r1, H)) {
+        float g[NB], c[P::n], s[P::n];
 #pragma unroll
-            for (int e = 0; e < NB; ++e) nx[e] = p[32 * e + lane];
+        for (int e = 0; e < NB; ++e) g[e] = a.q_gamma ? __ldg(a.q_gamma + 32 * e + lane) : 1.0f;
+#pragma unroll
+        for (int e = 0; e < P::n; ++e) {
+            const float4 v = tab[P::pair(e, lane)];
+            c[e] = v.x;
+            s[e] = v.y;
         }
-        const bool is_v = r >= H + K, is_q = r < H;
-        Block blk[NB];
-        if (!is_v) {
-            const float *gamma = is_q ? a.q_gamma : a.k_gamma;
-            bool far = false;  // squares whose sum leaves f32's range
-            if (gamma) {
-                float ss = 0.0f;
+        for (; r < min(r1, H); r += kWarps) {
+            float x[NB], o[NB];
+            next(x);
+            if (a.q_gamma) {
+                float ss = 0.0f, eps = a.eps;
 #pragma unroll
                 for (int e = 0; e < NB; ++e) ss = fmaf(x[e], x[e], ss);
                 ss = warp_sum(ss);
-                if (!(ss > 1e-30f && ss < 1e37f)) {
-                    bool any = false;
+                if (!in_range(ss)) {
+                    eps = into_range(x, eps);
+                    ss = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < NB; ++e) any |= x[e] != 0.0f;
-                    far = __any_sync(0xffffffffu, any);
+                    for (int e = 0; e < NB; ++e) ss = fmaf(x[e], x[e], ss);
+                    ss = warp_sum(ss);
                 }
-                const float inv = rms_scale(ss, hd, a.eps);
+                const float inv = rsqrtf(fmaf(ss, 1.0f / hd, eps));
 #pragma unroll
-                for (int e = 0; e < NB; ++e) x[e] = x[e] * inv * __ldg(gamma + 32 * e + lane);
+                for (int e = 0; e < NB; ++e) x[e] = x[e] * inv * g[e];
             }
-            rotate<NB, float>(x, mag, a.rope_mode, lane, [&](int i, float &cs, float &sn) {
-                const float2 c = tab[i];
-                cs = c.x;
-                sn = c.y;
-            });
-            bool again = far;
-            if (!is_q && a.kv.pages) {
-                bool unsure = false;
-#pragma unroll
-                for (int e = 0; e < NB; ++e) unsure |= quantise<false>(x[e], kKeyError * mag[e], blk[e]);
-                again = __any_sync(0xffffffffu, unsure) || far;
-            }
-            if (again) {
-                double z[NB];
-                head_f64<NB>(row_ptr(r), gamma, a.eps, pos, a.freq, a.rope_mode, lane, z);
-#pragma unroll
-                for (int e = 0; e < NB; ++e) {
-                    x[e] = static_cast<float>(z[e]);
-                    if (!is_q && a.kv.pages) quantise_f64(z[e], blk[e]);
-                }
-            }
-            if (is_q || !a.kv.pages) {
-                float *o = is_q ? a.q_out + t * a.ld_qo + (int64_t)r * hd
-                                : a.k_out ? a.k_out + (t * K + (r - H)) * (int64_t)hd : nullptr;
-                if (o) {
-#pragma unroll
-                    for (int e = 0; e < NB; ++e) o[32 * e + lane] = x[e];
-                }
-                continue;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < NB; ++e) quantise<true>(x[e], 0.0f, blk[e]);
-        }
-        // a key or value of the cache
-        const int h = is_v ? r - H - K : r - H;
-        float *o = is_v ? a.v_out : a.k_out;
-        if (o) {
-            o += (t * K + h) * (int64_t)hd;
-#pragma unroll
-            for (int e = 0; e < NB; ++e) o[32 * e + lane] = blk[e].value;
-        }
-        if (rec) {
-            uint8_t *base = rec + ((int64_t)h << a.kv.page_log) * q4_record_bytes(hd);
+            P::other(x, o, lane);
+            float *out = a.q_out + t * a.ld_qo + (int64_t)r * hd + lane;
 #pragma unroll
             for (int e = 0; e < NB; ++e) {
-                const int high = __shfl_down_sync(0xffffffffu, blk[e].code, 16);
-                if (lane < 16)
-                    base[is_v ? q4_v_byte(NB, tok, e, lane) : q4_k_byte(NB, tok, e, lane)] =
-                        static_cast<uint8_t>(blk[e].code | (high << 4));
-                if (lane == e)
-                    reinterpret_cast<uint16_t *>(base + (is_v ? q4_v_scale(NB, tok) : q4_k_scale(NB, tok)))[e] =
-                        blk[e].d;
+                const float sn = s[e % P::n];
+                out[32 * e] = fmaf(o[e], P::first(e, lane) ? -sn : sn, x[e] * c[e % P::n]);
             }
         }
+    }
+    // ---- keys
+    for (; r < min(r1, H + K); r += kWarps) {
+        float x[NB], o[NB], xl[NB], ol[NB];
+        next(x);
+#pragma unroll
+        for (int e = 0; e < NB; ++e) xl[e] = 0.0f;
+        if (a.k_gamma) {
+            float eps = a.eps;
+            Two ss = squares(x);
+            if (!in_range(ss.h)) {
+                eps = into_range(x, eps);
+                ss = squares(x);
+            }
+            const Two inv = inverse_rms(ss, hd, eps);
+#pragma unroll
+            for (int e = 0; e < NB; ++e) {
+                const Two y = mul(mul(inv, __ldg(a.k_gamma + 32 * e + lane)), x[e]);
+                x[e] = y.h;
+                xl[e] = y.l;
+            }
+        }
+        P::other(x, o, lane);
+        P::other(xl, ol, lane);
+        const int h = r - H;
+        float *out = a.k_out ? a.k_out + (t * K + h) * (int64_t)hd : nullptr;
+        uint8_t *base = rec ? rec + ((int64_t)h << a.kv.page_log) * q4_record_bytes(hd) : nullptr;
+#pragma unroll
+        for (int e = 0; e < NB; ++e) {
+            const float4 cs = tab[P::pair(e, lane)];
+            const bool first = P::first(e, lane);
+            const Two z = add(mul(Two{x[e], xl[e]}, Two{cs.x, cs.z}),
+                              mul(Two{o[e], ol[e]}, first ? Two{-cs.y, -cs.w} : Two{cs.y, cs.w}));
+            if (a.kv.pages) put_block<NB, false>(quantise(z), e, lane, out, base, tok);
+            else if (out) out[32 * e + lane] = z.h;
+        }
+    }
+    // ---- values
+    for (; r < r1; r += kWarps) {
+        float x[NB];
+        next(x);
+        const int h = r - H - K;
+        float *out = a.v_out ? a.v_out + (t * K + h) * (int64_t)hd : nullptr;
+        uint8_t *base = rec ? rec + ((int64_t)h << a.kv.page_log) * q4_record_bytes(hd) : nullptr;
+#pragma unroll
+        for (int e = 0; e < NB; ++e) put_block<NB, true>(quantise(Two{x[e], 0.0f}), e, lane, out, base, tok);
+    }
+}
+
+template <int kMode>
+cudaError_t launch(const cudaLaunchConfig_t &cfg, const HeadsArgs &a, int nb)
+{
+    switch (nb) {
+        case 1: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<1, kMode>, a);
+        case 2: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<2, kMode>, a);
+        case 3: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<3, kMode>, a);
+        case 4: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<4, kMode>, a);
+        case 5: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<5, kMode>, a);
+        case 6: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<6, kMode>, a);
+        case 7: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<7, kMode>, a);
+        default: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<8, kMode>, a);
     }
 }
 
@@ -357,8 +434,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
 cudaError_t launch_qk_norm_rope(HeadsArgs &a, int64_t rows, int head_dim, float rope_theta, cudaStream_t s)
 {
     for (int i = 0; i < head_dim / 2; ++i) {
-        a.freq[i] = pow((double)rope_theta, -2.0 * i / head_dim);
-        const double turns = a.freq[i] * kInvTwoPi;
+        const double turns = pow((double)rope_theta, -2.0 * i / head_dim) * kInvTwoPi;
         a.turn[i] = static_cast<uint64_t>(static_cast<int64_t>((turns - floor(turns)) * 0x1p62)) << 2;
     }
     const int per_token = a.n_heads + (a.kv.pages ? 2 : 1) * a.n_kv_heads;
@@ -375,16 +451,7 @@ cudaError_t launch_qk_norm_rope(HeadsArgs &a, int64_t rows, int head_dim, float 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = g_use_pdl ? 1 : 0;
-    switch (head_dim / 32) {
-        case 1: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<1>, a);
-        case 2: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<2>, a);
-        case 3: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<3>, a);
-        case 4: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<4>, a);
-        case 5: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<5>, a);
-        case 6: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<6>, a);
-        case 7: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<7>, a);
-        default: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<8>, a);
-    }
+    return a.rope_mode == 0 ? launch<0>(cfg, a, head_dim / 32) : launch<1>(cfg, a, head_dim / 32);
 }
 
 }  // namespace rz

@@ -251,7 +251,7 @@ struct PlanArgs {
 constexpr int kPlanMaxSeqs = 1024;
 cudaError_t launch_paged_plan(const PlanArgs &a, cudaStream_t s);
 
-// Norm, rotation and append (qk_norm_rope.cu).  freq and turn are filled by the launcher.
+// Norm, rotation and append (qk_norm_rope.cu).  turn is filled by the launcher.
 struct HeadsArgs {
     const float *q, *k, *v;
     int64_t ld_q, ld_k, ld_v;
@@ -264,8 +264,7 @@ struct HeadsArgs {
     int n_heads, n_kv_heads, rope_mode;
     float eps;
     unsigned *err;
-    double freq[128];    // theta^(-2i/head_dim)
-    uint64_t turn[128];  // the same as a fraction of a turn for each position, times 2^64
+    uint64_t turn[128];  // theta^(-2i/head_dim) as a fraction of a turn for each position, times 2^64
 };
 cudaError_t launch_qk_norm_rope(HeadsArgs &a, int64_t rows, int head_dim, float rope_theta, cudaStream_t s);
 

@@ -521,7 +521,7 @@ def test_attention_repeats_bit_for_bit(rz):
     first = s.run(rz).clone()
     for _ in range(5):
         assert torch.equal(s.run(rz), first)
-    assert not s.ws[:608].any()  # its counters are zero again
+    assert not s.ws[:1024].any()  # its counters are zero again
     rz.set_pdl(False)
     try:
         assert torch.equal(s.run(rz), first)
