@@ -6,15 +6,19 @@
 //   k_j = d_jb (code - 8) for each block b of 32 values, v_j alike; a row that sees
 //   nothing comes out as zeros.
 //
-// Products.  Codes become f16 integers -8..7, exactly: a nibble ORed into the low bits of
+// Products.  m16n8k16, the tokens in the rows and the queries in the columns: for the
+// scores A holds 16 tokens' codes and B the queries, for the sums A holds 16 values' codes of 16
+// tokens and B the weights.  So each code is unpacked once for all of a warp's
+// queries.  Codes become f16 integers -8..7, exactly: a nibble ORed into the low bits of
 // 1024 is 1024 + code (high nibbles: 1024 + 16 code), and one packed subtraction or
 // multiply-add takes the rest off, two codes at a time.  (A code left in the low bits alone
 // is a subnormal, exact too and without the subtraction, but the tensor cores align a
 // product by its operands' exponents and not by its size: sums came out at 2^-17.)  q and the
-// weights p * d of V are two f16 pieces each (22 bits), the high pieces in rows 0..7 of an
-// m16n8k16 product and the low ones in rows 8..15, so that one product gives both
-// halves of 8 query rows; sums are f32.  q is scaled by a power of two for each row
-// (exact) so that its pieces fill f16's range.
+// weights p * d of V are two f16 pieces each (22 bits) in neighbouring columns, 4 queries to a
+// product, so that a thread finds both halves of its query's sum in one register pair and adds them;
+// sums are f32.  q is scaled by a power of two for each row (exact) so that its pieces
+// fill f16's range.  The weights come out of the scores' layout with a lane for a token and have to
+// go into B's with a lane for a query: one movmatrix for 8 tokens and a block.
 //
 // Softmax.  The running maximum M of a row is one of log2(p) + log2 |d of V|, so that the
 // weights p * d that are split stay within f16 (2^7 near the maximum, up to 2^15)
@@ -22,14 +26,14 @@
 // leave that range, by 2^8 over the maximum, and not before.
 //
 // Work.  An item is (request, kv head, up to 8 W query rows: token-major, the group's
-// heads within a token); it reads tiles of W groups of 16 tokens.  All items' tiles,
+// heads within a token); it reads tiles of 2 W groups of 16 tokens.  All items' tiles,
 // weighted by their cost, are one line that the CTAs (two for each SM) share evenly, so
 // that one long request or many ragged ones load all SMs alike; a CTA whose share ends
 // within an item leaves its sums in the workspace and the CTA that finishes last adds them
 // up, in the order of the tiles (the result does not depend on which one it is).
-// Within a CTA the W consumer warps share a tile: with 8 query rows each takes one
-// group of 16 tokens, with 8 W each takes 8 rows; a producer warp copies records into a
-// ring of stages, a page at a time, with the bulk-copy engine.
+// Within a CTA the W consumer warps share a tile: with up to 8 query rows each takes two
+// groups of 16 tokens (with up to 4, both at once), with 8 W each takes 8 rows; a producer
+// warp copies records into a ring of stages, a page at a time, with the bulk-copy engine.
 #include <math.h>
 
 #include <algorithm>
@@ -45,6 +49,7 @@ namespace {
 // Consumer warps W of a CTA, two CTAs on an SM: 5 and a producer are 3 warps a scheduler, 168
 // registers a thread; heads of over 128 values need 255, and 3 and a producer.
 __host__ __device__ constexpr int consumers(int nb) { return nb <= 4 ? 5 : 3; }
+constexpr int kPad = 8;     // floats after a row of sums: its 4 rows fall into other banks
 constexpr int kFlush = 32;  // groups of 16 tokens summed in the tensor cores' accumulators at a time
 constexpr float kLazy = 8.0f;  // weights may grow by 2^8 over the running maximum
 constexpr float kBias = 7.0f;  // log2 of a weight p * |d| at the running maximum
@@ -68,11 +73,6 @@ __device__ __forceinline__ float quad_max(float v)
 {
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-__device__ __forceinline__ float quad_sum(float v)
-{
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 template <int W>
 __device__ __forceinline__ void consumer_sync()
@@ -131,7 +131,7 @@ __device__ __forceinline__ int item_tokens(const Seq &q, int group, int it)
 template <int W>
 __device__ __forceinline__ int item_tiles(const Seq &q, int group, int it)
 {
-    return (item_tokens(q, group, it) + 16 * W - 1) / (16 * W);
+    return (item_tokens(q, group, it) + 32 * W - 1) / (32 * W);
 }
 // Cost of a tile, and of an item's start and end, in halves of a tile of 8 query rows.
 __device__ __forceinline__ int tile_cost(int rg) { return rg == 1 ? 2 : rg == 2 ? 5 : 2 * rg; }
@@ -183,7 +183,7 @@ template <int W>
 __device__ __forceinline__ void load_item(Walk &w, const PagedAttnArgs &a, int group)
 {
     w.tokens = item_tokens(w.q, group, w.it);
-    w.tiles = (w.tokens + 16 * W - 1) / (16 * W);
+    w.tiles = (w.tokens + 32 * W - 1) / (32 * W);
     const int cost = tile_cost(w.q.rg);
     w.lo = tile_at(w.x0 - w.at, w.tiles, cost);
     w.hi = tile_at(w.x1 - w.at, w.tiles, cost);
@@ -252,97 +252,89 @@ __device__ __forceinline__ bool walk_has(const Walk &w)
 }
 
 // ---------------------------------------------------------------- one warp's sums
-template <int NB>
+// NT tiles of 4 queries; this lane (g, t) sums for query 4 j + t of tile j.
+template <int NB, int NT>
 struct Warp {
-    uint32_t qa[NB][2][4];  // A fragments: block, low and high half, {a0..a3}
-    float unit;             // log2(e) * scale * the unit of the products
-    float o[NB][4][4];      // sums of V: block, tile (r, nibble), {c0..c3}
-    float m, l;             // running maximum (see the top), sum of p
-    float *row;             // this lane's row of sums in shared memory
-    int since;              // groups of tokens in o
-    bool flushed;           // part of the sums is in row
+    uint32_t q[NT][NB][2][2];  // B fragments: tile, block, low and high half
+    float unit[NT];            // log2(e) * scale * the unit of the products
+    float o[NT][NB][2][4];     // sums of V: tile, block, half, {c0..c3}
+    float m[NT], l[NT];        // running maximum (see the top), sum of p
+    float *row;                // this lane's row of sums in shared memory (tile 0)
+    int since;                 // groups of tokens in o
+    bool flushed;              // part of the sums is in shared memory
 };
-
-// Visits the lane's sums: f(the two of a tile, their place in the row).
-template <int NB, typename F>
-__device__ __forceinline__ void each_sum(Warp<NB> &w, int t, F f)
-{
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)  // tile k: values 16 (k & 1) + 8 (k >> 1) .. of the block
-            f(w.o[b][k], reinterpret_cast<float2 *>(w.row + 32 * b + 16 * (k & 1) + 8 * (k >> 1) + 2 * t));
-}
 
 // The sums to shared memory, high and low pieces together.  The tensor cores cut what they
 // add to an accumulator instead of rounding it, so that a sum of n steps drifts towards zero by
 // up to n / 2 steps of 2^-24: 3.6e-6 after 4000 tokens.  Every kFlush groups the sums are
 // added to those in shared memory instead, rounded.
-template <int NB>
-__device__ __forceinline__ void flush(Warp<NB> &w, int t)
+template <int NB, int NT>
+__device__ __forceinline__ void flush(Warp<NB, NT> &w, int g)
 {
-    const bool more = w.flushed;
-    each_sum(w, t, [&](float(&c)[4], float2 *p) {
-        float2 v = make_float2(c[0] + c[2], c[1] + c[3]);
-        if (more) {
-            const float2 u = *p;
-            v.x += u.x;
-            v.y += u.y;
-        }
-        *p = v;
-        c[0] = c[1] = c[2] = c[3] = 0.0f;
-    });
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float *p = w.row + 4 * j * (32 * NB + kPad) + 32 * b + 16 * hf + g;
+                float(&c)[4] = w.o[j][b][hf];
+                p[0] = (c[0] + c[1]) + (w.flushed ? p[0] : 0.0f);
+                p[8] = (c[2] + c[3]) + (w.flushed ? p[8] : 0.0f);
+                c[0] = c[1] = c[2] = c[3] = 0.0f;
+            }
     w.flushed = true;
     w.since = 0;
 }
 
-// The query row of this lane's g: pieces in fragment order.  ptr == nullptr: a row of zeros.
-template <int NB>
-__device__ __forceinline__ void load_query(Warp<NB> &w, const float *ptr, float scale, int t)
+// The queries in fragment order: this lane holds, for tile j, values 4 t .. 4 t + 3 (of both
+// halves of each block) of query 4 j + g / 2 at ptr[j], its high piece (g even) or its low one.
+template <int NB, int NT>
+__device__ __forceinline__ void load_query(Warp<NB, NT> &w, const float *const (&ptr)[NT], float scale, int g, int t)
 {
-    float4 v[NB][2];
-    float mx = 0.0f;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int j = 0; j < NT; ++j) {
+        float4 v[NB][2];
+        float mx = 0.0f;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            v[b][hf] = ptr ? __ldg(reinterpret_cast<const float4 *>(ptr + 32 * b + 16 * hf + 4 * t))
-                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v[b][hf].x), fabsf(v[b][hf].y)),
-                                 fmaxf(fabsf(v[b][hf].z), fabsf(v[b][hf].w))));
-        }
-    mx = quad_max(mx);
-    // 2^up brings the largest value to [2^14, 2^15); powers of two, so exact
-    const int ex = (__float_as_int(mx) >> 23) - 127;
-    const int up = mx == 0.0f ? 0 : min(14 - ex, 126);
-    const float sc = __int_as_float((up + 127) << 23);
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const float x[4] = {v[b][hf].x * sc, v[b][hf].z * sc, v[b][hf].y * sc, v[b][hf].w * sc};
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t hi = pack_f16(x[2 * k], x[2 * k + 1]);
-                const float2 h = unpack_f16(hi);
-                w.qa[b][hf][2 * k] = hi;                                                      // a0, a2: row g
-                w.qa[b][hf][2 * k + 1] = pack_f16(x[2 * k] - h.x, x[2 * k + 1] - h.y);  // a1, a3: row g + 8
+            for (int hf = 0; hf < 2; ++hf) {
+                v[b][hf] = ptr[j] ? __ldg(reinterpret_cast<const float4 *>(ptr[j] + 32 * b + 16 * hf + 4 * t))
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v[b][hf].x), fabsf(v[b][hf].y)),
+                                     fmaxf(fabsf(v[b][hf].z), fabsf(v[b][hf].w))));
             }
-        }
+        mx = quad_max(mx);
+        // 2^up brings the largest value to [2^14, 2^15); powers of two, so exact
+        const int ex = (__float_as_int(mx) >> 23) - 127;
+        const int up = mx == 0.0f ? 0 : min(14 - ex, 126);
+        const float sc = __int_as_float((up + 127) << 23);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w.o[b][i][j] = 0.0f;
+            for (int hf = 0; hf < 2; ++hf) {
+                const float x[4] = {v[b][hf].x * sc, v[b][hf].z * sc, v[b][hf].y * sc, v[b][hf].w * sc};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t hi = pack_f16(x[2 * k], x[2 * k + 1]);
+                    const float2 h = unpack_f16(hi);
+                    w.q[j][b][hf][k] = (g & 1) ? pack_f16(x[2 * k] - h.x, x[2 * k + 1] - h.y) : hi;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w.o[j][b][hf][k] = 0.0f;
+            }
+        // the unit of query t is with lane g = 2 t
+        w.unit[j] = scale * 1.4426950408889634f * __int_as_float((127 - __shfl_sync(0xffffffffu, up, 8 * t)) << 23);
+        w.m[j] = -1e37f;
+        w.l[j] = 0.0f;
     }
-    w.unit = scale * 1.4426950408889634f * __int_as_float((127 - up) << 23);
-    w.m = -1e37f;
-    w.l = 0.0f;
     w.since = 0;
     w.flushed = false;
 }
 
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t (&r)[N], const uint8_t *p)
+__device__ __forceinline__ void lds_words(uint32_t *r, const uint8_t *p)
 {
     if constexpr (N % 4 == 0) {
 #pragma unroll
@@ -374,124 +366,173 @@ __device__ __forceinline__ float half_at(const uint32_t (&w)[N], int i)
     return (i & 1) ? v.y : v.x;
 }
 
-// 16 tokens of a record for the warp's 8 query rows.  sees: how many of the 16 this lane's
-// row sees (kMasked), else all.
-template <int NB, bool kMasked>
-__device__ __forceinline__ void tokens16(Warp<NB> &w, const uint8_t *rec, int g, int t, int sees)
+__device__ __forceinline__ uint32_t transposed(uint32_t v)
 {
-    constexpr int hd = 32 * NB;
-    // ---- scores of tokens 4 t .. 4 t + 3
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    {
-        uint32_t ks[2 * NB];
-        lds_words(ks, rec + q4_k_scale(NB, 4 * t));
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// NG groups of 16 tokens (records one after another) for the warp's 4 NT queries.
+// sees[j]: how many of the tokens this lane's query of tile j sees (kMasked), else all.
+// Row g of a product is token 2 g of the group, row g + 8 token 2 g + 1.
+template <int NB, int NT, int NG, bool kMasked>
+__device__ __forceinline__ void attend(Warp<NB, NT> &w, const uint8_t *rec, int g, int t, const int (&sees)[NT])
+{
+    constexpr int hd = 32 * NB, kRec = q4_record_bytes(hd);
+    // ---- scores of tokens 2 g, 2 g + 1 of each group
+    float s[NT][2 * NG];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            // column n of product j is token 4 (n / 2) + 2 j + n % 2
-            uint32_t kw[NB];
-            lds_words(kw, rec + (4 * (g >> 1) + 2 * j + (g & 1)) * (hd / 2) + t * 4 * NB);
+    for (int u = 0; u < NG; ++u) {
+        const uint8_t *r = rec + u * kRec;
+        uint32_t k0[NB], k1[NB], ks[NB];
+        lds_words<NB>(k0, r + 2 * g * (hd / 2) + t * 4 * NB);
+        lds_words<NB>(k1, r + (2 * g + 1) * (hd / 2) + t * 4 * NB);
+        lds_words<NB>(ks, r + q4_k_scale(NB, 2 * g));
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                const uint32_t u = kw[b] >> 8;
-                mma16816(c, w.qa[b][0], low_codes(kw[b]), low_codes(u), c);
-                mma16816(c, w.qa[b][1], high_codes(kw[b]), high_codes(u), c);
-                s[2 * j] = fmaf(half_at(ks, (2 * j) * NB + b), c[0] + c[2], s[2 * j]);
-                s[2 * j + 1] = fmaf(half_at(ks, (2 * j + 1) * NB + b), c[1] + c[3], s[2 * j + 1]);
-            }
-        }
-    }
-    uint32_t vs[2 * NB];
-    lds_words(vs, rec + q4_v_scale(NB, 4 * t));
-    if (kMasked) {
-        // what no row may see is whatever the page holds: its score and its scales are dropped
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (4 * t + i >= sees) {
-                s[i] = -INFINITY;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int k = i * NB + b;
-                    vs[k >> 1] &= (k & 1) ? 0x0000ffffu : 0xffff0000u;
-                }
-            }
-    }
-    // ---- running maximum of log2 p + log2 |d|
-    uint32_t dm = vs[0] & 0x7fff7fffu;
-#pragma unroll
-    for (int i = 1; i < 2 * NB; ++i) {
-        const uint32_t v = vs[i] & 0x7fff7fffu;
-        asm("max.f16x2 %0, %0, %1;" : "+r"(dm) : "r"(v));
-    }
-    const float2 dm2 = unpack_f16(dm);
-    // the exponent above the largest |d| (d = 0: that of the smallest f16)
-    const float ev = static_cast<float>((__float_as_int(fmaxf(fmaxf(dm2.x, dm2.y), 0x1p-25f)) >> 23) - 126);
-    const float y = fmaf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), w.unit, ev);
-    if (__any_sync(0xffffffffu, y > w.m + kLazy)) {
-        const float top = quad_max(y);
-        const float m = top > w.m + kLazy ? top : w.m;
-        const float f = ex2(w.m - m);
-        w.m = m;
-        w.l *= f;
+        for (int j = 0; j < NT; ++j) s[j][2 * u] = s[j][2 * u + 1] = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
+            const uint32_t h0 = k0[b] >> 8, h1 = k1[b] >> 8;
+            const uint32_t lo[4] = {low_codes(k0[b]), low_codes(k1[b]), low_codes(h0), low_codes(h1)};
+            const uint32_t hi[4] = {high_codes(k0[b]), high_codes(k1[b]), high_codes(h0), high_codes(h1)};
+            const float d0 = half_at(ks, b), d1 = half_at(ks, NB + b);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w.o[b][i][j] *= f;
+            for (int j = 0; j < NT; ++j) {
+                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma16816(c, lo, w.q[j][b][0][0], w.q[j][b][0][1], c);
+                mma16816(c, hi, w.q[j][b][1][0], w.q[j][b][1][1], c);
+                s[j][2 * u] = fmaf(d0, c[0] + c[1], s[j][2 * u]);
+                s[j][2 * u + 1] = fmaf(d1, c[2] + c[3], s[j][2 * u + 1]);
+            }
         }
-        if (w.flushed)
-            each_sum(w, t, [&](float(&)[4], float2 *p) {
-                const float2 u = *p;
-                *p = make_float2(u.x * f, u.y * f);
-            });
     }
-    float p[4];
-    const float off = kBias - w.m;
+    uint32_t vs[NG][NB];
+    uint32_t dm = 0;  // the largest |d| of this lane's tokens, two f16
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[i], w.unit, off));
-    w.l += (p[0] + p[1]) + (p[2] + p[3]);
-    // ---- sums of V
-    uint32_t vw[2 * NB];
-    constexpr int run = q4_v_run(NB);
+    for (int u = 0; u < NG; ++u) {
+        lds_words<NB>(vs[u], rec + u * kRec + q4_v_scale(NB, 2 * g));
+        if (kMasked) {
+            // what the last query does not see is whatever the page holds: its scales are dropped
+            // here (0), and each query's own mask below takes its score
+            int most = sees[0];
 #pragma unroll
-    for (int r = 0; r < 2 * NB; r += run) {
-        uint32_t part[run];
-        lds_words(part, rec + 9 * hd + ((r / run) * 32 + 4 * g + t) * run * 4);
+            for (int j = 1; j < NT; ++j) most = max(most, sees[j]);
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
 #pragma unroll
-        for (int i = 0; i < run; ++i) vw[r + i] = part[i];
+            for (int i = 0; i < 2; ++i)
+                if (16 * u + 2 * g + i >= most) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const int k = i * NB + b;
+                        vs[u][k >> 1] &= (k & 1) ? 0x0000ffffu : 0xffff0000u;
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (16 * u + 2 * g + i >= sees[j]) s[j][2 * u + i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const uint32_t v = vs[u][i] & 0x7fff7fffu;
+            asm("max.f16x2 %0, %0, %1;" : "+r"(dm) : "r"(v));
+        }
+    }
+    // ---- running maximum of log2 p + log2 |d|; the exponent above the largest |d| (0: of the smallest f16)
+    const float2 dm2 = unpack_f16(dm);
+    const float ev = static_cast<float>((__float_as_int(fmaxf(fmaxf(dm2.x, dm2.y), 0x1p-25f)) >> 23) - 126);
+    float y[NT];
+    bool grown = false;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        float top = s[j][0];
+#pragma unroll
+        for (int i = 1; i < 2 * NG; ++i) top = fmaxf(top, s[j][i]);
+        y[j] = fmaf(top, w.unit[j], ev);
+        grown |= y[j] > w.m[j] + kLazy;
+    }
+    if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float top = y[j];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float m = top > w.m[j] + kLazy ? top : w.m[j];
+            const float f = ex2(w.m[j] - m);
+            w.m[j] = m;
+            w.l[j] *= f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w.o[j][b][hf][k] *= f;
+                    if (w.flushed) {
+                        float *p = w.row + 4 * j * (hd + kPad) + 32 * b + 16 * hf + g;
+                        p[0] *= f;
+                        p[8] *= f;
+                    }
+                }
+        }
+    }
+    // ---- weights p, then the sums of V
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const float off = kBias - w.m[j];
+#pragma unroll
+        for (int i = 0; i < 2 * NG; ++i) {
+            s[j][i] = ex2(fmaf(s[j][i], w.unit[j], off));
+            w.l[j] += s[j][i];
+        }
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        // weights p * d of tokens (0, 2) and (1, 3), in two pieces
-        const float d0 = half_at(vs, b), d1 = half_at(vs, NB + b), d2 = half_at(vs, 2 * NB + b),
-                    d3 = half_at(vs, 3 * NB + b);
-        const float x0 = p[0] * d0, x1 = p[1] * d1, x2 = p[2] * d2, x3 = p[3] * d3;
-        uint32_t pa[4];
-        pa[0] = pack_f16(x0, x2);
-        pa[2] = pack_f16(x1, x3);
-        const float2 h0 = unpack_f16(pa[0]), h1 = unpack_f16(pa[2]);
-        pa[1] = pack_f16(x0 - h0.x, x2 - h0.y);
-        pa[3] = pack_f16(x1 - h1.x, x3 - h1.y);
+    for (int u = 0; u < NG; ++u) {
+        uint32_t vw[2 * NB];
+        constexpr int run = q4_v_run(NB);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t v = vw[2 * b + k], u = v >> 8;
-            mma16816(w.o[b][2 * k], pa, low_codes(v), low_codes(u), w.o[b][2 * k]);
-            mma16816(w.o[b][2 * k + 1], pa, high_codes(v), high_codes(u), w.o[b][2 * k + 1]);
+        for (int r = 0; r < 2 * NB; r += run)
+            lds_words<run>(vw + r, rec + u * kRec + 9 * hd + ((r / run) * 32 + 4 * g + t) * run * 4);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const float d0 = half_at(vs[u], b), d1 = half_at(vs[u], NB + b);
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float x0 = s[j][2 * u] * d0, x1 = s[j][2 * u + 1] * d1;
+                if (kMasked) {  // a NaN or infinite scale that another query sees
+                    if (16 * u + 2 * g >= sees[j]) x0 = 0.0f;
+                    if (16 * u + 2 * g + 1 >= sees[j]) x1 = 0.0f;
+                }
+                const uint32_t h = pack_f16(x0, x1);
+                const float2 hf = unpack_f16(h);
+                const uint32_t l = pack_f16(x0 - hf.x, x1 - hf.y);
+                pb[j][0] = transposed(__byte_perm(h, l, 0x5410));
+                pb[j][1] = transposed(__byte_perm(h, l, 0x7632));
+            }
+            const uint32_t w0 = vw[2 * b], w1 = vw[2 * b + 1], h0 = w0 >> 8, h1 = w1 >> 8;
+            const uint32_t lo[4] = {low_codes(w0), low_codes(w1), low_codes(h0), low_codes(h1)};
+            const uint32_t hi[4] = {high_codes(w0), high_codes(w1), high_codes(h0), high_codes(h1)};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mma16816(w.o[j][b][0], lo, pb[j][0], pb[j][1], w.o[j][b][0]);
+                mma16816(w.o[j][b][1], hi, pb[j][0], pb[j][1], w.o[j][b][1]);
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------- shared memory
-// stages of W records | the warps' sums, their (m, l) | mbarriers, flags, counts (256 bytes) |
+// stages of 2 W records | the warps' sums, their (m, l) | mbarriers, flags, counts (256 bytes) |
 // the parts of an item | the line's prefix
-constexpr int kPad = 8;  // floats after a row of sums: its 8 rows fall into other banks
 constexpr int kMaxStages = 10;
 constexpr int kMaxCtas = 512;  // of the grid
 template <int NB>
 struct Layout {
     static constexpr int W = consumers(NB), hd = 32 * NB, rows = 8 * W;
-    static constexpr int stage = W * q4_record_bytes(hd);
+    static constexpr int stage = 2 * W * q4_record_bytes(hd);
     static constexpr int sums = rows * (hd + kPad) * 4;
     static constexpr int fixed = sums + rows * 8 + 256 + kMaxCtas * 2;  // and 8 bytes for each request and one
     static constexpr int64_t part = (int64_t)rows * (hd + 2);  // floats of a partial record: sums, then (m, l)
@@ -522,6 +563,79 @@ __device__ __forceinline__ void write_row4(const PagedAttnArgs &a, float4 v, boo
                 qd[row * (q_pad / 32) + col / 32] = d;
                 qs[row * (q_pad / 32) + col / 32] = __fmul_rn(d, (float)sum);
             }
+        }
+    }
+}
+
+// A consumer warp's share of the current part of an item: its sums to shared memory.
+template <int NB, int NT, int NG>
+__device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, const uint8_t *ring, int stages, uint64_t *full,
+                                     uint64_t *empty, volatile int *gave_up, RingPos &pos, float *sums, float2 *ml, int warp,
+                                     int lane)
+{
+    using L = Layout<NB>;
+    constexpr int W = L::W, hd = L::hd;
+    const int g = lane >> 2, t = lane & 3, group = a.n_heads / a.kv.n_kv_heads;
+    const int rg = w.q.rg, copies = W / rg;
+    const int qg = warp % rg, ks = warp / rg;
+    const int row8 = (w.it * rg + qg) * 8;  // this warp's first query row
+    const int n_rows = w.q.m * group;       // of the request and kv head
+    const bool idle = row8 >= n_rows || ks >= copies;
+    // tokens that a row sees (rows beyond the last see what the last sees, and are not
+    // written): this lane's rows, the warp's first and its last
+    const int before = w.q.n - w.q.m + 1;
+    auto tokens_of = [&](int row) { return max(before + min(row, n_rows - 1) / group, 0); };
+    int sees[NT];
+    const float *ptr[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        sees[j] = tokens_of(row8 + 4 * j + t);
+        const int my = row8 + 4 * j + (g >> 1), tok = my / group;
+        ptr[j] = my < n_rows ? a.q + (w.q.row0 + tok) * a.ld_q + (int64_t)(w.h * group + (my - tok * group)) * hd : nullptr;
+    }
+    const int all_see = tokens_of(row8), any_see = idle ? 0 : tokens_of(row8 + 4 * NT - 1);
+    const int slot = (ks * rg + qg) * 8 + t;  // of this lane's row, copy ks
+    Warp<NB, NT> acc;
+    acc.row = sums + slot * (hd + kPad);
+    load_query<NB, NT>(acc, ptr, a.scale, g, t);
+    for (int tile = w.lo; tile < w.hi; ++tile) {
+        bool ok = __all_sync(0xffffffffu, !*gave_up);
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(full + pos.s, pos.par))) {
+            ok = false;
+            *gave_up = 1;
+            set_error(a.err, DEV_TIMEOUT_PAGED);
+        }
+        if (ok) {
+            const uint8_t *st = ring + (size_t)pos.s * L::stage;
+            // NG groups at a time; of the item's runs of NG groups every copies-th falls to this warp
+            constexpr int runs = 2 * W / NG;
+            const int r0 = tile * runs;
+            for (int r = copies == runs ? ks : (ks + copies - r0 % copies) % copies; r < runs; r += copies) {
+                const int t0 = (r0 + r) * NG * 16;
+                if (t0 >= any_see) break;
+                const uint8_t *rec = st + r * NG * q4_record_bytes(hd);
+                int left[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) left[j] = sees[j] - t0;
+                if (t0 + 16 * NG <= all_see)
+                    attend<NB, NT, NG, false>(acc, rec, g, t, left);
+                else
+                    attend<NB, NT, NG, true>(acc, rec, g, t, left);
+                if ((acc.since += NG) >= kFlush) flush(acc, g);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + pos.s);
+        }
+        ring_next(pos, stages);
+    }
+    if (ks < copies) {
+        flush(acc, g);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float l = acc.l[j];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (g == 0) ml[slot + 4 * j] = make_float2(acc.m[j], l);
         }
     }
 }
@@ -607,8 +721,8 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
         while (more && !*gave_up) {
             const int32_t *row = a.table + (int64_t)w.s * a.table_ld;
             for (int tile = w.lo; tile < w.hi; ++tile) {
-                const int t0 = tile * W * 16;
-                const int groups = min(W, (w.tokens - t0 + 15) >> 4);
+                const int t0 = tile * W * 32;
+                const int groups = min(2 * W, (w.tokens - t0 + 15) >> 4);
                 // lane i copies the part of the tile that lies in its i-th page
                 const int first = (t0 >> 4) >> lg;  // page of the tile's first group
                 const int in = (t0 >> 4) & (per_page - 1);
@@ -651,7 +765,6 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
     }
 
     // -------------------------------------------------------------------- consumers
-    const int g = lane >> 2, t = lane & 3;
     const int q_pad = (a.n_heads * hd + 255) / 256 * 256;
     RingPos pos{0, 0};
     bool more = true;
@@ -659,56 +772,11 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
         if (walk_has(w)) {
             // rg row groups, copies warps for each, the others idle
             const int rg = w.q.rg, copies = W / rg, row_it = w.it * 8 * rg;
-            const int qg = warp % rg, ks = warp / rg;
-            const int row8 = row_it + qg * 8;  // this warp's first query row
             const int n_rows = w.q.m * group;  // of the request and kv head
-            // this lane's query row, and how many tokens it sees
-            const int my = row8 + g;
-            const int tok = my / group;
-            const bool live = my < n_rows;
-            const int64_t row = w.q.row0 + tok;
-            const int col0 = (w.h * group + (my - tok * group)) * hd;
-            // what it sees, what all of the warp's rows see and what any of them does (rows
-            // beyond the last see what the last sees, and are not written)
-            const int before = w.q.n - w.q.m + 1;
-            const int sees = max(before + min(my, n_rows - 1) / group, 0);
-            const int all_see = max(before + min(row8, n_rows - 1) / group, 0);
-            const int any_see = row8 < n_rows && ks < copies ? max(before + min(row8 + 7, n_rows - 1) / group, 0) : 0;
-            Warp<NB> acc;
-            const int slot = (ks * rg + qg) * 8 + g;  // of this lane's row, copy ks
-            acc.row = sums + slot * ld;
-            load_query<NB>(acc, live ? a.q + row * a.ld_q + col0 : nullptr, a.scale, t);
-            for (int tile = w.lo; tile < w.hi; ++tile) {
-                bool ok = __all_sync(0xffffffffu, !*gave_up);
-                if (ok && !__all_sync(0xffffffffu, mbar_wait(full + pos.s, pos.par))) {
-                    ok = false;
-                    *gave_up = 1;
-                    set_error(a.err, DEV_TIMEOUT_PAGED);
-                }
-                if (ok) {
-                    const uint8_t *st = ring + (size_t)pos.s * kStage;
-                    // the first of the tile's groups whose number in the item falls to this warp
-                    const int g0 = tile * W;
-                    for (int gr = copies == W ? ks : (ks + copies - g0 % copies) % copies; gr < W; gr += copies) {
-                        const int t0 = (g0 + gr) * 16;
-                        if (t0 >= any_see) break;
-                        if (t0 + 16 <= all_see)
-                            tokens16<NB, false>(acc, st + gr * q4_record_bytes(hd), g, t, 16);
-                        else
-                            tokens16<NB, true>(acc, st + gr * q4_record_bytes(hd), g, t, sees - t0);
-                        if (++acc.since == kFlush) flush(acc, t);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(empty + pos.s);
-                }
-                ring_next(pos, stages);
-            }
-            // ---- the warps' sums
-            if (ks < copies) {
-                flush(acc, t);
-                const float l = quad_sum(acc.l);
-                if (t == 0) ml[slot] = make_float2(acc.m, l);
-            }
+            if (n_rows <= 4)
+                work<NB, 1, 2>(a, w, ring, stages, full, empty, gave_up, pos, sums, ml, warp, lane);
+            else
+                work<NB, 2, 1>(a, w, ring, stages, full, empty, gave_up, pos, sums, ml, warp, lane);
             consumer_sync<W>();
             const int rows_item = min(8 * rg, n_rows - row_it);
             const bool whole = w.lo == 0 && w.hi == w.tiles;
