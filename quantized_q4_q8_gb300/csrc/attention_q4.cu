@@ -26,17 +26,18 @@
 // leave that range, by 2^8 over the maximum, and not before.
 //
 // Work.  An item is (request, kv head, up to 8 W query rows: token-major, the group's
-// heads within a token); it reads tiles of 2 W groups of 16 tokens.  All items' tiles,
-// weighted by their cost, are one line that the CTAs (two for each SM) share evenly, so
-// that one long request or many ragged ones load all SMs alike; a CTA whose share ends
-// within an item leaves its sums in the workspace and the CTA that finishes last adds them
-// up, in the order of the tiles (the result does not depend on which one it is).
-// Within a CTA the W consumer warps share a tile: with up to 8 query rows each takes two
-// groups of 16 tokens (with up to 4, both at once), with 8 W each takes 8 rows; a producer
-// warp copies records into a ring of stages, a page at a time, with the bulk-copy engine.
+// heads within a token); it reads units of 32 tokens.  All items' units, weighted by
+// their cost, are one line that the CTAs (two for each SM) share evenly, so that one long
+// request or many ragged ones load all SMs alike; a CTA whose share ends within an item
+// leaves its sums in the workspace and the CTA that finishes last adds them up, in the order of
+// the units (the result does not depend on which one it is).  Of a CTA's W consumer
+// warps, W / (row groups of 8) work a row group, each its own units; with up to 4 rows
+// a warp works both groups of 16 tokens of a unit at once.  A producer warp copies units into a ring
+// of slots with the bulk-copy engine, a lane for a unit.
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "mma_f16.cuh"
 #include "paged_q4.cuh"
@@ -47,9 +48,12 @@ namespace rz {
 namespace {
 
 // Consumer warps W of a CTA, two CTAs on an SM: 5 and a producer are 3 warps a scheduler, 168
-// registers a thread; heads of over 128 values need 255, and 3 and a producer.
+// registers a thread (7, with 128 registers: 64 requests of 16384 tokens take 130 us instead
+// of 122, a chunk of 1000 rows 849 instead of 699); heads of over 128 values need 255, and 3 and
+// a producer.
 __host__ __device__ constexpr int consumers(int nb) { return nb <= 4 ? 5 : 3; }
 constexpr int kPad = 8;     // floats after a row of sums: its 4 rows fall into other banks
+constexpr int kUnit = 32;    // tokens of a unit
 constexpr int kFlush = 32;  // groups of 16 tokens summed in the tensor cores' accumulators at a time
 constexpr float kLazy = 8.0f;  // weights may grow by 2^8 over the running maximum
 constexpr float kBias = 7.0f;  // log2 of a weight p * |d| at the running maximum
@@ -99,45 +103,61 @@ struct Seq {
 
 // Row groups of an item: as few as hold the request's rows, else one for each warp.
 template <int W>
-__device__ __forceinline__ int row_groups(int64_t rows)
+__device__ __forceinline__ int row_groups(int rows)
 {
     return rows <= 8 ? 1 : rows <= 16 && W > 3 ? 2 : W;
 }
 
-template <int W>
-__device__ __forceinline__ Seq read_seq(const PagedAttnArgs &a, int s, bool &bad)
+// What shared memory holds of a request: first row, rows, held tokens (checked).
+struct SeqRow {
+    int row0, m, n;
+};
+
+__device__ __forceinline__ SeqRow read_seq(const PagedAttnArgs &a, int s, bool &bad)
 {
-    const int c0 = a.cu_rows[s], c1 = a.cu_rows[s + 1];
+    const int c0 = a.cu_rows[s], c1 = a.cu_rows[s + 1], n = a.kv_len[s];
     const int64_t most = (int64_t)a.max_blocks << (a.kv.page_log + 4);
-    Seq q;
-    q.n = a.kv_len[s];
-    if (c0 < 0 || c1 < c0 || c1 > a.n_rows || q.n > most) bad = true;
     const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.n_rows;
-    q.row0 = ok ? c0 : 0;
-    q.m = ok ? c1 - c0 : 0;
-    q.n = q.n > most ? 0 : max(q.n, 0);
-    const int64_t rows = (int64_t)q.m * (a.n_heads / a.kv.n_kv_heads);
+    if (!ok || n > most) bad = true;
+    return SeqRow{ok ? c0 : 0, ok ? c1 - c0 : 0, n > most ? 0 : max(n, 0)};
+}
+
+template <int W>
+__device__ __forceinline__ Seq make_seq(const SeqRow &r, int group)
+{
+    Seq q;
+    q.row0 = r.row0;
+    q.m = r.m;
+    q.n = r.n;
+    const int rows = q.m * group;
     q.rg = row_groups<W>(rows);
-    q.items = static_cast<int>((rows + 8 * q.rg - 1) / (8 * q.rg));
+    q.items = (rows + 8 * q.rg - 1) / (8 * q.rg);
     return q;
 }
 
 // Tokens that item it of a request sees (its last row's).
 __device__ __forceinline__ int item_tokens(const Seq &q, int group, int it)
 {
-    const int64_t last = min((int64_t)(it + 1) * 8 * q.rg - 1, (int64_t)q.m * group - 1) / group;
+    const unsigned last = static_cast<unsigned>(min((it + 1) * 8 * q.rg, q.m * group) - 1) / static_cast<unsigned>(group);
     return max(q.n - q.m + static_cast<int>(last) + 1, 0);
 }
-template <int W>
-__device__ __forceinline__ int item_tiles(const Seq &q, int group, int it)
+__device__ __forceinline__ int item_units(const Seq &q, int group, int it)
 {
-    return (item_tokens(q, group, it) + 32 * W - 1) / (32 * W);
+    return (item_tokens(q, group, it) + kUnit - 1) / kUnit;
 }
-// Cost of a tile, and of an item's start and end, in halves of a tile of 8 query rows.
-__device__ __forceinline__ int tile_cost(int rg) { return rg == 1 ? 2 : rg == 2 ? 5 : 2 * rg; }
-constexpr int kItemCost = 4;
+// Cost of a unit, which one of W / rg warps works while the others work the next ones; of
+// an item's start and end; and of what a CTA is worth starting for (a unit for each warp).
+template <int W>
+__device__ __forceinline__ int unit_cost(int rg)
+{
+    return 2 * W / (W / rg);
+}
+template <int W>
+constexpr int kItemCost = 4 * W;
+template <int W>
+constexpr int kShare = 2 * W;
 
-// The line, shared by as many CTAs as have a tile each: CTA c's share begins at
+// The line, shared by as many CTAs as are worth starting: CTA c's share begins at
 // c * step + c * rest / ctas.
 struct Line {
     int64_t total, step;
@@ -147,11 +167,12 @@ struct Line {
         return c * step + static_cast<unsigned>(c * rest) / static_cast<unsigned>(ctas);
     }
 };
+template <int W>
 __device__ __forceinline__ Line make_line(int64_t total, int grid)
 {
     Line l;
     l.total = total;
-    l.ctas = total < 2 * (int64_t)grid ? max(1, static_cast<int>(total) / 2) : grid;
+    l.ctas = total < kShare<W> * (int64_t)grid ? max(1, static_cast<int>(total) / kShare<W>) : grid;
     l.step = total < (1ll << 31) ? static_cast<unsigned>(total) / static_cast<unsigned>(l.ctas) : total / l.ctas;
     l.rest = static_cast<int>(total - l.step * l.ctas);
     return l;
@@ -163,35 +184,37 @@ struct Walk {
     int64_t at;      // where the current item begins
     Seq q;
     int s, h, it;
-    int tokens, tiles, lo, hi;  // the current item's tokens and tiles, the part [lo, hi) of them
+    int tokens, units, lo, hi;  // the current item's tokens and units, the part [lo, hi) of them
 };
 
 template <int W>
 __device__ __forceinline__ int64_t item_span(const Seq &q, int group, int it)
 {
-    return kItemCost + (int64_t)item_tiles<W>(q, group, it) * tile_cost(q.rg);
+    return kItemCost<W> + (int64_t)item_units(q, group, it) * unit_cost<W>(q.rg);
 }
-// The first tile at or after offset x of an item (kItemCost, then tiles).
-__device__ __forceinline__ int tile_at(int64_t x, int tiles, int cost)
+// The first unit at or after offset x of an item (kItemCost, then units).
+template <int W>
+__device__ __forceinline__ int unit_at(int64_t x, int units, int cost)
 {
-    if (x <= kItemCost) return 0;
-    if (x >= kItemCost + (int64_t)tiles * cost) return tiles;
-    return static_cast<unsigned>(x - kItemCost + cost - 1) / static_cast<unsigned>(cost);
+    if (x <= kItemCost<W>) return 0;
+    if (x >= kItemCost<W> + (int64_t)units * cost) return units;
+    return static_cast<unsigned>(x - kItemCost<W> + cost - 1) / static_cast<unsigned>(cost);
 }
 
 template <int W>
 __device__ __forceinline__ void load_item(Walk &w, const PagedAttnArgs &a, int group)
 {
     w.tokens = item_tokens(w.q, group, w.it);
-    w.tiles = (w.tokens + 32 * W - 1) / (32 * W);
-    const int cost = tile_cost(w.q.rg);
-    w.lo = tile_at(w.x0 - w.at, w.tiles, cost);
-    w.hi = tile_at(w.x1 - w.at, w.tiles, cost);
+    w.units = (w.tokens + kUnit - 1) / kUnit;
+    const int cost = unit_cost<W>(w.q.rg);
+    w.lo = unit_at<W>(w.x0 - w.at, w.units, cost);
+    w.hi = unit_at<W>(w.x1 - w.at, w.units, cost);
 }
 
 // To the first item of the share.  pre[s]: the line before request s.
 template <int W>
-__device__ __forceinline__ bool walk_begin(Walk &w, const PagedAttnArgs &a, const Line &line, const int64_t *pre, int group)
+__device__ __forceinline__ bool walk_begin(Walk &w, const PagedAttnArgs &a, const Line &line, const int64_t *pre, const SeqRow *seqs,
+                                           int group)
 {
     if (line.total == 0 || blockIdx.x >= line.ctas) return false;
     w.x0 = line.begin(blockIdx.x);
@@ -204,8 +227,7 @@ __device__ __forceinline__ bool walk_begin(Walk &w, const PagedAttnArgs &a, cons
         else hi = mid;
     }
     w.s = lo;
-    bool bad = false;
-    w.q = read_seq<W>(a, w.s, bad);
+    w.q = make_seq<W>(seqs[w.s], group);
     const int64_t span = pre[lo + 1] - pre[lo], in = w.x0 - pre[lo];
     int64_t head;
     if (span < (1ll << 31)) {
@@ -226,7 +248,7 @@ __device__ __forceinline__ bool walk_begin(Walk &w, const PagedAttnArgs &a, cons
     return true;
 }
 template <int W>
-__device__ __forceinline__ bool walk_next(Walk &w, const PagedAttnArgs &a, int group)
+__device__ __forceinline__ bool walk_next(Walk &w, const PagedAttnArgs &a, const SeqRow *seqs, int group)
 {
     w.at += item_span<W>(w.q, group, w.it);
     if (w.at >= w.x1) return false;
@@ -234,21 +256,20 @@ __device__ __forceinline__ bool walk_next(Walk &w, const PagedAttnArgs &a, int g
         w.it = 0;
         if (++w.h == a.kv.n_kv_heads) {
             w.h = 0;
-            bool bad = false;
             do {
                 if (++w.s >= a.n_seqs) return false;
-                w.q = read_seq<W>(a, w.s, bad);
+                w.q = make_seq<W>(seqs[w.s], group);
             } while (w.q.items == 0);
         }
     }
     load_item<W>(w, a, group);
     return true;
 }
-// Whether this CTA has something to do for the current item: tiles, or an item without
+// Whether this CTA has something to do for the current item: units, or an item without
 // any that begins in its share.
 __device__ __forceinline__ bool walk_has(const Walk &w)
 {
-    return w.lo < w.hi || (w.tiles == 0 && w.at >= w.x0);
+    return w.lo < w.hi || (w.units == 0 && w.at >= w.x0);
 }
 
 // ---------------------------------------------------------------- one warp's sums
@@ -525,16 +546,16 @@ __device__ __forceinline__ void attend(Warp<NB, NT> &w, const uint8_t *rec, int 
 }
 
 // ---------------------------------------------------------------- shared memory
-// stages of 2 W records | the warps' sums, their (m, l) | mbarriers, flags, counts (256 bytes) |
-// the parts of an item | the line's prefix
-constexpr int kMaxStages = 10;
+// slots of 2 records | the warps' sums, their (m, l) | mbarriers, flags, counts (512 bytes) |
+// the parts of an item | the line's prefix | the requests
+constexpr int kMaxSlots = 24;
 constexpr int kMaxCtas = 512;  // of the grid
 template <int NB>
 struct Layout {
     static constexpr int W = consumers(NB), hd = 32 * NB, rows = 8 * W;
-    static constexpr int stage = 2 * W * q4_record_bytes(hd);
+    static constexpr int slot = 2 * q4_record_bytes(hd);
     static constexpr int sums = rows * (hd + kPad) * 4;
-    static constexpr int fixed = sums + rows * 8 + 256 + kMaxCtas * 2;  // and 8 bytes for each request and one
+    static constexpr int fixed = sums + rows * 8 + 512 + kMaxCtas * 2;  // and 20 bytes for each request and 8
     static constexpr int64_t part = (int64_t)rows * (hd + 2);  // floats of a partial record: sums, then (m, l)
 };
 
@@ -567,9 +588,26 @@ __device__ __forceinline__ void write_row4(const PagedAttnArgs &a, float4 v, boo
     }
 }
 
+// n slots on
+__device__ __forceinline__ void ring_advance(RingPos &r, int n, int slots)
+{
+    const unsigned s = r.s + n, laps = s < static_cast<unsigned>(slots) ? 0 : s / static_cast<unsigned>(slots);
+    r.s = s - laps * slots;
+    r.par ^= laps & 1;
+}
+// the same for n <= slots
+__device__ __forceinline__ void ring_step(RingPos &r, int n, int slots)
+{
+    r.s += n;
+    if (r.s >= slots) {
+        r.s -= slots;
+        r.par ^= 1u;
+    }
+}
+
 // A consumer warp's share of the current part of an item: its sums to shared memory.
 template <int NB, int NT, int NG>
-__device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, const uint8_t *ring, int stages, uint64_t *full,
+__device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, const uint8_t *ring, int slots, uint64_t *full,
                                      uint64_t *empty, volatile int *gave_up, RingPos &pos, float *sums, float2 *ml, int warp,
                                      int lane)
 {
@@ -595,39 +633,39 @@ __device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, cons
     }
     const int all_see = tokens_of(row8), any_see = idle ? 0 : tokens_of(row8 + 4 * NT - 1);
     const int slot = (ks * rg + qg) * 8 + t;  // of this lane's row, copy ks
+    // a unit's readers together arrive W times on its slot's barrier
+    const int arrive = qg == 0 ? W + 1 - min(rg, (n_rows - w.it * rg * 8 + 7) >> 3) : 1;
     Warp<NB, NT> acc;
     acc.row = sums + slot * (hd + kPad);
     load_query<NB, NT>(acc, ptr, a.scale, g, t);
-    for (int tile = w.lo; tile < w.hi; ++tile) {
-        bool ok = __all_sync(0xffffffffu, !*gave_up);
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(full + pos.s, pos.par))) {
-            ok = false;
+    RingPos mine = pos;
+    ring_step(mine, ks, slots);
+    for (int u = idle || __any_sync(0xffffffffu, *gave_up) ? w.hi : w.lo + ks; u < w.hi; u += copies) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full + mine.s, mine.par))) {
             *gave_up = 1;
             set_error(a.err, DEV_TIMEOUT_PAGED);
+            break;
         }
-        if (ok) {
-            const uint8_t *st = ring + (size_t)pos.s * L::stage;
-            // NG groups at a time; of the item's runs of NG groups every copies-th falls to this warp
-            constexpr int runs = 2 * W / NG;
-            const int r0 = tile * runs;
-            for (int r = copies == runs ? ks : (ks + copies - r0 % copies) % copies; r < runs; r += copies) {
-                const int t0 = (r0 + r) * NG * 16;
-                if (t0 >= any_see) break;
-                const uint8_t *rec = st + r * NG * q4_record_bytes(hd);
-                int left[NT];
+        const uint8_t *st = ring + (size_t)mine.s * L::slot;
+#pragma unroll 1
+        for (int r = 0; r < 2 / NG; ++r) {
+            const int t0 = u * kUnit + 16 * r;
+            if (t0 >= any_see) break;
+            const uint8_t *rec = st + r * q4_record_bytes(hd);
+            int left[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) left[j] = sees[j] - t0;
-                if (t0 + 16 * NG <= all_see)
-                    attend<NB, NT, NG, false>(acc, rec, g, t, left);
-                else
-                    attend<NB, NT, NG, true>(acc, rec, g, t, left);
-                if ((acc.since += NG) >= kFlush) flush(acc, g);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + pos.s);
+            for (int j = 0; j < NT; ++j) left[j] = sees[j] - t0;
+            if (t0 + 16 * NG <= all_see)
+                attend<NB, NT, NG, false>(acc, rec, g, t, left);
+            else
+                attend<NB, NT, NG, true>(acc, rec, g, t, left);
+            if ((acc.since += NG) >= kFlush) flush(acc, g);
         }
-        ring_next(pos, stages);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(empty + mine.s, arrive);
+        ring_step(mine, copies, slots);
     }
+    ring_advance(pos, w.hi - w.lo, slots);
     if (ks < copies) {
         flush(acc, g);
 #pragma unroll
@@ -642,23 +680,24 @@ __device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, cons
 
 template <int NB>
 __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
-    paged_attention_kernel(const __grid_constant__ PagedAttnArgs a, int stages)
+    paged_attention_kernel(const __grid_constant__ PagedAttnArgs a, int slots)
 {
     using L = Layout<NB>;
-    constexpr int W = L::W, hd = L::hd, ld = hd + kPad, kStage = L::stage;
+    constexpr int W = L::W, hd = L::hd, ld = hd + kPad, kSlot = L::slot;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem;
-    float *sums = reinterpret_cast<float *>(ring + (size_t)stages * kStage);
+    float *sums = reinterpret_cast<float *>(ring + (size_t)slots * kSlot);
     float2 *ml = reinterpret_cast<float2 *>(sums + L::sums / 4);
-    uint64_t *full = reinterpret_cast<uint64_t *>(ml + L::rows), *empty = full + kMaxStages;
-    int *flags = reinterpret_cast<int *>(empty + kMaxStages);  // [0] a wait ran out, [1] this CTA adds the parts up
+    uint64_t *full = reinterpret_cast<uint64_t *>(ml + L::rows), *empty = full + kMaxSlots;
+    int *flags = reinterpret_cast<int *>(empty + kMaxSlots);  // [0] a wait ran out, [1] this CTA adds the parts up
     int *part_count = flags + 2;  // W
-    int16_t *part_list = reinterpret_cast<int16_t *>(reinterpret_cast<uint8_t *>(full) + 256);
+    int16_t *part_list = reinterpret_cast<int16_t *>(reinterpret_cast<uint8_t *>(full) + 512);
     int64_t *pre = reinterpret_cast<int64_t *>(part_list + kMaxCtas);
+    SeqRow *seqs = reinterpret_cast<SeqRow *>(pre + a.n_seqs + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = a.kv.n_kv_heads, group = a.n_heads / K;
     if (tid == 0) {
-        for (int i = 0; i < stages; ++i) {
+        for (int i = 0; i < slots; ++i) {
             mbar_init(full + i, 1);
             mbar_init(empty + i, W);
         }
@@ -676,7 +715,8 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
         bool bad = false;
         if (tid < W * 32)
             for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
-                const Seq q = read_seq<W>(a, i, bad);
+                seqs[i] = read_seq(a, i, bad);
+                const Seq q = make_seq<W>(seqs[i], group);
                 int64_t span = 0;
                 for (int it = 0; it < q.items; ++it) span += item_span<W>(q, group, it);
                 pre[i + 1] = span * K;
@@ -705,59 +745,67 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
 
     volatile int *gave_up = flags;
     Walk w;
-    const Line line = make_line(pre[a.n_seqs], gridDim.x);
-    const bool any = walk_begin<W>(w, a, line, pre, group);
+    const Line line = make_line<W>(pre[a.n_seqs], gridDim.x);
+    const bool any = walk_begin<W>(w, a, line, pre, seqs, group);
     if (!any) return;  // the same for the whole CTA
 
     if (warp == W) {
         // ---------------------------------------------------------------- producer
-        const int lg = a.kv.page_log, per_page = 1 << lg;  // groups of 16 tokens in a page
-        const int64_t head_bytes = (int64_t)q4_record_bytes(hd) << lg;
+        const int lg = a.kv.page_log;
+        constexpr int kRec = q4_record_bytes(hd);
+        const int64_t head_bytes = (int64_t)kRec << lg;
         RingPos pos{0, 0};
         int issued = 0;
         bool more = true;
         // the step's keys and values were written by another kernel through the generic proxy
         asm volatile("fence.proxy.async;" ::: "memory");
-        while (more && !*gave_up) {
+        while (more) {
             const int32_t *row = a.table + (int64_t)w.s * a.table_ld;
-            for (int tile = w.lo; tile < w.hi; ++tile) {
-                const int t0 = tile * W * 32;
-                const int groups = min(2 * W, (w.tokens - t0 + 15) >> 4);
-                // lane i copies the part of the tile that lies in its i-th page
-                const int first = (t0 >> 4) >> lg;  // page of the tile's first group
-                const int in = (t0 >> 4) & (per_page - 1);
-                const int g0 = lane == 0 ? 0 : (lane << lg) - in, g1 = min(groups, ((lane + 1) << lg) - in);
-                int32_t page = 0;
-                if (g0 < g1) {
-                    page = row[first + lane];
-                    if (page < 0 || page >= a.kv.n_pages) {
-                        set_error(a.err, DEV_BAD_PAGE);
-                        page = 0;  // a page there is; the request's rows are not to be used
+            for (int u0 = w.lo; u0 < w.hi; u0 += W) {
+                // lane i copies unit u0 + i: two groups of 16 tokens, or the last one, of one page or two
+                const int n = min(W, w.hi - u0), u = u0 + lane;
+                const int g0 = 2 * u, groups = min(2, ((w.tokens + 15) >> 4) - g0);
+                RingPos mine = pos;
+                ring_step(mine, min(lane, W), slots);
+                int32_t page[2] = {0, 0};
+                if (lane < n) {
+                    page[0] = row[g0 >> lg];
+                    page[1] = lg == 0 && groups == 2 ? row[g0 + 1] : page[0];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (page[i] < 0 || page[i] >= a.kv.n_pages) {
+                            set_error(a.err, DEV_BAD_PAGE);
+                            page[i] = 0;  // a page there is; the request's rows are not to be used
+                        }
+                }
+                bool ok = !*gave_up;
+                if (lane < n && ok) ok = mbar_wait(empty + mine.s, mine.par ^ 1u);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (!*gave_up) set_error(a.err, DEV_TIMEOUT_PAGED);
+                    *gave_up = 1;
+                    more = false;
+                    break;
+                }
+                if (lane < n) {
+                    uint8_t *dst = ring + (size_t)mine.s * kSlot;
+                    const uint8_t *src = a.kv.pages + ((int64_t)page[0] * K + w.h) * head_bytes + (g0 & ((1 << lg) - 1)) * kRec;
+                    mbar_arrive_expect_tx(full + mine.s, groups * kRec);
+                    if (lg || groups == 1) {
+                        bulk_g2s(dst, src, groups * kRec, full + mine.s);
+                    } else {
+                        bulk_g2s(dst, src, kRec, full + mine.s);
+                        bulk_g2s(dst + kRec, a.kv.pages + ((int64_t)page[1] * K + w.h) * head_bytes, kRec, full + mine.s);
                     }
                 }
-                if (!mbar_wait(empty + pos.s, pos.par ^ 1u)) {
-                    *gave_up = 1;
-                    set_error(a.err, DEV_TIMEOUT_PAGED);
-                }
-                __syncwarp();
-                if (*gave_up) break;
-                uint8_t *dst = ring + (size_t)pos.s * kStage;
-                if (lane == 0) mbar_arrive_expect_tx(full + pos.s, groups * q4_record_bytes(hd));
-                __syncwarp();
-                if (g0 < g1)
-                    bulk_g2s(dst + g0 * q4_record_bytes(hd),
-                             a.kv.pages + ((int64_t)page * K + w.h) * head_bytes +
-                                 (int64_t)(lane == 0 ? in : 0) * q4_record_bytes(hd),
-                             (g1 - g0) * q4_record_bytes(hd), full + pos.s);
-                ++issued;
-                ring_next(pos, stages);
+                issued += n;
+                ring_step(pos, n, slots);
             }
-            more = walk_next<W>(w, a, group);
+            if (more) more = walk_next<W>(w, a, seqs, group);
         }
         // no copy outlives the CTA: after an abort, those that no consumer waits for any more are waited out
         if (*gave_up) {
-            for (int k = max(0, issued - stages); k < issued; ++k) {
-                const RingPos p = ring_pos(k, stages);
+            for (int k = max(0, issued - slots); k < issued; ++k) {
+                const RingPos p = ring_pos(k, slots);
                 if (!mbar_wait(full + p.s, p.par)) set_error(a.err, DEV_TIMEOUT_DRAIN);
             }
         }
@@ -774,12 +822,12 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
             const int rg = w.q.rg, copies = W / rg, row_it = w.it * 8 * rg;
             const int n_rows = w.q.m * group;  // of the request and kv head
             if (n_rows <= 4)
-                work<NB, 1, 2>(a, w, ring, stages, full, empty, gave_up, pos, sums, ml, warp, lane);
+                work<NB, 1, 2>(a, w, ring, slots, full, empty, gave_up, pos, sums, ml, warp, lane);
             else
-                work<NB, 2, 1>(a, w, ring, stages, full, empty, gave_up, pos, sums, ml, warp, lane);
+                work<NB, 2, 1>(a, w, ring, slots, full, empty, gave_up, pos, sums, ml, warp, lane);
             consumer_sync<W>();
             const int rows_item = min(8 * rg, n_rows - row_it);
-            const bool whole = w.lo == 0 && w.hi == w.tiles;
+            const bool whole = w.lo == 0 && w.hi == w.units;
             const int quads = 8 * rg * (hd / 4);  // groups of 4 values of the item's rows
             float *part = a.part + (2 * (int64_t)blockIdx.x + (w.lo == 0)) * L::part;
             for (int i0 = 0; i0 < quads; i0 += W * 32) {
@@ -813,15 +861,15 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
                 }
             }
             if (!whole) {
-                // ---- the CTAs whose shares hold the item's tiles, in order; the last to arrive adds them up
-                const int cost = tile_cost(rg);
+                // ---- the CTAs whose shares hold the item's units, in order; the last to arrive adds them up
+                const int cost = unit_cost<W>(rg);
                 int c = static_cast<int>(w.at / max(line.step, (int64_t)1));  // at or after the CTA that holds w.at
                 c = min(c, line.ctas - 1);
                 while (line.begin(c) > w.at) --c;
                 int parts = 0;
                 for (int c0 = c; c0 < line.ctas; c0 += W * 32) {
                     const int k = c0 + tid;
-                    const int lo = tile_at(line.begin(k) - w.at, w.tiles, cost), hi = tile_at(line.begin(k + 1) - w.at, w.tiles, cost);
+                    const int lo = unit_at<W>(line.begin(k) - w.at, w.units, cost), hi = unit_at<W>(line.begin(k + 1) - w.at, w.units, cost);
                     const unsigned has = __ballot_sync(0xffffffffu, k < line.ctas && lo < hi);
                     consumer_sync<W>();  // the counts of the round before are read
                     if (lane == 0) part_count[warp] = __popc(has);
@@ -834,7 +882,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
                     }
                     // 2 k + 1: its part begins the item
                     if (has >> lane & 1) part_list[before + __popc(has & ((1u << lane) - 1))] = static_cast<int16_t>(2 * k + (lo == 0));
-                    if (line.begin(min(c0 + W * 32, line.ctas)) >= w.at + kItemCost + (int64_t)w.tiles * cost) break;
+                    if (line.begin(min(c0 + W * 32, line.ctas)) >= w.at + kItemCost<W> + (int64_t)w.units * cost) break;
                 }
                 __threadfence();
                 consumer_sync<W>();
@@ -897,7 +945,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
             }
             consumer_sync<W>();  // sums, ml and the flag are read
         }
-        more = walk_next<W>(w, a, group);
+        more = walk_next<W>(w, a, seqs, group);
     }
 }
 
@@ -907,13 +955,18 @@ template <int NB>
 cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
 {
     using L = Layout<NB>;
-    // half an SM's shared memory (228 KB, 1 KB of it for each CTA), as many stages as fit
+    // half an SM's shared memory (228 KB, 1 KB of it for each CTA), as many slots as fit
     const int most = 113 * 1024;
-    const int fixed = L::fixed + (a.n_seqs + 1) * 8;
-    const int stages = std::min(kMaxStages, (most - fixed) / L::stage);
-    const int bytes = stages * L::stage + fixed;
-    cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != cudaSuccess) return e;
+    const int fixed = L::fixed + a.n_seqs * 20 + 8;
+    const int slots = std::min(kMaxSlots, (most - fixed) / L::slot);
+    const int bytes = slots * L::slot + fixed;
+    static std::atomic<uint64_t> done{0};  // devices on which the kernel may have that much
+    const uint64_t bit = 1ull << (dev_info().device & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid_ctas());
     cfg.blockDim = dim3((L::W + 1) * 32);
@@ -924,7 +977,7 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = g_use_pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, paged_attention_kernel<NB>, a, stages);
+    return cudaLaunchKernelEx(&cfg, paged_attention_kernel<NB>, a, slots);
 }
 
 }  // namespace

@@ -30,38 +30,50 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = kPlanMaxSeqs / kThreads;  // requests of a thread: tid * kPer ..
+constexpr int kAhead = 8, kRows = 4;           // loads of a lane on their way at once
 
-// Inclusive prefix sum over the CTA's threads of one value each; tmp holds kWarps + 1 values.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *tmp, int lane, int warp)
+// Inclusive prefix sums over the CTA's threads of N values each; returns the totals in all.
+template <int N>
+__device__ __forceinline__ void block_scan(int64_t (&v)[N], int64_t (&all)[N], int64_t (*tmp)[kWarps], int lane, int warp)
 {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    __syncthreads();  // tmp of the scan before is read
-    if (lane == 31) tmp[warp] = v;
-    __syncthreads();
-    int64_t before = 0;
+    for (int k = 0; k < N; ++k) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) before += w < warp ? tmp[w] : 0;
-    return v + before;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v[k], o);
+            if (lane >= o) v[k] += u;
+        }
+        if (lane == 31) tmp[k][warp] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        int64_t before = 0;
+        all[k] = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const int64_t x = tmp[k][w];
+            all[k] += x;
+            before += w < warp ? x : 0;
+        }
+        v[k] += before;
+    }
 }
 
 __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_constant__ PlanArgs a)
 {
-    __shared__ int64_t tmp[kWarps];
+    __shared__ int64_t tmp[3][kWarps];
     __shared__ int32_t cu[kPlanMaxSeqs + 1];    // rows before request i
     __shared__ int32_t first[kPlanMaxSeqs];     // number of its first new page; -1: refused
     __shared__ int32_t cached[kPlanMaxSeqs], owned[kPlanMaxSeqs], back[kPlanMaxSeqs];
-    __shared__ int32_t last_cu;
+    __shared__ int32_t last_cu, all_handed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const cg::cluster_group cluster = cg::this_cluster();
     const int n_ctas = gridDim.x, cta = blockIdx.x;  // the grid is one cluster
     pdl_launch_dependents();
     pdl_wait();
 
-    if (tid == 0) last_cu = 0;
+    if (tid == 0) last_cu = all_handed = 0;
     const int64_t max_pages_seq = a.max_blocks;
     bool bad = false;
     int c[kPer], f[kPer], o[kPer], odd[kPer];
@@ -89,8 +101,16 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         bad = true;
         free0 = 0;
     }
-    // rows: the requests whose rows end beyond the last row have none
-    int64_t r = block_scan(rows, tmp, lane, warp) - rows;
+    // rows: the requests whose rows end beyond the last row have none.  Pages returned,
+    // and whether the stack has room for them
+    int64_t sums[2] = {rows, give}, totals[2];
+    block_scan(sums, totals, tmp, lane, warp);
+    int64_t r = sums[0] - rows, g = sums[1] - give;
+    int64_t total = free0 + totals[1];
+    if (total > a.n_pages) {
+        bad = true;
+        total = a.n_pages;
+    }
     int fits = 0;
     bool fit[kPer];
     int64_t at[kPer];
@@ -102,18 +122,8 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         if (fit[j]) fits = static_cast<int>(r);
         else if (f[j] > 0) bad = true;
     }
-    atomicMax(&last_cu, fits);
-    // pages returned, and whether the stack has room for them
-    const int64_t gave = block_scan(give, tmp, lane, warp);
-    int64_t g = gave - give;
-    __shared__ int64_t all_back;
-    if (tid == kThreads - 1) all_back = gave;
-    __syncthreads();
-    int64_t total = free0 + all_back;
-    if (total > a.n_pages) {
-        bad = true;
-        total = a.n_pages;
-    }
+    fits = __reduce_max_sync(0xffffffffu, fits);
+    if (lane == 0 && fits) atomicMax(&last_cu, fits);
     // pages needed
     int64_t need = 0, n[kPer];
     bool ok[kPer];
@@ -132,8 +142,10 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         if (!ok[j]) bad = true;
         need += n[j];
     }
-    int64_t p = block_scan(need, tmp, lane, warp) - need;
-    int64_t taken = 0;
+    int64_t upto[1] = {need}, wanted[1];
+    block_scan(upto, wanted, tmp + 2, lane, warp);  // and last_cu is whole
+    int64_t p = upto[0] - need;
+    int handed = 0;  // the pages of this and the served requests before it
     bool refused = false;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -142,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         p += n[j];
         const bool served = ok[j] && (n[j] == 0 || p <= total);
         if (ok[j] && !served) refused = true;
-        if (served) taken += n[j];
+        if (served && n[j]) handed = static_cast<int>(p);
         if (i < a.n_seqs) {
             cu[i] = fit[j] ? static_cast<int>(at[j]) : last_cu;
             cached[i] = c[j];
@@ -155,8 +167,8 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         n[j] = served ? n[j] : 0;
         ok[j] = served;
     }
-    const int64_t handed = block_scan(taken, tmp, lane, warp);
-    if (tid == kThreads - 1) all_back = handed;
+    handed = __reduce_max_sync(0xffffffffu, handed);
+    if (lane == 0 && handed) atomicMax(&all_handed, handed);
     if (tid == 0) cu[a.n_seqs] = last_cu;
     __syncthreads();
     if (cta == 0) {
@@ -167,8 +179,21 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
     for (int i = cta * kWarps + warp; i < a.n_seqs; i += n_ctas * kWarps) {
         if (back[i] < 0) continue;
         const int64_t to = free0 + back[i];
-        for (int b = lane; b < owned[i]; b += 32)
-            if (to + b < a.n_pages) a.free_pages[to + b] = a.table[i * a.table_ld + b];
+        const int32_t *row = a.table + i * a.table_ld;
+        const int n_back = static_cast<int>(min((int64_t)owned[i], a.n_pages - to));
+        for (int b0 = 0; b0 < n_back; b0 += 32 * kAhead) {
+            int32_t v[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int b = b0 + 32 * u + lane;
+                v[u] = b < n_back ? row[b] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int b = b0 + 32 * u + lane;
+                if (b < n_back) a.free_pages[to + b] = v[u];
+            }
+        }
     }
     // every CTA has read the state, and the stack is whole
     cluster.sync();
@@ -194,33 +219,46 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         }
         if (tid == 0) {
             a.cu_rows[a.n_seqs] = last_cu;
-            *a.free_count_out = static_cast<int>(total - all_back);
+            *a.free_count_out = static_cast<int>(total - all_handed);
         }
     }
     // rows
-    const int total_rows = cu[a.n_seqs];
-    for (int64_t row = (int64_t)cta * kThreads + tid; row < a.max_rows; row += (int64_t)n_ctas * kThreads) {
-        int32_t seq = -1, pos = -1;
-        int64_t slot = -1;
-        if (row < total_rows) {
-            int lo = 0, hi = a.n_seqs;  // cu[lo] <= row < cu[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (cu[mid] <= row) lo = mid;
-                else hi = mid;
-            }
-            seq = lo;
-            if (first[lo] >= 0) {
-                pos = cached[lo] + static_cast<int>(row - cu[lo]);
-                const int blk = pos / a.page_size;
-                const int32_t page = blk < owned[lo] ? a.table[lo * a.table_ld + blk]
-                                                     : page_number((int64_t)first[lo] + (blk - owned[lo]));
-                slot = (int64_t)page * a.page_size + pos % a.page_size;
+    const int total_rows = cu[a.n_seqs], page_log = __ffs(a.page_size) - 1;
+    // kRows at a time, so that their loads of the table are on their way together
+    for (int64_t row0 = (int64_t)cta * kThreads + tid; row0 < a.max_rows; row0 += (int64_t)n_ctas * kThreads * kRows) {
+        int32_t seq[kRows], pos[kRows];
+        int64_t page[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t row = row0 + (int64_t)u * n_ctas * kThreads;
+            seq[u] = pos[u] = -1;
+            page[u] = -1;
+            if (row < total_rows) {
+                int lo = 0, hi = a.n_seqs;  // cu[lo] <= row < cu[hi]
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (cu[mid] <= row) lo = mid;
+                    else hi = mid;
+                }
+                seq[u] = lo;
+                if (first[lo] >= 0) {
+                    pos[u] = cached[lo] + static_cast<int>(row - cu[lo]);
+                    const int blk = pos[u] >> page_log;
+                    const int32_t *from = blk < owned[lo] ? a.table + lo * a.table_ld + blk
+                                                          : a.free_pages + (total - 1 - first[lo] - (blk - owned[lo]));
+                    page[u] = __ldcg(from);
+                }
             }
         }
-        a.row_seq[row] = seq;
-        a.positions[row] = pos;
-        a.slots[row] = slot;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t row = row0 + (int64_t)u * n_ctas * kThreads;
+            if (row < a.max_rows) {
+                a.row_seq[row] = seq[u];
+                a.positions[row] = pos[u];
+                a.slots[row] = pos[u] < 0 ? -1 : (page[u] << page_log) + (pos[u] & (a.page_size - 1));
+            }
+        }
     }
 }
 

@@ -433,8 +433,12 @@ cudaError_t launch(const cudaLaunchConfig_t &cfg, const HeadsArgs &a, int nb)
 
 cudaError_t launch_qk_norm_rope(HeadsArgs &a, int64_t rows, int head_dim, float rope_theta, cudaStream_t s)
 {
+    // theta^(-2i/head_dim) as the product of two powers, i = 16 j + k: fewer calls of pow
+    double low[16], high[8];
+    for (int k = 0; k < 16; ++k) low[k] = pow((double)rope_theta, -2.0 * k / head_dim);
+    for (int j = 0; 16 * j < head_dim / 2; ++j) high[j] = pow((double)rope_theta, -32.0 * j / head_dim) * kInvTwoPi;
     for (int i = 0; i < head_dim / 2; ++i) {
-        const double turns = pow((double)rope_theta, -2.0 * i / head_dim) * kInvTwoPi;
+        const double turns = low[i % 16] * high[i / 16];
         a.turn[i] = static_cast<uint64_t>(static_cast<int64_t>((turns - floor(turns)) * 0x1p62)) << 2;
     }
     const int per_token = a.n_heads + (a.kv.pages ? 2 : 1) * a.n_kv_heads;

@@ -493,43 +493,53 @@ def kv_q4_page_bytes(page_size: int, n_kv_heads: int, head_dim: int) -> int:
     return n
 
 
-def _on_device(t, dtype, name, dim=None):
-    """A tensor of the current device, of this type (and number of dimensions)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _on_device(t, dtype, dim, dev, name):
+    """A CUDA tensor of device `dev`, of this type and number of dimensions."""
+    at = t.get_device() if hasattr(t, "get_device") else -1
+    if at < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if dim is not None and t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimension{'s' if dim > 1 else ''}, got {t.dim()}")
-    if t.device.index != torch.cuda.current_device():
+    if at != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimension{'s' if dim > 1 else ''}, got {t.dim()}")
     return t
 
 
-def _vector(t, dtype, n, name):
-    _on_device(t, dtype, name, 1)
-    if t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+def _vector(t, dtype, n, dev, name, more=False):
+    """The address of n contiguous values (or, with more, at least n)."""
+    _on_device(t, dtype, 1, dev, name)
+    have = t.shape[0]
+    if (have < n if more else have != n) or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous values")
-    return t
+    return t.data_ptr()
 
 
 def _row_ld(t, cols, name):
     """Row stride of a 2-D tensor of `cols` contiguous columns."""
     if t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must have {cols} contiguous columns")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+    return max(t.stride(0), cols) if t.shape[0] == 1 else t.stride(0)
 
 
-def _new(shape, dtype, device, stream):
+def _new(shape, dtype, dev, stream):
     """An output allocated for the stream that the call runs on."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _stream_on(stream, dev):
+    """The raw stream of a call on device `dev` (its current one unless given)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 class PagedKVQ4:
@@ -539,11 +549,12 @@ class PagedKVQ4:
     def __init__(self, pages, page_size: int, head_dim: int):
         import torch
         from ._lib import KvQ4Struct
-        _on_device(pages, torch.uint8, "pages", 3)
+        _on_device(pages, torch.uint8, 3, torch.cuda.current_device(), "pages")
         n_pages, n_kv_heads, size = pages.shape
         if not pages.is_contiguous() or n_pages < 1 or size * n_kv_heads != kv_q4_page_bytes(page_size, n_kv_heads, head_dim):
             raise ValueError("pages must be contiguous [n_pages, n_kv_heads, page_size * head_dim * 9 / 8]")
         self.pages, self.page_size, self.n_kv_heads, self.head_dim = pages, page_size, n_kv_heads, head_dim
+        self.dev = pages.get_device()
         self.struct = KvQ4Struct(pages.data_ptr(), n_pages, page_size, n_kv_heads, head_dim)
         self.ref = C.byref(self.struct)
 
@@ -583,22 +594,22 @@ def paged_plan(cached, fresh, block_table, owned, free_pages, free_count, page_s
     [n_pages] and free_count int32 [1]: the pool.  owned and free_count are updated in
     place unless owned_out / free_count_out take the new state."""
     import torch
-    i32 = torch.int32
-    n = out.n_seqs
-    _on_device(block_table, i32, "block_table", 2)
-    if block_table.shape[0] != n:
+    i32, dev, n = torch.int32, torch.cuda.current_device(), out.n_seqs
+    _on_device(block_table, i32, 2, dev, "block_table")
+    rows, max_blocks = block_table.shape
+    if rows != n:
         raise ValueError(f"block_table must have {n} rows")
-    _on_device(free_pages, i32, "free_pages", 1)
-    _on_device(out.slots, torch.int64, "out", 1)
-    owned_out = owned if owned_out is None else owned_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    for name, t, k in (("cached", cached, n), ("fresh", fresh, n), ("owned", owned, n), ("owned_out", owned_out, n),
-                       ("free_count", free_count, 1), ("free_count_out", free_count_out, 1),
-                       ("free_pages", free_pages, free_pages.shape[0])):
-        _vector(t, i32, k, name)
-    rz_paged_plan(cached, fresh, n, owned, owned_out, free_count, free_count_out, free_pages, free_pages.shape[0],
-                  block_table, _row_ld(block_table, block_table.shape[1], "block_table"), block_table.shape[1], page_size,
-                  out.max_rows, out.cu_rows, out.kv_len, out.row_seq, out.positions, out.slots, stream)
+    _on_device(out.slots, torch.int64, 1, dev, "out")
+    _on_device(free_pages, i32, 1, dev, "free_pages")
+    n_pages = free_pages.shape[0]
+    owned_at, count_at = _vector(owned, i32, n, dev, "owned"), _vector(free_count, i32, 1, dev, "free_count")
+    call("rz_paged_plan", _vector(cached, i32, n, dev, "cached"), _vector(fresh, i32, n, dev, "fresh"), n, owned_at,
+         owned_at if owned_out is None else _vector(owned_out, i32, n, dev, "owned_out"), count_at,
+         count_at if free_count_out is None else _vector(free_count_out, i32, 1, dev, "free_count_out"),
+         _vector(free_pages, i32, n_pages, dev, "free_pages"), n_pages, block_table.data_ptr(),
+         _row_ld(block_table, max_blocks, "block_table"), max_blocks, page_size, out.max_rows, out.cu_rows.data_ptr(),
+         out.kv_len.data_ptr(), out.row_seq.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
+         _stream_on(stream, dev))
     return out
 
 
@@ -616,36 +627,38 @@ def qk_norm_rope(q, k, v, positions, n_heads: int, n_kv_heads: int, head_dim: in
     and append k and v to the cache `kv` at `slots` (see rz.h).  Returns (q, k, v): k and
     v as the cache holds them when asked for (else None); without a cache k is the rotated k."""
     import torch
-    f32 = torch.float32
-    n = _on_device(q, f32, "q", 2).shape[0]
-    _on_device(k, f32, "k", 2)
+    f32, dev = torch.float32, torch.cuda.current_device()
+    n = _on_device(q, f32, 2, dev, "q").shape[0]
+    if _on_device(k, f32, 2, dev, "k").shape[0] != n:
+        raise ValueError("k must have a row for each of q")
     q_dim, kv_dim = n_heads * head_dim, n_kv_heads * head_dim
-    ld_q, ld_k, ld_v = _row_ld(q, q_dim, "q"), _row_ld(k, kv_dim, "k"), kv_dim
+    ref = v_at = slots_at = None
+    ld_v = kv_dim
     if kv is None:
         if want_v or slots is not None:
             raise ValueError("slots and want_v need a cache")
-        v, want_k = None, True
+        want_k = True
     else:
-        _on_device(v, f32, "v", 2)
-        ld_v = _row_ld(v, kv_dim, "v")
-        _vector(slots, torch.int64, slots.shape[0], "slots")
-        if v.shape[0] != n or slots.shape[0] < n:
-            raise ValueError("v and slots must have a row for each of q")
-        _on_device(kv.pages, torch.uint8, "kv")
-    _vector(positions, torch.int32, positions.shape[0], "positions")
-    if k.shape[0] != n or positions.shape[0] < n:
-        raise ValueError("k and positions must have a row for each of q")
-    for name, t in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
-        if t is not None:
-            _vector(t, f32, head_dim, name)
+        if _on_device(v, f32, 2, dev, "v").shape[0] != n:
+            raise ValueError("v must have a row for each of q")
+        if kv.dev != dev:
+            raise ValueError("the cache is not on the current device")
+        ref, v_at, ld_v = kv.ref, v.data_ptr(), _row_ld(v, kv_dim, "v")
+        slots_at = _vector(slots, torch.int64, n, dev, "slots", more=True)
+    pos_at = _vector(positions, torch.int32, n, dev, "positions", more=True)
+    qg_at = None if q_gamma is None else _vector(q_gamma, f32, head_dim, dev, "q_gamma")
+    kg_at = None if k_gamma is None else _vector(k_gamma, f32, head_dim, dev, "k_gamma")
     if q_out is None:
-        q_out = _new((n, q_dim), f32, q.device, stream)
-    elif _on_device(q_out, f32, "q_out", 2).shape[0] != n:
-        raise ValueError("q_out must have a row for each of q")
-    k_out = _new((n, kv_dim), f32, q.device, stream) if want_k else None
-    v_out = _new((n, kv_dim), f32, q.device, stream) if want_v else None
-    rz_qk_norm_rope(q, ld_q, k, ld_k, v, ld_v, q_gamma, k_gamma, eps, positions, slots, kv, n, n_heads, n_kv_heads,
-                    head_dim, rope_theta, rope_mode, q_out, _row_ld(q_out, q_dim, "q_out"), k_out, v_out, stream)
+        q_out, ld_qo = _new((n, q_dim), f32, dev, stream), q_dim
+    else:
+        if _on_device(q_out, f32, 2, dev, "q_out").shape[0] != n:
+            raise ValueError("q_out must have a row for each of q")
+        ld_qo = _row_ld(q_out, q_dim, "q_out")
+    k_out = _new((n, kv_dim), f32, dev, stream) if want_k else None
+    v_out = _new((n, kv_dim), f32, dev, stream) if want_v else None
+    call("rz_qk_norm_rope", q.data_ptr(), _row_ld(q, q_dim, "q"), k.data_ptr(), _row_ld(k, kv_dim, "k"), v_at, ld_v, qg_at,
+         kg_at, eps, pos_at, slots_at, ref, n, n_heads, n_kv_heads, head_dim, rope_theta, rope_mode, q_out.data_ptr(), ld_qo,
+         None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), _stream_on(stream, dev))
     return q_out, k_out, v_out
 
 
@@ -666,29 +679,27 @@ def attention_paged_q4(q, kv: PagedKVQ4, block_table, cu_rows, kv_len, n_heads: 
     pages (see rz.h); returns f32 [n_rows, n_heads * head_dim] (rows behind the last request's as
     they were in `out`).  att_q8: a uint8 tensor of q8_1_size(n_rows, q_pad) for the Q8_1 form."""
     import torch
-    i32 = torch.int32
-    n_rows = _on_device(q, torch.float32, "q", 2).shape[0]
+    i32, dev = torch.int32, torch.cuda.current_device()
+    n_rows = _on_device(q, torch.float32, 2, dev, "q").shape[0]
     q_dim = n_heads * kv.head_dim
-    ld_q = _row_ld(q, q_dim, "q")
-    _on_device(kv.pages, torch.uint8, "kv")
-    n = _on_device(block_table, i32, "block_table", 2).shape[0]
-    _vector(cu_rows, i32, n + 1, "cu_rows")
-    _vector(kv_len, i32, n, "kv_len")
+    if kv.dev != dev:
+        raise ValueError("the cache is not on the current device")
+    n, max_blocks = _on_device(block_table, i32, 2, dev, "block_table").shape
     if out is None:
-        out = _new((n_rows, q_dim), torch.float32, q.device, stream)
-    elif _on_device(out, torch.float32, "out", 2).shape != (n_rows, q_dim) or not out.is_contiguous():
+        out = _new((n_rows, q_dim), torch.float32, dev, stream)
+    elif _on_device(out, torch.float32, 2, dev, "out").shape != (n_rows, q_dim) or not out.is_contiguous():
         raise ValueError("out must be contiguous, with the shape of q")
-    if att_q8 is not None and _on_device(att_q8, torch.uint8, "att_q8", 1).shape[0] < q8_1_size(n_rows, -(-q_dim // 256) * 256):
-        raise ValueError("att_q8 is too small")
+    q8_at = None
+    if att_q8 is not None:
+        q8_at = _vector(att_q8, torch.uint8, q8_1_size(n_rows, -(-q_dim // 256) * 256), dev, "att_q8", more=True)
     if ws is None:
-        size = attention_paged_q4_workspace_bytes(n_heads, kv.n_kv_heads, kv.head_dim)
-        ws = _new((max(size, 16),), torch.uint8, q.device, stream)
-        if stream is None:
+        size = max(attention_paged_q4_workspace_bytes(n_heads, kv.n_kv_heads, kv.head_dim), 16)
+        ws = _new((size,), torch.uint8, dev, stream)
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                               torch.cuda.ExternalStream(_stream_on(stream, dev))):
             ws.zero_()
-        else:
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
-                ws.zero_()
-    rz_attention_paged_q4(q, ld_q, n_rows, kv, block_table, _row_ld(block_table, block_table.shape[1], "block_table"),
-                          block_table.shape[1], cu_rows, kv_len, n, n_heads, scale, out, att_q8, _on_device(ws, torch.uint8, "ws", 1),
-                          ws.numel(), stream)
+    call("rz_attention_paged_q4", q.data_ptr(), _row_ld(q, q_dim, "q"), n_rows, kv.ref, block_table.data_ptr(),
+         _row_ld(block_table, max_blocks, "block_table"), max_blocks, _vector(cu_rows, i32, n + 1, dev, "cu_rows"),
+         _vector(kv_len, i32, n, dev, "kv_len"), n, n_heads, scale, out.data_ptr(), q8_at,
+         _vector(ws, torch.uint8, 0, dev, "ws", more=True), ws.shape[0], _stream_on(stream, dev))
     return out

@@ -89,10 +89,20 @@ def test_sizes(lib):
     assert L.rz_attention_paged_q4_workspace_bytes(4, 2, 60) == 0
 
 
-def test_binding_checks_tensors():
+@pytest.fixture
+def binding(monkeypatch):
     torch = pytest.importorskip("torch")
     import quantized_q4_q8_gb300 as rz
-    rz.load()
+    from quantized_q4_q8_gb300.build import build
+    build()
+    if not torch.cuda.is_available():
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return rz
+
+
+def test_binding_checks_tensors(binding):
+    import torch
+    rz = binding
     t = torch.zeros(2, 4, 8, dtype=torch.uint8)
     with pytest.raises(TypeError, match="CUDA tensor"):
         rz.PagedKVQ4(t, 16, 64)
