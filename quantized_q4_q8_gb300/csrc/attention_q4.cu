@@ -119,7 +119,9 @@ __device__ __forceinline__ SeqRow read_seq(const PagedAttnArgs &a, int s, bool &
     const int64_t most = (int64_t)a.max_blocks << (a.kv.page_log + 4);
     const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.n_rows;
     if (!ok || n > most) bad = true;
-    return SeqRow{ok ? c0 : 0, ok ? c1 - c0 : 0, n > most ? 0 : max(n, 0)};
+    // one with many rows has none here: attention_q4_tc.cu works it
+    const bool here = ok && (c1 - c0) * (a.n_heads / a.kv.n_kv_heads) <= a.most_rows;
+    return SeqRow{here ? c0 : 0, here ? c1 - c0 : 0, n > most ? 0 : max(n, 0)};
 }
 
 template <int W>
@@ -980,20 +982,8 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, paged_attention_kernel<NB>, a, slots);
 }
 
-}  // namespace
-
-// counters (zero before the first call, zero again after each), then two partial records for each CTA
-size_t paged_attention_workspace_bytes(int head_dim)
+cudaError_t launch_any(const PagedAttnArgs &a, cudaStream_t s)
 {
-    const size_t ctas = grid_ctas();
-    return (ctas * 4 + 255) / 256 * 256 + 2 * ctas * 8 * consumers(head_dim / 32) * (head_dim + 2) * 4;
-}
-
-cudaError_t launch_paged_attention(const PagedAttnArgs &args, void *workspace, cudaStream_t s)
-{
-    PagedAttnArgs a = args;
-    a.counters = static_cast<int *>(workspace);
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ((size_t)grid_ctas() * 4 + 255) / 256 * 256);
     switch (a.kv.head_dim / 32) {
         case 1: return launch<1>(a, s);
         case 2: return launch<2>(a, s);
@@ -1004,6 +994,32 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &args, void *workspace, c
         case 7: return launch<7>(a, s);
         default: return launch<8>(a, s);
     }
+}
+
+}  // namespace
+
+// counters (zero before the first call, zero again after each), then two partial records for each CTA
+size_t paged_attention_workspace_bytes(int head_dim)
+{
+    const size_t ctas = grid_ctas();
+    const size_t parts = 2 * ctas * 8 * consumers(head_dim / 32) * (head_dim + 2) * 4;
+    return (ctas * 4 + 255) / 256 * 256 +
+           std::max(parts, paged_attention_tc_takes(head_dim) ? paged_attention_tc_part_bytes(head_dim) : size_t(0));
+}
+
+cudaError_t launch_paged_attention(const PagedAttnArgs &args, void *workspace, cudaStream_t s)
+{
+    PagedAttnArgs a = args;
+    a.counters = static_cast<int *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ((size_t)grid_ctas() * 4 + 255) / 256 * 256);
+    // Requests with many rows go to the tcgen05 kernel.  Whether there may be one: if every
+    // request has a row, one of them has at most n_rows - n_seqs + 1.  (If there is one all the
+    // same, because others have none, it is worked here.)
+    const int group = a.n_heads / a.kv.n_kv_heads;
+    const bool tc = paged_attention_tc_takes(a.kv.head_dim) && (a.n_rows - a.n_seqs + 1) * group > kTcRows;
+    a.most_rows = tc ? kTcRows : 0x7fffffff;
+    const cudaError_t e = launch_any(a, s);
+    return e != cudaSuccess || !tc ? e : launch_paged_attention_tc(a, s);
 }
 
 }  // namespace rz

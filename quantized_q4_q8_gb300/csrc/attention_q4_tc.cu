@@ -1,0 +1,927 @@
+// attention_q4_tc.cu -- attention of many new rows (a prompt chunk) over the pages of
+// the 4-bit KV cache, on tcgen05.mma.
+//
+// The formulas, the cache and the arguments are those of attention_q4.cu; this kernel
+// works the requests with more than kTcRows query rows for a kv head, that one the others.
+//
+// An item is (request, kv head, 128 query rows); a tile is 128 tokens.  For each tile
+//   S = Q K^T     128 x 128, A = Q and B = K from shared memory, S in tensor memory
+//   O += P V      128 x hd, A = P from tensor memory, B = V from shared memory
+// Precision: f16 operands in two pieces each.  q and the weights are split into a high and a
+// low half (22 bits); a key is d * (code - 8), 15 significant bits, so its high and low
+// halves hold it exactly.  high * high + low * high + high * low is three products, off by 2^-22
+// at most; three products of codes without scales would be two, but every block of 32 would then
+// need accumulators of its own, and 4 times the reads of tensor memory, which have to be
+// multiplied and added.  K and V are brought near 1 by a power of two for each tile
+// (exact), so that f16 holds them whatever their scale; it goes into the exponents.
+//
+// Softmax: a thread has one row: its 128 scores, its running maximum and sum.  The sums O stay in
+// tensor memory and are rescaled there when a row's maximum has grown by over 2^8, and not before
+// (see attention_q4.cu).
+//
+// The tensor pipe is never to wait: while it works P V of tile i, warps unpack K of tile i + 2
+// and V of tile i + 1 and form the weights of tile i + 1 from S, of which there are two:
+//   warp 0       copies records (K, V's scales; V's codes) with the bulk-copy engine
+//   warp 1       issues the products: QK(0), QK(1), PV(0), QK(2), PV(1), ...
+//   warps 4-7    softmax, and the outputs
+//   warps 8-11   unpack: K(0), K(1), V(0), K(2), V(1), ...
+// Operands lie in core matrices of 8 rows x 16 bytes without a swizzle.  Within every 4 values of the
+// inner dimension the order is 0, 2, 1, 3, that in which a word of packed codes unpacks into two
+// pairs: for K over the head's values (Q is laid out alike), for V over the tokens (so S's columns,
+// K's rows, are in that order too).
+//
+// Work is shared among the CTAs (one for each SM) as in attention_q4.cu.  Every wait is
+// bounded; after one that runs out every role stops, copies and products in flight are waited
+// for, and tensor memory is freed.
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "mma_f16.cuh"
+#include "paged_q4.cuh"
+#include "rz_common.cuh"
+#include "rz_kernels.h"
+
+namespace rz {
+namespace {
+
+constexpr int kRows = 128;  // query rows of an item
+constexpr int kTile = 128;  // tokens of a tile
+constexpr int kGroups = kTile / 16;
+constexpr int kThreads = 384;
+constexpr int kItemCost = 2;  // of an item's start and end, in tiles
+constexpr float kLazy = 8.0f, kBias = 7.0f;
+constexpr int kScaleTop = 8;  // the largest |d| of a tile becomes 2^8 .. 2^9
+
+// tensor memory columns
+constexpr uint32_t kColS = 0, kColO = 256, kColP = 384;  // S twice, O, P (64 columns of high pieces, 64 of low)
+
+template <int NB>
+struct Lay {
+    static constexpr int hd = 32 * NB;
+    static constexpr int q = kRows * hd * 2;        // one piece of Q (and of K)
+    static constexpr int v = hd * kTile * 2;        // one piece of V
+    static constexpr int raw_k = kGroups * 10 * hd; // K codes and scales, V scales
+    static constexpr int raw_v = kGroups * 8 * hd;  // V codes
+    static constexpr int off_q = 0, off_k = off_q + 2 * q, off_v = off_k + 2 * q;
+    static constexpr int off_raw_k = off_v + 2 * v, off_raw_v = off_raw_k + 2 * raw_k;
+    static constexpr int off_scale = off_raw_v + raw_v;                   // f16: K [128][NB], V twice
+    static constexpr int off_misc = off_scale + 3 * kTile * NB * 2;
+    static constexpr int bytes = off_misc + 512;
+};
+
+struct Bars {
+    uint64_t raw_k_full[2], raw_k_empty[2], raw_v_full, raw_v_empty;
+    uint64_t k_ready, k_free, v_ready, pv_done, s_full[2], s_free[2], p_ready, q_ready, unpack_sync, out_sync, done;
+    uint32_t tmem;
+    int gave_up, last;      // a wait ran out; this CTA adds the parts up
+    int exps[4][2];         // of tiles i mod 4: K's and V's exponents
+    uint32_t nan_v[4][4];   // their tokens with a NaN or infinite V scale, by position
+    uint32_t warp_max[4][2];
+    int parts, first_part;
+};
+
+__device__ __forceinline__ float ex2f(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t codes_low(uint32_t w) { return hsub2u(lop_and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u); }
+__device__ __forceinline__ uint32_t codes_high(uint32_t w)
+{
+    return hfma2u(lop_and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
+}
+__device__ __forceinline__ float power2(int e) { return __int_as_float((127 + min(max(e, -126), 127)) << 23); }
+// token of position p within 4: 0, 2, 1, 3 (its own inverse)
+__device__ __forceinline__ int swapped(int p) { return (p & ~3) | ((p & 1) << 1) | ((p >> 1) & 1); }
+
+// ---------------------------------------------------------------- tcgen05
+// K-major operand of 16-bit values, core matrices 128 bytes apart along K, groups of 8 rows
+// `stride` bytes apart, no swizzle
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t stride)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | (1ull << 46);
+}
+__host__ __device__ constexpr uint32_t idesc_f16(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24); }
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+#define RZ_O16(r)                                                                                                     \
+    "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),      \
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+#define RZ_I16(r)                                                                                              \
+    "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), \
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+
+// 16 columns of the warp's 32 rows, waited for in the same statement
+__device__ __forceinline__ void tm_load16(uint32_t at, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : RZ_O16(r)
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::
+            RZ_I16(r),
+        "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- the line of work
+struct Item {
+    int row0, m, n;  // of the request: first row, rows, held tokens
+    int s, h, it;
+    int items;       // of a kv head
+    int tokens, tiles, lo, hi;
+    int64_t at;      // where the item begins on the line
+};
+
+__device__ __forceinline__ bool load_request(Item &w, const PagedAttnArgs &a, int group)
+{
+    const int c0 = a.cu_rows[w.s], c1 = a.cu_rows[w.s + 1], n = a.kv_len[w.s];
+    const int64_t most = (int64_t)a.max_blocks << (a.kv.page_log + 4);
+    const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.n_rows;  // what is not is reported by the other kernel
+    w.row0 = ok ? c0 : 0;
+    w.m = ok ? c1 - c0 : 0;
+    w.n = n > most ? 0 : max(n, 0);
+    const int rows = w.m * group;
+    w.items = rows > kTcRows ? (rows + kRows - 1) / kRows : 0;
+    return w.items > 0;
+}
+__device__ __forceinline__ int item_tokens(const Item &w, int group, int it)
+{
+    const unsigned last = static_cast<unsigned>(min((it + 1) * kRows, w.m * group) - 1) / static_cast<unsigned>(group);
+    return max(w.n - w.m + static_cast<int>(last) + 1, 0);
+}
+__device__ __forceinline__ int64_t item_span(const Item &w, int group, int it)
+{
+    return kItemCost + (item_tokens(w, group, it) + kTile - 1) / kTile;
+}
+
+struct Line {
+    int64_t total, step;
+    int ctas, rest;
+    __device__ __forceinline__ int64_t begin(int c) const
+    {
+        return c * step + static_cast<unsigned>(c * rest) / static_cast<unsigned>(ctas);
+    }
+};
+__device__ __forceinline__ Line make_line(int64_t total, int grid)
+{
+    Line l;
+    l.total = total;
+    l.ctas = total < grid ? max(1, static_cast<int>(total)) : grid;
+    l.step = total / l.ctas;
+    l.rest = static_cast<int>(total - l.step * l.ctas);
+    return l;
+}
+__device__ __forceinline__ int tile_at(int64_t x, int tiles)
+{
+    return x <= kItemCost ? 0 : x - kItemCost >= tiles ? tiles : static_cast<int>(x - kItemCost);
+}
+__device__ __forceinline__ void load_item(Item &w, const Line &l, int group)
+{
+    w.tokens = item_tokens(w, group, w.it);
+    w.tiles = (w.tokens + kTile - 1) / kTile;
+    w.lo = tile_at(l.begin(blockIdx.x) - w.at, w.tiles);
+    w.hi = tile_at(l.begin(blockIdx.x + 1) - w.at, w.tiles);
+}
+__device__ __forceinline__ bool has_work(const Item &w, const Line &l)
+{
+    return w.lo < w.hi || (w.tiles == 0 && w.at >= l.begin(blockIdx.x));
+}
+__device__ __forceinline__ bool next_item(Item &w, const PagedAttnArgs &a, const Line &l, int group)
+{
+    w.at += item_span(w, group, w.it);
+    if (w.at >= l.begin(blockIdx.x + 1)) return false;
+    if (++w.it == w.items) {
+        w.it = 0;
+        if (++w.h == a.kv.n_kv_heads) {
+            w.h = 0;
+            do {
+                if (++w.s >= a.n_seqs) return false;
+            } while (!load_request(w, a, group));
+        }
+    }
+    load_item(w, l, group);
+    return true;
+}
+
+// Warp-wide bounded wait; false after a timeout or when another role gave up.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, unsigned par, Bars &b, unsigned *err)
+{
+    bool ok = false;
+    volatile int *gave_up = &b.gave_up;
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (mbar_try_wait(bar, par)) {
+            ok = true;
+            break;
+        }
+        if ((i & 63u) == 63u && *gave_up) break;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && !*gave_up) {
+        *gave_up = 1;
+        set_error(err, DEV_TIMEOUT_PAGED);
+    }
+    return ok;
+}
+
+// A barrier of four warps that no warp waits at for ever; phase counts its uses.
+__device__ __forceinline__ bool four_warps(uint64_t *bar, unsigned &phase, Bars &b, unsigned *err)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    return wait_for(bar, phase++ & 1u, b, err);
+}
+
+// 32 values of one output row (a block) to the outputs.
+__device__ __forceinline__ void write_block(const PagedAttnArgs &a, const float (&v)[32], int64_t row, int col, int q_dim, int q_pad)
+{
+    if (a.att) {
+        float4 *o = reinterpret_cast<float4 *>(a.att + row * q_dim + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    if (a.att_q8) {
+        float mx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(v[i]));
+        const float d = __fdiv_rn(mx, 127.0f);
+        const Q8Scale sc = q8_scale(d);
+        int8_t *q = static_cast<int8_t *>(a.att_q8);
+        float *qd = reinterpret_cast<float *>(q + a.n_rows * q_pad), *qs = qd + a.n_rows * (q_pad / 32);
+        int sum = 0;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[i] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int c = q8_code(v[4 * i + k], sc);
+                sum += c;
+                w[i] |= static_cast<uint32_t>(c & 255) << (8 * k);
+            }
+        }
+        uint4 *o = reinterpret_cast<uint4 *>(q + row * q_pad + col);
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        qd[row * (q_pad / 32) + col / 32] = d;
+        qs[row * (q_pad / 32) + col / 32] = __fmul_rn(d, (float)sum);
+    }
+}
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const __grid_constant__ PagedAttnArgs a)
+{
+    using L = Lay<NB>;
+    constexpr int hd = L::hd;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    Bars &b = *reinterpret_cast<Bars *>(sm + L::off_misc);
+    static_assert(sizeof(Bars) <= 512, "");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K = a.kv.n_kv_heads, group = a.n_heads / K;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // ---- the line, and this CTA's first item on it
+    Item first;
+    Line line;
+    {
+        int64_t *pre = reinterpret_cast<int64_t *>(sm);  // before the operands; n_seqs + 1
+        int64_t *tmp = pre + kPagedMaxSeqs + 8;
+        const int per = (a.n_seqs + kThreads - 1) / kThreads;
+        int64_t mine = 0;
+        for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
+            Item w;
+            w.s = i;
+            int64_t span = 0;
+            if (load_request(w, a, group))
+                for (int it = 0; it < w.items; ++it) span += item_span(w, group, it);
+            pre[i + 1] = span * K;
+            mine += span * K;
+        }
+        int64_t v = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) tmp[warp] = v;
+        __syncthreads();
+        for (int k = 0; k < warp; ++k) v += tmp[k];
+        v -= mine;
+        for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
+            v += pre[i + 1];
+            pre[i + 1] = v;
+        }
+        if (tid == 0) pre[0] = 0;
+        __syncthreads();
+        line = make_line(pre[a.n_seqs], gridDim.x);
+        if (line.total == 0 || blockIdx.x >= line.ctas) return;  // the same for the whole CTA
+        const int64_t x0 = line.begin(blockIdx.x);
+        int lo = 0, hi = a.n_seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= x0) lo = mid;
+            else hi = mid;
+        }
+        first.s = lo;
+        load_request(first, a, group);
+        const int64_t head = (pre[lo + 1] - pre[lo]) / K;
+        first.h = static_cast<int>((x0 - pre[lo]) / head);
+        first.at = pre[lo] + first.h * head;
+        first.it = 0;
+        for (; first.it + 1 < first.items; ++first.it) {
+            const int64_t span = item_span(first, group, first.it);
+            if (first.at + span > x0) break;
+            first.at += span;
+        }
+        load_item(first, line, group);
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.raw_k_full[i], 1);
+            mbar_init(&b.raw_k_empty[i], 4);
+            mbar_init(&b.s_full[i], 1);
+            mbar_init(&b.s_free[i], 4);
+        }
+        mbar_init(&b.raw_v_full, 1);
+        mbar_init(&b.raw_v_empty, 4);
+        mbar_init(&b.k_ready, 4);
+        mbar_init(&b.k_free, 1);
+        mbar_init(&b.v_ready, 4);
+        mbar_init(&b.pv_done, 1);
+        mbar_init(&b.p_ready, 4);
+        mbar_init(&b.q_ready, 4);
+        mbar_init(&b.unpack_sync, 4);
+        mbar_init(&b.out_sync, 4);
+        mbar_init(&b.done, 1);
+        b.gave_up = b.last = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&b.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();  // pre is read, the barriers and tensor memory are there
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&b.tmem);
+    Item w = first;
+    bool more = true, ok = true;
+    int i = 0;  // tiles of this CTA so far
+
+    // Registers: launched with 168 a thread, 504 for the three warpgroups together; the first gives
+    // 72 of its own to the softmax warps.
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        // K(i + 1) before V(i), the order in which they are unpacked
+        const int lg = a.kv.page_log;
+        constexpr int kRec = q4_record_bytes(hd);
+        const int64_t head_bytes = (int64_t)kRec << lg;
+        asm volatile("fence.proxy.async;" ::: "memory");
+        int n_k = 0, n_v = 0;
+        const uint8_t *v_src = nullptr;  // this lane's group of the tile whose V is next
+        int v_groups = 0;
+        auto copy_v = [&]() {
+            if (!wait_for(&b.raw_v_empty, (n_v & 1) ^ 1u, b, a.err)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(&b.raw_v_full, v_groups * 8 * hd);
+            __syncwarp();
+            if (lane < v_groups) bulk_g2s(sm + L::off_raw_v + lane * 8 * hd, v_src + 9 * hd, 8 * hd, &b.raw_v_full);
+            ++n_v;
+            return true;
+        };
+        while (more && ok) {
+            const int32_t *row = a.table + (int64_t)w.s * a.table_ld;
+            for (int tile = w.lo; tile < w.hi; ++tile) {
+                const int g0 = tile * kGroups, groups = min(kGroups, ((w.tokens + 15) >> 4) - g0);
+                const uint8_t *src = nullptr;
+                if (lane < groups) {
+                    int32_t page = row[(g0 + lane) >> lg];
+                    if (page < 0 || page >= a.kv.n_pages) {
+                        set_error(a.err, DEV_BAD_PAGE);
+                        page = 0;  // a page there is; the request's rows are not to be used
+                    }
+                    src = a.kv.pages + ((int64_t)page * K + w.h) * head_bytes + ((g0 + lane) & ((1 << lg) - 1)) * kRec;
+                }
+                const int slot = n_k & 1;
+                if (!(ok = wait_for(&b.raw_k_empty[slot], ((n_k >> 1) & 1) ^ 1u, b, a.err))) break;
+                if (lane == 0) mbar_arrive_expect_tx(&b.raw_k_full[slot], groups * 10 * hd);
+                __syncwarp();
+                if (lane < groups) {
+                    uint8_t *dst = sm + L::off_raw_k + slot * L::raw_k + lane * 10 * hd;
+                    bulk_g2s(dst, src, 9 * hd, &b.raw_k_full[slot]);
+                    bulk_g2s(dst + 9 * hd, src + 17 * hd, hd, &b.raw_k_full[slot]);
+                }
+                ++n_k;
+                if (n_k > 1 && !(ok = copy_v())) break;
+                v_src = src;
+                v_groups = groups;
+            }
+            if (ok) more = next_item(w, a, line, group);
+        }
+        if (ok && n_k > 0) copy_v();
+        // no copy outlives the CTA
+        for (int k = max(0, n_k - 2); k < n_k; ++k) mbar_wait(&b.raw_k_full[k & 1], (k >> 1) & 1);
+        if (n_v > 0) mbar_wait(&b.raw_v_full, (n_v - 1) & 1);
+        } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        const uint32_t q0 = smem_u32(sm + L::off_q), k0 = smem_u32(sm + L::off_k), v0 = smem_u32(sm + L::off_v);
+        constexpr uint32_t stride_q = hd * 16, stride_v = kTile * 16;  // 8 rows
+        int item = 0;
+        // QK(j): A = Q, B = K; high * high, low * high, high * low
+        auto qk = [&](int j) {
+            if (!wait_for(&b.k_ready, j & 1, b, a.err) || !wait_for(&b.s_free[j & 1], ((j >> 1) & 1) ^ 1u, b, a.err)) return false;
+            fence_after();
+            if (lane == 0) {
+                const uint32_t d = tmem + kColS + (j & 1) * kTile;
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+#pragma unroll
+                    for (int k = 0; k < hd / 16; ++k)
+                        mma_ss(d, operand_desc(q0 + (p == 1 ? L::q : 0) + 256 * k, stride_q),
+                               operand_desc(k0 + (p == 2 ? L::q : 0) + 256 * k, stride_q), idesc_f16(kTile), p || k);
+                commit(&b.k_free);
+                commit(&b.s_full[j & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
+        auto pv = [&](int j, bool start) {
+            if (!wait_for(&b.v_ready, j & 1, b, a.err) || !wait_for(&b.p_ready, j & 1, b, a.err)) return false;
+            fence_after();
+            if (lane == 0) {
+                const uint32_t d = tmem + kColO;
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(d, tmem + kColP + (p == 1 ? 64 : 0) + 8 * k,
+                               operand_desc(v0 + (p == 2 ? L::v : 0) + 256 * k, stride_v), idesc_f16(hd), !start || p || k);
+                commit(&b.pv_done);
+            }
+            __syncwarp();
+            return true;
+        };
+        while (more && ok) {
+            if (w.lo < w.hi) {
+                ok = wait_for(&b.q_ready, item & 1, b, a.err);
+                ++item;
+                for (int t = w.lo; t < w.hi && ok; ++t, ++i) {
+                    ok = qk(i);
+                    if (ok && t > w.lo) ok = pv(i - 1, t - 1 == w.lo);
+                }
+                if (ok) ok = pv(i - 1, w.hi - 1 == w.lo);
+            }
+            if (ok) more = next_item(w, a, line, group);
+        }
+        // every product issued has completed once this arrives
+        if (lane == 0) {
+            commit(&b.done);
+            mbar_wait(&b.done, 0);
+        }
+        __syncwarp();
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ unpacking
+        const int t128 = tid - 256, w4 = warp - 8, g = lane >> 2, t = lane & 3;
+        uint16_t *sk = reinterpret_cast<uint16_t *>(sm + L::off_scale), *sv = sk + kTile * NB;
+        unsigned phase = 0;
+        // two words' codes c0, c1 times their scales, high and low piece, to 8 bytes of a chunk
+        auto put = [&](uint8_t *hi_base, int piece, int kk, int half, uint32_t c0, uint32_t c1, uint32_t d0, uint32_t d1) {
+            const uint32_t h0 = hmul2u(c0, d0), h1 = hmul2u(c1, d1);
+            const uint32_t l0 = hfma2u(c0, d0, h0 ^ 0x80008000u), l1 = hfma2u(c1, d1, h1 ^ 0x80008000u);
+            uint8_t *p = hi_base + kk * 128 + half * 8;
+            *reinterpret_cast<uint2 *>(p) = make_uint2(h0, h1);
+            *reinterpret_cast<uint2 *>(p + piece) = make_uint2(l0, l1);
+        };
+        auto unpack_k = [&](int j, int valid) {
+            const int slot = j & 1;
+            if (!wait_for(&b.raw_k_full[slot], (j >> 1) & 1, b, a.err)) return false;
+            const uint8_t *raw = sm + L::off_raw_k + slot * L::raw_k;
+            // this thread's token: its scales, and the tile's largest of each kind
+            uint16_t dk[NB], dv[NB];
+            uint32_t mk = 0, mv = 0;
+            bool bad = false;
+            const uint16_t *pk = reinterpret_cast<const uint16_t *>(raw + (t128 >> 4) * 10 * hd + 8 * hd) + (t128 & 15) * NB;
+            const uint16_t *pv = pk + hd / 2;
+            const bool live = t128 < valid;
+#pragma unroll
+            for (int e = 0; e < NB; ++e) {
+                dk[e] = live ? pk[e] : uint16_t(0);
+                dv[e] = live ? pv[e] : uint16_t(0);
+                const uint32_t ak = dk[e] & 0x7fffu, av = dv[e] & 0x7fffu;
+                if (ak < 0x7c00u) mk = max(mk, ak);
+                if (av < 0x7c00u) mv = max(mv, av);
+                else bad = true;
+            }
+            mk = __reduce_max_sync(0xffffffffu, mk);
+            mv = __reduce_max_sync(0xffffffffu, mv);
+            const unsigned bads = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) {
+                b.warp_max[w4][0] = mk;
+                b.warp_max[w4][1] = mv;
+                // by position: bits 1 and 2 of every 4 change places
+                b.nan_v[j & 3][w4] = (bads & 0x99999999u) | ((bads & 0x22222222u) << 1) | ((bads & 0x44444444u) >> 1);
+            }
+            if (!four_warps(&b.unpack_sync, phase, b, a.err)) return false;
+            mk = max(max(b.warp_max[0][0], b.warp_max[1][0]), max(b.warp_max[2][0], b.warp_max[3][0]));
+            mv = max(max(b.warp_max[0][1], b.warp_max[1][1]), max(b.warp_max[2][1], b.warp_max[3][1]));
+            // d 2^up: the largest to 2^8 .. 2^9 (a tile of zeros: as it is)
+            const int uk = mk ? kScaleTop + 127 - (__float_as_int(h2f((uint16_t)mk)) >> 23) : 0;
+            const int uv = mv ? kScaleTop + 127 - (__float_as_int(h2f((uint16_t)mv)) >> 23) : 0;
+            if (t128 == 0) {
+                b.exps[j & 3][0] = uk;
+                b.exps[j & 3][1] = uv;
+            }
+#pragma unroll
+            for (int e = 0; e < NB; ++e) {
+                sk[t128 * NB + e] = __half_as_ushort(__float2half_rn(h2f(dk[e]) * power2(uk)));
+                // a V scale that is no number: nothing is added, and the row's sum is made NaN
+                const bool fine = (dv[e] & 0x7fffu) < 0x7c00u;
+                sv[(j & 1) * kTile * NB + t128 * NB + e] = fine ? __half_as_ushort(__float2half_rn(h2f(dv[e]) * power2(uv))) : uint16_t(0);
+            }
+            if (!four_warps(&b.unpack_sync, phase, b, a.err)) return false;
+            if (!wait_for(&b.k_free, (j & 1) ^ 1u, b, a.err)) return false;
+            // warp w4: groups 2 w4, 2 w4 + 1; lane (g, t): word t of each block of rows 8 hf + g
+#pragma unroll
+            for (int gr = 2 * w4; gr < 2 * w4 + 2; ++gr)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int pos = 8 * hf + g, tok = swapped(pos);
+                    const uint8_t *r = raw + gr * 10 * hd + tok * (hd / 2) + t * 4 * NB;
+                    uint8_t *dst = sm + L::off_k + (2 * gr + hf) * (hd * 16) + g * 16;
+#pragma unroll
+                    for (int e = 0; e < NB; ++e) {
+                        const uint32_t x = reinterpret_cast<const uint32_t *>(r)[e], y = x >> 8;
+                        const uint32_t d = sk[(gr * 16 + tok) * NB + e] * 0x10001u;
+                        put(dst, L::q, 4 * e + (t >> 1), t & 1, codes_low(x), codes_low(y), d, d);
+                        put(dst, L::q, 4 * e + 2 + (t >> 1), t & 1, codes_high(x), codes_high(y), d, d);
+                    }
+                }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&b.k_ready);
+                mbar_arrive(&b.raw_k_empty[slot]);
+            }
+            return true;
+        };
+        auto unpack_v = [&](int j) {
+            if (!wait_for(&b.raw_v_full, j & 1, b, a.err)) return false;
+            if (j > 0 && !wait_for(&b.pv_done, (j - 1) & 1, b, a.err)) return false;
+            const uint8_t *raw = sm + L::off_raw_v;
+            const uint16_t *s = sv + (j & 1) * kTile * NB;
+            constexpr int run = q4_v_run(NB);
+#pragma unroll
+            for (int gr = 2 * w4; gr < 2 * w4 + 2; ++gr) {
+                const uint16_t *d = s + (gr * 16 + 4 * t) * NB;
+#pragma unroll
+                for (int r = 0; r < 2 * NB; ++r) {
+                    const uint32_t x = *reinterpret_cast<const uint32_t *>(raw + gr * 8 * hd + ((r / run) * 32 + lane) * run * 4 + (r % run) * 4);
+                    const uint32_t y = x >> 8;
+                    const int e = r >> 1;
+                    const uint32_t d0 = d[e] | (uint32_t)d[2 * NB + e] << 16, d1 = d[NB + e] | (uint32_t)d[3 * NB + e] << 16;
+                    // rows (values) 32 e + 8 (r % 2) + g and 16 more; columns 16 gr + 4 t ..
+                    uint8_t *dst = sm + L::off_v + (4 * e + (r & 1)) * (kTile * 16) + g * 16;
+                    put(dst, L::v, 2 * gr + (t >> 1), t & 1, codes_low(x), codes_low(y), d0, d1);
+                    put(dst + 2 * (kTile * 16), L::v, 2 * gr + (t >> 1), t & 1, codes_high(x), codes_high(y), d0, d1);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&b.v_ready);
+                mbar_arrive(&b.raw_v_empty);
+            }
+            return true;
+        };
+        while (more && ok) {
+            for (int tile = w.lo; tile < w.hi && ok; ++tile, ++i) {
+                ok = unpack_k(i, w.tokens - tile * kTile);
+                if (ok && i > 0) ok = unpack_v(i - 1);
+            }
+            if (ok) more = next_item(w, a, line, group);
+        }
+        if (ok && i > 0) unpack_v(i - 1);
+    } else {
+        // ------------------------------------------------------------ softmax and outputs
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+        const int r = tid - 128;  // this thread's row of an item
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const int q_dim = a.n_heads * hd, q_pad = (q_dim + 255) / 256 * 256;
+        unsigned phase = 0;
+        while (more && ok) {
+            if (!has_work(w, line)) {
+                more = next_item(w, a, line, group);
+                continue;
+            }
+            const int n_rows = w.m * group, my = w.it * kRows + r;
+            const bool live = my < n_rows;
+            const int tok_q = min(my, n_rows - 1) / group;
+            const int before = w.n - w.m + 1;
+            const int sees = max(before + tok_q, 0), all_see = max(before + (w.it * kRows + (r & ~31)) / group, 0);
+            const int64_t row = w.row0 + tok_q;
+            const int col0 = (w.h * group + (min(my, n_rows - 1) - tok_q * group)) * hd;
+            float unit = 0.0f, m = -1e37f, l = 0.0f;
+            if (w.lo < w.hi) {
+                // ---- Q's pieces.  The products of the item before that read them are done: their S was waited for.
+                const float4 *src = reinterpret_cast<const float4 *>(a.q + row * a.ld_q + col0);
+                float mx = 0.0f;
+#pragma unroll 8
+                for (int k = 0; k < hd / 4; ++k) {
+                    const float4 v = __ldg(src + k);
+                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                }
+                const int up = mx == 0.0f || !live ? 0 : min(14 - ((__float_as_int(mx) >> 23) - 127), 126);
+                const float sc = live ? power2(up) : 0.0f;
+                unit = a.scale * 1.4426950408889634f * power2(-up);
+                uint8_t *dst = sm + L::off_q + (r >> 3) * (hd * 16) + (r & 7) * 16;
+#pragma unroll 4
+                for (int k = 0; k < hd / 8; ++k) {
+                    const float4 x = __ldg(src + 2 * k), y = __ldg(src + 2 * k + 1);
+                    const float f[8] = {x.x, x.z, x.y, x.w, y.x, y.z, y.y, y.w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = live ? f[2 * e] * sc : 0.0f, q = live ? f[2 * e + 1] * sc : 0.0f;
+                        hi[e] = pack2(p, q);
+                        const float2 h = unpack2(hi[e]);
+                        lo[e] = pack2(p - h.x, q - h.y);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + k * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(dst + L::q + k * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.q_ready);
+            }
+            for (int tile = w.lo; tile < w.hi; ++tile, ++i) {
+                if (!(ok = wait_for(&b.s_full[i & 1], (i >> 1) & 1, b, a.err))) break;
+                fence_after();
+                const float u = unit * power2(-b.exps[i & 3][0]), sub = static_cast<float>(-b.exps[i & 3][1]);
+                float y[kTile];  // log2 of the weights of V as it is unpacked
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kTile; c += 16) {
+                    uint32_t s[16];
+                    tm_load16(tmem + lanes + kColS + (i & 1) * kTile + c, s);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) y[c + e] = fmaf(__uint_as_float(s[e]), u, sub);
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.s_free[i & 1]);
+                const int left = sees - tile * kTile;
+                const bool masked = (tile + 1) * kTile > all_see;  // the same for the warp
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c)
+                        if (((c & ~3) | ((c & 1) << 1) | ((c >> 1) & 1)) >= left) y[c] = -INFINITY;
+                }
+#pragma unroll
+                for (int c = 0; c < kTile; ++c) top = fmaxf(top, y[c]);
+                // a NaN or infinite V scale that this row sees makes its sum NaN
+                float add = 0.0f;
+                if (b.nan_v[i & 3][0] | b.nan_v[i & 3][1] | b.nan_v[i & 3][2] | b.nan_v[i & 3][3]) {
+                    for (int c = 0; c < kTile; ++c)
+                        if ((b.nan_v[i & 3][c >> 5] >> (c & 31) & 1) && swapped(c) < left) add = __int_as_float(0x7fffffff);
+                }
+                // P and O are free once the tile before is done
+                if (i > 0 && !(ok = wait_for(&b.pv_done, (i - 1) & 1, b, a.err))) break;
+                fence_after();
+                const bool grown = top > m + kLazy;
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float mn = grown ? top : m, f = ex2f(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (tile > w.lo) {
+#pragma unroll 1
+                        for (int c = 0; c < hd; c += 16) {
+                            uint32_t o[16];
+                            tm_load16(tmem + lanes + kColO + c, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tm_store16(tmem + lanes + kColO + c, o);
+                        }
+                    }
+                }
+                const float off = kBias - m;
+                float sum = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kTile; c += 32) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float p = ex2f(y[c + 2 * e] + off), q = ex2f(y[c + 2 * e + 1] + off);
+                        sum += p + q;
+                        hi[e] = pack2(p, q);
+                        const float2 h = unpack2(hi[e]);
+                        lo[e] = pack2(p - h.x, q - h.y);
+                    }
+                    tm_store16(tmem + lanes + kColP + c / 2, hi);
+                    tm_store16(tmem + lanes + kColP + 64 + c / 2, lo);
+                }
+                l = fmaf(sum, power2(b.exps[i & 3][1]), l) + add;
+                tm_store_wait();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.p_ready);
+            }
+            if (!ok) break;
+            if (w.lo < w.hi) {
+                if (!(ok = wait_for(&b.pv_done, (i - 1) & 1, b, a.err))) break;
+                fence_after();
+            }
+            const bool whole = w.lo == 0 && w.hi == w.tiles;
+            float *part = a.part + (2 * (int64_t)blockIdx.x + (w.lo == 0)) * (kRows * (hd + 2));
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+            for (int c = 0; c < hd; c += 32) {
+                float v[32];
+                if (w.lo < w.hi) {
+                    uint32_t o[16];
+                    tm_load16(tmem + lanes + kColO + c, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]);
+                    tm_load16(tmem + lanes + kColO + c + 16, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[16 + e] = __uint_as_float(o[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                }
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = l == 0.0f ? 0.0f : v[e] * inv;
+                    if (live) write_block(a, v, row, col0 + c, q_dim, q_pad);
+                } else if (live) {
+                    float4 *o = reinterpret_cast<float4 *>(part + r * hd + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
+            }
+            if (!whole) {
+                if (live) *reinterpret_cast<float2 *>(part + kRows * hd + 2 * r) = make_float2(m, l);
+                // the CTAs with a part of the item, in order: CTA c0 has the first, the parts follow one another
+                if (r == 0) {
+                    int c = static_cast<int>(min(w.at / max(line.step, (int64_t)1), (int64_t)line.ctas - 1));
+                    while (line.begin(c) > w.at) --c;
+                    while (tile_at(line.begin(c + 1) - w.at, w.tiles) == 0) ++c;
+                    int n = 0;
+                    for (int k = c; k < line.ctas && tile_at(line.begin(k) - w.at, w.tiles) < w.tiles; ++k) ++n;
+                    b.first_part = c;
+                    b.parts = n;
+                }
+                __threadfence();
+                if (!(ok = four_warps(&b.out_sync, phase, b, a.err))) break;
+                if (r == 0) {
+                    int *counter = a.counters + b.first_part;
+                    const int arrived = atomicAdd(counter, 1);
+                    b.last = arrived == b.parts - 1;
+                    if (b.last) *counter = 0;
+                }
+                if (!(ok = four_warps(&b.out_sync, phase, b, a.err))) break;
+                if (b.last) {
+                    __threadfence();
+                    const int c0 = b.first_part, n = b.parts;
+                    if (live) {
+                        const int64_t size = kRows * (hd + 2);
+                        auto part_of = [&](int k) {
+                            return a.part + (2 * (int64_t)(c0 + k) + (tile_at(line.begin(c0 + k) - w.at, w.tiles) == 0)) * size;
+                        };
+                        float mm = -1e37f, ll = 0.0f;
+                        for (int k = 0; k < n; ++k) mm = fmaxf(mm, __ldcg(part_of(k) + kRows * hd + 2 * r));
+                        for (int k = 0; k < n; ++k) {
+                            const float2 x = __ldcg(reinterpret_cast<const float2 *>(part_of(k) + kRows * hd + 2 * r));
+                            ll = fmaf(x.y, ex2f(x.x - mm), ll);
+                        }
+                        const float iv = ll == 0.0f ? 0.0f : 1.0f / ll;
+#pragma unroll 1
+                        for (int c = 0; c < hd; c += 32) {
+                            float v[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                            for (int k = 0; k < n; ++k) {
+                                const float *p = part_of(k);
+                                const float f = ex2f(__ldcg(p + kRows * hd + 2 * r) - mm) * iv;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + r * hd + c) + e);
+                                    v[4 * e] = fmaf(x.x, f, v[4 * e]);
+                                    v[4 * e + 1] = fmaf(x.y, f, v[4 * e + 1]);
+                                    v[4 * e + 2] = fmaf(x.z, f, v[4 * e + 2]);
+                                    v[4 * e + 3] = fmaf(x.w, f, v[4 * e + 3]);
+                                }
+                            }
+                            write_block(a, v, row, col0 + c, q_dim, q_pad);
+                        }
+                    }
+                }
+                if (!(ok = four_warps(&b.out_sync, phase, b, a.err))) break;  // first_part, parts and last are read
+            }
+            // the zero padding of the Q8_1 rows, with kv head 0 and its first query head
+            if (a.att_q8 && w.h == 0 && w.lo == 0 && live && col0 == 0) {
+                int8_t *q8 = static_cast<int8_t *>(a.att_q8);
+                float *qd = reinterpret_cast<float *>(q8 + a.n_rows * q_pad), *qs = qd + a.n_rows * (q_pad / 32);
+                for (int c = q_dim; c < q_pad; c += 32) {
+                    uint4 *o = reinterpret_cast<uint4 *>(q8 + row * q_pad + c);
+                    o[0] = o[1] = make_uint4(0u, 0u, 0u, 0u);
+                    qd[row * (q_pad / 32) + c / 32] = 0.0f;
+                    qs[row * (q_pad / 32) + c / 32] = 0.0f;
+                }
+            }
+            // O is read: the next item's first product may overwrite it (p_ready orders it)
+            fence_before();
+            more = next_item(w, a, line, group);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <int NB>
+cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
+{
+    using L = Lay<NB>;
+    static_assert(L::bytes <= 227 * 1024, "");
+    static std::atomic<uint64_t> done{0};  // devices on which the kernel may have that much
+    const uint64_t bit = 1ull << (dev_info().device & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        cudaError_t e = cudaFuncSetAttribute(paged_attention_tc_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)dev_info().sm_count);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_use_pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, paged_attention_tc_kernel<NB>, a);
+}
+
+}  // namespace
+
+size_t paged_attention_tc_part_bytes(int head_dim) { return 2 * (size_t)dev_info().sm_count * kRows * (head_dim + 2) * 4; }
+
+bool paged_attention_tc_takes(int head_dim) { return head_dim == 64 || head_dim == 128; }
+
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, cudaStream_t s)
+{
+    return a.kv.head_dim == 64 ? launch<2>(a, s) : launch<4>(a, s);
+}
+
+}  // namespace rz

@@ -428,6 +428,53 @@ def test_attention_new_tokens(rz, m):
     s.check(s.run(rz).cpu().numpy())
 
 
+@pytest.mark.parametrize("hd,H,K", [(128, 8, 2), (64, 14, 2), (128, 4, 4), (128, 16, 1), (64, 7, 1), (96, 4, 2)])
+@pytest.mark.parametrize("page", [16, 128])
+def test_attention_prompt_chunks(rz, hd, H, K, page):
+    """Many rows: whole prompts, chunks behind a context, odd sizes, beside decodes and empty requests."""
+    s = Setup(hd + H + page, H, K, hd, page, [(130, 130), (1000, 65), (129, 128), (5, 5), (700, 1), (0, 0), (257, 256), (1500, 33)])
+    s.check(s.run(rz).cpu().numpy())
+
+
+@pytest.mark.parametrize("n,m", [(64, 64), (65, 65), (127, 127), (128, 128), (129, 129), (4000, 1000), (20, 200), (3, 150), (0, 150), (2999, 300)])
+def test_attention_one_prompt_chunk(rz, n, m):
+    s = Setup(n + m, 4, 2, 128, 64, [(n, m)])
+    out = s.run(rz).cpu().numpy()
+    assert not out[:max(m - n, 0)].any()
+    s.check(out)
+
+
+@pytest.mark.parametrize("spread,sharp,v_mean", [(1e-4, 0.01, 0.0), (3e4, 12.0, 0.0), (1.0, 12.0, 4.0), (1.0, 1.0, 4.0)])
+def test_attention_prompt_chunk_scales(rz, spread, sharp, v_mean):
+    s = Setup(8, 4, 2, 128, 16, [(900, 200), (33, 33), (2500, 100)], spread=spread, sharp=sharp, v_mean=v_mean)
+    s.check(s.run(rz).cpu().numpy())
+
+
+def test_attention_prompt_chunk_nan_and_padding(rz):
+    """NaN keys and values reach the rows that see them and no others; rows behind the last stay; q8; repeats."""
+    import torch
+    s = Setup(13, 4, 2, 64, 16, [(500, 200), (60, 1)], extra_rows=5)
+    out = torch.full((s.T, 256), 2.5, device="cuda")
+    q8 = torch.full((rz.q8_1_size(s.T, 256),), 0x55, dtype=torch.uint8, device="cuda")
+    good = s.run(rz, out=out, att_q8=q8).clone()
+    assert (good[201:] == 2.5).all()
+    assert torch.equal(q8.view(-1)[:201 * 256], rz.q8_1_quantize(good[:201].contiguous())[:201 * 256])
+    ds = q8[s.T * 256:].view(torch.float32).view(2, s.T, 8)
+    want = rz.q8_1_quantize(good[:201].contiguous())[201 * 256:].view(torch.float32).view(2, 201, 8)
+    assert torch.equal(ds[:, :201], want) and (q8[s.T * 256:].view(2, s.T, 32)[:, 201:] == 0x55).all()
+    for _ in range(3):
+        assert torch.equal(s.run(rz, out=out), good)
+    # token 450's value scale in kv head 1, token 470's key scale in kv head 0 (rows 150 and 170 are the first that see them)
+    for token, head, scales in ((450, 1, 17), (470, 0, 8)):
+        at = R.record_of(16, 2, 64, int(s.slots[0][token]), head) + scales * 64 + (token % 16) * 4
+        s.kv.pages.view(-1)[at:at + 4] = torch.tensor([0, 0x7e, 0, 0x7e], dtype=torch.uint8, device="cuda")
+    bad = s.run(rz, out=out)
+    seen = torch.zeros_like(good, dtype=torch.bool)
+    seen[150:200, 128:] = True
+    seen[170:200, :128] = True
+    assert torch.isnan(bad[seen]).all() and torch.equal(bad[~seen], good[~seen])
+
+
 def test_attention_long_and_split_over_all_ctas(rz):
     s = Setup(2, 4, 1, 128, 64, [(40001, 1)])
     s.check(s.run(rz).cpu().numpy())
@@ -547,10 +594,11 @@ def test_attention_bad_device_data_is_reported(rz, what):
     out = torch.zeros_like(good)
     s.run(rz, out=out)
     assert device_error(rz) == (0x206 if "page" in what else 0x203)
-    if what not in ("offsets", "rows"):
+    if "page" in what:
         assert torch.equal(out[[0, 2]], good[[0, 2]])
-    if what == "length":
-        assert not out[1].any()
+    elif what == "length":
+        s.reqs[1] = (0, 1)  # an empty request: zeros, and the others by the usual bound (their work is split elsewhere)
+        s.check(out.cpu().numpy())
     check_no_device_error()
 
 
