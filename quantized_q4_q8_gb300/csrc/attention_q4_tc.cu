@@ -15,7 +15,7 @@
 // multiplied and added.  K and V are brought near 1 by a power of two for each tile
 // (exact), so that f16 holds them whatever their scale; it goes into the exponents.
 //
-// Softmax: a thread has one row: its 128 scores, its running maximum and sum.  The sums O stay in
+// Softmax: two threads have a row, 64 of its scores each, and its running maximum and sum.  The sums O stay in
 // tensor memory and are rescaled there when a row's maximum has grown by over 2^8, and not before
 // (see attention_q4.cu).
 //
@@ -23,8 +23,8 @@
 // and V of tile i + 1 and form the weights of tile i + 1 from S, of which there are two:
 //   warp 0       copies records (K, V's scales; V's codes) with the bulk-copy engine
 //   warp 1       issues the products: QK(0), QK(1), PV(0), QK(2), PV(1), ...
-//   warps 4-7    softmax, and the outputs
-//   warps 8-11   unpack: K(0), K(1), V(0), K(2), V(1), ...
+//   warps 4-11   softmax, and the outputs: two threads a row, 64 columns each
+//   warps 12-15  unpack K, warps 16-19 V
 // Operands lie in core matrices of 8 rows x 16 bytes without a swizzle.  Within every 4 values of the
 // inner dimension the order is 0, 2, 1, 3, that in which a word of packed codes unpacks into two
 // pairs: for K over the head's values (Q is laid out alike), for V over the tokens (so S's columns,
@@ -49,7 +49,7 @@ namespace {
 constexpr int kRows = 128;  // query rows of an item
 constexpr int kTile = 128;  // tokens of a tile
 constexpr int kGroups = kTile / 16;
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kItemCost = 2;  // of an item's start and end, in tiles
 constexpr float kLazy = 8.0f, kBias = 7.0f;
 constexpr int kScaleTop = 8;  // the largest |d| of a tile becomes 2^8 .. 2^9
@@ -67,18 +67,19 @@ struct Lay {
     static constexpr int off_q = 0, off_k = off_q + 2 * q, off_v = off_k + 2 * q;
     static constexpr int off_raw_k = off_v + 2 * v, off_raw_v = off_raw_k + 2 * raw_k;
     static constexpr int off_scale = off_raw_v + raw_v;                   // f16: K [128][NB], V twice
-    static constexpr int off_misc = off_scale + 3 * kTile * NB * 2;
+    static constexpr int off_row = off_scale + 3 * kTile * NB * 2;        // a row's two maxima, or sums
+    static constexpr int off_misc = off_row + 4 * kRows * 4;
     static constexpr int bytes = off_misc + 512;
 };
 
 struct Bars {
     uint64_t raw_k_full[2], raw_k_empty[2], raw_v_full, raw_v_empty;
-    uint64_t k_ready, k_free, v_ready, pv_done, s_full[2], s_free[2], p_ready, q_ready, unpack_sync, out_sync, done;
+    uint64_t k_ready, k_free, v_ready, pv_done, s_full[2], s_free[2], p_ready, q_ready, k_sync, v_sync, out_sync, pair[4], done;
     uint32_t tmem;
     int gave_up, last;      // a wait ran out; this CTA adds the parts up
     int exps[4][2];         // of tiles i mod 4: K's and V's exponents
     uint32_t nan_v[4][4];   // their tokens with a NaN or infinite V scale, by position
-    uint32_t warp_max[4][2];
+    uint32_t warp_max[2][4];
     int parts, first_part;
 };
 
@@ -157,6 +158,26 @@ __device__ __forceinline__ void tm_load16(uint32_t at, uint32_t (&r)[16])
         : RZ_O16(r)
         : "r"(at)
         : "memory");
+}
+// 64 columns
+__device__ __forceinline__ void tm_load64(uint32_t at, float (&v)[64])
+{
+    uint32_t r[4][16];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : RZ_O16(r[k])
+            : "r"(at + 16 * k)
+            : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            asm volatile("" : "+r"(r[k][e]));  // not before the wait
+            v[16 * k + e] = __uint_as_float(r[k][e]);
+        }
 }
 __device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&r)[16])
 {
@@ -268,8 +289,8 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, unsigned par, Bars &b, u
     return ok;
 }
 
-// A barrier of four warps that no warp waits at for ever; phase counts its uses.
-__device__ __forceinline__ bool four_warps(uint64_t *bar, unsigned &phase, Bars &b, unsigned *err)
+// A barrier of some warps at which none waits for ever; phase counts its uses.
+__device__ __forceinline__ bool sync_warps(uint64_t *bar, unsigned &phase, Bars &b, unsigned *err)
 {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
@@ -383,20 +404,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.raw_k_full[i], 1);
-            mbar_init(&b.raw_k_empty[i], 4);
+            mbar_init(&b.raw_k_empty[i], 8);
             mbar_init(&b.s_full[i], 1);
-            mbar_init(&b.s_free[i], 4);
+            mbar_init(&b.s_free[i], 8);
         }
         mbar_init(&b.raw_v_full, 1);
         mbar_init(&b.raw_v_empty, 4);
-        mbar_init(&b.k_ready, 4);
+        mbar_init(&b.k_ready, 8);  // K's warps, and V's with the exponents of its scales
         mbar_init(&b.k_free, 1);
         mbar_init(&b.v_ready, 4);
         mbar_init(&b.pv_done, 1);
-        mbar_init(&b.p_ready, 4);
-        mbar_init(&b.q_ready, 4);
-        mbar_init(&b.unpack_sync, 4);
-        mbar_init(&b.out_sync, 4);
+        mbar_init(&b.p_ready, 8);
+        mbar_init(&b.q_ready, 8);
+        mbar_init(&b.k_sync, 4);
+        mbar_init(&b.v_sync, 4);
+        mbar_init(&b.out_sync, 8);
+        for (int i = 0; i < 4; ++i) mbar_init(&b.pair[i], 2);
         mbar_init(&b.done, 1);
         b.gave_up = b.last = 0;
         fence_mbar_init();
@@ -413,10 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
     bool more = true, ok = true;
     int i = 0;  // tiles of this CTA so far
 
-    // Registers: launched with 168 a thread, 504 for the three warpgroups together; the first gives
-    // 72 of its own to the softmax warps.
+    // Registers: launched with 96 a thread, 480 for the five warpgroups together: 80 for the first,
+    // 120 each for the softmax warps', 80 each for those that unpack.
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 0) {
         // ------------------------------------------------------------ copies
         // K(i + 1) before V(i), the order in which they are unpacked
@@ -470,8 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         if (n_v > 0) mbar_wait(&b.raw_v_full, (n_v - 1) & 1);
         } else if (warp == 1) {
         // ------------------------------------------------------------ products
-        const uint32_t q0 = smem_u32(sm + L::off_q), k0 = smem_u32(sm + L::off_k), v0 = smem_u32(sm + L::off_v);
+        // descriptors of the first pieces; 16 values on are 256 bytes, 16 in a descriptor's unit
         constexpr uint32_t stride_q = hd * 16, stride_v = kTile * 16;  // 8 rows
+        const uint64_t q0 = operand_desc(smem_u32(sm + L::off_q), stride_q), k0 = operand_desc(smem_u32(sm + L::off_k), stride_q),
+                       v0 = operand_desc(smem_u32(sm + L::off_v), stride_v);
         int item = 0;
         // QK(j): A = Q, B = K; high * high, low * high, high * low
         auto qk = [&](int j) {
@@ -483,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 for (int p = 0; p < 3; ++p)
 #pragma unroll
                     for (int k = 0; k < hd / 16; ++k)
-                        mma_ss(d, operand_desc(q0 + (p == 1 ? L::q : 0) + 256 * k, stride_q),
-                               operand_desc(k0 + (p == 2 ? L::q : 0) + 256 * k, stride_q), idesc_f16(kTile), p || k);
+                        mma_ss(d, q0 + (p == 1 ? L::q / 16 : 0) + 16 * k, k0 + (p == 2 ? L::q / 16 : 0) + 16 * k,
+                               idesc_f16(kTile), p || k);
                 commit(&b.k_free);
                 commit(&b.s_full[j & 1]);
             }
@@ -500,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 for (int p = 0; p < 3; ++p)
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(d, tmem + kColP + (p == 1 ? 64 : 0) + 8 * k,
-                               operand_desc(v0 + (p == 2 ? L::v : 0) + 256 * k, stride_v), idesc_f16(hd), !start || p || k);
+                        mma_ts(d, tmem + kColP + (p == 1 ? 64 : 0) + 8 * k, v0 + (p == 2 ? L::v / 16 : 0) + 16 * k,
+                               idesc_f16(hd), !start || p || k);
                 commit(&b.pv_done);
             }
             __syncwarp();
@@ -526,110 +551,115 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         }
         __syncwarp();
         }
-    } else if (warp >= 8) {
+    } else if (warp >= 12) {
         // ------------------------------------------------------------ unpacking
-        const int t128 = tid - 256, w4 = warp - 8, g = lane >> 2, t = lane & 3;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        const bool for_v = warp >= 16;
+        const int tok128 = (tid - 384) & 127, w4 = warp & 3, g = lane >> 2, t = lane & 3;
         uint16_t *sk = reinterpret_cast<uint16_t *>(sm + L::off_scale), *sv = sk + kTile * NB;
         unsigned phase = 0;
         // two words' codes c0, c1 times their scales, high and low piece, to 8 bytes of a chunk
-        auto put = [&](uint8_t *hi_base, int piece, int kk, int half, uint32_t c0, uint32_t c1, uint32_t d0, uint32_t d1) {
+        auto put = [&](uint8_t *p, int piece, uint32_t c0, uint32_t c1, uint32_t d0, uint32_t d1) {
             const uint32_t h0 = hmul2u(c0, d0), h1 = hmul2u(c1, d1);
-            const uint32_t l0 = hfma2u(c0, d0, h0 ^ 0x80008000u), l1 = hfma2u(c1, d1, h1 ^ 0x80008000u);
-            uint8_t *p = hi_base + kk * 128 + half * 8;
             *reinterpret_cast<uint2 *>(p) = make_uint2(h0, h1);
-            *reinterpret_cast<uint2 *>(p + piece) = make_uint2(l0, l1);
+            *reinterpret_cast<uint2 *>(p + piece) = make_uint2(hfma2u(c0, d0, h0 ^ 0x80008000u), hfma2u(c1, d1, h1 ^ 0x80008000u));
         };
-        auto unpack_k = [&](int j, int valid) {
-            const int slot = j & 1;
-            if (!wait_for(&b.raw_k_full[slot], (j >> 1) & 1, b, a.err)) return false;
-            const uint8_t *raw = sm + L::off_raw_k + slot * L::raw_k;
-            // this thread's token: its scales, and the tile's largest of each kind
-            uint16_t dk[NB], dv[NB];
-            uint32_t mk = 0, mv = 0;
+        // The scales of tile j's K or V, a token a thread, times 2^up: the tile's largest to
+        // 2^8 .. 2^9 (a tile of zeros: as it is).
+        auto scales = [&](int j, int valid) {
+            if (!wait_for(&b.raw_k_full[j & 1], (j >> 1) & 1, b, a.err)) return false;
+            const uint8_t *raw = sm + L::off_raw_k + (j & 1) * L::raw_k + (tok128 >> 4) * 10 * hd + (for_v ? 9 * hd : 8 * hd);
+            const uint16_t *src = reinterpret_cast<const uint16_t *>(raw) + (tok128 & 15) * NB;
+            uint16_t d[NB];
+            uint32_t most = 0;
             bool bad = false;
-            const uint16_t *pk = reinterpret_cast<const uint16_t *>(raw + (t128 >> 4) * 10 * hd + 8 * hd) + (t128 & 15) * NB;
-            const uint16_t *pv = pk + hd / 2;
-            const bool live = t128 < valid;
 #pragma unroll
             for (int e = 0; e < NB; ++e) {
-                dk[e] = live ? pk[e] : uint16_t(0);
-                dv[e] = live ? pv[e] : uint16_t(0);
-                const uint32_t ak = dk[e] & 0x7fffu, av = dv[e] & 0x7fffu;
-                if (ak < 0x7c00u) mk = max(mk, ak);
-                if (av < 0x7c00u) mv = max(mv, av);
+                d[e] = tok128 < valid ? src[e] : uint16_t(0);
+                const uint32_t abs = d[e] & 0x7fffu;
+                if (abs < 0x7c00u) most = max(most, abs);
                 else bad = true;
             }
-            mk = __reduce_max_sync(0xffffffffu, mk);
-            mv = __reduce_max_sync(0xffffffffu, mv);
+            most = __reduce_max_sync(0xffffffffu, most);
             const unsigned bads = __ballot_sync(0xffffffffu, bad);
             if (lane == 0) {
-                b.warp_max[w4][0] = mk;
-                b.warp_max[w4][1] = mv;
+                b.warp_max[for_v][w4] = most;
                 // by position: bits 1 and 2 of every 4 change places
-                b.nan_v[j & 3][w4] = (bads & 0x99999999u) | ((bads & 0x22222222u) << 1) | ((bads & 0x44444444u) >> 1);
+                if (for_v) b.nan_v[j & 3][w4] = (bads & 0x99999999u) | ((bads & 0x22222222u) << 1) | ((bads & 0x44444444u) >> 1);
             }
-            if (!four_warps(&b.unpack_sync, phase, b, a.err)) return false;
-            mk = max(max(b.warp_max[0][0], b.warp_max[1][0]), max(b.warp_max[2][0], b.warp_max[3][0]));
-            mv = max(max(b.warp_max[0][1], b.warp_max[1][1]), max(b.warp_max[2][1], b.warp_max[3][1]));
-            // d 2^up: the largest to 2^8 .. 2^9 (a tile of zeros: as it is)
-            const int uk = mk ? kScaleTop + 127 - (__float_as_int(h2f((uint16_t)mk)) >> 23) : 0;
-            const int uv = mv ? kScaleTop + 127 - (__float_as_int(h2f((uint16_t)mv)) >> 23) : 0;
-            if (t128 == 0) {
-                b.exps[j & 3][0] = uk;
-                b.exps[j & 3][1] = uv;
-            }
+            uint64_t *sync = for_v ? &b.v_sync : &b.k_sync;
+            if (!sync_warps(sync, phase, b, a.err)) return false;
+            most = max(max(b.warp_max[for_v][0], b.warp_max[for_v][1]), max(b.warp_max[for_v][2], b.warp_max[for_v][3]));
+            const int up = most ? kScaleTop + 127 - (__float_as_int(h2f((uint16_t)most)) >> 23) : 0;
+            if (tok128 == 0) b.exps[j & 3][for_v] = up;
+            uint16_t *dst = for_v ? sv + (j & 1) * kTile * NB : sk;
 #pragma unroll
             for (int e = 0; e < NB; ++e) {
-                sk[t128 * NB + e] = __half_as_ushort(__float2half_rn(h2f(dk[e]) * power2(uk)));
                 // a V scale that is no number: nothing is added, and the row's sum is made NaN
-                const bool fine = (dv[e] & 0x7fffu) < 0x7c00u;
-                sv[(j & 1) * kTile * NB + t128 * NB + e] = fine ? __half_as_ushort(__float2half_rn(h2f(dv[e]) * power2(uv))) : uint16_t(0);
+                const bool drop = for_v && (d[e] & 0x7fffu) >= 0x7c00u;
+                dst[tok128 * NB + e] = drop ? uint16_t(0) : __half_as_ushort(__float2half_rn(h2f(d[e]) * power2(up)));
             }
-            if (!four_warps(&b.unpack_sync, phase, b, a.err)) return false;
+            return sync_warps(sync, phase, b, a.err);
+        };
+        auto unpack_k = [&](int j) {
+            const uint8_t *raw = sm + L::off_raw_k + (j & 1) * L::raw_k;
             if (!wait_for(&b.k_free, (j & 1) ^ 1u, b, a.err)) return false;
-            // warp w4: groups 2 w4, 2 w4 + 1; lane (g, t): word t of each block of rows 8 hf + g
+            // groups 2 w4, 2 w4 + 1; lane (g, t): word t of each block of rows 8 hf + g
 #pragma unroll
-            for (int gr = 2 * w4; gr < 2 * w4 + 2; ++gr)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int pos = 8 * hf + g, tok = swapped(pos);
-                    const uint8_t *r = raw + gr * 10 * hd + tok * (hd / 2) + t * 4 * NB;
-                    uint8_t *dst = sm + L::off_k + (2 * gr + hf) * (hd * 16) + g * 16;
-#pragma unroll
-                    for (int e = 0; e < NB; ++e) {
-                        const uint32_t x = reinterpret_cast<const uint32_t *>(r)[e], y = x >> 8;
-                        const uint32_t d = sk[(gr * 16 + tok) * NB + e] * 0x10001u;
-                        put(dst, L::q, 4 * e + (t >> 1), t & 1, codes_low(x), codes_low(y), d, d);
-                        put(dst, L::q, 4 * e + 2 + (t >> 1), t & 1, codes_high(x), codes_high(y), d, d);
-                    }
+            for (int k = 0; k < 4; ++k) {
+                const int gr = 2 * w4 + (k >> 1), hf = k & 1, tok = swapped(8 * hf + g);
+                const uint32_t *r = reinterpret_cast<const uint32_t *>(raw + gr * 10 * hd + tok * (hd / 2) + t * 4 * NB);
+                uint32_t x[NB], s2[(NB + 1) / 2];
+                if constexpr (NB == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(r);
+                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                    const uint2 d = *reinterpret_cast<const uint2 *>(sk + (gr * 16 + tok) * NB);
+                    s2[0] = d.x, s2[1] = d.y;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(r);
+                    x[0] = v.x, x[1] = v.y;
+                    s2[0] = *reinterpret_cast<const uint32_t *>(sk + (gr * 16 + tok) * NB);
                 }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&b.k_ready);
-                mbar_arrive(&b.raw_k_empty[slot]);
+                uint8_t *dst = sm + L::off_k + (2 * gr + hf) * (hd * 16) + g * 16 + (t >> 1) * 128 + (t & 1) * 8;
+#pragma unroll
+                for (int e = 0; e < NB; ++e) {
+                    const uint32_t y = x[e] >> 8, d = __byte_perm(s2[e >> 1], 0, (e & 1) ? 0x3232 : 0x1010);
+                    put(dst + 4 * e * 128, L::q, codes_low(x[e]), codes_low(y), d, d);
+                    put(dst + (4 * e + 2) * 128, L::q, codes_high(x[e]), codes_high(y), d, d);
+                }
             }
             return true;
         };
         auto unpack_v = [&](int j) {
             if (!wait_for(&b.raw_v_full, j & 1, b, a.err)) return false;
             if (j > 0 && !wait_for(&b.pv_done, (j - 1) & 1, b, a.err)) return false;
-            const uint8_t *raw = sm + L::off_raw_v;
-            const uint16_t *s = sv + (j & 1) * kTile * NB;
-            constexpr int run = q4_v_run(NB);
-#pragma unroll
+#pragma unroll 1
             for (int gr = 2 * w4; gr < 2 * w4 + 2; ++gr) {
-                const uint16_t *d = s + (gr * 16 + 4 * t) * NB;
+                // scales of tokens 4 t .. 4 t + 3: half i * NB + e
+                uint32_t d[2 * NB];
+                const uint4 *dp = reinterpret_cast<const uint4 *>(sv + (j & 1) * kTile * NB + (gr * 16 + 4 * t) * NB);
 #pragma unroll
-                for (int r = 0; r < 2 * NB; ++r) {
-                    const uint32_t x = *reinterpret_cast<const uint32_t *>(raw + gr * 8 * hd + ((r / run) * 32 + lane) * run * 4 + (r % run) * 4);
-                    const uint32_t y = x >> 8;
-                    const int e = r >> 1;
-                    const uint32_t d0 = d[e] | (uint32_t)d[2 * NB + e] << 16, d1 = d[NB + e] | (uint32_t)d[3 * NB + e] << 16;
-                    // rows (values) 32 e + 8 (r % 2) + g and 16 more; columns 16 gr + 4 t ..
-                    uint8_t *dst = sm + L::off_v + (4 * e + (r & 1)) * (kTile * 16) + g * 16;
-                    put(dst, L::v, 2 * gr + (t >> 1), t & 1, codes_low(x), codes_low(y), d0, d1);
-                    put(dst + 2 * (kTile * 16), L::v, 2 * gr + (t >> 1), t & 1, codes_high(x), codes_high(y), d0, d1);
+                for (int k = 0; k < NB / 2; ++k) {
+                    const uint4 v = dp[k];
+                    d[4 * k] = v.x, d[4 * k + 1] = v.y, d[4 * k + 2] = v.z, d[4 * k + 3] = v.w;
+                }
+                constexpr int run = q4_v_run(NB);
+                const uint8_t *raw = sm + L::off_raw_v + gr * 8 * hd + lane * run * 4;
+                uint8_t *dst = sm + L::off_v + g * 16 + (2 * gr + (t >> 1)) * 128 + (t & 1) * 8;
+#pragma unroll
+                for (int q = 0; q < 2 * NB / run; ++q) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(raw + q * 32 * run * 4);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 4 * q + k, e = r >> 1;
+                        const uint32_t sel = (e & 1) ? 0x7632 : 0x5410;
+                        const uint32_t d0 = __byte_perm(d[e / 2], d[(2 * NB + e) / 2], sel), d1 = __byte_perm(d[(NB + e) / 2], d[(3 * NB + e) / 2], sel);
+                        // rows (values) 32 e + 8 (r % 2) + g and 16 more; columns 16 gr + 4 t ..
+                        uint8_t *p = dst + (4 * e + (r & 1)) * (kTile * 16);
+                        put(p, L::v, codes_low(x[k]), codes_low(x[k] >> 8), d0, d1);
+                        put(p + 2 * (kTile * 16), L::v, codes_high(x[k]), codes_high(x[k] >> 8), d0, d1);
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -642,19 +672,42 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         };
         while (more && ok) {
             for (int tile = w.lo; tile < w.hi && ok; ++tile, ++i) {
-                ok = unpack_k(i, w.tokens - tile * kTile);
-                if (ok && i > 0) ok = unpack_v(i - 1);
+                ok = scales(i, w.tokens - tile * kTile);
+                if (!ok) break;
+                if (for_v) {
+                    // (not before the tile before is counted)
+                    if (i > 0 && !(ok = wait_for(&b.k_ready, (i - 1) & 1, b, a.err))) break;
+                } else {
+                    if (!(ok = unpack_k(i))) break;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&b.k_ready);
+                    mbar_arrive(&b.raw_k_empty[i & 1]);
+                }
+                if (for_v && i > 0) ok = unpack_v(i - 1);
             }
             if (ok) more = next_item(w, a, line, group);
         }
-        if (ok && i > 0) unpack_v(i - 1);
+        if (ok && for_v && i > 0) unpack_v(i - 1);
     } else {
         // ------------------------------------------------------------ softmax and outputs
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
-        const int r = tid - 128;  // this thread's row of an item
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+        const int half = (warp - 4) >> 2, r = (tid - 128) & 127;  // this thread's columns and row of an item
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        // what the row's other thread gives for v: two places in turn, so that none is written before it is read
+        unsigned pair_phase = 0;
+        auto exchange = [&](float v, float &got) {
+            float *at = reinterpret_cast<float *>(sm + L::off_row) + (pair_phase & 1u) * 2 * kRows + r;
+            at[half * kRows] = v;
+            const bool fine = sync_warps(&b.pair[warp & 3], pair_phase, b, a.err);
+            got = *reinterpret_cast<const volatile float *>(at + (half ^ 1) * kRows);
+            return fine;
+        };
         const int q_dim = a.n_heads * hd, q_pad = (q_dim + 255) / 256 * 256;
         unsigned phase = 0;
+        constexpr int kCols = kTile / 2;
         while (more && ok) {
             if (!has_work(w, line)) {
                 more = next_item(w, a, line, group);
@@ -669,7 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             const int col0 = (w.h * group + (min(my, n_rows - 1) - tok_q * group)) * hd;
             float unit = 0.0f, m = -1e37f, l = 0.0f;
             if (w.lo < w.hi) {
-                // ---- Q's pieces.  The products of the item before that read them are done: their S was waited for.
+                // ---- Q's pieces (both threads look for the largest, each writes half).  The products of the
+                // item before that read them are done: their S was waited for.
                 const float4 *src = reinterpret_cast<const float4 *>(a.q + row * a.ld_q + col0);
                 float mx = 0.0f;
 #pragma unroll 8
@@ -682,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 unit = a.scale * 1.4426950408889634f * power2(-up);
                 uint8_t *dst = sm + L::off_q + (r >> 3) * (hd * 16) + (r & 7) * 16;
 #pragma unroll 4
-                for (int k = 0; k < hd / 8; ++k) {
+                for (int k = half * (hd / 16); k < (half + 1) * (hd / 16); ++k) {
                     const float4 x = __ldg(src + 2 * k), y = __ldg(src + 2 * k + 1);
                     const float f[8] = {x.x, x.z, x.y, x.w, y.x, y.z, y.y, y.w};
                     uint32_t hi[4], lo[4];
@@ -704,32 +758,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 if (!(ok = wait_for(&b.s_full[i & 1], (i >> 1) & 1, b, a.err))) break;
                 fence_after();
                 const float u = unit * power2(-b.exps[i & 3][0]), sub = static_cast<float>(-b.exps[i & 3][1]);
-                float y[kTile];  // log2 of the weights of V as it is unpacked
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < kTile; c += 16) {
-                    uint32_t s[16];
-                    tm_load16(tmem + lanes + kColS + (i & 1) * kTile + c, s);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) y[c + e] = fmaf(__uint_as_float(s[e]), u, sub);
-                }
+                float y[kCols];  // log2 of the weights of V as it is unpacked
+                tm_load64(tmem + lanes + kColS + (i & 1) * kTile + half * kCols, y);
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.s_free[i & 1]);
-                const int left = sees - tile * kTile;
-                const bool masked = (tile + 1) * kTile > all_see;  // the same for the warp
-                if (masked) {
+                float top = -INFINITY, top2 = -INFINITY;
+                const int left = sees - tile * kTile - half * kCols;
+                if ((tile + 1) * kTile > all_see) {  // the same for the warp
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c)
+                    for (int c = 0; c < kCols; ++c) {
+                        y[c] = fmaf(y[c], u, sub);
                         if (((c & ~3) | ((c & 1) << 1) | ((c >> 1) & 1)) >= left) y[c] = -INFINITY;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) y[c] = fmaf(y[c], u, sub);
                 }
 #pragma unroll
-                for (int c = 0; c < kTile; ++c) top = fmaxf(top, y[c]);
+                for (int c = 0; c < kCols; c += 2) {
+                    top = fmaxf(top, y[c]);
+                    top2 = fmaxf(top2, y[c + 1]);
+                }
+                top = fmaxf(top, top2);
+                if (!(ok = exchange(top, top2))) break;
+                top = fmaxf(top, top2);
                 // a NaN or infinite V scale that this row sees makes its sum NaN
                 float add = 0.0f;
-                if (b.nan_v[i & 3][0] | b.nan_v[i & 3][1] | b.nan_v[i & 3][2] | b.nan_v[i & 3][3]) {
-                    for (int c = 0; c < kTile; ++c)
-                        if ((b.nan_v[i & 3][c >> 5] >> (c & 31) & 1) && swapped(c) < left) add = __int_as_float(0x7fffffff);
+                if (b.nan_v[i & 3][2 * half] | b.nan_v[i & 3][2 * half + 1]) {
+                    for (int c = 0; c < kCols; ++c)
+                        if ((b.nan_v[i & 3][2 * half + (c >> 5)] >> (c & 31) & 1) && swapped(c) < left) add = __int_as_float(0x7fffffff);
                 }
                 // P and O are free once the tile before is done
                 if (i > 0 && !(ok = wait_for(&b.pv_done, (i - 1) & 1, b, a.err))) break;
@@ -741,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     l *= f;
                     if (tile > w.lo) {
 #pragma unroll 1
-                        for (int c = 0; c < hd; c += 16) {
+                        for (int c = half * (hd / 2); c < (half + 1) * (hd / 2); c += 16) {
                             uint32_t o[16];
                             tm_load16(tmem + lanes + kColO + c, o);
 #pragma unroll
@@ -751,28 +809,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     }
                 }
                 const float off = kBias - m;
-                float sum = 0.0f;
+                float sum = 0.0f, sum2 = 0.0f;
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) {
+                for (int c = 0; c < kCols; c += 32) {
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float p = ex2f(y[c + 2 * e] + off), q = ex2f(y[c + 2 * e + 1] + off);
-                        sum += p + q;
+                        sum += p;
+                        sum2 += q;
                         hi[e] = pack2(p, q);
                         const float2 h = unpack2(hi[e]);
                         lo[e] = pack2(p - h.x, q - h.y);
                     }
-                    tm_store16(tmem + lanes + kColP + c / 2, hi);
-                    tm_store16(tmem + lanes + kColP + 64 + c / 2, lo);
+                    tm_store16(tmem + lanes + kColP + half * 32 + c / 2, hi);
+                    tm_store16(tmem + lanes + kColP + 64 + half * 32 + c / 2, lo);
                 }
-                l = fmaf(sum, power2(b.exps[i & 3][1]), l) + add;
+                l = fmaf(sum + sum2, power2(b.exps[i & 3][1]), l) + add;
                 tm_store_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.p_ready);
             }
             if (!ok) break;
+            // ---- the row's sum is that of its two threads; each writes half of its values
+            float l2;
+            if (!(ok = exchange(l, l2))) break;
+            l += l2;
             if (w.lo < w.hi) {
                 if (!(ok = wait_for(&b.pv_done, (i - 1) & 1, b, a.err))) break;
                 fence_after();
@@ -781,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             float *part = a.part + (2 * (int64_t)blockIdx.x + (w.lo == 0)) * (kRows * (hd + 2));
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-            for (int c = 0; c < hd; c += 32) {
+            for (int c = half * (hd / 2); c < (half + 1) * (hd / 2); c += 32) {
                 float v[32];
                 if (w.lo < w.hi) {
                     uint32_t o[16];
@@ -806,9 +869,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 }
             }
             if (!whole) {
-                if (live) *reinterpret_cast<float2 *>(part + kRows * hd + 2 * r) = make_float2(m, l);
+                if (live && half == 0) *reinterpret_cast<float2 *>(part + kRows * hd + 2 * r) = make_float2(m, l);
                 // the CTAs with a part of the item, in order: CTA c0 has the first, the parts follow one another
-                if (r == 0) {
+                if (tid == 128) {
                     int c = static_cast<int>(min(w.at / max(line.step, (int64_t)1), (int64_t)line.ctas - 1));
                     while (line.begin(c) > w.at) --c;
                     while (tile_at(line.begin(c + 1) - w.at, w.tiles) == 0) ++c;
@@ -818,14 +881,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     b.parts = n;
                 }
                 __threadfence();
-                if (!(ok = four_warps(&b.out_sync, phase, b, a.err))) break;
-                if (r == 0) {
+                if (!(ok = sync_warps(&b.out_sync, phase, b, a.err))) break;
+                if (tid == 128) {
                     int *counter = a.counters + b.first_part;
                     const int arrived = atomicAdd(counter, 1);
                     b.last = arrived == b.parts - 1;
                     if (b.last) *counter = 0;
                 }
-                if (!(ok = four_warps(&b.out_sync, phase, b, a.err))) break;
+                if (!(ok = sync_warps(&b.out_sync, phase, b, a.err))) break;
                 if (b.last) {
                     __threadfence();
                     const int c0 = b.first_part, n = b.parts;
@@ -842,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                         }
                         const float iv = ll == 0.0f ? 0.0f : 1.0f / ll;
 #pragma unroll 1
-                        for (int c = 0; c < hd; c += 32) {
+                        for (int c = half * (hd / 2); c < (half + 1) * (hd / 2); c += 32) {
                             float v[32];
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = 0.0f;
@@ -862,10 +925,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                         }
                     }
                 }
-                if (!(ok = four_warps(&b.out_sync, phase, b, a.err))) break;  // first_part, parts and last are read
+                if (!(ok = sync_warps(&b.out_sync, phase, b, a.err))) break;  // first_part, parts and last are read
             }
             // the zero padding of the Q8_1 rows, with kv head 0 and its first query head
-            if (a.att_q8 && w.h == 0 && w.lo == 0 && live && col0 == 0) {
+            if (a.att_q8 && w.h == 0 && w.lo == 0 && live && half == 0 && col0 == 0) {
                 int8_t *q8 = static_cast<int8_t *>(a.att_q8);
                 float *qd = reinterpret_cast<float *>(q8 + a.n_rows * q_pad), *qs = qd + a.n_rows * (q_pad / 32);
                 for (int c = q_dim; c < q_pad; c += 32) {
