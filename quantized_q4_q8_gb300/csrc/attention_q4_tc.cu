@@ -159,12 +159,12 @@ __device__ __forceinline__ void tm_load16(uint32_t at, uint32_t (&r)[16])
         : "r"(at)
         : "memory");
 }
-// 64 columns
-__device__ __forceinline__ void tm_load64(uint32_t at, float (&v)[64])
+// 32 columns
+__device__ __forceinline__ void tm_load32(uint32_t at, float (&v)[32])
 {
-    uint32_t r[4][16];
+    uint32_t r[2][16];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 2; ++k)
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
             : RZ_O16(r[k])
@@ -172,7 +172,7 @@ __device__ __forceinline__ void tm_load64(uint32_t at, float (&v)[64])
             : "memory");
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             asm volatile("" : "+r"(r[k][e]));  // not before the wait
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             const uint8_t *raw = sm + L::off_raw_k + (j & 1) * L::raw_k;
             if (!wait_for(&b.k_free, (j & 1) ^ 1u, b, a.err)) return false;
             // groups 2 w4, 2 w4 + 1; lane (g, t): word t of each block of rows 8 hf + g
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 const int gr = 2 * w4 + (k >> 1), hf = k & 1, tok = swapped(8 * hf + g);
                 const uint32_t *r = reinterpret_cast<const uint32_t *>(raw + gr * 10 * hd + tok * (hd / 2) + t * 4 * NB);
@@ -758,29 +758,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 if (!(ok = wait_for(&b.s_full[i & 1], (i >> 1) & 1, b, a.err))) break;
                 fence_after();
                 const float u = unit * power2(-b.exps[i & 3][0]), sub = static_cast<float>(-b.exps[i & 3][1]);
-                float y[kCols];  // log2 of the weights of V as it is unpacked
-                tm_load64(tmem + lanes + kColS + (i & 1) * kTile + half * kCols, y);
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.s_free[i & 1]);
-                float top = -INFINITY, top2 = -INFINITY;
+                // The scores are read twice, 32 at a time in loops that are not unrolled, and not kept: code for
+                // 64 values at once, of 8 warps beside 8 others with code of their own, waits for its instructions.
+                const uint32_t at = tmem + lanes + kColS + (i & 1) * kTile + half * kCols;
                 const int left = sees - tile * kTile - half * kCols;
-                if ((tile + 1) * kTile > all_see) {  // the same for the warp
+                const bool masked = (tile + 1) * kTile > all_see;  // the same for the warp
+                float top = -INFINITY, top2 = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 32) {
+                    float s[32];
+                    tm_load32(at + c, s);
+                    if (masked) {
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c) {
-                        y[c] = fmaf(y[c], u, sub);
-                        if (((c & ~3) | ((c & 1) << 1) | ((c >> 1) & 1)) >= left) y[c] = -INFINITY;
+                        for (int e = 0; e < 32; ++e)
+                            if (c + ((e & ~3) | ((e & 1) << 1) | ((e >> 1) & 1)) >= left) s[e] = -INFINITY;
                     }
-                } else {
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c) y[c] = fmaf(y[c], u, sub);
+                    for (int e = 0; e < 32; e += 2) {
+                        top = fmaxf(top, s[e]);
+                        top2 = fmaxf(top2, s[e + 1]);
+                    }
                 }
-#pragma unroll
-                for (int c = 0; c < kCols; c += 2) {
-                    top = fmaxf(top, y[c]);
-                    top2 = fmaxf(top2, y[c + 1]);
-                }
-                top = fmaxf(top, top2);
+                top = fmaf(fmaxf(top, top2), u, sub);  // log2 of the largest weight of V as it is unpacked
                 if (!(ok = exchange(top, top2))) break;
                 top = fmaxf(top, top2);
                 // a NaN or infinite V scale that this row sees makes its sum NaN
@@ -808,14 +807,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                         }
                     }
                 }
-                const float off = kBias - m;
+                const float off = sub + (kBias - m);
                 float sum = 0.0f, sum2 = 0.0f;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kCols; c += 32) {
+                    float s[32];
+                    tm_load32(at + c, s);
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c + ((e & ~3) | ((e & 1) << 1) | ((e >> 1) & 1)) >= left) s[e] = -INFINITY;
+                    }
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p = ex2f(y[c + 2 * e] + off), q = ex2f(y[c + 2 * e + 1] + off);
+                        const float p = ex2f(fmaf(s[2 * e], u, off)), q = ex2f(fmaf(s[2 * e + 1], u, off));
                         sum += p;
                         sum2 += q;
                         hi[e] = pack2(p, q);
@@ -825,6 +831,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     tm_store16(tmem + lanes + kColP + half * 32 + c / 2, hi);
                     tm_store16(tmem + lanes + kColP + 64 + half * 32 + c / 2, lo);
                 }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.s_free[i & 1]);
                 l = fmaf(sum + sum2, power2(b.exps[i & 3][1]), l) + add;
                 tm_store_wait();
                 fence_before();
