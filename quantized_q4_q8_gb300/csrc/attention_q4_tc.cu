@@ -20,7 +20,7 @@
 // (see attention_q4.cu).
 //
 // The tensor pipe is never to wait: while it works P V of tile i, warps unpack K of tile i + 2
-// and V of tile i + 1 and form the weights of tile i + 1 from S, of which there are two:
+// and V of tile i + 1 and form the weights of tile i + 1 from S, of which there are three (P takes its S's place):
 //   warp 0       copies records (K, V's scales; V's codes) with the bulk-copy engine
 //   warp 1       issues the products: QK(0), QK(1), PV(0), QK(2), PV(1), ...
 //   warps 4-11   softmax, and the outputs: two threads a row, 64 columns each
@@ -54,8 +54,10 @@ constexpr int kItemCost = 2;  // of an item's start and end, in tiles
 constexpr float kLazy = 8.0f, kBias = 7.0f;
 constexpr int kScaleTop = 8;  // the largest |d| of a tile becomes 2^8 .. 2^9
 
-// tensor memory columns
-constexpr uint32_t kColS = 0, kColO = 256, kColP = 384;  // S twice, O, P (64 columns of high pieces, 64 of low)
+// Tensor memory columns: S three times (tile i in i mod 3), O.  P takes S's place: of every 32
+// tokens, 16 columns of high pieces, then 16 of low ones.
+constexpr uint32_t kColO = 256;
+__device__ __forceinline__ uint32_t s_column(int third) { return third == 2 ? 384u : 128u * third; }
 
 template <int NB>
 struct Lay {
@@ -74,7 +76,7 @@ struct Lay {
 
 struct Bars {
     uint64_t raw_k_full[2], raw_k_empty[2], raw_v_full, raw_v_empty;
-    uint64_t k_ready, k_free, v_ready, pv_done, s_full[2], s_free[2], p_ready, q_ready, k_sync, v_sync, out_sync, pair[4], done;
+    uint64_t k_ready, v_ready, pv_done[2], s_full[2], p_ready[2], q_ready, k_sync, v_sync, out_sync, pair[4], done;
     uint32_t tmem;
     int gave_up, last;      // a wait ran out; this CTA adds the parts up
     int exps[4][2];         // of tiles i mod 4: K's and V's exponents
@@ -99,6 +101,13 @@ __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b)
 {
     uint32_t d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// a * b - c
+__device__ __forceinline__ uint32_t hfms2u(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("{\n\t.reg .b32 n;\n\tneg.f16x2 n, %3;\n\tfma.rn.f16x2 %0, %1, %2, n;\n\t}" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
 __device__ __forceinline__ uint32_t codes_low(uint32_t w) { return hsub2u(lop_and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u); }
@@ -274,7 +283,7 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, unsigned par, Bars &b, u
 {
     bool ok = false;
     volatile int *gave_up = &b.gave_up;
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    for (uint32_t i = 0; i < kWaitLimit / 8; ++i) {
         if (mbar_try_wait(bar, par)) {
             ok = true;
             break;
@@ -406,15 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             mbar_init(&b.raw_k_full[i], 1);
             mbar_init(&b.raw_k_empty[i], 8);
             mbar_init(&b.s_full[i], 1);
-            mbar_init(&b.s_free[i], 8);
+            mbar_init(&b.p_ready[i], 8);
+            mbar_init(&b.pv_done[i], 1);
         }
         mbar_init(&b.raw_v_full, 1);
         mbar_init(&b.raw_v_empty, 4);
         mbar_init(&b.k_ready, 8);  // K's warps, and V's with the exponents of its scales
-        mbar_init(&b.k_free, 1);
         mbar_init(&b.v_ready, 4);
-        mbar_init(&b.pv_done, 1);
-        mbar_init(&b.p_ready, 8);
         mbar_init(&b.q_ready, 8);
         mbar_init(&b.k_sync, 4);
         mbar_init(&b.v_sync, 4);
@@ -497,37 +504,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         constexpr uint32_t stride_q = hd * 16, stride_v = kTile * 16;  // 8 rows
         const uint64_t q0 = operand_desc(smem_u32(sm + L::off_q), stride_q), k0 = operand_desc(smem_u32(sm + L::off_k), stride_q),
                        v0 = operand_desc(smem_u32(sm + L::off_v), stride_v);
-        int item = 0;
-        // QK(j): A = Q, B = K; high * high, low * high, high * low
-        auto qk = [&](int j) {
-            if (!wait_for(&b.k_ready, j & 1, b, a.err) || !wait_for(&b.s_free[j & 1], ((j >> 1) & 1) ^ 1u, b, a.err)) return false;
+        int item = 0, third = 0;  // i mod 3
+        // QK(j): A = Q, B = K; high * high, low * high, high * low.  S's place holds P(j - 3): of the
+        // item (reused), PV(j - 3) has to be done; of the one before, it is, since Q is there.  (Within an
+        // item PV(j - 1) is not issued yet, so that the phase waited for cannot have been overtaken.)  One
+        // commit a product: a wait or a commit costs this warp some hundred cycles.
+        auto qk = [&](int j, int third, bool reused) {
+            const uint32_t d = tmem + s_column(third);
+            if (reused && !wait_for(&b.pv_done[(j - 3) & 1], ((j - 3) >> 1) & 1, b, a.err)) return false;
+            if (!wait_for(&b.k_ready, j & 1, b, a.err)) return false;
             fence_after();
             if (lane == 0) {
-                const uint32_t d = tmem + kColS + (j & 1) * kTile;
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
 #pragma unroll
                     for (int k = 0; k < hd / 16; ++k)
                         mma_ss(d, q0 + (p == 1 ? L::q / 16 : 0) + 16 * k, k0 + (p == 2 ? L::q / 16 : 0) + 16 * k,
                                idesc_f16(kTile), p || k);
-                commit(&b.k_free);
                 commit(&b.s_full[j & 1]);
             }
             __syncwarp();
             return true;
         };
-        auto pv = [&](int j, bool start) {
-            if (!wait_for(&b.v_ready, j & 1, b, a.err) || !wait_for(&b.p_ready, j & 1, b, a.err)) return false;
+        // PV(j): A = P, B = V
+        auto pv = [&](int j, int third, bool start) {
+            const uint32_t d = tmem + kColO, p0 = tmem + s_column(third);
+            if (!wait_for(&b.v_ready, j & 1, b, a.err) || !wait_for(&b.p_ready[j & 1], (j >> 1) & 1, b, a.err)) return false;
             fence_after();
             if (lane == 0) {
-                const uint32_t d = tmem + kColO;
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(d, tmem + kColP + (p == 1 ? 64 : 0) + 8 * k, v0 + (p == 2 ? L::v / 16 : 0) + 16 * k,
+                        mma_ts(d, p0 + 32 * (k >> 1) + 8 * (k & 1) + (p == 1 ? 16 : 0), v0 + (p == 2 ? L::v / 16 : 0) + 16 * k,
                                idesc_f16(hd), !start || p || k);
-                commit(&b.pv_done);
+                commit(&b.pv_done[j & 1]);
             }
             __syncwarp();
             return true;
@@ -537,10 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 ok = wait_for(&b.q_ready, item & 1, b, a.err);
                 ++item;
                 for (int t = w.lo; t < w.hi && ok; ++t, ++i) {
-                    ok = qk(i);
-                    if (ok && t > w.lo) ok = pv(i - 1, t - 1 == w.lo);
+                    ok = qk(i, third, t - w.lo >= 3);
+                    if (ok && t > w.lo) ok = pv(i - 1, third ? third - 1 : 2, t - 1 == w.lo);
+                    third = third == 2 ? 0 : third + 1;
                 }
-                if (ok) ok = pv(i - 1, w.hi - 1 == w.lo);
+                if (ok) ok = pv(i - 1, third ? third - 1 : 2, w.hi - 1 == w.lo);
             }
             if (ok) more = next_item(w, a, line, group);
         }
@@ -562,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         auto put = [&](uint8_t *p, int piece, uint32_t c0, uint32_t c1, uint32_t d0, uint32_t d1) {
             const uint32_t h0 = hmul2u(c0, d0), h1 = hmul2u(c1, d1);
             *reinterpret_cast<uint2 *>(p) = make_uint2(h0, h1);
-            *reinterpret_cast<uint2 *>(p + piece) = make_uint2(hfma2u(c0, d0, h0 ^ 0x80008000u), hfma2u(c1, d1, h1 ^ 0x80008000u));
+            *reinterpret_cast<uint2 *>(p + piece) = make_uint2(hfms2u(c0, d0, h0), hfms2u(c1, d1, h1));
         };
         // The scales of tile j's K or V, a token a thread, times 2^up: the tile's largest to
         // 2^8 .. 2^9 (a tile of zeros: as it is).
@@ -603,13 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         };
         auto unpack_k = [&](int j) {
             const uint8_t *raw = sm + L::off_raw_k + (j & 1) * L::raw_k;
-            if (!wait_for(&b.k_free, (j & 1) ^ 1u, b, a.err)) return false;
+            // the operand is free once QK(j - 1) is done
+            if (j > 0 && !wait_for(&b.s_full[(j - 1) & 1], ((j - 1) >> 1) & 1, b, a.err)) return false;
             // groups 2 w4, 2 w4 + 1; lane (g, t): word t of each block of rows 8 hf + g
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 const int gr = 2 * w4 + (k >> 1), hf = k & 1, tok = swapped(8 * hf + g);
                 const uint32_t *r = reinterpret_cast<const uint32_t *>(raw + gr * 10 * hd + tok * (hd / 2) + t * 4 * NB);
-                uint32_t x[NB], s2[(NB + 1) / 2];
+                uint32_t x[NB], s2[NB / 2];
                 if constexpr (NB == 4) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(r);
                     x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
@@ -624,15 +637,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
 #pragma unroll
                 for (int e = 0; e < NB; ++e) {
                     const uint32_t y = x[e] >> 8, d = __byte_perm(s2[e >> 1], 0, (e & 1) ? 0x3232 : 0x1010);
-                    put(dst + 4 * e * 128, L::q, codes_low(x[e]), codes_low(y), d, d);
-                    put(dst + (4 * e + 2) * 128, L::q, codes_high(x[e]), codes_high(y), d, d);
+                    put(dst + e * 512, L::q, codes_low(x[e]), codes_low(y), d, d);
+                    put(dst + e * 512 + 256, L::q, codes_high(x[e]), codes_high(y), d, d);
                 }
             }
             return true;
         };
         auto unpack_v = [&](int j) {
             if (!wait_for(&b.raw_v_full, j & 1, b, a.err)) return false;
-            if (j > 0 && !wait_for(&b.pv_done, (j - 1) & 1, b, a.err)) return false;
+            // the operand is free once PV(j - 1) is done
+            if (j > 0 && !wait_for(&b.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, b, a.err)) return false;
 #pragma unroll 1
             for (int gr = 2 * w4; gr < 2 * w4 + 2; ++gr) {
                 // scales of tokens 4 t .. 4 t + 3: half i * NB + e
@@ -677,10 +691,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 if (for_v) {
                     // (not before the tile before is counted)
                     if (i > 0 && !(ok = wait_for(&b.k_ready, (i - 1) & 1, b, a.err))) break;
-                } else {
-                    if (!(ok = unpack_k(i))) break;
-                    fence_proxy_async_smem();
+                } else if (!(ok = unpack_k(i))) {
+                    break;
                 }
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&b.k_ready);
@@ -707,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         };
         const int q_dim = a.n_heads * hd, q_pad = (q_dim + 255) / 256 * 256;
         unsigned phase = 0;
+        int third = 0;  // i mod 3
         constexpr int kCols = kTile / 2;
         while (more && ok) {
             if (!has_work(w, line)) {
@@ -760,7 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 const float u = unit * power2(-b.exps[i & 3][0]), sub = static_cast<float>(-b.exps[i & 3][1]);
                 // The scores are read twice, 32 at a time in loops that are not unrolled, and not kept: code for
                 // 64 values at once, of 8 warps beside 8 others with code of their own, waits for its instructions.
-                const uint32_t at = tmem + lanes + kColS + (i & 1) * kTile + half * kCols;
+                const uint32_t at = tmem + lanes + s_column(third) + half * kCols;
+                third = third == 2 ? 0 : third + 1;
                 const int left = sees - tile * kTile - half * kCols;
                 const bool masked = (tile + 1) * kTile > all_see;  // the same for the warp
                 float top = -INFINITY, top2 = -INFINITY;
@@ -788,11 +804,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     for (int c = 0; c < kCols; ++c)
                         if ((b.nan_v[i & 3][2 * half + (c >> 5)] >> (c & 31) & 1) && swapped(c) < left) add = __int_as_float(0x7fffffff);
                 }
-                // P and O are free once the tile before is done
-                if (i > 0 && !(ok = wait_for(&b.pv_done, (i - 1) & 1, b, a.err))) break;
-                fence_after();
                 const bool grown = top > m + kLazy;
                 if (__any_sync(0xffffffffu, grown)) {
+                    // O is at rest once the tile before is done
+                    if (tile > w.lo) {
+                        if (!(ok = wait_for(&b.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
+                        fence_after();
+                    }
                     const float mn = grown ? top : m, f = ex2f(m - mn);
                     m = mn;
                     l *= f;
@@ -828,17 +846,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                         const float2 h = unpack2(hi[e]);
                         lo[e] = pack2(p - h.x, q - h.y);
                     }
-                    tm_store16(tmem + lanes + kColP + half * 32 + c / 2, hi);
-                    tm_store16(tmem + lanes + kColP + 64 + half * 32 + c / 2, lo);
+                    tm_store16(at + c, hi);  // in the place of the scores that were read
+                    tm_store16(at + c + 16, lo);
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.s_free[i & 1]);
                 l = fmaf(sum + sum2, power2(b.exps[i & 3][1]), l) + add;
                 tm_store_wait();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.p_ready);
+                if (lane == 0) mbar_arrive(&b.p_ready[i & 1]);
             }
             if (!ok) break;
             // ---- the row's sum is that of its two threads; each writes half of its values
@@ -846,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             if (!(ok = exchange(l, l2))) break;
             l += l2;
             if (w.lo < w.hi) {
-                if (!(ok = wait_for(&b.pv_done, (i - 1) & 1, b, a.err))) break;
+                if (!(ok = wait_for(&b.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
                 fence_after();
             }
             const bool whole = w.lo == 0 && w.hi == w.tiles;
