@@ -15,7 +15,9 @@
 // multiplied and added.  K and V are brought near 1 by a power of two for each tile
 // (exact), so that f16 holds them whatever their scale; it goes into the exponents.
 //
-// Softmax: two threads have a row, 64 of its scores each, and its running maximum and sum.  The sums O stay in
+// Softmax: a thread has a row of a tile, two groups of warps the tiles in turn: what one needs of the other is the
+// running maximum, early.  (One group of twice the width, two threads for a row, took as long for a tile as the
+// products of nearly two: loads, exchanges and stores one after another.)  The sums O stay in
 // tensor memory and are rescaled there when a row's maximum has grown by over 2^8, and not before
 // (see attention_q4.cu).
 //
@@ -23,7 +25,7 @@
 // and V of tile i + 1 and form the weights of tile i + 1 from S, of which there are three (P takes its S's place):
 //   warp 0       copies records (K, V's scales; V's codes) with the bulk-copy engine
 //   warp 1       issues the products: QK(0), QK(1), PV(0), QK(2), PV(1), ...
-//   warps 4-11   softmax, and the outputs: two threads a row, 64 columns each
+//   warps 4-11   softmax (4-7 the even tiles, 8-11 the odd ones), and the outputs
 //   warps 12-15  unpack K, warps 16-19 V
 // Operands lie in core matrices of 8 rows x 16 bytes without a swizzle.  Within every 4 values of the
 // inner dimension the order is 0, 2, 1, 3, that in which a word of packed codes unpacks into two
@@ -69,14 +71,14 @@ struct Lay {
     static constexpr int off_q = 0, off_k = off_q + 2 * q, off_v = off_k + 2 * q;
     static constexpr int off_raw_k = off_v + 2 * v, off_raw_v = off_raw_k + 2 * raw_k;
     static constexpr int off_scale = off_raw_v + raw_v;                   // f16: K [128][NB], V twice
-    static constexpr int off_row = off_scale + 3 * kTile * NB * 2;        // a row's two maxima, or sums
-    static constexpr int off_misc = off_row + 4 * kRows * 4;
+    static constexpr int off_row = off_scale + 3 * kTile * NB * 2;        // the rows' maxima after even and odd tiles, and sums
+    static constexpr int off_misc = off_row + 6 * kRows * 4;
     static constexpr int bytes = off_misc + 512;
 };
 
 struct Bars {
     uint64_t raw_k_full[2], raw_k_empty[2], raw_v_full, raw_v_empty;
-    uint64_t k_ready, v_ready, pv_done[2], s_full[2], p_ready[2], q_ready, k_sync, v_sync, out_sync, pair[4], done;
+    uint64_t k_ready, v_ready, pv_done[2], s_full[2], p_ready[2], m_ready[2], q_ready, k_sync, v_sync, out_sync, pair[4], done;
     uint32_t tmem;
     int gave_up, last;      // a wait ran out; this CTA adds the parts up
     int exps[4][2];         // of tiles i mod 4: K's and V's exponents
@@ -415,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             mbar_init(&b.raw_k_full[i], 1);
             mbar_init(&b.raw_k_empty[i], 8);
             mbar_init(&b.s_full[i], 1);
-            mbar_init(&b.p_ready[i], 8);
+            mbar_init(&b.p_ready[i], 4);
+            mbar_init(&b.m_ready[i], 4);
             mbar_init(&b.pv_done[i], 1);
         }
         mbar_init(&b.raw_v_full, 1);
@@ -708,21 +711,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
     } else {
         // ------------------------------------------------------------ softmax and outputs
         asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
-        const int half = (warp - 4) >> 2, r = (tid - 128) & 127;  // this thread's columns and row of an item
+        const int half = (warp - 4) >> 2, r = (tid - 128) & 127;  // this thread's tiles (and values of the output), its row
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const int q_dim = a.n_heads * hd, q_pad = (q_dim + 255) / 256 * 256;
+        volatile float *maxima = reinterpret_cast<float *>(sm + L::off_row) + r;
         // what the row's other thread gives for v: two places in turn, so that none is written before it is read
         unsigned pair_phase = 0;
         auto exchange = [&](float v, float &got) {
-            float *at = reinterpret_cast<float *>(sm + L::off_row) + (pair_phase & 1u) * 2 * kRows + r;
+            float *at = reinterpret_cast<float *>(sm + L::off_row) + (2 + 2 * (pair_phase & 1u)) * kRows + r;
             at[half * kRows] = v;
             const bool fine = sync_warps(&b.pair[warp & 3], pair_phase, b, a.err);
             got = *reinterpret_cast<const volatile float *>(at + (half ^ 1) * kRows);
             return fine;
         };
-        const int q_dim = a.n_heads * hd, q_pad = (q_dim + 255) / 256 * 256;
         unsigned phase = 0;
         int third = 0;  // i mod 3
-        constexpr int kCols = kTile / 2;
         while (more && ok) {
             if (!has_work(w, line)) {
                 more = next_item(w, a, line, group);
@@ -769,19 +772,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.q_ready);
             }
-            for (int tile = w.lo; tile < w.hi; ++tile, ++i) {
+            for (int tile = w.lo; tile < w.hi; ++tile, ++i, third = third == 2 ? 0 : third + 1) {
+                if ((i & 1) != half) continue;
                 if (!(ok = wait_for(&b.s_full[i & 1], (i >> 1) & 1, b, a.err))) break;
                 fence_after();
                 const float u = unit * power2(-b.exps[i & 3][0]), sub = static_cast<float>(-b.exps[i & 3][1]);
                 // The scores are read twice, 32 at a time in loops that are not unrolled, and not kept: code for
-                // 64 values at once, of 8 warps beside 8 others with code of their own, waits for its instructions.
-                const uint32_t at = tmem + lanes + s_column(third) + half * kCols;
-                third = third == 2 ? 0 : third + 1;
-                const int left = sees - tile * kTile - half * kCols;
+                // all values at once, of 8 warps beside 8 others with code of their own, waits for its instructions.
+                const uint32_t at = tmem + lanes + s_column(third);
+                const int left = sees - tile * kTile;
                 const bool masked = (tile + 1) * kTile > all_see;  // the same for the warp
                 float top = -INFINITY, top2 = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < kCols; c += 32) {
+                for (int c = 0; c < kTile; c += 32) {
                     float s[32];
                     tm_load32(at + c, s);
                     if (masked) {
@@ -796,39 +799,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     }
                 }
                 top = fmaf(fmaxf(top, top2), u, sub);  // log2 of the largest weight of V as it is unpacked
-                if (!(ok = exchange(top, top2))) break;
-                top = fmaxf(top, top2);
+                // the running maximum of the tile before, this one's for the next
+                float before_m = -1e37f;
+                if (tile > w.lo) {
+                    if (!(ok = wait_for(&b.m_ready[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
+                    before_m = maxima[((i - 1) & 1) * kRows];
+                }
+                const bool grown = top > before_m + kLazy;
+                const float m_new = grown ? top : before_m;
+                maxima[(i & 1) * kRows] = m_new;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.m_ready[i & 1]);
+                l *= ex2f(m - m_new);
+                m = m_new;
+                if (tile > w.lo && __any_sync(0xffffffffu, grown)) {
+                    // O is at rest once the tile before is done
+                    if (!(ok = wait_for(&b.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
+                    fence_after();
+                    const float f = ex2f(before_m - m);
+#pragma unroll 1
+                    for (int c = 0; c < hd; c += 16) {
+                        uint32_t o[16];
+                        tm_load16(tmem + lanes + kColO + c, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tm_store16(tmem + lanes + kColO + c, o);
+                    }
+                }
                 // a NaN or infinite V scale that this row sees makes its sum NaN
                 float add = 0.0f;
-                if (b.nan_v[i & 3][2 * half] | b.nan_v[i & 3][2 * half + 1]) {
-                    for (int c = 0; c < kCols; ++c)
-                        if ((b.nan_v[i & 3][2 * half + (c >> 5)] >> (c & 31) & 1) && swapped(c) < left) add = __int_as_float(0x7fffffff);
-                }
-                const bool grown = top > m + kLazy;
-                if (__any_sync(0xffffffffu, grown)) {
-                    // O is at rest once the tile before is done
-                    if (tile > w.lo) {
-                        if (!(ok = wait_for(&b.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
-                        fence_after();
-                    }
-                    const float mn = grown ? top : m, f = ex2f(m - mn);
-                    m = mn;
-                    l *= f;
-                    if (tile > w.lo) {
+                if (b.nan_v[i & 3][0] | b.nan_v[i & 3][1] | b.nan_v[i & 3][2] | b.nan_v[i & 3][3]) {
 #pragma unroll 1
-                        for (int c = half * (hd / 2); c < (half + 1) * (hd / 2); c += 16) {
-                            uint32_t o[16];
-                            tm_load16(tmem + lanes + kColO + c, o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tm_store16(tmem + lanes + kColO + c, o);
-                        }
-                    }
+                    for (int c = 0; c < kTile; ++c)
+                        if ((b.nan_v[i & 3][c >> 5] >> (c & 31) & 1) && swapped(c) < left) add = __int_as_float(0x7fffffff);
                 }
                 const float off = sub + (kBias - m);
                 float sum = 0.0f, sum2 = 0.0f;
 #pragma unroll 1
-                for (int c = 0; c < kCols; c += 32) {
+                for (int c = 0; c < kTile; c += 32) {
                     float s[32];
                     tm_load32(at + c, s);
                     if (masked) {
@@ -856,10 +864,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 if (lane == 0) mbar_arrive(&b.p_ready[i & 1]);
             }
             if (!ok) break;
-            // ---- the row's sum is that of its two threads; each writes half of its values
+            // ---- the row's sum is that of its two threads, at the last tile's maximum; each writes half of its values
+            if (w.lo < w.hi) {
+                if (!(ok = wait_for(&b.m_ready[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
+                const float last_m = maxima[((i - 1) & 1) * kRows];
+                l *= ex2f(m - last_m);
+                m = last_m;
+            }
             float l2;
             if (!(ok = exchange(l, l2))) break;
-            l += l2;
+            l = half ? l2 + l : l + l2;
             if (w.lo < w.hi) {
                 if (!(ok = wait_for(&b.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
                 fence_after();
