@@ -21,10 +21,10 @@
 // tensor memory and are rescaled there when a row's maximum has grown by over 2^8, and not before
 // (see attention_q4.cu).
 //
-// The tensor pipe is never to wait: while it works P V of tile i, warps unpack K of tile i + 2
-// and V of tile i + 1 and form the weights of tile i + 1 from S, of which there are three (P takes its S's place):
+// The tensor pipe is never to wait: while it works P V of tile i, warps unpack K of tile i + 3
+// and V of tile i + 1 and form the weights of tiles i + 1 and i + 2 from S, of which there are three (P takes its S's place):
 //   warp 0       copies records (K, V's scales; V's codes) with the bulk-copy engine
-//   warp 1       issues the products: QK(0), QK(1), PV(0), QK(2), PV(1), ...
+//   warp 1       issues the products as their operands come, QK up to two tiles ahead of PV
 //   warps 4-11   softmax (4-7 the even tiles, 8-11 the odd ones), and the outputs
 //   warps 12-15  unpack K, warps 16-19 V
 // Operands lie in core matrices of 8 rows x 16 bytes without a swizzle.  Within every 4 values of the
@@ -70,15 +70,15 @@ struct Lay {
     static constexpr int raw_v = kGroups * 8 * hd;  // V codes
     static constexpr int off_q = 0, off_k = off_q + 2 * q, off_v = off_k + 2 * q;
     static constexpr int off_raw_k = off_v + 2 * v, off_raw_v = off_raw_k + 2 * raw_k;
-    static constexpr int off_scale = off_raw_v + raw_v;                   // f16: K [128][NB], V twice
-    static constexpr int off_row = off_scale + 3 * kTile * NB * 2;        // the rows' maxima after even and odd tiles, and sums
-    static constexpr int off_misc = off_row + 6 * kRows * 4;
+    static constexpr int off_scale = off_raw_v + raw_v;                   // f16: K [128][NB], V of 3 tiles
+    static constexpr int off_row = off_scale + 4 * kTile * NB * 2;        // the rows' maxima after even and odd tiles, and sums
+    static constexpr int off_misc = off_row + 4 * kRows * 4;
     static constexpr int bytes = off_misc + 512;
 };
 
 struct Bars {
     uint64_t raw_k_full[2], raw_k_empty[2], raw_v_full, raw_v_empty;
-    uint64_t k_ready, v_ready, pv_done[2], s_full[2], p_ready[2], m_ready[2], q_ready, k_sync, v_sync, out_sync, pair[4], done;
+    uint64_t k_ready, scales_ready[3], v_ready, pv_done[2], s_full[3], p_ready[3], m_ready[2], q_ready, k_sync, out_sync, pair[4], done;
     uint32_t tmem;
     int gave_up, last;      // a wait ran out; this CTA adds the parts up
     int exps[4][2];         // of tiles i mod 4: K's and V's exponents
@@ -280,6 +280,20 @@ __device__ __forceinline__ bool next_item(Item &w, const PagedAttnArgs &a, const
     return true;
 }
 
+// Whether a phase is complete, at once (try_wait would sleep on one that is not).
+__device__ __forceinline__ bool test_phase(uint64_t *bar, unsigned par)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(par)
+        : "memory");
+    return ok != 0;
+}
+
 // Warp-wide bounded wait; false after a timeout or when another role gave up.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, unsigned par, Bars &b, unsigned *err)
 {
@@ -415,19 +429,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.raw_k_full[i], 1);
-            mbar_init(&b.raw_k_empty[i], 8);
-            mbar_init(&b.s_full[i], 1);
-            mbar_init(&b.p_ready[i], 4);
+            mbar_init(&b.raw_k_empty[i], 4);
             mbar_init(&b.m_ready[i], 4);
             mbar_init(&b.pv_done[i], 1);
         }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&b.s_full[i], 1);
+            mbar_init(&b.p_ready[i], 4);
+            mbar_init(&b.scales_ready[i], 4);
+        }
         mbar_init(&b.raw_v_full, 1);
         mbar_init(&b.raw_v_empty, 4);
-        mbar_init(&b.k_ready, 8);  // K's warps, and V's with the exponents of its scales
+        mbar_init(&b.k_ready, 4);
         mbar_init(&b.v_ready, 4);
         mbar_init(&b.q_ready, 8);
         mbar_init(&b.k_sync, 4);
-        mbar_init(&b.v_sync, 4);
         mbar_init(&b.out_sync, 8);
         for (int i = 0; i < 4; ++i) mbar_init(&b.pair[i], 2);
         mbar_init(&b.done, 1);
@@ -507,34 +523,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         constexpr uint32_t stride_q = hd * 16, stride_v = kTile * 16;  // 8 rows
         const uint64_t q0 = operand_desc(smem_u32(sm + L::off_q), stride_q), k0 = operand_desc(smem_u32(sm + L::off_k), stride_q),
                        v0 = operand_desc(smem_u32(sm + L::off_v), stride_v);
-        int item = 0, third = 0;  // i mod 3
-        // QK(j): A = Q, B = K; high * high, low * high, high * low.  S's place holds P(j - 3): of the
-        // item (reused), PV(j - 3) has to be done; of the one before, it is, since Q is there.  (Within an
-        // item PV(j - 1) is not issued yet, so that the phase waited for cannot have been overtaken.)  One
-        // commit a product: a wait or a commit costs this warp some hundred cycles.
-        auto qk = [&](int j, int third, bool reused) {
-            const uint32_t d = tmem + s_column(third);
-            if (reused && !wait_for(&b.pv_done[(j - 3) & 1], ((j - 3) >> 1) & 1, b, a.err)) return false;
-            if (!wait_for(&b.k_ready, j & 1, b, a.err)) return false;
-            fence_after();
+        int item = 0;
+        // QK(j): A = Q, B = K; high * high, low * high, high * low.  One commit a product: a wait or a
+        // commit costs this warp some hundred cycles.
+        auto qk = [&](int j, int third) {
             if (lane == 0) {
+                const uint32_t d = tmem + s_column(third);
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
 #pragma unroll
                     for (int k = 0; k < hd / 16; ++k)
                         mma_ss(d, q0 + (p == 1 ? L::q / 16 : 0) + 16 * k, k0 + (p == 2 ? L::q / 16 : 0) + 16 * k,
                                idesc_f16(kTile), p || k);
-                commit(&b.s_full[j & 1]);
+                commit(&b.s_full[third]);
             }
             __syncwarp();
-            return true;
         };
         // PV(j): A = P, B = V
         auto pv = [&](int j, int third, bool start) {
-            const uint32_t d = tmem + kColO, p0 = tmem + s_column(third);
-            if (!wait_for(&b.v_ready, j & 1, b, a.err) || !wait_for(&b.p_ready[j & 1], (j >> 1) & 1, b, a.err)) return false;
-            fence_after();
             if (lane == 0) {
+                const uint32_t d = tmem + kColO, p0 = tmem + s_column(third);
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
 #pragma unroll
@@ -544,18 +552,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 commit(&b.pv_done[j & 1]);
             }
             __syncwarp();
-            return true;
         };
+        // Products in the order in which their operands are there: QK up to two tiles ahead of PV.
+        //   QK(j): K(j) unpacked, and P(j - 3), in whose place S(j) goes, used up: PV(j - 3) done
+        //   PV(j): P(j) and V(j) there, and PV(j - 2) known to be done (of each parity one is on its way)
+        int j_qk = 0, j_pv = 0, done = 0;      // the next ones, and how many PV are done
+        int third_qk = 0, third_pv = 0;        // j mod 3
+        auto test = [&](uint64_t *bar, unsigned par) { return __all_sync(0xffffffffu, test_phase(bar, par)) != 0; };
+        volatile int *gave_up = &b.gave_up;
         while (more && ok) {
             if (w.lo < w.hi) {
                 ok = wait_for(&b.q_ready, item & 1, b, a.err);
                 ++item;
-                for (int t = w.lo; t < w.hi && ok; ++t, ++i) {
-                    ok = qk(i, third, t - w.lo >= 3);
-                    if (ok && t > w.lo) ok = pv(i - 1, third ? third - 1 : 2, t - 1 == w.lo);
-                    third = third == 2 ? 0 : third + 1;
+                const int first_j = j_pv, last_j = j_pv + (w.hi - w.lo);
+                uint32_t idle = 0;
+                while (ok && j_pv < last_j) {
+                    bool moved = false;
+                    if (done < j_pv && test(&b.pv_done[done & 1], (done >> 1) & 1)) {
+                        ++done;
+                        moved = true;
+                    }
+                    if (j_pv < j_qk && done >= j_pv - 1 && test(&b.p_ready[third_pv], (j_pv / 3) & 1) && test(&b.v_ready, j_pv & 1)) {
+                        fence_after();
+                        pv(j_pv, third_pv, j_pv == first_j);
+                        ++j_pv;
+                        third_pv = third_pv == 2 ? 0 : third_pv + 1;
+                        moved = true;
+                    }
+                    if (j_qk < last_j && j_qk <= j_pv + 2 && done >= j_qk - 2 && test(&b.k_ready, j_qk & 1)) {
+                        fence_after();
+                        qk(j_qk, third_qk);
+                        ++j_qk;
+                        third_qk = third_qk == 2 ? 0 : third_qk + 1;
+                        moved = true;
+                    }
+                    idle = moved ? 0 : idle + 1;
+                    if (idle >= kWaitLimit * 4 || ((idle & 63u) == 63u && __any_sync(0xffffffffu, *gave_up))) {
+                        if (!*gave_up) set_error(a.err, DEV_TIMEOUT_PAGED);
+                        *gave_up = 1;
+                        ok = false;
+                    }
                 }
-                if (ok) ok = pv(i - 1, third ? third - 1 : 2, w.hi - 1 == w.lo);
             }
             if (ok) more = next_item(w, a, line, group);
         }
@@ -579,47 +616,56 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             *reinterpret_cast<uint2 *>(p) = make_uint2(h0, h1);
             *reinterpret_cast<uint2 *>(p + piece) = make_uint2(hfms2u(c0, d0, h0), hfms2u(c1, d1, h1));
         };
-        // The scales of tile j's K or V, a token a thread, times 2^up: the tile's largest to
-        // 2^8 .. 2^9 (a tile of zeros: as it is).
+        // The scales of tile j, a token a thread, times 2^up: the tile's largest of K and of V to
+        // 2^8 .. 2^9 (none but zeros: as they are).  V's last for 3 tiles: K(j) is copied after V(j - 2), which
+        // is once V(j - 3) is unpacked.
         auto scales = [&](int j, int valid) {
             if (!wait_for(&b.raw_k_full[j & 1], (j >> 1) & 1, b, a.err)) return false;
-            const uint8_t *raw = sm + L::off_raw_k + (j & 1) * L::raw_k + (tok128 >> 4) * 10 * hd + (for_v ? 9 * hd : 8 * hd);
-            const uint16_t *src = reinterpret_cast<const uint16_t *>(raw) + (tok128 & 15) * NB;
-            uint16_t d[NB];
-            uint32_t most = 0;
+            const uint8_t *raw = sm + L::off_raw_k + (j & 1) * L::raw_k + (tok128 >> 4) * 10 * hd + 8 * hd;
+            uint16_t d[2][NB];
+            uint32_t most[2] = {0, 0};
             bool bad = false;
 #pragma unroll
-            for (int e = 0; e < NB; ++e) {
-                d[e] = tok128 < valid ? src[e] : uint16_t(0);
-                const uint32_t abs = d[e] & 0x7fffu;
-                if (abs < 0x7c00u) most = max(most, abs);
-                else bad = true;
+            for (int v = 0; v < 2; ++v) {
+                const uint16_t *src = reinterpret_cast<const uint16_t *>(raw + v * hd) + (tok128 & 15) * NB;
+#pragma unroll
+                for (int e = 0; e < NB; ++e) {
+                    d[v][e] = tok128 < valid ? src[e] : uint16_t(0);
+                    const uint32_t abs = d[v][e] & 0x7fffu;
+                    if (abs < 0x7c00u) most[v] = max(most[v], abs);
+                    else if (v) bad = true;
+                }
+                most[v] = __reduce_max_sync(0xffffffffu, most[v]);
             }
-            most = __reduce_max_sync(0xffffffffu, most);
             const unsigned bads = __ballot_sync(0xffffffffu, bad);
             if (lane == 0) {
-                b.warp_max[for_v][w4] = most;
+                b.warp_max[0][w4] = most[0];
+                b.warp_max[1][w4] = most[1];
                 // by position: bits 1 and 2 of every 4 change places
-                if (for_v) b.nan_v[j & 3][w4] = (bads & 0x99999999u) | ((bads & 0x22222222u) << 1) | ((bads & 0x44444444u) >> 1);
+                b.nan_v[j & 3][w4] = (bads & 0x99999999u) | ((bads & 0x22222222u) << 1) | ((bads & 0x44444444u) >> 1);
             }
-            uint64_t *sync = for_v ? &b.v_sync : &b.k_sync;
-            if (!sync_warps(sync, phase, b, a.err)) return false;
-            most = max(max(b.warp_max[for_v][0], b.warp_max[for_v][1]), max(b.warp_max[for_v][2], b.warp_max[for_v][3]));
-            const int up = most ? kScaleTop + 127 - (__float_as_int(h2f((uint16_t)most)) >> 23) : 0;
-            if (tok128 == 0) b.exps[j & 3][for_v] = up;
-            uint16_t *dst = for_v ? sv + (j & 1) * kTile * NB : sk;
+            if (!sync_warps(&b.k_sync, phase, b, a.err)) return false;
 #pragma unroll
-            for (int e = 0; e < NB; ++e) {
-                // a V scale that is no number: nothing is added, and the row's sum is made NaN
-                const bool drop = for_v && (d[e] & 0x7fffu) >= 0x7c00u;
-                dst[tok128 * NB + e] = drop ? uint16_t(0) : __half_as_ushort(__float2half_rn(h2f(d[e]) * power2(up)));
+            for (int v = 0; v < 2; ++v) {
+                const uint32_t top = max(max(b.warp_max[v][0], b.warp_max[v][1]), max(b.warp_max[v][2], b.warp_max[v][3]));
+                const int up = top ? kScaleTop + 127 - (__float_as_int(h2f((uint16_t)top)) >> 23) : 0;
+                if (tok128 == 0) b.exps[j & 3][v] = up;
+                uint16_t *dst = (v ? sv + (j % 3) * kTile * NB : sk) + tok128 * NB;
+#pragma unroll
+                for (int e = 0; e < NB; ++e) {
+                    // a V scale that is no number: nothing is added, and the row's sum is made NaN
+                    const bool drop = v && (d[v][e] & 0x7fffu) >= 0x7c00u;
+                    dst[e] = drop ? uint16_t(0) : __half_as_ushort(__float2half_rn(h2f(d[v][e]) * power2(up)));
+                }
             }
-            return sync_warps(sync, phase, b, a.err);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.scales_ready[j % 3]);
+            return sync_warps(&b.k_sync, phase, b, a.err);
         };
         auto unpack_k = [&](int j) {
             const uint8_t *raw = sm + L::off_raw_k + (j & 1) * L::raw_k;
             // the operand is free once QK(j - 1) is done
-            if (j > 0 && !wait_for(&b.s_full[(j - 1) & 1], ((j - 1) >> 1) & 1, b, a.err)) return false;
+            if (j > 0 && !wait_for(&b.s_full[(j - 1) % 3], ((j - 1) / 3) & 1, b, a.err)) return false;
             // groups 2 w4, 2 w4 + 1; lane (g, t): word t of each block of rows 8 hf + g
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
@@ -647,14 +693,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             return true;
         };
         auto unpack_v = [&](int j) {
-            if (!wait_for(&b.raw_v_full, j & 1, b, a.err)) return false;
+            if (!wait_for(&b.raw_v_full, j & 1, b, a.err) || !wait_for(&b.scales_ready[j % 3], (j / 3) & 1, b, a.err)) return false;
             // the operand is free once PV(j - 1) is done
             if (j > 0 && !wait_for(&b.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, b, a.err)) return false;
 #pragma unroll 1
             for (int gr = 2 * w4; gr < 2 * w4 + 2; ++gr) {
                 // scales of tokens 4 t .. 4 t + 3: half i * NB + e
                 uint32_t d[2 * NB];
-                const uint4 *dp = reinterpret_cast<const uint4 *>(sv + (j & 1) * kTile * NB + (gr * 16 + 4 * t) * NB);
+                const uint4 *dp = reinterpret_cast<const uint4 *>(sv + (j % 3) * kTile * NB + (gr * 16 + 4 * t) * NB);
 #pragma unroll
                 for (int k = 0; k < NB / 2; ++k) {
                     const uint4 v = dp[k];
@@ -689,25 +735,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         };
         while (more && ok) {
             for (int tile = w.lo; tile < w.hi && ok; ++tile, ++i) {
-                ok = scales(i, w.tokens - tile * kTile);
-                if (!ok) break;
                 if (for_v) {
-                    // (not before the tile before is counted)
-                    if (i > 0 && !(ok = wait_for(&b.k_ready, (i - 1) & 1, b, a.err))) break;
-                } else if (!(ok = unpack_k(i))) {
-                    break;
+                    ok = unpack_v(i);
+                    continue;
                 }
+                if (!(ok = scales(i, w.tokens - tile * kTile)) || !(ok = unpack_k(i))) break;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&b.k_ready);
                     mbar_arrive(&b.raw_k_empty[i & 1]);
                 }
-                if (for_v && i > 0) ok = unpack_v(i - 1);
             }
             if (ok) more = next_item(w, a, line, group);
         }
-        if (ok && for_v && i > 0) unpack_v(i - 1);
     } else {
         // ------------------------------------------------------------ softmax and outputs
         asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
@@ -715,14 +756,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int q_dim = a.n_heads * hd, q_pad = (q_dim + 255) / 256 * 256;
         volatile float *maxima = reinterpret_cast<float *>(sm + L::off_row) + r;
-        // what the row's other thread gives for v: two places in turn, so that none is written before it is read
+        // what the row's other thread gives for v
         unsigned pair_phase = 0;
         auto exchange = [&](float v, float &got) {
-            float *at = reinterpret_cast<float *>(sm + L::off_row) + (2 + 2 * (pair_phase & 1u)) * kRows + r;
+            volatile float *at = maxima + 2 * kRows;
             at[half * kRows] = v;
-            const bool fine = sync_warps(&b.pair[warp & 3], pair_phase, b, a.err);
-            got = *reinterpret_cast<const volatile float *>(at + (half ^ 1) * kRows);
-            return fine;
+            bool fine = sync_warps(&b.pair[warp & 3], pair_phase, b, a.err);
+            got = at[(half ^ 1) * kRows];
+            return sync_warps(&b.pair[warp & 3], pair_phase, b, a.err) && fine;  // read, before it is written again
         };
         unsigned phase = 0;
         int third = 0;  // i mod 3
@@ -774,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             }
             for (int tile = w.lo; tile < w.hi; ++tile, ++i, third = third == 2 ? 0 : third + 1) {
                 if ((i & 1) != half) continue;
-                if (!(ok = wait_for(&b.s_full[i & 1], (i >> 1) & 1, b, a.err))) break;
+                if (!(ok = wait_for(&b.s_full[third], (i / 3) & 1, b, a.err))) break;
                 fence_after();
                 const float u = unit * power2(-b.exps[i & 3][0]), sub = static_cast<float>(-b.exps[i & 3][1]);
                 // The scores are read twice, 32 at a time in loops that are not unrolled, and not kept: code for
@@ -861,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 tm_store_wait();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.p_ready[i & 1]);
+                if (lane == 0) mbar_arrive(&b.p_ready[third]);
             }
             if (!ok) break;
             // ---- the row's sum is that of its two threads, at the last tile's maximum; each writes half of its values
