@@ -278,7 +278,11 @@ __device__ __forceinline__ bool walk_has(const Walk &w)
 // NT tiles of 4 queries; this lane (g, t) sums for query 4 j + t of tile j.
 template <int NB, int NT>
 struct Warp {
-    uint32_t q[NT][NB][2][2];  // B fragments: tile, block, low and high half
+    // B fragments of the queries, {low half, high half} of a block: in registers for one tile; for two, beside
+    // twice the sums, in shared memory (32 lanes' uint4 for each tile and block)
+    uint4 q[NT == 1 ? NB : 1];
+    const uint4 *q_shared;
+    __device__ __forceinline__ uint4 query(int j, int b) const { return NT == 1 ? q[b] : q_shared[(j * NB + b) * 32]; }
     float unit[NT];            // log2(e) * scale * the unit of the products
     float o[NT][NB][2][4];     // sums of V: tile, block, half, {c0..c3}
     float m[NT], l[NT];        // running maximum (see the top), sum of p
@@ -313,7 +317,8 @@ __device__ __forceinline__ void flush(Warp<NB, NT> &w, int g)
 // The queries in fragment order: this lane holds, for tile j, values 4 t .. 4 t + 3 (of both
 // halves of each block) of query 4 j + g / 2 at ptr[j], its high piece (g even) or its low one.
 template <int NB, int NT>
-__device__ __forceinline__ void load_query(Warp<NB, NT> &w, const float *const (&ptr)[NT], float scale, int g, int t)
+__device__ __forceinline__ void load_query(Warp<NB, NT> &w, uint4 *q_shared, const float *const (&ptr)[NT], float scale, int g,
+                                           int t)
 {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -334,7 +339,8 @@ __device__ __forceinline__ void load_query(Warp<NB, NT> &w, const float *const (
         const int up = mx == 0.0f ? 0 : min(14 - ex, 126);
         const float sc = __int_as_float((up + 127) << 23);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b) {
+            uint32_t piece[2][2];
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const float x[4] = {v[b][hf].x * sc, v[b][hf].z * sc, v[b][hf].y * sc, v[b][hf].w * sc};
@@ -342,16 +348,21 @@ __device__ __forceinline__ void load_query(Warp<NB, NT> &w, const float *const (
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t hi = pack_f16(x[2 * k], x[2 * k + 1]);
                     const float2 h = unpack_f16(hi);
-                    w.q[j][b][hf][k] = (g & 1) ? pack_f16(x[2 * k] - h.x, x[2 * k + 1] - h.y) : hi;
+                    piece[hf][k] = (g & 1) ? pack_f16(x[2 * k] - h.x, x[2 * k + 1] - h.y) : hi;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w.o[j][b][hf][k] = 0.0f;
             }
+            const uint4 v = make_uint4(piece[0][0], piece[0][1], piece[1][0], piece[1][1]);
+            if (NT == 1) w.q[b] = v;
+            else q_shared[(j * NB + b) * 32] = v;
+        }
         // the unit of query t is with lane g = 2 t
         w.unit[j] = scale * 1.4426950408889634f * __int_as_float((127 - __shfl_sync(0xffffffffu, up, 8 * t)) << 23);
         w.m[j] = -1e37f;
         w.l[j] = 0.0f;
     }
+    w.q_shared = q_shared;
     w.since = 0;
     w.flushed = false;
 }
@@ -423,8 +434,9 @@ __device__ __forceinline__ void attend(Warp<NB, NT> &w, const uint8_t *rec, int 
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma16816(c, lo, w.q[j][b][0][0], w.q[j][b][0][1], c);
-                mma16816(c, hi, w.q[j][b][1][0], w.q[j][b][1][1], c);
+                const uint4 q = w.query(j, b);
+                mma16816(c, lo, q.x, q.y, c);
+                mma16816(c, hi, q.z, q.w, c);
                 s[j][2 * u] = fmaf(d0, c[0] + c[1], s[j][2 * u]);
                 s[j][2 * u + 1] = fmaf(d1, c[2] + c[3], s[j][2 * u + 1]);
             }
@@ -548,7 +560,7 @@ __device__ __forceinline__ void attend(Warp<NB, NT> &w, const uint8_t *rec, int 
 }
 
 // ---------------------------------------------------------------- shared memory
-// slots of 2 records | the warps' sums, their (m, l) | mbarriers, flags, counts (512 bytes) |
+// slots of 2 records | query fragments | the warps' sums, their (m, l) | mbarriers, flags, counts (512 bytes) |
 // the parts of an item | the line's prefix | the requests
 constexpr int kMaxSlots = 24;
 constexpr int kMaxCtas = 512;  // of the grid
@@ -557,7 +569,8 @@ struct Layout {
     static constexpr int W = consumers(NB), hd = 32 * NB, rows = 8 * W;
     static constexpr int slot = 2 * q4_record_bytes(hd);
     static constexpr int sums = rows * (hd + kPad) * 4;
-    static constexpr int fixed = sums + rows * 8 + 512 + kMaxCtas * 2;  // and 20 bytes for each request and 8
+    static constexpr int queries = W * 2 * NB * 512;  // fragments of two tiles of queries for each warp
+    static constexpr int fixed = queries + sums + rows * 8 + 512 + kMaxCtas * 2;  // and 20 bytes for each request and 8
     static constexpr int64_t part = (int64_t)rows * (hd + 2);  // floats of a partial record: sums, then (m, l)
 };
 
@@ -610,7 +623,7 @@ __device__ __forceinline__ void ring_step(RingPos &r, int n, int slots)
 // A consumer warp's share of the current part of an item: its sums to shared memory.
 template <int NB, int NT, int NG>
 __device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, const uint8_t *ring, int slots, uint64_t *full,
-                                     uint64_t *empty, volatile int *gave_up, RingPos &pos, float *sums, float2 *ml, int warp,
+                                     uint64_t *empty, volatile int *gave_up, RingPos &pos, float *sums, float2 *ml, uint4 *queries, int warp,
                                      int lane)
 {
     using L = Layout<NB>;
@@ -639,7 +652,7 @@ __device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, cons
     const int arrive = qg == 0 ? W + 1 - min(rg, (n_rows - w.it * rg * 8 + 7) >> 3) : 1;
     Warp<NB, NT> acc;
     acc.row = sums + slot * (hd + kPad);
-    load_query<NB, NT>(acc, ptr, a.scale, g, t);
+    load_query<NB, NT>(acc, queries + warp * 2 * NB * 32 + lane, ptr, a.scale, g, t);
     RingPos mine = pos;
     ring_step(mine, ks, slots);
     for (int u = idle || __any_sync(0xffffffffu, *gave_up) ? w.hi : w.lo + ks; u < w.hi; u += copies) {
@@ -688,7 +701,8 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
     constexpr int W = L::W, hd = L::hd, ld = hd + kPad, kSlot = L::slot;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem;
-    float *sums = reinterpret_cast<float *>(ring + (size_t)slots * kSlot);
+    uint4 *queries = reinterpret_cast<uint4 *>(ring + (size_t)slots * kSlot);
+    float *sums = reinterpret_cast<float *>(queries + L::queries / 16);
     float2 *ml = reinterpret_cast<float2 *>(sums + L::sums / 4);
     uint64_t *full = reinterpret_cast<uint64_t *>(ml + L::rows), *empty = full + kMaxSlots;
     int *flags = reinterpret_cast<int *>(empty + kMaxSlots);  // [0] a wait ran out, [1] this CTA adds the parts up
@@ -824,9 +838,9 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
             const int rg = w.q.rg, copies = W / rg, row_it = w.it * 8 * rg;
             const int n_rows = w.q.m * group;  // of the request and kv head
             if (n_rows <= 4)
-                work<NB, 1, 2>(a, w, ring, slots, full, empty, gave_up, pos, sums, ml, warp, lane);
+                work<NB, 1, 2>(a, w, ring, slots, full, empty, gave_up, pos, sums, ml, queries, warp, lane);
             else
-                work<NB, 2, 1>(a, w, ring, slots, full, empty, gave_up, pos, sums, ml, warp, lane);
+                work<NB, 2, 1>(a, w, ring, slots, full, empty, gave_up, pos, sums, ml, queries, warp, lane);
             consumer_sync<W>();
             const int rows_item = min(8 * rg, n_rows - row_it);
             const bool whole = w.lo == 0 && w.hi == w.units;

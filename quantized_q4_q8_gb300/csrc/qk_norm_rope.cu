@@ -9,11 +9,13 @@
 //   infinity gets d = NaN, so that what reads it sees it.
 //
 // A warp works one head of one token; lane l holds value 32 e + l of it in register
-// e, so that a Q4_0 block is one register across the warp.  A CTA works the heads of
-// one token (several CTAs share a token's heads when there are few tokens) and forms
+// e, which keeps most pairs of the rotation in a lane.  A CTA of 4 warps works the heads of one
+// token (several CTAs share a token's heads when there are few tokens) and forms
 // the token's cosines and sines once: the angle as a fraction of a turn is
 // position * F_i mod 2^64 with F_i = 2^64 theta^(-2i/head_dim) / (2 pi), a product of
-// integers, which drops whole turns exactly at any position.
+// integers, which drops whole turns exactly at any position.  Blocks are quantised four at a
+// time, 8 lanes with 4 values each to a block: keys go through shared memory into that
+// order, values are loaded in it.
 //
 // The cache holds the codes that the definition gives in 64 bits, whatever the order of
 // the sums: a key that rounds to the other side of a border in f32 would be off by a
@@ -36,7 +38,7 @@
 namespace rz {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr double kInvTwoPi = 0.15915494309189533576888376337251;
 
@@ -121,13 +123,6 @@ __device__ __forceinline__ float redux_max(float v)
     asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
-__device__ __forceinline__ float redux_min(float v)
-{
-    float r;
-    asm volatile("redux.sync.min.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 // Rotation of a head held as x[e] = value 32 e + lane: z[e] = x[e] cos + o[e] sin', o the
 // other value of the pair and sin' its sine, negative in the pair's first value.
 //   kMode 0: pairs (2i, 2i + 1), the neighbouring lane
@@ -225,52 +220,123 @@ __device__ __forceinline__ Two inverse_rms(Two ss, int n, float eps)
     return Two{y, a.h < INFINITY ? y * e * fmaf(0.375f, e, 0.5f) : 0.0f};
 }
 
-struct Block {
-    uint16_t d;   // f16 bits of the scale
-    int code;     // this lane's code
-    float value;  // and what it stands for
+// Codes and scale of a block of 32 values held by 8 lanes, 4 values z[k] + l[k] each (values
+// 4 (lane & 7) ..): this lane's codes in 4 bytes, the values they stand for, the f16 bits of d.
+struct Block4 {
+    uint32_t codes;
+    float4 value;
+    uint16_t d;
 };
 
-// The block of 32 values z, one in each lane.
-__device__ __forceinline__ Block quantise(Two z)
+__device__ __forceinline__ float max8(float v)
 {
-    const float mx = redux_max(z.h), mn = redux_min(z.h);
-    if (!(mx < INFINITY && mn > -INFINITY)) return Block{0x7e00, 8, __int_as_float(0x7fffffff)};
-    float s = mx >= -mn ? mx : mn;
-    if (mx == -mn) {  // the low parts tell which is larger
-        const float top = redux_max(z.h == mx ? z.l : -INFINITY), low = redux_min(z.h == mn ? z.l : INFINITY);
-        if (top < -low) s = mn;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+template <bool kTwo>
+__device__ __forceinline__ Block4 quantise(const float (&z)[4], const float (&l)[4])
+{
+    float mx = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), mn = fminf(fminf(z[0], z[1]), fminf(z[2], z[3]));
+    // fmaxf passes over a NaN: a sum of zeros times the values does not
+    const float odd = (z[0] * 0.0f + z[1] * 0.0f) + (z[2] * 0.0f + z[3] * 0.0f);
+    mx = max8(mx);
+    mn = -max8(-mn);
+    const unsigned bad = __ballot_sync(0xffffffffu, odd != 0.0f || odd != odd);
+    Block4 o;
+    if (bad >> (threadIdx.x & 24) & 0xffu) {  // a NaN or an infinity in these 8 lanes' block
+        const float nan = __int_as_float(0x7fffffff);
+        mx = mn = 0.0f;
+        o = Block4{0x08080808u, make_float4(nan, nan, nan, nan), 0x7e00};
     }
-    Block o;
+    float s = mx >= -mn ? mx : mn;
+    if (kTwo) {  // of two peaks of one size in the high parts, the low ones tell which is larger
+        const unsigned tie = __ballot_sync(0xffffffffu, mx == -mn && mx != 0.0f);
+        if (tie) {
+            float top = -INFINITY, low = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (z[k] == mx) top = fmaxf(top, l[k]);
+                if (z[k] == mn) low = fmaxf(low, -l[k]);
+            }
+            top = max8(top);
+            low = max8(low);
+            if (mx == -mn && top < low) s = mn;
+        }
+    }
+    if (bad >> (threadIdx.x & 24) & 0xffu) return o;
     o.d = __half_as_ushort(__float2half_rn(fminf(fmaxf(s * -0.125f, -65504.0f), 65504.0f)));
-    if ((o.d & 0x7fffu) == 0) return Block{0, 8, 0.0f};
-    const float d = h2f(o.d), ad = fabsf(d), az = fabsf(z.h), al = z.h < 0.0f ? -z.l : z.l;
-    const float k = floorf(fminf(az * rcp_approx(ad), 64.0f));
-    const float t = __fmaf_rn(-(k + 0.5f), ad, az);
-    // beyond the border, or on it: then the low part tells, and of a tie the even code is taken
-    const bool up = t > 0.0f || (t == 0.0f && (al > 0.0f || (al == 0.0f && (static_cast<int>(k) & 1))));
-    const int m = static_cast<int>(up ? k + 1.0f : k);
-    o.code = min(max((z.h < 0.0f) != (d < 0.0f) ? 8 - m : 8 + m, 0), 15);
-    o.value = static_cast<float>(o.code - 8) * d;
+    if ((o.d & 0x7fffu) == 0) return Block4{0x08080808u, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0};
+    const float d = h2f(o.d), ad = fabsf(d), rd = rcp_approx(ad);
+    float v[4];
+    o.codes = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float az = fabsf(z[k]);
+        const float n = floorf(fminf(az * rd, 64.0f));
+        const float t = __fmaf_rn(-(n + 0.5f), ad, az);
+        int m = static_cast<int>(n);
+        // beyond the border, or on it: then the low part tells, and of a tie the even code is taken
+        bool up = t > 0.0f;
+        if (t == 0.0f) {
+            const float al = kTwo ? (z[k] < 0.0f ? -l[k] : l[k]) : 0.0f;
+            up = al > 0.0f || (al == 0.0f && (m & 1));
+        }
+        m += up;
+        const int c = min(max((z[k] < 0.0f) != (d < 0.0f) ? 8 - m : 8 + m, 0), 15);
+        o.codes |= static_cast<uint32_t>(c) << (8 * k);
+        v[k] = static_cast<float>(c - 8) * d;
+    }
+    o.value = make_float4(v[0], v[1], v[2], v[3]);
     return o;
 }
 
-// One block of a token's key or value: values to `out` (or nowhere), bytes into the record.
+// A block's bytes into its token's record.  Every lane calls it; live: this lane has a block.
 template <int NB, bool kIsV>
-__device__ __forceinline__ void put_block(const Block &b, int e, int lane, float *out, uint8_t *rec, int tok)
+__device__ __forceinline__ void put(const Block4 &o, int b, int lane, uint8_t *rec, int tok, bool live)
 {
-    if (out) out[32 * e + lane] = b.value;
-    if (!rec) return;
-    const int high = __shfl_down_sync(0xffffffffu, b.code, 16);
-    if (lane < 16)
-        rec[kIsV ? q4_v_byte(NB, tok, e, lane) : q4_k_byte(NB, tok, e, lane)] = static_cast<uint8_t>(b.code | (high << 4));
-    if (lane == e)
-        reinterpret_cast<uint16_t *>(rec + (kIsV ? q4_v_scale(NB, tok) : q4_k_scale(NB, tok)))[e] = b.d;
+    const int q = lane & 7;
+    const uint32_t bytes = o.codes | __shfl_down_sync(0xffffffffu, o.codes, 4) << 4;
+    if (!live) return;
+    if (q < 4) {  // bytes 4 q .. 4 q + 3
+        if (kIsV) {
+            uint8_t *p = rec + q4_v_byte(NB, tok, b, 4 * q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[16 * q4_v_run(NB) * k] = static_cast<uint8_t>(bytes >> (8 * k));
+        } else {
+            *reinterpret_cast<uint32_t *>(rec + q4_k_byte(NB, tok, b, 4 * q)) = bytes;
+        }
+    }
+    if (q == 0) reinterpret_cast<uint16_t *>(rec + (kIsV ? q4_v_scale(NB, tok) : q4_k_scale(NB, tok)))[b] = o.d;
 }
 
+__device__ __forceinline__ void load4(float (&x)[4], const float *p, bool vector)
+{
+    if (vector) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = p[k];
+    }
+}
+__device__ __forceinline__ void store4(float *p, const float4 &v, bool vector)
+{
+    if (vector) {
+        *reinterpret_cast<float4 *>(p) = v;
+    } else {
+        p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
+    }
+}
+
+static_assert(q4_v_byte(4, 5, 1, 7) - q4_v_byte(4, 5, 1, 4) == 3 * 16 * q4_v_run(4) &&
+                  q4_v_byte(3, 5, 1, 15) - q4_v_byte(3, 5, 1, 12) == 3 * 16 * q4_v_run(3),
+              "V's bytes of 4 values from a multiple of 4 on lie evenly");
+
 // grid (tokens, splits): CTA (t, y) works rows y * per .. of token t's n_heads queries, then
-// n_kv_heads keys, then values, a row a warp; a row's values are on their way
-// while the warp works the one before.
+// n_kv_heads keys, then its values 4 blocks at a time, a row a warp; a row's values are on their
+// way while the warp works the one before.
 template <int NB, int kMode>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ HeadsArgs a)
 {
@@ -278,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
     using P = Pairs<NB, kMode>;
     __shared__ float4 tab[hd / 2];  // cos h, sin h, cos l, sin l of each pair
     __shared__ float2 cos64[17];
+    __shared__ __align__(16) float keys[kWarps][2][hd];  // a rotated key, high and low parts
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t t = blockIdx.x;
     if (tid < 17) cos64[tid] = kCos64[tid];
@@ -286,7 +353,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
     const int pos = a.positions[t];
     if (pos < 0) return;  // the same for the whole CTA: a padding row
     const int H = a.n_heads, K = a.n_kv_heads;
-    const int rows = a.kv.pages ? H + 2 * K : H + K;
+    const int v_rows = a.kv.pages ? (K * NB + 3) / 4 : 0, rows = H + K + v_rows;
     const int per = (rows + gridDim.y - 1) / gridDim.y;
     const int r0 = blockIdx.y * per, r1 = min(rows, r0 + per);
 
@@ -305,14 +372,13 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
         }
     }
     auto load = [&](float (&x)[NB], int r) {
-        const float *p = r < H ? a.q + t * a.ld_q + (int64_t)r * hd
-                               : r < H + K ? a.k + t * a.ld_k + (int64_t)(r - H) * hd
-                                           : a.v + t * a.ld_v + (int64_t)(r - H - K) * hd;
+        const float *p = r < H ? a.q + t * a.ld_q + (int64_t)r * hd : a.k + t * a.ld_k + (int64_t)(r - H) * hd;
 #pragma unroll
         for (int e = 0; e < NB; ++e) x[e] = p[32 * e + lane];
     };
     float nx[NB];
-    if (r0 + warp < r1) load(nx, r0 + warp);
+    const int last = min(r1, H + K);  // of the rows of whole heads
+    if (r0 + warp < last) load(nx, r0 + warp);
     __syncthreads();  // cos64
     for (int i = tid; i < hd / 2; i += kThreads) {
         Two c, s;
@@ -325,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
     auto next = [&](float (&x)[NB]) {  // row r's values, and the next row's on their way
 #pragma unroll
         for (int e = 0; e < NB; ++e) x[e] = nx[e];
-        if (r + kWarps < r1) load(nx, r + kWarps);
+        if (r + kWarps < last) load(nx, r + kWarps);
     };
     // ---- queries
     if (r < min(r1, H)) {
@@ -367,7 +433,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
         }
     }
     // ---- keys
-    for (; r < min(r1, H + K); r += kWarps) {
+    const bool k_vector = a.k_out && (reinterpret_cast<uintptr_t>(a.k_out) & 15) == 0;
+    for (; r < last; r += kWarps) {
         float x[NB], o[NB], xl[NB], ol[NB];
         next(x);
 #pragma unroll
@@ -398,19 +465,40 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
             const bool first = P::first(e, lane);
             const Two z = add(mul(Two{x[e], xl[e]}, Two{cs.x, cs.z}),
                               mul(Two{o[e], ol[e]}, first ? Two{-cs.y, -cs.w} : Two{cs.y, cs.w}));
-            if (a.kv.pages) put_block<NB, false>(quantise(z), e, lane, out, base, tok);
-            else if (out) out[32 * e + lane] = z.h;
+            if (a.kv.pages) {
+                keys[warp][0][32 * e + lane] = z.h;
+                keys[warp][1][32 * e + lane] = z.l;
+            } else if (out) {
+                out[32 * e + lane] = z.h;
+            }
         }
-    }
-    // ---- values
-    for (; r < r1; r += kWarps) {
-        float x[NB];
-        next(x);
-        const int h = r - H - K;
-        float *out = a.v_out ? a.v_out + (t * K + h) * (int64_t)hd : nullptr;
-        uint8_t *base = rec ? rec + ((int64_t)h << a.kv.page_log) * q4_record_bytes(hd) : nullptr;
+        if (!a.kv.pages) continue;
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < NB; ++e) put_block<NB, true>(quantise(Two{x[e], 0.0f}), e, lane, out, base, tok);
+        for (int b0 = 0; b0 < NB; b0 += 4) {
+            const int b = b0 + (lane >> 3);
+            const bool live = b < NB;
+            float zh[4], zl[4];
+            load4(zh, keys[warp][0] + (live ? 32 * b : 0) + 4 * (lane & 7), true);
+            load4(zl, keys[warp][1] + (live ? 32 * b : 0) + 4 * (lane & 7), true);
+            const Block4 blk = quantise<true>(zh, zl);
+            if (out && live) store4(out + 32 * b + 4 * (lane & 7), blk.value, k_vector);
+            put<NB, false>(blk, b, lane, base, tok, live && base != nullptr);
+        }
+        __syncwarp();  // keys is read
+    }
+    // ---- values: rows H + K ..
+    const bool v_vector = ((reinterpret_cast<uintptr_t>(a.v) | static_cast<uintptr_t>(a.ld_v) * 4) & 15) == 0;
+    const bool o_vector = (reinterpret_cast<uintptr_t>(a.v_out) & 15) == 0;
+    for (; r < r1; r += kWarps) {
+        const int beta = 4 * (r - H - K) + (lane >> 3), h = beta / NB, b = beta - h * NB;  // block of the token's values
+        const bool live = beta < K * NB;
+        const int64_t at = live ? 32 * beta + 4 * (lane & 7) : 0;
+        float x[4];
+        load4(x, a.v + t * a.ld_v + at, v_vector);
+        const Block4 blk = quantise<false>(x, x);
+        if (a.v_out && live) store4(a.v_out + t * (int64_t)(K * hd) + at, blk.value, o_vector);
+        put<NB, true>(blk, b, lane, rec + ((int64_t)h << a.kv.page_log) * q4_record_bytes(hd), tok, live && rec != nullptr);
     }
 }
 
@@ -441,7 +529,7 @@ cudaError_t launch_qk_norm_rope(HeadsArgs &a, int64_t rows, int head_dim, float 
         const double turns = low[i % 16] * high[i / 16];
         a.turn[i] = static_cast<uint64_t>(static_cast<int64_t>((turns - floor(turns)) * 0x1p62)) << 2;
     }
-    const int per_token = a.n_heads + (a.kv.pages ? 2 : 1) * a.n_kv_heads;
+    const int per_token = a.n_heads + a.n_kv_heads + (a.kv.pages ? (a.n_kv_heads * (head_dim / 32) + 3) / 4 : 0);
     // CTAs for each token: up to one row for each warp, so that a few tokens spread over
     // the SMs, and one for each token once the tokens alone fill them twice
     const int64_t want = 2 * (int64_t)dev_info().sm_count;

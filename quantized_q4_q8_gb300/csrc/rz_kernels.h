@@ -290,7 +290,7 @@ constexpr int kPagedMaxSeqs = 1024;
 size_t paged_attention_workspace_bytes(int head_dim);
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *workspace, cudaStream_t s);
 // Requests with more query rows than this for a kv head on tcgen05 (attention_q4_tc.cu).
-constexpr int kTcRows = 64;
+constexpr int kTcRows = 31;
 bool paged_attention_tc_takes(int head_dim);
 size_t paged_attention_tc_part_bytes(int head_dim);
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, cudaStream_t s);
