@@ -528,8 +528,9 @@ rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t 
  *   att_q8     Q8_1 of n_rows rows of q_pad (n_heads * head_dim rounded up to 256; the O
  *              projection's input), or NULL
  *   workspace  rz_attention_paged_q4_workspace_bytes bytes, 16-byte aligned, zero-filled
- *              once after allocating it (a completed call leaves its counters zero); calls
- *              that share it must not overlap on the GPU, captured ones among them
+ *              once after allocating it (a completed call leaves its counters zero; after
+ *              RZ_ERR_TIMEOUT fill it with zeros again); calls that share it must not overlap on
+ *              the GPU, captured ones among them
  * Scores and sums are f32-accurate: q and the weights enter as two f16 pieces each, the
  * codes exactly.  A length, row offset or page outside its range records RZ_ERR_DEVICE:
  * the request counts as empty (lengths beyond its table, bad row offsets), or its

@@ -78,6 +78,13 @@ __device__ __forceinline__ float quad_max(float v)
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
+__device__ __forceinline__ int add_acq_rel(int *p, int v)
+{
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
 template <int W>
 __device__ __forceinline__ void consumer_sync()
 {
@@ -570,7 +577,7 @@ struct Layout {
     static constexpr int slot = 2 * q4_record_bytes(hd);
     static constexpr int sums = rows * (hd + kPad) * 4;
     static constexpr int queries = W * 2 * NB * 512;  // fragments of two tiles of queries for each warp
-    static constexpr int fixed = queries + sums + rows * 8 + 512 + kMaxCtas * 2;  // and 20 bytes for each request and 8
+    static constexpr int fixed = queries + sums + rows * 8 + 512 + 2 * kMaxCtas * 2;  // and 20 bytes for each request and 8
     static constexpr int64_t part = (int64_t)rows * (hd + 2);  // floats of a partial record: sums, then (m, l)
 };
 
@@ -706,9 +713,10 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
     float2 *ml = reinterpret_cast<float2 *>(sums + L::sums / 4);
     uint64_t *full = reinterpret_cast<uint64_t *>(ml + L::rows), *empty = full + kMaxSlots;
     int *flags = reinterpret_cast<int *>(empty + kMaxSlots);  // [0] a wait ran out, [1] this CTA adds the parts up
-    int *part_count = flags + 2;  // W
+    int *part_count = flags + 2;  // 2
+    uint64_t *listed = empty + kMaxSlots + 2;  // the lists of parts are there
     int16_t *part_list = reinterpret_cast<int16_t *>(reinterpret_cast<uint8_t *>(full) + 512);
-    int64_t *pre = reinterpret_cast<int64_t *>(part_list + kMaxCtas);
+    int64_t *pre = reinterpret_cast<int64_t *>(part_list + 2 * kMaxCtas);
     SeqRow *seqs = reinterpret_cast<SeqRow *>(pre + a.n_seqs + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = a.kv.n_kv_heads, group = a.n_heads / K;
@@ -717,8 +725,11 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
             mbar_init(full + i, 1);
             mbar_init(empty + i, W);
         }
+        mbar_init(listed, 1);
+        mbar_init(listed + 1, 1);
         fence_mbar_init();
         flags[0] = flags[1] = 0;
+        part_count[0] = part_count[1] = 0;
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -816,6 +827,28 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
                 issued += n;
                 ring_step(pos, n, slots);
             }
+            if (more && w.lo < w.hi && (w.lo > 0 || w.hi < w.units)) {
+                // a part of an item, its copies on their way: the CTAs whose shares hold its units, in order (a CTA
+                // has one part that begins its item and one that does not)
+                const int cost = unit_cost<W>(w.q.rg);
+                int16_t *list = part_list + (w.lo == 0) * kMaxCtas;
+                int c = min(static_cast<int>(min(w.at / max(line.step, (int64_t)1), (int64_t)line.ctas)), line.ctas - 1);
+                while (line.begin(c) > w.at) --c;
+                int parts = 0;
+                for (int c0 = c; c0 < line.ctas && line.begin(c0) < w.at + kItemCost<W> + (int64_t)w.units * cost; c0 += 32) {
+                    const int k = c0 + lane;
+                    const int lo = unit_at<W>(line.begin(k) - w.at, w.units, cost), hi = unit_at<W>(line.begin(k + 1) - w.at, w.units, cost);
+                    const bool has = k < line.ctas && lo < hi;
+                    const unsigned all = __ballot_sync(0xffffffffu, has);
+                    if (has) list[parts + __popc(all & ((1u << lane) - 1))] = static_cast<int16_t>(2 * k + (lo == 0));  // odd: begins the item
+                    parts += __popc(all);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    part_count[w.lo == 0] = parts;
+                    mbar_arrive(listed + (w.lo == 0));
+                }
+            }
             if (more) more = walk_next<W>(w, a, seqs, group);
         }
         // no copy outlives the CTA: after an abort, those that no consumer waits for any more are waited out
@@ -877,40 +910,20 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
                 }
             }
             if (!whole) {
-                // ---- the CTAs whose shares hold the item's units, in order; the last to arrive adds them up
-                const int cost = unit_cost<W>(rg);
-                int c = static_cast<int>(w.at / max(line.step, (int64_t)1));  // at or after the CTA that holds w.at
-                c = min(c, line.ctas - 1);
-                while (line.begin(c) > w.at) --c;
-                int parts = 0;
-                for (int c0 = c; c0 < line.ctas; c0 += W * 32) {
-                    const int k = c0 + tid;
-                    const int lo = unit_at<W>(line.begin(k) - w.at, w.units, cost), hi = unit_at<W>(line.begin(k + 1) - w.at, w.units, cost);
-                    const unsigned has = __ballot_sync(0xffffffffu, k < line.ctas && lo < hi);
-                    consumer_sync<W>();  // the counts of the round before are read
-                    if (lane == 0) part_count[warp] = __popc(has);
-                    consumer_sync<W>();
-                    int before = parts;
-#pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        if (i < warp) before += part_count[i];
-                        parts += part_count[i];
-                    }
-                    // 2 k + 1: its part begins the item
-                    if (has >> lane & 1) part_list[before + __popc(has & ((1u << lane) - 1))] = static_cast<int16_t>(2 * k + (lo == 0));
-                    if (line.begin(min(c0 + W * 32, line.ctas)) >= w.at + kItemCost<W> + (int64_t)w.units * cost) break;
-                }
-                __threadfence();
-                consumer_sync<W>();
+                // ---- the last CTA to arrive adds the parts up
+                const bool known = mbar_wait(listed + (w.lo == 0), 0);  // false: the producer gave up
+                const int parts = known ? part_count[w.lo == 0] : 0;
+                const int16_t *list = part_list + (w.lo == 0) * kMaxCtas;
+                consumer_sync<W>();  // the part is written
                 if (tid == 0) {
-                    int *counter = a.counters + (part_list[0] >> 1);
-                    const int before = atomicAdd(counter, 1);
-                    flags[1] = before == parts - 1;
-                    if (before == parts - 1) *counter = 0;
+                    // (the add releases what the barrier gathered, and acquires the other parts)
+                    int *counter = a.counters + (known ? list[0] >> 1 : 0);
+                    const int before = known ? add_acq_rel(counter, 1) : -1;
+                    flags[1] = known && before == parts - 1;
+                    if (flags[1]) *counter = 0;
                 }
                 consumer_sync<W>();
                 if (flags[1]) {
-                    __threadfence();
                     for (int i0 = 0; i0 < quads; i0 += W * 32) {
                         const int i = i0 + tid;
                         const int r = i / (hd / 4), c4 = i % (hd / 4) * 4;
@@ -918,9 +931,9 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
                         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         float m = -1e37f, l = 0.0f;
                         if (mine) {
-#pragma unroll 4
+#pragma unroll 8
                             for (int k = 0; k < parts; ++k) {
-                                const float *pk = a.part + part_list[k] * L::part;
+                                const float *pk = a.part + list[k] * L::part;
                                 const float2 x = __ldcg(reinterpret_cast<const float2 *>(pk + L::rows * hd + 2 * r));
                                 const float4 u = __ldcg(reinterpret_cast<const float4 *>(pk + r * hd + c4));
                                 const float mn = fmaxf(m, x.x), f0 = ex2(m - mn), f1 = ex2(x.x - mn);

@@ -338,7 +338,7 @@ static_assert(q4_v_byte(4, 5, 1, 7) - q4_v_byte(4, 5, 1, 4) == 3 * 16 * q4_v_run
 // n_kv_heads keys, then its values 4 blocks at a time, a row a warp; a row's values are on their
 // way while the warp works the one before.
 template <int NB, int kMode>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ HeadsArgs a)
+__global__ void __launch_bounds__(kThreads, 10) qk_norm_rope_kernel(const __grid_constant__ HeadsArgs a)
 {
     constexpr int hd = 32 * NB;
     using P = Pairs<NB, kMode>;
