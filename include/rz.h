@@ -544,6 +544,25 @@ rz_status rz_attention_paged_q4(const float *q, int64_t ld_q, int64_t n_rows, co
                                 rz_stream stream);
 
 /*
+ * rz_decode_layer_paged -- rz_decode_layer over the paged 4-bit cache: the new tokens of
+ * any requests, m rows in all (1 .. RZ_MAX_BATCH), through one layer: the RMSNorm and Q, K, V
+ * projections, rz_qk_norm_rope, rz_attention_paged_q4, then the O projection and the FFN.
+ *   input, output f32 [m][hidden_pad] (output may alias input)
+ *   w             as rz_decode_layer; q_gamma, k_gamma f32 [head_dim] norms of the heads, or NULL
+ *   kv            this layer's cache; positions, slots, block_table, cu_rows, kv_len: of one
+ *                 rz_paged_plan, for every layer of the step.  Rows without a request (or of
+ *                 a refused one) come out undefined.
+ *   workspace     rz_decode_layer_paged_workspace_bytes bytes, 16-byte aligned, zero-filled
+ *                 once after allocating it; calls that share it must not overlap on the GPU
+ */
+size_t rz_decode_layer_paged_workspace_bytes(const rz_layer_weights *w, int64_t m);
+rz_status rz_decode_layer_paged(const float *input, const rz_layer_weights *w, const float *q_gamma, const float *k_gamma,
+                                const rz_kv_q4 *kv, const int32_t *positions, const int64_t *slots,
+                                const int32_t *block_table, int64_t ld_table, int32_t max_blocks, const int32_t *cu_rows,
+                                const int32_t *kv_len, int32_t n_seqs, int64_t m, float *output, void *workspace,
+                                size_t ws_bytes, rz_stream stream);
+
+/*
  * rz_check_device_error -- synchronise `stream`, read the device error word of the
  * current device and clear it.  *code_out (nullable) receives the raw code (0 = none).
  * Returns RZ_OK, RZ_ERR_TIMEOUT (a bounded wait ran out) or RZ_ERR_DEVICE (a

@@ -112,6 +112,9 @@ SIGNATURES = {
     "rz_attention_paged_q4_workspace_bytes": [_i32, _i32, _i32],
     "rz_attention_paged_q4": [_vp, _i64, _i64, _KQP, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _sz,
                               _vp],
+    "rz_decode_layer_paged_workspace_bytes": [_LWP, _i64],
+    "rz_decode_layer_paged": [_vp, _LWP, _vp, _vp, _KQP, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _i64, _vp, _vp, _sz,
+                              _vp],
     "rz_check_device_error": [_vp, C.POINTER(C.c_uint32)],
     "rz_set_pdl": [C.c_int],
     "rz_debug_stall_next_gemv": [C.c_uint32],
@@ -123,6 +126,7 @@ _RESTYPES = {"rz_last_error": C.c_char_p, "rz_version": C.c_char_p,
              "rz_decode_layer_workspace_bytes": _sz, "rz_decode_stack_workspace_bytes": _sz,
              "rz_decode_layer_q4_0_workspace_bytes": _sz, "rz_q4k_q8_gemm_workspace_bytes": _sz,
              "rz_kv_q4_page_bytes": _sz, "rz_attention_paged_q4_workspace_bytes": _sz,
+             "rz_decode_layer_paged_workspace_bytes": _sz,
              "rz_decode_stack_launches": C.c_int32}
 
 _lib = None

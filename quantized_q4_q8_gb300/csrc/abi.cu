@@ -102,6 +102,7 @@ rz_status record_error(rz_status st, const char *msg)
 }
 
 rz_status ensure_device() { return check_device(); }
+rz_status check_layer_weights(const rz_layer_weights *w, const char *fn, int64_t m, LayerDesc *out);
 
 const DevInfo &dev_info()
 {
@@ -474,6 +475,16 @@ rz_status check_layer(const rz_layer_weights *w, const char *fn, int64_t m, Laye
     *out = d;
     return RZ_OK;
 }
+
+}  // namespace
+
+// Shared with the entry points of the paged cache.
+rz_status rz::check_layer_weights(const rz_layer_weights *w, const char *fn, int64_t m, LayerDesc *out)
+{
+    return check_layer(w, fn, m, out);
+}
+
+namespace {
 
 rz_status check_kv(const rz_kv_cache *kv, const char *fn, int64_t m, int kv_dim, KvDesc *out)
 {

@@ -12,6 +12,7 @@
 namespace rz {
 rz_status record_error(rz_status st, const char *msg);
 rz_status ensure_device();
+rz_status check_layer_weights(const rz_layer_weights *w, const char *fn, int64_t m, LayerDesc *out);
 }  // namespace rz
 
 using namespace rz;
@@ -270,6 +271,61 @@ rz_status rz_attention_paged_q4(const float *q, int64_t ld_q, int64_t n_rows, co
     a.att_q8 = att_q8;
     a.err = dev_error_word();
     return launched(fn, launch_paged_attention(a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+size_t rz_decode_layer_paged_workspace_bytes(const rz_layer_weights *w, int64_t m)
+{
+    record_error(RZ_OK, "");
+    LayerDesc L;
+    if (check_layer_weights(w, "rz_decode_layer_paged_workspace_bytes", m, &L) != RZ_OK) return 0;
+    return layer_paged_workspace_bytes(L, m);
+}
+
+rz_status rz_decode_layer_paged(const float *input, const rz_layer_weights *w, const float *q_gamma, const float *k_gamma,
+                                const rz_kv_q4 *kv, const int32_t *positions, const int64_t *slots,
+                                const int32_t *block_table, int64_t ld_table, int32_t max_blocks, const int32_t *cu_rows,
+                                const int32_t *kv_len, int32_t n_seqs, int64_t m, float *output, void *workspace,
+                                size_t ws_bytes, rz_stream stream)
+{
+    const char *fn = "rz_decode_layer_paged";
+    record_error(RZ_OK, "");
+    if (!input || !output || !positions || !slots || !block_table || !cu_rows || !kv_len)
+        return fail(RZ_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(input, 16) || !aligned(output, 16)) return fail(RZ_ERR_ALIGN, "%s: input/output alignment", fn);
+    const void *words[] = {q_gamma, k_gamma, positions, block_table, cu_rows, kv_len};
+    for (const void *p : words)
+        if (!aligned(p, 4)) return fail(RZ_ERR_ALIGN, "%s: buffers must be 4-byte aligned", fn);
+    if (!aligned(slots, 8)) return fail(RZ_ERR_ALIGN, "%s: slots must be 8-byte aligned", fn);
+    if (n_seqs < 1 || n_seqs > kPagedMaxSeqs) return fail(RZ_ERR_SHAPE, "%s: n_seqs=%d outside [1, %d]", fn, n_seqs, kPagedMaxSeqs);
+    PagedKv pk{};
+    RZ_TRY(check_kv_q4(fn, kv, &pk));
+    RZ_TRY(check_blocks(fn, max_blocks, ld_table, kv->page_size));
+    if (w && (pk.n_kv_heads != w->n_kv_heads || pk.head_dim != w->head_dim))
+        return fail(RZ_ERR_SHAPE, "%s: the cache holds %d heads of %d", fn, pk.n_kv_heads, pk.head_dim);
+    LayerDesc L;
+    RZ_TRY(check_layer_weights(w, fn, m, &L));
+    if (!workspace) return fail(RZ_ERR_INVALID_ARG, "%s: null workspace", fn);
+    if (!aligned(workspace, 16)) return fail(RZ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+    const size_t need = layer_paged_workspace_bytes(L, m);
+    if (ws_bytes < need) return fail(RZ_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+    HeadsArgs h{};
+    h.q_gamma = q_gamma;
+    h.k_gamma = k_gamma;
+    h.positions = positions;
+    h.slots = slots;
+    h.kv = pk;
+    h.err = dev_error_word();
+    PagedAttnArgs a{};
+    a.kv = pk;
+    a.table = block_table;
+    a.table_ld = ld_table;
+    a.max_blocks = max_blocks;
+    a.cu_rows = cu_rows;
+    a.kv_len = kv_len;
+    a.n_seqs = n_seqs;
+    a.scale = 1.0f / std::sqrt((float)pk.head_dim);
+    a.err = h.err;
+    return launched(fn, launch_decode_layer_paged(input, L, h, a, m, output, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

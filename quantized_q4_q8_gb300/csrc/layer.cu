@@ -165,16 +165,11 @@ AttnArgs make_attn_args(const LayerDesc &L, int64_t m, const KvDesc &kv, const i
     return a;
 }
 
-cudaError_t launch_decode_layer(const float *input, const LayerDesc &L, const KvDesc &kv,
-                                const int32_t *positions, int position, int64_t m, float *output,
-                                void *workspace, cudaStream_t s)
+// RMSNorm -> Q8_1 -> the Q, K and V projections side by side in w.qkv
+static cudaError_t launch_qkv(const float *input, const LayerDesc &L, const LayerWs &w, int64_t m, cudaStream_t s)
 {
-    LayerWs w = layer_ws(L, m, kv.max_seq, static_cast<uint8_t *>(workspace));
     const int q_dim = L.n_heads * L.head_dim, kv_dim = L.n_kv_heads * L.head_dim;
-    const int q_pad = (q_dim + 255) / 256 * 256;
     const int64_t ld_qkv = q_dim + 2 * kv_dim;
-
-    cudaError_t e;
     Q4kSegment qkv[3] = {{L.wq, w.qkv, nullptr, q_dim, ld_qkv, 0, L.bq},
                          {L.wk, w.qkv + q_dim, nullptr, kv_dim, ld_qkv, 0, L.bk},
                          {L.wv, w.qkv + q_dim + kv_dim, nullptr, kv_dim, ld_qkv, 0, L.bv}};
@@ -186,23 +181,83 @@ cudaError_t launch_decode_layer(const float *input, const LayerDesc &L, const Kv
     }
     if (q4k_gemv_f32_input_preferred(m, L.hidden_pad)) {
         // RMSNorm -> Q8_1 inside the Q|K|V GEMV
-        e = launch_q4k_gemv_f32(qkv, nseg, EPI_STORE,
-                                F32Input{input, L.hidden_pad, L.attn_gamma, L.hidden, L.eps}, m, L.hidden_pad, s);
-    } else {
-        e = launch_rmsnorm(input, L.attn_gamma, nullptr, w.x8, m, L.hidden, L.hidden_pad, L.eps, s);
-        if (e != cudaSuccess) return e;
-        e = launch_q4k_gemv(qkv, nseg, EPI_STORE, w.x8, m, L.hidden_pad, s);
+        return launch_q4k_gemv_f32(qkv, nseg, EPI_STORE,
+                                   F32Input{input, L.hidden_pad, L.attn_gamma, L.hidden, L.eps}, m, L.hidden_pad, s);
     }
+    const cudaError_t e = launch_rmsnorm(input, L.attn_gamma, nullptr, w.x8, m, L.hidden, L.hidden_pad, L.eps, s);
+    if (e != cudaSuccess) return e;
+    return launch_q4k_gemv(qkv, nseg, EPI_STORE, w.x8, m, L.hidden_pad, s);
+}
+
+// The O projection of the quantised attention output with the residual, then the FFN.
+static cudaError_t launch_after_attention(const float *input, const LayerDesc &L, const LayerWs &w, int64_t m, float *output,
+                                          cudaStream_t s)
+{
+    const int q_pad = (L.n_heads * L.head_dim + 255) / 256 * 256;
+    Q4kSegment o = {L.wo, w.res1, input, L.hidden, L.hidden_pad, L.hidden_pad};
+    const cudaError_t e = launch_q4k_gemv(&o, 1, EPI_RESID, w.a8, m, q_pad, s);
+    if (e != cudaSuccess) return e;
+    return launch_swiglu_ffn(w.res1, L.ffn_gamma, L.wgate, L.wup, L.wdown, output, m, L.hidden,
+                             L.hidden_pad, L.inter, L.eps, w.ffn, s);
+}
+
+cudaError_t launch_decode_layer(const float *input, const LayerDesc &L, const KvDesc &kv,
+                                const int32_t *positions, int position, int64_t m, float *output,
+                                void *workspace, cudaStream_t s)
+{
+    LayerWs w = layer_ws(L, m, kv.max_seq, static_cast<uint8_t *>(workspace));
+    const int q_dim = L.n_heads * L.head_dim, kv_dim = L.n_kv_heads * L.head_dim;
+    const int64_t ld_qkv = q_dim + 2 * kv_dim;
+
+    cudaError_t e = launch_qkv(input, L, w, m, s);
     if (e != cudaSuccess) return e;
     AttnArgs a = make_attn_args(L, m, kv, positions, position, w.part, w.counters,
                                 w.qkv, w.qkv + q_dim, w.qkv + q_dim + kv_dim, ld_qkv, nullptr, w.a8);
     e = launch_attention(a, s);
     if (e != cudaSuccess) return e;
-    Q4kSegment o = {L.wo, w.res1, input, L.hidden, L.hidden_pad, L.hidden_pad};
-    e = launch_q4k_gemv(&o, 1, EPI_RESID, w.a8, m, q_pad, s);
+    return launch_after_attention(input, L, w, m, output, s);
+}
+
+// ---------------------------------------------------------------- decode layer over the paged 4-bit cache
+// The workspace of the paged attention (its counters first) lies before the intermediates, of
+// which the f32 cache's attention takes none.
+static size_t paged_attention_ws(const LayerDesc &L) { return align256(paged_attention_workspace_bytes(L.head_dim)); }
+
+size_t layer_paged_workspace_bytes(const LayerDesc &L, int64_t m)
+{
+    return paged_attention_ws(L) + layer_ws(L, m, 1, nullptr).total;
+}
+
+cudaError_t launch_decode_layer_paged(const float *input, const LayerDesc &L, const HeadsArgs &heads,
+                                      const PagedAttnArgs &attn, int64_t m, float *output, void *workspace,
+                                      cudaStream_t s)
+{
+    LayerWs w = layer_ws(L, m, 1, static_cast<uint8_t *>(workspace) + paged_attention_ws(L));
+    const int q_dim = L.n_heads * L.head_dim, kv_dim = L.n_kv_heads * L.head_dim;
+    const int64_t ld_qkv = q_dim + 2 * kv_dim;
+    cudaError_t e = launch_qkv(input, L, w, m, s);
     if (e != cudaSuccess) return e;
-    return launch_swiglu_ffn(w.res1, L.ffn_gamma, L.wgate, L.wup, L.wdown, output, m, L.hidden,
-                             L.hidden_pad, L.inter, L.eps, w.ffn, s);
+    // q is normed and rotated in place
+    HeadsArgs h = heads;
+    h.q = h.q_out = w.qkv;
+    h.k = w.qkv + q_dim;
+    h.v = w.qkv + q_dim + kv_dim;
+    h.ld_q = h.ld_qo = h.ld_k = h.ld_v = ld_qkv;
+    h.n_heads = L.n_heads;
+    h.n_kv_heads = L.n_kv_heads;
+    h.rope_mode = L.rope_mode;
+    h.eps = L.eps;
+    e = launch_qk_norm_rope(h, m, L.head_dim, L.rope_theta, s);
+    if (e != cudaSuccess) return e;
+    PagedAttnArgs a = attn;
+    a.q = w.qkv;
+    a.ld_q = ld_qkv;
+    a.n_rows = m;
+    a.n_heads = L.n_heads;
+    a.att_q8 = w.a8;
+    e = launch_paged_attention(a, workspace, s);
+    if (e != cudaSuccess) return e;
+    return launch_after_attention(input, L, w, m, output, s);
 }
 
 // ---------------------------------------------------------------- stack

@@ -212,6 +212,15 @@ cudaError_t launch_decode_layer(const float *input, const LayerDesc &L, const Kv
                                 void *workspace, cudaStream_t s);
 size_t stack_workspace_bytes(const LayerDesc &L, int64_t m, int max_seq);
 
+// The decode layer over the paged 4-bit cache: heads and attn as the layer's caller gives
+// them (positions, slots, gammas; table, offsets, lengths), the rest filled by the launcher.
+struct HeadsArgs;
+struct PagedAttnArgs;
+size_t layer_paged_workspace_bytes(const LayerDesc &L, int64_t m);
+cudaError_t launch_decode_layer_paged(const float *input, const LayerDesc &L, const HeadsArgs &heads,
+                                      const PagedAttnArgs &attn, int64_t m, float *output, void *workspace,
+                                      cudaStream_t s);
+
 // The Q4_0 whole-model layer (every projection Q4_0 against f32 activations).
 struct LayerQ40Desc {
     const void *wqkv, *wo, *wgate, *wup, *wdown;  // wgate nullptr: GELU FFN

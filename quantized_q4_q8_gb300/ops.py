@@ -21,6 +21,7 @@ __all__ = [
     "rz_decode_layers", "decode_layers", "DeviceLayerQ40", "decode_layer_q4_0",
     "kv_q4_page_bytes", "PagedKVQ4", "PagedPlan", "rz_paged_plan", "paged_plan", "rz_qk_norm_rope", "qk_norm_rope",
     "rz_attention_paged_q4", "attention_paged_q4_workspace_bytes", "attention_paged_q4",
+    "decode_layer_paged_workspace_bytes", "decode_layer_paged",
 ]
 
 
@@ -702,4 +703,40 @@ def attention_paged_q4(q, kv: PagedKVQ4, block_table, cu_rows, kv_len, n_heads: 
          _row_ld(block_table, max_blocks, "block_table"), max_blocks, _vector(cu_rows, i32, n + 1, dev, "cu_rows"),
          _vector(kv_len, i32, n, dev, "kv_len"), n, n_heads, scale, out.data_ptr(), q8_at,
          _vector(ws, torch.uint8, 0, dev, "ws", more=True), ws.shape[0], _stream_on(stream, dev))
+    return out
+
+
+def decode_layer_paged_workspace_bytes(layer: DeviceLayer, m: int) -> int:
+    return int(load().rz_decode_layer_paged_workspace_bytes(C.byref(layer.struct), m))
+
+
+def decode_layer_paged(x, layer: DeviceLayer, kv: PagedKVQ4, block_table, plan: PagedPlan, q_gamma=None, k_gamma=None,
+                       out=None, ws=None, stream=None):
+    """One decode step of one layer over the paged 4-bit cache, for the rows of `plan` (see
+    rz.h).  x f32 [m, hidden_pad], m up to 16 and to plan.max_rows; the plan serves every layer of the step."""
+    import torch
+    i32, dev = torch.int32, torch.cuda.current_device()
+    m, width = _on_device(x, torch.float32, 2, dev, "x").shape
+    if width != layer.hidden_pad or not x.is_contiguous():
+        raise ValueError("x must be contiguous [m, hidden_pad]")
+    if m > plan.max_rows or kv.dev != dev:
+        raise ValueError("the plan has fewer rows than x, or the cache is on another device")
+    n, max_blocks = _on_device(block_table, i32, 2, dev, "block_table").shape
+    if n != plan.n_seqs:
+        raise ValueError("block_table must have a row for each request of the plan")
+    gammas = [None if t is None else _vector(t, torch.float32, layer.head_dim, dev, name)
+              for name, t in (("q_gamma", q_gamma), ("k_gamma", k_gamma))]
+    if out is None:
+        out = _new((m, width), torch.float32, dev, stream)
+    elif _on_device(out, torch.float32, 2, dev, "out").shape != x.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous, with the shape of x")
+    if ws is None:
+        ws = _new((max(decode_layer_paged_workspace_bytes(layer, m), 16),), torch.uint8, dev, stream)
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                               torch.cuda.ExternalStream(_stream_on(stream, dev))):
+            ws.zero_()
+    call("rz_decode_layer_paged", x.data_ptr(), C.byref(layer.struct), *gammas, kv.ref,
+         _on_device(plan.positions, i32, 1, dev, "plan").data_ptr(), plan.slots.data_ptr(), block_table.data_ptr(),
+         _row_ld(block_table, max_blocks, "block_table"), max_blocks, plan.cu_rows.data_ptr(), plan.kv_len.data_ptr(), n, m,
+         out.data_ptr(), _vector(ws, torch.uint8, 0, dev, "ws", more=True), ws.shape[0], _stream_on(stream, dev))
     return out

@@ -691,3 +691,72 @@ def test_calls_on_two_streams_with_two_workspaces(rz):
         ob = b.run(rz, stream=sb.cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(oa, wa) and torch.equal(ob, wb)
+
+
+# ------------------------------------------------------------------ the decode layer over the paged cache
+@pytest.mark.parametrize("normed", [False, True])
+def test_decode_layer_paged_is_its_steps(rz, normed):
+    """Bit for bit the composition of the public calls, for a prompt's rows, drafts and single tokens."""
+    import torch
+
+    import rz_synth as S
+    sh = S.QWEN2
+    L = S.layer(sh, "paged.l0")
+    w = {k: to_dev(v) for k, v in L.w.items()} | {"attn_gamma": to_dev(L.attn_gamma), "ffn_gamma": to_dev(L.ffn_gamma)}
+    layer = rz.DeviceLayer(w, sh.hidden, sh.hidden_pad, sh.n_heads, sh.n_kv_heads, sh.head_dim, sh.inter, sh.eps, sh.rope_theta, sh.rope_mode)
+    H, K, hd, page, n = sh.n_heads, sh.n_kv_heads, sh.head_dim, 16, 3
+    rng = np.random.default_rng(2)
+    gq, gk = (to_dev(rng.uniform(0.5, 1.5, (2, hd)).astype(np.float32))) if normed else (None, None)
+    kvs = [rz.PagedKVQ4.empty(9, page, K, hd) for _ in range(2)]
+    for kv in kvs:
+        kv.pages.zero_()
+    table = torch.full((n, 4), -1, dtype=torch.int32, device="cuda")
+    owned, count, free = torch.zeros(n, dtype=torch.int32, device="cuda"), ints([9]), torch.arange(9, dtype=torch.int32, device="cuda")
+    lens = np.zeros(n, np.int32)
+    q_pad = -(-H * hd // 256) * 256
+    ws = rz.workspace(rz.decode_layer_paged_workspace_bytes(layer, 16), "cuda")
+    for news in ([11, 4, 0], [1, 3, 9], [0, 1, 1]):
+        m = sum(news)
+        plan = rz.PagedPlan(n, m)
+        rz.paged_plan(ints(lens), ints(news), table, owned, free, count, page, plan)
+        x = to_dev(S.hidden_input(f"paged.x{m}", m, sh.hidden, sh.hidden_pad))
+        out = rz.decode_layer_paged(x, layer, kvs[0], table, plan, q_gamma=gq, k_gamma=gk, ws=ws)
+        # the same from its steps (the FFN of the layer's own workspace-free form)
+        if m <= 3:
+            qkv = rz.rmsnorm_q4k_gemv(x, w["attn_gamma"], sh.hidden, sh.eps, [w["wq"], w["wk"], w["wv"]], [H * hd, K * hd, K * hd], sh.hidden_pad)
+        else:
+            x8 = rz.rmsnorm(x, w["attn_gamma"], sh.hidden, sh.hidden_pad, sh.eps, want_y=False)[1]
+            qkv = rz.q4k_q8_gemv_multi(x8, [w["wq"], w["wk"], w["wv"]], [H * hd, K * hd, K * hd], m, sh.hidden_pad)
+        q, _, _ = rz.qk_norm_rope(qkv[:, :H * hd], qkv[:, H * hd:(H + K) * hd], qkv[:, (H + K) * hd:], plan.positions, H, K, hd, sh.rope_theta,
+                                  sh.rope_mode, q_gamma=gq, k_gamma=gk, eps=sh.eps, kv=kvs[1], slots=plan.slots)
+        a8 = torch.empty(rz.q8_1_size(m, q_pad), dtype=torch.uint8, device="cuda")
+        rz.attention_paged_q4(q, kvs[1], table, plan.cu_rows, plan.kv_len, H, att_q8=a8)
+        res = torch.zeros(m, sh.hidden_pad, device="cuda")
+        rz.q4k_q8_gemv_ex(w["wo"], a8, m, sh.hidden, q_pad, residual=x, out=res, ld=sh.hidden_pad)
+        res[:, sh.hidden:] = 0
+        want = rz.swiglu_ffn(res, w["ffn_gamma"], w["wgate"], w["wup"], w["wdown"], sh.hidden, sh.hidden_pad, sh.inter, sh.eps)
+        assert torch.equal(out, want), news
+        assert torch.equal(kvs[0].pages, kvs[1].pages)
+        lens = lens + np.array(news, np.int32)
+
+
+def test_decode_layer_paged_refusals(rz):
+    import torch
+
+    import rz_synth as S
+    sh = S.QWEN2
+    L = S.layer(sh, "paged.l0")
+    w = {k: to_dev(v) for k, v in L.w.items()} | {"attn_gamma": to_dev(L.attn_gamma), "ffn_gamma": to_dev(L.ffn_gamma)}
+    layer = rz.DeviceLayer(w, sh.hidden, sh.hidden_pad, sh.n_heads, sh.n_kv_heads, sh.head_dim, sh.inter, sh.eps, sh.rope_theta, sh.rope_mode)
+    x = torch.zeros(2, sh.hidden_pad, device="cuda")
+    table, plan = torch.zeros(1, 4, dtype=torch.int32, device="cuda"), rz.PagedPlan(1, 2)
+    kv = rz.PagedKVQ4.empty(4, 16, sh.n_kv_heads, sh.head_dim)
+    with pytest.raises(rz.RzError, match="cache holds"):
+        rz.decode_layer_paged(x, layer, rz.PagedKVQ4.empty(4, 16, sh.n_kv_heads, 2 * sh.head_dim), table, plan)
+    with pytest.raises(rz.RzError, match="workspace"):
+        rz.decode_layer_paged(x, layer, kv, table, plan, ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="fewer rows"):
+        rz.decode_layer_paged(torch.zeros(3, sh.hidden_pad, device="cuda"), layer, kv, table, plan)
+    with pytest.raises(ValueError, match="q_gamma"):
+        rz.decode_layer_paged(x, layer, kv, table, plan, q_gamma=torch.zeros(5, device="cuda"))
+    assert rz.decode_layer_paged_workspace_bytes(layer, 17) == 0
