@@ -506,7 +506,8 @@ rz_status rz_paged_plan(const int32_t *cached, const int32_t *fresh, int32_t n_s
  *   k_out, v_out f32 [n_rows][n_kv_heads * head_dim] or NULL: with a cache the values as
  *              it holds them, without one the rotated k
  * The cache's codes and scales are those of the format evaluated in f64 (the kernel
- * decides in f32 and works heads that lie next to a border again in f64).
+ * carries a key as a sum of two f32; a value within 2^-40 of a border between two codes
+ * may take either).
  */
 rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t ld_k, const float *v, int64_t ld_v,
                           const float *q_gamma, const float *k_gamma, float eps, const int32_t *positions,

@@ -175,7 +175,7 @@ rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t 
         return fail(RZ_ERR_SHAPE, "%s: n_heads=%d n_kv_heads=%d", fn, n_heads, n_kv_heads);
     if (rope_mode != 0 && rope_mode != 1) return fail(RZ_ERR_INVALID_ARG, "%s: rope_mode", fn);
     if (!(rope_theta > 0.0f) || std::isinf(rope_theta)) return fail(RZ_ERR_INVALID_ARG, "%s: rope_theta", fn);
-    if (!(eps >= 0.0f)) return fail(RZ_ERR_INVALID_ARG, "%s: eps", fn);
+    if (!(eps >= 0.0f) || std::isinf(eps)) return fail(RZ_ERR_INVALID_ARG, "%s: eps", fn);
     const int64_t q_dim = (int64_t)n_heads * head_dim, kv_dim = (int64_t)n_kv_heads * head_dim;
     if (ld_q < q_dim || ld_qo < q_dim || ld_k < kv_dim || (v && ld_v < kv_dim))
         return fail(RZ_ERR_SHAPE, "%s: a row stride is smaller than its row", fn);

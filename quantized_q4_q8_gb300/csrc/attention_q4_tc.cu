@@ -21,6 +21,13 @@
 // tensor memory and are rescaled there when a row's maximum has grown by over 2^8, and not before
 // (see attention_q4.cu).
 //
+// Sums.  The tensor cores cut what they add to an accumulator instead of rounding it: 24 steps a
+// tile let O drift towards zero by 1.6e-8 a step (1.2e-5 after 4000 tokens).  So O starts again every
+// kPeriod tiles, and the sums before are added up in the workspace (rounded adds, one thread after the other
+// for each value, in the unit of the row's maximum when its first sums went there, or when it had grown by
+// 2^60 since).  S's low products come
+// first, while its accumulators are small.
+//
 // The tensor pipe is never to wait: while it works P V of tile i, warps unpack K of tile i + 3
 // and V of tile i + 1 and form the weights of tiles i + 1 and i + 2 from S, of which there are three (P takes its S's place):
 //   warp 0       copies records (K, V's scales; V's codes) with the bulk-copy engine
@@ -54,6 +61,10 @@ constexpr int kGroups = kTile / 16;
 constexpr int kThreads = 640;
 constexpr int kItemCost = 2;  // of an item's start and end, in tiles
 constexpr float kLazy = 8.0f, kBias = 7.0f;
+// Tiles that O sums before it starts again.  1000 new rows of a request holding 4096 (32 query heads, 8 of keys
+// and values, of 128): never 204 us and off by 1.2e-5; 5 tiles 218 us and 2.8e-6; 3 tiles 224 us and 2.0e-6;
+// 2 tiles 235 us and 1.6e-6.
+constexpr int kPeriod = 3;
 constexpr int kScaleTop = 8;  // the largest |d| of a tile becomes 2^8 .. 2^9
 
 // Tensor memory columns: S three times (tile i in i mod 3), O.  P takes S's place: of every 32
@@ -71,8 +82,8 @@ struct Lay {
     static constexpr int off_q = 0, off_k = off_q + 2 * q, off_v = off_k + 2 * q;
     static constexpr int off_raw_k = off_v + 2 * v, off_raw_v = off_raw_k + 2 * raw_k;
     static constexpr int off_scale = off_raw_v + raw_v;                   // f16: K [128][NB], V of 3 tiles
-    static constexpr int off_row = off_scale + 4 * kTile * NB * 2;        // the rows' maxima after even and odd tiles, and sums
-    static constexpr int off_misc = off_row + 4 * kRows * 4;
+    static constexpr int off_row = off_scale + 4 * kTile * NB * 2;        // the rows' maxima after even and odd tiles, sums, units of the workspace's sums
+    static constexpr int off_misc = off_row + 5 * kRows * 4;
     static constexpr int bytes = off_misc + 512;
 };
 
@@ -524,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         const uint64_t q0 = operand_desc(smem_u32(sm + L::off_q), stride_q), k0 = operand_desc(smem_u32(sm + L::off_k), stride_q),
                        v0 = operand_desc(smem_u32(sm + L::off_v), stride_v);
         int item = 0;
-        // QK(j): A = Q, B = K; high * high, low * high, high * low.  One commit a product: a wait or a
+        // QK(j): A = Q, B = K; low * high, high * low, high * high.  One commit a product: a wait or a
         // commit costs this warp some hundred cycles.
         auto qk = [&](int j, int third) {
             if (lane == 0) {
@@ -533,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 for (int p = 0; p < 3; ++p)
 #pragma unroll
                     for (int k = 0; k < hd / 16; ++k)
-                        mma_ss(d, q0 + (p == 1 ? L::q / 16 : 0) + 16 * k, k0 + (p == 2 ? L::q / 16 : 0) + 16 * k,
+                        mma_ss(d, q0 + (p == 0 ? L::q / 16 : 0) + 16 * k, k0 + (p == 1 ? L::q / 16 : 0) + 16 * k,
                                idesc_f16(kTile), p || k);
                 commit(&b.s_full[third]);
             }
@@ -574,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     }
                     if (j_pv < j_qk && done >= j_pv - 1 && test(&b.p_ready[third_pv], (j_pv / 3) & 1) && test(&b.v_ready, j_pv & 1)) {
                         fence_after();
-                        pv(j_pv, third_pv, j_pv == first_j);
+                        pv(j_pv, third_pv, (j_pv - first_j) % kPeriod == 0);
                         ++j_pv;
                         third_pv = third_pv == 2 ? 0 : third_pv + 1;
                         moved = true;
@@ -756,6 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int q_dim = a.n_heads * hd, q_pad = (q_dim + 255) / 256 * 256;
         volatile float *maxima = reinterpret_cast<float *>(sm + L::off_row) + r;
+        // this row's sums of the periods before: 4 values of all rows after another
+        float *kept = a.kept + (int64_t)blockIdx.x * kRows * hd + 4 * r;
         // what the row's other thread gives for v
         unsigned pair_phase = 0;
         auto exchange = [&](float v, float &got) {
@@ -853,7 +866,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 if (lane == 0) mbar_arrive(&b.m_ready[i & 1]);
                 l *= ex2f(m - m_new);
                 m = m_new;
-                if (tile > w.lo && __any_sync(0xffffffffu, grown)) {
+                const bool again = tile > w.lo && (tile - w.lo) % kPeriod == 0;  // O starts again with this tile
+                if (again) {
+                    // its sums so far (in the unit of the maximum before) to the workspace
+                    if (!(ok = wait_for(&b.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
+                    fence_after();
+                    const bool first = tile - w.lo == kPeriod;
+                    float ref = first ? before_m : maxima[4 * kRows];
+                    if (before_m - ref > 60.0f) {  // f32's range is not to be left
+                        const float f = ex2f(ref - before_m);
+#pragma unroll 1
+                        for (int c = 0; c < hd / 4; ++c) {
+                            float4 *p = reinterpret_cast<float4 *>(kept) + c * kRows;
+                            const float4 x = __ldcg(p);
+                            *p = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+                        }
+                        ref = before_m;
+                    }
+                    maxima[4 * kRows] = ref;
+                    const float f = ex2f(before_m - ref);
+#pragma unroll 1
+                    for (int c = 0; c < hd; c += 32) {
+                        float o[32];
+                        tm_load32(tmem + lanes + kColO + c, o);
+                        float *p = kept + (c / 4 * kRows) * 4;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4, p += kRows * 4) {
+                            if (first) *reinterpret_cast<float4 *>(p) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            else
+                                asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(o[e] * f),
+                                             "f"(o[e + 1] * f), "f"(o[e + 2] * f), "f"(o[e + 3] * f)
+                                             : "memory");
+                        }
+                    }
+                    fence_before();
+                } else if (tile > w.lo && __any_sync(0xffffffffu, grown)) {
                     // O is at rest once the tile before is done
                     if (!(ok = wait_for(&b.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
                     fence_after();
@@ -914,6 +961,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             }
             float l2;
             if (!(ok = exchange(l, l2))) break;
+            const bool more_sums = w.hi - w.lo > kPeriod;
+            const float kept_ref = more_sums ? maxima[4 * kRows] : -INFINITY;
+            const float kept_f = kept_ref == -INFINITY ? 0.0f : ex2f(kept_ref - m);
+            if (more_sums) __threadfence();  // the other thread's adds are past, too
             l = half ? l2 + l : l + l2;
             if (w.lo < w.hi) {
                 if (!(ok = wait_for(&b.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, b, a.err))) break;
@@ -933,6 +984,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     tm_load16(tmem + lanes + kColO + c + 16, o);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[16 + e] = __uint_as_float(o[e]);
+                    if (more_sums) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(kept + ((c + e) / 4 * kRows) * 4));
+                            v[e] = fmaf(x.x, kept_f, v[e]);
+                            v[e + 1] = fmaf(x.y, kept_f, v[e + 1]);
+                            v[e + 2] = fmaf(x.z, kept_f, v[e + 2]);
+                            v[e + 3] = fmaf(x.w, kept_f, v[e + 3]);
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.0f;
@@ -1057,12 +1118,18 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
 
 }  // namespace
 
-size_t paged_attention_tc_part_bytes(int head_dim) { return 2 * (size_t)dev_info().sm_count * kRows * (head_dim + 2) * 4; }
+// two partial records for each CTA, then its sums of earlier periods
+size_t paged_attention_tc_part_bytes(int head_dim)
+{
+    return (size_t)dev_info().sm_count * kRows * (2 * (head_dim + 2) + head_dim) * 4;
+}
 
 bool paged_attention_tc_takes(int head_dim) { return head_dim == 64 || head_dim == 128; }
 
-cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, cudaStream_t s)
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs &args, cudaStream_t s)
 {
+    PagedAttnArgs a = args;
+    a.kept = a.part + (size_t)dev_info().sm_count * kRows * 2 * (a.kv.head_dim + 2);
     return a.kv.head_dim == 64 ? launch<2>(a, s) : launch<4>(a, s);
 }
 

@@ -291,6 +291,7 @@ struct PagedAttnArgs {
     float *att;
     void *att_q8;
     float *part;
+    float *kept;  // the tcgen05 kernel's sums of earlier periods, within part's space
     int *counters;
     unsigned *err;
     int most_rows;  // requests with more rows than this for a kv head are left to the other kernel
@@ -298,8 +299,10 @@ struct PagedAttnArgs {
 constexpr int kPagedMaxSeqs = 1024;
 size_t paged_attention_workspace_bytes(int head_dim);
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *workspace, cudaStream_t s);
-// Requests with more query rows than this for a kv head on tcgen05 (attention_q4_tc.cu).
-constexpr int kTcRows = 31;
+// Requests with more query rows than this for a kv head go to the tcgen05 kernel (attention_q4_tc.cu), whose
+// items are always 128 rows.  32 requests of 8000 tokens with 32 rows: 155 us there and 172 here; 24 requests
+// of 5 tokens, 35 rows, some hundred tokens held: 39 and 36; 20 rows: 383 and 329.
+constexpr int kTcRows = 40;
 bool paged_attention_tc_takes(int head_dim);
 size_t paged_attention_tc_part_bytes(int head_dim);
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, cudaStream_t s);

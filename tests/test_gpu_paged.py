@@ -322,7 +322,8 @@ def test_heads_codes_hold_next_to_borders(rz):
 class Setup:
     """Requests (held, new) over a cache of random pages; what no request holds is NaN."""
 
-    def __init__(self, seed, H, K, hd, page, reqs, spread=1.0, sharp=1.0, v_mean=0.0, ld=0, extra_rows=0, ld_table=0):
+    def __init__(self, seed, H, K, hd, page, reqs, spread=1.0, sharp=1.0, v_mean=0.0, ld=0, extra_rows=0, ld_table=0,
+                 key_size=None):
         import torch
         rng = np.random.default_rng(seed)
         self.H, self.K, self.hd, self.page, self.reqs = H, K, hd, page, reqs
@@ -341,6 +342,8 @@ class Setup:
             s = self.table[i, np.arange(n) // page] * page + np.arange(n) % page
             self.slots.append(s)
             used[s] = True
+            if key_size is not None:
+                k[s] *= key_size(np.arange(n))[:, None, None]
         k[~used], v[~used] = np.nan, np.nan
         with np.errstate(all="ignore"):
             flat, self.kval, self.vval = R.pack(k, v, page)
@@ -447,6 +450,15 @@ def test_attention_one_prompt_chunk(rz, n, m):
 @pytest.mark.parametrize("spread,sharp,v_mean", [(1e-4, 0.01, 0.0), (3e4, 12.0, 0.0), (1.0, 12.0, 4.0), (1.0, 1.0, 4.0)])
 def test_attention_prompt_chunk_scales(rz, spread, sharp, v_mean):
     s = Setup(8, 4, 2, 128, 16, [(900, 200), (33, 33), (2500, 100)], spread=spread, sharp=sharp, v_mean=v_mean)
+    s.check(s.run(rz).cpu().numpy())
+
+
+@pytest.mark.parametrize("first,then", [(0.05, 16.0), (16.0, 0.05)])
+@pytest.mark.parametrize("hd,H,K", [(64, 4, 1), (128, 4, 2)])
+def test_attention_prompt_chunk_maximum_moves(rz, hd, H, K, first, then):
+    """The rows' maxima grow by about 2^70 at token 2100 (or never again after it), far within the parts of an
+    item: sums that were put aside before are as good as nothing (or all there is)."""
+    s = Setup(hd, H, K, hd, 32, [(5000, 1500)], key_size=lambda j: np.where(j < 2100, first, then))
     s.check(s.run(rz).cpu().numpy())
 
 

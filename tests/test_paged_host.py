@@ -49,7 +49,7 @@ HEADS = dict(q=16, ld_q=256, k=16, ld_k=128, v=16, ld_v=128, qg=None, kg=None, e
     (dict(q=18), 3), (dict(qg=17), 3), (dict(slots=12), 3), (dict(n=0), 1), (dict(n=1 << 31), 1),
     (dict(hd=48), 2), (dict(hd=0), 2), (dict(hd=288), 2), (dict(H=0), 2), (dict(K=0), 2), (dict(K=3), 2), (dict(hd=32), 2),
     (dict(mode=2), 1), (dict(theta=0.0), 1), (dict(theta=float("nan")), 1), (dict(theta=float("inf")), 1),
-    (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
+    (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
     (dict(ld_q=255), 2), (dict(ld_k=127), 2), (dict(ld_v=127), 2), (dict(ld_qo=255), 2),
     (dict(kv=dict(pages=None)), 1), (dict(kv=dict(pages=8)), 3), (dict(kv=dict(page=20)), 2), (dict(kv=dict(n_pages=0)), 2),
     (dict(kv=dict(n_pages=1 << 31)), 2), (dict(kv=dict(heads=0)), 2), (dict(kv=dict(heads=1025)), 2),
@@ -76,6 +76,29 @@ def test_attention_refusals(lib, change, status):
     a = {**ATT, **change}
     a["kv"] = kv(lib, **(a["kv"] if isinstance(a["kv"], dict) else {})) if a["kv"] else None
     st = lib.status("rz_attention_paged_q4", *a.values())
+    assert st == status and lib.last_error(), (st, lib.last_error())
+
+
+WEIGHTS = dict(wq=16, wk=32, wv=48, wo=64, wgate=80, wup=96, wdown=112, attn_gamma=128, ffn_gamma=144, hidden=256, hidden_pad=256,
+               n_heads=4, n_kv_heads=2, head_dim=64, inter=512, eps=1e-6, rope_theta=1e4, rope_mode=0, bq=None, bk=None, bv=None)
+LAYER = dict(input=16, w=True, qg=None, kg=None, kv=True, positions=16, slots=16, table=16, ld_table=4, max_blocks=4, cu=16, kv_len=16,
+             n_seqs=2, m=5, output=32, ws=16, ws_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(input=None), 1), (dict(output=None), 1), (dict(positions=None), 1), (dict(slots=None), 1), (dict(table=None), 1),
+    (dict(cu=None), 1), (dict(kv_len=None), 1), (dict(w=None), 1), (dict(kv=None), 1),
+    (dict(input=20), 3), (dict(output=24), 3), (dict(qg=17), 3), (dict(kg=18), 3), (dict(slots=12), 3), (dict(table=17), 3), (dict(cu=18), 3),
+    (dict(kv_len=19), 3), (dict(positions=21), 3),
+    (dict(n_seqs=0), 2), (dict(n_seqs=1025), 2), (dict(ld_table=3), 2), (dict(max_blocks=0), 2), (dict(m=0), 2), (dict(m=17), 2),
+    (dict(kv=dict(hd=40)), 2), (dict(kv=dict(hd=32)), 2), (dict(kv=dict(heads=1)), 2), (dict(kv=dict(page=20)), 2), (dict(kv=dict(pages=8)), 3),
+    (dict(w=dict(wo=None)), 1), (dict(w=dict(wk=None)), 1), (dict(w=dict(wq=24)), 3), (dict(w=dict(n_kv_heads=3)), 2),
+])
+def test_layer_refusals(lib, change, status):
+    a = {**LAYER, **change}
+    a["kv"] = kv(lib, **(a["kv"] if isinstance(a["kv"], dict) else {})) if a["kv"] else None
+    a["w"] = C.byref(lib.LayerWeightsStruct(**{**WEIGHTS, **(a["w"] if isinstance(a["w"], dict) else {})})) if a["w"] else None
+    st = lib.status("rz_decode_layer_paged", *a.values())
     assert st == status and lib.last_error(), (st, lib.last_error())
 
 
