@@ -336,7 +336,7 @@ static_assert(q4_v_byte(4, 5, 1, 7) - q4_v_byte(4, 5, 1, 4) == 3 * 16 * q4_v_run
 
 // grid (tokens, splits): CTA (t, y) works rows y * per .. of token t's n_heads queries, then
 // n_kv_heads keys, then its values 4 blocks at a time, a row a warp; a row's values are on their
-// way while the warp works the one before.
+// way while the warp works the one before.  The values come first, while the angles are formed.
 template <int NB, int kMode>
 __global__ void __launch_bounds__(kThreads, 10) qk_norm_rope_kernel(const __grid_constant__ HeadsArgs a)
 {
@@ -350,18 +350,36 @@ __global__ void __launch_bounds__(kThreads, 10) qk_norm_rope_kernel(const __grid
     if (tid < 17) cos64[tid] = kCos64[tid];
     pdl_launch_dependents();
     pdl_wait();
-    const int pos = a.positions[t];
-    if (pos < 0) return;  // the same for the whole CTA: a padding row
     const int H = a.n_heads, K = a.n_kv_heads;
     const int v_rows = a.kv.pages ? (K * NB + 3) / 4 : 0, rows = H + K + v_rows;
     const int per = (rows + gridDim.y - 1) / gridDim.y;
     const int r0 = blockIdx.y * per, r1 = min(rows, r0 + per);
+    // position, slot, a row of values and one of a query or key are on their way together
+    const int pos = a.positions[t];
+    const int64_t slot = a.kv.pages ? a.slots[t] : -1;
+    const bool v_vector = ((reinterpret_cast<uintptr_t>(a.v) | static_cast<uintptr_t>(a.ld_v) * 4) & 15) == 0;
+    auto load_v = [&](float (&x)[4], int r) {  // 4 values of block beta of the token's values
+        const int beta = 4 * (r - H - K) + (lane >> 3);
+        load4(x, a.v + t * a.ld_v + (beta < K * NB ? 32 * beta + 4 * (lane & 7) : 0), v_vector);
+    };
+    int rv = r0 + warp;
+    if (rv < H + K) rv += (H + K - rv + kWarps - 1) / kWarps * kWarps;
+    float nv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (rv < r1) load_v(nv, rv);
+    auto load = [&](float (&x)[NB], int r) {
+        const float *p = r < H ? a.q + t * a.ld_q + (int64_t)r * hd : a.k + t * a.ld_k + (int64_t)(r - H) * hd;
+#pragma unroll
+        for (int e = 0; e < NB; ++e) x[e] = p[32 * e + lane];
+    };
+    float nx[NB];
+    const int last = min(r1, H + K);  // of the rows of whole heads
+    if (r0 + warp < last) load(nx, r0 + warp);
+    if (pos < 0) return;  // the same for the whole CTA: a padding row
 
     // where the token lies in the cache
     uint8_t *rec = nullptr;
     int tok = 0;
-    if (a.kv.pages) {
-        const int64_t slot = a.slots[t];
+    {
         const int lg = a.kv.page_log + 4;
         if (slot >= 0 && (slot >> lg) < a.kv.n_pages) {
             const int in_page = static_cast<int>(slot & ((1 << lg) - 1));
@@ -371,19 +389,22 @@ __global__ void __launch_bounds__(kThreads, 10) qk_norm_rope_kernel(const __grid
             set_error(a.err, DEV_BAD_SLOT);
         }
     }
-    auto load = [&](float (&x)[NB], int r) {
-        const float *p = r < H ? a.q + t * a.ld_q + (int64_t)r * hd : a.k + t * a.ld_k + (int64_t)(r - H) * hd;
-#pragma unroll
-        for (int e = 0; e < NB; ++e) x[e] = p[32 * e + lane];
-    };
-    float nx[NB];
-    const int last = min(r1, H + K);  // of the rows of whole heads
-    if (r0 + warp < last) load(nx, r0 + warp);
     __syncthreads();  // cos64
     for (int i = tid; i < hd / 2; i += kThreads) {
         Two c, s;
         turn_cos_sin(static_cast<uint64_t>(pos) * a.turn[i], cos64, c, s);
         tab[i] = make_float4(c.h, s.h, c.l, s.l);
+    }
+    // ---- values: rows H + K .., which need no angles
+    const bool o_vector = (reinterpret_cast<uintptr_t>(a.v_out) & 15) == 0;
+    for (; rv < r1; rv += kWarps) {
+        const int beta = 4 * (rv - H - K) + (lane >> 3), h = beta / NB, b = beta - h * NB;
+        const bool live = beta < K * NB;
+        const float x[4] = {nv[0], nv[1], nv[2], nv[3]};
+        if (rv + kWarps < r1) load_v(nv, rv + kWarps);
+        const Block4 blk = quantise<false>(x, x);
+        if (a.v_out && live) store4(a.v_out + t * (int64_t)(K * hd) + 32 * beta + 4 * (lane & 7), blk.value, o_vector);
+        put<NB, true>(blk, b, lane, rec + ((int64_t)h << a.kv.page_log) * q4_record_bytes(hd), tok, live && rec != nullptr);
     }
     __syncthreads();
 
@@ -486,19 +507,6 @@ __global__ void __launch_bounds__(kThreads, 10) qk_norm_rope_kernel(const __grid
             put<NB, false>(blk, b, lane, base, tok, live && base != nullptr);
         }
         __syncwarp();  // keys is read
-    }
-    // ---- values: rows H + K ..
-    const bool v_vector = ((reinterpret_cast<uintptr_t>(a.v) | static_cast<uintptr_t>(a.ld_v) * 4) & 15) == 0;
-    const bool o_vector = (reinterpret_cast<uintptr_t>(a.v_out) & 15) == 0;
-    for (; r < r1; r += kWarps) {
-        const int beta = 4 * (r - H - K) + (lane >> 3), h = beta / NB, b = beta - h * NB;  // block of the token's values
-        const bool live = beta < K * NB;
-        const int64_t at = live ? 32 * beta + 4 * (lane & 7) : 0;
-        float x[4];
-        load4(x, a.v + t * a.ld_v + at, v_vector);
-        const Block4 blk = quantise<false>(x, x);
-        if (a.v_out && live) store4(a.v_out + t * (int64_t)(K * hd) + at, blk.value, o_vector);
-        put<NB, true>(blk, b, lane, rec + ((int64_t)h << a.kv.page_log) * q4_record_bytes(hd), tok, live && rec != nullptr);
     }
 }
 
