@@ -523,17 +523,21 @@ rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t 
  *   q          f32 [n_rows] rows of n_heads * head_dim, stride ld_q (a multiple of 4),
  *              16-byte aligned, |q| < 1e35; rows behind cu_rows[n_seqs] are not read and their outputs not
  *              written
- *   block_table int32 [n_seqs][ld_table], max_blocks entries of a row in use
+ *   block_table int32 [n_seqs][ld_table], max_blocks entries of a row in use; a page may
+ *              stand in several rows (a shared prefix; rz_paged_plan itself gives each page to one request)
  *   scale      0 for 1 / sqrt(head_dim)
  *   att        f32 [n_rows][n_heads * head_dim], or NULL
  *   att_q8     Q8_1 of n_rows rows of q_pad (n_heads * head_dim rounded up to 256; the O
  *              projection's input), or NULL
+ *              (the outputs and q may not overlap)
  *   workspace  rz_attention_paged_q4_workspace_bytes bytes, 16-byte aligned, zero-filled
  *              once after allocating it (a completed call leaves its counters zero; after
  *              RZ_ERR_TIMEOUT fill it with zeros again); calls that share it must not overlap on
  *              the GPU, captured ones among them
  * Scores and sums are f32-accurate: q and the weights enter as two f16 pieces each, the
- * codes exactly.  A length, row offset or page outside its range records RZ_ERR_DEVICE:
+ * codes exactly.  (Requests of more than 40 query rows for a kv head, at a head_dim of 64 or 128, are
+ * worked 128 tokens at a time, K and V as two f16 pieces each below the largest |d| of the 128:
+ * a value comes to within 2^-30 of that d.)  A length, row offset or page outside its range records RZ_ERR_DEVICE:
  * the request counts as empty (lengths beyond its table, bad row offsets), or its
  * rows are undefined (a bad page).  1 <= n_seqs <= 1024.
  */

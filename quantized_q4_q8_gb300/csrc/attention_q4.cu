@@ -987,7 +987,10 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
     // half an SM's shared memory (228 KB, 1 KB of it for each CTA), as many slots as fit
     const int most = 113 * 1024;
     const int fixed = L::fixed + a.n_seqs * 20 + 8;
-    const int slots = std::min(kMaxSlots, (most - fixed) / L::slot);
+    // A multiple of every number of copies (W, W / 2, 1), so that the unit that was in a slot before is one that the same
+    // warp has worked: it would take the phase before, whose copies may land later than others', for its own.
+    constexpr int step = L::W > 3 ? L::W / 2 * L::W : L::W;
+    const int slots = std::min(kMaxSlots, (most - fixed) / L::slot) / step * step;
     const int bytes = slots * L::slot + fixed;
     static std::atomic<uint64_t> done{0};  // devices on which the kernel may have that much
     const uint64_t bit = 1ull << (dev_info().device & 63);

@@ -499,6 +499,42 @@ def test_attention_many_requests(rz):
     s.check(s.run(rz).cpu().numpy())
 
 
+@pytest.mark.parametrize("hd", [128, 256])
+def test_attention_most_requests_of_wide_heads(rz, hd):
+    """1024 requests, whose rows of the plan take shared memory from the ring of units."""
+    rng = np.random.default_rng(hd)
+    reqs = [(int(n), 1) for n in rng.integers(1, 80, 1023)] + [(700, 3)]
+    s = Setup(hd, 2, 1, hd, 16, reqs)
+    s.check(s.run(rz).cpu().numpy())
+
+
+def test_attention_shared_pages(rz):
+    """A prefix whose pages stand in the rows of several requests; with row counts of every width of an item."""
+    H, K, hd, page = 8, 2, 64, 16
+    s = Setup(5, H, K, hd, page, [(333, 1), (1, 1), (1, 1), (1, 1)])
+    prefix = s.table[0, :20]
+    reqs, s.slots = [(333, 1), (322, 2), (336, 4), (330, 9)], [s.slots[0]]
+    for i in (1, 2, 3):
+        own = s.table[i, 0]
+        s.table[i, :20], s.table[i, 20] = prefix, own
+        n = reqs[i][0]
+        s.slots.append(s.table[i, np.arange(n) // page] * page + np.arange(n) % page)
+    # the requests' own last pages hold one token each so far: give them sixteen
+    rng = np.random.default_rng(6)
+    pages = s.kv.pages.shape[0]
+    k, v = s.kval.reshape(pages, page, K, hd).copy(), s.vval.reshape(pages, page, K, hd).copy()
+    for i in (1, 2, 3):
+        k[s.table[i, 20]], v[s.table[i, 20]] = rng.standard_normal((2, page, K, hd))
+    flat, s.kval, s.vval = R.pack(k.reshape(-1, K, hd), v.reshape(-1, K, hd), page)
+    s.kd, s.vd = (np.abs(x.reshape(-1, K, hd // 32, 32)).max(-1) / 7 for x in (s.kval, s.vval))
+    s.reqs, s.cu = reqs, np.concatenate([[0], np.cumsum([m for _, m in reqs])])
+    s.T = int(s.cu[-1])
+    s.q = rng.standard_normal((s.T, H * hd)).astype(np.float32)
+    s.qd, s.td, s.cud, s.lend = to_dev(s.q), ints(s.table), ints(s.cu), ints([n for n, _ in reqs])
+    s.kv = rz.PagedKVQ4(to_dev(flat.reshape(pages, K, -1)), page, hd)
+    s.check(s.run(rz).cpu().numpy())
+
+
 def test_attention_more_new_rows_than_held_tokens(rz):
     """Rows that see nothing come out as zeros, whatever their neighbours see."""
     s = Setup(6, 4, 2, 64, 16, [(3, 8), (0, 5), (20, 33)])
