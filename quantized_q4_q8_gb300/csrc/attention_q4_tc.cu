@@ -39,6 +39,11 @@
 // pairs: for K over the head's values (Q is laid out alike), for V over the tokens (so S's columns,
 // K's rows, are in that order too).
 //
+// Bound: a tile takes 3 + 3 products of 128 x 128 x hd.  1000 new rows beside 7 decodes over up to 4000 tokens, 32 heads on
+// 8 kv heads of 128: 225 us; 4000 new rows of 8000 tokens: 1100 us, 358 TFLOP/s of the formula's or 1070 of the tensor
+// cores', 57% of a large matrix product's rate.  The tensor pipe is busy 38% of the time at the first; the rest is waiting of
+// a tile's stages for one another (softmax of 128 x 128, unpacking, putting O aside) and the start and end of items.
+//
 // Work is shared among the CTAs (one for each SM) as in attention_q4.cu.  Every wait is
 // bounded; after one that runs out every role stops, copies and products in flight are waited
 // for, and tensor memory is freed.

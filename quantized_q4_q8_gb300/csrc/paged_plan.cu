@@ -15,6 +15,10 @@
 // nothing but one cluster barrier, between the reads of the state and its updates, joins
 // them, and each writes its share of the pages and rows.  A row whose page is new takes it from
 // the stack, not from the table, so it needs not wait for the table's update.
+//
+// Measured, in a graph whose empty kernels take 2.5 us each: 8 decodes 5.0 us; 1000 requests of up to 32768 tokens, 37
+// with 777 new ones and 90 that end, 12.3 us (its reads, two sums, a barrier, the stack's pages, the rows' table
+// entries: six dependent trips to L2).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -27,6 +31,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+// One CTA alone: 8 requests take as long, 64 with 500 rows 6.4 us (8 CTAs: 5.1), 500 with a row each 17 (6.9), 1000 with
+// 29 thousand rows 45 (12.3).
+constexpr int kCtas = 8;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = kPlanMaxSeqs / kThreads;  // requests of a thread: tid * kPer ..
@@ -69,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
     __shared__ int32_t last_cu, all_handed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const cg::cluster_group cluster = cg::this_cluster();
-    const int n_ctas = gridDim.x, cta = blockIdx.x;  // the grid is one cluster
+    const int n_ctas = kCtas, cta = blockIdx.x;  // the grid is one cluster
     pdl_launch_dependents();
     pdl_wait();
 
@@ -266,15 +273,13 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
 
 cudaError_t launch_paged_plan(const PlanArgs &a, cudaStream_t s)
 {
-    // one CTA until its share of the rows is over some rows for each thread
-    const int ctas = a.max_rows <= 4 * kThreads && a.n_seqs <= kThreads ? 1 : 8;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.gridDim = dim3(kCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.x = kCtas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
