@@ -35,7 +35,7 @@
 // a warp works both groups of 16 tokens of a unit at once.  A producer warp copies units into a ring
 // of slots with the bulk-copy engine, a lane for a unit.
 //
-// Bound: instructions.  32 tokens of a head of 128 take a warp some 770: 288 unpack codes, 112 split the weights, 32
+// Bound: instructions.  32 tokens of a head of 128 take a warp some 700: 288 unpack codes, 112 split the weights, 32
 // are products, 48 scale scores.  64 requests of 8192 tokens, 32 heads on 8 kv heads of 128: 140 us, 4.3 TB/s of the cache as it is
 // held or 64% of a copy's rate, the issue slots 53% full (12 warps an SM), the tensor cores 20%.  1 request of 1000
 // tokens: 10.6 us, of which 4 join the parts.

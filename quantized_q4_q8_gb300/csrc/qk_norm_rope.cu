@@ -30,7 +30,7 @@
 // heads in doubt takes 6.4 us instead of 5.7 and 50.3 instead of 52.7.  Queries are f32.
 //
 // Bound: 4096 tokens of 32 + 16 heads of 128 read and write 206 MB and take 50.3 us, 4.1 TB/s or 60% of a copy's
-// rate; the issue slots are 72% full (keys: 8 heads of 48 take 40% of the instructions).  Queries alone run at 6.7
+// rate; the issue slots are 75% full (keys: 8 heads of 48 take 40% of the instructions).  Queries alone run at 6.7
 // TB/s.  10 CTAs of 4 warps an SM (48 registers): 9 take 49.7 us there and 0.1 us more at 33 tokens, 12 (spills) 56.8,
 // 8 50.0.  Two rows ahead in flight instead of one: 53.3 against 52.7.  33 tokens of 32 + 64 heads: 5.7 us, latency.
 #include <math.h>
