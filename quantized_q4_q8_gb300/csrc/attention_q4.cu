@@ -707,13 +707,13 @@ __device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, cons
 
 template <int NB>
 __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
-    paged_attention_kernel(const __grid_constant__ PagedAttnArgs a, int slots)
+    paged_attention_kernel(const __grid_constant__ PagedAttnArgs a, int most_slots)
 {
     using L = Layout<NB>;
     constexpr int W = L::W, hd = L::hd, ld = hd + kPad, kSlot = L::slot;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem;
-    uint4 *queries = reinterpret_cast<uint4 *>(ring + (size_t)slots * kSlot);
+    uint4 *queries = reinterpret_cast<uint4 *>(ring + (size_t)most_slots * kSlot);
     float *sums = reinterpret_cast<float *>(queries + L::queries / 16);
     float2 *ml = reinterpret_cast<float2 *>(sums + L::sums / 4);
     uint64_t *full = reinterpret_cast<uint64_t *>(ml + L::rows), *empty = full + kMaxSlots;
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = a.kv.n_kv_heads, group = a.n_heads / K;
     if (tid == 0) {
-        for (int i = 0; i < slots; ++i) {
+        for (int i = 0; i < most_slots; ++i) {
             mbar_init(full + i, 1);
             mbar_init(empty + i, W);
         }
@@ -740,6 +740,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
     pdl_wait();
 
     // ---- the line: what comes before each request
+    bool halves = false;  // items of two row groups, W / 2 copies of each
     {
         int64_t *tmp = reinterpret_cast<int64_t *>(sums);
         const int per = (a.n_seqs + W * 32 - 1) / (W * 32);
@@ -749,6 +750,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
             for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
                 seqs[i] = read_seq(a, i, bad);
                 const Seq q = make_seq<W>(seqs[i], group);
+                halves |= W > 3 && q.rg == 2 && q.items > 0;
                 int64_t span = 0;
                 for (int it = 0; it < q.items; ++it) span += item_span<W>(q, group, it);
                 pre[i + 1] = span * K;
@@ -762,7 +764,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
             if (lane >= o) v += u;
         }
         if (lane == 31) tmp[warp] = v;
-        __syncthreads();
+        halves = __syncthreads_or(halves);
         if (tid < W * 32) {
             for (int k = 0; k < warp; ++k) v += tmp[k];
             v -= mine;
@@ -775,6 +777,9 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
         __syncthreads();
     }
 
+    // A multiple of every number of copies that there is (W, W / 2, 1), so that the unit that was in a slot before is one
+    // that the same warp has worked: it would take the phase before, whose copies may land later than others', for its own.
+    const int step = halves ? W / 2 * W : W, slots = most_slots / step * step;
     volatile int *gave_up = flags;
     Walk w;
     const Line line = make_line<W>(pre[a.n_seqs], gridDim.x);
@@ -990,12 +995,10 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
 {
     using L = Layout<NB>;
     // half an SM's shared memory (228 KB, 1 KB of it for each CTA), as many slots as fit
-    const int most = 113 * 1024;
+    constexpr int most = 113 * 1024;
+    static_assert((most - L::fixed - kPagedMaxSeqs * 20 - 8) / L::slot >= (L::W > 3 ? L::W / 2 * L::W : L::W), "a ring for any number of requests");
     const int fixed = L::fixed + a.n_seqs * 20 + 8;
-    // A multiple of every number of copies (W, W / 2, 1), so that the unit that was in a slot before is one that the same
-    // warp has worked: it would take the phase before, whose copies may land later than others', for its own.
-    constexpr int step = L::W > 3 ? L::W / 2 * L::W : L::W;
-    const int slots = std::min(kMaxSlots, (most - fixed) / L::slot) / step * step;
+    const int slots = std::min(kMaxSlots, (most - fixed) / L::slot);
     const int bytes = slots * L::slot + fixed;
     static std::atomic<uint64_t> done{0};  // devices on which the kernel may have that much
     const uint64_t bit = 1ull << (dev_info().device & 63);
