@@ -633,8 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             *reinterpret_cast<uint2 *>(p + piece) = make_uint2(hfms2u(c0, d0, h0), hfms2u(c1, d1, h1));
         };
         // The scales of tile j, a token a thread, times 2^up: the tile's largest of K and of V to
-        // 2^8 .. 2^9 (none but zeros: as they are).  V's last for 3 tiles: K(j) is copied after V(j - 2), which
-        // is once V(j - 3) is unpacked.
+        // 2^8 .. 2^9.  A tile without a value but zeros counts as one of the smallest f16: its exponent enters the rows'
+        // maxima, and may not lift them over those of tiles that have values.  V's last for 3 tiles: K(j) is copied after
+        // V(j - 2), which is once V(j - 3) is unpacked.
         auto scales = [&](int j, int valid) {
             if (!wait_for(&b.raw_k_full[j & 1], (j >> 1) & 1, b, a.err)) return false;
             const uint8_t *raw = sm + L::off_raw_k + (j & 1) * L::raw_k + (tok128 >> 4) * 10 * hd + 8 * hd;
@@ -664,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 const uint32_t top = max(max(b.warp_max[v][0], b.warp_max[v][1]), max(b.warp_max[v][2], b.warp_max[v][3]));
-                const int up = top ? kScaleTop + 127 - (__float_as_int(h2f((uint16_t)top)) >> 23) : 0;
+                const int up = kScaleTop + 127 - (__float_as_int(h2f((uint16_t)max(top, 1u))) >> 23);
                 if (tok128 == 0) b.exps[j & 3][v] = up;
                 uint16_t *dst = (v ? sv + (j % 3) * kTile * NB : sk) + tok128 * NB;
 #pragma unroll

@@ -1,0 +1,45 @@
+"""The paged 4-bit KV cache on the GPU at its edges: values of no size beside small ones, numbers that are none in one
+block of a head, scales that underflow, state carried from step to step on the device."""
+import numpy as np
+import pytest
+
+import paged_reference as R
+from gpu_common import check_no_device_error, to_dev
+from test_gpu_paged import Setup, device_error, ints, no_error_left, rz  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def with_cache(s, k=None, v=None):
+    """The setup over other keys and values ([slots, K, hd]; the format's own rounding applies to them)."""
+    import quantized_q4_q8_gb300 as rz
+    with np.errstate(all="ignore"):
+        flat, s.kval, s.vval = R.pack(s.kval.astype(np.float64) if k is None else k, s.vval.astype(np.float64) if v is None else v, s.page)
+    s.kd, s.vd = (np.abs(x.reshape(-1, s.K, s.hd // 32, 32)).max(-1) / 7 for x in (s.kval, s.vval))
+    s.kv = rz.PagedKVQ4(to_dev(flat.reshape(s.kv.pages.shape)), s.page, s.hd)
+    return s
+
+
+# ------------------------------------------------------------------ values of no size
+@pytest.mark.parametrize("size", [1e-2, 1e-4, 3e-6])
+@pytest.mark.parametrize("hd,H,K,reqs", [
+    (128, 32, 8, [(1000, 1000)]),          # whole items within a CTA's share
+    (128, 4, 2, [(2900, 300)]),            # items in parts of a tile or two
+    (64, 8, 1, [(897, 130), (300, 1)]),
+    (64, 14, 2, [(700, 20), (650, 1)]),
+])
+@pytest.mark.parametrize("zero", ["first", "middle", "last", "all"])
+def test_attention_tiles_of_zero_values(rz, size, hd, H, K, reqs, zero):
+    """Tokens whose values are all zeros say nothing, so they may not set what the others' weights are measured by.
+    (The bound is that of Setup.check: relative to the sums of |d| that the row sees, and 1e-5 of all outputs.)"""
+    s = Setup(hd + H, H, K, hd, 64, reqs)
+    v = s.vval.astype(np.float64) * size
+    for (n, _), slots in zip(reqs, s.slots):
+        last = (n - 1) // 128 * 128
+        tiles = {"first": [(0, 128)], "middle": [(256, 384), (512, 640)], "last": [(last, n)], "all": [(0, n)]}[zero]
+        for a, b in tiles:
+            v[slots[a:min(b, n)]] = 0.0
+    with_cache(s, v=v)
+    out = s.run(rz).cpu().numpy()
+    s.check(out)
+    assert zero != "all" or not out.any()
