@@ -98,7 +98,7 @@ struct Bars {
     uint32_t tmem;
     int gave_up, last;      // a wait ran out; this CTA adds the parts up
     int exps[4][2];         // of tiles i mod 4: K's and V's exponents
-    uint32_t nan_v[4][4];   // their tokens with a NaN or infinite V scale, by position
+    uint32_t nan_v[4][4];   // of 32 tokens of theirs: byte e is the first with a V scale of block e that is no number (255: none)
     uint32_t warp_max[2][4];
     int parts, first_part;
 };
@@ -640,8 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             if (!wait_for(&b.raw_k_full[j & 1], (j >> 1) & 1, b, a.err)) return false;
             const uint8_t *raw = sm + L::off_raw_k + (j & 1) * L::raw_k + (tok128 >> 4) * 10 * hd + 8 * hd;
             uint16_t d[2][NB];
-            uint32_t most[2] = {0, 0};
-            bool bad = false;
+            uint32_t most[2] = {0, 0}, firsts = 0xffffffffu;
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 const uint16_t *src = reinterpret_cast<const uint16_t *>(raw + v * hd) + (tok128 & 15) * NB;
@@ -650,16 +649,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     d[v][e] = tok128 < valid ? src[e] : uint16_t(0);
                     const uint32_t abs = d[v][e] & 0x7fffu;
                     if (abs < 0x7c00u) most[v] = max(most[v], abs);
-                    else if (v) bad = true;
+                    if (v) {
+                        const unsigned bads = __ballot_sync(0xffffffffu, abs >= 0x7c00u);
+                        if (bads) firsts = (firsts & ~(255u << (8 * e))) | (uint32_t)(__ffs(bads) - 1) << (8 * e);
+                    }
                 }
                 most[v] = __reduce_max_sync(0xffffffffu, most[v]);
             }
-            const unsigned bads = __ballot_sync(0xffffffffu, bad);
             if (lane == 0) {
                 b.warp_max[0][w4] = most[0];
                 b.warp_max[1][w4] = most[1];
-                // by position: bits 1 and 2 of every 4 change places
-                b.nan_v[j & 3][w4] = (bads & 0x99999999u) | ((bads & 0x22222222u) << 1) | ((bads & 0x44444444u) >> 1);
+                b.nan_v[j & 3][w4] = firsts;
             }
             if (!sync_warps(&b.k_sync, phase, b, a.err)) return false;
 #pragma unroll
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 uint16_t *dst = (v ? sv + (j % 3) * kTile * NB : sk) + tok128 * NB;
 #pragma unroll
                 for (int e = 0; e < NB; ++e) {
-                    // a V scale that is no number: nothing is added, and the row's sum is made NaN
+                    // a V scale that is no number: nothing is added, and the block's values of the rows that see it are made NaN
                     const bool drop = v && (d[v][e] & 0x7fffu) >= 0x7c00u;
                     dst[e] = drop ? uint16_t(0) : __half_as_ushort(__float2half_rn(h2f(d[v][e]) * power2(up)));
                 }
@@ -775,13 +775,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         volatile float *maxima = reinterpret_cast<float *>(sm + L::off_row) + r;
         // this row's sums of the periods before: 4 values of all rows after another
         float *kept = a.kept + (int64_t)blockIdx.x * kRows * hd + 4 * r;
-        // what the row's other thread gives for v
+        // what the row's other thread gives for v, and both threads' bits (in the place of the maximum of the tile before
+        // the last, which both have done with)
         unsigned pair_phase = 0;
-        auto exchange = [&](float v, float &got) {
+        auto exchange = [&](float v, float &got, unsigned &bits) {
             volatile float *at = maxima + 2 * kRows;
+            volatile uint16_t *two = reinterpret_cast<volatile uint16_t *>(maxima + (i & 1) * kRows);
             at[half * kRows] = v;
+            two[half] = static_cast<uint16_t>(bits);
             bool fine = sync_warps(&b.pair[warp & 3], pair_phase, b, a.err);
             got = at[(half ^ 1) * kRows];
+            bits |= two[half ^ 1];
             return sync_warps(&b.pair[warp & 3], pair_phase, b, a.err) && fine;  // read, before it is written again
         };
         unsigned phase = 0;
@@ -799,6 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             const int64_t row = w.row0 + tok_q;
             const int col0 = (w.h * group + (min(my, n_rows - 1) - tok_q * group)) * hd;
             float unit = 0.0f, m = -1e37f, l = 0.0f;
+            unsigned nan_blocks = 0;  // the blocks of this row's values that are NaN
             if (w.lo < w.hi) {
                 // ---- Q's pieces (both threads look for the largest, each writes half).  The products of the
                 // item before that read them are done: their S was waited for.
@@ -920,12 +925,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                         tm_store16(tmem + lanes + kColO + c, o);
                     }
                 }
-                // a NaN or infinite V scale that this row sees makes its sum NaN
-                float add = 0.0f;
-                if (b.nan_v[i & 3][0] | b.nan_v[i & 3][1] | b.nan_v[i & 3][2] | b.nan_v[i & 3][3]) {
+                // blocks of which this row sees a V scale that is no number
+                if ((b.nan_v[i & 3][0] & b.nan_v[i & 3][1] & b.nan_v[i & 3][2] & b.nan_v[i & 3][3]) != 0xffffffffu) {
 #pragma unroll 1
-                    for (int c = 0; c < kTile; ++c)
-                        if ((b.nan_v[i & 3][c >> 5] >> (c & 31) & 1) && swapped(c) < left) add = __int_as_float(0x7fffffff);
+                    for (int c = 0; c < 4 * NB; ++c) {
+                        const int tok = b.nan_v[i & 3][c / NB] >> (8 * (c % NB)) & 255;
+                        if (tok < 32 && 32 * (c / NB) + tok < left) nan_blocks |= 1u << (c % NB);
+                    }
                 }
                 const float off = sub + (kBias - m);
                 float sum = 0.0f, sum2 = 0.0f;
@@ -951,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                     tm_store16(at + c, hi);  // in the place of the scores that were read
                     tm_store16(at + c + 16, lo);
                 }
-                l = fmaf(sum + sum2, power2(b.exps[i & 3][1]), l) + add;
+                l = fmaf(sum + sum2, power2(b.exps[i & 3][1]), l);
                 tm_store_wait();
                 fence_before();
                 __syncwarp();
@@ -966,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 m = last_m;
             }
             float l2;
-            if (!(ok = exchange(l, l2))) break;
+            if (!(ok = exchange(l, l2, nan_blocks))) break;
             const bool more_sums = w.hi - w.lo > kPeriod;
             const float kept_ref = more_sums ? maxima[4 * kRows] : -INFINITY;
             const float kept_f = kept_ref == -INFINITY ? 0.0f : ex2f(kept_ref - m);
@@ -1003,6 +1009,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                }
+                if (nan_blocks >> (c >> 5) & 1) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __int_as_float(0x7fffffff);
                 }
                 if (whole) {
 #pragma unroll

@@ -43,3 +43,24 @@ def test_attention_tiles_of_zero_values(rz, size, hd, H, K, reqs, zero):
     out = s.run(rz).cpu().numpy()
     s.check(out)
     assert zero != "all" or not out.any()
+
+
+# ------------------------------------------------------------------ no number in one block
+@pytest.mark.parametrize("hd,H,K,reqs", [(128, 4, 2, [(500, 200), (60, 1)]), (64, 4, 2, [(500, 200), (60, 1)]),
+                                         (128, 32, 8, [(900, 900)]), (128, 4, 2, [(500, 3), (60, 1)]), (96, 4, 2, [(500, 60)])])
+def test_attention_no_number_in_one_block_of_a_value(rz, hd, H, K, reqs):
+    """A block of 32 values whose scale is NaN reaches those 32 values of the rows that see it, and no others."""
+    import torch
+    s = Setup(17 + hd, H, K, hd, 16, reqs)
+    good = s.run(rz).clone()
+    n, m = reqs[0]
+    G, nb = H // K, hd // 32
+    seen = torch.zeros_like(good, dtype=torch.bool)
+    for token, head, block in ((n - m // 2, 1, nb - 1), (n - 1, 0, 0), (n - m + 1, K - 1, 1)):
+        at = R.record_of(16, K, hd, int(s.slots[0][token]), head) + 17 * hd + (token % 16) * 2 * nb + 2 * block
+        s.kv.pages.view(-1)[at:at + 2] = torch.tensor([0, 0x7e], dtype=torch.uint8, device="cuda")
+        for h in range(head * G, (head + 1) * G):
+            seen[token - (n - m):m, h * hd + 32 * block:h * hd + 32 * block + 32] = True
+    out = s.run(rz)
+    assert torch.equal(out[~seen], good[~seen])
+    assert torch.isnan(out[seen]).all()
