@@ -841,6 +841,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 if ((i & 1) != half) continue;
                 if (!(ok = wait_for(&b.s_full[third], (i / 3) & 1, b, a.err))) break;
                 fence_after();
+                // blocks of which this row sees a V scale that is no number
+                if ((b.nan_v[i & 3][0] & b.nan_v[i & 3][1] & b.nan_v[i & 3][2] & b.nan_v[i & 3][3]) != 0xffffffffu) {
+#pragma unroll 1
+                    for (int c = 0; c < 4 * NB; ++c) {
+                        const int tok = b.nan_v[i & 3][c / NB] >> (8 * (c % NB)) & 255;
+                        if (tok < 32 && 32 * (c / NB) + tok < sees - tile * kTile) nan_blocks |= 1u << (c % NB);
+                    }
+                }
                 const float u = unit * power2(-b.exps[i & 3][0]), sub = static_cast<float>(-b.exps[i & 3][1]);
                 // The scores are read twice, 32 at a time in loops that are not unrolled, and not kept: code for
                 // all values at once, of 8 warps beside 8 others with code of their own, waits for its instructions.
@@ -923,14 +931,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                         tm_store16(tmem + lanes + kColO + c, o);
-                    }
-                }
-                // blocks of which this row sees a V scale that is no number
-                if ((b.nan_v[i & 3][0] & b.nan_v[i & 3][1] & b.nan_v[i & 3][2] & b.nan_v[i & 3][3]) != 0xffffffffu) {
-#pragma unroll 1
-                    for (int c = 0; c < 4 * NB; ++c) {
-                        const int tok = b.nan_v[i & 3][c / NB] >> (8 * (c % NB)) & 255;
-                        if (tok < 32 && 32 * (c / NB) + tok < left) nan_blocks |= 1u << (c % NB);
                     }
                 }
                 const float off = sub + (kBias - m);
