@@ -64,3 +64,20 @@ def test_attention_no_number_in_one_block_of_a_value(rz, hd, H, K, reqs):
     out = s.run(rz)
     assert torch.equal(out[~seen], good[~seen])
     assert torch.isnan(out[seen]).all()
+
+
+# ------------------------------------------------------------------ scales that underflow
+@pytest.mark.parametrize("hd,H,K", [(64, 4, 2), (128, 4, 1), (96, 4, 2)])
+@pytest.mark.parametrize("scale", [1e-44, 1e-38])
+def test_attention_scale_of_next_to_nothing(rz, hd, H, K, scale):
+    """All tokens that a row sees count alike, those that it does not see for nothing."""
+    s = Setup(21, H, K, hd, 16, [(77, 5), (200, 100), (9, 1), (3, 6)])
+    s.check(s.run(rz, scale=scale).cpu().numpy(), scale=scale)
+
+
+@pytest.mark.parametrize("hd,H,K", [(64, 4, 2), (128, 4, 1)])
+def test_attention_queries_and_keys_of_next_to_nothing(rz, hd, H, K):
+    s = Setup(22, H, K, hd, 16, [(77, 5), (200, 100), (9, 1)], sharp=1e-6)
+    s.q = (s.q * np.float32(1e-39)).astype(np.float32)
+    s.qd = to_dev(s.q)
+    s.check(s.run(rz).cpu().numpy())
