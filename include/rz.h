@@ -538,8 +538,8 @@ rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t 
  * codes exactly.  (Requests of more than 40 query rows for a kv head, at a head_dim of 64 or 128, are
  * worked 128 tokens at a time, K and V as two f16 pieces each below the largest |d| of the 128:
  * a value comes to within 2^-30 of that d.)  A length, row offset or page outside its range records RZ_ERR_DEVICE:
- * the request counts as empty (lengths beyond its table, bad row offsets), or its
- * rows are undefined (a bad page).  1 <= n_seqs <= 1024.
+ * a request of a length below 0 or beyond its table holds no token (zeros), one of bad row offsets has
+ * no rows (its outputs stay as they were), and one of a bad page has rows that are undefined.  1 <= n_seqs <= 1024.
  */
 size_t rz_attention_paged_q4_workspace_bytes(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
 rz_status rz_attention_paged_q4(const float *q, int64_t ld_q, int64_t n_rows, const rz_kv_q4 *kv,

@@ -130,7 +130,7 @@ __device__ __forceinline__ SeqRow read_seq(const PagedAttnArgs &a, int s, bool &
     const int c0 = a.cu_rows[s], c1 = a.cu_rows[s + 1], n = a.kv_len[s];
     const int64_t most = (int64_t)a.max_blocks << (a.kv.page_log + 4);
     const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.n_rows;
-    if (!ok || n > most) bad = true;
+    if (!ok || n < 0 || n > most) bad = true;
     // one with many rows has none here: attention_q4_tc.cu works it
     const bool here = ok && (c1 - c0) * (a.n_heads / a.kv.n_kv_heads) <= a.most_rows;
     return SeqRow{here ? c0 : 0, here ? c1 - c0 : 0, n > most ? 0 : max(n, 0)};
@@ -369,8 +369,9 @@ __device__ __forceinline__ void load_query(Warp<NB, NT> &w, uint4 *q_shared, con
             if (NT == 1) w.q[b] = v;
             else q_shared[(j * NB + b) * 32] = v;
         }
-        // the unit of query t is with lane g = 2 t
-        w.unit[j] = scale * 1.4426950408889634f * __int_as_float((127 - __shfl_sync(0xffffffffu, up, 8 * t)) << 23);
+        // the unit of query t is with lane g = 2 t.  2^-126 at least (scores are below 2^42: the exponents are 0 all the
+        // same): a masked score, -infinity, times 0 would be NaN
+        w.unit[j] = fmaxf(scale * 1.4426950408889634f * __int_as_float((127 - __shfl_sync(0xffffffffu, up, 8 * t)) << 23), 0x1p-126f);
         w.m[j] = -1e37f;
         w.l[j] = 0.0f;
     }

@@ -849,7 +849,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                         if (tok < 32 && 32 * (c / NB) + tok < sees - tile * kTile) nan_blocks |= 1u << (c % NB);
                     }
                 }
-                const float u = unit * power2(-b.exps[i & 3][0]), sub = static_cast<float>(-b.exps[i & 3][1]);
+                // (u of a normal f32 at least: a masked score, -infinity, times 0 would be NaN)
+                const float u = fmaxf(unit * power2(-b.exps[i & 3][0]), 0x1p-126f), sub = static_cast<float>(-b.exps[i & 3][1]);
                 // The scores are read twice, 32 at a time in loops that are not unrolled, and not kept: code for
                 // all values at once, of 8 warps beside 8 others with code of their own, waits for its instructions.
                 const uint32_t at = tmem + lanes + s_column(third);

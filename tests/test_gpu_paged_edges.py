@@ -81,3 +81,19 @@ def test_attention_queries_and_keys_of_next_to_nothing(rz, hd, H, K):
     s.q = (s.q * np.float32(1e-39)).astype(np.float32)
     s.qd = to_dev(s.q)
     s.check(s.run(rz).cpu().numpy())
+
+
+# ------------------------------------------------------------------ bad lengths
+@pytest.mark.parametrize("m", [1, 3, 60])
+@pytest.mark.parametrize("length", [-1, -(2 ** 31)])
+def test_attention_negative_length_is_reported(rz, m, length):
+    """It counts as empty, as one beyond the table does; the others by the usual bound."""
+    import torch
+    s = Setup(15, 4, 2, 64, 16, [(50, 1), (80, m), (70, 2)])
+    s.lend[1] = length
+    out = torch.full((s.T, 256), 2.5, device="cuda")
+    s.run(rz, out=out)
+    assert device_error(rz) == 0x203
+    assert not out[1:1 + m].any()
+    s.reqs[1] = (0, m)
+    s.check(out.cpu().numpy())
