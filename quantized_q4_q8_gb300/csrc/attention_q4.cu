@@ -327,7 +327,8 @@ __device__ __forceinline__ void flush(Warp<NB, NT> &w, int g)
 }
 
 // The queries in fragment order: this lane holds, for tile j, values 4 t .. 4 t + 3 (of both
-// halves of each block) of query 4 j + g / 2 at ptr[j], its high piece (g even) or its low one.
+// halves of each block) of query 4 j + g / 2 at ptr[j], its high piece (g even) or its low one.  (Plain loads: the
+// launch before may write q while this kernel is resident already, which the read-only path does not allow for.)
 template <int NB, int NT>
 __device__ __forceinline__ void load_query(Warp<NB, NT> &w, uint4 *q_shared, const float *const (&ptr)[NT], float scale, int g,
                                            int t)
@@ -340,7 +341,7 @@ __device__ __forceinline__ void load_query(Warp<NB, NT> &w, uint4 *q_shared, con
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                v[b][hf] = ptr[j] ? __ldg(reinterpret_cast<const float4 *>(ptr[j] + 32 * b + 16 * hf + 4 * t))
+                v[b][hf] = ptr[j] ? *reinterpret_cast<const float4 *>(ptr[j] + 32 * b + 16 * hf + 4 * t)
                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v[b][hf].x), fabsf(v[b][hf].y)),
                                      fmaxf(fabsf(v[b][hf].z), fabsf(v[b][hf].w))));

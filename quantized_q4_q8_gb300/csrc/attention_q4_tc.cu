@@ -805,13 +805,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
             float unit = 0.0f, m = -1e37f, l = 0.0f;
             unsigned nan_blocks = 0;  // the blocks of this row's values that are NaN
             if (w.lo < w.hi) {
-                // ---- Q's pieces (both threads look for the largest, each writes half).  The products of the
+                // ---- Q's pieces (both threads look for the largest, each writes half; plain loads, as in attention_q4.cu).  The products of the
                 // item before that read them are done: their S was waited for.
                 const float4 *src = reinterpret_cast<const float4 *>(a.q + row * a.ld_q + col0);
                 float mx = 0.0f;
 #pragma unroll 8
                 for (int k = 0; k < hd / 4; ++k) {
-                    const float4 v = __ldg(src + k);
+                    const float4 v = src[k];
                     mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
                 }
                 const int up = mx == 0.0f || !live ? 0 : min(14 - ((__float_as_int(mx) >> 23) - 127), 126);
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 uint8_t *dst = sm + L::off_q + (r >> 3) * (hd * 16) + (r & 7) * 16;
 #pragma unroll 4
                 for (int k = half * (hd / 16); k < (half + 1) * (hd / 16); ++k) {
-                    const float4 x = __ldg(src + 2 * k), y = __ldg(src + 2 * k + 1);
+                    const float4 x = src[2 * k], y = src[2 * k + 1];
                     const float f[8] = {x.x, x.z, x.y, x.w, y.x, y.z, y.y, y.w};
                     uint32_t hi[4], lo[4];
 #pragma unroll

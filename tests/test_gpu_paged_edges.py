@@ -97,3 +97,33 @@ def test_attention_negative_length_is_reported(rz, m, length):
     assert not out[1:1 + m].any()
     s.reqs[1] = (0, m)
     s.check(out.cpu().numpy())
+
+
+# ------------------------------------------------------------------ launches that overlap
+def test_steps_one_after_another_read_what_the_last_wrote(rz):
+    """Norm + rotation into the same rows of q, then attention, many times without a wait, a long request among the
+    requests (a launch becomes resident while the ones before still run): each step's outputs as with every launch
+    waiting for the whole one before."""
+    import torch
+    H, K, hd, page, steps = 8, 2, 128, 64, 24
+    s = Setup(33, H, K, hd, page, [(30000, 1), (70, 2), (900, 60), (10, 1)])
+    rng = np.random.default_rng(1)
+    x = to_dev(rng.standard_normal((steps, s.T, (H + K) * hd)).astype(np.float32))
+    pos = ints(rng.integers(0, 4096, s.T))
+    q_out = torch.zeros(s.T, H * hd, device="cuda")
+
+    def run():
+        outs = []
+        for i in range(steps):
+            rz.qk_norm_rope(x[i, :, :H * hd], x[i, :, H * hd:], None, pos, H, K, hd, 1e4, 1, q_out=q_out)
+            outs.append(rz.attention_paged_q4(q_out, s.kv, s.td, s.cud, s.lend, H, ws=s.ws))
+        return torch.stack(outs)
+
+    got = [run() for _ in range(4)]
+    rz.set_pdl(False)
+    try:
+        want = run()
+    finally:
+        rz.set_pdl(True)
+    for g in got:
+        assert torch.equal(g, want)
