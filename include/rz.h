@@ -496,7 +496,7 @@ rz_status rz_paged_plan(const int32_t *cached, const int32_t *fresh, int32_t n_s
  * [head_dim], each NULL for none), rotation by the row's position (angles, theta and
  * rope_mode as rz_layer_weights), and the append of k and v to the cache at the row's slot.
  *   q, k, v    f32 rows of n_heads, n_kv_heads, n_kv_heads heads, row strides ld_*
- *              (parts of one fused Q|K|V output, say); 4-byte aligned
+ *              (parts of one fused Q|K|V output, say); 4-byte aligned; n_heads <= 65536, n_kv_heads <= 1024
  *   positions  int32 [n_rows]; a negative one marks a padding row, whose outputs and
  *              cache stay as they are
  *   slots      int64 [n_rows]; negative: the row is not appended.  A slot beyond the cache
@@ -519,7 +519,7 @@ rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t 
  * rz_attention_paged_q4 -- softmax(scale * q k^T) v of each request's new rows over its
  * pages: row r of request i (r = 0 .. m - 1, m = cu_rows[i + 1] - cu_rows[i]) sees its first
  * kv_len[i] - m + r + 1 tokens (the new ones are in the cache already); a row that sees
- * none comes out as zeros.  Query head h reads kv head h / (n_heads / n_kv_heads).
+ * none comes out as zeros.  Query head h reads kv head h / (n_heads / n_kv_heads); n_heads <= 65536.
  *   q          f32 [n_rows] rows of n_heads * head_dim, stride ld_q (a multiple of 4),
  *              16-byte aligned, |q| < 1e35; rows behind cu_rows[n_seqs] are not read and their outputs not
  *              written

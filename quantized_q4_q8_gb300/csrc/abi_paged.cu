@@ -45,6 +45,7 @@ rz_status launched(const char *fn, cudaError_t e)
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;  // of one request
 constexpr int64_t kMaxInt = 2147483647;
+constexpr int kMaxHeads = 65536;  // a row's values are counted in 32 bits
 
 int page_log(int page_size)
 {
@@ -171,7 +172,7 @@ rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t 
     if (!aligned(slots, 8)) return fail(RZ_ERR_ALIGN, "%s: slots must be 8-byte aligned", fn);
     if (n_rows < 1 || n_rows > kMaxInt) return fail(RZ_ERR_INVALID_ARG, "%s: n_rows=%lld", fn, (long long)n_rows);
     RZ_TRY(check_head_dim(fn, head_dim));
-    if (n_heads < 1 || n_kv_heads < 1 || n_kv_heads > 1024 || n_heads > 65536)
+    if (n_heads < 1 || n_kv_heads < 1 || n_kv_heads > 1024 || n_heads > kMaxHeads)
         return fail(RZ_ERR_SHAPE, "%s: n_heads=%d n_kv_heads=%d", fn, n_heads, n_kv_heads);
     if (rope_mode != 0 && rope_mode != 1) return fail(RZ_ERR_INVALID_ARG, "%s: rope_mode", fn);
     if (!(rope_theta > 0.0f) || std::isinf(rope_theta)) return fail(RZ_ERR_INVALID_ARG, "%s: rope_theta", fn);
@@ -215,7 +216,7 @@ size_t rz_attention_paged_q4_workspace_bytes(int32_t n_heads, int32_t n_kv_heads
     const char *fn = "rz_attention_paged_q4_workspace_bytes";
     record_error(RZ_OK, "");
     if (check_head_dim(fn, head_dim) != RZ_OK) return 0;
-    if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads) {
+    if (n_heads < 1 || n_heads > kMaxHeads || n_kv_heads < 1 || n_kv_heads > 1024 || n_heads % n_kv_heads) {
         fail(RZ_ERR_SHAPE, "%s: n_heads=%d n_kv_heads=%d", fn, n_heads, n_kv_heads);
         return 0;
     }
@@ -236,7 +237,7 @@ rz_status rz_attention_paged_q4(const float *q, int64_t ld_q, int64_t n_rows, co
     RZ_TRY(check_kv_q4(fn, kv, &pk));
     RZ_TRY(check_blocks(fn, max_blocks, ld_table, kv->page_size));
     if (n_seqs < 1 || n_seqs > kPagedMaxSeqs) return fail(RZ_ERR_SHAPE, "%s: n_seqs=%d outside [1, %d]", fn, n_seqs, kPagedMaxSeqs);
-    if (n_heads < 1 || n_heads % pk.n_kv_heads)
+    if (n_heads < 1 || n_heads > kMaxHeads || n_heads % pk.n_kv_heads)
         return fail(RZ_ERR_SHAPE, "%s: n_heads=%d with n_kv_heads=%d", fn, n_heads, pk.n_kv_heads);
     if (n_rows < 1) return fail(RZ_ERR_INVALID_ARG, "%s: n_rows=%lld", fn, (long long)n_rows);
     if (n_rows > kMaxInt || n_rows * (n_heads / pk.n_kv_heads) > kMaxTokens)
