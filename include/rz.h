@@ -472,7 +472,9 @@ size_t rz_kv_q4_page_bytes(int32_t page_size, int32_t n_kv_heads, int32_t head_d
  * Outputs:
  *   cu_rows   int32 [n_seqs + 1]  rows of request i: cu_rows[i] .. cu_rows[i + 1]
  *   kv_len    int32 [n_seqs]      cached + fresh; 0 for ended and refused requests (not
- *             the buffer of cached or fresh).  The next step's cached.
+ *             the buffer of cached or fresh).  What rz_attention_paged_q4 takes.  The next step's cached
+ *             it is for served requests only: a refused one still holds its cached tokens, so a caller that
+ *             carries lengths on the device takes fresh < 0 ? 0 : kv_len > 0 ? kv_len : cached.
  *   row_seq, positions int32 [max_rows], slots int64 [max_rows]: the request, position and
  *             cache slot of each row; -1 in the rows behind the last and, but for
  *             row_seq, in those of a refused request

@@ -579,6 +579,15 @@ class PagedPlan:
         self.positions = torch.full((max_rows,), -1, dtype=torch.int32, device=device)
         self.slots = torch.full((max_rows,), -1, dtype=torch.int64, device=device)
 
+    def next_cached(self, cached, fresh, out=None):
+        """The tokens that each request holds after the step whose plan this is, from the step's cached and
+        fresh: the next step's cached.  kv_len for served requests; a refused one keeps its cached tokens (its
+        kv_len is 0, so that attention passes over it), an ended one has none.  Into `out` (which may be
+        cached) if given; on the current stream."""
+        import torch
+        new = torch.where(self.kv_len > 0, self.kv_len, cached).masked_fill_(fresh < 0, 0)
+        return new if out is None else out.copy_(new)
+
 
 def rz_paged_plan(cached, fresh, n_seqs, owned, owned_out, free_count, free_count_out, free_pages, n_pages, block_table,
                   ld_table, max_blocks, page_size, max_rows, cu_rows, kv_len, row_seq, positions, slots, stream=None):

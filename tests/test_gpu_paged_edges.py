@@ -5,7 +5,7 @@ import pytest
 
 import paged_reference as R
 from gpu_common import check_no_device_error, to_dev
-from test_gpu_paged import Setup, device_error, ints, no_error_left, rz  # noqa: F401
+from test_gpu_paged import Setup, device_error, ints, no_error_left, rz, want_heads  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,66 @@ def test_steps_one_after_another_read_what_the_last_wrote(rz):
         rz.set_pdl(True)
     for g in got:
         assert torch.equal(g, want)
+
+
+# ------------------------------------------------------------------ lengths carried on the device
+def test_state_carried_on_the_device_over_a_refused_step(rz):
+    """One captured graph of plan -> norm, rotation, append -> attention -> next lengths, run until the pool is empty
+    and on when there are pages again: the refused request keeps its tokens and goes on where it was."""
+    import torch
+    rng = np.random.default_rng(3)
+    n, H, K, hd, page, max_rows, n_pages = 3, 4, 2, 64, 16, 32, 5
+    kv = rz.PagedKVQ4(torch.zeros((n_pages, K, page * hd * 9 // 8), dtype=torch.uint8, device="cuda"), page, hd)
+    table = torch.full((n, 4), -1, dtype=torch.int32, device="cuda")
+    owned, count = torch.zeros(n, dtype=torch.int32, device="cuda"), ints([n_pages])
+    free = torch.arange(n_pages, dtype=torch.int32, device="cuda")
+    cached, fresh = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    plan = rz.PagedPlan(n, max_rows)
+    qkv = torch.zeros(max_rows, (H + 2 * K) * hd, device="cuda")
+    q_out, att = torch.zeros(max_rows, H * hd, device="cuda"), torch.zeros(max_rows, H * hd, device="cuda")
+    ws = rz.workspace(rz.attention_paged_q4_workspace_bytes(H, K, hd), "cuda")
+
+    def step():
+        rz.paged_plan(cached, fresh, table, owned, free, count, page, plan)
+        rz.qk_norm_rope(qkv[:, :H * hd], qkv[:, H * hd:(H + K) * hd], qkv[:, (H + K) * hd:], plan.positions, H, K, hd, 1e4, 1,
+                        kv=kv, slots=plan.slots, q_out=q_out)
+        rz.attention_paged_q4(q_out, kv, table, plan.cu_rows, plan.kv_len, H, out=att, ws=ws)
+        plan.next_cached(cached, fresh, out=cached)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+    held, lens = [(np.zeros((0, K, hd)), np.zeros((0, K, hd)))] * n, [0] * n
+    # 16 + 16 + 23 tokens take 4 pages; then request 0 takes the last page and 1 is refused, twice; 2 ends; 1 goes on
+    for news, refused in (([16, 1, 7], []), ([0, 15, 16], []), ([1, 2, 9], [1]), ([1, 3, 0], [1]), ([1, 0, -1], []), ([1, 2, 5], []), ([2, 1, 1], [])):
+        x = rng.standard_normal((max_rows, (H + 2 * K) * hd)).astype(np.float32)
+        with torch.cuda.stream(stream):
+            fresh.copy_(ints(news))
+            qkv.copy_(to_dev(x))
+            graph.replay()
+        stream.synchronize()
+        assert device_error(rz) == (0x204 if refused else 0)
+        out, at = att.cpu().numpy().astype(np.float64), 0
+        for r, m in enumerate(news):
+            if m < 0:
+                held[r], lens[r] = (np.zeros((0, K, hd)), np.zeros((0, K, hd))), 0
+            if m <= 0:
+                continue
+            if r in refused:
+                assert not out[at:at + m].any() and (plan.positions[at:at + m] == -1).all()
+                at += m
+                continue
+            pos = lens[r] + np.arange(m)
+            wq, wk, wv = want_heads(x[at:at + m], H, K, hd, pos, 1e4, 1, None, None)
+            held[r] = k, v = tuple(np.concatenate([old, R.quantise(new)[2]]) for old, new in zip(held[r], (wk, wv)))
+            for h in range(H):
+                want, _ = R.attention(wq[:, h], k[:, h // 2], v[:, h // 2], pos + 1, hd ** -0.5)
+                # as in test_step_after_step_matches_dense_attention: 2^-20 of q over scores of up to |q| |k| ... 8
+                assert np.abs(out[at:at + m, h * hd:(h + 1) * hd] - want).max() <= 2.0 ** -16 * np.abs(v).max()
+            lens[r] += m
+            at += m
+        assert list(cached.cpu().numpy()) == lens
