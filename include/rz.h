@@ -484,7 +484,8 @@ size_t rz_kv_q4_page_bytes(int32_t page_size, int32_t n_kv_heads, int32_t head_d
  * RZ_ERR_DEVICE too: negative lengths, owned outside [0, max_blocks], more tokens
  * cached than its pages hold or in all than max_blocks pages do, and a request whose rows end
  * beyond max_rows (it has none).  A page that an ended request returns beyond n_pages
- * is dropped.
+ * is dropped.  A page below 0 that holds a new row records RZ_ERR_DEVICE (0x206), and the row's slot
+ * is -1; one beyond the cache is reported by the calls that use it.
  * 1 <= n_seqs <= 1024, page_size as above, max_blocks * page_size <= 2^30.
  */
 rz_status rz_paged_plan(const int32_t *cached, const int32_t *fresh, int32_t n_seqs, const int32_t *owned,

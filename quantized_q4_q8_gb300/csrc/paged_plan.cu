@@ -257,15 +257,19 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
                 }
             }
         }
+        bool lost = false;
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
             const int64_t row = row0 + (int64_t)u * n_ctas * kThreads;
             if (row < a.max_rows) {
                 a.row_seq[row] = seq[u];
                 a.positions[row] = pos[u];
-                a.slots[row] = pos[u] < 0 ? -1 : (page[u] << page_log) + (pos[u] & (a.page_size - 1));
+                // a page below 0 would be a slot below 0, which stands for a row that is not to be appended
+                lost |= pos[u] >= 0 && page[u] < 0;
+                a.slots[row] = page[u] < 0 ? -1 : (page[u] << page_log) + (pos[u] & (a.page_size - 1));
             }
         }
+        if (lost) set_error(a.err, DEV_BAD_PAGE);
     }
 }
 

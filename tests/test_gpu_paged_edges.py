@@ -5,7 +5,7 @@ import pytest
 
 import paged_reference as R
 from gpu_common import check_no_device_error, to_dev
-from test_gpu_paged import Setup, device_error, ints, no_error_left, rz, want_heads  # noqa: F401
+from test_gpu_paged import Setup, device_error, ints, no_error_left, run_plan, rz, want_heads  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -190,3 +190,24 @@ def test_state_carried_on_the_device_over_a_refused_step(rz):
             lens[r] += m
             at += m
         assert list(cached.cpu().numpy()) == lens
+
+
+# ------------------------------------------------------------------ bad pages in a plan
+@pytest.mark.parametrize("where", ["table", "pool"])
+def test_plan_reports_pages_below_zero(rz, where):
+    """The rows on such a page would lose their tokens without a word: a slot below 0 is one that is not written."""
+    cached, fresh = np.array([10, 20, 30], np.int32), np.array([1, 3, 5], np.int32)
+    table = np.array([[3, -1, -1], [4, 5, -1], [6, 7, -1]], np.int32)
+    free = np.array([1, 2, 8, 9, 0, 0, 0, 0, 0, 0], np.int32)
+    if where == "table":
+        table[1, 1] = -3
+    else:
+        free[3] = -(2 ** 31)
+    args = cached, fresh, np.array([1, 2, 2], np.int32), table, free, 4, 16, 12
+    want, got = R.plan(*args), run_plan(rz, *args)
+    assert device_error(rz) == 0x206
+    want["slots"][want["slots"] < 0] = -1
+    for k, v in got.items():
+        assert np.array_equal(v, want[k]), k
+    lost = [1, 2, 3] if where == "table" else [6, 7, 8]  # request 2's first two new tokens go into the page that it has
+    assert (got["slots"][lost] == -1).all() and (got["slots"][:9] >= 0).sum() == 6 and (got["positions"][:9] >= 0).all()
