@@ -863,12 +863,10 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
             }
             if (more) more = walk_next<W>(w, a, seqs, group);
         }
-        // no copy outlives the CTA: after an abort, those that no consumer waits for any more are waited out
-        if (*gave_up) {
-            for (int k = max(0, issued - slots); k < issued; ++k) {
-                const RingPos p = ring_pos(k, slots);
-                if (!mbar_wait(full + p.s, p.par)) set_error(a.err, DEV_TIMEOUT_DRAIN);
-            }
+        // No copy outlives the CTA: consumers that give up, now or later, leave copies that they do not wait for.
+        for (int k = max(0, issued - slots); k < issued; ++k) {
+            const RingPos p = ring_pos(k, slots);
+            if (!mbar_wait(full + p.s, p.par)) set_error(a.err, DEV_TIMEOUT_DRAIN);
         }
         return;
     }
