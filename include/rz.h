@@ -600,6 +600,14 @@ rz_status rz_set_pdl(int enable);
  */
 rz_status rz_debug_stall_next_gemv(uint32_t wait_limit);
 
+/*
+ * rz_debug_stall_next_paged -- the same for the next rz_attention_paged_q4 (or
+ * rz_decode_layer_paged) of this process: CTA 0 leaves its first tokens uncopied, in each
+ * kernel of the call in which it has any.  Code 0x110, RZ_ERR_TIMEOUT; the rows of the
+ * items that CTA 0 works are undefined, and the workspace is to be filled with zeros again.
+ */
+rz_status rz_debug_stall_next_paged(uint32_t wait_limit);
+
 
 #ifdef __cplusplus
 }

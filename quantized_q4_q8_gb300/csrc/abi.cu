@@ -16,6 +16,7 @@ namespace rz {
 
 bool g_use_pdl = true;
 uint32_t g_stall_next_gemv = 0;
+uint32_t g_stall_next_paged = 0;
 
 namespace {
 
@@ -424,6 +425,15 @@ rz_status rz_debug_stall_next_gemv(uint32_t wait_limit)
     if (wait_limit < 1024 || wait_limit > (1u << 22))
         return fail(RZ_ERR_INVALID_ARG, "rz_debug_stall_next_gemv: wait_limit=%u outside [1024, 2^22]", wait_limit);
     g_stall_next_gemv = wait_limit;
+    return RZ_OK;
+}
+
+rz_status rz_debug_stall_next_paged(uint32_t wait_limit)
+{
+    t_last_error.clear();
+    if (wait_limit < 1024 || wait_limit > (1u << 22))
+        return fail(RZ_ERR_INVALID_ARG, "rz_debug_stall_next_paged: wait_limit=%u outside [1024, 2^22]", wait_limit);
+    g_stall_next_paged = wait_limit;
     return RZ_OK;
 }
 

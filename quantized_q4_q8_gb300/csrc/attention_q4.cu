@@ -634,6 +634,19 @@ __device__ __forceinline__ void ring_step(RingPos &r, int n, int slots)
     }
 }
 
+// Most polls of a wait: those that the test aid gives its CTA 0, else the usual number.
+__device__ __forceinline__ uint32_t wait_limit(const PagedAttnArgs &a) { return a.stall && blockIdx.x == 0 ? a.stall : kWaitLimit; }
+
+// Bounded wait that ends, too, when another warp has given up.
+__device__ __forceinline__ bool wait_unless(uint64_t *bar, unsigned par, uint32_t limit, const volatile int *gave_up)
+{
+    for (uint32_t i = 0; i < limit; ++i) {
+        if (mbar_try_wait(bar, par)) return true;
+        if (*gave_up) return false;
+    }
+    return false;
+}
+
 // A consumer warp's share of the current part of an item: its sums to shared memory.
 template <int NB, int NT, int NG>
 __device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, const uint8_t *ring, int slots, uint64_t *full,
@@ -670,7 +683,7 @@ __device__ __forceinline__ void work(const PagedAttnArgs &a, const Walk &w, cons
     RingPos mine = pos;
     ring_step(mine, ks, slots);
     for (int u = idle || __any_sync(0xffffffffu, *gave_up) ? w.hi : w.lo + ks; u < w.hi; u += copies) {
-        if (!__all_sync(0xffffffffu, mbar_wait(full + mine.s, mine.par))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full + mine.s, mine.par, wait_limit(a)))) {
             *gave_up = 1;
             set_error(a.err, DEV_TIMEOUT_PAGED);
             break;
@@ -796,6 +809,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
         RingPos pos{0, 0};
         int issued = 0;
         bool more = true;
+        const bool stalled = a.stall && blockIdx.x == 0;  // test aid: the first unit is not issued
         // the step's keys and values were written by another kernel through the generic proxy
         asm volatile("fence.proxy.async;" ::: "memory");
         while (more) {
@@ -818,14 +832,14 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
                         }
                 }
                 bool ok = !*gave_up;
-                if (lane < n && ok) ok = mbar_wait(empty + mine.s, mine.par ^ 1u);
+                if (lane < n && ok) ok = mbar_wait(empty + mine.s, mine.par ^ 1u, wait_limit(a));
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (!*gave_up) set_error(a.err, DEV_TIMEOUT_PAGED);
                     *gave_up = 1;
                     more = false;
                     break;
                 }
-                if (lane < n) {
+                if (lane < n && !(stalled && issued + lane == 0)) {
                     uint8_t *dst = ring + (size_t)mine.s * kSlot;
                     const uint8_t *src = a.kv.pages + ((int64_t)page[0] * K + w.h) * head_bytes + (g0 & ((1 << lg) - 1)) * kRec;
                     mbar_arrive_expect_tx(full + mine.s, groups * kRec);
@@ -866,7 +880,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
         // No copy outlives the CTA: consumers that give up, now or later, leave copies that they do not wait for.
         for (int k = max(0, issued - slots); k < issued; ++k) {
             const RingPos p = ring_pos(k, slots);
-            if (!mbar_wait(full + p.s, p.par)) set_error(a.err, DEV_TIMEOUT_DRAIN);
+            if (!(stalled && k == 0) && !mbar_wait(full + p.s, p.par)) set_error(a.err, DEV_TIMEOUT_DRAIN);
         }
         return;
     }
@@ -921,7 +935,7 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
             }
             if (!whole) {
                 // ---- the last CTA to arrive adds the parts up
-                const bool known = mbar_wait(listed + (w.lo == 0), 0);  // false: the producer gave up
+                const bool known = wait_unless(listed + (w.lo == 0), 0, wait_limit(a), gave_up);  // false: the producer gave up
                 const int parts = known ? part_count[w.lo == 0] : 0;
                 const int16_t *list = part_list + (w.lo == 0) * kMaxCtas;
                 consumer_sync<W>();  // the part is written
@@ -1056,6 +1070,8 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &args, void *workspace, c
     const int group = a.n_heads / a.kv.n_kv_heads;
     const bool tc = paged_attention_tc_takes(a.kv.head_dim) && (a.n_rows - a.n_seqs + 1) * group > kTcRows;
     a.most_rows = tc ? kTcRows : 0x7fffffff;
+    a.stall = g_stall_next_paged;
+    g_stall_next_paged = 0;  // one call only
     const cudaError_t e = launch_any(a, s);
     return e != cudaSuccess || !tc ? e : launch_paged_attention_tc(a, s);
 }

@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         constexpr int kRec = q4_record_bytes(hd);
         const int64_t head_bytes = (int64_t)kRec << lg;
         asm volatile("fence.proxy.async;" ::: "memory");
+        const bool stalled = a.stall && blockIdx.x == 0;  // test aid: the first tile's K is not copied
         int n_k = 0, n_v = 0;
         const uint8_t *v_src = nullptr;  // this lane's group of the tile whose V is next
         int v_groups = 0;
@@ -515,9 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
                 }
                 const int slot = n_k & 1;
                 if (!(ok = wait_for(&b.raw_k_empty[slot], ((n_k >> 1) & 1) ^ 1u, b, a.err))) break;
-                if (lane == 0) mbar_arrive_expect_tx(&b.raw_k_full[slot], groups * 10 * hd);
+                const bool copy = !(stalled && n_k == 0);
+                if (lane == 0 && copy) mbar_arrive_expect_tx(&b.raw_k_full[slot], groups * 10 * hd);
                 __syncwarp();
-                if (lane < groups) {
+                if (lane < groups && copy) {
                     uint8_t *dst = sm + L::off_raw_k + slot * L::raw_k + lane * 10 * hd;
                     bulk_g2s(dst, src, 9 * hd, &b.raw_k_full[slot]);
                     bulk_g2s(dst + 9 * hd, src + 17 * hd, hd, &b.raw_k_full[slot]);
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_tc_kernel(const _
         }
         if (ok && n_k > 0) copy_v();
         // no copy outlives the CTA
-        for (int k = max(0, n_k - 2); k < n_k; ++k) mbar_wait(&b.raw_k_full[k & 1], (k >> 1) & 1);
+        for (int k = max(stalled ? 1 : 0, n_k - 2); k < n_k; ++k) mbar_wait(&b.raw_k_full[k & 1], (k >> 1) & 1);
         if (n_v > 0) mbar_wait(&b.raw_v_full, (n_v - 1) & 1);
         } else if (warp == 1) {
         // ------------------------------------------------------------ products

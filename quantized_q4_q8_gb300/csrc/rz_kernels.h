@@ -37,6 +37,9 @@ unsigned *dev_error_word();
 // Test aid: non-zero makes the next Q4_K GEMV launch leave its first stage in
 // CTA 0 unissued and bound that CTA's waits by this many polls (then reset to 0).
 extern uint32_t g_stall_next_gemv;
+// The same for the next call of the paged attention: its kernels leave the first unit of tokens (128 in the tcgen05
+// kernel) of CTA 0 uncopied.  The polls bound the waits of the first kernel's CTA 0; the other's are bounded as ever.
+extern uint32_t g_stall_next_paged;
 
 // Launch with the programmatic-stream-serialization attribute (PDL) so that the
 // kernel's weight prefetch overlaps the tail of the previous kernel in the stream.
@@ -294,6 +297,7 @@ struct PagedAttnArgs {
     float *kept;  // the tcgen05 kernel's sums of earlier periods, within part's space
     int *counters;
     unsigned *err;
+    uint32_t stall;  // test aid (rz_debug_stall_next_paged), 0 otherwise
     int most_rows;  // requests with more rows than this for a kv head are left to the other kernel
 };
 constexpr int kPagedMaxSeqs = 1024;

@@ -211,3 +211,35 @@ def test_plan_reports_pages_below_zero(rz, where):
         assert np.array_equal(v, want[k]), k
     lost = [1, 2, 3] if where == "table" else [6, 7, 8]  # request 2's first two new tokens go into the page that it has
     assert (got["slots"][lost] == -1).all() and (got["slots"][:9] >= 0).sum() == 6 and (got["positions"][:9] >= 0).all()
+
+
+# ------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("hd,H,K,reqs", [
+    (128, 8, 8, [(20000, 1)]),             # items in parts of many CTAs
+    (64, 4, 2, [(700, 1)] * 200),          # many whole items for a CTA
+    (256, 8, 2, [(30000, 5), (900, 1)]),
+    (64, 14, 2, [(3000, 5)] * 24),
+    (128, 8, 2, [(6000, 700)]),            # the tcgen05 kernel, parts of items
+    (64, 32, 8, [(1500, 1500)]),           # its whole items, several for a CTA
+    (128, 16, 16, [(5000, 1)] * 8 + [(2000, 300)]),  # both kernels
+])
+def test_attention_whose_copies_do_not_come_ends_in_an_error(rz, hd, H, K, reqs):
+    """CTA 0 (whose share of the work is longer than the start of an item here) waits for tokens that are never copied: the call ends with a timeout's code, and with a workspace of
+    zeros the next one is right."""
+    import torch
+    s = Setup(51, H, K, hd, 64, reqs)
+    good = s.run(rz).clone()
+    rz.rz_debug_stall_next_paged(1 << 14)
+    s.run(rz)
+    st, code = rz.check_device_error()  # synchronises: the kernels ended
+    assert st == 5 and code == 0x110, (st, hex(code))
+    s.ws.zero_()
+    for _ in range(2):
+        assert torch.equal(s.run(rz), good)
+    assert not s.ws[:1024].any()
+
+
+def test_stall_of_the_paged_attention_is_checked_on_the_host(rz):
+    from quantized_q4_q8_gb300 import _lib
+    assert _lib.status("rz_debug_stall_next_paged", 10) == 1
+    assert _lib.status("rz_debug_stall_next_paged", 1 << 30) == 1
