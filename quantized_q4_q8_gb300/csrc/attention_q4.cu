@@ -576,7 +576,7 @@ __device__ __forceinline__ void attend(Warp<NB, NT> &w, const uint8_t *rec, int 
 // ---------------------------------------------------------------- shared memory
 // slots of 2 records | query fragments | the warps' sums, their (m, l) | mbarriers, flags, counts (512 bytes) |
 // the parts of an item | the line's prefix | the requests
-constexpr int kMaxSlots = 24;
+constexpr int kMaxSlots = 24;  // at most 32: a lane of the producer waits for each at the end
 constexpr int kMaxCtas = 512;  // of the grid
 template <int NB>
 struct Layout {
@@ -877,11 +877,10 @@ __global__ void __launch_bounds__((consumers(NB) + 1) * 32, 2)
             }
             if (more) more = walk_next<W>(w, a, seqs, group);
         }
-        // No copy outlives the CTA: consumers that give up, now or later, leave copies that they do not wait for.
-        for (int k = max(0, issued - slots); k < issued; ++k) {
-            const RingPos p = ring_pos(k, slots);
-            if (!(stalled && k == 0) && !mbar_wait(full + p.s, p.par)) set_error(a.err, DEV_TIMEOUT_DRAIN);
-        }
+        // No copy outlives the CTA: consumers that give up, now or later, leave copies that they do not wait for.  Lane i
+        // waits for the last unit in slot i.
+        if (lane < min(issued, slots) && !(stalled && lane == 0) && !mbar_wait(full + lane, lane < pos.s ? pos.par : pos.par ^ 1u))
+            set_error(a.err, DEV_TIMEOUT_DRAIN);
         return;
     }
 
