@@ -243,3 +243,87 @@ def test_stall_of_the_paged_attention_is_checked_on_the_host(rz):
     from quantized_q4_q8_gb300 import _lib
     assert _lib.status("rz_debug_stall_next_paged", 10) == 1
     assert _lib.status("rz_debug_stall_next_paged", 1 << 30) == 1
+
+
+# ------------------------------------------------------------------ capacity for more requests than have rows
+@pytest.mark.parametrize("hd,H,K", [(128, 8, 2), (64, 14, 2), (64, 4, 4)])
+@pytest.mark.parametrize("spare_rows", [0, 700])
+def test_attention_one_prompt_among_idle_requests(rz, hd, H, K, spare_rows):
+    """Room for a thousand requests, of which one has a prompt and a few a token: more requests than rows, or spare rows
+    for all of them (which kernel works the prompt depends on that, what it gives does not)."""
+    reqs = [(0, 0)] * 1000
+    reqs[3], reqs[500], reqs[777], reqs[999] = (900, 1), (1200, 300), (40, 0), (17, 2)
+    s = Setup(61, H, K, hd, 16, reqs, extra_rows=spare_rows)
+    s.check(s.run(rz).cpu().numpy())
+
+
+# ------------------------------------------------------------------ the layer
+def layer_of(rz, sh, tag, bias, fused):
+    import torch
+
+    import rz_synth as S
+    L = S.layer(sh, tag)
+    w = {k: to_dev(v) for k, v in L.w.items()} | {"attn_gamma": to_dev(L.attn_gamma), "ffn_gamma": to_dev(L.ffn_gamma)}
+    biases = [to_dev(S.uniform(f"{tag}.b{i}", n, -0.5, 0.5)) if bias else None for i, n in enumerate((sh.q_dim, sh.kv_dim, sh.kv_dim))]
+    own = dict(w)
+    if fused:
+        own["wq"] = torch.cat([own.pop("wq"), own.pop("wk"), own.pop("wv")])
+    if bias:
+        own |= {"bq": torch.cat(biases)} if fused else dict(zip(("bq", "bk", "bv"), biases))
+    layer = rz.DeviceLayer(own, sh.hidden, sh.hidden_pad, sh.n_heads, sh.n_kv_heads, sh.head_dim, sh.inter, sh.eps, sh.rope_theta, sh.rope_mode)
+    return layer, w, biases if bias else None
+
+
+def layer_steps(rz, sh, w, biases, x, kv, table, plan):
+    """rz_decode_layer_paged from its public calls, for the rows of x."""
+    import torch
+    H, K, hd, m = sh.n_heads, sh.n_kv_heads, sh.head_dim, x.shape[0]
+    rows = [H * hd, K * hd, K * hd]
+    if m <= 3:
+        qkv = rz.rmsnorm_q4k_gemv(x, w["attn_gamma"], sh.hidden, sh.eps, [w["wq"], w["wk"], w["wv"]], rows, sh.hidden_pad, biases=biases)
+    else:
+        x8 = rz.rmsnorm(x, w["attn_gamma"], sh.hidden, sh.hidden_pad, sh.eps, want_y=False)[1]
+        qkv = rz.q4k_q8_gemv_multi(x8, [w["wq"], w["wk"], w["wv"]], rows, m, sh.hidden_pad, biases=biases)
+    q, _, _ = rz.qk_norm_rope(qkv[:, :H * hd], qkv[:, H * hd:(H + K) * hd], qkv[:, (H + K) * hd:], plan.positions, H, K, hd, sh.rope_theta,
+                              sh.rope_mode, eps=sh.eps, kv=kv, slots=plan.slots)
+    a8 = torch.zeros(rz.q8_1_size(m, sh.q_pad), dtype=torch.uint8, device="cuda")
+    rz.attention_paged_q4(q, kv, table, plan.cu_rows, plan.kv_len, H, att_q8=a8)
+    res = torch.zeros(m, sh.hidden_pad, device="cuda")
+    rz.q4k_q8_gemv_ex(w["wo"], a8, m, sh.hidden, sh.q_pad, residual=x, out=res, ld=sh.hidden_pad)
+    res[:, sh.hidden:] = 0
+    return rz.swiglu_ffn(res, w["ffn_gamma"], w["wgate"], w["wup"], w["wdown"], sh.hidden, sh.hidden_pad, sh.inter, sh.eps)
+
+
+@pytest.mark.parametrize("dims,bias,fused", [
+    ((896, 4864, 14, 2, 64, 1e6, 1), True, False), ((896, 4864, 14, 2, 64, 1e6, 1), True, True),
+    ((512, 512, 4, 4, 128, 1e4, 0), False, True), ((576, 768, 6, 2, 96, 1e4, 0), True, False), ((512, 512, 2, 1, 256, 1e4, 1), False, False)])
+def test_decode_layer_paged_with_spare_rows_and_a_refused_request(rz, dims, bias, fused):
+    """The rows of the requests that the plan serves are those of the public calls, bit for bit, whatever stands in the
+    rows of a refused request and in those of none."""
+    import torch
+
+    import rz_synth as S
+    sh = S.LayerShape(*dims)
+    layer, w, biases = layer_of(rz, sh, f"edges.{dims}", bias, fused)
+    page, n, n_pages = 16, 4, 5
+    kvs = [rz.PagedKVQ4(torch.zeros((n_pages, sh.n_kv_heads, page * sh.head_dim * 9 // 8), dtype=torch.uint8, device="cuda"), page, sh.head_dim)
+           for _ in range(2)]
+    table = torch.full((n, 4), -1, dtype=torch.int32, device="cuda")
+    owned, count, free = torch.zeros(n, dtype=torch.int32, device="cuda"), ints([n_pages]), torch.arange(n_pages, dtype=torch.int32, device="cuda")
+    cached = torch.zeros(n, dtype=torch.int32, device="cuda")
+    for step, (news, m, refused) in enumerate((([9, 3, 1, 0], 16, None), ([1, 14, 0, 1], 16, None), ([7, 2, 1, 2], 14, 0), ([1, 0, 1, 0], 3, None), ([1, 0, 0, 0], 1, None))):
+        fresh = ints(news)
+        plan = rz.PagedPlan(n, m)
+        rz.paged_plan(cached, fresh, table, owned, free, count, page, plan)
+        assert device_error(rz) == (0 if refused is None else 0x204)
+        rows = sum(news)
+        live = [r for r, i in enumerate(np.repeat(np.arange(n), news)) if i != refused]
+        x = to_dev(S.hidden_input(f"edges.x{step}", m, sh.hidden, sh.hidden_pad))
+        dead = [r for r in range(m) if r not in live]
+        x[dead, :sh.hidden] = float("nan")
+        out = rz.decode_layer_paged(x, layer, kvs[0], table, plan)
+        x[dead, :sh.hidden] = 3.0
+        want = layer_steps(rz, sh, w, biases, x, kvs[1], table, plan)
+        assert torch.isfinite(want[live]).all() and torch.equal(out[live], want[live]), (step, rows)
+        assert torch.equal(kvs[0].pages, kvs[1].pages)
+        plan.next_cached(cached, fresh, out=cached)
