@@ -438,7 +438,7 @@ rz_status rz_swiglu_ffn_static(const float *x, const float *gamma, const void *w
  * K and V are held as Q4_0 blocks of 32 values along the head: d = f16 of the value
  * of largest magnitude (of +a and -a the positive one) divided by -8, clamped to f16's
  * range; code = round-half-even(x / d) + 8 clamped to 0..15; value = d * (code - 8).
- * d == 0 gives codes 8; a block with a NaN or an infinity gets d = NaN.  Bytes are laid
+ * d == 0 gives codes 8; a block with a NaN or an infinity gets d = NaN (d is never an infinity).  Bytes are laid
  * out for the kernels (csrc/paged_q4.cuh), 16 tokens of one kv head in a record of
  * 18 * head_dim bytes.
  * ---------------------------------------------------------------------------
@@ -509,8 +509,9 @@ rz_status rz_paged_plan(const int32_t *cached, const int32_t *fresh, int32_t n_s
  *   k_out, v_out f32 [n_rows][n_kv_heads * head_dim] or NULL: with a cache the values as
  *              it holds them, without one the rotated k
  * The cache's codes and scales are those of the format evaluated in f64 (the kernel
- * carries a key as a sum of two f32; a value within 2^-40 of a border between two codes
- * may take either).
+ * carries a key as a sum of two f32; a value may take either of two codes within 2^-40 of the border
+ * between them, relative to its pair, or within position * 2^-52 from position 4096 on, the rounding of
+ * the angle: 2^-35 at 131072).
  */
 rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t ld_k, const float *v, int64_t ld_v,
                           const float *q_gamma, const float *k_gamma, float eps, const int32_t *positions,
@@ -537,10 +538,16 @@ rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t 
  *              once after allocating it (a completed call leaves its counters zero; after
  *              RZ_ERR_TIMEOUT fill it with zeros again); calls that share it must not overlap on
  *              the GPU, captured ones among them
- * Scores and sums are f32-accurate: q and the weights enter as two f16 pieces each, the
- * codes exactly.  (Requests of more than 40 query rows for a kv head, at a head_dim of 64 or 128, are
- * worked 128 tokens at a time, K and V as two f16 pieces each below the largest |d| of the 128:
- * a value comes to within 2^-30 of that d.)  A length, row offset or page outside its range records RZ_ERR_DEVICE:
+ * Scores and sums are f32-accurate: q and the weights enter as two f16 pieces each (22 bits), the
+ * codes exactly.  A weight p |d| of V does not come closer than 2^-31 of the row's largest p |d|, taking for
+ * |d| the largest of the blocks of the token and of up to 3 others near it: where the blocks of a head, or such
+ * tokens, differ by more than some 2^9, the small ones have fewer bits than f32.
+ * Requests of more than 40 query rows for a kv head, at a head_dim of 64 or 128, are worked 128 tokens at a time, K and V
+ * as two f16 pieces each: a value comes to within 2^-30 of the largest |d| of the 128, which stands in the place
+ * of the 4 tokens' above.  (Where n_rows - n_seqs + 1 rows would be 40 query rows or fewer, which is what one request
+ * can have when every other has a row, they are worked as few rows are: a prompt among more idle requests than
+ * there are rows takes about twice as long.)
+ * A length, row offset or page outside its range records RZ_ERR_DEVICE:
  * a request of a length below 0 or beyond its table holds no token (zeros), one of bad row offsets has
  * no rows (its outputs stay as they were), and one of a bad page has rows that are undefined.  1 <= n_seqs <= 1024.
  */

@@ -40,7 +40,7 @@
 // K's rows, are in that order too).
 //
 // Bound: a tile takes 3 + 3 products of 128 x 128 x hd.  1000 new rows beside 7 decodes over up to 4000 tokens, 32 heads on
-// 8 kv heads of 128: 227 us; 4000 new rows of 8000 tokens: 1100 us, 358 TFLOP/s of the formula's or 1070 of the tensor
+// 8 kv heads of 128: 227 us; 4000 new rows of 8000 tokens: 1102 us, 357 TFLOP/s of the formula's or 1070 of the tensor
 // cores', 57% of a large matrix product's rate.  The tensor pipe is busy 38% of the time at the first; the rest is waiting of
 // a tile's stages for one another (softmax of 128 x 128, unpacking, putting O aside) and the start and end of items.
 //

@@ -23,16 +23,19 @@
 // sign of |x| - h |d| at a border h is exact in one fused multiply-add, since h |d| has 16
 // significant bits).  K is carried as sums of two floats from the load to the code: squares,
 // the inverse root (one Newton step), cosines and sines, rotation; each is good to about 2^-45, so
-// a key is off by 2^-40 of its pair, as far as the f64 form itself is at positions beyond
-// 10^4.  That costs some 250 more instructions for a key head.  f64 costs more here: working
+// a key is off by 2^-40 of its pair, but for the angle: its fraction of a turn for each position is a double's, so that
+// it is off by position * 2^-52, which is more from position 4096 on (the f64 form's own angle is rounded at that size).
+// That costs some 250 more instructions for a key head.  f64 costs more here: working
 // only the doubtful heads (one in a hundred) in f64 took 12 us of 18 at 33 tokens of 32 + 64 heads of 128
 // and 23 us of 79 at 4096 tokens of 32 + 16; f32 with bounds of its errors and the sums of two floats only for
-// heads in doubt takes 6.4 us instead of 5.7 and 50.3 instead of 52.7.  Queries are f32.
+// heads in doubt takes 6.8 us instead of 5.9 and 50.7 instead of 50.3.  Queries are f32.
 //
 // Bound: 4096 tokens of 32 + 16 heads of 128 read and write 206 MB and take 50.3 us, 4.1 TB/s or 60% of a copy's
 // rate; the issue slots are 75% full (keys: 8 heads of 48 take 40% of the instructions).  Queries alone run at 6.7
 // TB/s.  10 CTAs of 4 warps an SM (48 registers): 9 take 49.7 us there and 0.1 us more at 33 tokens, 12 (spills) 56.8,
-// 8 50.0.  Two rows ahead in flight instead of one: 53.3 against 52.7.  33 tokens of 32 + 64 heads: 5.7 us, latency.
+// 8 50.0.  Two rows ahead in flight instead of one: 53.3.  Heads of 160 to 256 spill some registers at that (256: up to
+// 200 bytes stored, 148 loaded a thread); 4096 tokens of 16 + 8 heads of 256, the same bytes, take 45.7 us all the
+// same.  33 tokens of 32 + 64 heads: 5.9 us, latency.
 #include <math.h>
 
 #include <algorithm>
@@ -58,8 +61,9 @@ __device__ const float2 kCos64[17] = {
     {0x1.917a6cp-4f, -0x1.eb25eap-31f}, {0x0p+0f, 0x0p+0f}};
 
 // ---------------------------------------------------------------- sums of two floats
-// h + l, |l| at most half a step of h.  Products by __fmul_rn: a product whose error is
-// taken must not be fused into what uses it.
+// h + l, |l| at most half a step of h: Knuth's sum with its error (two_sum), Dekker's shorter one for |a| >= |b|, the
+// error of a product by a fused multiply-add, and Dekker's sums and products of pairs.  Products by __fmul_rn: a
+// product whose error is taken must not be fused into what uses it.
 struct Two {
     float h, l;
 };

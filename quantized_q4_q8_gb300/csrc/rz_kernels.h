@@ -304,8 +304,11 @@ constexpr int kPagedMaxSeqs = 1024;
 size_t paged_attention_workspace_bytes(int head_dim);
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *workspace, cudaStream_t s);
 // Requests with more query rows than this for a kv head go to the tcgen05 kernel (attention_q4_tc.cu), whose
-// items are always 128 rows.  32 requests of 8000 tokens with 32 rows: 155 us there and 172 here; 24 requests
-// of 5 tokens, 35 rows, some hundred tokens held: 39 and 36; 20 rows: 383 and 329.
+// items are always 128 rows.  What is better goes by the tokens held too, which the rule leaves out (us there and in the
+// kernel for few rows): 42 rows over 400 to 6000 tokens (24 requests of 6 new tokens, 14 on 2 heads of 64) 40.4 and
+// 48.2, over 200 to 400 tokens 23.3 and 23.2; 35 rows over 70 to 6000 40.3 and 38.2; 32 rows (32 requests of 8 new tokens,
+// 32 on 8 heads of 128) over 400 to 8000 168 and 172, over 8000 369 and 413, over 300 51 and 41; 20 rows (64 requests of
+// 20, 32 on 32 of 128) over 400 to 1000 423 and 330.
 constexpr int kTcRows = 40;
 bool paged_attention_tc_takes(int head_dim);
 size_t paged_attention_tc_part_bytes(int head_dim);

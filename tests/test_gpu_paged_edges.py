@@ -45,6 +45,38 @@ def test_attention_tiles_of_zero_values(rz, size, hd, H, K, reqs, zero):
     assert zero != "all" or not out.any()
 
 
+@pytest.mark.parametrize("hd,H,K,reqs", [(128, 8, 2, [(1000, 1), (33, 3)]), (64, 14, 2, [(900, 5)]), (128, 8, 2, [(1500, 200)]), (64, 8, 1, [(700, 100)])])
+@pytest.mark.parametrize("small", [2.0 ** -9, 2.0 ** -16])
+def test_attention_blocks_of_different_sizes(rz, hd, H, K, reqs, small):
+    """A head whose last block of values is much smaller than its first, and every fifth token small throughout: on top of
+    Setup.check's bound a weight is off by up to 2^-31 of the row's largest p |d| (|d| the largest of 128 tokens here),
+    for each token, times codes of up to 8."""
+    s = Setup(71 + hd, H, K, hd, 32, reqs)
+    v = s.vval.astype(np.float64)
+    v[..., -32:] *= small
+    v[::5] *= small
+    with_cache(s, v=v)
+    got, G, sc = s.run(rz).cpu().numpy().astype(np.float64), H // K, hd ** -0.5
+    for i, (n, m) in enumerate(reqs):
+        slots = s.slots[i]
+        for h in range(K):
+            q = s.q[s.cu[i]:s.cu[i] + m].reshape(m, H, hd)[:, h * G:(h + 1) * G].astype(np.float64).reshape(m * G, hd)
+            k, vv = s.kval[slots, h].astype(np.float64), s.vval[slots, h].astype(np.float64)
+            want, p = R.attention(q, k, vv, np.repeat(n - m + np.arange(m) + 1, G), sc)
+            out = got[s.cu[i]:s.cu[i] + m].reshape(m, H, hd)[:, h * G:(h + 1) * G].reshape(m * G, hd)
+            qb = np.abs(q).reshape(m * G, -1, 32).sum(-1) + 2.0 ** -2 * np.abs(q).max(-1, keepdims=True)
+            delta = (sc * 2.0 ** -20 * 23 * (qb @ s.kd[slots, h].T)).max(-1)
+            top = np.abs(q @ k.T * sc).max(-1)
+            rel = 2 * (delta + 2.0 ** -24 * (top * 1.45 + 40)) + 2.0 ** -21 + 2.0 ** -22 + 2.0 ** -23 * (n / 16 + 40)
+            tile = np.pad(s.vd[slots, h].max(-1), (0, -n % 128)).reshape(-1, 128).max(-1).repeat(128)[:n]
+            floor = n * 8 * 2.0 ** -31 * (p * tile).max(-1, keepdims=True)
+            err = np.abs(out - want)
+            assert (err <= rel[:, None] * 23 * np.repeat(p @ s.vd[slots, h], 32, axis=-1) + floor).all(), (i, h)
+            # the small block by itself: 1e-5 of it, and what the floor of independent roundings comes to
+            e, w = err[:, -32:], want[:, -32:]
+            assert np.sqrt((e ** 2).mean()) <= 1e-5 * np.sqrt((w ** 2).mean()) + floor.max() / np.sqrt(n)
+
+
 # ------------------------------------------------------------------ no number in one block
 @pytest.mark.parametrize("hd,H,K,reqs", [(128, 4, 2, [(500, 200), (60, 1)]), (64, 4, 2, [(500, 200), (60, 1)]),
                                          (128, 32, 8, [(900, 900)]), (128, 4, 2, [(500, 3), (60, 1)]), (96, 4, 2, [(500, 60)])])
