@@ -180,6 +180,8 @@ rz_status rz_qk_norm_rope(const float *q, int64_t ld_q, const float *k, int64_t 
     const int64_t q_dim = (int64_t)n_heads * head_dim, kv_dim = (int64_t)n_kv_heads * head_dim;
     if (ld_q < q_dim || ld_qo < q_dim || ld_k < kv_dim || (v && ld_v < kv_dim))
         return fail(RZ_ERR_SHAPE, "%s: a row stride is smaller than its row", fn);
+    if (q_out == q && ld_qo != ld_q && n_rows > 1)
+        return fail(RZ_ERR_SHAPE, "%s: q_out is q, but ld_qo=%lld is not ld_q=%lld", fn, (long long)ld_qo, (long long)ld_q);
     PagedKv pk{};
     if (kv) {
         RZ_TRY(check_kv_q4(fn, kv, &pk));

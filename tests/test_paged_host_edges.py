@@ -19,6 +19,12 @@ def test_heads_refuses_as_many(lib):
     assert lib.status("rz_qk_norm_rope", *a.values()) == 2 and "n_heads" in lib.last_error()
 
 
+def test_heads_in_place_needs_one_row_stride(lib):
+    """Rows written at another stride would run into rows that are still to be read."""
+    a = {**HEADS, "kv": kv(lib), "ld_qo": 512}
+    assert lib.status("rz_qk_norm_rope", *a.values()) == 2 and "ld_qo" in lib.last_error()
+
+
 def carried(torch, rz, cached, fresh, w):
     plan = rz.PagedPlan(len(cached), 8, "cpu")
     plan.kv_len.copy_(torch.from_numpy(w["kv_len"]))
