@@ -359,3 +359,32 @@ def test_decode_layer_paged_with_spare_rows_and_a_refused_request(rz, dims, bias
         assert torch.isfinite(want[live]).all() and torch.equal(out[live], want[live]), (step, rows)
         assert torch.equal(kvs[0].pages, kvs[1].pages)
         plan.next_cached(cached, fresh, out=cached)
+
+
+# ------------------------------------------------------------------ offsets beyond 32 bits
+@pytest.mark.parametrize("hd,H,K,reqs", [(128, 16, 8, [(700, 1), (300, 4)]), (64, 16, 16, [(500, 3)]), (128, 16, 8, [(400, 90)])])
+def test_pages_beyond_four_gigabytes(rz, hd, H, K, reqs):
+    """The same pages, the same rows appended to them and the same attention over them at the end of a cache of some 5 GB."""
+    import torch
+    s = Setup(81, H, K, hd, 64, reqs)
+    small, first = s.kv.pages, 5 * 2 ** 30 // (s.kv.pages[0].numel())
+    big = torch.empty((first + small.shape[0], *small.shape[1:]), dtype=torch.uint8, device="cuda")
+    big[first:] = small
+    far = rz.PagedKVQ4(big, 64, hd)
+    T = 9
+    slots = ints(s.slots[0][-T:], np.int64)  # new keys and values for tokens that the first request holds
+    x = to_dev(np.random.default_rng(2).standard_normal((T, (H + 2 * K) * hd)).astype(np.float32))
+    want_q = None
+    for kv, off in ((s.kv, 0), (far, first)):
+        q, _, _ = rz.qk_norm_rope(x[:, :H * hd], x[:, H * hd:(H + K) * hd], x[:, (H + K) * hd:], ints(np.arange(T)), H, K, hd, 1e4, 1, kv=kv,
+                                  slots=slots + off * 64)
+        table = torch.where(s.td < small.shape[0], s.td + off, s.td)
+        out = rz.attention_paged_q4(s.qd, kv, table, s.cud, s.lend, H, ws=s.ws)
+        if want_q is None:
+            want_q, want = q, out
+    assert torch.equal(q, want_q) and torch.equal(out, want) and torch.equal(big[first:], small)
+    # a plan hands such pages out as any others
+    n = first + small.shape[0]
+    free, plan = torch.arange(n, dtype=torch.int32, device="cuda"), rz.PagedPlan(1, 4)
+    rz.paged_plan(ints([0]), ints([3]), ints(np.full((1, 4), -1)), ints([0]), free, ints([n]), 64, plan)
+    assert list(plan.slots.cpu().numpy()) == [(n - 1) * 64 + i for i in range(3)] + [-1]
