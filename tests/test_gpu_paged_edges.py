@@ -283,10 +283,11 @@ def test_stall_of_the_paged_attention_is_checked_on_the_host(rz):
 def test_attention_one_prompt_among_idle_requests(rz, hd, H, K, spare_rows):
     """Room for a thousand requests, of which one has a prompt and a few a token: more requests than rows, or spare rows
     for all of them (which kernel works the prompt depends on that, what it gives does not)."""
+    import torch
     reqs = [(0, 0)] * 1000
     reqs[3], reqs[500], reqs[777], reqs[999] = (900, 1), (1200, 300), (40, 0), (17, 2)
     s = Setup(61, H, K, hd, 16, reqs, extra_rows=spare_rows)
-    s.check(s.run(rz).cpu().numpy())
+    s.check(s.run(rz, out=torch.zeros(s.T, H * hd, device="cuda")).cpu().numpy())
 
 
 # ------------------------------------------------------------------ the layer
