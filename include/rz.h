@@ -578,6 +578,96 @@ rz_status rz_decode_layer_paged(const float *input, const rz_layer_weights *w, c
                                 size_t ws_bytes, rz_stream stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * An FFN of experts (a mixture of experts) in Q4_K.  A layer calls, in this order:
+ *   rz_residual_rmsnorm  the attention's output is added to the hidden state, the sum normed
+ *   (the router's product, logits = W_router y, is the caller's: rz_q4_0_gemv, say)
+ *   rz_moe_route         the experts of each token, their weights, the rows by expert
+ *   rz_moe_swiglu        silu(gate) * up of each (token, choice) row with its expert
+ *   rz_moe_down          the product back, the weighted sum of a token's rows, the residual
+ * and rz_moe_ffn is the last three in one call.
+ *
+ * Row r of a plan is one (token, choice): the rows of expert e are offsets[e] .. offsets[e + 1], in
+ * the order of their tokens.  All of a plan is in device memory, so that one captured graph serves every
+ * step.  A plan may also come from elsewhere; offsets outside [0, n_tokens * top_k] make an expert have no
+ * rows, a row or place outside it records RZ_ERR_DEVICE and reads row 0 or is left out, and offsets that
+ * overlap or decrease give undefined values.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+    int32_t *experts; /* [n_tokens][top_k] the experts of a token, the largest logit first; -1: none */
+    float *weights;   /* [n_tokens][top_k] */
+    int32_t *offsets; /* [n_experts + 1] */
+    int32_t *rows;    /* [n_tokens * top_k] token * top_k + choice of row r; -1 behind offsets[n_experts] */
+    int32_t *places;  /* [n_tokens * top_k] the row of token * top_k + choice; -1: none */
+    int64_t n_tokens; /* n_tokens * top_k <= 2^27 */
+    int32_t n_experts, top_k; /* 1 <= top_k <= n_experts <= 512, top_k <= 32 */
+} rz_moe_plan;
+
+/*
+ * rz_residual_rmsnorm -- rz_residual_add, rz_rmsnorm and its Q8_1 form in one pass, for any
+ * number of rows:
+ *   s = x + delta (f32);  y_i = s_i / sqrt(sum_{i<n} s_i^2 / n + eps) * gamma_i (i < n), 0 for n <= i < n_pad
+ *   x, delta  f32 [m][n_pad] (the first n of each row are read); delta may be NULL: s = x
+ *   gamma     f32 [n]
+ *   sum       f32 [m][n_pad] output: s, 0 behind n; or NULL.  May be x or delta.
+ *   y         f32 [m][n_pad] output, or NULL.  May be x or delta (not sum).
+ *   q8        Q8_1 of m rows of n_pad, of the y as it is rounded; or NULL.  (One of y, q8 is given.)  Its scales are
+ *             max|y| times the f32 nearest to 1/127, at most an ulp from rz_q8_1_quantize's quotient; codes
+ *             and sums follow from them as there.
+ *   n_pad a multiple of 32 up to 16384; all buffers 16-byte aligned.
+ * y is the f32 nearest to the formula's value of s but for about one value in 2^20 (sums and products are
+ * carried as sums of two f32), so that codes do not depend on the order of a sum.  Squares of s stay in f32's range.
+ */
+rz_status rz_residual_rmsnorm(const float *x, const float *delta, const float *gamma, float *sum, float *y, void *q8,
+                              int64_t m, int64_t n, int64_t n_pad, float eps, rz_stream stream);
+
+/*
+ * rz_moe_route -- the top_k experts of each token by its logits, their weights, and the rows
+ * grouped by expert, into the buffers of `plan`.
+ *   logits    f32 [n_tokens] rows of n_experts, row stride ld, 4-byte aligned
+ *   row_seq   int32 [n_tokens], or NULL: a negative entry marks a token without a request
+ *             (rz_paged_plan's row_seq): it has no experts and no rows, its logits are not read
+ *   renormalise  0: weights are the softmax over all experts, taken at the chosen; else the
+ *             softmax over the chosen
+ *   scale     times every weight
+ * Of equal logits the lowest index comes first.  A logit of -infinity masks its expert for the token: it is
+ * never chosen; a choice that is left without an expert has -1 and the weight 0.  A token with a NaN or +infinity among its
+ * logits has weights NaN (a NaN is chosen after every number).
+ *   workspace rz_moe_route_workspace_bytes bytes, 16-byte aligned; no initialisation; may be
+ *             NULL where that is 0 (up to 128 tokens, one launch; more: two)
+ */
+size_t rz_moe_route_workspace_bytes(int64_t n_tokens, int32_t n_experts);
+rz_status rz_moe_route(const float *logits, int64_t ld, const int32_t *row_seq, const rz_moe_plan *plan,
+                       int32_t renormalise, float scale, void *workspace, size_t ws_bytes, rz_stream stream);
+
+/*
+ * rz_moe_swiglu -- h_r = silu(G_e x_t) * (U_e x_t) for every row r of the plan, e its expert, t its
+ * token; the product of rz_q4k_q8_gemv.
+ *   w_gate, w_up  Q4_K [n_experts][inter][in_dim]     x_q8  Q8_1 of n_tokens rows of in_dim
+ *   h         f32 [n_tokens * top_k][inter] output, in the plan's order of rows, or NULL
+ *   h_q8      Q8_1 of n_tokens * top_k rows of inter (rz_moe_down's input): exactly the quantisation of
+ *             h; or NULL (inter % 32 == 0)
+ *   in_dim % 256 == 0; all 16-byte aligned.  Rows behind offsets[n_experts] stay as they were.
+ */
+rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, const rz_moe_plan *plan, int64_t inter,
+                        int64_t in_dim, float *h, void *h_q8, rz_stream stream);
+
+/*
+ * rz_moe_down -- y_t = residual_t + sum_j weights[t][j] D_e h_r, r = places[t][j], e its expert, the
+ * choices in order.
+ *   w_down    Q4_K [n_experts][out_dim][in_dim]       h_q8  Q8_1 of n_tokens * top_k rows of in_dim
+ *   residual  f32 [n_tokens][out_pad], or NULL: 0
+ *   y         f32 [n_tokens][out_pad] output; may be residual; 0 in the columns out_dim .. out_pad.  A token
+ *             without experts gets its residual.
+ *   workspace rz_moe_down_workspace_bytes bytes, 16-byte aligned; no initialisation
+ */
+size_t rz_moe_down_workspace_bytes(int64_t n_tokens, int32_t top_k, int64_t out_dim);
+rz_status rz_moe_down(const void *w_down, const void *h_q8, const rz_moe_plan *plan, const float *residual, float *y,
+                      int64_t out_dim, int64_t out_pad, int64_t in_dim, void *workspace, size_t ws_bytes,
+                      rz_stream stream);
+
+/*
  * rz_check_device_error -- synchronise `stream`, read the device error word of the
  * current device and clear it.  *code_out (nullable) receives the raw code (0 = none).
  * Returns RZ_OK, RZ_ERR_TIMEOUT (a bounded wait ran out) or RZ_ERR_DEVICE (a

@@ -67,6 +67,13 @@ class KvQ4Struct(C.Structure):
     _fields_ = [("pages", _vp), ("n_pages", _i64), ("page_size", _i32), ("n_kv_heads", _i32), ("head_dim", _i32)]
 
 
+class MoePlanStruct(C.Structure):
+    """rz_moe_plan."""
+    _fields_ = [("experts", _vp), ("weights", _vp), ("offsets", _vp), ("rows", _vp), ("places", _vp),
+                ("n_tokens", _i64), ("n_experts", _i32), ("top_k", _i32)]
+
+
+_MPP = C.POINTER(MoePlanStruct)
 _KQP = C.POINTER(KvQ4Struct)
 _LWP = C.POINTER(LayerWeightsStruct)
 _LQP = C.POINTER(LayerWeightsQ40Struct)
@@ -115,6 +122,12 @@ SIGNATURES = {
     "rz_decode_layer_paged_workspace_bytes": [_LWP, _i64],
     "rz_decode_layer_paged": [_vp, _LWP, _vp, _vp, _KQP, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _i64, _vp, _vp, _sz,
                               _vp],
+    "rz_residual_rmsnorm": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _f32, _vp],
+    "rz_moe_route_workspace_bytes": [_i64, _i32],
+    "rz_moe_route": [_vp, _i64, _vp, _MPP, _i32, _f32, _vp, _sz, _vp],
+    "rz_moe_swiglu": [_vp, _vp, _vp, _MPP, _i64, _i64, _vp, _vp, _vp],
+    "rz_moe_down_workspace_bytes": [_i64, _i32, _i64],
+    "rz_moe_down": [_vp, _vp, _MPP, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp],
     "rz_check_device_error": [_vp, C.POINTER(C.c_uint32)],
     "rz_set_pdl": [C.c_int],
     "rz_debug_stall_next_gemv": [C.c_uint32],
@@ -128,6 +141,7 @@ _RESTYPES = {"rz_last_error": C.c_char_p, "rz_version": C.c_char_p,
              "rz_decode_layer_q4_0_workspace_bytes": _sz, "rz_q4k_q8_gemm_workspace_bytes": _sz,
              "rz_kv_q4_page_bytes": _sz, "rz_attention_paged_q4_workspace_bytes": _sz,
              "rz_decode_layer_paged_workspace_bytes": _sz,
+             "rz_moe_route_workspace_bytes": _sz, "rz_moe_down_workspace_bytes": _sz,
              "rz_decode_stack_launches": C.c_int32}
 
 _lib = None

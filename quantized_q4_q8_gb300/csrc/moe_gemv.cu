@@ -1,0 +1,249 @@
+// moe_gemv.cu -- products grouped by expert of few rows: Q4_K weights of each expert against
+// the Q8_1 rows that chose it, and the sum of a token's rows.
+//
+//   h[r][i] = silu(G_e[i] . x_t) * (U_e[i] . x_t)     row r of expert e, token t = rows[r] / k
+//   o[r][i] = D_e[i] . h_r
+//   y[t][i] = residual[t][i] + sum_j weights[t][j] * o[places[t][j]][i]
+// with the product of rz_q4k_q8_gemv (exact integer dots of 32 codes, f32 sums).
+//
+// A CTA has 32 outputs and up to kTokens rows of one expert: 8 warps of 4 outputs, 4 lanes for a
+// super-block of 256 weights (64 each), 8 super-blocks side by side.  The weights come straight from
+// global memory, 12 loads of 16 bytes in flight for a lane.
+#include <algorithm>
+
+#include "q4k_dot.cuh"
+#include "rz_common.cuh"
+#include "rz_kernels.h"
+
+namespace rz {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 32;    // outputs of a CTA
+constexpr int kTokens = 4;   // rows of one expert that share a load of its weights
+constexpr int kRows = 4;     // weight rows that a warp works at once
+
+struct Weights64 {  // a lane's 64 weights: a header and 32 bytes of codes
+    int4 h, a, b;
+};
+
+__device__ __forceinline__ int4 load_stream(const void *p)
+{
+    int4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// The expert of row r (the CTA's first row), and the end of its rows; -1 where there is none.
+__device__ __forceinline__ int2 find_expert(const MoeGemvArgs &a, int r, int2 *found)
+{
+    if (threadIdx.x == 0) *found = make_int2(-1, 0);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.n_experts; e += kThreads) {
+        const int lo = a.offsets[e], hi = a.offsets[e + 1];
+        if (lo <= r && r < hi && lo >= 0 && hi <= a.n_pairs && (r - lo) % kTokens == 0) *found = make_int2(e, hi);
+    }
+    __syncthreads();
+    return *found;
+}
+
+template <bool kSwiglu>
+__global__ void __launch_bounds__(kThreads, 2) moe_gemv_kernel(const MoeGemvArgs a)
+{
+    __shared__ int2 found;
+    __shared__ float out[kTokens][kTile];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c = lane & 3, sub = lane >> 2;
+    const int nsb = a.in_dim / 256, nb = a.in_dim / 32;
+    const LaneConst L = lane_const(c);
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int r = blockIdx.y; r < a.n_pairs; r += gridDim.y) {
+        const int2 ex = find_expert(a, r, &found);
+        if (ex.x < 0) {
+            __syncthreads();
+            continue;
+        }
+        const int m = min(kTokens, ex.y - r);
+        int src[kTokens];  // the rows of x
+#pragma unroll
+        for (int t = 0; t < kTokens; ++t) {
+            int s = r + min(t, m - 1);
+            if (a.rows) {
+                const int pair = a.rows[s];
+                if (pair < 0 || pair >= a.n_pairs) {
+                    if (tid == 0) set_error(a.err, DEV_BAD_LENGTH);
+                    s = 0;
+                } else {
+                    s = pair / a.top_k;
+                }
+            }
+            src[t] = s;
+        }
+        const int64_t wbase = static_cast<int64_t>(ex.x) * a.out_dim;
+#pragma unroll 1
+        for (int pass = 0; pass < (kSwiglu ? 2 : 1); ++pass) {
+            // a warp's outputs 4 warp .. + 3; with gate and up two of them at once
+            const int o0 = 4 * warp + 2 * pass;
+            const uint8_t *wr[kRows];
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                const int64_t o = min(static_cast<int64_t>(blockIdx.x) * kTile + o0 + (kSwiglu ? k >> 1 : k), a.out_dim - 1);
+                wr[k] = (kSwiglu && (k & 1) ? a.w2 : a.w1) + (wbase + o) * nsb * 144;
+            }
+            float acc[kRows][kTokens] = {};
+#pragma unroll 1
+            for (int sb = sub; sb < nsb; sb += 8) {
+                Weights64 w[kRows];
+#pragma unroll
+                for (int k = 0; k < kRows; ++k) {
+                    const uint8_t *p = wr[k] + sb * 144;
+                    w[k].h = load_stream(p);
+                    w[k].a = load_stream(p + 16 + 32 * c);
+                    w[k].b = load_stream(p + 32 + 32 * c);
+                }
+                float ds0[kRows], ds1[kRows], dm0[kRows], dm1[kRows];
+#pragma unroll
+                for (int k = 0; k < kRows; ++k) {
+                    const float d = h2f(static_cast<uint16_t>(static_cast<uint32_t>(w[k].h.x) & 0xffffu));
+                    const float dmin = h2f(static_cast<uint16_t>(static_cast<uint32_t>(w[k].h.x) >> 16));
+                    const uint32_t A = static_cast<uint32_t>(w[k].h.y) >> L.sh, B = static_cast<uint32_t>(w[k].h.z) >> L.sh,
+                                   C = static_cast<uint32_t>(w[k].h.w) >> L.sh;
+                    const uint32_t scp = (A & L.mask_lo) | (C & L.mask_c) | ((A >> 2) & L.mask_hi);
+                    const uint32_t mnp = (B & L.mask_lo) | ((C >> 4) & L.mask_c) | ((B >> 2) & L.mask_hi);
+                    ds0[k] = d * static_cast<float>(scp & 0xffu);
+                    ds1[k] = d * static_cast<float>((scp >> 8) & 0xffu);
+                    dm0[k] = dmin * static_cast<float>(mnp & 0xffu);
+                    dm1[k] = dmin * static_cast<float>((mnp >> 8) & 0xffu);
+                }
+#pragma unroll
+                for (int t = 0; t < kTokens; ++t) {
+                    if (t >= m) break;
+                    const int64_t j = static_cast<int64_t>(src[t]) * nb + sb * 8 + 2 * c;
+                    const int4 *xp = reinterpret_cast<const int4 *>(a.xq + j * 32);
+                    const int4 x0 = __ldg(xp), x1 = __ldg(xp + 1), x2 = __ldg(xp + 2), x3 = __ldg(xp + 3);
+                    const float2 d8 = __ldg(reinterpret_cast<const float2 *>(a.xd + j)), s8 = __ldg(reinterpret_cast<const float2 *>(a.xs + j));
+                    const int xa[16] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w, x2.x, x2.y, x2.z, x2.w, x3.x, x3.y, x3.z, x3.w};
+#pragma unroll
+                    for (int k = 0; k < kRows; ++k) {
+                        const int q[8] = {w[k].a.x, w[k].a.y, w[k].a.z, w[k].a.w, w[k].b.x, w[k].b.y, w[k].b.z, w[k].b.w};
+                        int i0 = 0, i1 = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            i0 = __dp4a(q[i] & 0x0f0f0f0f, xa[i], i0);
+                            i1 = __dp4a((q[i] >> 4) & 0x0f0f0f0f, xa[8 + i], i1);
+                        }
+                        float v = fmaf(ds0[k], d8.x * static_cast<float>(i0), acc[k][t]);
+                        v = fmaf(ds1[k], d8.y * static_cast<float>(i1), v);
+                        v = fmaf(-dm0[k], s8.x, v);
+                        acc[k][t] = fmaf(-dm1[k], s8.y, v);
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t) {
+                if (t >= m) break;
+#pragma unroll
+                for (int k = 0; k < kRows; ++k) acc[k][t] = warp_sum(acc[k][t]);
+                if (kSwiglu) {
+                    if (lane < 2) {
+                        const float g = lane ? acc[2][t] : acc[0][t], u = lane ? acc[3][t] : acc[1][t];
+                        out[t][o0 + lane] = g / (1.0f + expf(-g)) * u;
+                    }
+                } else if (lane < 4) {
+                    out[t][o0 + lane] = lane == 0 ? acc[0][t] : lane == 1 ? acc[1][t] : lane == 2 ? acc[2][t] : acc[3][t];
+                }
+            }
+        }
+        __syncthreads();
+        if (warp < m) {
+            const int64_t o = static_cast<int64_t>(blockIdx.x) * kTile + lane, at = static_cast<int64_t>(r + warp) * a.out_dim + o;
+            const float v = o < a.out_dim ? out[warp][lane] : 0.0f;
+            if (a.y && o < a.out_dim) a.y[at] = v;
+            if (a.yq) {  // out_dim is a multiple of 32
+                const float d = __fdiv_rn(warp_max(fabsf(v)), 127.0f);
+                const int code = q8_code(v, q8_scale(d)), total = warp_sum_int(code);
+                a.yq[at] = static_cast<int8_t>(code);
+                if (lane == 0) {
+                    a.yd[at / 32] = d;
+                    a.ys[at / 32] = __fmul_rn(d, static_cast<float>(total));
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// y[t] = residual[t] + sum_j w_j o[place_j], zeros behind out_dim; a thread has kVec columns
+template <int kVec>
+__global__ void __launch_bounds__(256) moe_combine_kernel(const MoeCombineArgs a)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t t = blockIdx.x;
+    const int col = (blockIdx.y * 256 + threadIdx.x) * kVec;
+    if (col >= a.out_pad) return;
+    float v[kVec];
+    if (col < a.out_dim) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] = a.residual ? a.residual[t * a.out_pad + col + e] : 0.0f;
+        for (int j = 0; j < a.top_k; ++j) {
+            const int place = a.places[t * a.top_k + j];
+            if (place < 0) continue;
+            if (place >= a.n_pairs) {
+                if (col == 0) set_error(a.err, DEV_BAD_LENGTH);
+                continue;
+            }
+            const float w = a.weights[t * a.top_k + j];
+            const float *o = a.o + static_cast<int64_t>(place) * a.out_dim + col;
+            if constexpr (kVec == 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(o));
+                v[0] = fmaf(w, x.x, v[0]);
+                v[1] = fmaf(w, x.y, v[1]);
+                v[2] = fmaf(w, x.z, v[2]);
+                v[3] = fmaf(w, x.w, v[3]);
+            } else {
+                v[0] = fmaf(w, __ldg(o), v[0]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] = 0.0f;
+    }
+    if constexpr (kVec == 4)
+        *reinterpret_cast<float4 *>(a.y + t * a.out_pad + col) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+        a.y[t * a.out_pad + col] = v[0];
+}
+
+template <typename K, typename A>
+cudaError_t launch(K kernel, dim3 grid, const A &a, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_use_pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_gemv(const MoeGemvArgs &a, cudaStream_t s)
+{
+    const dim3 grid(static_cast<unsigned>((a.out_dim + kTile - 1) / kTile), static_cast<unsigned>(std::min<int64_t>(a.n_pairs, 65535)));
+    return a.w2 ? launch(moe_gemv_kernel<true>, grid, a, s) : launch(moe_gemv_kernel<false>, grid, a, s);
+}
+
+cudaError_t launch_moe_combine(const MoeCombineArgs &a, int64_t n_tokens, cudaStream_t s)
+{
+    const int vec = a.out_dim % 4 == 0 && a.out_pad % 4 == 0 ? 4 : 1;
+    const dim3 grid(static_cast<unsigned>(n_tokens), static_cast<unsigned>((a.out_pad + 256 * vec - 1) / (256 * vec)));
+    return vec == 4 ? launch(moe_combine_kernel<4>, grid, a, s) : launch(moe_combine_kernel<1>, grid, a, s);
+}
+
+}  // namespace rz

@@ -314,4 +314,53 @@ bool paged_attention_tc_takes(int head_dim);
 size_t paged_attention_tc_part_bytes(int head_dim);
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, cudaStream_t s);
 
+// ---------------------------------------------------------------- an FFN of experts
+cudaError_t launch_residual_rmsnorm(const float *x, const float *delta, const float *gamma, float *sum, float *y, void *q8, int64_t m,
+                                    int64_t n, int64_t n_pad, float eps, cudaStream_t s);
+
+constexpr int kMoeMaxExperts = 512, kMoeMaxTopK = 32;
+constexpr int64_t kMoeMaxPairs = int64_t(1) << 27;  // rows of a call: n_tokens * top_k
+
+// Routing (moe_route.cu).  chunk is filled by the launcher.
+struct MoeRouteArgs {
+    const float *logits;
+    int64_t ld;
+    const int32_t *row_seq;
+    int64_t n_tokens, chunk;
+    int n_experts, top_k, renormalise;
+    float scale;
+    int32_t *experts;
+    float *weights;
+    int32_t *offsets, *rows, *places;
+    int32_t *hist;
+};
+int64_t moe_route_workspace_bytes(int64_t n_tokens, int n_experts);
+cudaError_t launch_moe_route(MoeRouteArgs a, cudaStream_t s);
+
+// Products grouped by expert (moe_gemv.cu): rows r of expert e, offsets[e] <= r < offsets[e + 1], read row
+// rows[r] / top_k of x (row r where rows is nullptr).  w2 != nullptr: silu(w1 x) * (w2 x).
+struct MoeGemvArgs {
+    const uint8_t *w1, *w2;  // [n_experts][out_dim][in_dim]
+    const int8_t *xq;
+    const float *xd, *xs;
+    const int32_t *offsets, *rows;
+    float *y;        // [n_pairs][out_dim], or nullptr
+    int8_t *yq;      // its Q8_1 form, or nullptr
+    float *yd, *ys;
+    int64_t out_dim;
+    int in_dim, n_experts, top_k, n_pairs;
+    unsigned *err;
+};
+cudaError_t launch_moe_gemv(const MoeGemvArgs &a, cudaStream_t s);
+
+struct MoeCombineArgs {
+    const float *o;  // [n_pairs][out_dim]
+    const int32_t *places;
+    const float *weights, *residual;
+    float *y;        // [n_tokens][out_pad]
+    int out_dim, out_pad, top_k, n_pairs;
+    unsigned *err;
+};
+cudaError_t launch_moe_combine(const MoeCombineArgs &a, int64_t n_tokens, cudaStream_t s);
+
 }  // namespace rz

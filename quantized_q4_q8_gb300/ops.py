@@ -22,6 +22,8 @@ __all__ = [
     "kv_q4_page_bytes", "PagedKVQ4", "PagedPlan", "rz_paged_plan", "paged_plan", "rz_qk_norm_rope", "qk_norm_rope",
     "rz_attention_paged_q4", "attention_paged_q4_workspace_bytes", "attention_paged_q4",
     "decode_layer_paged_workspace_bytes", "decode_layer_paged",
+    "rz_residual_rmsnorm", "residual_rmsnorm", "MoePlan", "moe_route_workspace_bytes", "rz_moe_route", "moe_route",
+    "rz_moe_swiglu", "moe_swiglu", "moe_down_workspace_bytes", "rz_moe_down", "moe_down",
 ]
 
 
@@ -753,4 +755,156 @@ def decode_layer_paged(x, layer: DeviceLayer, kv: PagedKVQ4, block_table, plan: 
          _on_device(plan.positions, i32, 1, dev, "plan").data_ptr(), plan.slots.data_ptr(), block_table.data_ptr(),
          _row_ld(block_table, max_blocks, "block_table"), max_blocks, plan.cu_rows.data_ptr(), plan.kv_len.data_ptr(), n, m,
          out.data_ptr(), _vector(ws, torch.uint8, 0, dev, "ws", more=True), ws.shape[0], _stream_on(stream, dev))
+    return out
+
+
+# ------------------------------------------------------------------ an FFN of experts
+def rz_residual_rmsnorm(x, delta, gamma, sum, y, q8, m, n, n_pad, eps, stream=None):
+    return call("rz_residual_rmsnorm", _ptr(x), _ptr(delta), _ptr(gamma), _ptr(sum), _ptr(y), _ptr(q8), m, n, n_pad, eps,
+                _stream(stream))
+
+
+def _matrix(t, dtype, rows, cols, dev, name):
+    """The address of a contiguous tensor [rows, cols]."""
+    _on_device(t, dtype, 2, dev, name)
+    if tuple(t.shape) != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{rows}, {cols}], got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def residual_rmsnorm(x, delta, gamma, n: int, n_pad: int, eps: float, want_y: bool = True, want_q8: bool = True, sum_out=None,
+                     stream=None):
+    """x + delta (f32 [m, n_pad] each; delta may be None), its RMSNorm and the Q8_1 form of that (see rz.h), in
+    one pass.  Returns (sum, y, q8), y and q8 None where not wanted; sum_out may be x or delta."""
+    import torch
+    f32, dev = torch.float32, torch.cuda.current_device()
+    m = _on_device(x, f32, 2, dev, "x").shape[0]
+    x_at = _matrix(x, f32, m, n_pad, dev, "x")
+    delta_at = None if delta is None else _matrix(delta, f32, m, n_pad, dev, "delta")
+    if sum_out is None:
+        sum_out = _new((m, n_pad), f32, dev, stream)
+    y = _new((m, n_pad), f32, dev, stream) if want_y else None
+    q8 = _new((q8_1_size(m, n_pad),), torch.uint8, dev, stream) if want_q8 else None
+    call("rz_residual_rmsnorm", x_at, delta_at, _vector(gamma, f32, n, dev, "gamma"), _matrix(sum_out, f32, m, n_pad, dev, "sum_out"),
+         _ptr(y), _ptr(q8), m, n, n_pad, eps, _stream_on(stream, dev))
+    return sum_out, y, q8
+
+
+class MoePlan:
+    """Which experts the tokens of a batch go to (rz_moe_plan): experts, weights [n_tokens, top_k], offsets
+    [n_experts + 1], rows and places [n_tokens * top_k]; moe_route fills it, and it is kept from step
+    to step.  Tensors given by name are taken as they are."""
+
+    def __init__(self, n_tokens: int, n_experts: int, top_k: int, device="cuda", **given):
+        import torch
+        from ._lib import MoePlanStruct
+        i32, pairs = torch.int32, n_tokens * top_k
+        shapes = {"experts": ((n_tokens, top_k), i32), "weights": ((n_tokens, top_k), torch.float32), "offsets": ((n_experts + 1,), i32),
+                  "rows": ((pairs,), i32), "places": ((pairs,), i32)}
+        if not set(given) <= set(shapes):
+            raise TypeError(f"unknown tensors {sorted(set(given) - set(shapes))}")
+        self.n_tokens, self.n_experts, self.top_k = n_tokens, n_experts, top_k
+        for name, (shape, dtype) in shapes.items():
+            t = given.get(name)
+            if t is None:
+                t = torch.zeros(shape, dtype=dtype, device=device)
+            elif _on_device(t, dtype, len(shape), t.get_device(), name).shape != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {list(shape)}")
+            setattr(self, name, t)
+        self.dev = self.experts.get_device()
+        if any(getattr(self, name).get_device() != self.dev for name in shapes):
+            raise ValueError("the tensors of a plan must be on one device")
+        self.struct = MoePlanStruct(*[getattr(self, name).data_ptr() for name in shapes], n_tokens, n_experts, top_k)
+        self.ref = C.byref(self.struct)
+
+
+def _plan_on(plan, dev):
+    if plan.dev != dev:
+        raise ValueError("the plan is not on the current device")
+    return plan.ref
+
+
+def moe_route_workspace_bytes(n_tokens: int, n_experts: int) -> int:
+    return int(load().rz_moe_route_workspace_bytes(n_tokens, n_experts))
+
+
+def rz_moe_route(logits, ld, row_seq, plan, renormalise, scale, ws, ws_bytes, stream=None):
+    return call("rz_moe_route", _ptr(logits), ld, _ptr(row_seq), plan.ref, renormalise, scale, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def _scratch(ws, need, dev, stream):
+    """(address, bytes) of the workspace given, or of a new one of `need` bytes and the tensor that holds it."""
+    import torch
+    if ws is None:
+        ws = _new((max(need, 16),), torch.uint8, dev, stream)
+    return _vector(ws, torch.uint8, 0, dev, "ws", more=True), ws.shape[0], ws
+
+
+def moe_route(logits, plan: MoePlan, renormalise: bool = True, scale: float = 1.0, row_seq=None, ws=None, stream=None) -> MoePlan:
+    """The top_k experts of each token by its logits (f32 [n_tokens, n_experts], rows may be strided), their softmax
+    weights, and the rows by expert (see rz.h), into `plan`.  row_seq int32 [n_tokens]: negative for tokens without
+    a request."""
+    import torch
+    dev = torch.cuda.current_device()
+    if _on_device(logits, torch.float32, 2, dev, "logits").shape[0] != plan.n_tokens:
+        raise ValueError("logits must have a row for each token of the plan")
+    at, size, ws = _scratch(ws, moe_route_workspace_bytes(plan.n_tokens, plan.n_experts), dev, stream)
+    call("rz_moe_route", logits.data_ptr(), _row_ld(logits, plan.n_experts, "logits"),
+         None if row_seq is None else _vector(row_seq, torch.int32, plan.n_tokens, dev, "row_seq", more=True), _plan_on(plan, dev),
+         1 if renormalise else 0, scale, at, size, _stream_on(stream, dev))
+    return plan
+
+
+def _expert_weights(w, n_experts, out_dim, in_dim, dev, name):
+    """The address of Q4_K weights [n_experts][out_dim][in_dim]: a contiguous uint8 tensor of any shape."""
+    import torch
+    if not isinstance(w, torch.Tensor) or w.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if w.dtype != torch.uint8:
+        raise TypeError(f"{name} must be {torch.uint8}, got {w.dtype}")
+    if not w.is_contiguous() or w.numel() != n_experts * q4k_bytes(out_dim, in_dim):
+        raise ValueError(f"{name} must hold {n_experts} x {out_dim} x {in_dim} Q4_K weights, contiguous")
+    return w.data_ptr()
+
+
+def rz_moe_swiglu(w_gate, w_up, x_q8, plan, inter, in_dim, h, h_q8, stream=None):
+    return call("rz_moe_swiglu", _ptr(w_gate), _ptr(w_up), _ptr(x_q8), plan.ref, inter, in_dim, _ptr(h), _ptr(h_q8), _stream(stream))
+
+
+def moe_swiglu(w_gate, w_up, x_q8, plan: MoePlan, inter: int, in_dim: int, out=None, out_q8=None, want_h: bool = True, stream=None):
+    """silu(gate) * up of each row of the plan with its expert (see rz.h): f32 [n_tokens * top_k, inter] in the plan's
+    order (None with want_h False), and its Q8_1 form into out_q8 where that is given."""
+    import torch
+    u8, dev, pairs = torch.uint8, torch.cuda.current_device(), plan.n_tokens * plan.top_k
+    if out is None and want_h:
+        out = _new((pairs, inter), torch.float32, dev, stream)
+    call("rz_moe_swiglu", _expert_weights(w_gate, plan.n_experts, inter, in_dim, dev, "w_gate"),
+         _expert_weights(w_up, plan.n_experts, inter, in_dim, dev, "w_up"),
+         _vector(x_q8, u8, q8_1_size(plan.n_tokens, in_dim), dev, "x_q8"), _plan_on(plan, dev), inter, in_dim,
+         None if out is None else _matrix(out, torch.float32, pairs, inter, dev, "out"),
+         None if out_q8 is None else _vector(out_q8, u8, q8_1_size(pairs, inter), dev, "out_q8"), _stream_on(stream, dev))
+    return out
+
+
+def moe_down_workspace_bytes(n_tokens: int, top_k: int, out_dim: int) -> int:
+    return int(load().rz_moe_down_workspace_bytes(n_tokens, top_k, out_dim))
+
+
+def rz_moe_down(w_down, h_q8, plan, residual, y, out_dim, out_pad, in_dim, ws, ws_bytes, stream=None):
+    return call("rz_moe_down", _ptr(w_down), _ptr(h_q8), plan.ref, _ptr(residual), _ptr(y), out_dim, out_pad, in_dim, _ptr(ws), ws_bytes,
+                _stream(stream))
+
+
+def moe_down(w_down, h_q8, plan: MoePlan, out_dim: int, in_dim: int, residual=None, out=None, out_pad: int = 0, ws=None, stream=None):
+    """The product back of each row of the plan, the weighted sum of a token's rows and the residual (see rz.h):
+    f32 [n_tokens, out_pad or out_dim].  out may be residual."""
+    import torch
+    f32, dev, out_pad = torch.float32, torch.cuda.current_device(), out_pad or out_dim
+    if out is None:
+        out = _new((plan.n_tokens, out_pad), f32, dev, stream)
+    at, size, ws = _scratch(ws, moe_down_workspace_bytes(plan.n_tokens, plan.top_k, out_dim), dev, stream)
+    call("rz_moe_down", _expert_weights(w_down, plan.n_experts, out_dim, in_dim, dev, "w_down"),
+         _vector(h_q8, torch.uint8, q8_1_size(plan.n_tokens * plan.top_k, in_dim), dev, "h_q8"), _plan_on(plan, dev),
+         None if residual is None else _matrix(residual, f32, plan.n_tokens, out_pad, dev, "residual"),
+         _matrix(out, f32, plan.n_tokens, out_pad, dev, "out"), out_dim, out_pad, in_dim, at, size, _stream_on(stream, dev))
     return out
