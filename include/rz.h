@@ -648,10 +648,15 @@ rz_status rz_moe_route(const float *logits, int64_t ld, const int32_t *row_seq, 
  *   h         f32 [n_tokens * top_k][inter] output, in the plan's order of rows, or NULL
  *   h_q8      Q8_1 of n_tokens * top_k rows of inter (rz_moe_down's input): exactly the quantisation of
  *             h; or NULL (inter % 32 == 0)
+ *   workspace rz_moe_swiglu_workspace_bytes bytes; no initialisation; may be NULL where that is 0
  *   in_dim % 256 == 0; all 16-byte aligned.  Rows behind offsets[n_experts] stay as they were.
+ * Sums are f32-accurate: exact integer dots for few rows of an expert, else the tensor cores, where
+ * activations enter with 22 bits and a scale d below 2^-13 dmin is rounded to 11 bits (its codes then
+ * make less than an eighth of a min).
  */
+size_t rz_moe_swiglu_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k, int64_t in_dim);
 rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, const rz_moe_plan *plan, int64_t inter,
-                        int64_t in_dim, float *h, void *h_q8, rz_stream stream);
+                        int64_t in_dim, float *h, void *h_q8, void *workspace, size_t ws_bytes, rz_stream stream);
 
 /*
  * rz_moe_down -- y_t = residual_t + sum_j weights[t][j] D_e h_r, r = places[t][j], e its expert, the
@@ -662,7 +667,7 @@ rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, 
  *             without experts gets its residual.
  *   workspace rz_moe_down_workspace_bytes bytes, 16-byte aligned; no initialisation
  */
-size_t rz_moe_down_workspace_bytes(int64_t n_tokens, int32_t top_k, int64_t out_dim);
+size_t rz_moe_down_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k, int64_t out_dim, int64_t in_dim);
 rz_status rz_moe_down(const void *w_down, const void *h_q8, const rz_moe_plan *plan, const float *residual, float *y,
                       int64_t out_dim, int64_t out_pad, int64_t in_dim, void *workspace, size_t ws_bytes,
                       rz_stream stream);

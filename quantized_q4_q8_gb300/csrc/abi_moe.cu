@@ -119,6 +119,26 @@ void swiglu_args(MoeGemvArgs &a, const void *w_gate, const void *w_up, const voi
     a.ys = const_cast<float *>(o.s);
 }
 
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// B of the tensor-core kernel, for that many rows of x; the integer kernel needs none
+int64_t pack_bytes(int64_t x_rows, int64_t n_pairs, int n_experts, int64_t in_dim)
+{
+    return moe_columns(n_pairs, n_experts) ? moe_pack_bytes(x_rows, in_dim) : 0;
+}
+
+int64_t swiglu_workspace_bytes(int64_t n_tokens, int n_experts, int top_k, int64_t in_dim)
+{
+    return pack_bytes(n_tokens, n_tokens * top_k, n_experts, in_dim);
+}
+
+// the rows' products, then B
+int64_t down_workspace_bytes(int64_t n_tokens, int n_experts, int top_k, int64_t out_dim, int64_t in_dim)
+{
+    const int64_t pairs = n_tokens * top_k;
+    return align256(pairs * out_dim * 4) + pack_bytes(pairs, pairs, n_experts, in_dim);
+}
+
 cudaError_t run_down(const void *w_down, const void *h_q8, const rz_moe_plan *p, const float *residual, float *y, int64_t out_dim,
                      int64_t out_pad, int64_t in_dim, void *workspace, cudaStream_t s)
 {
@@ -141,11 +161,9 @@ cudaError_t run_down(const void *w_down, const void *h_q8, const rz_moe_plan *p,
     c.top_k = p->top_k;
     c.n_pairs = a.n_pairs;
     c.err = a.err;
-    const cudaError_t e = launch_moe_gemv(a, s);
+    const cudaError_t e = launch_moe_product(a, static_cast<uint8_t *>(workspace) + align256(a.n_pairs * out_dim * 4), s);
     return e != cudaSuccess ? e : launch_moe_combine(c, p->n_tokens, s);
 }
-
-int64_t down_workspace_bytes(int64_t n_tokens, int top_k, int64_t out_dim) { return n_tokens * top_k * out_dim * 4; }
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
 
@@ -243,8 +261,16 @@ rz_status rz_moe_route(const float *logits, int64_t ld, const int32_t *row_seq, 
     return launched(fn, run_route(logits, ld, row_seq, plan, renormalise != 0, scale, workspace, static_cast<cudaStream_t>(stream)));
 }
 
+size_t rz_moe_swiglu_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k, int64_t in_dim)
+{
+    const char *fn = "rz_moe_swiglu_workspace_bytes";
+    record_error(RZ_OK, "");
+    if (check_counts(fn, n_tokens, n_experts, top_k) != RZ_OK || check_in_dim(fn, in_dim) != RZ_OK) return 0;
+    return swiglu_workspace_bytes(n_tokens, n_experts, top_k, in_dim);
+}
+
 rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, const rz_moe_plan *plan, int64_t inter, int64_t in_dim,
-                        float *h, void *h_q8, rz_stream stream)
+                        float *h, void *h_q8, void *workspace, size_t ws_bytes, rz_stream stream)
 {
     const char *fn = "rz_moe_swiglu";
     record_error(RZ_OK, "");
@@ -256,18 +282,20 @@ rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, 
     const void *bufs[] = {w_gate, w_up, x_q8, h, h_q8};
     for (const void *p : bufs)
         if (!aligned(p, 16)) return fail(RZ_ERR_ALIGN, "%s: buffers must be 16-byte aligned", fn);
+    RZ_TRY(check_workspace(fn, workspace, ws_bytes, swiglu_workspace_bytes(plan->n_tokens, plan->n_experts, plan->top_k, in_dim)));
     RZ_TRY(ensure_device());
     MoeGemvArgs a{};
     swiglu_args(a, w_gate, w_up, x_q8, plan, inter, in_dim, h, h_q8);
-    return launched(fn, launch_moe_gemv(a, static_cast<cudaStream_t>(stream)));
+    return launched(fn, launch_moe_product(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
-size_t rz_moe_down_workspace_bytes(int64_t n_tokens, int32_t top_k, int64_t out_dim)
+size_t rz_moe_down_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k, int64_t out_dim, int64_t in_dim)
 {
     const char *fn = "rz_moe_down_workspace_bytes";
     record_error(RZ_OK, "");
-    if (check_counts(fn, n_tokens, kMoeMaxExperts, top_k) != RZ_OK || check_out_dim(fn, "out_dim", out_dim) != RZ_OK) return 0;
-    return align16(down_workspace_bytes(n_tokens, top_k, out_dim));
+    if (check_counts(fn, n_tokens, n_experts, top_k) != RZ_OK || check_out_dim(fn, "out_dim", out_dim) != RZ_OK || check_in_dim(fn, in_dim) != RZ_OK)
+        return 0;
+    return down_workspace_bytes(n_tokens, n_experts, top_k, out_dim, in_dim);
 }
 
 rz_status rz_moe_down(const void *w_down, const void *h_q8, const rz_moe_plan *plan, const float *residual, float *y, int64_t out_dim,
@@ -279,7 +307,7 @@ rz_status rz_moe_down(const void *w_down, const void *h_q8, const rz_moe_plan *p
     RZ_TRY(check_plan(fn, plan));
     RZ_TRY(check_down(fn, w_down, residual, y, out_dim, out_pad, in_dim));
     if (!aligned(h_q8, 16)) return fail(RZ_ERR_ALIGN, "%s: buffers must be 16-byte aligned", fn);
-    RZ_TRY(check_workspace(fn, workspace, ws_bytes, down_workspace_bytes(plan->n_tokens, plan->top_k, out_dim)));
+    RZ_TRY(check_workspace(fn, workspace, ws_bytes, down_workspace_bytes(plan->n_tokens, plan->n_experts, plan->top_k, out_dim, in_dim)));
     RZ_TRY(ensure_device());
     return launched(fn, run_down(w_down, h_q8, plan, residual, y, out_dim, out_pad, in_dim, workspace, static_cast<cudaStream_t>(stream)));
 }

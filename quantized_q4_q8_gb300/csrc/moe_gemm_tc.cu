@@ -1,0 +1,857 @@
+// moe_gemm_tc.cu -- products grouped by expert of many rows on tcgen05.mma: Q4_K weights of
+// each expert against the Q8_1 rows that chose it (formulas and arguments of moe_gemv.cu).
+//
+// A tile is two matrices of 128 weight rows (gate and up of the same outputs; or 256
+// outputs) by kN rows of one expert.  For each super-block of 256 weights
+//   D = A B,  A [128][256 + 32] the weights' codes, B [256 + 32][kN] the activations
+//   sum += g * (2^E * D)                 g a scale for each weight row, E an exponent for each column
+// A holds sc * code (at most 945, exact in f16) and, in 32 further columns, the mins over the scale;
+// it is made in registers and stored in tensor memory, which leaves shared memory's bandwidth to B.
+// B holds d8 * code / 2^E as two f16 pieces (22 bits), so that one super-block is one
+// accumulation of 2 x 16 instructions of K = 16, and accumulators are read once for 256 weights:
+// products of the codes alone, exact in f16, would have to be read and scaled for each 32
+// (rz_q4k_q8_gemm: 344 TFLOP/s of the formula's operations).  A kernel before this one forms B's pieces,
+// once for a row of activations however many experts and tiles of outputs read it.
+//
+// The min term -sum_j dmin m_j s_j goes into the same accumulators: A's r_j = -m_j dmin / (8 d) and
+// B's 8 s_j / 2^E, two f16 pieces each, all four products.  So g = d.  Where dmin is over 2^13 times
+// d (f16 would not hold r_j; d = 0 among them), g = dmin, and the codes are scaled by d / dmin
+// instead, rounded to f16: 2^-12 of codes that are less than an eighth of dmin.
+//
+// The tensor cores cut what they add to an accumulator; after 34 additions it starts again, so
+// that the loss stays near 2^-22.  A super-block with a scale that is no number gives its row NaN (g),
+// a block of x its column (B's pieces).
+//
+// Roles of the warps, one CTA for each SM, items (expert, tile of its outputs, tile of its rows) in turn:
+//   warps 0, 1   issue the products of the first and second matrix (what synchronises costs a warp some 50 to 100
+//                cycles each, so that one warp for both was the bottleneck)
+//   warp 2       copies the raw weights, 128 rows x 144 bytes a box
+//   warp 3       gathers B's rows by the plan, 16 bytes a lane (cp.async)
+//   groups of 4  unpack A, a thread for a weight row, the groups taking the steps of both matrices in turn
+//   8 warps      add up: a thread has a weight row of both matrices and half of the columns
+// Few rows (kN <= 32): the two pieces of B stand side by side as 2 kN columns, which halves the instructions.
+//
+// Every wait is bounded; after one that runs out every role stops, copies and products in flight
+// are waited for, and tensor memory is freed.
+#include <math.h>
+
+#include <algorithm>
+
+#include "mma_f16.cuh"
+#include "rz_common.cuh"
+#include "rz_kernels.h"
+
+namespace rz {
+namespace {
+
+constexpr int kRawBytes = 144 * 128;
+constexpr int kHdr = 4;      // super-blocks whose scales are held
+constexpr int kBufD = 3;     // accumulators
+constexpr int kPackBytes = 1024;  // of B for a row and super-block: of each 64 values the high pieces, then the low ones
+
+template <int N>
+struct Cfg {
+    static constexpr bool kStack = N <= 32;           // pieces side by side
+    static constexpr int kColsD = kStack ? 2 * N : N;
+    static constexpr int kChunks = N >= 64 ? 1 : 2;   // of 64 weights, in a step
+    static constexpr bool kOwnMins = N >= 64;         // the mins are a step of their own (no room in tensor memory for wider slots)
+    static constexpr int kSteps = 4 / kChunks + (kOwnMins ? 1 : 0);  // of a super-block, the last one with the mins
+    static constexpr int kGroups = N >= 64 ? 2 : 4;   // that unpack A: half of them each matrix, in turn its steps
+    static constexpr int kShare = kGroups / 2;
+    static constexpr int kSlotsA = N == 64 ? 4 : 2;   // of A for each matrix
+    static constexpr int kBytesB = kChunks * N * 256; // two pieces of 64 * kChunks values
+    static constexpr int kSlotB = kBytesB + (kOwnMins ? 0 : N * 64);
+    static constexpr int kRingB = N == 128 ? 4 : 5;
+    static constexpr int kLagB = 2;                   // steps whose gathers are under way while the next is issued
+    static constexpr int kGather = N >= 32 ? 4 : 2;   // warps that gather B
+    static constexpr int kRowsB = N / 8 / kGather;    // rows of a lane there
+    static constexpr int kRingRaw = N == 128 ? 4 : N == 16 ? 8 : 6;
+    static constexpr int kColA = kBufD * kColsD;      // tensor memory: accumulators, then A
+    static constexpr int kWidthA = 32 * kChunks + (kOwnMins ? 0 : 16);
+    static constexpr int kHalf = N / 2;               // columns of a thread that adds up
+    static constexpr int kFirstUnpack = 8, kFirstSum = kFirstUnpack + 4 * kGroups;
+    static constexpr int kThreads = 32 * (kFirstSum + 8);
+    // registers of the roles (0: as launched)
+    static constexpr int kRegsIssue = N == 128 ? 32 : 0, kRegsGather = N == 128 ? 32 : 0, kRegsUnpack = N == 128 ? 56 : 0,
+                         kRegsSum = N == 128 ? 152 : 0;
+    static constexpr int off_b = 0;
+    static constexpr int off_raw = off_b + kRingB * kSlotB;
+    static constexpr int off_g = off_raw + kRingRaw * kRawBytes;   // [kHdr][2][128]
+    static constexpr int off_cs = off_g + kHdr * 2 * 128 * 4;      // [kHdr][N]
+    static constexpr int off_src = off_cs + kHdr * N * 4;          // [N]
+    static constexpr int off_cum = off_src + N * 4;                // int64 [kMoeMaxExperts + 1]
+    static constexpr int off_bars = off_cum + 8 * (kMoeMaxExperts + 1) + 8;
+    static constexpr int bytes = off_bars + 640 + 1024;
+    static_assert(kColA + 2 * kSlotsA * kWidthA <= 512, "tensor memory");
+    static_assert(off_raw % 128 == 0, "copies start on 128 bytes");
+    static_assert(bytes <= 227 * 1024, "shared memory");
+    // A slot of A is filled again by the group that filled it before, or by one that has seen the product before that done: otherwise
+    // a wait could take the phase before for the one it waits for
+    static_assert(kSlotsA % kShare == 0 && kLagB < kRingB && kRingRaw % 2 == 0, "rings");
+    // Scales of super-block k take the place of those of k - kHdr, added up by then: whoever writes them has seen the products of a
+    // step at most kRingB (or kSlotsA) before done, whose accumulators were free, which takes all but the last three of those before
+    static_assert((kRingB + kSteps - 1) / kSteps + 1 <= kHdr, "scales");
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static_assert(kRegsSum == 0 || 128 * (kRegsIssue + kRegsGather + kGroups * kRegsUnpack) + 256 * kRegsSum <= kThreads * kLaunchRegs, "registers");
+};
+
+struct Bars {
+    uint64_t a_full[2][4], a_empty[2][4], b_full[6], b_empty[6], raw_full[8], raw_empty[8], d_full[kBufD], d_empty[kBufD], h_full[kHdr], done[2];
+    uint32_t tmem;
+    int gave_up;
+};
+static_assert(sizeof(Bars) <= 640, "barriers");
+
+struct TcArgs {
+    CUtensorMap map1, map2;
+    MoeGemvArgs g;
+    const uint8_t *pack, *mins;  // B: [rows][super-blocks][kPackBytes], [rows][super-blocks][32]
+    const float *col_scale;      // 2^E [rows][super-blocks]
+};
+
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t stride)
+{
+    // K-major, no swizzle: core matrices of 8 rows x 16 bytes, 128 bytes apart along K, groups of 8 rows `stride` apart
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | (1ull << 46);
+}
+__host__ __device__ constexpr uint32_t idesc_f16(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 8 columns of the warp's 32 rows, waited for in the same statement
+__device__ __forceinline__ void tm_load8(uint32_t at, float (&v)[16])
+{
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(at)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 8 columns at one place, and 8 at another
+__device__ __forceinline__ void tm_load8x2(uint32_t at, uint32_t at2, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at), "r"(at2)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// s += g * (v * c) on two values at once
+__device__ __forceinline__ void add_scaled(float &s0, float &s1, float v0, float v1, float c0, float c1, float g)
+{
+    asm("{\n\t.reg .b64 s, v, c, g;\n\t"
+        "mov.b64 s, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\tmov.b64 g, {%6, %6};\n\t"
+        "mul.rn.f32x2 v, v, c;\n\tfma.rn.f32x2 s, g, v, s;\n\tmov.b64 {%0, %1}, s;\n\t}"
+        : "+f"(s0), "+f"(s1)
+        : "f"(v0), "f"(v1), "f"(c0), "f"(c1), "f"(g));
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+// 16 bytes global -> shared, zeros where `bytes` is 0; and 4 bytes
+__device__ __forceinline__ void gather16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void gather4(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t hneg2u(uint32_t a) { return a ^ 0x80008000u; }
+
+// Shared memory by 32-bit address (a pointer rounded up to 1024 bytes is a generic one to the compiler)
+__device__ __forceinline__ uint4 lds4(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 lds4f(uint32_t at)
+{
+    const uint4 v = lds4(at);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ float lds1f(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ int lds1i(uint32_t at)
+{
+    int v;
+    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts1(uint32_t at, uint32_t x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory"); }
+
+// Bounded waits; false after a timeout or when another role gave up.
+__device__ __forceinline__ bool give_up(Bars &b, unsigned *err)
+{
+    volatile int *flag = &b.gave_up;
+    if (!*flag) {
+        *flag = 1;
+        set_error(err, DEV_TIMEOUT_MOE);
+    }
+    return false;
+}
+__device__ __forceinline__ bool wait_one(uint64_t *bar, unsigned par, Bars &b, unsigned *err)
+{
+    volatile int *flag = &b.gave_up;
+    for (uint32_t i = 0; i < kWaitLimit / 8; ++i) {
+        if (mbar_try_wait(bar, par)) return true;
+        if ((i & 63u) == 63u && *flag) return false;
+    }
+    return give_up(b, err);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned par, Bars &b, unsigned *err)
+{
+    // All lanes wait for the same barrier: lanes that wait for different ones drift apart, and what follows (tcgen05.ld, products
+    // issued for the warp) needs the warp together.
+    const bool ok = __all_sync(0xffffffffu, wait_one(bar, par, b, err));
+    __syncwarp();
+    return ok;
+}
+
+// A super-block's two scales; wide: the mins' is the unit (see above).
+struct Head {
+    float d, dmin;
+    bool wide, fine;
+};
+__device__ __forceinline__ Head head_of(uint32_t word)
+{
+    const float d = h2f(static_cast<uint16_t>(word & 0xffffu)), dmin = h2f(static_cast<uint16_t>(word >> 16));
+    return {d, dmin, fabsf(dmin) > 8192.0f * fabsf(d), isfinite(d) && isfinite(dmin)};
+}
+
+// Whether a phase is complete, at once.
+__device__ __forceinline__ bool test_phase(uint64_t *bar, unsigned par)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(par)
+        : "memory");
+    return ok != 0;
+}
+
+// Item number i: its expert, tile of outputs and first row.
+struct Item {
+    int e, rt, row, m;  // m rows, up to kN
+};
+template <int N>
+__device__ __forceinline__ Item item_at(int64_t i, const int64_t *cum, const MoeGemvArgs &g)
+{
+    int lo = 0, hi = g.n_experts;  // cum[lo] <= i < cum[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= i)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int first = g.offsets[lo], end = g.offsets[lo + 1];
+    const int tiles = (end - first + N - 1) / N;
+    const int64_t at = i - cum[lo];
+    Item w;
+    w.e = lo;
+    w.rt = static_cast<int>(at / tiles);
+    w.row = first + static_cast<int>(at - static_cast<int64_t>(w.rt) * tiles) * N;
+    w.m = min(N, end - w.row);
+    return w;
+}
+
+// B's pieces of a row and super-block: a warp, 8 codes a lane.
+constexpr int kPackWarps = 8;
+__global__ void __launch_bounds__(32 * kPackWarps) moe_pack_kernel(const int8_t *__restrict__ q, const float *__restrict__ d8,
+                                                                   const float *__restrict__ s8, uint8_t *__restrict__ pack,
+                                                                   uint8_t *__restrict__ mins, float *__restrict__ col_scale, int64_t cells)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t cell = static_cast<int64_t>(blockIdx.x) * kPackWarps + (threadIdx.x >> 5);
+    pdl_launch_dependents();
+    pdl_wait();
+    if (cell >= cells) return;
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q + cell * 256) + lane);
+    const float d = __ldg(d8 + cell * 8 + (lane >> 2)), s = __ldg(s8 + cell * 8 + (lane & 7));
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(d) & 0x7fffffffu);
+    const uint32_t e = min(top >> 23, 252u);
+    const float up = __uint_as_float((253u - e) << 23);  // the largest scale becomes 1/2 .. 1
+    const float v = d * up, vh = __half2float(__float2half_rn(v));
+    const uint32_t dh = pack2(vh, vh), dl = pack2(v - vh, v - vh);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        // codes as 1024 + 128 + code, which is f16 0x64xx, in the order 0, 2, 1, 3
+        const uint32_t u = (i ? w.y : w.x) ^ 0x80808080u;
+        const uint32_t e02 = hsub2u(__byte_perm(u, 0x64646464u, 0x4240), 0x64806480u), e13 = hsub2u(__byte_perm(u, 0x64646464u, 0x4341), 0x64806480u);
+        hi[2 * i] = hmul2u(e02, dh);
+        hi[2 * i + 1] = hmul2u(e13, dh);
+        lo[2 * i] = hfma2u(e02, dl, hfma2u(e02, dh, hneg2u(hi[2 * i])));  // the inner one is exact
+        lo[2 * i + 1] = hfma2u(e13, dl, hfma2u(e13, dh, hneg2u(hi[2 * i + 1])));
+    }
+    uint8_t *to = pack + cell * kPackBytes + (lane >> 3) * 256 + (lane & 7) * 16;
+    *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(to + 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (lane < 8) {
+        const float t = s * up * 8.0f;
+        const __half sh = __float2half_rn(t);
+        __half *m = reinterpret_cast<__half *>(mins + cell * 32);
+        m[lane] = sh;
+        m[8 + lane] = __float2half_rn(t - __half2float(sh));
+        if (lane == 0) col_scale[cell] = __uint_as_float((e + 1u) << 23);
+    }
+}
+
+// Ring position `by` further.
+__device__ __forceinline__ void ring_add(RingPos &p, int by, int n)
+{
+    p.s += by;
+    if (p.s >= n) {
+        p.s -= n;
+        p.par ^= 1u;
+    }
+}
+
+template <int N, bool kSwiglu>
+__global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const __grid_constant__ TcArgs a)
+{
+    using C = Cfg<N>;
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    Bars &b = *reinterpret_cast<Bars *>(sm + C::off_bars);
+    int64_t *cum = reinterpret_cast<int64_t *>(sm + C::off_cum);
+    const uint32_t sm32 = smem_u32(sm);
+    const MoeGemvArgs &g = a.g;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int nsb = g.in_dim / 256;
+    const int row_tiles = static_cast<int>((g.out_dim + (kSwiglu ? 127 : 255)) / (kSwiglu ? 128 : 256));
+
+    if (tid == 0) {
+        for (int i = 0; i < 2 * C::kSlotsA; ++i) {
+            mbar_init(&b.a_full[i & 1][i >> 1], 4);
+            mbar_init(&b.a_empty[i & 1][i >> 1], 1);
+        }
+        for (int i = 0; i < C::kRingB; ++i) {
+            mbar_init(&b.b_full[i], C::kGather);
+            mbar_init(&b.b_empty[i], 2);
+        }
+        for (int i = 0; i < C::kRingRaw; ++i) {
+            mbar_init(&b.raw_full[i], 1);
+            mbar_init(&b.raw_empty[i], 4 * C::kShare);
+        }
+        for (int i = 0; i < kBufD; ++i) {
+            mbar_init(&b.d_full[i], 1);
+            mbar_init(&b.d_empty[i], 8);
+        }
+        for (int i = 0; i < kHdr; ++i) mbar_init(&b.h_full[i], 8 + C::kGather);
+        mbar_init(&b.done[0], 1);
+        mbar_init(&b.done[1], 1);
+        b.gave_up = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&a.map1);
+        if (kSwiglu) tma_prefetch_desc(&a.map2);
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&b.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    // items before each expert
+    if (warp == 1) {
+        int64_t base = 0;
+        for (int e0 = 0; e0 < g.n_experts; e0 += 32) {
+            const int e = e0 + lane;
+            int64_t own = 0;
+            if (e < g.n_experts) {
+                const int lo = g.offsets[e], hi = g.offsets[e + 1];
+                if (lo >= 0 && hi > lo && hi <= g.n_pairs) own = static_cast<int64_t>((hi - lo + N - 1) / N) * row_tiles;
+            }
+            int64_t v = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (e < g.n_experts) cum[e] = base + v - own;
+            base += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) cum[g.n_experts] = base;
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = b.tmem;
+    const int64_t items = cum[g.n_experts];
+    // this CTA's super-blocks, all items one after another
+    const int64_t my_items = items > blockIdx.x ? (items - blockIdx.x + gridDim.x - 1) / gridDim.x : 0, blocks = my_items * nsb;
+
+    if (warp < 4) {
+        if constexpr (C::kRegsIssue) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsIssue ? C::kRegsIssue : 24));
+        if (warp < 2) {
+            // -------------------------------------------------------- products of matrix `warp`
+            const int mt = warp;
+            RingPos pa{0, 0}, pb{0, 0}, pd{mt, 0};
+            bool ok = true;
+            for (int64_t k = 0; k < blocks && ok; ++k) {
+#pragma unroll
+                for (int step = 0; step < C::kSteps; ++step) {
+                    // the phases tested together, one latency; what is not complete is waited for
+                    const bool ra = test_phase(&b.a_full[mt][pa.s], pa.par), rb = test_phase(&b.b_full[pb.s], pb.par);
+                    const bool rd = step > 0 || test_phase(&b.d_empty[pd.s], pd.par ^ 1u);
+                    if (!__all_sync(0xffffffffu, ra && rb && rd)) {
+                        if (step == 0 && !(ok = wait_warp(&b.d_empty[pd.s], pd.par ^ 1u, b, g.err))) break;
+                        if (!(ok = wait_warp(&b.b_full[pb.s], pb.par, b, g.err))) break;
+                        if (!(ok = wait_warp(&b.a_full[mt][pa.s], pa.par, b, g.err))) break;
+                    }
+                    fence_after();
+                    if (lane == 0) {
+                        const uint32_t d = tmem + pd.s * C::kColsD;
+                        const uint32_t ta = tmem + C::kColA + (mt * C::kSlotsA + pa.s) * C::kWidthA;
+                        const uint32_t tb = sm32 + C::off_b + pb.s * C::kSlotB;
+                        if (!C::kOwnMins || step < C::kSteps - 1) {
+                            const uint64_t desc = operand_desc(tb, C::kChunks * 1024);
+#pragma unroll
+                            for (int i = 0; i < 4 * C::kChunks; ++i) {
+                                mma_ts(d, ta + 8 * i, desc + 16 * i, idesc_f16(C::kColsD), step > 0 || i > 0);
+                                if constexpr (!C::kStack) mma_ts(d, ta + 8 * i, desc + (N * C::kChunks * 8 + 16 * i), idesc_f16(N), 1);
+                            }
+                        }
+                        if (step == C::kSteps - 1) {
+                            const uint64_t desc = operand_desc(tb + (C::kOwnMins ? 0 : C::kBytesB), 512);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) mma_ts(d, ta + (C::kOwnMins ? 0 : 32 * C::kChunks) + 8 * i, desc + 16 * i, idesc_f16(N), 1);
+                        }
+                        commit(&b.a_empty[mt][pa.s]);
+                        commit(&b.b_empty[pb.s]);
+                        if (step == C::kSteps - 1) commit(&b.d_full[pd.s]);
+                    }
+                    __syncwarp();
+                    ring_next(pa, C::kSlotsA);
+                    ring_next(pb, C::kRingB);
+                }
+                ring_add(pd, 2, kBufD);
+            }
+            if (lane == 0) {
+                commit(&b.done[mt]);  // every product issued has completed once this arrives
+                mbar_wait(&b.done[mt], 0);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // -------------------------------------------------------- copies of the weights
+            if (lane == 0) {
+                const uint64_t pol = l2_evict_first_policy();
+                RingPos p{0, 0};
+                int64_t issued = 0;
+                bool ok = true;
+                for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+                    const Item w = item_at<N>(it, cum, g);
+                    const int y0 = static_cast<int>(w.e * g.out_dim + static_cast<int64_t>(w.rt) * (kSwiglu ? 128 : 256));
+                    for (int sb = 0; sb < nsb && ok; ++sb) {
+                        for (int mt = 0; mt < 2; ++mt) {
+                            if (!(ok = wait_one(&b.raw_empty[p.s], p.par ^ 1u, b, g.err))) break;
+                            mbar_arrive_expect_tx(&b.raw_full[p.s], kRawBytes);
+                            tma_load_2d(sm + C::off_raw + p.s * kRawBytes, kSwiglu && mt ? &a.map2 : &a.map1, sb * 144,
+                                        y0 + (kSwiglu ? 0 : 128 * mt), &b.raw_full[p.s], pol);
+                            ++issued;
+                            ring_next(p, C::kRingRaw);
+                        }
+                    }
+                }
+                // copies in flight land before the CTA ends
+                for (int64_t k = max(static_cast<int64_t>(0), issued - C::kRingRaw); k < issued; ++k) {
+                    const RingPos q = ring_pos(k, C::kRingRaw);
+                    mbar_wait(&b.raw_full[q.s], q.par);
+                }
+            }
+        }
+    } else if (warp < C::kFirstUnpack) {
+        // ------------------------------------------------------------ B: lanes have kRowsB rows by 4 pieces of 16 bytes
+        if constexpr (C::kRegsGather) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsGather ? C::kRegsGather : 24));
+        if (warp - 4 < C::kGather) {
+            const int col = (lane & 7) + 8 * C::kRowsB * (warp - 4), quarter = lane >> 3;  // this lane's first column; then every 8th
+            RingPos pb{0, 0}, pf{0, 0};
+            int h = 0, behind = 0, fstep = 0, fh = 0;  // gathers under way; the step and super-block that arrive next
+            bool ok = true;
+            auto arrived = [&] {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&b.b_full[pf.s]);
+                    if (fstep == C::kSteps - 1) mbar_arrive(&b.h_full[fh]);
+                }
+                ring_next(pf, C::kRingB);
+                if (++fstep == C::kSteps) {
+                    fstep = 0;
+                    fh = (fh + 1) % kHdr;
+                }
+            };
+            for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+                const Item w = item_at<N>(it, cum, g);
+                __syncwarp();
+                for (int c = 8 * C::kRowsB * (warp - 4) + lane; c < 8 * C::kRowsB * (warp - 3); c += 32) {
+                    int r = -1;  // the row of x, -1 beyond the expert's
+                    if (c < w.m) {
+                        r = w.row + c;
+                        if (g.rows) {
+                            const int pair = g.rows[r];
+                            const bool fine = pair >= 0 && pair < g.n_pairs;
+                            if (!fine) set_error(g.err, DEV_BAD_LENGTH);
+                            r = fine ? pair / g.top_k : 0;
+                        }
+                    }
+                    sts1(sm32 + C::off_src + 4 * c, static_cast<uint32_t>(r));
+                }
+                __syncwarp();
+                for (int sb = 0; sb < nsb && ok; ++sb) {
+#pragma unroll 1
+                    for (int step = 0; step < C::kSteps; ++step) {
+                        if (!(ok = wait_warp(&b.b_empty[pb.s], pb.par ^ 1u, b, g.err))) break;
+                        const uint32_t dst = sm32 + C::off_b + pb.s * C::kSlotB;
+#pragma unroll 2
+                        for (int j = 0; j < C::kRowsB; ++j) {
+                            const int c0 = col + 8 * j, src = lds1i(sm32 + C::off_src + 4 * c0);
+                            const int64_t cell = static_cast<int64_t>(max(src, 0)) * nsb + sb;
+                            const uint32_t bytes = src >= 0 ? 16 : 0;
+                            if (!C::kOwnMins || step < C::kSteps - 1) {
+                                const uint8_t *from = a.pack + cell * kPackBytes + step * (C::kChunks * 256) + quarter * 16;
+                                const uint32_t to = dst + (c0 >> 3) * (C::kChunks * 1024) + quarter * 128 + (lane & 7) * 16;
+#pragma unroll
+                                for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {  // the chunk's first and second half
+                                        gather16(to + c * 1024 + i * 512, from + c * 256 + i * 64, bytes);
+                                        gather16(to + N * C::kChunks * 128 + c * 1024 + i * 512, from + c * 256 + 128 + i * 64, bytes);
+                                    }
+                            }
+                            if (step == C::kSteps - 1) {
+                                // 8 high pieces of s, 8 low ones, and both again; the columns' exponents
+                                const uint32_t to = dst + (C::kOwnMins ? 0 : C::kBytesB) + (c0 >> 3) * 512 + quarter * 128 + (lane & 7) * 16;
+                                gather16(to, a.mins + cell * 32 + (quarter & 1) * 16, bytes);
+                                if (quarter == 0) gather4(sm32 + C::off_cs + 4 * (h * N + c0), a.col_scale + cell, bytes / 4);
+                            }
+                        }
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        ring_next(pb, C::kRingB);
+                        if (behind == C::kLagB) {
+                            asm volatile("cp.async.wait_group %0;" ::"n"(C::kLagB) : "memory");
+                            arrived();
+                        } else {
+                            ++behind;
+                        }
+                    }
+                    h = (h + 1) % kHdr;
+                }
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            if (ok)
+                for (; behind > 0; --behind) arrived();
+        }
+    } else if (warp < C::kFirstSum) {
+        // ------------------------------------------------------------ unpacking
+        if constexpr (C::kRegsUnpack) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsUnpack ? C::kRegsUnpack : 24));
+        // group: matrix, and which of its steps
+        const int cw = warp - C::kFirstUnpack, wrow = 32 * (cw & 3) + lane, mt = (cw >> 2) & 1, turn = cw >> 3;
+        const uint32_t ta0 = tmem + (static_cast<uint32_t>(32 * (cw & 3)) << 16) + C::kColA + mt * C::kSlotsA * C::kWidthA;
+        RingPos pa{turn % C::kSlotsA, 0}, praw{mt, 0};
+        int h = 0;
+        bool ok = true;
+        for (int64_t k = 0; k < blocks && ok; ++k) {
+            if (!(ok = wait_warp(&b.raw_full[praw.s], praw.par, b, g.err))) break;
+            const uint32_t raw = sm32 + C::off_raw + praw.s * kRawBytes + wrow * 144;
+            uint4 hd = lds4(raw);
+            const bool any_wide = __any_sync(0xffffffffu, head_of(hd.x).wide);
+            // six-bit scales, four to a word: sub-blocks 0-3 and 4-7
+            const uint32_t sc0 = hd.y & 0x3f3f3f3fu, sc1 = (hd.w & 0x0f0f0f0fu) | ((hd.y >> 2) & 0x30303030u);
+#pragma unroll
+            for (int step0 = 0; step0 < C::kSteps; step0 += C::kShare) {
+                const int step = step0 + turn;  // kShare divides kSteps, or is 1
+                const uint32_t ta = ta0 + pa.s * C::kWidthA;
+                bool waited = false;
+                if (!C::kOwnMins || step < C::kSteps - 1) {
+#pragma unroll
+                    for (int cc = 0; cc < C::kChunks; ++cc) {
+                        const int c = step * C::kChunks + cc;
+                        const uint4 qa = lds4(raw + 16 + 32 * c), qb = lds4(raw + 32 + 32 * c);
+                        const uint32_t words[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
+                        const uint32_t six = (c < 2 ? sc0 : sc1) >> (16 * (c & 1));
+#pragma unroll
+                        for (int hi = 0; hi < 2; ++hi) {
+                            // (1024 + q) sc - 1024 sc, or (1024 + 16 q) (sc / 16) - 64 sc: one rounding of an exact small integer
+                            const float s6 = static_cast<float>((six >> (8 * hi)) & 63u);
+                            const uint32_t mul = pack2(hi ? s6 * 0.0625f : s6, hi ? s6 * 0.0625f : s6);
+                            const uint32_t add = pack2(hi ? s6 * -64.0f : s6 * -1024.0f, hi ? s6 * -64.0f : s6 * -1024.0f);
+                            const uint32_t mask = hi ? 0x00f000f0u : 0x000f000fu;
+                            uint32_t o[16];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                o[2 * i] = hfma2u(lop_and_or(words[i], mask, 0x64006400u), mul, add);
+                                o[2 * i + 1] = hfma2u(lop_and_or(words[i] >> 8, mask, 0x64006400u), mul, add);
+                            }
+                            if (any_wide) {
+                                const Head head = head_of(lds4(raw).x);
+                                const float f = head.wide && head.fine ? __fdiv_rn(head.d, head.dmin) : 1.0f;
+                                const uint32_t shrink = pack2(f, f);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = hmul2u(o[i], shrink);
+                            }
+                            if (!waited) {
+                                ok = wait_warp(&b.a_empty[mt][pa.s], pa.par ^ 1u, b, g.err);
+                                fence_after();
+                                waited = true;
+                            }
+                            if (ok) tm_store16(ta + 32 * cc + 16 * hi, o);
+                        }
+                    }
+                }
+                if (step == C::kSteps - 1) {
+                    hd = lds4(raw);
+                    const Head head = head_of(hd.x);
+                    const float ratio = head.wide ? 1.0f : head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
+                    const float by = head.fine ? -0.125f * ratio : 0.0f;
+                    const uint32_t mn0 = hd.z & 0x3f3f3f3fu, mn1 = ((hd.w >> 4) & 0x0f0f0f0fu) | ((hd.z >> 2) & 0x30303030u);
+                    uint32_t o[16];  // 8 high pieces, twice, 8 low ones, twice
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t two = (i < 2 ? mn0 : mn1) >> (16 * (i & 1));
+                        const float r0 = by * static_cast<float>(two & 63u), r1 = by * static_cast<float>((two >> 8) & 63u);
+                        o[i] = o[4 + i] = pack2(r0, r1);
+                        const float2 t = unpack2(o[i]);
+                        o[8 + i] = o[12 + i] = pack2(r0 - t.x, r1 - t.y);
+                    }
+                    sts1(sm32 + C::off_g + 4 * ((h * 2 + mt) * 128 + wrow), __float_as_uint(!head.fine ? NAN : head.wide ? head.dmin : head.d));
+                    if (!waited) {
+                        ok = wait_warp(&b.a_empty[mt][pa.s], pa.par ^ 1u, b, g.err);
+                        fence_after();
+                    }
+                    if (ok) tm_store16(ta + (C::kOwnMins ? 0 : 32 * C::kChunks), o);
+                }
+                if (!ok) break;
+                tm_store_wait();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&b.a_full[mt][pa.s]);
+                    if (step == C::kSteps - 1) mbar_arrive(&b.h_full[h]);
+                    if (step0 + C::kShare >= C::kSteps) mbar_arrive(&b.raw_empty[praw.s]);
+                }
+                ring_add(pa, C::kShare, C::kSlotsA);
+            }
+            h = (h + 1) % kHdr;
+            ring_add(praw, 2, C::kRingRaw);
+        }
+    } else {
+        // ------------------------------------------------------------ sums
+        if constexpr (C::kRegsSum) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSum ? C::kRegsSum : 24));
+        const int dw = warp - C::kFirstSum, col0 = (dw >> 2) * C::kHalf, wrow = 32 * (dw & 3) + lane;
+        const uint32_t at = tmem + (static_cast<uint32_t>(32 * (dw & 3)) << 16) + col0;
+        RingPos pd{0, 0}, ph{0, 0};
+        bool ok = true;
+        for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+            float sum[2][C::kHalf];
+#pragma unroll
+            for (int i = 0; i < C::kHalf; ++i) sum[0][i] = sum[1][i] = 0.0f;
+            for (int sb = 0; sb < nsb && ok; ++sb) {
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    if (mt == 0 && !(ok = wait_warp(&b.h_full[ph.s], ph.par, b, g.err))) break;
+                    if (!(ok = wait_warp(&b.d_full[pd.s], pd.par, b, g.err))) break;
+                    fence_after();
+                    const float gs = lds1f(sm32 + C::off_g + 4 * ((ph.s * 2 + mt) * 128 + wrow));
+                    const uint32_t cs = sm32 + C::off_cs + 4 * (ph.s * N + col0);
+                    const uint32_t from = at + pd.s * C::kColsD;
+#pragma unroll
+                    for (int i = 0; i < C::kHalf; i += 8) {
+                        float v[16];
+                        if constexpr (C::kStack) {
+                            tm_load8x2(from + i, from + N + i, v);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] += v[8 + j];
+                        } else {
+                            tm_load8(from + i, v);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; j += 4) {
+                            const float4 c = lds4f(cs + 4 * (i + j));
+                            add_scaled(sum[mt][i + j], sum[mt][i + j + 1], v[j], v[j + 1], c.x, c.y, gs);
+                            add_scaled(sum[mt][i + j + 2], sum[mt][i + j + 3], v[j + 2], v[j + 3], c.z, c.w, gs);
+                        }
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.d_empty[pd.s]);
+                    ring_next(pd, kBufD);
+                }
+                ring_next(ph, kHdr);
+            }
+            if (!ok || *static_cast<volatile int *>(&b.gave_up)) break;
+            // ---- outputs: a warp's 32 rows lie side by side in each column's row of y
+            const Item w = item_at<N>(it, cum, g);
+            if constexpr (kSwiglu) {
+                const int64_t o = static_cast<int64_t>(w.rt) * 128 + wrow;
+                const bool in = o < g.out_dim;
+                int64_t to = static_cast<int64_t>(w.row + col0) * g.out_dim + o;
+#pragma unroll
+                for (int i = 0; i < C::kHalf; ++i, to += g.out_dim) {
+                    if (col0 + i >= w.m) break;
+                    const float v = in ? __fdividef(sum[0][i], 1.0f + expf(-sum[0][i])) * sum[1][i] : 0.0f;
+                    if (g.y && in) g.y[to] = v;
+                    if (g.yq && in) {  // out_dim is a multiple of 32: all of the warp or none
+                        const uint32_t key = isnan(v) ? 0u : __float_as_uint(fabsf(v)) + 1u;
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+                        const float d = top ? __fdiv_rn(__uint_as_float(top - 1u), 127.0f) : NAN;
+                        const int code = q8_code(v, q8_scale(d));
+                        const int total = __reduce_add_sync(0xffffffffu, code);
+                        g.yq[to] = static_cast<int8_t>(code);
+                        if (lane == 0) {
+                            g.yd[to / 32] = d;
+                            g.ys[to / 32] = __fmul_rn(d, static_cast<float>(total));
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    const int64_t o = static_cast<int64_t>(w.rt) * 256 + 128 * mt + wrow;
+                    if (o < g.out_dim) {
+                        float *to = g.y + static_cast<int64_t>(w.row + col0) * g.out_dim + o;
+#pragma unroll
+                        for (int i = 0; i < C::kHalf; ++i, to += g.out_dim) {
+                            if (col0 + i >= w.m) break;
+                            *to = sum[mt][i];
+                        }
+                    }
+                }
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <int N, bool kSwiglu>
+cudaError_t launch(const TcArgs &a, cudaStream_t s)
+{
+    using C = Cfg<N>;
+    cudaError_t e = cudaFuncSetAttribute(moe_gemm_tc_kernel<N, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(dev_info().sm_count));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_use_pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, moe_gemm_tc_kernel<N, kSwiglu>, a);
+}
+
+template <int N>
+cudaError_t launch_n(const TcArgs &a, cudaStream_t s)
+{
+    return a.g.w2 ? launch<N, true>(a, s) : launch<N, false>(a, s);
+}
+
+}  // namespace
+
+int64_t moe_pack_bytes(int64_t rows, int64_t in_dim) { return rows * (in_dim / 256) * (kPackBytes + 32 + 4); }
+
+cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &g, int columns, void *workspace, cudaStream_t s)
+{
+    TcArgs a{};
+    a.g = g;
+    const int64_t x_rows = g.rows ? g.n_pairs / g.top_k : g.n_pairs, cells = x_rows * (g.in_dim / 256);
+    uint8_t *pack = static_cast<uint8_t *>(workspace), *mins = pack + cells * kPackBytes;
+    float *col_scale = reinterpret_cast<float *>(mins + cells * 32);
+    a.pack = pack;
+    a.mins = mins;
+    a.col_scale = col_scale;
+    const uint64_t row_bytes = static_cast<uint64_t>(g.in_dim) / 256 * 144, rows = static_cast<uint64_t>(g.n_experts) * g.out_dim;
+    cudaError_t e = encode_tensor_map_2d(&a.map1, g.w1, 1, row_bytes, rows, row_bytes, 144, 128);
+    if (e == cudaSuccess && g.w2) e = encode_tensor_map_2d(&a.map2, g.w2, 1, row_bytes, rows, row_bytes, 144, 128);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((cells + kPackWarps - 1) / kPackWarps));
+    cfg.blockDim = dim3(32 * kPackWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_use_pdl ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, moe_pack_kernel, g.xq, g.xd, g.xs, pack, mins, col_scale, cells);
+    if (e != cudaSuccess) return e;
+    switch (columns) {
+        case 16: return launch_n<16>(a, s);
+        case 32: return launch_n<32>(a, s);
+        default: return launch_n<128>(a, s);
+    }
+}
+
+int moe_columns(int64_t n_pairs, int n_experts)
+{
+    const int64_t rows = n_pairs / n_experts;
+    return rows <= 2 ? 0 : rows <= 12 ? 16 : rows <= 64 ? 32 : 128;
+}
+
+cudaError_t launch_moe_product(const MoeGemvArgs &a, void *workspace, cudaStream_t s)
+{
+    const int columns = moe_columns(a.n_pairs, a.n_experts);
+    return columns ? launch_moe_gemm_tc(a, columns, workspace, s) : launch_moe_gemv(a, s);
+}
+
+}  // namespace rz

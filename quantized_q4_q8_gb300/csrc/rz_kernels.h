@@ -353,6 +353,14 @@ struct MoeGemvArgs {
 };
 cudaError_t launch_moe_gemv(const MoeGemvArgs &a, cudaStream_t s);
 
+// The same on the tensor cores (moe_gemm_tc.cu), in tiles of `columns` rows: 16, 32, 64 or 128.
+cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &a, int columns, void *workspace, cudaStream_t s);
+int64_t moe_pack_bytes(int64_t rows, int64_t in_dim);  // of its workspace, for that many rows of x
+
+// Whichever of the two the sizes call for.
+int moe_columns(int64_t n_pairs, int n_experts);
+cudaError_t launch_moe_product(const MoeGemvArgs &a, void *workspace, cudaStream_t s);
+
 struct MoeCombineArgs {
     const float *o;  // [n_pairs][out_dim]
     const int32_t *places;

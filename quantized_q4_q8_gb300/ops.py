@@ -23,7 +23,7 @@ __all__ = [
     "rz_attention_paged_q4", "attention_paged_q4_workspace_bytes", "attention_paged_q4",
     "decode_layer_paged_workspace_bytes", "decode_layer_paged",
     "rz_residual_rmsnorm", "residual_rmsnorm", "MoePlan", "moe_route_workspace_bytes", "rz_moe_route", "moe_route",
-    "rz_moe_swiglu", "moe_swiglu", "moe_down_workspace_bytes", "rz_moe_down", "moe_down",
+    "moe_swiglu_workspace_bytes", "rz_moe_swiglu", "moe_swiglu", "moe_down_workspace_bytes", "rz_moe_down", "moe_down",
 ]
 
 
@@ -867,27 +867,34 @@ def _expert_weights(w, n_experts, out_dim, in_dim, dev, name):
     return w.data_ptr()
 
 
-def rz_moe_swiglu(w_gate, w_up, x_q8, plan, inter, in_dim, h, h_q8, stream=None):
-    return call("rz_moe_swiglu", _ptr(w_gate), _ptr(w_up), _ptr(x_q8), plan.ref, inter, in_dim, _ptr(h), _ptr(h_q8), _stream(stream))
+def moe_swiglu_workspace_bytes(n_tokens: int, n_experts: int, top_k: int, in_dim: int) -> int:
+    return int(load().rz_moe_swiglu_workspace_bytes(n_tokens, n_experts, top_k, in_dim))
 
 
-def moe_swiglu(w_gate, w_up, x_q8, plan: MoePlan, inter: int, in_dim: int, out=None, out_q8=None, want_h: bool = True, stream=None):
+def rz_moe_swiglu(w_gate, w_up, x_q8, plan, inter, in_dim, h, h_q8, ws, ws_bytes, stream=None):
+    return call("rz_moe_swiglu", _ptr(w_gate), _ptr(w_up), _ptr(x_q8), plan.ref, inter, in_dim, _ptr(h), _ptr(h_q8), _ptr(ws), ws_bytes,
+                _stream(stream))
+
+
+def moe_swiglu(w_gate, w_up, x_q8, plan: MoePlan, inter: int, in_dim: int, out=None, out_q8=None, want_h: bool = True, ws=None,
+               stream=None):
     """silu(gate) * up of each row of the plan with its expert (see rz.h): f32 [n_tokens * top_k, inter] in the plan's
     order (None with want_h False), and its Q8_1 form into out_q8 where that is given."""
     import torch
     u8, dev, pairs = torch.uint8, torch.cuda.current_device(), plan.n_tokens * plan.top_k
     if out is None and want_h:
         out = _new((pairs, inter), torch.float32, dev, stream)
+    at, size, ws = _scratch(ws, moe_swiglu_workspace_bytes(plan.n_tokens, plan.n_experts, plan.top_k, in_dim), dev, stream)
     call("rz_moe_swiglu", _expert_weights(w_gate, plan.n_experts, inter, in_dim, dev, "w_gate"),
          _expert_weights(w_up, plan.n_experts, inter, in_dim, dev, "w_up"),
          _vector(x_q8, u8, q8_1_size(plan.n_tokens, in_dim), dev, "x_q8"), _plan_on(plan, dev), inter, in_dim,
          None if out is None else _matrix(out, torch.float32, pairs, inter, dev, "out"),
-         None if out_q8 is None else _vector(out_q8, u8, q8_1_size(pairs, inter), dev, "out_q8"), _stream_on(stream, dev))
+         None if out_q8 is None else _vector(out_q8, u8, q8_1_size(pairs, inter), dev, "out_q8"), at, size, _stream_on(stream, dev))
     return out
 
 
-def moe_down_workspace_bytes(n_tokens: int, top_k: int, out_dim: int) -> int:
-    return int(load().rz_moe_down_workspace_bytes(n_tokens, top_k, out_dim))
+def moe_down_workspace_bytes(n_tokens: int, n_experts: int, top_k: int, out_dim: int, in_dim: int) -> int:
+    return int(load().rz_moe_down_workspace_bytes(n_tokens, n_experts, top_k, out_dim, in_dim))
 
 
 def rz_moe_down(w_down, h_q8, plan, residual, y, out_dim, out_pad, in_dim, ws, ws_bytes, stream=None):
@@ -902,7 +909,7 @@ def moe_down(w_down, h_q8, plan: MoePlan, out_dim: int, in_dim: int, residual=No
     f32, dev, out_pad = torch.float32, torch.cuda.current_device(), out_pad or out_dim
     if out is None:
         out = _new((plan.n_tokens, out_pad), f32, dev, stream)
-    at, size, ws = _scratch(ws, moe_down_workspace_bytes(plan.n_tokens, plan.top_k, out_dim), dev, stream)
+    at, size, ws = _scratch(ws, moe_down_workspace_bytes(plan.n_tokens, plan.n_experts, plan.top_k, out_dim, in_dim), dev, stream)
     call("rz_moe_down", _expert_weights(w_down, plan.n_experts, out_dim, in_dim, dev, "w_down"),
          _vector(h_q8, torch.uint8, q8_1_size(plan.n_tokens * plan.top_k, in_dim), dev, "h_q8"), _plan_on(plan, dev),
          None if residual is None else _matrix(residual, f32, plan.n_tokens, out_pad, dev, "residual"),

@@ -377,14 +377,15 @@ class Block:
         self.d = {k: dev(v) for k, v in (("gate", self.gate), ("up", self.up), ("down", self.down), ("gamma", self.gamma), ("router", self.router))}
         self.plan = rz.MoePlan(T, E, k)
         self.h8 = torch.empty(rz.q8_1_size(T * k, inter), dtype=torch.uint8, device="cuda")
-        self.ws = rz.workspace(max(rz.moe_down_workspace_bytes(T, k, n), rz.moe_route_workspace_bytes(T, E)), "cuda")
+        self.ws = rz.workspace(max(rz.moe_down_workspace_bytes(T, E, k, n, inter), rz.moe_swiglu_workspace_bytes(T, E, k, n_pad),
+                                   rz.moe_route_workspace_bytes(T, E)), "cuda")
         self.h8.zero_()
 
     def run(self, x, delta, seq):
         rz = self.rz
         s, y, q8 = rz.residual_rmsnorm(x, delta, self.d["gamma"], self.n, self.n_pad, 1e-6)
         rz.moe_route(y @ self.d["router"].t(), self.plan, row_seq=seq, ws=self.ws)
-        rz.moe_swiglu(self.d["gate"], self.d["up"], q8, self.plan, self.inter, self.n_pad, out_q8=self.h8, want_h=False)
+        rz.moe_swiglu(self.d["gate"], self.d["up"], q8, self.plan, self.inter, self.n_pad, out_q8=self.h8, want_h=False, ws=self.ws)
         return rz.moe_down(self.d["down"], self.h8, self.plan, self.n, self.inter, residual=s, out_pad=self.n_pad, ws=self.ws)
 
     def reference(self, x, delta, plan, h8):

@@ -44,7 +44,7 @@ def plan(lib, change):
 
 
 ROUTE = dict(logits=16, ld=8, row_seq=16, plan={}, renormalise=1, scale=1.0, ws=16, ws_bytes=1 << 20, stream=None)
-SWIGLU = dict(gate=16, up=32, x=48, plan={}, inter=512, in_dim=256, h=64, h_q8=80, stream=None)
+SWIGLU = dict(gate=16, up=32, x=48, plan={}, inter=512, in_dim=256, h=64, h_q8=80, ws=96, ws_bytes=1 << 30, stream=None)
 DOWN = dict(down=16, h=32, plan={}, residual=48, y=64, out_dim=100, out_pad=128, in_dim=512, ws=80, ws_bytes=1 << 30, stream=None)
 
 
@@ -75,7 +75,7 @@ def test_route_refusals(lib, change, status):
 @pytest.mark.parametrize("change,status", [
     (dict(gate=None), 1), (dict(up=None), 1), (dict(x=None), 1), (dict(h=None, h_q8=None), 1), (dict(inter=0), 2),
     (dict(inter=(1 << 20) + 1, h_q8=None), 2), (dict(inter=48), 2), (dict(in_dim=0), 2), (dict(in_dim=300), 2), (dict(in_dim=1 << 21), 2),
-    (dict(gate=20), 3), (dict(up=8), 3), (dict(x=4), 3), (dict(h=72), 3), (dict(h_q8=88), 3),
+    (dict(gate=20), 3), (dict(up=8), 3), (dict(x=4), 3), (dict(h=72), 3), (dict(h_q8=88), 3), (dict(ws=None), 1), (dict(ws=88), 3), (dict(ws_bytes=200 * 1060 - 1), 1),
 ])
 def test_swiglu_refusals(lib, change, status):
     refused(lib, "rz_moe_swiglu", SWIGLU, change, status)
@@ -96,9 +96,14 @@ def test_workspace_sizes(lib):
     assert L.rz_moe_route_workspace_bytes(129, 8) > 0
     assert L.rz_moe_route_workspace_bytes(0, 8) == 0 and lib.last_error()
     assert L.rz_moe_route_workspace_bytes(5, 600) == 0 and lib.last_error()
-    assert L.rz_moe_down_workspace_bytes(200, 2, 100) == 200 * 2 * 100 * 4
-    assert L.rz_moe_down_workspace_bytes(200, 0, 100) == 0 and lib.last_error()
-    assert L.rz_moe_down_workspace_bytes(200, 2, 0) == 0 and lib.last_error()
+    assert L.rz_moe_swiglu_workspace_bytes(1, 64, 8, 2048) == 0 and not lib.last_error()
+    assert L.rz_moe_swiglu_workspace_bytes(200, 8, 2, 512) >= 200 * 512 * 4
+    assert L.rz_moe_swiglu_workspace_bytes(200, 8, 2, 100) == 0 and lib.last_error()
+    assert L.rz_moe_down_workspace_bytes(1, 64, 8, 100, 512) >= 8 * 100 * 4
+    assert L.rz_moe_down_workspace_bytes(200, 8, 2, 100, 512) >= 200 * 2 * (100 * 4 + 512 * 4)
+    assert L.rz_moe_down_workspace_bytes(200, 8, 0, 100, 512) == 0 and lib.last_error()
+    assert L.rz_moe_down_workspace_bytes(200, 8, 2, 0, 512) == 0 and lib.last_error()
+    assert L.rz_moe_down_workspace_bytes(200, 8, 2, 100, 500) == 0 and lib.last_error()
 
 
 # ---------------------------------------------------------------- the reference itself
