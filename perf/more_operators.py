@@ -211,8 +211,10 @@ def prepare(c, seed):
     if own:
         import quantized_q4_q8_gb300 as rz
         s["own_plan"] = rz.MoePlan(T, E, k, DEV, **plan)
-        if c["op"] == "down":
-            s["ws"] = rz.workspace(rz.moe_down_workspace_bytes(T, k, n), DEV)
+        if c["op"] == "gateup":
+            s["ws"] = rz.workspace(rz.moe_swiglu_workspace_bytes(T, E, k, n), DEV)
+        else:
+            s["ws"] = rz.workspace(rz.moe_down_workspace_bytes(T, E, k, n, i), DEV)
     return s
 
 
@@ -270,7 +272,7 @@ def _gateup(s):
     n = s["gate"].shape[-2] * 256
     if own:
         import quantized_q4_q8_gb300 as rz
-        return rz.moe_swiglu(s["gate"], s["up"], s["x"], s["own_plan"], i, n, out=s["h"])
+        return rz.moe_swiglu(s["gate"], s["up"], s["x"], s["own_plan"], i, n, out=s["h"], ws=s["ws"])
     x = _q8_values(s["x"], T, n)
     gate, up = _grouped(s, (s["gate"], s["up"]), lambda pairs, places: x[pairs // k])
     return gate / (1 + torch.exp(-gate)) * up
