@@ -121,22 +121,17 @@ void swiglu_args(MoeGemvArgs &a, const void *w_gate, const void *w_up, const voi
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// B of the tensor-core kernel, for that many rows of x; the integer kernel needs none
-int64_t pack_bytes(int64_t x_rows, int64_t n_pairs, int n_experts, int64_t in_dim)
+// the activations as the tensor-core kernel takes them; the integer kernel needs nothing
+int64_t pack_bytes(int64_t n_pairs, int n_experts, int64_t in_dim)
 {
-    return moe_columns(n_pairs, n_experts) ? moe_pack_bytes(x_rows, in_dim) : 0;
-}
-
-int64_t swiglu_workspace_bytes(int64_t n_tokens, int n_experts, int top_k, int64_t in_dim)
-{
-    return pack_bytes(n_tokens, n_tokens * top_k, n_experts, in_dim);
+    return moe_pack_bytes(moe_columns(n_pairs, n_experts), n_pairs, n_experts, in_dim);
 }
 
 // the rows' products, then B
 int64_t down_workspace_bytes(int64_t n_tokens, int n_experts, int top_k, int64_t out_dim, int64_t in_dim)
 {
     const int64_t pairs = n_tokens * top_k;
-    return align256(pairs * out_dim * 4) + pack_bytes(pairs, pairs, n_experts, in_dim);
+    return align256(pairs * out_dim * 4) + pack_bytes(pairs, n_experts, in_dim);
 }
 
 cudaError_t run_down(const void *w_down, const void *h_q8, const rz_moe_plan *p, const float *residual, float *y, int64_t out_dim,
@@ -266,7 +261,7 @@ size_t rz_moe_swiglu_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_
     const char *fn = "rz_moe_swiglu_workspace_bytes";
     record_error(RZ_OK, "");
     if (check_counts(fn, n_tokens, n_experts, top_k) != RZ_OK || check_in_dim(fn, in_dim) != RZ_OK) return 0;
-    return swiglu_workspace_bytes(n_tokens, n_experts, top_k, in_dim);
+    return pack_bytes(n_tokens * top_k, n_experts, in_dim);
 }
 
 rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, const rz_moe_plan *plan, int64_t inter, int64_t in_dim,
@@ -282,7 +277,7 @@ rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, 
     const void *bufs[] = {w_gate, w_up, x_q8, h, h_q8};
     for (const void *p : bufs)
         if (!aligned(p, 16)) return fail(RZ_ERR_ALIGN, "%s: buffers must be 16-byte aligned", fn);
-    RZ_TRY(check_workspace(fn, workspace, ws_bytes, swiglu_workspace_bytes(plan->n_tokens, plan->n_experts, plan->top_k, in_dim)));
+    RZ_TRY(check_workspace(fn, workspace, ws_bytes, pack_bytes(plan->n_tokens * plan->top_k, plan->n_experts, in_dim)));
     RZ_TRY(ensure_device());
     MoeGemvArgs a{};
     swiglu_args(a, w_gate, w_up, x_q8, plan, inter, in_dim, h, h_q8);

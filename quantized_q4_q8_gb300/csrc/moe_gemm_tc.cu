@@ -47,8 +47,7 @@ namespace {
 constexpr int kRawBytes = 144 * 128;
 constexpr int kHdr = 4;      // super-blocks whose scales are held
 constexpr int kBufD = 3;     // accumulators
-constexpr int kPackBytes = 1024;  // of B for a row and super-block: of each 64 values the high pieces, then the low ones
-
+constexpr int kItems = 16;   // items whose places are held (copies are some six super-blocks ahead of the sums)
 template <int N>
 struct Cfg {
     static constexpr bool kStack = N <= 32;           // pieces side by side
@@ -62,41 +61,38 @@ struct Cfg {
     static constexpr int kBytesB = kChunks * N * 256; // two pieces of 64 * kChunks values
     static constexpr int kSlotB = kBytesB + (kOwnMins ? 0 : N * 64);
     static constexpr int kRingB = N == 128 ? 4 : 5;
-    static constexpr int kLagB = 2;                   // steps whose gathers are under way while the next is issued
-    static constexpr int kGather = N >= 32 ? 4 : 2;   // warps that gather B
-    static constexpr int kRowsB = N / 8 / kGather;    // rows of a lane there
+    static constexpr int kCellB = 4 / kChunks * kBytesB + N * 64;  // of a super-block: the steps, the mins
     static constexpr int kRingRaw = N == 128 ? 4 : N == 16 ? 8 : 6;
     static constexpr int kColA = kBufD * kColsD;      // tensor memory: accumulators, then A
     static constexpr int kWidthA = 32 * kChunks + (kOwnMins ? 0 : 16);
     static constexpr int kHalf = N / 2;               // columns of a thread that adds up
-    static constexpr int kFirstUnpack = 8, kFirstSum = kFirstUnpack + 4 * kGroups;
+    static constexpr int kFirstUnpack = 4, kFirstSum = kFirstUnpack + 4 * kGroups;
     static constexpr int kThreads = 32 * (kFirstSum + 8);
     // registers of the roles (0: as launched)
-    static constexpr int kRegsIssue = N == 128 ? 32 : 0, kRegsGather = N == 128 ? 32 : 0, kRegsUnpack = N == 128 ? 56 : 0,
-                         kRegsSum = N == 128 ? 152 : 0;
+    static constexpr int kRegsIssue = N == 128 ? 40 : 0, kRegsUnpack = N == 128 ? 64 : 0, kRegsSum = N == 128 ? 152 : 0;
     static constexpr int off_b = 0;
     static constexpr int off_raw = off_b + kRingB * kSlotB;
     static constexpr int off_g = off_raw + kRingRaw * kRawBytes;   // [kHdr][2][128]
     static constexpr int off_cs = off_g + kHdr * 2 * 128 * 4;      // [kHdr][N]
-    static constexpr int off_src = off_cs + kHdr * N * 4;          // [N]
-    static constexpr int off_cum = off_src + N * 4;                // int64 [kMoeMaxExperts + 1]
-    static constexpr int off_bars = off_cum + 8 * (kMoeMaxExperts + 1) + 8;
+    static constexpr int off_item = off_cs + kHdr * N * 4;         // int4 [kItems]
+    static constexpr int off_cum = off_item + 16 * kItems;         // int [kMoeMaxExperts + 1]
+    static constexpr int off_bars = off_cum + 4 * (kMoeMaxExperts + 1) + 12;
     static constexpr int bytes = off_bars + 640 + 1024;
     static_assert(kColA + 2 * kSlotsA * kWidthA <= 512, "tensor memory");
     static_assert(off_raw % 128 == 0, "copies start on 128 bytes");
     static_assert(bytes <= 227 * 1024, "shared memory");
     // A slot of A is filled again by the group that filled it before, or by one that has seen the product before that done: otherwise
     // a wait could take the phase before for the one it waits for
-    static_assert(kSlotsA % kShare == 0 && kLagB < kRingB && kRingRaw % 2 == 0, "rings");
+    static_assert(kSlotsA % kShare == 0 && kRingRaw % 2 == 0, "rings");
     // Scales of super-block k take the place of those of k - kHdr, added up by then: whoever writes them has seen the products of a
     // step at most kRingB (or kSlotsA) before done, whose accumulators were free, which takes all but the last three of those before
     static_assert((kRingB + kSteps - 1) / kSteps + 1 <= kHdr, "scales");
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static_assert(kRegsSum == 0 || 128 * (kRegsIssue + kRegsGather + kGroups * kRegsUnpack) + 256 * kRegsSum <= kThreads * kLaunchRegs, "registers");
+    static_assert(kRegsSum == 0 || 128 * (kRegsIssue + kGroups * kRegsUnpack) + 256 * kRegsSum <= kThreads * kLaunchRegs, "registers");
 };
 
 struct Bars {
-    uint64_t a_full[2][4], a_empty[2][4], b_full[6], b_empty[6], raw_full[8], raw_empty[8], d_full[kBufD], d_empty[kBufD], h_full[kHdr], done[2];
+    uint64_t a_full[2][4], a_empty[2][4], b_full[6], b_empty[6], raw_full[8], raw_empty[8], d_full[kBufD], d_empty[kBufD], h_full[kHdr], cs_full[kHdr], done[2];
     uint32_t tmem;
     int gave_up;
 };
@@ -105,8 +101,8 @@ static_assert(sizeof(Bars) <= 640, "barriers");
 struct TcArgs {
     CUtensorMap map1, map2;
     MoeGemvArgs g;
-    const uint8_t *pack, *mins;  // B: [rows][super-blocks][kPackBytes], [rows][super-blocks][32]
-    const float *col_scale;      // 2^E [rows][super-blocks]
+    const uint8_t *pack;     // B of tile i and super-block j, as its copies go to shared memory: at (i * nsb + j) * kCellB
+    const float *col_scale;  // 2^E [tiles][super-blocks][kN]
 };
 
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t stride)
@@ -185,16 +181,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ float2 unpack2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
-// 16 bytes global -> shared, zeros where `bytes` is 0; and 4 bytes
-__device__ __forceinline__ void gather16(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void gather4(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b)
 {
     uint32_t d;
@@ -221,11 +207,9 @@ __device__ __forceinline__ float lds1f(uint32_t at)
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
 }
-__device__ __forceinline__ int lds1i(uint32_t at)
+__device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
 {
-    int v;
-    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 __device__ __forceinline__ void sts1(uint32_t at, uint32_t x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory"); }
 
@@ -268,6 +252,13 @@ __device__ __forceinline__ Head head_of(uint32_t word)
     return {d, dmin, fabsf(dmin) > 8192.0f * fabsf(d), isfinite(d) && isfinite(dmin)};
 }
 
+// The most tiles that so many rows of so many experts can have.
+template <int N>
+__host__ __device__ constexpr int64_t max_tiles(int64_t n_pairs, int n_experts)
+{
+    return n_pairs / N + (n_pairs < n_experts ? n_pairs : n_experts);
+}
+
 // Whether a phase is complete, at once.
 __device__ __forceinline__ bool test_phase(uint64_t *bar, unsigned par)
 {
@@ -282,14 +273,36 @@ __device__ __forceinline__ bool test_phase(uint64_t *bar, unsigned par)
     return ok != 0;
 }
 
-// Item number i: its expert, tile of outputs and first row.
-struct Item {
-    int e, rt, row, m;  // m rows, up to kN
-};
+// Tiles of kN rows before each expert, by one warp; returns how many there are.
 template <int N>
-__device__ __forceinline__ Item item_at(int64_t i, const int64_t *cum, const MoeGemvArgs &g)
+__device__ __forceinline__ int tiles_before(const MoeGemvArgs &g, int *cum, int lane)
 {
-    int lo = 0, hi = g.n_experts;  // cum[lo] <= i < cum[hi]
+    int base = 0;
+    for (int e0 = 0; e0 < g.n_experts; e0 += 32) {
+        const int e = e0 + lane;
+        int own = 0;
+        if (e < g.n_experts) {
+            const int lo = g.offsets[e], hi = g.offsets[e + 1];
+            if (lo >= 0 && hi > lo && hi <= g.n_pairs) own = (hi - lo + N - 1) / N;
+        }
+        int v = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (e < g.n_experts) cum[e] = base + v - own;
+        base += __shfl_sync(0xffffffffu, v, 31);
+    }
+    // offsets that overlap could ask for more tiles than the workspace holds
+    base = min(base, static_cast<int>(max_tiles<N>(g.n_pairs, g.n_experts)));
+    if (lane == 0) cum[g.n_experts] = base;
+    return base;
+}
+// The expert of tile i.
+__device__ __forceinline__ int expert_of(int i, const int *cum, int n_experts)
+{
+    int lo = 0, hi = n_experts;  // cum[lo] <= i < cum[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (cum[mid] <= i)
@@ -297,56 +310,95 @@ __device__ __forceinline__ Item item_at(int64_t i, const int64_t *cum, const Moe
         else
             hi = mid;
     }
-    const int first = g.offsets[lo], end = g.offsets[lo + 1];
-    const int tiles = (end - first + N - 1) / N;
-    const int64_t at = i - cum[lo];
-    Item w;
-    w.e = lo;
-    w.rt = static_cast<int>(at / tiles);
-    w.row = first + static_cast<int>(at - static_cast<int64_t>(w.rt) * tiles) * N;
-    w.m = min(N, end - w.row);
-    return w;
+    return lo;
 }
 
-// B's pieces of a row and super-block: a warp, 8 codes a lane.
-constexpr int kPackWarps = 8;
-__global__ void __launch_bounds__(32 * kPackWarps) moe_pack_kernel(const int8_t *__restrict__ q, const float *__restrict__ d8,
-                                                                   const float *__restrict__ s8, uint8_t *__restrict__ pack,
-                                                                   uint8_t *__restrict__ mins, float *__restrict__ col_scale, int64_t cells)
+// B: a CTA has a tile and some of its super-blocks, a warp a row's super-block at a time, a lane 8 codes.
+constexpr int kPackThreads = 256;
+template <int N>
+__global__ void __launch_bounds__(kPackThreads) moe_pack_kernel(const MoeGemvArgs g, uint8_t *__restrict__ pack, float *__restrict__ col_scale)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t cell = static_cast<int64_t>(blockIdx.x) * kPackWarps + (threadIdx.x >> 5);
+    using C = Cfg<N>;
+    __shared__ int cum[kMoeMaxExperts + 1], src[N];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nsb = g.in_dim / 256;
     pdl_launch_dependents();
     pdl_wait();
-    if (cell >= cells) return;
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q + cell * 256) + lane);
-    const float d = __ldg(d8 + cell * 8 + (lane >> 2)), s = __ldg(s8 + cell * 8 + (lane & 7));
-    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(d) & 0x7fffffffu);
-    const uint32_t e = min(top >> 23, 252u);
-    const float up = __uint_as_float((253u - e) << 23);  // the largest scale becomes 1/2 .. 1
-    const float v = d * up, vh = __half2float(__float2half_rn(v));
-    const uint32_t dh = pack2(vh, vh), dl = pack2(v - vh, v - vh);
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        // codes as 1024 + 128 + code, which is f16 0x64xx, in the order 0, 2, 1, 3
-        const uint32_t u = (i ? w.y : w.x) ^ 0x80808080u;
-        const uint32_t e02 = hsub2u(__byte_perm(u, 0x64646464u, 0x4240), 0x64806480u), e13 = hsub2u(__byte_perm(u, 0x64646464u, 0x4341), 0x64806480u);
-        hi[2 * i] = hmul2u(e02, dh);
-        hi[2 * i + 1] = hmul2u(e13, dh);
-        lo[2 * i] = hfma2u(e02, dl, hfma2u(e02, dh, hneg2u(hi[2 * i])));  // the inner one is exact
-        lo[2 * i + 1] = hfma2u(e13, dl, hfma2u(e13, dh, hneg2u(hi[2 * i + 1])));
+    if (warp == 0) tiles_before<N>(g, cum, lane);
+    __syncthreads();
+    const int tile = blockIdx.x;
+    if (tile >= cum[g.n_experts]) return;
+    const int e = expert_of(tile, cum, g.n_experts), first = g.offsets[e] + (tile - cum[e]) * N, end = g.offsets[e + 1];
+    for (int c = tid; c < N; c += kPackThreads) {
+        int r = -1;  // the row of x, -1 beyond the expert's
+        if (first + c < end) {
+            r = first + c;
+            if (g.rows) {
+                const int pair = g.rows[r];
+                const bool fine = pair >= 0 && pair < g.n_pairs;
+                if (!fine) set_error(g.err, DEV_BAD_LENGTH);
+                r = fine ? pair / g.top_k : 0;
+            }
+        }
+        src[c] = r;
     }
-    uint8_t *to = pack + cell * kPackBytes + (lane >> 3) * 256 + (lane & 7) * 16;
-    *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4 *>(to + 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    if (lane < 8) {
-        const float t = s * up * 8.0f;
-        const __half sh = __float2half_rn(t);
-        __half *m = reinterpret_cast<__half *>(mins + cell * 32);
-        m[lane] = sh;
-        m[8 + lane] = __float2half_rn(t - __half2float(sh));
-        if (lane == 0) col_scale[cell] = __uint_as_float((e + 1u) << 23);
+    __syncthreads();
+    const int sb0 = blockIdx.y * nsb / gridDim.y, sb1 = (blockIdx.y + 1) * nsb / gridDim.y;
+    // eight rows side by side for a warp's stores: lanes have row lane & 7 of 8, and a quarter of its codes at a time
+    const int row = lane & 7, quarter = lane >> 3;
+    for (int u = warp; u < (sb1 - sb0) * (N / 8); u += kPackThreads / 32) {
+        const int sb = sb0 + u / (N / 8), c = u % (N / 8) * 8 + row, r = src[c];
+        const int64_t cell = static_cast<int64_t>(tile) * nsb + sb, from = static_cast<int64_t>(max(r, 0)) * nsb + sb;
+        uint8_t *to = pack + cell * C::kCellB;
+        // this quarter's blocks 2 quarter, 2 quarter + 1
+        float2 d = make_float2(0.0f, 0.0f), s = d;
+        if (r >= 0) {
+            d = __ldg(reinterpret_cast<const float2 *>(g.xd + from * 8) + quarter);
+            s = __ldg(reinterpret_cast<const float2 *>(g.xs + from * 8) + quarter);
+        }
+        uint4 codes[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) codes[k] = r >= 0 ? __ldg(reinterpret_cast<const uint4 *>(g.xq + from * 256 + 64 * quarter + 16 * k)) : make_uint4(0, 0, 0, 0);
+        uint32_t top = max(__float_as_uint(d.x) & 0x7fffffffu, __float_as_uint(d.y) & 0x7fffffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const uint32_t e2 = min(top >> 23, 252u);
+        const float up = __uint_as_float((253u - e2) << 23);  // the largest scale becomes 1/2 .. 1
+        const float v[4] = {d.x * up, d.y * up, s.x * up * 8.0f, s.y * up * 8.0f};
+        float high[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) high[k] = __half2float(__float2half_rn(v[k]));
+        // step, and the chunk of 64 within it
+        uint8_t *base = to + quarter / C::kChunks * C::kBytesB + (c >> 3) * (C::kChunks * 1024) + quarter % C::kChunks * 1024 + row * 16;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // 16 codes, half a block
+            const uint32_t dh = pack2(high[k >> 1], high[k >> 1]), dl = pack2(v[k >> 1] - high[k >> 1], v[k >> 1] - high[k >> 1]);
+            const uint32_t words[4] = {codes[k].x, codes[k].y, codes[k].z, codes[k].w};
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // codes as 1024 + 128 + code, which is f16 0x64xx, in the order 0, 2, 1, 3
+                const uint32_t w = words[i] ^ 0x80808080u;
+                const uint32_t e02 = hsub2u(__byte_perm(w, 0x64646464u, 0x4240), 0x64806480u), e13 = hsub2u(__byte_perm(w, 0x64646464u, 0x4341), 0x64806480u);
+                hi[2 * i] = hmul2u(e02, dh);
+                hi[2 * i + 1] = hmul2u(e13, dh);
+                lo[2 * i] = hfma2u(e02, dl, hfma2u(e02, dh, hneg2u(hi[2 * i])));  // the inner one is exact
+                lo[2 * i + 1] = hfma2u(e13, dl, hfma2u(e13, dh, hneg2u(hi[2 * i + 1])));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                *reinterpret_cast<uint4 *>(base + (2 * k + i) * 128) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+                // the low pieces: kN rows on (side by side) or an operand of their own
+                *reinterpret_cast<uint4 *>(base + N * C::kChunks * 128 + (2 * k + i) * 128) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+            }
+        }
+        // 8 high pieces of s, 8 low ones, and both again
+        uint8_t *m = to + 4 / C::kChunks * C::kBytesB + (c >> 3) * 512 + row * 16 + quarter * 4;
+        const uint32_t sh = pack2(high[2], high[3]), sl = pack2(v[2] - high[2], v[3] - high[3]);
+        *reinterpret_cast<uint32_t *>(m) = sh;
+        *reinterpret_cast<uint32_t *>(m + 128) = sl;
+        *reinterpret_cast<uint32_t *>(m + 256) = sh;
+        *reinterpret_cast<uint32_t *>(m + 384) = sl;
+        if (quarter == 0) col_scale[cell * N + c] = __uint_as_float((e2 + 1u) << 23);
     }
 }
 
@@ -367,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
     extern __shared__ uint8_t raw_smem[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
     Bars &b = *reinterpret_cast<Bars *>(sm + C::off_bars);
-    int64_t *cum = reinterpret_cast<int64_t *>(sm + C::off_cum);
+    int *cum = reinterpret_cast<int *>(sm + C::off_cum);
     const uint32_t sm32 = smem_u32(sm);
     const MoeGemvArgs &g = a.g;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -380,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             mbar_init(&b.a_empty[i & 1][i >> 1], 1);
         }
         for (int i = 0; i < C::kRingB; ++i) {
-            mbar_init(&b.b_full[i], C::kGather);
+            mbar_init(&b.b_full[i], 1);
             mbar_init(&b.b_empty[i], 2);
         }
         for (int i = 0; i < C::kRingRaw; ++i) {
@@ -391,7 +443,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             mbar_init(&b.d_full[i], 1);
             mbar_init(&b.d_empty[i], 8);
         }
-        for (int i = 0; i < kHdr; ++i) mbar_init(&b.h_full[i], 8 + C::kGather);
+        for (int i = 0; i < kHdr; ++i) {
+            mbar_init(&b.h_full[i], 8);
+            mbar_init(&b.cs_full[i], 1);
+        }
         mbar_init(&b.done[0], 1);
         mbar_init(&b.done[1], 1);
         b.gave_up = 0;
@@ -405,34 +460,15 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
     }
     pdl_launch_dependents();
     pdl_wait();
-    // items before each expert
-    if (warp == 1) {
-        int64_t base = 0;
-        for (int e0 = 0; e0 < g.n_experts; e0 += 32) {
-            const int e = e0 + lane;
-            int64_t own = 0;
-            if (e < g.n_experts) {
-                const int lo = g.offsets[e], hi = g.offsets[e + 1];
-                if (lo >= 0 && hi > lo && hi <= g.n_pairs) own = static_cast<int64_t>((hi - lo + N - 1) / N) * row_tiles;
-            }
-            int64_t v = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            if (e < g.n_experts) cum[e] = base + v - own;
-            base += __shfl_sync(0xffffffffu, v, 31);
-        }
-        if (lane == 0) cum[g.n_experts] = base;
-    }
+    if (warp == 1) tiles_before<N>(g, cum, lane);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = b.tmem;
-    const int64_t items = cum[g.n_experts];
-    // this CTA's super-blocks, all items one after another
-    const int64_t my_items = items > blockIdx.x ? (items - blockIdx.x + gridDim.x - 1) / gridDim.x : 0, blocks = my_items * nsb;
+    const int64_t items = static_cast<int64_t>(cum[g.n_experts]) * row_tiles;
+    // this CTA's items, and super-blocks, one after another
+    const int my_items = items > blockIdx.x ? static_cast<int>((items - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
+    const int64_t blocks = static_cast<int64_t>(my_items) * nsb;
 
     if (warp < 4) {
         if constexpr (C::kRegsIssue) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsIssue ? C::kRegsIssue : 24));
@@ -486,15 +522,23 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             }
             __syncwarp();
         } else if (warp == 2) {
-            // -------------------------------------------------------- copies of the weights
+            // -------------------------------------------------------- copies: raw weights, B, the columns' exponents
             if (lane == 0) {
                 const uint64_t pol = l2_evict_first_policy();
-                RingPos p{0, 0};
-                int64_t issued = 0;
+                RingPos p{0, 0}, pb{0, 0}, ph{0, 0};
+                int64_t issued = 0, issued_b = 0, issued_h = 0;
                 bool ok = true;
-                for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
-                    const Item w = item_at<N>(it, cum, g);
-                    const int y0 = static_cast<int>(w.e * g.out_dim + static_cast<int64_t>(w.rt) * (kSwiglu ? 128 : 256));
+                for (int i = 0; i < my_items && ok; ++i) {
+                    // tiles of outputs after one another, the expert's tiles of rows within
+                    const int64_t it = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+                    const int e = expert_of(static_cast<int>(it / row_tiles), cum, g.n_experts);
+                    const int tiles = cum[e + 1] - cum[e];
+                    const int64_t at = it - static_cast<int64_t>(cum[e]) * row_tiles;
+                    const int rt = static_cast<int>(at / tiles), tile = static_cast<int>(at - static_cast<int64_t>(rt) * tiles);
+                    const int row = g.offsets[e] + tile * N;
+                    sts4(sm32 + C::off_item + 16 * (i % kItems), row, min(N, g.offsets[e + 1] - row), rt, 0);
+                    const int y0 = static_cast<int>(e * g.out_dim + static_cast<int64_t>(rt) * (kSwiglu ? 128 : 256));
+                    const int64_t cell0 = static_cast<int64_t>(cum[e] + tile) * nsb;
                     for (int sb = 0; sb < nsb && ok; ++sb) {
                         for (int mt = 0; mt < 2; ++mt) {
                             if (!(ok = wait_one(&b.raw_empty[p.s], p.par ^ 1u, b, g.err))) break;
@@ -504,6 +548,22 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                             ++issued;
                             ring_next(p, C::kRingRaw);
                         }
+                        const uint8_t *from = a.pack + (cell0 + sb) * C::kCellB;
+                        for (int step = 0; step < C::kSteps && ok; ++step) {
+                            if (!(ok = wait_one(&b.b_empty[pb.s], pb.par ^ 1u, b, g.err))) break;
+                            const bool last = step == C::kSteps - 1;
+                            const uint32_t bytes = (!C::kOwnMins || !last ? C::kBytesB : 0) + (last ? N * 64 : 0);
+                            mbar_arrive_expect_tx(&b.b_full[pb.s], bytes);
+                            bulk_g2s(sm + C::off_b + pb.s * C::kSlotB, from, bytes, &b.b_full[pb.s]);
+                            from += bytes;
+                            ++issued_b;
+                            ring_next(pb, C::kRingB);
+                        }
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&b.cs_full[ph.s], N * 4);
+                        bulk_g2s(sm + C::off_cs + ph.s * N * 4, a.col_scale + (cell0 + sb) * N, N * 4, &b.cs_full[ph.s]);
+                        ++issued_h;
+                        ring_next(ph, kHdr);
                     }
                 }
                 // copies in flight land before the CTA ends
@@ -511,89 +571,15 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     const RingPos q = ring_pos(k, C::kRingRaw);
                     mbar_wait(&b.raw_full[q.s], q.par);
                 }
-            }
-        }
-    } else if (warp < C::kFirstUnpack) {
-        // ------------------------------------------------------------ B: lanes have kRowsB rows by 4 pieces of 16 bytes
-        if constexpr (C::kRegsGather) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsGather ? C::kRegsGather : 24));
-        if (warp - 4 < C::kGather) {
-            const int col = (lane & 7) + 8 * C::kRowsB * (warp - 4), quarter = lane >> 3;  // this lane's first column; then every 8th
-            RingPos pb{0, 0}, pf{0, 0};
-            int h = 0, behind = 0, fstep = 0, fh = 0;  // gathers under way; the step and super-block that arrive next
-            bool ok = true;
-            auto arrived = [&] {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&b.b_full[pf.s]);
-                    if (fstep == C::kSteps - 1) mbar_arrive(&b.h_full[fh]);
+                for (int64_t k = max(static_cast<int64_t>(0), issued_b - C::kRingB); k < issued_b; ++k) {
+                    const RingPos q = ring_pos(k, C::kRingB);
+                    mbar_wait(&b.b_full[q.s], q.par);
                 }
-                ring_next(pf, C::kRingB);
-                if (++fstep == C::kSteps) {
-                    fstep = 0;
-                    fh = (fh + 1) % kHdr;
-                }
-            };
-            for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
-                const Item w = item_at<N>(it, cum, g);
-                __syncwarp();
-                for (int c = 8 * C::kRowsB * (warp - 4) + lane; c < 8 * C::kRowsB * (warp - 3); c += 32) {
-                    int r = -1;  // the row of x, -1 beyond the expert's
-                    if (c < w.m) {
-                        r = w.row + c;
-                        if (g.rows) {
-                            const int pair = g.rows[r];
-                            const bool fine = pair >= 0 && pair < g.n_pairs;
-                            if (!fine) set_error(g.err, DEV_BAD_LENGTH);
-                            r = fine ? pair / g.top_k : 0;
-                        }
-                    }
-                    sts1(sm32 + C::off_src + 4 * c, static_cast<uint32_t>(r));
-                }
-                __syncwarp();
-                for (int sb = 0; sb < nsb && ok; ++sb) {
-#pragma unroll 1
-                    for (int step = 0; step < C::kSteps; ++step) {
-                        if (!(ok = wait_warp(&b.b_empty[pb.s], pb.par ^ 1u, b, g.err))) break;
-                        const uint32_t dst = sm32 + C::off_b + pb.s * C::kSlotB;
-#pragma unroll 2
-                        for (int j = 0; j < C::kRowsB; ++j) {
-                            const int c0 = col + 8 * j, src = lds1i(sm32 + C::off_src + 4 * c0);
-                            const int64_t cell = static_cast<int64_t>(max(src, 0)) * nsb + sb;
-                            const uint32_t bytes = src >= 0 ? 16 : 0;
-                            if (!C::kOwnMins || step < C::kSteps - 1) {
-                                const uint8_t *from = a.pack + cell * kPackBytes + step * (C::kChunks * 256) + quarter * 16;
-                                const uint32_t to = dst + (c0 >> 3) * (C::kChunks * 1024) + quarter * 128 + (lane & 7) * 16;
-#pragma unroll
-                                for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-                                    for (int i = 0; i < 2; ++i) {  // the chunk's first and second half
-                                        gather16(to + c * 1024 + i * 512, from + c * 256 + i * 64, bytes);
-                                        gather16(to + N * C::kChunks * 128 + c * 1024 + i * 512, from + c * 256 + 128 + i * 64, bytes);
-                                    }
-                            }
-                            if (step == C::kSteps - 1) {
-                                // 8 high pieces of s, 8 low ones, and both again; the columns' exponents
-                                const uint32_t to = dst + (C::kOwnMins ? 0 : C::kBytesB) + (c0 >> 3) * 512 + quarter * 128 + (lane & 7) * 16;
-                                gather16(to, a.mins + cell * 32 + (quarter & 1) * 16, bytes);
-                                if (quarter == 0) gather4(sm32 + C::off_cs + 4 * (h * N + c0), a.col_scale + cell, bytes / 4);
-                            }
-                        }
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                        ring_next(pb, C::kRingB);
-                        if (behind == C::kLagB) {
-                            asm volatile("cp.async.wait_group %0;" ::"n"(C::kLagB) : "memory");
-                            arrived();
-                        } else {
-                            ++behind;
-                        }
-                    }
-                    h = (h + 1) % kHdr;
+                for (int64_t k = max(static_cast<int64_t>(0), issued_h - kHdr); k < issued_h; ++k) {
+                    const RingPos q = ring_pos(k, kHdr);
+                    mbar_wait(&b.cs_full[q.s], q.par);
                 }
             }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            if (ok)
-                for (; behind > 0; --behind) arrived();
         }
     } else if (warp < C::kFirstSum) {
         // ------------------------------------------------------------ unpacking
@@ -695,14 +681,14 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         const uint32_t at = tmem + (static_cast<uint32_t>(32 * (dw & 3)) << 16) + col0;
         RingPos pd{0, 0}, ph{0, 0};
         bool ok = true;
-        for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        for (int item = 0; item < my_items && ok; ++item) {
             float sum[2][C::kHalf];
 #pragma unroll
             for (int i = 0; i < C::kHalf; ++i) sum[0][i] = sum[1][i] = 0.0f;
             for (int sb = 0; sb < nsb && ok; ++sb) {
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
-                    if (mt == 0 && !(ok = wait_warp(&b.h_full[ph.s], ph.par, b, g.err))) break;
+                    if (mt == 0 && !(ok = wait_warp(&b.h_full[ph.s], ph.par, b, g.err) && wait_warp(&b.cs_full[ph.s], ph.par, b, g.err))) break;
                     if (!(ok = wait_warp(&b.d_full[pd.s], pd.par, b, g.err))) break;
                     fence_after();
                     const float gs = lds1f(sm32 + C::off_g + 4 * ((ph.s * 2 + mt) * 128 + wrow));
@@ -734,7 +720,15 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             }
             if (!ok || *static_cast<volatile int *>(&b.gave_up)) break;
             // ---- outputs: a warp's 32 rows lie side by side in each column's row of y
-            const Item w = item_at<N>(it, cum, g);
+            struct {
+                int row, m, rt;
+            } w;
+            {
+                const uint4 t = lds4(sm32 + C::off_item + 16 * (item % kItems));
+                w.row = t.x;
+                w.m = t.y;
+                w.rt = t.z;
+            }
             if constexpr (kSwiglu) {
                 const int64_t o = static_cast<int64_t>(w.rt) * 128 + wrow;
                 const bool in = o < g.out_dim;
@@ -800,45 +794,62 @@ cudaError_t launch(const TcArgs &a, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, moe_gemm_tc_kernel<N, kSwiglu>, a);
 }
 
-template <int N>
-cudaError_t launch_n(const TcArgs &a, cudaStream_t s)
-{
-    return a.g.w2 ? launch<N, true>(a, s) : launch<N, false>(a, s);
-}
-
 }  // namespace
 
-int64_t moe_pack_bytes(int64_t rows, int64_t in_dim) { return rows * (in_dim / 256) * (kPackBytes + 32 + 4); }
-
-cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &g, int columns, void *workspace, cudaStream_t s)
+namespace {
+template <int N>
+int64_t pack_bytes(int64_t n_pairs, int n_experts, int64_t in_dim)
 {
+    return max_tiles<N>(n_pairs, n_experts) * (in_dim / 256) * (Cfg<N>::kCellB + N * 4);
+}
+
+template <int N>
+cudaError_t launch_all(const MoeGemvArgs &g, void *workspace, cudaStream_t s)
+{
+    using C = Cfg<N>;
     TcArgs a{};
     a.g = g;
-    const int64_t x_rows = g.rows ? g.n_pairs / g.top_k : g.n_pairs, cells = x_rows * (g.in_dim / 256);
-    uint8_t *pack = static_cast<uint8_t *>(workspace), *mins = pack + cells * kPackBytes;
-    float *col_scale = reinterpret_cast<float *>(mins + cells * 32);
+    const int nsb = g.in_dim / 256;
+    const int64_t tiles = max_tiles<N>(g.n_pairs, g.n_experts);
+    uint8_t *pack = static_cast<uint8_t *>(workspace);
+    float *col_scale = reinterpret_cast<float *>(pack + tiles * nsb * C::kCellB);
     a.pack = pack;
-    a.mins = mins;
     a.col_scale = col_scale;
-    const uint64_t row_bytes = static_cast<uint64_t>(g.in_dim) / 256 * 144, rows = static_cast<uint64_t>(g.n_experts) * g.out_dim;
+    const uint64_t row_bytes = static_cast<uint64_t>(nsb) * 144, rows = static_cast<uint64_t>(g.n_experts) * g.out_dim;
     cudaError_t e = encode_tensor_map_2d(&a.map1, g.w1, 1, row_bytes, rows, row_bytes, 144, 128);
     if (e == cudaSuccess && g.w2) e = encode_tensor_map_2d(&a.map2, g.w2, 1, row_bytes, rows, row_bytes, 144, 128);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((cells + kPackWarps - 1) / kPackWarps));
-    cfg.blockDim = dim3(32 * kPackWarps);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(std::min<int64_t>(nsb, std::max<int64_t>(1, 2048 / tiles))));
+    cfg.blockDim = dim3(kPackThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = g_use_pdl ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, moe_pack_kernel, g.xq, g.xd, g.xs, pack, mins, col_scale, cells);
+    e = cudaLaunchKernelEx(&cfg, moe_pack_kernel<N>, g, pack, col_scale);
     if (e != cudaSuccess) return e;
+    return g.w2 ? launch<N, true>(a, s) : launch<N, false>(a, s);
+}
+}  // namespace
+
+int64_t moe_pack_bytes(int columns, int64_t n_pairs, int n_experts, int64_t in_dim)
+{
     switch (columns) {
-        case 16: return launch_n<16>(a, s);
-        case 32: return launch_n<32>(a, s);
-        default: return launch_n<128>(a, s);
+        case 16: return pack_bytes<16>(n_pairs, n_experts, in_dim);
+        case 32: return pack_bytes<32>(n_pairs, n_experts, in_dim);
+        case 128: return pack_bytes<128>(n_pairs, n_experts, in_dim);
+        default: return 0;
+    }
+}
+
+cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &g, int columns, void *workspace, cudaStream_t s)
+{
+    switch (columns) {
+        case 16: return launch_all<16>(g, workspace, s);
+        case 32: return launch_all<32>(g, workspace, s);
+        default: return launch_all<128>(g, workspace, s);
     }
 }
 

@@ -353,9 +353,9 @@ struct MoeGemvArgs {
 };
 cudaError_t launch_moe_gemv(const MoeGemvArgs &a, cudaStream_t s);
 
-// The same on the tensor cores (moe_gemm_tc.cu), in tiles of `columns` rows: 16, 32, 64 or 128.
+// The same on the tensor cores (moe_gemm_tc.cu), in tiles of `columns` rows: 16, 32 or 128.
 cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &a, int columns, void *workspace, cudaStream_t s);
-int64_t moe_pack_bytes(int64_t rows, int64_t in_dim);  // of its workspace, for that many rows of x
+int64_t moe_pack_bytes(int columns, int64_t n_pairs, int n_experts, int64_t in_dim);  // of its workspace
 
 // Whichever of the two the sizes call for.
 int moe_columns(int64_t n_pairs, int n_experts);
