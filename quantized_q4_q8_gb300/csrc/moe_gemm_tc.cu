@@ -55,9 +55,8 @@ struct Cfg {
     static constexpr int kChunks = N >= 64 ? 1 : 2;   // of 64 weights, in a step
     static constexpr bool kOwnMins = N >= 64;         // the mins are a step of their own (no room in tensor memory for wider slots)
     static constexpr int kSteps = 4 / kChunks + (kOwnMins ? 1 : 0);  // of a super-block, the last one with the mins
-    static constexpr int kGroups = N >= 64 ? 2 : 4;   // that unpack A: half of them each matrix, in turn its steps
-    static constexpr int kShare = kGroups / 2;
-    static constexpr int kSlotsA = N == 64 ? 4 : 2;   // of A for each matrix
+    static constexpr int kGroups = 4;                 // that unpack A: two for each matrix, taking its steps in turn
+    static constexpr int kSlotsA = 2;                 // of A for each matrix: one for each group
     static constexpr int kBytesB = kChunks * N * 256; // two pieces of 64 * kChunks values
     static constexpr int kSlotB = kBytesB + (kOwnMins ? 0 : N * 64);
     static constexpr int kRingB = N == 128 ? 4 : 5;
@@ -69,7 +68,7 @@ struct Cfg {
     static constexpr int kFirstUnpack = 4, kFirstSum = kFirstUnpack + 4 * kGroups;
     static constexpr int kThreads = 32 * (kFirstSum + 8);
     // registers of the roles (0: as launched)
-    static constexpr int kRegsIssue = N == 128 ? 40 : 0, kRegsUnpack = N == 128 ? 64 : 0, kRegsSum = N == 128 ? 152 : 0;
+    static constexpr int kRegsIssue = N == 128 ? 40 : 0, kRegsUnpack = N == 128 ? 40 : 0, kRegsSum = N == 128 ? 152 : 0;
     static constexpr int off_b = 0;
     static constexpr int off_raw = off_b + kRingB * kSlotB;
     static constexpr int off_g = off_raw + kRingRaw * kRawBytes;   // [kHdr][2][128]
@@ -81,9 +80,7 @@ struct Cfg {
     static_assert(kColA + 2 * kSlotsA * kWidthA <= 512, "tensor memory");
     static_assert(off_raw % 128 == 0, "copies start on 128 bytes");
     static_assert(bytes <= 227 * 1024, "shared memory");
-    // A slot of A is filled again by the group that filled it before, or by one that has seen the product before that done: otherwise
-    // a wait could take the phase before for the one it waits for
-    static_assert(kSlotsA % kShare == 0 && kRingRaw % 2 == 0, "rings");
+    static_assert(kRingRaw % 2 == 0, "rings");
     // Scales of super-block k take the place of those of k - kHdr, added up by then: whoever writes them has seen the products of a
     // step at most kRingB (or kSlotsA) before done, whose accumulators were free, which takes all but the last three of those before
     static_assert((kRingB + kSteps - 1) / kSteps + 1 <= kHdr, "scales");
@@ -105,35 +102,45 @@ struct TcArgs {
     const float *col_scale;  // 2^E [tiles][super-blocks][kN]
 };
 
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t stride)
-{
-    // K-major, no swizzle: core matrices of 8 rows x 16 bytes, 128 bytes apart along K, groups of 8 rows `stride` apart
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | (1ull << 46);
-}
+// Shared-memory operand, K-major, no swizzle: core matrices of 8 rows x 16 bytes, 128 bytes apart along K, groups of 8 rows `stride`
+// apart; in two words
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((128u >> 4) << 16); }
+__host__ __device__ constexpr uint32_t operand_high(uint32_t stride) { return (stride >> 4) | (1u << 14); }
 __host__ __device__ constexpr uint32_t idesc_f16(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// One lane of the warp, all of which are here.
+__device__ __forceinline__ uint32_t elect()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+// Issued by the elected lane.  A predicate and no branch: the operands are the same for the warp and stay in uniform registers (in a
+// branch of one lane each would be moved there for every instruction, some 100 cycles).
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a, uint32_t b_low, uint32_t b_high, uint32_t idesc, bool acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_low), "r"(b_high), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(elected)
         : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t *bar)
+__device__ __forceinline__ void commit(uint32_t elected, uint64_t *bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(elected)
+        : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&r)[16])
+__device__ __forceinline__ void tm_store8(uint32_t at, const uint32_t (&r)[8])
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
-        : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(at)
+                 : "memory");
 }
 __device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // 8 columns of the warp's 32 rows, waited for in the same statement
@@ -437,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         }
         for (int i = 0; i < C::kRingRaw; ++i) {
             mbar_init(&b.raw_full[i], 1);
-            mbar_init(&b.raw_empty[i], 4 * C::kShare);
+            mbar_init(&b.raw_empty[i], 4 * 2);
         }
         for (int i = 0; i < kBufD; ++i) {
             mbar_init(&b.d_full[i], 1);
@@ -464,8 +471,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = b.tmem;
-    const int64_t items = static_cast<int64_t>(cum[g.n_experts]) * row_tiles;
+    constexpr uint32_t tmem = 0;  // all 512 columns are allocated
+    const int64_t items = b.tmem == tmem ? static_cast<int64_t>(cum[g.n_experts]) * row_tiles : 0;
     // this CTA's items, and super-blocks, one after another
     const int my_items = items > blockIdx.x ? static_cast<int>((items - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
     const int64_t blocks = static_cast<int64_t>(my_items) * nsb;
@@ -475,6 +482,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         if (warp < 2) {
             // -------------------------------------------------------- products of matrix `warp`
             const int mt = warp;
+            const uint32_t elected = elect();
             RingPos pa{0, 0}, pb{0, 0}, pd{mt, 0};
             bool ok = true;
             for (int64_t k = 0; k < blocks && ok; ++k) {
@@ -489,38 +497,33 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         if (!(ok = wait_warp(&b.a_full[mt][pa.s], pa.par, b, g.err))) break;
                     }
                     fence_after();
-                    if (lane == 0) {
-                        const uint32_t d = tmem + pd.s * C::kColsD;
-                        const uint32_t ta = tmem + C::kColA + (mt * C::kSlotsA + pa.s) * C::kWidthA;
-                        const uint32_t tb = sm32 + C::off_b + pb.s * C::kSlotB;
-                        if (!C::kOwnMins || step < C::kSteps - 1) {
-                            const uint64_t desc = operand_desc(tb, C::kChunks * 1024);
+                    const uint32_t d = tmem + pd.s * C::kColsD;
+                    const uint32_t ta = tmem + C::kColA + (mt * C::kSlotsA + pa.s) * C::kWidthA;
+                    const uint32_t tb = operand_low(sm32 + C::off_b + pb.s * C::kSlotB);
+                    if (!C::kOwnMins || step < C::kSteps - 1) {
 #pragma unroll
-                            for (int i = 0; i < 4 * C::kChunks; ++i) {
-                                mma_ts(d, ta + 8 * i, desc + 16 * i, idesc_f16(C::kColsD), step > 0 || i > 0);
-                                if constexpr (!C::kStack) mma_ts(d, ta + 8 * i, desc + (N * C::kChunks * 8 + 16 * i), idesc_f16(N), 1);
-                            }
+                        for (int i = 0; i < 4 * C::kChunks; ++i) {
+                            mma_ts(elected, d, ta + 8 * i, tb + 16 * i, operand_high(C::kChunks * 1024), idesc_f16(C::kColsD), step > 0 || i > 0);
+                            if constexpr (!C::kStack)
+                                mma_ts(elected, d, ta + 8 * i, tb + (N * C::kChunks * 8 + 16 * i), operand_high(C::kChunks * 1024), idesc_f16(N), true);
                         }
-                        if (step == C::kSteps - 1) {
-                            const uint64_t desc = operand_desc(tb + (C::kOwnMins ? 0 : C::kBytesB), 512);
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) mma_ts(d, ta + (C::kOwnMins ? 0 : 32 * C::kChunks) + 8 * i, desc + 16 * i, idesc_f16(N), 1);
-                        }
-                        commit(&b.a_empty[mt][pa.s]);
-                        commit(&b.b_empty[pb.s]);
-                        if (step == C::kSteps - 1) commit(&b.d_full[pd.s]);
                     }
-                    __syncwarp();
+                    if (step == C::kSteps - 1) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            mma_ts(elected, d, ta + (C::kOwnMins ? 0 : 32 * C::kChunks) + 8 * i, tb + (C::kOwnMins ? 0 : C::kBytesB / 16) + 16 * i,
+                                   operand_high(512), idesc_f16(N), true);
+                    }
+                    commit(elected, &b.a_empty[mt][pa.s]);
+                    commit(elected, &b.b_empty[pb.s]);
+                    if (step == C::kSteps - 1) commit(elected, &b.d_full[pd.s]);
                     ring_next(pa, C::kSlotsA);
                     ring_next(pb, C::kRingB);
                 }
                 ring_add(pd, 2, kBufD);
             }
-            if (lane == 0) {
-                commit(&b.done[mt]);  // every product issued has completed once this arrives
-                mbar_wait(&b.done[mt], 0);
-            }
-            __syncwarp();
+            commit(elected, &b.done[mt]);  // every product issued has completed once this arrives
+            mbar_wait(&b.done[mt], 0);
         } else if (warp == 2) {
             // -------------------------------------------------------- copies: raw weights, B, the columns' exponents
             if (lane == 0) {
@@ -587,90 +590,100 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         // group: matrix, and which of its steps
         const int cw = warp - C::kFirstUnpack, wrow = 32 * (cw & 3) + lane, mt = (cw >> 2) & 1, turn = cw >> 3;
         const uint32_t ta0 = tmem + (static_cast<uint32_t>(32 * (cw & 3)) << 16) + C::kColA + mt * C::kSlotsA * C::kWidthA;
-        RingPos pa{turn % C::kSlotsA, 0}, praw{mt, 0};
-        int h = 0;
+        RingPos praw{mt, 0};
+        unsigned apar = 0;
+        const uint32_t ta = ta0 + turn * C::kWidthA;
+        int h = 0, step = turn;  // this group's steps are every other one, over the super-blocks' ends
         bool ok = true;
         for (int64_t k = 0; k < blocks && ok; ++k) {
             if (!(ok = wait_warp(&b.raw_full[praw.s], praw.par, b, g.err))) break;
             const uint32_t raw = sm32 + C::off_raw + praw.s * kRawBytes + wrow * 144;
-            uint4 hd = lds4(raw);
-            const bool any_wide = __any_sync(0xffffffffu, head_of(hd.x).wide);
-            // six-bit scales, four to a word: sub-blocks 0-3 and 4-7
-            const uint32_t sc0 = hd.y & 0x3f3f3f3fu, sc1 = (hd.w & 0x0f0f0f0fu) | ((hd.y >> 2) & 0x30303030u);
-#pragma unroll
-            for (int step0 = 0; step0 < C::kSteps; step0 += C::kShare) {
-                const int step = step0 + turn;  // kShare divides kSteps, or is 1
-                const uint32_t ta = ta0 + pa.s * C::kWidthA;
-                bool waited = false;
+            uint32_t sc0, sc1;  // six-bit scales, four to a word: sub-blocks 0-3 and 4-7
+            bool any_wide;
+            {
+                const uint4 hd = lds4(raw);
+                any_wide = __any_sync(0xffffffffu, head_of(hd.x).wide);
+                sc0 = hd.y & 0x3f3f3f3fu;
+                sc1 = (hd.w & 0x0f0f0f0fu) | ((hd.y >> 2) & 0x30303030u);
+            }
+#pragma unroll 1
+            for (; step < C::kSteps; step += 2) {
+                if (!(ok = wait_warp(&b.a_empty[mt][turn], apar ^ 1u, b, g.err))) break;
+                fence_after();
                 if (!C::kOwnMins || step < C::kSteps - 1) {
 #pragma unroll
                     for (int cc = 0; cc < C::kChunks; ++cc) {
                         const int c = step * C::kChunks + cc;
-                        const uint4 qa = lds4(raw + 16 + 32 * c), qb = lds4(raw + 32 + 32 * c);
-                        const uint32_t words[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
                         const uint32_t six = (c < 2 ? sc0 : sc1) >> (16 * (c & 1));
+                        // (1024 + q) sc - 1024 sc for the low codes, (1024 + 16 q) (sc / 16) - 64 sc for the high ones: one rounding of an exact
+                        // small integer
+                        const float s0 = static_cast<float>(six & 63u), s1 = static_cast<float>((six >> 8) & 63u);
+                        const uint32_t mul0 = pack2(s0, s0), add0 = pack2(s0 * -1024.0f, s0 * -1024.0f);
+                        const uint32_t mul1 = pack2(s1 * 0.0625f, s1 * 0.0625f), add1 = pack2(s1 * -64.0f, s1 * -64.0f);
 #pragma unroll
-                        for (int hi = 0; hi < 2; ++hi) {
-                            // (1024 + q) sc - 1024 sc, or (1024 + 16 q) (sc / 16) - 64 sc: one rounding of an exact small integer
-                            const float s6 = static_cast<float>((six >> (8 * hi)) & 63u);
-                            const uint32_t mul = pack2(hi ? s6 * 0.0625f : s6, hi ? s6 * 0.0625f : s6);
-                            const uint32_t add = pack2(hi ? s6 * -64.0f : s6 * -1024.0f, hi ? s6 * -64.0f : s6 * -1024.0f);
-                            const uint32_t mask = hi ? 0x00f000f0u : 0x000f000fu;
-                            uint32_t o[16];
+                        for (int half = 0; half < 2; ++half) {
+                            const uint4 q = lds4(raw + 16 + 32 * c + 16 * half);
+                            const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+                            uint32_t lo[8], hi[8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                o[2 * i] = hfma2u(lop_and_or(words[i], mask, 0x64006400u), mul, add);
-                                o[2 * i + 1] = hfma2u(lop_and_or(words[i] >> 8, mask, 0x64006400u), mul, add);
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t w8 = words[i] >> 8;
+                                lo[2 * i] = hfma2u(lop_and_or(words[i], 0x000f000fu, 0x64006400u), mul0, add0);
+                                lo[2 * i + 1] = hfma2u(lop_and_or(w8, 0x000f000fu, 0x64006400u), mul0, add0);
+                                hi[2 * i] = hfma2u(lop_and_or(words[i], 0x00f000f0u, 0x64006400u), mul1, add1);
+                                hi[2 * i + 1] = hfma2u(lop_and_or(w8, 0x00f000f0u, 0x64006400u), mul1, add1);
                             }
                             if (any_wide) {
                                 const Head head = head_of(lds4(raw).x);
                                 const float f = head.wide && head.fine ? __fdiv_rn(head.d, head.dmin) : 1.0f;
                                 const uint32_t shrink = pack2(f, f);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = hmul2u(o[i], shrink);
+                                for (int i = 0; i < 8; ++i) {
+                                    lo[i] = hmul2u(lo[i], shrink);
+                                    hi[i] = hmul2u(hi[i], shrink);
+                                }
                             }
-                            if (!waited) {
-                                ok = wait_warp(&b.a_empty[mt][pa.s], pa.par ^ 1u, b, g.err);
-                                fence_after();
-                                waited = true;
-                            }
-                            if (ok) tm_store16(ta + 32 * cc + 16 * hi, o);
+                            tm_store8(ta + 32 * cc + 8 * half, lo);
+                            tm_store8(ta + 32 * cc + 16 + 8 * half, hi);
                         }
                     }
                 }
                 if (step == C::kSteps - 1) {
-                    hd = lds4(raw);
+                    const uint4 hd = lds4(raw);
                     const Head head = head_of(hd.x);
                     const float ratio = head.wide ? 1.0f : head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
                     const float by = head.fine ? -0.125f * ratio : 0.0f;
                     const uint32_t mn0 = hd.z & 0x3f3f3f3fu, mn1 = ((hd.w >> 4) & 0x0f0f0f0fu) | ((hd.z >> 2) & 0x30303030u);
-                    uint32_t o[16];  // 8 high pieces, twice, 8 low ones, twice
+                    uint32_t o[8];  // 4 words of high pieces, twice; 4 of low ones, twice
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t two = (i < 2 ? mn0 : mn1) >> (16 * (i & 1));
-                        const float r0 = by * static_cast<float>(two & 63u), r1 = by * static_cast<float>((two >> 8) & 63u);
-                        o[i] = o[4 + i] = pack2(r0, r1);
-                        const float2 t = unpack2(o[i]);
-                        o[8 + i] = o[12 + i] = pack2(r0 - t.x, r1 - t.y);
+                    for (int low = 0; low < 2; ++low) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t two = (i < 2 ? mn0 : mn1) >> (16 * (i & 1));
+                            float r0 = by * static_cast<float>(two & 63u), r1 = by * static_cast<float>((two >> 8) & 63u);
+                            if (low) {
+                                const float2 t = unpack2(pack2(r0, r1));
+                                r0 -= t.x;
+                                r1 -= t.y;
+                            }
+                            o[i] = o[4 + i] = pack2(r0, r1);
+                        }
+                        tm_store8(ta + (C::kOwnMins ? 0 : 32 * C::kChunks) + 8 * low, o);
                     }
                     sts1(sm32 + C::off_g + 4 * ((h * 2 + mt) * 128 + wrow), __float_as_uint(!head.fine ? NAN : head.wide ? head.dmin : head.d));
-                    if (!waited) {
-                        ok = wait_warp(&b.a_empty[mt][pa.s], pa.par ^ 1u, b, g.err);
-                        fence_after();
-                    }
-                    if (ok) tm_store16(ta + (C::kOwnMins ? 0 : 32 * C::kChunks), o);
                 }
-                if (!ok) break;
                 tm_store_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&b.a_full[mt][pa.s]);
+                    mbar_arrive(&b.a_full[mt][turn]);
                     if (step == C::kSteps - 1) mbar_arrive(&b.h_full[h]);
-                    if (step0 + C::kShare >= C::kSteps) mbar_arrive(&b.raw_empty[praw.s]);
                 }
-                ring_add(pa, C::kShare, C::kSlotsA);
+                apar ^= 1u;
             }
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&b.raw_empty[praw.s]);
+            step -= C::kSteps;
             h = (h + 1) % kHdr;
             ring_add(praw, 2, C::kRingRaw);
         }
@@ -729,40 +742,39 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                 w.m = t.y;
                 w.rt = t.z;
             }
-            if constexpr (kSwiglu) {
-                const int64_t o = static_cast<int64_t>(w.rt) * 128 + wrow;
-                const bool in = o < g.out_dim;
-                int64_t to = static_cast<int64_t>(w.row + col0) * g.out_dim + o;
+            // eight columns in straight code, then the others move up: 64 in straight code are more than the instruction caches hold
+            const int64_t o = static_cast<int64_t>(w.rt) * (kSwiglu ? 128 : 256) + wrow;
+            const bool in = o < g.out_dim, in2 = o + 128 < g.out_dim;
+            int64_t to = static_cast<int64_t>(w.row + col0) * g.out_dim + o;
+#pragma unroll 1
+            for (int i0 = 0; i0 < C::kHalf && col0 + i0 < w.m; i0 += 8) {
 #pragma unroll
-                for (int i = 0; i < C::kHalf; ++i, to += g.out_dim) {
-                    if (col0 + i >= w.m) break;
-                    const float v = in ? __fdividef(sum[0][i], 1.0f + expf(-sum[0][i])) * sum[1][i] : 0.0f;
-                    if (g.y && in) g.y[to] = v;
-                    if (g.yq && in) {  // out_dim is a multiple of 32: all of the warp or none
-                        const uint32_t key = isnan(v) ? 0u : __float_as_uint(fabsf(v)) + 1u;
-                        const uint32_t top = __reduce_max_sync(0xffffffffu, key);
-                        const float d = top ? __fdiv_rn(__uint_as_float(top - 1u), 127.0f) : NAN;
-                        const int code = q8_code(v, q8_scale(d));
-                        const int total = __reduce_add_sync(0xffffffffu, code);
-                        g.yq[to] = static_cast<int8_t>(code);
-                        if (lane == 0) {
-                            g.yd[to / 32] = d;
-                            g.ys[to / 32] = __fmul_rn(d, static_cast<float>(total));
+                for (int i = 0; i < 8; ++i, to += g.out_dim) {
+                    if (col0 + i0 + i >= w.m) break;
+                    if constexpr (kSwiglu) {
+                        const float v = in ? __fdividef(sum[0][i], 1.0f + expf(-sum[0][i])) * sum[1][i] : 0.0f;
+                        if (g.y && in) g.y[to] = v;
+                        if (g.yq && in) {  // out_dim is a multiple of 32: all of the warp or none
+                            const uint32_t key = isnan(v) ? 0u : __float_as_uint(fabsf(v)) + 1u;
+                            const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+                            const float d = top ? __fdiv_rn(__uint_as_float(top - 1u), 127.0f) : NAN;
+                            const int code = q8_code(v, q8_scale(d));
+                            const int total = __reduce_add_sync(0xffffffffu, code);
+                            g.yq[to] = static_cast<int8_t>(code);
+                            if (lane == 0) {
+                                g.yd[to / 32] = d;
+                                g.ys[to / 32] = __fmul_rn(d, static_cast<float>(total));
+                            }
                         }
+                    } else {
+                        if (in) g.y[to] = sum[0][i];
+                        if (in2) g.y[to + 128] = sum[1][i];
                     }
                 }
-            } else {
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    const int64_t o = static_cast<int64_t>(w.rt) * 256 + 128 * mt + wrow;
-                    if (o < g.out_dim) {
-                        float *to = g.y + static_cast<int64_t>(w.row + col0) * g.out_dim + o;
-#pragma unroll
-                        for (int i = 0; i < C::kHalf; ++i, to += g.out_dim) {
-                            if (col0 + i >= w.m) break;
-                            *to = sum[mt][i];
-                        }
-                    }
+                for (int i = 0; i + 8 < C::kHalf; ++i) {
+                    sum[0][i] = sum[0][i + 8];
+                    sum[1][i] = sum[1][i + 8];
                 }
             }
         }
@@ -771,7 +783,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
     __syncthreads();
     if (warp == 0) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(b.tmem) : "memory");
     }
 }
 
