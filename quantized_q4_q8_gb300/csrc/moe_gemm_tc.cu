@@ -46,7 +46,6 @@ namespace {
 
 constexpr int kRawBytes = 144 * 128;
 constexpr int kHdr = 4;      // super-blocks whose scales are held
-constexpr int kBufD = 3;     // accumulators
 constexpr int kItems = 16;   // items whose places are held (copies are some six super-blocks ahead of the sums)
 template <int N>
 struct Cfg {
@@ -56,7 +55,8 @@ struct Cfg {
     static constexpr bool kOwnMins = N >= 64;         // the mins are a step of their own (no room in tensor memory for wider slots)
     static constexpr int kSteps = 4 / kChunks + (kOwnMins ? 1 : 0);  // of a super-block, the last one with the mins
     static constexpr int kGroups = 4;                 // that unpack A: two for each matrix, taking its steps in turn
-    static constexpr int kSlotsA = 2;                 // of A for each matrix: one for each group
+    static constexpr int kBufD = N == 128 ? 2 : 3;    // accumulators: one for each matrix, or three in turn
+    static constexpr int kSlotsA = N == 128 ? 4 : 2;  // of A for each matrix; its two groups fill them in turn
     static constexpr int kBytesB = kChunks * N * 256; // two pieces of 64 * kChunks values
     static constexpr int kSlotB = kBytesB + (kOwnMins ? 0 : N * 64);
     static constexpr int kRingB = N == 128 ? 4 : 5;
@@ -89,7 +89,7 @@ struct Cfg {
 };
 
 struct Bars {
-    uint64_t a_full[2][4], a_empty[2][4], b_full[6], b_empty[6], raw_full[8], raw_empty[8], d_full[kBufD], d_empty[kBufD], h_full[kHdr], cs_full[kHdr], done[2];
+    uint64_t a_full[2][4], a_empty[2][4], b_full[6], b_empty[6], raw_full[8], raw_empty[8], d_full[3], d_empty[3], h_full[kHdr], cs_full[kHdr], done[2];
     uint32_t tmem;
     int gave_up;
 };
@@ -257,6 +257,13 @@ __device__ __forceinline__ Head head_of(uint32_t word)
 {
     const float d = h2f(static_cast<uint16_t>(word & 0xffffu)), dmin = h2f(static_cast<uint16_t>(word >> 16));
     return {d, dmin, fabsf(dmin) > 8192.0f * fabsf(d), isfinite(d) && isfinite(dmin)};
+}
+
+// Whether the mins' scale is over 2^13 times the other (in f16, where that is exact or infinite)
+__device__ __forceinline__ bool mins_are_unit(uint32_t word)
+{
+    const __half d = __ushort_as_half(static_cast<unsigned short>(word & 0x7fffu)), m = __ushort_as_half(static_cast<unsigned short>((word >> 16) & 0x7fffu));
+    return __hgt(m, __hmul(d, __ushort_as_half(0x7000)));
 }
 
 // The most tiles that so many rows of so many experts can have.
@@ -446,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             mbar_init(&b.raw_full[i], 1);
             mbar_init(&b.raw_empty[i], 4 * 2);
         }
-        for (int i = 0; i < kBufD; ++i) {
+        for (int i = 0; i < C::kBufD; ++i) {
             mbar_init(&b.d_full[i], 1);
             mbar_init(&b.d_empty[i], 8);
         }
@@ -520,28 +527,28 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     ring_next(pa, C::kSlotsA);
                     ring_next(pb, C::kRingB);
                 }
-                ring_add(pd, 2, kBufD);
+                ring_add(pd, 2, C::kBufD);
             }
             commit(elected, &b.done[mt]);  // every product issued has completed once this arrives
             mbar_wait(&b.done[mt], 0);
-        } else if (warp == 2) {
-            // -------------------------------------------------------- copies: raw weights, B, the columns' exponents
-            if (lane == 0) {
-                const uint64_t pol = l2_evict_first_policy();
-                RingPos p{0, 0}, pb{0, 0}, ph{0, 0};
-                int64_t issued = 0, issued_b = 0, issued_h = 0;
-                bool ok = true;
-                for (int i = 0; i < my_items && ok; ++i) {
-                    // tiles of outputs after one another, the expert's tiles of rows within
-                    const int64_t it = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
-                    const int e = expert_of(static_cast<int>(it / row_tiles), cum, g.n_experts);
-                    const int tiles = cum[e + 1] - cum[e];
-                    const int64_t at = it - static_cast<int64_t>(cum[e]) * row_tiles;
-                    const int rt = static_cast<int>(at / tiles), tile = static_cast<int>(at - static_cast<int64_t>(rt) * tiles);
+        } else if (lane == 0) {
+            // -------------------------------------------------------- copies: warp 2 B and the columns' exponents, warp 3 the raw weights
+            const uint64_t pol = l2_evict_first_policy();
+            const bool weights = warp == 3;
+            RingPos p{0, 0}, ph{0, 0};
+            int64_t issued = 0, issued_h = 0;
+            bool ok = true;
+            for (int i = 0; i < my_items && ok; ++i) {
+                // tiles of outputs after one another, the expert's tiles of rows within
+                const int64_t it = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+                const int e = expert_of(static_cast<int>(it / row_tiles), cum, g.n_experts);
+                const int tiles = cum[e + 1] - cum[e];
+                const int64_t at = it - static_cast<int64_t>(cum[e]) * row_tiles;
+                const int rt = static_cast<int>(at / tiles), tile = static_cast<int>(at - static_cast<int64_t>(rt) * tiles);
+                if (weights) {
                     const int row = g.offsets[e] + tile * N;
                     sts4(sm32 + C::off_item + 16 * (i % kItems), row, min(N, g.offsets[e + 1] - row), rt, 0);
                     const int y0 = static_cast<int>(e * g.out_dim + static_cast<int64_t>(rt) * (kSwiglu ? 128 : 256));
-                    const int64_t cell0 = static_cast<int64_t>(cum[e] + tile) * nsb;
                     for (int sb = 0; sb < nsb && ok; ++sb) {
                         for (int mt = 0; mt < 2; ++mt) {
                             if (!(ok = wait_one(&b.raw_empty[p.s], p.par ^ 1u, b, g.err))) break;
@@ -551,16 +558,20 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                             ++issued;
                             ring_next(p, C::kRingRaw);
                         }
+                    }
+                } else {
+                    const int64_t cell0 = static_cast<int64_t>(cum[e] + tile) * nsb;
+                    for (int sb = 0; sb < nsb && ok; ++sb) {
                         const uint8_t *from = a.pack + (cell0 + sb) * C::kCellB;
-                        for (int step = 0; step < C::kSteps && ok; ++step) {
-                            if (!(ok = wait_one(&b.b_empty[pb.s], pb.par ^ 1u, b, g.err))) break;
+                        for (int step = 0; step < C::kSteps; ++step) {
+                            if (!(ok = wait_one(&b.b_empty[p.s], p.par ^ 1u, b, g.err))) break;
                             const bool last = step == C::kSteps - 1;
                             const uint32_t bytes = (!C::kOwnMins || !last ? C::kBytesB : 0) + (last ? N * 64 : 0);
-                            mbar_arrive_expect_tx(&b.b_full[pb.s], bytes);
-                            bulk_g2s(sm + C::off_b + pb.s * C::kSlotB, from, bytes, &b.b_full[pb.s]);
+                            mbar_arrive_expect_tx(&b.b_full[p.s], bytes);
+                            bulk_g2s(sm + C::off_b + p.s * C::kSlotB, from, bytes, &b.b_full[p.s]);
                             from += bytes;
-                            ++issued_b;
-                            ring_next(pb, C::kRingB);
+                            ++issued;
+                            ring_next(p, C::kRingB);
                         }
                         if (!ok) break;
                         mbar_arrive_expect_tx(&b.cs_full[ph.s], N * 4);
@@ -569,19 +580,16 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         ring_next(ph, kHdr);
                     }
                 }
-                // copies in flight land before the CTA ends
-                for (int64_t k = max(static_cast<int64_t>(0), issued - C::kRingRaw); k < issued; ++k) {
-                    const RingPos q = ring_pos(k, C::kRingRaw);
-                    mbar_wait(&b.raw_full[q.s], q.par);
-                }
-                for (int64_t k = max(static_cast<int64_t>(0), issued_b - C::kRingB); k < issued_b; ++k) {
-                    const RingPos q = ring_pos(k, C::kRingB);
-                    mbar_wait(&b.b_full[q.s], q.par);
-                }
-                for (int64_t k = max(static_cast<int64_t>(0), issued_h - kHdr); k < issued_h; ++k) {
-                    const RingPos q = ring_pos(k, kHdr);
-                    mbar_wait(&b.cs_full[q.s], q.par);
-                }
+            }
+            // copies in flight land before the CTA ends
+            const int ring = weights ? C::kRingRaw : C::kRingB;
+            for (int64_t k = max(static_cast<int64_t>(0), issued - ring); k < issued; ++k) {
+                const RingPos q = ring_pos(k, ring);
+                mbar_wait(weights ? &b.raw_full[q.s] : &b.b_full[q.s], q.par);
+            }
+            for (int64_t k = max(static_cast<int64_t>(0), issued_h - kHdr); k < issued_h; ++k) {
+                const RingPos q = ring_pos(k, kHdr);
+                mbar_wait(&b.cs_full[q.s], q.par);
             }
         }
     } else if (warp < C::kFirstSum) {
@@ -591,8 +599,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         const int cw = warp - C::kFirstUnpack, wrow = 32 * (cw & 3) + lane, mt = (cw >> 2) & 1, turn = cw >> 3;
         const uint32_t ta0 = tmem + (static_cast<uint32_t>(32 * (cw & 3)) << 16) + C::kColA + mt * C::kSlotsA * C::kWidthA;
         RingPos praw{mt, 0};
-        unsigned apar = 0;
-        const uint32_t ta = ta0 + turn * C::kWidthA;
+        RingPos pa{turn, 0};
         int h = 0, step = turn;  // this group's steps are every other one, over the super-blocks' ends
         bool ok = true;
         for (int64_t k = 0; k < blocks && ok; ++k) {
@@ -602,14 +609,15 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             bool any_wide;
             {
                 const uint4 hd = lds4(raw);
-                any_wide = __any_sync(0xffffffffu, head_of(hd.x).wide);
+                any_wide = __any_sync(0xffffffffu, mins_are_unit(hd.x));
                 sc0 = hd.y & 0x3f3f3f3fu;
                 sc1 = (hd.w & 0x0f0f0f0fu) | ((hd.y >> 2) & 0x30303030u);
             }
 #pragma unroll 1
             for (; step < C::kSteps; step += 2) {
-                if (!(ok = wait_warp(&b.a_empty[mt][turn], apar ^ 1u, b, g.err))) break;
+                if (!(ok = wait_warp(&b.a_empty[mt][pa.s], pa.par ^ 1u, b, g.err))) break;
                 fence_after();
+                const uint32_t ta = ta0 + pa.s * C::kWidthA;
                 if (!C::kOwnMins || step < C::kSteps - 1) {
 #pragma unroll
                     for (int cc = 0; cc < C::kChunks; ++cc) {
@@ -617,9 +625,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         const uint32_t six = (c < 2 ? sc0 : sc1) >> (16 * (c & 1));
                         // (1024 + q) sc - 1024 sc for the low codes, (1024 + 16 q) (sc / 16) - 64 sc for the high ones: one rounding of an exact
                         // small integer
-                        const float s0 = static_cast<float>(six & 63u), s1 = static_cast<float>((six >> 8) & 63u);
-                        const uint32_t mul0 = pack2(s0, s0), add0 = pack2(s0 * -1024.0f, s0 * -1024.0f);
-                        const uint32_t mul1 = pack2(s1 * 0.0625f, s1 * 0.0625f), add1 = pack2(s1 * -64.0f, s1 * -64.0f);
+                        const uint32_t mul0 = hsub2u(__byte_perm(six, 0x64646464u, 0x4040), 0x64006400u), add0 = hmul2u(mul0, 0xe400e400u);
+                        const uint32_t s1 = hsub2u(__byte_perm(six, 0x64646464u, 0x4141), 0x64006400u);
+                        const uint32_t mul1 = hmul2u(s1, 0x2c002c00u), add1 = hmul2u(s1, 0xd400d400u);  // / 16, * -64
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const uint4 q = lds4(raw + 16 + 32 * c + 16 * half);
@@ -652,34 +660,29 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     const uint4 hd = lds4(raw);
                     const Head head = head_of(hd.x);
                     const float ratio = head.wide ? 1.0f : head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
-                    const float by = head.fine ? -0.125f * ratio : 0.0f;
-                    const uint32_t mn0 = hd.z & 0x3f3f3f3fu, mn1 = ((hd.w >> 4) & 0x0f0f0f0fu) | ((hd.z >> 2) & 0x30303030u);
-                    uint32_t o[8];  // 4 words of high pieces, twice; 4 of low ones, twice
+                    const float by = head.fine ? -0.125f * ratio : 0.0f, bh = __half2float(__float2half_rn(by));
+                    const uint32_t rh = pack2(bh, bh), rl = pack2(by - bh, by - bh);
+                    const uint32_t mn[2] = {hd.z & 0x3f3f3f3fu, ((hd.w >> 4) & 0x0f0f0f0fu) | ((hd.z >> 2) & 0x30303030u)};
+                    uint32_t hi[8], lo[8];  // 4 words of high pieces, twice; 4 of low ones, twice
 #pragma unroll
-                    for (int low = 0; low < 2; ++low) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t two = (i < 2 ? mn0 : mn1) >> (16 * (i & 1));
-                            float r0 = by * static_cast<float>(two & 63u), r1 = by * static_cast<float>((two >> 8) & 63u);
-                            if (low) {
-                                const float2 t = unpack2(pack2(r0, r1));
-                                r0 -= t.x;
-                                r1 -= t.y;
-                            }
-                            o[i] = o[4 + i] = pack2(r0, r1);
-                        }
-                        tm_store8(ta + (C::kOwnMins ? 0 : 32 * C::kChunks) + 8 * low, o);
+                    for (int i = 0; i < 4; ++i) {
+                        // two mins as f16 (1024 + m is 0x64 m), times the ratio as it is times activations' scales (moe_pack_kernel)
+                        const uint32_t m = hsub2u(__byte_perm(mn[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u);
+                        hi[i] = hi[4 + i] = hmul2u(m, rh);
+                        lo[i] = lo[4 + i] = hfma2u(m, rl, hfma2u(m, rh, hneg2u(hi[i])));
                     }
+                    tm_store8(ta + (C::kOwnMins ? 0 : 32 * C::kChunks), hi);
+                    tm_store8(ta + (C::kOwnMins ? 0 : 32 * C::kChunks) + 8, lo);
                     sts1(sm32 + C::off_g + 4 * ((h * 2 + mt) * 128 + wrow), __float_as_uint(!head.fine ? NAN : head.wide ? head.dmin : head.d));
                 }
                 tm_store_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&b.a_full[mt][turn]);
+                    mbar_arrive(&b.a_full[mt][pa.s]);
                     if (step == C::kSteps - 1) mbar_arrive(&b.h_full[h]);
                 }
-                apar ^= 1u;
+                ring_add(pa, 2, C::kSlotsA);
             }
             if (!ok) break;
             if (lane == 0) mbar_arrive(&b.raw_empty[praw.s]);
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b.d_empty[pd.s]);
-                    ring_next(pd, kBufD);
+                    ring_next(pd, C::kBufD);
                 }
                 ring_next(ph, kHdr);
             }
