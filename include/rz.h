@@ -665,12 +665,29 @@ rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, 
  *   residual  f32 [n_tokens][out_pad], or NULL: 0
  *   y         f32 [n_tokens][out_pad] output; may be residual; 0 in the columns out_dim .. out_pad.  A token
  *             without experts gets its residual.
- *   workspace rz_moe_down_workspace_bytes bytes, 16-byte aligned; no initialisation
+ *   workspace rz_moe_down_workspace_bytes bytes, 16-byte aligned; no initialisation; may be NULL where that is 0
+ * Sums as in rz_moe_swiglu.
  */
 size_t rz_moe_down_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k, int64_t out_dim, int64_t in_dim);
 rz_status rz_moe_down(const void *w_down, const void *h_q8, const rz_moe_plan *plan, const float *residual, float *y,
                       int64_t out_dim, int64_t out_pad, int64_t in_dim, void *workspace, size_t ws_bytes,
                       rz_stream stream);
+
+/*
+ * rz_moe_ffn -- rz_moe_route, rz_moe_swiglu (its Q8_1 output) and rz_moe_down in one call, the
+ * same results:  out = residual + the experts' FFNs of x, weighted.
+ *   x_q8      Q8_1 of n_tokens rows of hidden_pad (rz_residual_rmsnorm's)
+ *   w_gate, w_up Q4_K [n_experts][inter][hidden_pad]   w_down Q4_K [n_experts][hidden][inter]
+ *   residual, out f32 [n_tokens][hidden_pad]; residual may be NULL or out; the padding of out is 0
+ *   plan      receives the routing; hidden_pad and inter multiples of 256
+ *   workspace rz_moe_ffn_workspace_bytes bytes, 16-byte aligned; no initialisation
+ */
+size_t rz_moe_ffn_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k, int64_t hidden, int64_t hidden_pad,
+                                  int64_t inter);
+rz_status rz_moe_ffn(const float *logits, int64_t ld, const int32_t *row_seq, const void *x_q8, const void *w_gate,
+                     const void *w_up, const void *w_down, const float *residual, float *out, const rz_moe_plan *plan,
+                     int32_t renormalise, float scale, int64_t hidden, int64_t hidden_pad, int64_t inter, void *workspace,
+                     size_t ws_bytes, rz_stream stream);
 
 /*
  * rz_check_device_error -- synchronise `stream`, read the device error word of the

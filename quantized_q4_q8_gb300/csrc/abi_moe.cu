@@ -1,6 +1,7 @@
 // abi_moe.cu -- the extern "C" boundary of an FFN of experts: argument checks of its
 // entry points (see abi.cu for the conventions).  Every check runs on the host before any
 // launch.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -131,7 +132,14 @@ int64_t pack_bytes(int64_t n_pairs, int n_experts, int64_t in_dim)
 int64_t down_workspace_bytes(int64_t n_tokens, int n_experts, int top_k, int64_t out_dim, int64_t in_dim)
 {
     const int64_t pairs = n_tokens * top_k;
+    if (moe_columns(pairs, n_experts) == 0) return 0;
     return align256(pairs * out_dim * 4) + pack_bytes(pairs, n_experts, in_dim);
+}
+
+cudaError_t run_swiglu(const MoeGemvArgs &a, void *workspace, cudaStream_t s)
+{
+    const int columns = moe_columns(a.n_pairs, a.n_experts);
+    return columns ? launch_moe_gemm_tc(a, columns, workspace, s) : launch_moe_swiglu(a, s);
 }
 
 cudaError_t run_down(const void *w_down, const void *h_q8, const rz_moe_plan *p, const float *residual, float *y, int64_t out_dim,
@@ -147,6 +155,7 @@ cudaError_t run_down(const void *w_down, const void *h_q8, const rz_moe_plan *p,
     a.y = static_cast<float *>(workspace);
     MoeCombineArgs c{};
     c.o = a.y;
+    c.experts = p->experts;
     c.places = p->places;
     c.weights = p->weights;
     c.residual = residual;
@@ -156,7 +165,9 @@ cudaError_t run_down(const void *w_down, const void *h_q8, const rz_moe_plan *p,
     c.top_k = p->top_k;
     c.n_pairs = a.n_pairs;
     c.err = a.err;
-    const cudaError_t e = launch_moe_product(a, static_cast<uint8_t *>(workspace) + align256(a.n_pairs * out_dim * 4), s);
+    const int columns = moe_columns(a.n_pairs, a.n_experts);
+    if (columns == 0) return launch_moe_down_tokens(a, c, p->n_tokens, s);
+    const cudaError_t e = launch_moe_gemm_tc(a, columns, static_cast<uint8_t *>(workspace) + align256(a.n_pairs * out_dim * 4), s);
     return e != cudaSuccess ? e : launch_moe_combine(c, p->n_tokens, s);
 }
 
@@ -281,7 +292,7 @@ rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, 
     RZ_TRY(ensure_device());
     MoeGemvArgs a{};
     swiglu_args(a, w_gate, w_up, x_q8, plan, inter, in_dim, h, h_q8);
-    return launched(fn, launch_moe_product(a, workspace, static_cast<cudaStream_t>(stream)));
+    return launched(fn, run_swiglu(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 size_t rz_moe_down_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k, int64_t out_dim, int64_t in_dim)
@@ -305,6 +316,55 @@ rz_status rz_moe_down(const void *w_down, const void *h_q8, const rz_moe_plan *p
     RZ_TRY(check_workspace(fn, workspace, ws_bytes, down_workspace_bytes(plan->n_tokens, plan->n_experts, plan->top_k, out_dim, in_dim)));
     RZ_TRY(ensure_device());
     return launched(fn, run_down(w_down, h_q8, plan, residual, y, out_dim, out_pad, in_dim, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+// Q8_1 of h, then what routing and the products need, one after another
+static size_t ffn_h_bytes(int64_t n_tokens, int top_k, int64_t inter) { return align256(RZ_Q8_1_BYTES(n_tokens * top_k, inter)); }
+static size_t ffn_workspace_bytes(int64_t n_tokens, int n_experts, int top_k, int64_t hidden, int64_t hidden_pad, int64_t inter)
+{
+    const int64_t parts[] = {moe_route_workspace_bytes(n_tokens, n_experts), pack_bytes(n_tokens * top_k, n_experts, hidden_pad),
+                             down_workspace_bytes(n_tokens, n_experts, top_k, hidden, inter)};
+    return ffn_h_bytes(n_tokens, top_k, inter) + align256(std::max({parts[0], parts[1], parts[2]}));
+}
+
+static rz_status check_ffn_dims(const char *fn, int64_t hidden, int64_t hidden_pad, int64_t inter)
+{
+    RZ_TRY(check_out_dim(fn, "hidden", hidden));
+    RZ_TRY(check_in_dim(fn, hidden_pad));
+    if (hidden_pad < hidden) return fail(RZ_ERR_SHAPE, "%s: hidden_pad=%lld < hidden=%lld", fn, (long long)hidden_pad, (long long)hidden);
+    return check_in_dim(fn, inter);
+}
+
+size_t rz_moe_ffn_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k, int64_t hidden, int64_t hidden_pad, int64_t inter)
+{
+    const char *fn = "rz_moe_ffn_workspace_bytes";
+    record_error(RZ_OK, "");
+    if (check_counts(fn, n_tokens, n_experts, top_k) != RZ_OK || check_ffn_dims(fn, hidden, hidden_pad, inter) != RZ_OK) return 0;
+    return ffn_workspace_bytes(n_tokens, n_experts, top_k, hidden, hidden_pad, inter);
+}
+
+rz_status rz_moe_ffn(const float *logits, int64_t ld, const int32_t *row_seq, const void *x_q8, const void *w_gate, const void *w_up,
+                     const void *w_down, const float *residual, float *out, const rz_moe_plan *plan, int32_t renormalise, float scale,
+                     int64_t hidden, int64_t hidden_pad, int64_t inter, void *workspace, size_t ws_bytes, rz_stream stream)
+{
+    const char *fn = "rz_moe_ffn";
+    record_error(RZ_OK, "");
+    RZ_TRY(check_route(fn, logits, ld, row_seq, plan, scale));
+    if (!x_q8 || !w_gate || !w_up) return fail(RZ_ERR_INVALID_ARG, "%s: null pointer", fn);
+    RZ_TRY(check_ffn_dims(fn, hidden, hidden_pad, inter));
+    RZ_TRY(check_down(fn, w_down, residual, out, hidden, hidden_pad, inter));
+    const void *bufs[] = {x_q8, w_gate, w_up};
+    for (const void *p : bufs)
+        if (!aligned(p, 16)) return fail(RZ_ERR_ALIGN, "%s: buffers must be 16-byte aligned", fn);
+    RZ_TRY(check_workspace(fn, workspace, ws_bytes, ffn_workspace_bytes(plan->n_tokens, plan->n_experts, plan->top_k, hidden, hidden_pad, inter)));
+    RZ_TRY(ensure_device());
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t *rest = static_cast<uint8_t *>(workspace) + ffn_h_bytes(plan->n_tokens, plan->top_k, inter);
+    RZ_TRY(launched(fn, run_route(logits, ld, row_seq, plan, renormalise != 0, scale, rest, s)));
+    MoeGemvArgs a{};
+    swiglu_args(a, w_gate, w_up, x_q8, plan, inter, hidden_pad, nullptr, workspace);
+    RZ_TRY(launched(fn, run_swiglu(a, rest, s)));
+    return launched(fn, run_down(w_down, workspace, plan, residual, out, hidden, hidden_pad, inter, rest, s));
 }
 
 }  // extern "C"

@@ -745,19 +745,28 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                 w.m = t.y;
                 w.rt = t.z;
             }
-            // eight columns in straight code, then the others move up: 64 in straight code are more than the instruction caches hold
             const int64_t o = static_cast<int64_t>(w.rt) * (kSwiglu ? 128 : 256) + wrow;
-            const bool in = o < g.out_dim, in2 = o + 128 < g.out_dim;
+            const bool in = o < g.out_dim;
+            const int m = w.m - col0;
             int64_t to = static_cast<int64_t>(w.row + col0) * g.out_dim + o;
-#pragma unroll 1
-            for (int i0 = 0; i0 < C::kHalf && col0 + i0 < w.m; i0 += 8) {
+            if constexpr (kSwiglu) {
+                // in place first: half of the registers are free for what follows
 #pragma unroll
-                for (int i = 0; i < 8; ++i, to += g.out_dim) {
-                    if (col0 + i0 + i >= w.m) break;
-                    if constexpr (kSwiglu) {
-                        const float v = in ? __fdividef(sum[0][i], 1.0f + expf(-sum[0][i])) * sum[1][i] : 0.0f;
-                        if (g.y && in) g.y[to] = v;
-                        if (g.yq && in) {  // out_dim is a multiple of 32: all of the warp or none
+                for (int i = 0; i < C::kHalf; ++i) sum[0][i] = in ? __fdividef(sum[0][i], 1.0f + expf(-sum[0][i])) * sum[1][i] : 0.0f;
+                if (g.y && in) {
+                    float *y = g.y + to;
+#pragma unroll
+                    for (int i = 0; i < C::kHalf; ++i, y += g.out_dim)
+                        if (i < m) *y = sum[0][i];
+                }
+                if (g.yq && in) {  // out_dim is a multiple of 32: all of the warp or none
+                    // eight columns in straight code, then the others move up
+#pragma unroll 1
+                    for (int i0 = 0; i0 < C::kHalf && i0 < m; i0 += 8) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i, to += g.out_dim) {
+                            if (i0 + i >= m) break;
+                            const float v = sum[0][i];
                             const uint32_t key = isnan(v) ? 0u : __float_as_uint(fabsf(v)) + 1u;
                             const uint32_t top = __reduce_max_sync(0xffffffffu, key);
                             const float d = top ? __fdiv_rn(__uint_as_float(top - 1u), 127.0f) : NAN;
@@ -769,15 +778,19 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                                 g.ys[to / 32] = __fmul_rn(d, static_cast<float>(total));
                             }
                         }
-                    } else {
-                        if (in) g.y[to] = sum[0][i];
-                        if (in2) g.y[to + 128] = sum[1][i];
+#pragma unroll
+                        for (int i = 0; i + 8 < C::kHalf; ++i) sum[0][i] = sum[0][i + 8];
                     }
                 }
+            } else {
 #pragma unroll
-                for (int i = 0; i + 8 < C::kHalf; ++i) {
-                    sum[0][i] = sum[0][i + 8];
-                    sum[1][i] = sum[1][i + 8];
+                for (int mt = 0; mt < 2; ++mt) {
+                    float *y = g.y + to + 128 * mt;
+                    if (o + 128 * mt < g.out_dim) {
+#pragma unroll
+                        for (int i = 0; i < C::kHalf; ++i, y += g.out_dim)
+                            if (i < m) *y = sum[mt][i];
+                    }
                 }
             }
         }
@@ -868,16 +881,15 @@ cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &g, int columns, void *workspac
     }
 }
 
+// By the rows that an expert has on average (us with integer dots, and in tiles of 16, 32 and 128 rows; gate and up):
+//   2 of 8 experts of 4096 > 14336:  1 row 74, 87, 94;  2 rows 126, 115, 128;  12 rows 632, 168, 152, 365;  40 rows 2081, 378, 270, 371;
+//                                    80 rows -, 693, 447, 453;  128 rows -, 1066, 635, 515
+//   8 of 64 experts of 2048 > 1024:  0.5 rows 21, 33, 36;  2 rows 55, 46, 51;  12 rows 239, 67, 64, 149;  96 rows -, 256, 171, 191;
+//                                    128 rows -, 334, 221, 217
 int moe_columns(int64_t n_pairs, int n_experts)
 {
     const int64_t rows = n_pairs / n_experts;
-    return rows <= 2 ? 0 : rows <= 12 ? 16 : rows <= 64 ? 32 : 128;
-}
-
-cudaError_t launch_moe_product(const MoeGemvArgs &a, void *workspace, cudaStream_t s)
-{
-    const int columns = moe_columns(a.n_pairs, a.n_experts);
-    return columns ? launch_moe_gemm_tc(a, columns, workspace, s) : launch_moe_gemv(a, s);
+    return rows < 2 ? 0 : rows <= 10 ? 16 : rows < 96 ? 32 : 128;
 }
 
 }  // namespace rz

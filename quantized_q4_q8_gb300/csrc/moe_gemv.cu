@@ -47,14 +47,69 @@ __device__ __forceinline__ int2 find_expert(const MoeGemvArgs &a, int r, int2 *f
     return *found;
 }
 
-template <bool kSwiglu>
-__global__ void __launch_bounds__(kThreads, 2) moe_gemv_kernel(const MoeGemvArgs a)
+// acc[k][t] += the lane's share of weight row k times row src[t] of x, for m rows of x.
+template <int kT>
+__device__ __forceinline__ void dot_rows(const MoeGemvArgs &a, const uint8_t *const (&wr)[kRows], const int (&src)[kT], int m, int sub, int c,
+                                         const LaneConst &L, float (&acc)[kRows][kT])
+{
+    const int nsb = a.in_dim / 256, nb = a.in_dim / 32;
+#pragma unroll 1
+    for (int sb = sub; sb < nsb; sb += 8) {
+        Weights64 w[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const uint8_t *p = wr[k] + sb * 144;
+            w[k].h = load_stream(p);
+            w[k].a = load_stream(p + 16 + 32 * c);
+            w[k].b = load_stream(p + 32 + 32 * c);
+        }
+        float ds0[kRows], ds1[kRows], dm0[kRows], dm1[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const float d = h2f(static_cast<uint16_t>(static_cast<uint32_t>(w[k].h.x) & 0xffffu));
+            const float dmin = h2f(static_cast<uint16_t>(static_cast<uint32_t>(w[k].h.x) >> 16));
+            const uint32_t A = static_cast<uint32_t>(w[k].h.y) >> L.sh, B = static_cast<uint32_t>(w[k].h.z) >> L.sh,
+                           C = static_cast<uint32_t>(w[k].h.w) >> L.sh;
+            const uint32_t scp = (A & L.mask_lo) | (C & L.mask_c) | ((A >> 2) & L.mask_hi);
+            const uint32_t mnp = (B & L.mask_lo) | ((C >> 4) & L.mask_c) | ((B >> 2) & L.mask_hi);
+            ds0[k] = d * static_cast<float>(scp & 0xffu);
+            ds1[k] = d * static_cast<float>((scp >> 8) & 0xffu);
+            dm0[k] = dmin * static_cast<float>(mnp & 0xffu);
+            dm1[k] = dmin * static_cast<float>((mnp >> 8) & 0xffu);
+        }
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            if (t >= m) break;
+            const int64_t j = static_cast<int64_t>(src[t]) * nb + sb * 8 + 2 * c;
+            const int4 *xp = reinterpret_cast<const int4 *>(a.xq + j * 32);
+            const int4 x0 = __ldg(xp), x1 = __ldg(xp + 1), x2 = __ldg(xp + 2), x3 = __ldg(xp + 3);
+            const float2 d8 = __ldg(reinterpret_cast<const float2 *>(a.xd + j)), s8 = __ldg(reinterpret_cast<const float2 *>(a.xs + j));
+            const int xa[16] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w, x2.x, x2.y, x2.z, x2.w, x3.x, x3.y, x3.z, x3.w};
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                const int q[8] = {w[k].a.x, w[k].a.y, w[k].a.z, w[k].a.w, w[k].b.x, w[k].b.y, w[k].b.z, w[k].b.w};
+                int i0 = 0, i1 = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    i0 = __dp4a(q[i] & 0x0f0f0f0f, xa[i], i0);
+                    i1 = __dp4a((q[i] >> 4) & 0x0f0f0f0f, xa[8 + i], i1);
+                }
+                float v = fmaf(ds0[k], d8.x * static_cast<float>(i0), acc[k][t]);
+                v = fmaf(ds1[k], d8.y * static_cast<float>(i1), v);
+                v = fmaf(-dm0[k], s8.x, v);
+                acc[k][t] = fmaf(-dm1[k], s8.y, v);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 2) moe_swiglu_kernel(const MoeGemvArgs a)
 {
     __shared__ int2 found;
     __shared__ float out[kTokens][kTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c = lane & 3, sub = lane >> 2;
-    const int nsb = a.in_dim / 256, nb = a.in_dim / 32;
+    const int nsb = a.in_dim / 256;
     const LaneConst L = lane_const(c);
     pdl_launch_dependents();
     pdl_wait();
@@ -82,76 +137,25 @@ __global__ void __launch_bounds__(kThreads, 2) moe_gemv_kernel(const MoeGemvArgs
         }
         const int64_t wbase = static_cast<int64_t>(ex.x) * a.out_dim;
 #pragma unroll 1
-        for (int pass = 0; pass < (kSwiglu ? 2 : 1); ++pass) {
-            // a warp's outputs 4 warp .. + 3; with gate and up two of them at once
+        for (int pass = 0; pass < 2; ++pass) {
+            // a warp's outputs 4 warp .. + 3, gate and up of two of them at once
             const int o0 = 4 * warp + 2 * pass;
             const uint8_t *wr[kRows];
 #pragma unroll
             for (int k = 0; k < kRows; ++k) {
-                const int64_t o = min(static_cast<int64_t>(blockIdx.x) * kTile + o0 + (kSwiglu ? k >> 1 : k), a.out_dim - 1);
-                wr[k] = (kSwiglu && (k & 1) ? a.w2 : a.w1) + (wbase + o) * nsb * 144;
+                const int64_t o = min(static_cast<int64_t>(blockIdx.x) * kTile + o0 + (k >> 1), a.out_dim - 1);
+                wr[k] = (k & 1 ? a.w2 : a.w1) + (wbase + o) * nsb * 144;
             }
             float acc[kRows][kTokens] = {};
-#pragma unroll 1
-            for (int sb = sub; sb < nsb; sb += 8) {
-                Weights64 w[kRows];
-#pragma unroll
-                for (int k = 0; k < kRows; ++k) {
-                    const uint8_t *p = wr[k] + sb * 144;
-                    w[k].h = load_stream(p);
-                    w[k].a = load_stream(p + 16 + 32 * c);
-                    w[k].b = load_stream(p + 32 + 32 * c);
-                }
-                float ds0[kRows], ds1[kRows], dm0[kRows], dm1[kRows];
-#pragma unroll
-                for (int k = 0; k < kRows; ++k) {
-                    const float d = h2f(static_cast<uint16_t>(static_cast<uint32_t>(w[k].h.x) & 0xffffu));
-                    const float dmin = h2f(static_cast<uint16_t>(static_cast<uint32_t>(w[k].h.x) >> 16));
-                    const uint32_t A = static_cast<uint32_t>(w[k].h.y) >> L.sh, B = static_cast<uint32_t>(w[k].h.z) >> L.sh,
-                                   C = static_cast<uint32_t>(w[k].h.w) >> L.sh;
-                    const uint32_t scp = (A & L.mask_lo) | (C & L.mask_c) | ((A >> 2) & L.mask_hi);
-                    const uint32_t mnp = (B & L.mask_lo) | ((C >> 4) & L.mask_c) | ((B >> 2) & L.mask_hi);
-                    ds0[k] = d * static_cast<float>(scp & 0xffu);
-                    ds1[k] = d * static_cast<float>((scp >> 8) & 0xffu);
-                    dm0[k] = dmin * static_cast<float>(mnp & 0xffu);
-                    dm1[k] = dmin * static_cast<float>((mnp >> 8) & 0xffu);
-                }
-#pragma unroll
-                for (int t = 0; t < kTokens; ++t) {
-                    if (t >= m) break;
-                    const int64_t j = static_cast<int64_t>(src[t]) * nb + sb * 8 + 2 * c;
-                    const int4 *xp = reinterpret_cast<const int4 *>(a.xq + j * 32);
-                    const int4 x0 = __ldg(xp), x1 = __ldg(xp + 1), x2 = __ldg(xp + 2), x3 = __ldg(xp + 3);
-                    const float2 d8 = __ldg(reinterpret_cast<const float2 *>(a.xd + j)), s8 = __ldg(reinterpret_cast<const float2 *>(a.xs + j));
-                    const int xa[16] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w, x2.x, x2.y, x2.z, x2.w, x3.x, x3.y, x3.z, x3.w};
-#pragma unroll
-                    for (int k = 0; k < kRows; ++k) {
-                        const int q[8] = {w[k].a.x, w[k].a.y, w[k].a.z, w[k].a.w, w[k].b.x, w[k].b.y, w[k].b.z, w[k].b.w};
-                        int i0 = 0, i1 = 0;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            i0 = __dp4a(q[i] & 0x0f0f0f0f, xa[i], i0);
-                            i1 = __dp4a((q[i] >> 4) & 0x0f0f0f0f, xa[8 + i], i1);
-                        }
-                        float v = fmaf(ds0[k], d8.x * static_cast<float>(i0), acc[k][t]);
-                        v = fmaf(ds1[k], d8.y * static_cast<float>(i1), v);
-                        v = fmaf(-dm0[k], s8.x, v);
-                        acc[k][t] = fmaf(-dm1[k], s8.y, v);
-                    }
-                }
-            }
+            dot_rows(a, wr, src, m, sub, c, L, acc);
 #pragma unroll
             for (int t = 0; t < kTokens; ++t) {
                 if (t >= m) break;
 #pragma unroll
                 for (int k = 0; k < kRows; ++k) acc[k][t] = warp_sum(acc[k][t]);
-                if (kSwiglu) {
-                    if (lane < 2) {
-                        const float g = lane ? acc[2][t] : acc[0][t], u = lane ? acc[3][t] : acc[1][t];
-                        out[t][o0 + lane] = g / (1.0f + expf(-g)) * u;
-                    }
-                } else if (lane < 4) {
-                    out[t][o0 + lane] = lane == 0 ? acc[0][t] : lane == 1 ? acc[1][t] : lane == 2 ? acc[2][t] : acc[3][t];
+                if (lane < 2) {
+                    const float g = lane ? acc[2][t] : acc[0][t], u = lane ? acc[3][t] : acc[1][t];
+                    out[t][o0 + lane] = g / (1.0f + expf(-g)) * u;
                 }
             }
         }
@@ -172,6 +176,51 @@ __global__ void __launch_bounds__(kThreads, 2) moe_gemv_kernel(const MoeGemvArgs
         }
         __syncthreads();
     }
+}
+
+// y[t] = residual[t] + sum_j w_j D_e h_r in one launch, for few rows of an expert: a CTA has a token and 4 * quads outputs,
+// a warp 4 outputs of one of its choices at a time.  What two tokens share comes from L2 again.
+__global__ void __launch_bounds__(kThreads, 2) moe_down_tokens_kernel(const MoeGemvArgs a, const MoeCombineArgs b, int quads)
+{
+    __shared__ float out[kMoeMaxTopK][kTile];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c = lane & 3, sub = lane >> 2;
+    const int nsb = a.in_dim / 256;
+    const LaneConst L = lane_const(c);
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t t = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
+    if (t * a.top_k >= a.n_pairs) return;
+    const int64_t o0 = static_cast<int64_t>(blockIdx.x) * 4 * quads;
+    for (int u = warp; u < a.top_k * quads; u += kThreads / 32) {
+        const int j = u / quads, q = u - j * quads;
+        const int e = b.experts[t * a.top_k + j], place = b.places[t * a.top_k + j];
+        const bool bad = e >= a.n_experts || place >= a.n_pairs || (e < 0) != (place < 0);
+        if (bad && lane == 0) set_error(a.err, DEV_BAD_LENGTH);
+        if (bad || e < 0) continue;
+        const uint8_t *wr[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) wr[k] = a.w1 + (e * a.out_dim + min(o0 + 4 * q + k, a.out_dim - 1)) * nsb * 144;
+        const int src[1] = {place};
+        float acc[kRows][1] = {};
+        dot_rows(a, wr, src, 1, sub, c, L, acc);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) acc[k][0] = warp_sum(acc[k][0]);
+        if (lane < 4) out[j][4 * q + lane] = lane == 0 ? acc[0][0] : lane == 1 ? acc[1][0] : lane == 2 ? acc[2][0] : acc[3][0];
+    }
+    __syncthreads();
+    const int64_t col = o0 + tid;
+    if (tid < 4 * quads && col < a.out_dim) {
+        float v = b.residual ? b.residual[t * b.out_pad + col] : 0.0f;
+        for (int j = 0; j < a.top_k; ++j) {
+            const int e = b.experts[t * a.top_k + j], place = b.places[t * a.top_k + j];
+            if (e >= 0 && e < a.n_experts && place >= 0 && place < a.n_pairs) v = fmaf(b.weights[t * a.top_k + j], out[j][tid], v);
+        }
+        b.y[t * b.out_pad + col] = v;
+    }
+    // zeros behind out_dim, by the last CTA of the token
+    if (blockIdx.x == gridDim.x - 1)
+        for (int64_t z = a.out_dim + tid; z < b.out_pad; z += kThreads) b.y[t * b.out_pad + z] = 0.0f;
 }
 
 // y[t] = residual[t] + sum_j w_j o[place_j], zeros behind out_dim; a thread has kVec columns
@@ -233,10 +282,26 @@ cudaError_t launch(K kernel, dim3 grid, const A &a, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_moe_gemv(const MoeGemvArgs &a, cudaStream_t s)
+cudaError_t launch_moe_swiglu(const MoeGemvArgs &a, cudaStream_t s)
 {
     const dim3 grid(static_cast<unsigned>((a.out_dim + kTile - 1) / kTile), static_cast<unsigned>(std::min<int64_t>(a.n_pairs, 65535)));
-    return a.w2 ? launch(moe_gemv_kernel<true>, grid, a, s) : launch(moe_gemv_kernel<false>, grid, a, s);
+    return launch(moe_swiglu_kernel, grid, a, s);
+}
+
+cudaError_t launch_moe_down_tokens(const MoeGemvArgs &a, const MoeCombineArgs &b, int64_t n_tokens, cudaStream_t s)
+{
+    const int quads = a.top_k >= 8 ? 1 : 8 / a.top_k;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.out_dim + 4 * quads - 1) / (4 * quads)), static_cast<unsigned>(std::min<int64_t>(n_tokens, 65535)),
+                       static_cast<unsigned>((n_tokens + 65534) / 65535));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_use_pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, moe_down_tokens_kernel, a, b, quads);
 }
 
 cudaError_t launch_moe_combine(const MoeCombineArgs &a, int64_t n_tokens, cudaStream_t s)

@@ -337,8 +337,8 @@ struct MoeRouteArgs {
 int64_t moe_route_workspace_bytes(int64_t n_tokens, int n_experts);
 cudaError_t launch_moe_route(MoeRouteArgs a, cudaStream_t s);
 
-// Products grouped by expert (moe_gemv.cu): rows r of expert e, offsets[e] <= r < offsets[e + 1], read row
-// rows[r] / top_k of x (row r where rows is nullptr).  w2 != nullptr: silu(w1 x) * (w2 x).
+// Products grouped by expert: rows r of expert e, offsets[e] <= r < offsets[e + 1], read row rows[r] / top_k of x (row r where
+// rows is nullptr).  w2 != nullptr: silu(w1 x) * (w2 x).
 struct MoeGemvArgs {
     const uint8_t *w1, *w2;  // [n_experts][out_dim][in_dim]
     const int8_t *xq;
@@ -351,24 +351,24 @@ struct MoeGemvArgs {
     int in_dim, n_experts, top_k, n_pairs;
     unsigned *err;
 };
-cudaError_t launch_moe_gemv(const MoeGemvArgs &a, cudaStream_t s);
+cudaError_t launch_moe_swiglu(const MoeGemvArgs &a, cudaStream_t s);  // with integer dots (moe_gemv.cu), w2 given
 
 // The same on the tensor cores (moe_gemm_tc.cu), in tiles of `columns` rows: 16, 32 or 128.
 cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &a, int columns, void *workspace, cudaStream_t s);
 int64_t moe_pack_bytes(int columns, int64_t n_pairs, int n_experts, int64_t in_dim);  // of its workspace
 
-// Whichever of the two the sizes call for.
-int moe_columns(int64_t n_pairs, int n_experts);
-cudaError_t launch_moe_product(const MoeGemvArgs &a, void *workspace, cudaStream_t s);
+int moe_columns(int64_t n_pairs, int n_experts);  // of the tiles for so many rows of so many experts; 0: integer dots
 
 struct MoeCombineArgs {
     const float *o;  // [n_pairs][out_dim]
-    const int32_t *places;
+    const int32_t *experts, *places;
     const float *weights, *residual;
     float *y;        // [n_tokens][out_pad]
     int out_dim, out_pad, top_k, n_pairs;
     unsigned *err;
 };
+// Both in one launch, with integer dots (a.y is not used).
+cudaError_t launch_moe_down_tokens(const MoeGemvArgs &a, const MoeCombineArgs &b, int64_t n_tokens, cudaStream_t s);
 cudaError_t launch_moe_combine(const MoeCombineArgs &a, int64_t n_tokens, cudaStream_t s);
 
 }  // namespace rz

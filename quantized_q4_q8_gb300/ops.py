@@ -24,6 +24,7 @@ __all__ = [
     "decode_layer_paged_workspace_bytes", "decode_layer_paged",
     "rz_residual_rmsnorm", "residual_rmsnorm", "MoePlan", "moe_route_workspace_bytes", "rz_moe_route", "moe_route",
     "moe_swiglu_workspace_bytes", "rz_moe_swiglu", "moe_swiglu", "moe_down_workspace_bytes", "rz_moe_down", "moe_down",
+    "moe_ffn_workspace_bytes", "rz_moe_ffn", "moe_ffn",
 ]
 
 
@@ -914,4 +915,33 @@ def moe_down(w_down, h_q8, plan: MoePlan, out_dim: int, in_dim: int, residual=No
          _vector(h_q8, torch.uint8, q8_1_size(plan.n_tokens * plan.top_k, in_dim), dev, "h_q8"), _plan_on(plan, dev),
          None if residual is None else _matrix(residual, f32, plan.n_tokens, out_pad, dev, "residual"),
          _matrix(out, f32, plan.n_tokens, out_pad, dev, "out"), out_dim, out_pad, in_dim, at, size, _stream_on(stream, dev))
+    return out
+
+
+def moe_ffn_workspace_bytes(n_tokens: int, n_experts: int, top_k: int, hidden: int, hidden_pad: int, inter: int) -> int:
+    return int(load().rz_moe_ffn_workspace_bytes(n_tokens, n_experts, top_k, hidden, hidden_pad, inter))
+
+
+def rz_moe_ffn(logits, ld, row_seq, x_q8, w_gate, w_up, w_down, residual, out, plan, renormalise, scale, hidden, hidden_pad, inter, ws,
+               ws_bytes, stream=None):
+    return call("rz_moe_ffn", _ptr(logits), ld, _ptr(row_seq), _ptr(x_q8), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(residual), _ptr(out),
+                plan.ref, renormalise, scale, hidden, hidden_pad, inter, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_ffn(logits, x_q8, w_gate, w_up, w_down, plan: MoePlan, hidden: int, hidden_pad: int, inter: int, renormalise: bool = True,
+            scale: float = 1.0, row_seq=None, residual=None, out=None, ws=None, stream=None):
+    """moe_route, moe_swiglu and moe_down in one call (see rz.h): f32 [n_tokens, hidden_pad].  out may be residual."""
+    import torch
+    f32, dev, T, E = torch.float32, torch.cuda.current_device(), plan.n_tokens, plan.n_experts
+    if _on_device(logits, f32, 2, dev, "logits").shape[0] != T:
+        raise ValueError("logits must have a row for each token of the plan")
+    if out is None:
+        out = _new((T, hidden_pad), f32, dev, stream)
+    at, size, ws = _scratch(ws, moe_ffn_workspace_bytes(T, E, plan.top_k, hidden, hidden_pad, inter), dev, stream)
+    call("rz_moe_ffn", logits.data_ptr(), _row_ld(logits, E, "logits"),
+         None if row_seq is None else _vector(row_seq, torch.int32, T, dev, "row_seq", more=True),
+         _vector(x_q8, torch.uint8, q8_1_size(T, hidden_pad), dev, "x_q8"), _expert_weights(w_gate, E, inter, hidden_pad, dev, "w_gate"),
+         _expert_weights(w_up, E, inter, hidden_pad, dev, "w_up"), _expert_weights(w_down, E, hidden, inter, dev, "w_down"),
+         None if residual is None else _matrix(residual, f32, T, hidden_pad, dev, "residual"), _matrix(out, f32, T, hidden_pad, dev, "out"),
+         _plan_on(plan, dev), 1 if renormalise else 0, scale, hidden, hidden_pad, inter, at, size, _stream_on(stream, dev))
     return out

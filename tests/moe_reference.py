@@ -5,7 +5,7 @@ import numpy as np
 def q8_quantize(y, multiplied=False):
     """y f32 [m, n] -> int8 codes, f32 scales, f32 scale * sum: the format's definition, step by step in f32.  multiplied: the
     scale is max|y| * (1 / 127), as rz_residual_rmsnorm has it."""
-    b = y.astype(np.float32).reshape(y.shape[0], -1, 32)
+    b = y.astype(np.float32).reshape(y.shape[0], y.shape[1] // 32, 32)
     top = np.abs(b).max(-1)
     d = top * (np.float32(1) / np.float32(127)) if multiplied else top / np.float32(127)
     with np.errstate(divide="ignore", invalid="ignore"):

@@ -214,6 +214,8 @@ def within(got, ref, tol, what):
 SHAPES = [  # T, E, k, inter, in
     (1, 1, 1, 1, 256), (1, 8, 3, 33, 256), (2, 4, 4, 32, 512), (5, 3, 2, 100, 768), (9, 2, 2, 160, 2304), (17, 64, 8, 64, 256),
     (33, 4, 1, 129, 512), (40, 3, 3, 256, 1024), (130, 8, 2, 130, 256), (150, 2, 2, 320, 512), (300, 16, 4, 96, 256), (270, 1, 1, 200, 768),
+    (64, 32, 2, 640, 256), (240, 8, 1, 2600, 256), (820, 8, 1, 2560, 512),  # more tiles than SMs, for each of the tiles' sizes
+    (7, 8, 2, 65, 1280), (6, 16, 1, 40, 2560), (9, 256, 32, 32, 256),
 ]
 
 
@@ -320,8 +322,8 @@ def test_values_that_are_no_numbers_stay_in_their_rows(rz):
 
 def test_bad_plans_are_reported(rz):
     rng = np.random.default_rng(2)
-    for T in (4, 200):
-        E, k, out_dim, in_dim = 4, 2, 64, 256
+    for T, E in ((3, 8), (4, 4), (200, 4)):
+        k, out_dim, in_dim = 2, 64, 256
         plan, _ = make_plan(rz, rng, T, E, k, idle=0.0)
         w, x = dev(q4k(rng, E, out_dim, in_dim=in_dim)), dev(R.q8_buffer(*activations(rng, T, in_dim)))
         h8 = dev(R.q8_buffer(*activations(rng, T * k, in_dim)))
@@ -342,10 +344,11 @@ def test_bad_plans_are_reported(rz):
         assert st == 7 and code == 0x203
         plan.places[0] = at
         off = plan.offsets.clone()
-        plan.offsets[-1] = T * k + 5  # the last expert's rows end outside
+        last = int((off[1:] > off[:-1]).nonzero()[-1])
+        plan.offsets[last + 1:] = T * k + 5  # the last rows end outside
         out = torch.full_like(ref, 3.0)
         rz.moe_swiglu(w, w, x, plan, out_dim, in_dim, out=out)
-        first = int(off[-2])
+        first = int(off[last])
         assert torch.equal(out[:first], ref[:first]) and bool((out[first:] == 3.0).all())
         plan.offsets.copy_(off)
         rz.check_device_error()
@@ -414,6 +417,36 @@ def test_block(rz, T, E, k, n, n_pad, inter):
     ref, tol = b.reference(x, delta, b.plan, host(b.h8))
     within(y[:, :n], ref, tol, "y")
     assert np.all(y[:, n:] == 0)
+
+
+@pytest.mark.parametrize("T,E,k,n,n_pad,inter", [(1, 8, 2, 200, 256, 256), (7, 4, 3, 512, 512, 512), (130, 16, 4, 900, 1024, 256), (160, 4, 2, 256, 256, 768),
+                                                 (300, 3, 1, 130, 256, 256)])
+def test_ffn_is_its_steps(rz, T, E, k, n, n_pad, inter):
+    b = Block(rz, T, E, k, n, n_pad, inter, T + 3)
+    rng = np.random.default_rng(T + 1)
+    logits, res = dev(rng.normal(size=(T, E)).astype(np.float32)), dev(rng.normal(size=(T, n_pad)).astype(np.float32))
+    seq = dev(np.where(rng.random(T) < 0.2, -1, 0).astype(np.int32))
+    q8 = dev(R.q8_buffer(*activations(rng, T, n_pad)))
+    d = b.d
+    for renorm, scale, r in ((True, 1.0, res), (False, 2.5, None)):
+        rz.moe_route(logits, b.plan, renormalise=renorm, scale=scale, row_seq=seq)
+        h8 = torch.zeros_like(b.h8)
+        h = rz.moe_swiglu(d["gate"], d["up"], q8, b.plan, inter, n_pad, out_q8=h8)
+        live = R.experts_of(host(b.plan.offsets), T * k) >= 0
+        assert np.array_equal(R.q8_quantize(host(h)[live])[0], R.q8_parts(host(h8), T * k, inter)[0][live])
+        want = rz.moe_down(d["down"], h8, b.plan, n, inter, residual=r, out_pad=n_pad)
+        plan = rz.MoePlan(T, E, k)
+        got = rz.moe_ffn(logits, q8, d["gate"], d["up"], d["down"], plan, n, n_pad, inter, renormalise=renorm, scale=scale, row_seq=seq, residual=r)
+        assert torch.equal(got, want)
+        for name in ("experts", "weights", "offsets", "rows", "places"):
+            assert torch.equal(getattr(plan, name), getattr(b.plan, name)), name
+    out = res.clone()
+    rz.moe_route(logits, b.plan, row_seq=seq)
+    want = rz.moe_ffn(logits, q8, d["gate"], d["up"], d["down"], plan, n, n_pad, inter, row_seq=seq, residual=res)
+    ws = rz.workspace(rz.moe_ffn_workspace_bytes(T, E, k, n, n_pad, inter), "cuda")
+    ws.fill_(255)
+    assert rz.moe_ffn(logits, q8, d["gate"], d["up"], d["down"], plan, n, n_pad, inter, row_seq=seq, residual=out, out=out, ws=ws) is out
+    assert torch.equal(out, want)
 
 
 def test_block_in_a_graph_and_on_another_stream(rz):

@@ -90,6 +90,26 @@ def test_down_refusals(lib, change, status):
     refused(lib, "rz_moe_down", DOWN, change, status)
 
 
+FFN = dict(logits=16, ld=8, row_seq=16, x=16, gate=32, up=48, down=64, residual=80, out=96, plan={}, renormalise=1, scale=1.0, hidden=900,
+           hidden_pad=1024, inter=512, ws=16, ws_bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(logits=None), 1), (dict(x=None), 1), (dict(gate=None), 1), (dict(up=None), 1), (dict(down=None), 1), (dict(out=None), 1),
+    (dict(ld=7), 2), (dict(scale=float("nan")), 1), (dict(hidden=0), 2), (dict(hidden=1025), 2), (dict(hidden_pad=1000), 2), (dict(inter=500), 2),
+    (dict(logits=18), 3), (dict(row_seq=18), 3), (dict(x=24), 3), (dict(gate=20), 3), (dict(down=8), 3), (dict(residual=88), 3), (dict(out=100), 3),
+    (dict(ws=None), 1), (dict(ws=8), 3), (dict(ws_bytes=200 * 2 * 512), 1),
+])
+def test_ffn_refusals(lib, change, status):
+    refused(lib, "rz_moe_ffn", FFN, change, status)
+
+
+@pytest.mark.parametrize("change,status", PLAN_CHANGES)
+def test_ffn_plan_refusals(lib, change, status):
+    st = lib.status("rz_moe_ffn", *{**FFN, "plan": plan(lib, change)}.values())
+    assert st == status and lib.last_error()
+
+
 def test_workspace_sizes(lib):
     L = lib.load()
     assert L.rz_moe_route_workspace_bytes(128, 512) == 0 and not lib.last_error()
@@ -99,11 +119,14 @@ def test_workspace_sizes(lib):
     assert L.rz_moe_swiglu_workspace_bytes(1, 64, 8, 2048) == 0 and not lib.last_error()
     assert L.rz_moe_swiglu_workspace_bytes(200, 8, 2, 512) >= 200 * 512 * 4
     assert L.rz_moe_swiglu_workspace_bytes(200, 8, 2, 100) == 0 and lib.last_error()
-    assert L.rz_moe_down_workspace_bytes(1, 64, 8, 100, 512) >= 8 * 100 * 4
+    assert L.rz_moe_down_workspace_bytes(1, 64, 8, 100, 512) == 0 and not lib.last_error()
     assert L.rz_moe_down_workspace_bytes(200, 8, 2, 100, 512) >= 200 * 2 * (100 * 4 + 512 * 4)
     assert L.rz_moe_down_workspace_bytes(200, 8, 0, 100, 512) == 0 and lib.last_error()
     assert L.rz_moe_down_workspace_bytes(200, 8, 2, 0, 512) == 0 and lib.last_error()
     assert L.rz_moe_down_workspace_bytes(200, 8, 2, 100, 500) == 0 and lib.last_error()
+    assert L.rz_moe_ffn_workspace_bytes(1, 64, 8, 900, 1024, 512) >= 8 * 512 * 5 // 4 and not lib.last_error()
+    assert L.rz_moe_ffn_workspace_bytes(1, 64, 8, 900, 800, 512) == 0 and lib.last_error()
+    assert L.rz_moe_ffn_workspace_bytes(1, 64, 8, 900, 1024, 500) == 0 and lib.last_error()
 
 
 # ---------------------------------------------------------------- the reference itself
