@@ -5,7 +5,7 @@
 // outputs) by kN rows of one expert.  For each super-block of 256 weights
 //   D = A B,  A [128][256 + 32] the weights' codes, B [256 + 32][kN] the activations
 //   sum += g * (2^E * D)                 g a scale for each weight row, E an exponent for each column
-// A holds sc * code (at most 945, exact in f16) and, in 32 further columns, the mins over the scale;
+// A holds sc * (code - 8) (at most 504, exact in f16) and, in 32 further columns, the mins over the scale;
 // it is made in registers and stored in tensor memory, which leaves shared memory's bandwidth to B.
 // B holds d8 * code / 2^E as two f16 pieces (22 bits), so that one super-block is one
 // accumulation of 2 x 16 instructions of K = 16, and accumulators are read once for 256 weights:
@@ -13,10 +13,11 @@
 // (rz_q4k_q8_gemm: 344 TFLOP/s of the formula's operations).  A kernel before this one forms B's pieces,
 // once for a row of activations however many experts and tiles of outputs read it.
 //
-// The min term -sum_j dmin m_j s_j goes into the same accumulators: A's r_j = -m_j dmin / (8 d) and
-// B's 8 s_j / 2^E, two f16 pieces each, all four products.  So g = d.  Where dmin is over 2^13 times
-// d (f16 would not hold r_j; d = 0 among them), g = dmin, and the codes are scaled by d / dmin
-// instead, rounded to f16: 2^-12 of codes that are less than an eighth of dmin.
+// The rest of a weight, 8 d sc - dmin m, times the sum s of a block of x, goes into the same accumulators: A's
+// r_j = sc_j - m_j dmin / (8 d) and B's 8 s_j / 2^E, two f16 pieces each, all four products.  (Of weights around zero r_j is
+// small; with codes that are not centred the two parts are each twice as large as what is left of them, and so is what is cut.)
+// So g = d.  Where dmin is over 2^13 times d (f16 would not hold r_j; d = 0 among them), g = dmin, and the codes are scaled by
+// d / dmin instead, rounded to f16: 2^-12 of codes that are less than an eighth of dmin.
 //
 // The tensor cores cut what they add to an accumulator; after 34 additions it starts again, so
 // that the loss stays near 2^-22.  A super-block with a scale that is no number gives its row NaN (g),
@@ -252,6 +253,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned par, Bars &b, 
 struct Head {
     float d, dmin;
     bool wide, fine;
+    __device__ __forceinline__ float shrink() const { return wide && fine ? __half2float(__float2half_rn(__fdiv_rn(d, dmin))) : 1.0f; }
 };
 __device__ __forceinline__ Head head_of(uint32_t word)
 {
@@ -623,11 +625,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     for (int cc = 0; cc < C::kChunks; ++cc) {
                         const int c = step * C::kChunks + cc;
                         const uint32_t six = (c < 2 ? sc0 : sc1) >> (16 * (c & 1));
-                        // (1024 + q) sc - 1024 sc for the low codes, (1024 + 16 q) (sc / 16) - 64 sc for the high ones: one rounding of an exact
-                        // small integer
-                        const uint32_t mul0 = hsub2u(__byte_perm(six, 0x64646464u, 0x4040), 0x64006400u), add0 = hmul2u(mul0, 0xe400e400u);
+                        // (1024 + 16 q) (sc / 16) - 72 sc = sc (q - 8), one rounding of an exact small integer
+                        const uint32_t s0 = hsub2u(__byte_perm(six, 0x64646464u, 0x4040), 0x64006400u);
                         const uint32_t s1 = hsub2u(__byte_perm(six, 0x64646464u, 0x4141), 0x64006400u);
-                        const uint32_t mul1 = hmul2u(s1, 0x2c002c00u), add1 = hmul2u(s1, 0xd400d400u);  // / 16, * -64
+                        const uint32_t mul0 = hmul2u(s0, 0x2c002c00u), add0 = hmul2u(s0, 0xd480d480u);  // / 16, * -72
+                        const uint32_t mul1 = hmul2u(s1, 0x2c002c00u), add1 = hmul2u(s1, 0xd480d480u);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const uint4 q = lds4(raw + 16 + 32 * c + 16 * half);
@@ -635,16 +637,14 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                             uint32_t lo[8], hi[8];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const uint32_t w8 = words[i] >> 8;
-                                lo[2 * i] = hfma2u(lop_and_or(words[i], 0x000f000fu, 0x64006400u), mul0, add0);
-                                lo[2 * i + 1] = hfma2u(lop_and_or(w8, 0x000f000fu, 0x64006400u), mul0, add0);
+                                lo[2 * i] = hfma2u(lop_and_or(words[i] << 4, 0x00f000f0u, 0x64006400u), mul0, add0);
+                                lo[2 * i + 1] = hfma2u(lop_and_or(words[i] >> 4, 0x00f000f0u, 0x64006400u), mul0, add0);
                                 hi[2 * i] = hfma2u(lop_and_or(words[i], 0x00f000f0u, 0x64006400u), mul1, add1);
-                                hi[2 * i + 1] = hfma2u(lop_and_or(w8, 0x00f000f0u, 0x64006400u), mul1, add1);
+                                hi[2 * i + 1] = hfma2u(lop_and_or(words[i] >> 8, 0x00f000f0u, 0x64006400u), mul1, add1);
                             }
                             if (any_wide) {
                                 const Head head = head_of(lds4(raw).x);
-                                const float f = head.wide && head.fine ? __fdiv_rn(head.d, head.dmin) : 1.0f;
-                                const uint32_t shrink = pack2(f, f);
+                                const uint32_t shrink = pack2(head.shrink(), head.shrink());
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
                                     lo[i] = hmul2u(lo[i], shrink);
@@ -660,16 +660,18 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     const uint4 hd = lds4(raw);
                     const Head head = head_of(hd.x);
                     const float ratio = head.wide ? 1.0f : head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
-                    const float by = head.fine ? -0.125f * ratio : 0.0f, bh = __half2float(__float2half_rn(by));
-                    const uint32_t rh = pack2(bh, bh), rl = pack2(by - bh, by - bh);
+                    const float by = head.fine ? -0.125f * ratio : 0.0f, f = any_wide ? head.shrink() : 1.0f;
                     const uint32_t mn[2] = {hd.z & 0x3f3f3f3fu, ((hd.w >> 4) & 0x0f0f0f0fu) | ((hd.z >> 2) & 0x30303030u)};
                     uint32_t hi[8], lo[8];  // 4 words of high pieces, twice; 4 of low ones, twice
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        // two mins as f16 (1024 + m is 0x64 m), times the ratio as it is times activations' scales (moe_pack_kernel)
-                        const uint32_t m = hsub2u(__byte_perm(mn[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u);
-                        hi[i] = hi[4 + i] = hmul2u(m, rh);
-                        lo[i] = lo[4 + i] = hfma2u(m, rl, hfma2u(m, rh, hneg2u(hi[i])));
+                        // two mins, and the scales 8 of which the codes leave out, as f16 (1024 + m is 0x64 m)
+                        const float2 m = unpack2(hsub2u(__byte_perm(mn[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u));
+                        const float2 sc = unpack2(hsub2u(__byte_perm(i < 2 ? sc0 : sc1, 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u));
+                        const float r0 = fmaf(by, m.x, f * sc.x), r1 = fmaf(by, m.y, f * sc.y);
+                        hi[i] = hi[4 + i] = pack2(r0, r1);
+                        const float2 t = unpack2(hi[i]);
+                        lo[i] = lo[4 + i] = pack2(r0 - t.x, r1 - t.y);
                     }
                     tm_store8(ta + (C::kOwnMins ? 0 : 32 * C::kChunks), hi);
                     tm_store8(ta + (C::kOwnMins ? 0 : 32 * C::kChunks) + 8, lo);

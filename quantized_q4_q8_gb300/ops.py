@@ -767,10 +767,23 @@ def rz_residual_rmsnorm(x, delta, gamma, sum, y, q8, m, n, n_pad, eps, stream=No
 
 def _matrix(t, dtype, rows, cols, dev, name):
     """The address of a contiguous tensor [rows, cols]."""
+    try:
+        if t.get_device() == dev and t.dtype == dtype and t.shape == (rows, cols) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _on_device(t, dtype, 2, dev, name)
-    if tuple(t.shape) != (rows, cols) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous [{rows}, {cols}], got {list(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous [{rows}, {cols}], got {list(t.shape)}")
+
+
+def _values(t, dtype, n, dev, name):
+    """The address of a contiguous tensor of n values."""
+    try:
+        if t.get_device() == dev and t.dtype == dtype and t.shape == (n,) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _vector(t, dtype, n, dev, name)
 
 
 def residual_rmsnorm(x, delta, gamma, n: int, n_pad: int, eps: float, want_y: bool = True, want_q8: bool = True, sum_out=None,
@@ -782,12 +795,16 @@ def residual_rmsnorm(x, delta, gamma, n: int, n_pad: int, eps: float, want_y: bo
     m = _on_device(x, f32, 2, dev, "x").shape[0]
     x_at = _matrix(x, f32, m, n_pad, dev, "x")
     delta_at = None if delta is None else _matrix(delta, f32, m, n_pad, dev, "delta")
+    gamma_at = _values(gamma, f32, n, dev, "gamma")
     if sum_out is None:
         sum_out = _new((m, n_pad), f32, dev, stream)
+        sum_at = sum_out.data_ptr()
+    else:
+        sum_at = _matrix(sum_out, f32, m, n_pad, dev, "sum_out")
     y = _new((m, n_pad), f32, dev, stream) if want_y else None
     q8 = _new((q8_1_size(m, n_pad),), torch.uint8, dev, stream) if want_q8 else None
-    call("rz_residual_rmsnorm", x_at, delta_at, _vector(gamma, f32, n, dev, "gamma"), _matrix(sum_out, f32, m, n_pad, dev, "sum_out"),
-         _ptr(y), _ptr(q8), m, n, n_pad, eps, _stream_on(stream, dev))
+    call("rz_residual_rmsnorm", x_at, delta_at, gamma_at, sum_at, None if y is None else y.data_ptr(), None if q8 is None else q8.data_ptr(), m,
+         n, n_pad, eps, _stream_on(stream, dev))
     return sum_out, y, q8
 
 
@@ -834,10 +851,13 @@ def rz_moe_route(logits, ld, row_seq, plan, renormalise, scale, ws, ws_bytes, st
 
 
 def _scratch(ws, need, dev, stream):
-    """(address, bytes) of the workspace given, or of a new one of `need` bytes and the tensor that holds it."""
+    """(address, bytes, tensor) of the workspace given, or of a new one of need() bytes."""
     import torch
     if ws is None:
-        ws = _new((max(need, 16),), torch.uint8, dev, stream)
+        size = need()
+        if size == 0:
+            return None, 0, None
+        ws = _new((size,), torch.uint8, dev, stream)
     return _vector(ws, torch.uint8, 0, dev, "ws", more=True), ws.shape[0], ws
 
 
@@ -849,7 +869,7 @@ def moe_route(logits, plan: MoePlan, renormalise: bool = True, scale: float = 1.
     dev = torch.cuda.current_device()
     if _on_device(logits, torch.float32, 2, dev, "logits").shape[0] != plan.n_tokens:
         raise ValueError("logits must have a row for each token of the plan")
-    at, size, ws = _scratch(ws, moe_route_workspace_bytes(plan.n_tokens, plan.n_experts), dev, stream)
+    at, size, ws = _scratch(ws, lambda: moe_route_workspace_bytes(plan.n_tokens, plan.n_experts), dev, stream)
     call("rz_moe_route", logits.data_ptr(), _row_ld(logits, plan.n_experts, "logits"),
          None if row_seq is None else _vector(row_seq, torch.int32, plan.n_tokens, dev, "row_seq", more=True), _plan_on(plan, dev),
          1 if renormalise else 0, scale, at, size, _stream_on(stream, dev))
@@ -859,13 +879,13 @@ def moe_route(logits, plan: MoePlan, renormalise: bool = True, scale: float = 1.
 def _expert_weights(w, n_experts, out_dim, in_dim, dev, name):
     """The address of Q4_K weights [n_experts][out_dim][in_dim]: a contiguous uint8 tensor of any shape."""
     import torch
-    if not isinstance(w, torch.Tensor) or w.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if w.dtype != torch.uint8:
-        raise TypeError(f"{name} must be {torch.uint8}, got {w.dtype}")
-    if not w.is_contiguous() or w.numel() != n_experts * q4k_bytes(out_dim, in_dim):
-        raise ValueError(f"{name} must hold {n_experts} x {out_dim} x {in_dim} Q4_K weights, contiguous")
-    return w.data_ptr()
+    try:
+        if w.get_device() == dev and w.dtype == torch.uint8 and w.is_contiguous() and w.numel() == n_experts * out_dim * (in_dim // 256) * 144:
+            return w.data_ptr()
+    except AttributeError:
+        pass
+    _on_device(w, torch.uint8, w.dim() if hasattr(w, "dim") else 0, dev, name)
+    raise ValueError(f"{name} must hold {n_experts} x {out_dim} x {in_dim} Q4_K weights, contiguous")
 
 
 def moe_swiglu_workspace_bytes(n_tokens: int, n_experts: int, top_k: int, in_dim: int) -> int:
@@ -885,12 +905,12 @@ def moe_swiglu(w_gate, w_up, x_q8, plan: MoePlan, inter: int, in_dim: int, out=N
     u8, dev, pairs = torch.uint8, torch.cuda.current_device(), plan.n_tokens * plan.top_k
     if out is None and want_h:
         out = _new((pairs, inter), torch.float32, dev, stream)
-    at, size, ws = _scratch(ws, moe_swiglu_workspace_bytes(plan.n_tokens, plan.n_experts, plan.top_k, in_dim), dev, stream)
+    at, size, ws = _scratch(ws, lambda: moe_swiglu_workspace_bytes(plan.n_tokens, plan.n_experts, plan.top_k, in_dim), dev, stream)
     call("rz_moe_swiglu", _expert_weights(w_gate, plan.n_experts, inter, in_dim, dev, "w_gate"),
          _expert_weights(w_up, plan.n_experts, inter, in_dim, dev, "w_up"),
-         _vector(x_q8, u8, q8_1_size(plan.n_tokens, in_dim), dev, "x_q8"), _plan_on(plan, dev), inter, in_dim,
+         _values(x_q8, u8, q8_1_size(plan.n_tokens, in_dim), dev, "x_q8"), _plan_on(plan, dev), inter, in_dim,
          None if out is None else _matrix(out, torch.float32, pairs, inter, dev, "out"),
-         None if out_q8 is None else _vector(out_q8, u8, q8_1_size(pairs, inter), dev, "out_q8"), at, size, _stream_on(stream, dev))
+         None if out_q8 is None else _values(out_q8, u8, q8_1_size(pairs, inter), dev, "out_q8"), at, size, _stream_on(stream, dev))
     return out
 
 
@@ -910,11 +930,14 @@ def moe_down(w_down, h_q8, plan: MoePlan, out_dim: int, in_dim: int, residual=No
     f32, dev, out_pad = torch.float32, torch.cuda.current_device(), out_pad or out_dim
     if out is None:
         out = _new((plan.n_tokens, out_pad), f32, dev, stream)
-    at, size, ws = _scratch(ws, moe_down_workspace_bytes(plan.n_tokens, plan.n_experts, plan.top_k, out_dim, in_dim), dev, stream)
+        out_at = out.data_ptr()
+    else:
+        out_at = _matrix(out, f32, plan.n_tokens, out_pad, dev, "out")
+    at, size, ws = _scratch(ws, lambda: moe_down_workspace_bytes(plan.n_tokens, plan.n_experts, plan.top_k, out_dim, in_dim), dev, stream)
     call("rz_moe_down", _expert_weights(w_down, plan.n_experts, out_dim, in_dim, dev, "w_down"),
-         _vector(h_q8, torch.uint8, q8_1_size(plan.n_tokens * plan.top_k, in_dim), dev, "h_q8"), _plan_on(plan, dev),
+         _values(h_q8, torch.uint8, q8_1_size(plan.n_tokens * plan.top_k, in_dim), dev, "h_q8"), _plan_on(plan, dev),
          None if residual is None else _matrix(residual, f32, plan.n_tokens, out_pad, dev, "residual"),
-         _matrix(out, f32, plan.n_tokens, out_pad, dev, "out"), out_dim, out_pad, in_dim, at, size, _stream_on(stream, dev))
+         out_at, out_dim, out_pad, in_dim, at, size, _stream_on(stream, dev))
     return out
 
 
@@ -937,10 +960,10 @@ def moe_ffn(logits, x_q8, w_gate, w_up, w_down, plan: MoePlan, hidden: int, hidd
         raise ValueError("logits must have a row for each token of the plan")
     if out is None:
         out = _new((T, hidden_pad), f32, dev, stream)
-    at, size, ws = _scratch(ws, moe_ffn_workspace_bytes(T, E, plan.top_k, hidden, hidden_pad, inter), dev, stream)
+    at, size, ws = _scratch(ws, lambda: moe_ffn_workspace_bytes(T, E, plan.top_k, hidden, hidden_pad, inter), dev, stream)
     call("rz_moe_ffn", logits.data_ptr(), _row_ld(logits, E, "logits"),
          None if row_seq is None else _vector(row_seq, torch.int32, T, dev, "row_seq", more=True),
-         _vector(x_q8, torch.uint8, q8_1_size(T, hidden_pad), dev, "x_q8"), _expert_weights(w_gate, E, inter, hidden_pad, dev, "w_gate"),
+         _values(x_q8, torch.uint8, q8_1_size(T, hidden_pad), dev, "x_q8"), _expert_weights(w_gate, E, inter, hidden_pad, dev, "w_gate"),
          _expert_weights(w_up, E, inter, hidden_pad, dev, "w_up"), _expert_weights(w_down, E, hidden, inter, dev, "w_down"),
          None if residual is None else _matrix(residual, f32, T, hidden_pad, dev, "residual"), _matrix(out, f32, T, hidden_pad, dev, "out"),
          _plan_on(plan, dev), 1 if renormalise else 0, scale, hidden, hidden_pad, inter, at, size, _stream_on(stream, dev))
