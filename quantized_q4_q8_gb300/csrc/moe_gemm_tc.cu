@@ -26,8 +26,8 @@
 // Roles of the warps, one CTA for each SM, items (expert, tile of its outputs, tile of its rows) in turn:
 //   warps 0, 1   issue the products of the first and second matrix (what synchronises costs a warp some 50 to 100
 //                cycles each, so that one warp for both was the bottleneck)
-//   warp 2       copies the raw weights, 128 rows x 144 bytes a box
-//   warp 3       gathers B's rows by the plan, 16 bytes a lane (cp.async)
+//   warp 2       copies B, bulk copies of tiles laid out as shared memory takes them (moe_pack_kernel, the launch before)
+//   warp 3       copies the raw weights, 128 rows x 144 bytes a box
 //   groups of 4  unpack A, a thread for a weight row, the groups taking the steps of both matrices in turn
 //   8 warps      add up: a thread has a weight row of both matrices and half of the columns
 // Few rows (kN <= 32): the two pieces of B stand side by side as 2 kN columns, which halves the instructions.
@@ -52,19 +52,24 @@ template <int N>
 struct Cfg {
     static constexpr bool kStack = N <= 32;           // pieces side by side
     static constexpr int kColsD = kStack ? 2 * N : N;
-    static constexpr int kChunks = N >= 64 ? 1 : 2;   // of 64 weights, in a step
-    static constexpr bool kOwnMins = N >= 64;         // the mins are a step of their own (no room in tensor memory for wider slots)
-    static constexpr int kSteps = 4 / kChunks + (kOwnMins ? 1 : 0);  // of a super-block, the last one with the mins
+    static constexpr int kChunks = kStack ? 2 : 1;    // of 64 weights, in a slot of A
+    // What A is filled with for a super-block: side by side, two slots of two chunks, the second with the mins; else the mins, then
+    // four slots of a chunk (no room in tensor memory for wider ones)
+    static constexpr int kUses = kStack ? 2 : 5;
+    // What B's copies bring: side by side, the same two; else the mins, the low pieces of the four chunks, their high ones.  The low
+    // pieces come first, while the accumulators are small: what is added to a large one is cut by as much, however small it is.
+    static constexpr int kEntries = kStack ? 2 : 9;
     static constexpr int kGroups = 4;                 // that unpack A: two for each matrix, taking its steps in turn
     static constexpr int kBufD = N == 128 ? 2 : 3;    // accumulators: one for each matrix, or three in turn
     static constexpr int kSlotsA = N == 128 ? 4 : 2;  // of A for each matrix; its two groups fill them in turn
-    static constexpr int kBytesB = kChunks * N * 256; // two pieces of 64 * kChunks values
-    static constexpr int kSlotB = kBytesB + (kOwnMins ? 0 : N * 64);
-    static constexpr int kRingB = N == 128 ? 4 : 5;
-    static constexpr int kCellB = 4 / kChunks * kBytesB + N * 64;  // of a super-block: the steps, the mins
+    static constexpr int kMinsB = N * 64;
+    static constexpr int kBytesB = N * (kStack ? 512 : 128);  // two pieces of 128 values, or one of 64
+    static constexpr int kSlotB = kBytesB + (kStack ? kMinsB : 0);
+    static constexpr int kRingB = kStack ? 5 : 8;
+    static constexpr int kCellB = N * 1024 + kMinsB;   // of a super-block
     static constexpr int kRingRaw = N == 128 ? 4 : N == 16 ? 8 : 6;
     static constexpr int kColA = kBufD * kColsD;      // tensor memory: accumulators, then A
-    static constexpr int kWidthA = 32 * kChunks + (kOwnMins ? 0 : 16);
+    static constexpr int kWidthA = 32 * kChunks + (kStack ? 16 : 0);
     static constexpr int kHalf = N / 2;               // columns of a thread that adds up
     static constexpr int kFirstUnpack = 4, kFirstSum = kFirstUnpack + 4 * kGroups;
     static constexpr int kThreads = 32 * (kFirstSum + 8);
@@ -77,24 +82,24 @@ struct Cfg {
     static constexpr int off_item = off_cs + kHdr * N * 4;         // int4 [kItems]
     static constexpr int off_cum = off_item + 16 * kItems;         // int [kMoeMaxExperts + 1]
     static constexpr int off_bars = off_cum + 4 * (kMoeMaxExperts + 1) + 12;
-    static constexpr int bytes = off_bars + 640 + 1024;
+    static constexpr int bytes = off_bars + 768 + 1024;
     static_assert(kColA + 2 * kSlotsA * kWidthA <= 512, "tensor memory");
     static_assert(off_raw % 128 == 0, "copies start on 128 bytes");
     static_assert(bytes <= 227 * 1024, "shared memory");
     static_assert(kRingRaw % 2 == 0, "rings");
     // Scales of super-block k take the place of those of k - kHdr, added up by then: whoever writes them has seen the products of a
     // step at most kRingB (or kSlotsA) before done, whose accumulators were free, which takes all but the last three of those before
-    static_assert((kRingB + kSteps - 1) / kSteps + 1 <= kHdr, "scales");
+    static_assert((kRingB + kEntries - 1) / kEntries + 1 <= kHdr, "scales");
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
     static_assert(kRegsSum == 0 || 128 * (kRegsIssue + kGroups * kRegsUnpack) + 256 * kRegsSum <= kThreads * kLaunchRegs, "registers");
 };
 
 struct Bars {
-    uint64_t a_full[2][4], a_empty[2][4], b_full[6], b_empty[6], raw_full[8], raw_empty[8], d_full[3], d_empty[3], h_full[kHdr], cs_full[kHdr], done[2];
+    uint64_t a_full[2][4], a_empty[2][4], b_full[8], b_empty[8], raw_full[8], raw_empty[8], d_full[3], d_empty[3], h_full[kHdr], cs_full[kHdr], done[2];
     uint32_t tmem;
     int gave_up;
 };
-static_assert(sizeof(Bars) <= 640, "barriers");
+static_assert(sizeof(Bars) <= 768, "barriers");
 
 struct TcArgs {
     CUtensorMap map1, map2;
@@ -383,8 +388,10 @@ __global__ void __launch_bounds__(kPackThreads) moe_pack_kernel(const MoeGemvArg
         float high[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) high[k] = __half2float(__float2half_rn(v[k]));
-        // step, and the chunk of 64 within it
-        uint8_t *base = to + quarter / C::kChunks * C::kBytesB + (c >> 3) * (C::kChunks * 1024) + quarter % C::kChunks * 1024 + row * 16;
+        // this quarter is a chunk of 64: its high pieces, and how far behind the low ones are (kN rows on, side by side)
+        uint8_t *base = to + (c >> 3) * (C::kChunks * 1024) + row * 16 +
+                        (C::kStack ? quarter / 2 * C::kBytesB + quarter % 2 * 1024 : C::kMinsB + (4 + quarter) * C::kBytesB);
+        constexpr int kLow = C::kStack ? N * 256 : -4 * C::kBytesB;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // 16 codes, half a block
             const uint32_t dh = pack2(high[k >> 1], high[k >> 1]), dl = pack2(v[k >> 1] - high[k >> 1], v[k >> 1] - high[k >> 1]);
@@ -403,12 +410,11 @@ __global__ void __launch_bounds__(kPackThreads) moe_pack_kernel(const MoeGemvArg
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 *reinterpret_cast<uint4 *>(base + (2 * k + i) * 128) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                // the low pieces: kN rows on (side by side) or an operand of their own
-                *reinterpret_cast<uint4 *>(base + N * C::kChunks * 128 + (2 * k + i) * 128) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                *reinterpret_cast<uint4 *>(base + kLow + (2 * k + i) * 128) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
             }
         }
         // 8 high pieces of s, 8 low ones, and both again
-        uint8_t *m = to + 4 / C::kChunks * C::kBytesB + (c >> 3) * 512 + row * 16 + quarter * 4;
+        uint8_t *m = to + (C::kStack ? 2 * C::kBytesB : 0) + (c >> 3) * 512 + row * 16 + quarter * 4;
         const uint32_t sh = pack2(high[2], high[3]), sl = pack2(v[2] - high[2], v[3] - high[3]);
         *reinterpret_cast<uint32_t *>(m) = sh;
         *reinterpret_cast<uint32_t *>(m + 128) = sl;
@@ -492,41 +498,42 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             // -------------------------------------------------------- products of matrix `warp`
             const int mt = warp;
             const uint32_t elected = elect();
-            RingPos pa{0, 0}, pb{0, 0}, pd{mt, 0};
+            RingPos pa{0, 0}, pagain{0, 0}, pb{0, 0}, pd{mt, 0};
             bool ok = true;
             for (int64_t k = 0; k < blocks && ok; ++k) {
 #pragma unroll
-                for (int step = 0; step < C::kSteps; ++step) {
+                for (int entry = 0; entry < C::kEntries; ++entry) {
+                    // of A: the next slot, but for the high pieces, which go over the chunks' slots again
+                    const bool again = !C::kStack && entry > 4, last = entry == C::kEntries - 1;
+                    RingPos &slot = again ? pagain : pa;
                     // the phases tested together, one latency; what is not complete is waited for
-                    const bool ra = test_phase(&b.a_full[mt][pa.s], pa.par), rb = test_phase(&b.b_full[pb.s], pb.par);
-                    const bool rd = step > 0 || test_phase(&b.d_empty[pd.s], pd.par ^ 1u);
+                    const bool ra = again || test_phase(&b.a_full[mt][pa.s], pa.par), rb = test_phase(&b.b_full[pb.s], pb.par);
+                    const bool rd = entry > 0 || test_phase(&b.d_empty[pd.s], pd.par ^ 1u);
                     if (!__all_sync(0xffffffffu, ra && rb && rd)) {
-                        if (step == 0 && !(ok = wait_warp(&b.d_empty[pd.s], pd.par ^ 1u, b, g.err))) break;
+                        if (entry == 0 && !(ok = wait_warp(&b.d_empty[pd.s], pd.par ^ 1u, b, g.err))) break;
                         if (!(ok = wait_warp(&b.b_full[pb.s], pb.par, b, g.err))) break;
-                        if (!(ok = wait_warp(&b.a_full[mt][pa.s], pa.par, b, g.err))) break;
+                        if (!again && !(ok = wait_warp(&b.a_full[mt][pa.s], pa.par, b, g.err))) break;
                     }
                     fence_after();
                     const uint32_t d = tmem + pd.s * C::kColsD;
-                    const uint32_t ta = tmem + C::kColA + (mt * C::kSlotsA + pa.s) * C::kWidthA;
+                    const uint32_t ta = tmem + C::kColA + (mt * C::kSlotsA + slot.s) * C::kWidthA;
                     const uint32_t tb = operand_low(sm32 + C::off_b + pb.s * C::kSlotB);
-                    if (!C::kOwnMins || step < C::kSteps - 1) {
+                    if (C::kStack || entry > 0) {
 #pragma unroll
-                        for (int i = 0; i < 4 * C::kChunks; ++i) {
-                            mma_ts(elected, d, ta + 8 * i, tb + 16 * i, operand_high(C::kChunks * 1024), idesc_f16(C::kColsD), step > 0 || i > 0);
-                            if constexpr (!C::kStack)
-                                mma_ts(elected, d, ta + 8 * i, tb + (N * C::kChunks * 8 + 16 * i), operand_high(C::kChunks * 1024), idesc_f16(N), true);
-                        }
+                        for (int i = 0; i < 4 * C::kChunks; ++i)
+                            mma_ts(elected, d, ta + 8 * i, tb + 16 * i, operand_high(C::kChunks * 1024), idesc_f16(C::kColsD), entry > 0 || i > 0);
                     }
-                    if (step == C::kSteps - 1) {
+                    if (C::kStack ? last : entry == 0) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            mma_ts(elected, d, ta + (C::kOwnMins ? 0 : 32 * C::kChunks) + 8 * i, tb + (C::kOwnMins ? 0 : C::kBytesB / 16) + 16 * i,
-                                   operand_high(512), idesc_f16(N), true);
+                            mma_ts(elected, d, ta + (C::kStack ? 32 * C::kChunks : 0) + 8 * i, tb + (C::kStack ? C::kBytesB / 16 : 0) + 16 * i,
+                                   operand_high(512), idesc_f16(N), C::kStack || i > 0);
                     }
-                    commit(elected, &b.a_empty[mt][pa.s]);
+                    if (C::kStack || entry == 0 || again) commit(elected, &b.a_empty[mt][slot.s]);
                     commit(elected, &b.b_empty[pb.s]);
-                    if (step == C::kSteps - 1) commit(elected, &b.d_full[pd.s]);
-                    ring_next(pa, C::kSlotsA);
+                    if (last) commit(elected, &b.d_full[pd.s]);
+                    ring_next(slot, C::kSlotsA);
+                    if (!C::kStack && entry == 0) pagain = pa;
                     ring_next(pb, C::kRingB);
                 }
                 ring_add(pd, 2, C::kBufD);
@@ -565,10 +572,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     const int64_t cell0 = static_cast<int64_t>(cum[e] + tile) * nsb;
                     for (int sb = 0; sb < nsb && ok; ++sb) {
                         const uint8_t *from = a.pack + (cell0 + sb) * C::kCellB;
-                        for (int step = 0; step < C::kSteps; ++step) {
+                        for (int entry = 0; entry < C::kEntries; ++entry) {
                             if (!(ok = wait_one(&b.b_empty[p.s], p.par ^ 1u, b, g.err))) break;
-                            const bool last = step == C::kSteps - 1;
-                            const uint32_t bytes = (!C::kOwnMins || !last ? C::kBytesB : 0) + (last ? N * 64 : 0);
+                            const uint32_t bytes = C::kStack ? C::kBytesB + (entry == 1 ? C::kMinsB : 0) : entry == 0 ? C::kMinsB : C::kBytesB;
                             mbar_arrive_expect_tx(&b.b_full[p.s], bytes);
                             bulk_g2s(sm + C::off_b + p.s * C::kSlotB, from, bytes, &b.b_full[p.s]);
                             from += bytes;
@@ -602,7 +608,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         const uint32_t ta0 = tmem + (static_cast<uint32_t>(32 * (cw & 3)) << 16) + C::kColA + mt * C::kSlotsA * C::kWidthA;
         RingPos praw{mt, 0};
         RingPos pa{turn, 0};
-        int h = 0, step = turn;  // this group's steps are every other one, over the super-blocks' ends
+        int h = 0, use = turn;  // this group's slots are every other one, over the super-blocks' ends
         bool ok = true;
         for (int64_t k = 0; k < blocks && ok; ++k) {
             if (!(ok = wait_warp(&b.raw_full[praw.s], praw.par, b, g.err))) break;
@@ -616,14 +622,15 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                 sc1 = (hd.w & 0x0f0f0f0fu) | ((hd.y >> 2) & 0x30303030u);
             }
 #pragma unroll 1
-            for (; step < C::kSteps; step += 2) {
+            for (; use < C::kUses; use += 2) {
+                const bool mins = use == (C::kStack ? 1 : 0);
                 if (!(ok = wait_warp(&b.a_empty[mt][pa.s], pa.par ^ 1u, b, g.err))) break;
                 fence_after();
                 const uint32_t ta = ta0 + pa.s * C::kWidthA;
-                if (!C::kOwnMins || step < C::kSteps - 1) {
+                if (C::kStack || !mins) {
 #pragma unroll
                     for (int cc = 0; cc < C::kChunks; ++cc) {
-                        const int c = step * C::kChunks + cc;
+                        const int c = C::kStack ? 2 * use + cc : use - 1;
                         const uint32_t six = (c < 2 ? sc0 : sc1) >> (16 * (c & 1));
                         // (1024 + 16 q) (sc / 16) - 72 sc = sc (q - 8), one rounding of an exact small integer
                         const uint32_t s0 = hsub2u(__byte_perm(six, 0x64646464u, 0x4040), 0x64006400u);
@@ -656,7 +663,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         }
                     }
                 }
-                if (step == C::kSteps - 1) {
+                if (mins) {
                     const uint4 hd = lds4(raw);
                     const Head head = head_of(hd.x);
                     const float ratio = head.wide ? 1.0f : head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
@@ -673,8 +680,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         const float2 t = unpack2(hi[i]);
                         lo[i] = lo[4 + i] = pack2(r0 - t.x, r1 - t.y);
                     }
-                    tm_store8(ta + (C::kOwnMins ? 0 : 32 * C::kChunks), hi);
-                    tm_store8(ta + (C::kOwnMins ? 0 : 32 * C::kChunks) + 8, lo);
+                    tm_store8(ta + (C::kStack ? 32 * C::kChunks : 0), hi);
+                    tm_store8(ta + (C::kStack ? 32 * C::kChunks : 0) + 8, lo);
                     sts1(sm32 + C::off_g + 4 * ((h * 2 + mt) * 128 + wrow), __float_as_uint(!head.fine ? NAN : head.wide ? head.dmin : head.d));
                 }
                 tm_store_wait();
@@ -682,13 +689,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&b.a_full[mt][pa.s]);
-                    if (step == C::kSteps - 1) mbar_arrive(&b.h_full[h]);
+                    if (mins) mbar_arrive(&b.h_full[h]);
                 }
                 ring_add(pa, 2, C::kSlotsA);
             }
             if (!ok) break;
             if (lane == 0) mbar_arrive(&b.raw_empty[praw.s]);
-            step -= C::kSteps;
+            use -= C::kUses;
             h = (h + 1) % kHdr;
             ring_add(praw, 2, C::kRingRaw);
         }
