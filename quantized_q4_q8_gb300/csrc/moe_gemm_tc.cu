@@ -5,23 +5,27 @@
 // outputs) by kN rows of one expert.  For each super-block of 256 weights
 //   D = A B,  A [128][256 + 32] the weights' codes, B [256 + 32][kN] the activations
 //   sum += g * (2^E * D)                 g a scale for each weight row, E an exponent for each column
-// A holds sc * (code - 8) (at most 504, exact in f16) and, in 32 further columns, the mins over the scale;
-// it is made in registers and stored in tensor memory, which leaves shared memory's bandwidth to B.
+// A holds sc * code or sc * (code - 8), at most 945, exact in f16, and, in further columns, what is left of the weights; it is
+// made in registers and stored in tensor memory, which leaves shared memory's bandwidth to B.
 // B holds d8 * code / 2^E as two f16 pieces (22 bits), so that one super-block is one
 // accumulation of 2 x 16 instructions of K = 16, and accumulators are read once for 256 weights:
 // products of the codes alone, exact in f16, would have to be read and scaled for each 32
 // (rz_q4k_q8_gemm: 344 TFLOP/s of the formula's operations).  A kernel before this one forms B's pieces,
 // once for a row of activations however many experts and tiles of outputs read it.
 //
-// The rest of a weight, 8 d sc - dmin m, times the sum s of a block of x, goes into the same accumulators: A's
-// r_j = sc_j - m_j dmin / (8 d) and B's 8 s_j / 2^E, two f16 pieces each, all four products.  (Of weights around zero r_j is
-// small; with codes that are not centred the two parts are each twice as large as what is left of them, and so is what is cut.)
-// So g = d.  Where dmin is over 2^13 times d (f16 would not hold r_j; d = 0 among them), g = dmin, and the codes are scaled by
+// The rest of a weight, -dmin m or 8 d sc - dmin m, times the sum s of a block of x, goes into the same accumulators: A's
+// r_j = -m_j dmin / (8 d) (+ sc_j) and B's 8 s_j / 2^E, two f16 pieces each, all four products.
+//
+// The tensor cores cut what they add to an accumulator: up to 2^-23 of it for each of 18 instructions (with the low pieces of B
+// apart, in columns of their own or before the high ones), always towards zero; then it is added up, rounded, and starts again.
+// Of weights around zero codes and mins cancel, so what is cut goes by the sums on the way.  In tiles of 16 and 32 rows the mins of 4
+// sub-blocks come beside their codes and every other sub-block is centred, which costs nothing; in those of 128 the mins come first,
+// all codes are centred.  Off by 5.5 to 7e-7 of the values of a SwiGLU (1.2e-6 without either; the plain form in f32 0.6 to 1.7e-6).
+//
+// The scale g of a row is d.  Where dmin is over 2^13 times d (f16 would not hold r_j; d = 0 among them), g = dmin, and the codes are scaled by
 // d / dmin instead, rounded to f16: 2^-12 of codes that are less than an eighth of dmin.
 //
-// The tensor cores cut what they add to an accumulator; after 34 additions it starts again, so
-// that the loss stays near 2^-22.  A super-block with a scale that is no number gives its row NaN (g),
-// a block of x its column (B's pieces).
+// A super-block with a scale that is no number gives its row NaN (g), a block of x its column (B's pieces).
 //
 // Roles of the warps, one CTA for each SM, items (expert, tile of its outputs, tile of its rows) in turn:
 //   warps 0, 1   issue the products of the first and second matrix (what synchronises costs a warp some 50 to 100
@@ -53,7 +57,7 @@ struct Cfg {
     static constexpr bool kStack = N <= 32;           // pieces side by side
     static constexpr int kColsD = kStack ? 2 * N : N;
     static constexpr int kChunks = kStack ? 2 : 1;    // of 64 weights, in a slot of A
-    // What A is filled with for a super-block: side by side, two slots of two chunks, the second with the mins; else the mins, then
+    // What A is filled with for a super-block: side by side, two slots of two chunks and their four mins; else the mins, then
     // four slots of a chunk (no room in tensor memory for wider ones)
     static constexpr int kUses = kStack ? 2 : 5;
     // What B's copies bring: side by side, the same two; else the mins, the low pieces of the four chunks, their high ones.  The low
@@ -62,14 +66,14 @@ struct Cfg {
     static constexpr int kGroups = 4;                 // that unpack A: two for each matrix, taking its steps in turn
     static constexpr int kBufD = N == 128 ? 2 : 3;    // accumulators: one for each matrix, or three in turn
     static constexpr int kSlotsA = N == 128 ? 4 : 2;  // of A for each matrix; its two groups fill them in turn
-    static constexpr int kMinsB = N * 64;
+    static constexpr int kMinsB = N * (kStack ? 32 : 64);
     static constexpr int kBytesB = N * (kStack ? 512 : 128);  // two pieces of 128 values, or one of 64
     static constexpr int kSlotB = kBytesB + (kStack ? kMinsB : 0);
     static constexpr int kRingB = kStack ? 5 : 8;
-    static constexpr int kCellB = N * 1024 + kMinsB;   // of a super-block
+    static constexpr int kCellB = N * 1024 + N * 64;   // of a super-block
     static constexpr int kRingRaw = N == 128 ? 4 : N == 16 ? 8 : 6;
     static constexpr int kColA = kBufD * kColsD;      // tensor memory: accumulators, then A
-    static constexpr int kWidthA = 32 * kChunks + (kStack ? 16 : 0);
+    static constexpr int kWidthA = 32 * kChunks + (kStack ? 8 : 0);
     static constexpr int kHalf = N / 2;               // columns of a thread that adds up
     static constexpr int kFirstUnpack = 4, kFirstSum = kFirstUnpack + 4 * kGroups;
     static constexpr int kThreads = 32 * (kFirstSum + 8);
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kPackThreads) moe_pack_kernel(const MoeGemvArg
         for (int k = 0; k < 4; ++k) high[k] = __half2float(__float2half_rn(v[k]));
         // this quarter is a chunk of 64: its high pieces, and how far behind the low ones are (kN rows on, side by side)
         uint8_t *base = to + (c >> 3) * (C::kChunks * 1024) + row * 16 +
-                        (C::kStack ? quarter / 2 * C::kBytesB + quarter % 2 * 1024 : C::kMinsB + (4 + quarter) * C::kBytesB);
+                        (C::kStack ? quarter / 2 * C::kSlotB + quarter % 2 * 1024 : C::kMinsB + (4 + quarter) * C::kBytesB);
         constexpr int kLow = C::kStack ? N * 256 : -4 * C::kBytesB;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // 16 codes, half a block
@@ -413,13 +417,21 @@ __global__ void __launch_bounds__(kPackThreads) moe_pack_kernel(const MoeGemvArg
                 *reinterpret_cast<uint4 *>(base + kLow + (2 * k + i) * 128) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
             }
         }
-        // 8 high pieces of s, 8 low ones, and both again
-        uint8_t *m = to + (C::kStack ? 2 * C::kBytesB : 0) + (c >> 3) * 512 + row * 16 + quarter * 4;
+        // the high pieces of s, the low ones, and both again: four blocks' beside their chunks, or all eight's
         const uint32_t sh = pack2(high[2], high[3]), sl = pack2(v[2] - high[2], v[3] - high[3]);
-        *reinterpret_cast<uint32_t *>(m) = sh;
-        *reinterpret_cast<uint32_t *>(m + 128) = sl;
-        *reinterpret_cast<uint32_t *>(m + 256) = sh;
-        *reinterpret_cast<uint32_t *>(m + 384) = sl;
+        if constexpr (C::kStack) {
+            uint8_t *m = to + quarter / 2 * C::kSlotB + C::kBytesB + (c >> 3) * 256 + row * 16 + quarter % 2 * 4;
+            *reinterpret_cast<uint32_t *>(m) = sh;
+            *reinterpret_cast<uint32_t *>(m + 8) = sl;
+            *reinterpret_cast<uint32_t *>(m + 128) = sh;
+            *reinterpret_cast<uint32_t *>(m + 136) = sl;
+        } else {
+            uint8_t *m = to + (c >> 3) * 512 + row * 16 + quarter * 4;
+            *reinterpret_cast<uint32_t *>(m) = sh;
+            *reinterpret_cast<uint32_t *>(m + 128) = sl;
+            *reinterpret_cast<uint32_t *>(m + 256) = sh;
+            *reinterpret_cast<uint32_t *>(m + 384) = sl;
+        }
         if (quarter == 0) col_scale[cell * N + c] = __uint_as_float((e2 + 1u) << 23);
     }
 }
@@ -432,6 +444,13 @@ __device__ __forceinline__ void ring_add(RingPos &p, int by, int n)
         p.s -= n;
         p.par ^= 1u;
     }
+}
+
+// Two low codes, v = 1024 + q: sc q = v sc - 1024 sc, or centred sc (q - 8) = (v - 1032) sc (1032 sc is not exact in f16)
+template <bool kPlain>
+__device__ __forceinline__ uint32_t low_codes(uint32_t v, uint32_t sc, uint32_t add)
+{
+    return kPlain ? hfma2u(v, sc, add) : hmul2u(hsub2u(v, 0x64086408u), sc);
 }
 
 template <int N, bool kSwiglu>
@@ -518,16 +537,18 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     const uint32_t d = tmem + pd.s * C::kColsD;
                     const uint32_t ta = tmem + C::kColA + (mt * C::kSlotsA + slot.s) * C::kWidthA;
                     const uint32_t tb = operand_low(sm32 + C::off_b + pb.s * C::kSlotB);
-                    if (C::kStack || entry > 0) {
+                    if constexpr (C::kStack) {
+                        // the mins early: the codes' sums cancel against them as they grow
+                        mma_ts(elected, d, ta, tb, operand_high(2048), idesc_f16(2 * N), entry > 0);
+                        mma_ts(elected, d, ta + 64, tb + C::kBytesB / 16, operand_high(256), idesc_f16(N), true);
 #pragma unroll
-                        for (int i = 0; i < 4 * C::kChunks; ++i)
-                            mma_ts(elected, d, ta + 8 * i, tb + 16 * i, operand_high(C::kChunks * 1024), idesc_f16(C::kColsD), entry > 0 || i > 0);
-                    }
-                    if (C::kStack ? last : entry == 0) {
+                        for (int i = 1; i < 8; ++i) mma_ts(elected, d, ta + 8 * i, tb + 16 * i, operand_high(2048), idesc_f16(2 * N), true);
+                    } else if (entry == 0) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            mma_ts(elected, d, ta + (C::kStack ? 32 * C::kChunks : 0) + 8 * i, tb + (C::kStack ? C::kBytesB / 16 : 0) + 16 * i,
-                                   operand_high(512), idesc_f16(N), C::kStack || i > 0);
+                        for (int i = 0; i < 2; ++i) mma_ts(elected, d, ta + 8 * i, tb + 16 * i, operand_high(512), idesc_f16(N), i > 0);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_ts(elected, d, ta + 8 * i, tb + 16 * i, operand_high(1024), idesc_f16(N), true);
                     }
                     if (C::kStack || entry == 0 || again) commit(elected, &b.a_empty[mt][slot.s]);
                     commit(elected, &b.b_empty[pb.s]);
@@ -574,7 +595,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         const uint8_t *from = a.pack + (cell0 + sb) * C::kCellB;
                         for (int entry = 0; entry < C::kEntries; ++entry) {
                             if (!(ok = wait_one(&b.b_empty[p.s], p.par ^ 1u, b, g.err))) break;
-                            const uint32_t bytes = C::kStack ? C::kBytesB + (entry == 1 ? C::kMinsB : 0) : entry == 0 ? C::kMinsB : C::kBytesB;
+                            const uint32_t bytes = C::kStack ? C::kSlotB : entry == 0 ? C::kMinsB : C::kBytesB;
                             mbar_arrive_expect_tx(&b.b_full[p.s], bytes);
                             bulk_g2s(sm + C::off_b + p.s * C::kSlotB, from, bytes, &b.b_full[p.s]);
                             from += bytes;
@@ -623,20 +644,20 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             }
 #pragma unroll 1
             for (; use < C::kUses; use += 2) {
-                const bool mins = use == (C::kStack ? 1 : 0);
+                const bool mins = !C::kStack && use == 0;  // the mins alone
                 if (!(ok = wait_warp(&b.a_empty[mt][pa.s], pa.par ^ 1u, b, g.err))) break;
                 fence_after();
                 const uint32_t ta = ta0 + pa.s * C::kWidthA;
-                if (C::kStack || !mins) {
+                if (!mins) {
 #pragma unroll
                     for (int cc = 0; cc < C::kChunks; ++cc) {
                         const int c = C::kStack ? 2 * use + cc : use - 1;
                         const uint32_t six = (c < 2 ? sc0 : sc1) >> (16 * (c & 1));
-                        // (1024 + 16 q) (sc / 16) - 72 sc = sc (q - 8), one rounding of an exact small integer
+                        // the high codes (1024 + 16 q) (sc / 16) - 72 sc = sc (q - 8): one rounding of an exact small integer
                         const uint32_t s0 = hsub2u(__byte_perm(six, 0x64646464u, 0x4040), 0x64006400u);
                         const uint32_t s1 = hsub2u(__byte_perm(six, 0x64646464u, 0x4141), 0x64006400u);
-                        const uint32_t mul0 = hmul2u(s0, 0x2c002c00u), add0 = hmul2u(s0, 0xd480d480u);  // / 16, * -72
-                        const uint32_t mul1 = hmul2u(s1, 0x2c002c00u), add1 = hmul2u(s1, 0xd480d480u);
+                        const uint32_t add0 = hmul2u(s0, 0xe400e400u);  // * -1024
+                        const uint32_t mul1 = hmul2u(s1, 0x2c002c00u), add1 = hmul2u(s1, 0xd480d480u);  // / 16, * -72
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const uint4 q = lds4(raw + 16 + 32 * c + 16 * half);
@@ -644,10 +665,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                             uint32_t lo[8], hi[8];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                lo[2 * i] = hfma2u(lop_and_or(words[i] << 4, 0x00f000f0u, 0x64006400u), mul0, add0);
-                                lo[2 * i + 1] = hfma2u(lop_and_or(words[i] >> 4, 0x00f000f0u, 0x64006400u), mul0, add0);
+                                const uint32_t w8 = words[i] >> 8;
+                                lo[2 * i] = low_codes<C::kStack>(lop_and_or(words[i], 0x000f000fu, 0x64006400u), s0, add0);
+                                lo[2 * i + 1] = low_codes<C::kStack>(lop_and_or(w8, 0x000f000fu, 0x64006400u), s0, add0);
                                 hi[2 * i] = hfma2u(lop_and_or(words[i], 0x00f000f0u, 0x64006400u), mul1, add1);
-                                hi[2 * i + 1] = hfma2u(lop_and_or(words[i] >> 8, 0x00f000f0u, 0x64006400u), mul1, add1);
+                                hi[2 * i + 1] = hfma2u(lop_and_or(w8, 0x00f000f0u, 0x64006400u), mul1, add1);
                             }
                             if (any_wide) {
                                 const Head head = head_of(lds4(raw).x);
@@ -663,33 +685,42 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         }
                     }
                 }
-                if (mins) {
+                if (C::kStack || mins) {
                     const uint4 hd = lds4(raw);
                     const Head head = head_of(hd.x);
                     const float ratio = head.wide ? 1.0f : head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
                     const float by = head.fine ? -0.125f * ratio : 0.0f, f = any_wide ? head.shrink() : 1.0f;
                     const uint32_t mn[2] = {hd.z & 0x3f3f3f3fu, ((hd.w >> 4) & 0x0f0f0f0fu) | ((hd.z >> 2) & 0x30303030u)};
-                    uint32_t hi[8], lo[8];  // 4 words of high pieces, twice; 4 of low ones, twice
+                    constexpr int kWords = C::kStack ? 2 : 4;  // of two sub-blocks: this slot's, or all
+                    uint32_t hi[2 * kWords], lo[2 * kWords];   // high pieces, twice; low ones, twice
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // two mins, and the scales 8 of which the codes leave out, as f16 (1024 + m is 0x64 m)
-                        const float2 m = unpack2(hsub2u(__byte_perm(mn[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u));
-                        const float2 sc = unpack2(hsub2u(__byte_perm(i < 2 ? sc0 : sc1, 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u));
-                        const float r0 = fmaf(by, m.x, f * sc.x), r1 = fmaf(by, m.y, f * sc.y);
-                        hi[i] = hi[4 + i] = pack2(r0, r1);
+                    for (int i = 0; i < kWords; ++i) {
+                        // two mins, and the scales 8 of which centred codes leave out, as f16 (1024 + m is 0x64 m)
+                        const int quad = C::kStack ? use : i >> 1;
+                        const uint32_t mm = C::kStack ? (use ? mn[1] : mn[0]) : mn[i >> 1], ss = quad ? sc1 : sc0;
+                        const float2 m = unpack2(hsub2u(__byte_perm(mm, 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u));
+                        const float2 sc = unpack2(hsub2u(__byte_perm(ss, 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u));
+                        const float r0 = C::kStack ? by * m.x : fmaf(by, m.x, any_wide ? f * sc.x : sc.x), r1 = fmaf(by, m.y, any_wide ? f * sc.y : sc.y);
+                        hi[i] = hi[kWords + i] = pack2(r0, r1);
                         const float2 t = unpack2(hi[i]);
-                        lo[i] = lo[4 + i] = pack2(r0 - t.x, r1 - t.y);
+                        lo[i] = lo[kWords + i] = pack2(r0 - t.x, r1 - t.y);
                     }
-                    tm_store8(ta + (C::kStack ? 32 * C::kChunks : 0), hi);
-                    tm_store8(ta + (C::kStack ? 32 * C::kChunks : 0) + 8, lo);
-                    sts1(sm32 + C::off_g + 4 * ((h * 2 + mt) * 128 + wrow), __float_as_uint(!head.fine ? NAN : head.wide ? head.dmin : head.d));
+                    if constexpr (C::kStack) {
+                        const uint32_t o[8] = {hi[0], hi[1], hi[2], hi[3], lo[0], lo[1], lo[2], lo[3]};
+                        tm_store8(ta + 64, o);
+                    } else {
+                        tm_store8(ta, hi);
+                        tm_store8(ta + 8, lo);
+                    }
+                    if (!C::kStack || use == 1)
+                        sts1(sm32 + C::off_g + 4 * ((h * 2 + mt) * 128 + wrow), __float_as_uint(!head.fine ? NAN : head.wide ? head.dmin : head.d));
                 }
                 tm_store_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&b.a_full[mt][pa.s]);
-                    if (mins) mbar_arrive(&b.h_full[h]);
+                    if (C::kStack ? use == 1 : mins) mbar_arrive(&b.h_full[h]);
                 }
                 ring_add(pa, 2, C::kSlotsA);
             }
