@@ -635,7 +635,7 @@ rz_status rz_residual_rmsnorm(const float *x, const float *delta, const float *g
  * never chosen; a choice that is left without an expert has -1 and the weight 0.  A token with a NaN or +infinity among its
  * logits has weights NaN (a NaN is chosen after every number).
  *   workspace rz_moe_route_workspace_bytes bytes, 16-byte aligned; no initialisation; may be
- *             NULL where that is 0 (up to 128 tokens, one launch; more: two)
+ *             NULL where that is 0 (few tokens: one launch; more: two)
  */
 size_t rz_moe_route_workspace_bytes(int64_t n_tokens, int32_t n_experts);
 rz_status rz_moe_route(const float *logits, int64_t ld, const int32_t *row_seq, const rz_moe_plan *plan,

@@ -9,10 +9,9 @@
 // Grouping is a counting sort that keeps the order of the tokens.  Few tokens: one CTA
 // selects, counts and places, one launch.  More: each CTA of the first launch selects for a
 // range of tokens and writes down how many rows each expert gets from it; each CTA of the second adds up what the CTAs
-// before it wrote and places its own range.  Rows of a range are ranked 32 at a time by one warp
-// (__match_any_sync), so that nothing depends on the order of atomics: those here only count.
+// before it wrote and places its own range.  Atomics only count and set bits, so that nothing depends on their order.
 //
-// Bound: latency.  4 bytes a logit and 16 a row are read and written.
+// Bound: latency, of the rounds and of two launches' trips to memory.  4 bytes a logit and 16 a row are read and written.
 #include <math.h>
 
 #include "rz_common.cuh"
@@ -21,8 +20,6 @@
 namespace rz {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 
 // Order-preserving: -infinity (masked) and what is taken become 0, NaN 1, numbers more.
 __device__ __forceinline__ uint32_t order_key(float f)
@@ -126,32 +123,48 @@ __device__ __forceinline__ int scan_experts(const int *total, int *next, int n_e
     return base;
 }
 
-// The rows [p0, p1) in order, one warp: each to the next place of its expert.
-__device__ __forceinline__ void place_rows(const MoeRouteArgs &a, int64_t p0, int64_t p1, int *next, int lane)
+// The rows of tokens [t0, t1) in order, all of the CTA: each to the next place of its expert.  A token has an expert once, so
+// that of 32 tokens a row's rank is the number of those before it that chose the same expert: bits of a word, whatever order they are set in.
+template <int kThreads>
+__device__ __forceinline__ void place_rows(const MoeRouteArgs &a, int64_t t0, int64_t t1, int *next, unsigned *chosen, int tid)
 {
-    for (int64_t p = p0; p < p1; p += 32) {
-        const int64_t i = p + lane;
-        const int e = i < p1 ? a.experts[i] : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        int at = -1;
-        if (e >= 0) at = next[e] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (e >= 0 && (same >> lane) == 1u) next[e] = at + 1;  // the last of its expert
-        __syncwarp();
-        if (i < p1) {
-            a.places[i] = at;
-            if (at >= 0) a.rows[at] = static_cast<int>(i);
+    for (int64_t t = t0; t < t1; t += 32) {
+        for (int e = tid; e < a.n_experts; e += kThreads) chosen[e] = 0;
+        __syncthreads();
+        const int rows = static_cast<int>(min(static_cast<int64_t>(32), t1 - t)) * a.top_k;
+        const int64_t base = t * a.top_k;
+        static_assert(2 * kThreads >= 32 * kMoeMaxTopK, "rows of 32 tokens");
+        int mine[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int p = tid + u * kThreads;
+            mine[u] = p < rows ? a.experts[base + p] : -1;
+            if (mine[u] >= 0) atomicOr(chosen + mine[u], 1u << (p / a.top_k));
         }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int p = tid + u * kThreads;
+            if (p >= rows) break;
+            const int at = mine[u] < 0 ? -1 : next[mine[u]] + __popc(chosen[mine[u]] & ((1u << (p / a.top_k)) - 1u));
+            a.places[base + p] = at;
+            if (at >= 0) a.rows[at] = static_cast<int>(base) + p;
+        }
+        __syncthreads();
+        for (int e = tid; e < a.n_experts; e += kThreads) next[e] += __popc(chosen[e]);
+        __syncthreads();
     }
 }
 
 // kPlace: one CTA does all.  Otherwise CTA c selects tokens [c * chunk, (c + 1) * chunk) and writes
 // its counts to hist[c][e].
-template <bool kPlace>
+template <int kThreads, bool kPlace>
 __global__ void __launch_bounds__(kThreads) moe_select_kernel(MoeRouteArgs a)
 {
     __shared__ int count[kMoeMaxExperts], next[kMoeMaxExperts];
+    __shared__ unsigned chosen[kPlace ? kMoeMaxExperts : 1];
     __shared__ int used;
+    constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < a.n_experts; e += kThreads) count[e] = 0;
     __syncthreads();
@@ -168,20 +181,21 @@ __global__ void __launch_bounds__(kThreads) moe_select_kernel(MoeRouteArgs a)
                 a.offsets[a.n_experts] = all;
                 used = all;
             }
-            __syncwarp();
-            place_rows(a, 0, a.n_tokens * a.top_k, next, lane);
         }
-        __syncthreads();
+        place_rows<kThreads>(a, 0, a.n_tokens, next, chosen, tid);
         for (int64_t r = used + tid; r < a.n_tokens * a.top_k; r += kThreads) a.rows[r] = -1;
     } else {
         for (int e = tid; e < a.n_experts; e += kThreads) a.hist[blockIdx.x * a.n_experts + e] = count[e];
     }
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) moe_place_kernel(MoeRouteArgs a)
 {
     __shared__ int total[kMoeMaxExperts], before[kMoeMaxExperts], next[kMoeMaxExperts];
+    __shared__ unsigned chosen[kMoeMaxExperts];
     __shared__ int used;
+    constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < a.n_experts; e += kThreads) total[e] = before[e] = 0;
     __syncthreads();
@@ -190,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) moe_place_kernel(MoeRouteArgs a)
     // warps share the ranges, lanes the experts
     for (int e = lane; e < a.n_experts; e += 32) {
         int all = 0, mine = 0;
-#pragma unroll 4
+#pragma unroll 16
         for (int c = warp; c < static_cast<int>(gridDim.x); c += kWarps) {
             const int v = a.hist[c * a.n_experts + e];
             all += v;
@@ -210,22 +224,20 @@ __global__ void __launch_bounds__(kThreads) moe_place_kernel(MoeRouteArgs a)
             if (blockIdx.x == 0) a.offsets[a.n_experts] = all;
             used = all;
         }
-        __syncwarp();
-        const int64_t t0 = blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.n_tokens);
-        place_rows(a, t0 * a.top_k, t1 * a.top_k, next, lane);
     }
-    __syncthreads();
+    const int64_t t0 = blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.n_tokens);
+    place_rows<kThreads>(a, t0, t1, next, chosen, tid);
     for (int64_t r = used + static_cast<int64_t>(blockIdx.x) * kThreads + tid; r < a.n_tokens * a.top_k;
          r += static_cast<int64_t>(gridDim.x) * kThreads)
         a.rows[r] = -1;
 }
 
 template <typename K>
-cudaError_t launch(K kernel, int grid, const MoeRouteArgs &a, cudaStream_t s)
+cudaError_t launch(K kernel, int grid, int threads, const MoeRouteArgs &a, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -235,15 +247,18 @@ cudaError_t launch(K kernel, int grid, const MoeRouteArgs &a, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Tokens of a CTA, and CTAs.
-constexpr int64_t kOneCta = 128;  // up to so many tokens, one CTA and one launch
-constexpr int64_t kMostCtas = 256;
+// Up to 16 tokens, one CTA and one launch (8 of 128 experts: 16 tokens 4.8 us, 32 tokens 7.2; two launches 6.8); up to 512, CTAs of 512
+// threads, a token for each warp (128 tokens 7.5 us, in CTAs of 1024 threads 8.6); more, of 1024 (4095 tokens 12.6 us, in the smaller ones
+// 15.2: each CTA of the second launch reads what all of the first have counted).
+constexpr int64_t kOneCta = 16, kSmallCtas = 512;
+constexpr int64_t kMostCtas = 128;
 
 int64_t route_chunk(int64_t n_tokens)
 {
     if (n_tokens <= kOneCta) return n_tokens;
+    if (n_tokens <= kSmallCtas) return 16;
     const int64_t least = (n_tokens + kMostCtas - 1) / kMostCtas;
-    return (least + kWarps - 1) / kWarps * kWarps;
+    return (least + 31) / 32 * 32;
 }
 
 }  // namespace
@@ -258,10 +273,12 @@ int64_t moe_route_workspace_bytes(int64_t n_tokens, int n_experts)
 cudaError_t launch_moe_route(MoeRouteArgs a, cudaStream_t s)
 {
     a.chunk = route_chunk(a.n_tokens);
-    if (a.n_tokens <= kOneCta) return launch(moe_select_kernel<true>, 1, a, s);
+    if (a.n_tokens <= kOneCta) return launch(moe_select_kernel<512, true>, 1, 512, a, s);
     const int grid = static_cast<int>((a.n_tokens + a.chunk - 1) / a.chunk);
-    const cudaError_t e = launch(moe_select_kernel<false>, grid, a, s);
-    return e != cudaSuccess ? e : launch(moe_place_kernel, grid, a, s);
+    const bool small = a.n_tokens <= kSmallCtas;
+    const cudaError_t e = small ? launch(moe_select_kernel<512, false>, grid, 512, a, s) : launch(moe_select_kernel<1024, false>, grid, 1024, a, s);
+    if (e != cudaSuccess) return e;
+    return small ? launch(moe_place_kernel<512>, grid, 512, a, s) : launch(moe_place_kernel<1024>, grid, 1024, a, s);
 }
 
 }  // namespace rz

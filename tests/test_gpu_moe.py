@@ -143,8 +143,8 @@ def check_route(rz, logits, k, renorm, scale=1.0, row_seq=None, plan=None, ld=No
     return plan
 
 
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (5, 8, 2), (33, 65, 6), (128, 128, 8), (129, 32, 32), (200, 512, 32), (1000, 128, 8),
-                                   (4097, 8, 2), (70, 256, 1)])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (5, 8, 2), (16, 65, 6), (17, 128, 8), (129, 32, 32), (200, 512, 32), (512, 16, 3),
+                                   (513, 512, 32), (1000, 128, 8), (4097, 8, 2), (9000, 33, 5), (70, 256, 1)])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_route(rz, T, E, k, renorm):
     rng = np.random.default_rng(T + E)

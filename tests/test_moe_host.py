@@ -112,8 +112,8 @@ def test_ffn_plan_refusals(lib, change, status):
 
 def test_workspace_sizes(lib):
     L = lib.load()
-    assert L.rz_moe_route_workspace_bytes(128, 512) == 0 and not lib.last_error()
-    assert L.rz_moe_route_workspace_bytes(129, 8) > 0
+    assert L.rz_moe_route_workspace_bytes(16, 512) == 0 and not lib.last_error()
+    assert L.rz_moe_route_workspace_bytes(17, 8) > 0
     assert L.rz_moe_route_workspace_bytes(0, 8) == 0 and lib.last_error()
     assert L.rz_moe_route_workspace_bytes(5, 600) == 0 and lib.last_error()
     assert L.rz_moe_swiglu_workspace_bytes(1, 64, 8, 2048) == 0 and not lib.last_error()
