@@ -591,7 +591,8 @@ rz_status rz_decode_layer_paged(const float *input, const rz_layer_weights *w, c
  * the order of their tokens.  All of a plan is in device memory, so that one captured graph serves every
  * step.  A plan may also come from elsewhere; offsets outside [0, n_tokens * top_k] make an expert have no
  * rows, a row or place outside it records RZ_ERR_DEVICE and reads row 0 or is left out, and offsets that
- * overlap or decrease give undefined values.
+ * overlap or decrease give undefined values.  Calls that share a workspace or write one plan must not overlap on
+ * the GPU, captured ones among them.
  * ---------------------------------------------------------------------------
  */
 typedef struct {
@@ -726,6 +727,13 @@ rz_status rz_debug_stall_next_gemv(uint32_t wait_limit);
  * items that CTA 0 works are undefined, and the workspace is to be filled with zeros again.
  */
 rz_status rz_debug_stall_next_paged(uint32_t wait_limit);
+
+/*
+ * rz_debug_stall_next_moe -- the same for the next product of rz_moe_swiglu, rz_moe_down or
+ * rz_moe_ffn that runs on the tensor cores: CTA 0 leaves its first weights uncopied.  Code 0x120,
+ * RZ_ERR_TIMEOUT; the outputs of CTA 0 are undefined.
+ */
+rz_status rz_debug_stall_next_moe(uint32_t wait_limit);
 
 
 #ifdef __cplusplus

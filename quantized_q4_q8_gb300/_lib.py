@@ -135,6 +135,7 @@ SIGNATURES = {
     "rz_set_pdl": [C.c_int],
     "rz_debug_stall_next_gemv": [C.c_uint32],
     "rz_debug_stall_next_paged": [C.c_uint32],
+    "rz_debug_stall_next_moe": [C.c_uint32],
     "rz_last_error": [],
     "rz_version": [],
 }

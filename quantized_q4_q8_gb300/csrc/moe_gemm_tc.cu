@@ -100,7 +100,7 @@ struct Cfg {
 
 struct Bars {
     uint64_t a_full[2][4], a_empty[2][4], b_full[8], b_empty[8], raw_full[8], raw_empty[8], d_full[3], d_empty[3], h_full[kHdr], cs_full[kHdr], done[2];
-    uint32_t tmem;
+    uint32_t tmem, limit;    // polls of a wait
     int gave_up;
 };
 static_assert(sizeof(Bars) <= 768, "barriers");
@@ -110,6 +110,7 @@ struct TcArgs {
     MoeGemvArgs g;
     const uint8_t *pack;     // B of tile i and super-block j, as its copies go to shared memory: at (i * nsb + j) * kCellB
     const float *col_scale;  // 2^E [tiles][super-blocks][kN]
+    uint32_t stall;          // test aid (rz_debug_stall_next_moe), 0 otherwise
 };
 
 // Shared-memory operand, K-major, no swizzle: core matrices of 8 rows x 16 bytes, 128 bytes apart along K, groups of 8 rows `stride`
@@ -243,11 +244,13 @@ __device__ __forceinline__ bool give_up(Bars &b, unsigned *err)
 __device__ __forceinline__ bool wait_one(uint64_t *bar, unsigned par, Bars &b, unsigned *err)
 {
     volatile int *flag = &b.gave_up;
-    for (uint32_t i = 0; i < kWaitLimit / 8; ++i) {
+    for (uint32_t i = 0;; ++i) {
         if (mbar_try_wait(bar, par)) return true;
-        if ((i & 63u) == 63u && *flag) return false;
+        if ((i & 63u) == 63u) {
+            if (*flag) return false;
+            if (i >= b.limit) return give_up(b, err);
+        }
     }
-    return give_up(b, err);
 }
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned par, Bars &b, unsigned *err)
 {
@@ -491,6 +494,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         mbar_init(&b.done[0], 1);
         mbar_init(&b.done[1], 1);
         b.gave_up = 0;
+        b.limit = a.stall && blockIdx.x == 0 ? a.stall : kWaitLimit / 8;
         fence_mbar_init();
         tma_prefetch_desc(&a.map1);
         if (kSwiglu) tma_prefetch_desc(&a.map2);
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         } else if (lane == 0) {
             // -------------------------------------------------------- copies: warp 2 B and the columns' exponents, warp 3 the raw weights
             const uint64_t pol = l2_evict_first_policy();
-            const bool weights = warp == 3;
+            const bool weights = warp == 3, stalled = weights && a.stall && blockIdx.x == 0;  // the first weights are not copied
             RingPos p{0, 0}, ph{0, 0};
             int64_t issued = 0, issued_h = 0;
             bool ok = true;
@@ -582,9 +586,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     for (int sb = 0; sb < nsb && ok; ++sb) {
                         for (int mt = 0; mt < 2; ++mt) {
                             if (!(ok = wait_one(&b.raw_empty[p.s], p.par ^ 1u, b, g.err))) break;
-                            mbar_arrive_expect_tx(&b.raw_full[p.s], kRawBytes);
-                            tma_load_2d(sm + C::off_raw + p.s * kRawBytes, kSwiglu && mt ? &a.map2 : &a.map1, sb * 144,
-                                        y0 + (kSwiglu ? 0 : 128 * mt), &b.raw_full[p.s], pol);
+                            if (!stalled || issued > 0) {
+                                mbar_arrive_expect_tx(&b.raw_full[p.s], kRawBytes);
+                                tma_load_2d(sm + C::off_raw + p.s * kRawBytes, kSwiglu && mt ? &a.map2 : &a.map1, sb * 144,
+                                            y0 + (kSwiglu ? 0 : 128 * mt), &b.raw_full[p.s], pol);
+                            }
                             ++issued;
                             ring_next(p, C::kRingRaw);
                         }
@@ -612,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             }
             // copies in flight land before the CTA ends
             const int ring = weights ? C::kRingRaw : C::kRingB;
-            for (int64_t k = max(static_cast<int64_t>(0), issued - ring); k < issued; ++k) {
+            for (int64_t k = max(static_cast<int64_t>(stalled), issued - ring); k < issued; ++k) {
                 const RingPos q = ring_pos(k, ring);
                 mbar_wait(weights ? &b.raw_full[q.s] : &b.b_full[q.s], q.par);
             }
@@ -883,6 +889,8 @@ cudaError_t launch_all(const MoeGemvArgs &g, void *workspace, cudaStream_t s)
     float *col_scale = reinterpret_cast<float *>(pack + tiles * nsb * C::kCellB);
     a.pack = pack;
     a.col_scale = col_scale;
+    a.stall = g_stall_next_moe;
+    g_stall_next_moe = 0;  // one product only
     const uint64_t row_bytes = static_cast<uint64_t>(nsb) * 144, rows = static_cast<uint64_t>(g.n_experts) * g.out_dim;
     cudaError_t e = encode_tensor_map_2d(&a.map1, g.w1, 1, row_bytes, rows, row_bytes, 144, 128);
     if (e == cudaSuccess && g.w2) e = encode_tensor_map_2d(&a.map2, g.w2, 1, row_bytes, rows, row_bytes, 144, 128);

@@ -1,5 +1,5 @@
 // moe_gemv.cu -- products grouped by expert of few rows: Q4_K weights of each expert against
-// the Q8_1 rows that chose it, and the sum of a token's rows.
+// the Q8_1 rows that chose it, with exact integer dots; and the sum of a token's rows.
 //
 //   h[r][i] = silu(G_e[i] . x_t) * (U_e[i] . x_t)     row r of expert e, token t = rows[r] / k
 //   o[r][i] = D_e[i] . h_r
@@ -113,68 +113,63 @@ __global__ void __launch_bounds__(kThreads, 2) moe_swiglu_kernel(const MoeGemvAr
     const LaneConst L = lane_const(c);
     pdl_launch_dependents();
     pdl_wait();
-    for (int r = blockIdx.y; r < a.n_pairs; r += gridDim.y) {
-        const int2 ex = find_expert(a, r, &found);
-        if (ex.x < 0) {
-            __syncthreads();
-            continue;
+    const int r = blockIdx.y;
+    const int2 ex = find_expert(a, r, &found);
+    if (ex.x < 0) return;
+    const int m = min(kTokens, ex.y - r);
+    int src[kTokens];  // the rows of x
+#pragma unroll
+    for (int t = 0; t < kTokens; ++t) {
+        int s = r + min(t, m - 1);
+        if (a.rows) {
+            const int pair = a.rows[s];
+            if (pair < 0 || pair >= a.n_pairs) {
+                if (tid == 0) set_error(a.err, DEV_BAD_LENGTH);
+                s = 0;
+            } else {
+                s = pair / a.top_k;
+            }
         }
-        const int m = min(kTokens, ex.y - r);
-        int src[kTokens];  // the rows of x
+        src[t] = s;
+    }
+    const int64_t wbase = static_cast<int64_t>(ex.x) * a.out_dim;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        // a warp's outputs 4 warp .. + 3, gate and up of two of them at once
+        const int o0 = 4 * warp + 2 * pass;
+        const uint8_t *wr[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int64_t o = min(static_cast<int64_t>(blockIdx.x) * kTile + o0 + (k >> 1), a.out_dim - 1);
+            wr[k] = (k & 1 ? a.w2 : a.w1) + (wbase + o) * nsb * 144;
+        }
+        float acc[kRows][kTokens] = {};
+        dot_rows(a, wr, src, m, sub, c, L, acc);
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
-            int s = r + min(t, m - 1);
-            if (a.rows) {
-                const int pair = a.rows[s];
-                if (pair < 0 || pair >= a.n_pairs) {
-                    if (tid == 0) set_error(a.err, DEV_BAD_LENGTH);
-                    s = 0;
-                } else {
-                    s = pair / a.top_k;
-                }
-            }
-            src[t] = s;
-        }
-        const int64_t wbase = static_cast<int64_t>(ex.x) * a.out_dim;
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-            // a warp's outputs 4 warp .. + 3, gate and up of two of them at once
-            const int o0 = 4 * warp + 2 * pass;
-            const uint8_t *wr[kRows];
+            if (t >= m) break;
 #pragma unroll
-            for (int k = 0; k < kRows; ++k) {
-                const int64_t o = min(static_cast<int64_t>(blockIdx.x) * kTile + o0 + (k >> 1), a.out_dim - 1);
-                wr[k] = (k & 1 ? a.w2 : a.w1) + (wbase + o) * nsb * 144;
-            }
-            float acc[kRows][kTokens] = {};
-            dot_rows(a, wr, src, m, sub, c, L, acc);
-#pragma unroll
-            for (int t = 0; t < kTokens; ++t) {
-                if (t >= m) break;
-#pragma unroll
-                for (int k = 0; k < kRows; ++k) acc[k][t] = warp_sum(acc[k][t]);
-                if (lane < 2) {
-                    const float g = lane ? acc[2][t] : acc[0][t], u = lane ? acc[3][t] : acc[1][t];
-                    out[t][o0 + lane] = g / (1.0f + expf(-g)) * u;
-                }
+            for (int k = 0; k < kRows; ++k) acc[k][t] = warp_sum(acc[k][t]);
+            if (lane < 2) {
+                const float g = lane ? acc[2][t] : acc[0][t], u = lane ? acc[3][t] : acc[1][t];
+                out[t][o0 + lane] = g / (1.0f + expf(-g)) * u;
             }
         }
-        __syncthreads();
-        if (warp < m) {
-            const int64_t o = static_cast<int64_t>(blockIdx.x) * kTile + lane, at = static_cast<int64_t>(r + warp) * a.out_dim + o;
-            const float v = o < a.out_dim ? out[warp][lane] : 0.0f;
-            if (a.y && o < a.out_dim) a.y[at] = v;
-            if (a.yq) {  // out_dim is a multiple of 32
-                const float d = __fdiv_rn(warp_max(fabsf(v)), 127.0f);
-                const int code = q8_code(v, q8_scale(d)), total = warp_sum_int(code);
-                a.yq[at] = static_cast<int8_t>(code);
-                if (lane == 0) {
-                    a.yd[at / 32] = d;
-                    a.ys[at / 32] = __fmul_rn(d, static_cast<float>(total));
-                }
+    }
+    __syncthreads();
+    if (warp < m) {
+        const int64_t o = static_cast<int64_t>(blockIdx.x) * kTile + lane, at = static_cast<int64_t>(r + warp) * a.out_dim + o;
+        const float v = o < a.out_dim ? out[warp][lane] : 0.0f;
+        if (a.y && o < a.out_dim) a.y[at] = v;
+        if (a.yq) {  // out_dim is a multiple of 32
+            const float d = __fdiv_rn(warp_max(fabsf(v)), 127.0f);
+            const int code = q8_code(v, q8_scale(d)), total = warp_sum_int(code);
+            a.yq[at] = static_cast<int8_t>(code);
+            if (lane == 0) {
+                a.yd[at / 32] = d;
+                a.ys[at / 32] = __fmul_rn(d, static_cast<float>(total));
             }
         }
-        __syncthreads();
     }
 }
 
@@ -189,8 +184,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_tokens_kernel(const MoeG
     const LaneConst L = lane_const(c);
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t t = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
-    if (t * a.top_k >= a.n_pairs) return;
+    const int64_t t = blockIdx.y;
     const int64_t o0 = static_cast<int64_t>(blockIdx.x) * 4 * quads;
     for (int u = warp; u < a.top_k * quads; u += kThreads / 32) {
         const int j = u / quads, q = u - j * quads;
@@ -284,7 +278,7 @@ cudaError_t launch(K kernel, dim3 grid, const A &a, cudaStream_t s)
 
 cudaError_t launch_moe_swiglu(const MoeGemvArgs &a, cudaStream_t s)
 {
-    const dim3 grid(static_cast<unsigned>((a.out_dim + kTile - 1) / kTile), static_cast<unsigned>(std::min<int64_t>(a.n_pairs, 65535)));
+    const dim3 grid(static_cast<unsigned>((a.out_dim + kTile - 1) / kTile), static_cast<unsigned>(a.n_pairs));  // fewer than 2 kMoeMaxExperts
     return launch(moe_swiglu_kernel, grid, a, s);
 }
 
@@ -292,8 +286,7 @@ cudaError_t launch_moe_down_tokens(const MoeGemvArgs &a, const MoeCombineArgs &b
 {
     const int quads = a.top_k >= 8 ? 1 : 8 / a.top_k;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.out_dim + 4 * quads - 1) / (4 * quads)), static_cast<unsigned>(std::min<int64_t>(n_tokens, 65535)),
-                       static_cast<unsigned>((n_tokens + 65534) / 65535));
+    cfg.gridDim = dim3(static_cast<unsigned>((a.out_dim + 4 * quads - 1) / (4 * quads)), static_cast<unsigned>(n_tokens));  // fewer than 2 kMoeMaxExperts
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

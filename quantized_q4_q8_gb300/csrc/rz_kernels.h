@@ -40,6 +40,8 @@ extern uint32_t g_stall_next_gemv;
 // The same for the next call of the paged attention: its kernels leave the first unit of tokens (128 in the tcgen05
 // kernel) of CTA 0 uncopied.  The polls bound the waits of the first kernel's CTA 0; the other's are bounded as ever.
 extern uint32_t g_stall_next_paged;
+// The same for the next grouped product on the tensor cores: its CTA 0 leaves the first tile of weights uncopied.
+extern uint32_t g_stall_next_moe;
 
 // Launch with the programmatic-stream-serialization attribute (PDL) so that the
 // kernel's weight prefetch overlaps the tail of the previous kernel in the stream.

@@ -13,6 +13,7 @@ __all__ = [
     "rz_q4k_f32_gemv", "q4k_f32_gemv",
     "rz_q4k_q8_gemm", "q4k_q8_gemm_workspace_bytes", "q4k_q8_gemm",
     "rz_rmsnorm", "rz_residual_add", "rz_check_device_error", "rz_set_pdl", "rz_debug_stall_next_gemv", "rz_debug_stall_next_paged",
+    "rz_debug_stall_next_moe",
     "q8_1_quantize", "q4k_q8_gemv", "q4k_q8_subblock_dots", "q4_0_gemv",
     "rmsnorm", "residual_add", "check_device_error", "set_pdl", "version",
     "DeviceLayer", "DeviceKV", "DeviceStack", "workspace", "swiglu_ffn_workspace_bytes",
@@ -151,6 +152,11 @@ def rz_debug_stall_next_gemv(wait_limit: int):
 def rz_debug_stall_next_paged(wait_limit: int):
     """Test aid: the next paged attention runs out of a bounded wait (see rz.h)."""
     return call("rz_debug_stall_next_paged", int(wait_limit))
+
+
+def rz_debug_stall_next_moe(wait_limit: int):
+    """Test aid: the next grouped product on the tensor cores runs out of a bounded wait (see rz.h)."""
+    return call("rz_debug_stall_next_moe", int(wait_limit))
 
 
 # ------------------------------------------------------------------ tensor helpers

@@ -475,3 +475,28 @@ def test_block_in_a_graph_and_on_another_stream(rz):
         got = b.run(ins[1][0], ins[1][1], seqs[1])
     side.synchronize()
     assert torch.equal(got, eager[1])
+
+
+@pytest.mark.parametrize("T,E", [(12, 4), (60, 4), (300, 2)])
+def test_wait_that_runs_out(rz, T, E):
+    """The first weights of CTA 0 are left uncopied: the product reports it, ends, and the next is as before."""
+    rng = np.random.default_rng(T)
+    k, out_dim, in_dim = 2, 384, 1024
+    plan, _ = make_plan(rz, rng, T, E, k, idle=0.0)
+    w, x = dev(q4k(rng, E, out_dim, in_dim=in_dim)), dev(R.q8_buffer(*activations(rng, T, in_dim)))
+    want = rz.moe_swiglu(w, w, x, plan, out_dim, in_dim)
+    assert rz.check_device_error() == (0, 0)
+    rz.rz_debug_stall_next_moe(1 << 12)
+    got = rz.moe_swiglu(w, w, x, plan, out_dim, in_dim)
+    assert rz.check_device_error() == (5, 0x120)
+    # the first item is the first expert's first tile; other CTAs' outputs are whole
+    assert torch.equal(got[:, 128:], want[:, 128:])
+    for _ in range(3):
+        assert torch.equal(rz.moe_swiglu(w, w, x, plan, out_dim, in_dim), want)
+    assert rz.check_device_error() == (0, 0)
+
+
+def test_stall_limit_is_checked_on_the_host(rz):
+    from quantized_q4_q8_gb300 import _lib
+    assert _lib.status("rz_debug_stall_next_moe", 10) == 1
+    assert _lib.status("rz_debug_stall_next_moe", 1 << 30) == 1
