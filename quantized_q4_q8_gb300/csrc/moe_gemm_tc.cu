@@ -796,9 +796,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             const int m = w.m - col0;
             int64_t to = static_cast<int64_t>(w.row + col0) * g.out_dim + o;
             if constexpr (kSwiglu) {
-                // in place first: half of the registers are free for what follows
+                // In place first: half of the registers are free for what follows.  __expf is within 2 + 1.2 |g| ulp: 3% of the time less than
+                // expf at 4096 rows of 4096 > 14336, as this runs while no product does.
 #pragma unroll
-                for (int i = 0; i < C::kHalf; ++i) sum[0][i] = in ? __fdividef(sum[0][i], 1.0f + expf(-sum[0][i])) * sum[1][i] : 0.0f;
+                for (int i = 0; i < C::kHalf; ++i) sum[0][i] = in ? __fdividef(sum[0][i], 1.0f + __expf(-sum[0][i])) * sum[1][i] : 0.0f;
                 if (g.y && in) {
                     float *y = g.y + to;
 #pragma unroll

@@ -110,8 +110,9 @@ def swiglu(gate, up, x, rows, expert, k):
         with np.errstate(over="ignore"):
             silu = g / (1 + np.exp(-g))
         h[r] = silu * u
-        # |silu'| < 1.1; exp within 2 ulp, an addition, a division, a product: 8 half-ulps of h
-        tol[r] = 1.1 * dg * np.abs(u) + np.abs(silu) * du + 1.1 * dg * du + 8 * 2.0 ** -24 * np.abs(h[r]) + 1e-37
+        # |silu'| < 1.1; then, in half-ulps of h (2^-24): e^-g within 3 + 1.173 |g| ulp, which 1 + e^-g does not make larger (twice that in
+        # half-ulps), an addition (1), a division within 2 ulp (4), a product (1)
+        tol[r] = 1.1 * dg * np.abs(u) + np.abs(silu) * du + 1.1 * dg * du + (12 + 2.4 * np.abs(g)) * 2.0 ** -24 * np.abs(h[r]) + 1e-37
     return h, tol
 
 
