@@ -39,6 +39,7 @@
 // Every wait is bounded; after one that runs out every role stops, copies and products in flight
 // are waited for, and tensor memory is freed.
 #include <math.h>
+#include <stddef.h>
 
 #include <algorithm>
 
@@ -136,11 +137,11 @@ __device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a,
         "r"(a), "r"(b_low), "r"(b_high), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(elected)
         : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t elected, uint64_t *bar)
+__device__ __forceinline__ void commit(uint32_t elected, uint32_t bar)
 {
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
         "r"(elected)
         : "memory");
 }
@@ -229,36 +230,77 @@ __device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32
 {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+__device__ __forceinline__ int lds1i(uint32_t at)
+{
+    int v;
+    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ void sts1(uint32_t at, uint32_t x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory"); }
 
-// Bounded waits; false after a timeout or when another role gave up.
-__device__ __forceinline__ bool give_up(Bars &b, unsigned *err)
+// Barriers by 32-bit address too.
+#define RZ_BAR(field) (bars + static_cast<uint32_t>(offsetof(Bars, field)))
+__device__ __forceinline__ bool try_phase(uint32_t bar, unsigned par)
 {
-    volatile int *flag = &b.gave_up;
-    if (!*flag) {
-        *flag = 1;
-        set_error(err, DEV_TIMEOUT_MOE);
-    }
-    return false;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(par)
+        : "memory");
+    return ok != 0;
 }
-__device__ __forceinline__ bool wait_one(uint64_t *bar, unsigned par, Bars &b, unsigned *err)
+__device__ __forceinline__ void arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
 {
-    volatile int *flag = &b.gave_up;
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t pol)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(pol)
+        : "memory");
+}
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ bool gave_up(uint32_t bars) { return lds1i(RZ_BAR(gave_up)) != 0; }
+
+// Bounded waits; false after a timeout or when another role gave up.
+__device__ __forceinline__ bool wait_one(uint32_t bar, unsigned par, uint32_t bars, unsigned *err)
+{
     for (uint32_t i = 0;; ++i) {
-        if (mbar_try_wait(bar, par)) return true;
+        if (try_phase(bar, par)) return true;
         if ((i & 63u) == 63u) {
-            if (*flag) return false;
-            if (i >= b.limit) return give_up(b, err);
+            if (gave_up(bars)) return false;
+            if (i >= static_cast<uint32_t>(lds1i(RZ_BAR(limit)))) {
+                sts1(RZ_BAR(gave_up), 1);
+                set_error(err, DEV_TIMEOUT_MOE);
+                return false;
+            }
         }
     }
 }
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned par, Bars &b, unsigned *err)
+__device__ __forceinline__ bool wait_warp(uint32_t bar, unsigned par, uint32_t bars, unsigned *err)
 {
     // All lanes wait for the same barrier: lanes that wait for different ones drift apart, and what follows (tcgen05.ld, products
     // issued for the warp) needs the warp together.
-    const bool ok = __all_sync(0xffffffffu, wait_one(bar, par, b, err));
+    const bool ok = __all_sync(0xffffffffu, wait_one(bar, par, bars, err));
     __syncwarp();
     return ok;
+}
+// A copy that is under way lands.
+__device__ __forceinline__ void wait_landed(uint32_t bar, unsigned par)
+{
+    for (uint32_t i = 0; i < kWaitLimit && !try_phase(bar, par); ++i) {
+    }
 }
 
 // A super-block's two scales; wide: the mins' is the unit (see above).
@@ -288,7 +330,7 @@ __host__ __device__ constexpr int64_t max_tiles(int64_t n_pairs, int n_experts)
 }
 
 // Whether a phase is complete, at once.
-__device__ __forceinline__ bool test_phase(uint64_t *bar, unsigned par)
+__device__ __forceinline__ bool test_phase(uint32_t bar, unsigned par)
 {
     uint32_t ok;
     asm volatile(
@@ -296,7 +338,7 @@ __device__ __forceinline__ bool test_phase(uint64_t *bar, unsigned par)
         "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(par)
+        : "r"(bar), "r"(par)
         : "memory");
     return ok != 0;
 }
@@ -439,21 +481,41 @@ __global__ void __launch_bounds__(kPackThreads) moe_pack_kernel(const MoeGemvArg
     }
 }
 
-// Ring position `by` further.
-__device__ __forceinline__ void ring_add(RingPos &p, int by, int n)
-{
-    p.s += by;
-    if (p.s >= n) {
-        p.s -= n;
-        p.par ^= 1u;
+// A place in a ring of R slots and the parity of its phase.  kFew, where registers are short (tiles of 128 rows): one counter where
+// R is a power of two.  With barriers by 32-bit address 3198 to 3002 us (gate and up, 4096 tokens, 8 experts of 14336 x 4096, top 2);
+// tiles of 16 rows would lose 2% by the counter.
+template <int R, bool kFew>
+struct Ring {
+    static constexpr bool kCount = kFew && (R & (R - 1)) == 0;
+    unsigned n, phase;
+    __device__ __forceinline__ explicit Ring(int first) : n(first), phase(0) {}
+    __device__ __forceinline__ unsigned slot() const { return kCount ? n & (R - 1) : n; }
+    __device__ __forceinline__ unsigned par() const { return kCount ? (n / R) & 1u : phase; }
+    __device__ __forceinline__ void add(unsigned by)
+    {
+        n += by;
+        if (!kCount && n >= R) {
+            n -= R;
+            phase ^= 1u;
+        }
     }
-}
+};
 
 // Two low codes, v = 1024 + q: sc q = v sc - 1024 sc, or centred sc (q - 8) = (v - 1032) sc (1032 sc is not exact in f16)
 template <bool kPlain>
 __device__ __forceinline__ uint32_t low_codes(uint32_t v, uint32_t sc, uint32_t add)
 {
     return kPlain ? hfma2u(v, sc, add) : hmul2u(hsub2u(v, 0x64086408u), sc);
+}
+
+// Codes of the row at `raw` in the unit of its mins, where that is the unit.
+__device__ __forceinline__ float shrink_of(uint32_t raw) { return head_of(lds4(raw).x).shrink(); }
+__device__ __forceinline__ void shrink8(uint32_t (&o)[8], uint32_t raw)
+{
+    const float f = shrink_of(raw);
+    const uint32_t by = pack2(f, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = hmul2u(o[i], by);
 }
 
 template <int N, bool kSwiglu>
@@ -464,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
     Bars &b = *reinterpret_cast<Bars *>(sm + C::off_bars);
     int *cum = reinterpret_cast<int *>(sm + C::off_cum);
-    const uint32_t sm32 = smem_u32(sm);
+    const uint32_t sm32 = smem_u32(sm), bars = sm32 + C::off_bars;
     const MoeGemvArgs &g = a.g;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int nsb = g.in_dim / 256;
@@ -521,26 +583,34 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             // -------------------------------------------------------- products of matrix `warp`
             const int mt = warp;
             const uint32_t elected = elect();
-            RingPos pa{0, 0}, pagain{0, 0}, pb{0, 0}, pd{mt, 0};
+            Ring<C::kSlotsA, N == 128> pa(0);
+            Ring<C::kRingB, N == 128> pb(0);
+            Ring<C::kBufD, N == 128> pd(mt);
             bool ok = true;
             for (int64_t k = 0; k < blocks && ok; ++k) {
-#pragma unroll
+                const uint32_t d = tmem + pd.slot() * C::kColsD;
+                const Ring<C::kSlotsA, N == 128> first = pa;
+#pragma unroll (C::kStack ? 4 : 1)
                 for (int entry = 0; entry < C::kEntries; ++entry) {
                     // of A: the next slot, but for the high pieces, which go over the chunks' slots again
                     const bool again = !C::kStack && entry > 4, last = entry == C::kEntries - 1;
-                    RingPos &slot = again ? pagain : pa;
+                    Ring<C::kSlotsA, N == 128> at = pa;
+                    if (again) {
+                        at = first;
+                        at.add(entry - 4);
+                    }
                     // the phases tested together, one latency; what is not complete is waited for
-                    const bool ra = again || test_phase(&b.a_full[mt][pa.s], pa.par), rb = test_phase(&b.b_full[pb.s], pb.par);
-                    const bool rd = entry > 0 || test_phase(&b.d_empty[pd.s], pd.par ^ 1u);
+                    const bool ra = again || test_phase(RZ_BAR(a_full) + 32 * mt + 8 * at.slot(), at.par());
+                    const bool rb = test_phase(RZ_BAR(b_full) + 8 * pb.slot(), pb.par());
+                    const bool rd = entry > 0 || test_phase(RZ_BAR(d_empty) + 8 * pd.slot(), pd.par() ^ 1u);
                     if (!__all_sync(0xffffffffu, ra && rb && rd)) {
-                        if (entry == 0 && !(ok = wait_warp(&b.d_empty[pd.s], pd.par ^ 1u, b, g.err))) break;
-                        if (!(ok = wait_warp(&b.b_full[pb.s], pb.par, b, g.err))) break;
-                        if (!again && !(ok = wait_warp(&b.a_full[mt][pa.s], pa.par, b, g.err))) break;
+                        if (entry == 0 && !(ok = wait_warp(RZ_BAR(d_empty) + 8 * pd.slot(), pd.par() ^ 1u, bars, g.err))) break;
+                        if (!(ok = wait_warp(RZ_BAR(b_full) + 8 * pb.slot(), pb.par(), bars, g.err))) break;
+                        if (!again && !(ok = wait_warp(RZ_BAR(a_full) + 32 * mt + 8 * at.slot(), at.par(), bars, g.err))) break;
                     }
                     fence_after();
-                    const uint32_t d = tmem + pd.s * C::kColsD;
-                    const uint32_t ta = tmem + C::kColA + (mt * C::kSlotsA + slot.s) * C::kWidthA;
-                    const uint32_t tb = operand_low(sm32 + C::off_b + pb.s * C::kSlotB);
+                    const uint32_t ta = tmem + C::kColA + (mt * C::kSlotsA + at.slot()) * C::kWidthA;
+                    const uint32_t tb = operand_low(sm32 + C::off_b + pb.slot() * C::kSlotB);
                     if constexpr (C::kStack) {
                         // the mins early: the codes' sums cancel against them as they grow
                         mma_ts(elected, d, ta, tb, operand_high(2048), idesc_f16(2 * N), entry > 0);
@@ -554,17 +624,16 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
 #pragma unroll
                         for (int i = 0; i < 4; ++i) mma_ts(elected, d, ta + 8 * i, tb + 16 * i, operand_high(1024), idesc_f16(N), true);
                     }
-                    if (C::kStack || entry == 0 || again) commit(elected, &b.a_empty[mt][slot.s]);
-                    commit(elected, &b.b_empty[pb.s]);
-                    if (last) commit(elected, &b.d_full[pd.s]);
-                    ring_next(slot, C::kSlotsA);
-                    if (!C::kStack && entry == 0) pagain = pa;
-                    ring_next(pb, C::kRingB);
+                    if (C::kStack || entry == 0 || again) commit(elected, RZ_BAR(a_empty) + 32 * mt + 8 * at.slot());
+                    commit(elected, RZ_BAR(b_empty) + 8 * pb.slot());
+                    if (last) commit(elected, RZ_BAR(d_full) + 8 * pd.slot());
+                    if (!again) pa.add(1);
+                    pb.add(1);
                 }
-                ring_add(pd, 2, C::kBufD);
+                pd.add(2);
             }
-            commit(elected, &b.done[mt]);  // every product issued has completed once this arrives
-            mbar_wait(&b.done[mt], 0);
+            commit(elected, RZ_BAR(done) + 8 * mt);  // every product issued has completed once this arrives
+            wait_landed(RZ_BAR(done) + 8 * mt, 0);
         } else if (lane == 0) {
             // -------------------------------------------------------- copies: warp 2 B and the columns' exponents, warp 3 the raw weights
             const uint64_t pol = l2_evict_first_policy();
@@ -585,11 +654,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     const int y0 = static_cast<int>(e * g.out_dim + static_cast<int64_t>(rt) * (kSwiglu ? 128 : 256));
                     for (int sb = 0; sb < nsb && ok; ++sb) {
                         for (int mt = 0; mt < 2; ++mt) {
-                            if (!(ok = wait_one(&b.raw_empty[p.s], p.par ^ 1u, b, g.err))) break;
+                            if (!(ok = wait_one(RZ_BAR(raw_empty) + 8 * p.s, p.par ^ 1u, bars, g.err))) break;
                             if (!stalled || issued > 0) {
-                                mbar_arrive_expect_tx(&b.raw_full[p.s], kRawBytes);
-                                tma_load_2d(sm + C::off_raw + p.s * kRawBytes, kSwiglu && mt ? &a.map2 : &a.map1, sb * 144,
-                                            y0 + (kSwiglu ? 0 : 128 * mt), &b.raw_full[p.s], pol);
+                                expect_tx(RZ_BAR(raw_full) + 8 * p.s, kRawBytes);
+                                copy_box(sm32 + C::off_raw + p.s * kRawBytes, kSwiglu && mt ? &a.map2 : &a.map1, sb * 144,
+                                         y0 + (kSwiglu ? 0 : 128 * mt), RZ_BAR(raw_full) + 8 * p.s, pol);
                             }
                             ++issued;
                             ring_next(p, C::kRingRaw);
@@ -600,17 +669,17 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     for (int sb = 0; sb < nsb && ok; ++sb) {
                         const uint8_t *from = a.pack + (cell0 + sb) * C::kCellB;
                         for (int entry = 0; entry < C::kEntries; ++entry) {
-                            if (!(ok = wait_one(&b.b_empty[p.s], p.par ^ 1u, b, g.err))) break;
+                            if (!(ok = wait_one(RZ_BAR(b_empty) + 8 * p.s, p.par ^ 1u, bars, g.err))) break;
                             const uint32_t bytes = C::kStack ? C::kSlotB : entry == 0 ? C::kMinsB : C::kBytesB;
-                            mbar_arrive_expect_tx(&b.b_full[p.s], bytes);
-                            bulk_g2s(sm + C::off_b + p.s * C::kSlotB, from, bytes, &b.b_full[p.s]);
+                            expect_tx(RZ_BAR(b_full) + 8 * p.s, bytes);
+                            copy_bulk(sm32 + C::off_b + p.s * C::kSlotB, from, bytes, RZ_BAR(b_full) + 8 * p.s);
                             from += bytes;
                             ++issued;
                             ring_next(p, C::kRingB);
                         }
                         if (!ok) break;
-                        mbar_arrive_expect_tx(&b.cs_full[ph.s], N * 4);
-                        bulk_g2s(sm + C::off_cs + ph.s * N * 4, a.col_scale + (cell0 + sb) * N, N * 4, &b.cs_full[ph.s]);
+                        expect_tx(RZ_BAR(cs_full) + 8 * ph.s, N * 4);
+                        copy_bulk(sm32 + C::off_cs + ph.s * N * 4, a.col_scale + (cell0 + sb) * N, N * 4, RZ_BAR(cs_full) + 8 * ph.s);
                         ++issued_h;
                         ring_next(ph, kHdr);
                     }
@@ -620,11 +689,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             const int ring = weights ? C::kRingRaw : C::kRingB;
             for (int64_t k = max(static_cast<int64_t>(stalled), issued - ring); k < issued; ++k) {
                 const RingPos q = ring_pos(k, ring);
-                mbar_wait(weights ? &b.raw_full[q.s] : &b.b_full[q.s], q.par);
+                wait_landed(weights ? RZ_BAR(raw_full) + 8 * q.s : RZ_BAR(b_full) + 8 * q.s, q.par);
             }
             for (int64_t k = max(static_cast<int64_t>(0), issued_h - kHdr); k < issued_h; ++k) {
                 const RingPos q = ring_pos(k, kHdr);
-                mbar_wait(&b.cs_full[q.s], q.par);
+                wait_landed(RZ_BAR(cs_full) + 8 * q.s, q.par);
             }
         }
     } else if (warp < C::kFirstSum) {
@@ -633,13 +702,14 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         // group: matrix, and which of its steps
         const int cw = warp - C::kFirstUnpack, wrow = 32 * (cw & 3) + lane, mt = (cw >> 2) & 1, turn = cw >> 3;
         const uint32_t ta0 = tmem + (static_cast<uint32_t>(32 * (cw & 3)) << 16) + C::kColA + mt * C::kSlotsA * C::kWidthA;
-        RingPos praw{mt, 0};
-        RingPos pa{turn, 0};
-        int h = 0, use = turn;  // this group's slots are every other one, over the super-blocks' ends
+        Ring<C::kRingRaw, N == 128> praw(mt);
+        Ring<C::kSlotsA, N == 128> pa(turn);
+        Ring<kHdr, N == 128> ph(0);
+        int use = turn;  // this group's slots are every other one, over the super-blocks' ends
         bool ok = true;
         for (int64_t k = 0; k < blocks && ok; ++k) {
-            if (!(ok = wait_warp(&b.raw_full[praw.s], praw.par, b, g.err))) break;
-            const uint32_t raw = sm32 + C::off_raw + praw.s * kRawBytes + wrow * 144;
+            if (!(ok = wait_warp(RZ_BAR(raw_full) + 8 * praw.slot(), praw.par(), bars, g.err))) break;
+            const uint32_t raw = sm32 + C::off_raw + praw.slot() * kRawBytes + wrow * 144;
             uint32_t sc0, sc1;  // six-bit scales, four to a word: sub-blocks 0-3 and 4-7
             bool any_wide;
             {
@@ -651,9 +721,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
 #pragma unroll 1
             for (; use < C::kUses; use += 2) {
                 const bool mins = !C::kStack && use == 0;  // the mins alone
-                if (!(ok = wait_warp(&b.a_empty[mt][pa.s], pa.par ^ 1u, b, g.err))) break;
+                if (!(ok = wait_warp(RZ_BAR(a_empty) + 32 * mt + 8 * pa.slot(), pa.par() ^ 1u, bars, g.err))) break;
                 fence_after();
-                const uint32_t ta = ta0 + pa.s * C::kWidthA;
+                const uint32_t ta = ta0 + pa.slot() * C::kWidthA;
                 if (!mins) {
 #pragma unroll
                     for (int cc = 0; cc < C::kChunks; ++cc) {
@@ -678,13 +748,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                                 hi[2 * i + 1] = hfma2u(lop_and_or(w8, 0x00f000f0u, 0x64006400u), mul1, add1);
                             }
                             if (any_wide) {
-                                const Head head = head_of(lds4(raw).x);
-                                const uint32_t shrink = pack2(head.shrink(), head.shrink());
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    lo[i] = hmul2u(lo[i], shrink);
-                                    hi[i] = hmul2u(hi[i], shrink);
-                                }
+                                shrink8(lo, raw);
+                                shrink8(hi, raw);
                             }
                             tm_store8(ta + 32 * cc + 8 * half, lo);
                             tm_store8(ta + 32 * cc + 16 + 8 * half, hi);
@@ -719,29 +784,30 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         tm_store8(ta + 8, lo);
                     }
                     if (!C::kStack || use == 1)
-                        sts1(sm32 + C::off_g + 4 * ((h * 2 + mt) * 128 + wrow), __float_as_uint(!head.fine ? NAN : head.wide ? head.dmin : head.d));
+                        sts1(sm32 + C::off_g + 4 * ((ph.slot() * 2 + mt) * 128 + wrow), __float_as_uint(!head.fine ? NAN : head.wide ? head.dmin : head.d));
                 }
                 tm_store_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&b.a_full[mt][pa.s]);
-                    if (C::kStack ? use == 1 : mins) mbar_arrive(&b.h_full[h]);
+                    arrive(RZ_BAR(a_full) + 32 * mt + 8 * pa.slot());
+                    if (C::kStack ? use == 1 : mins) arrive(RZ_BAR(h_full) + 8 * ph.slot());
                 }
-                ring_add(pa, 2, C::kSlotsA);
+                pa.add(2);
             }
             if (!ok) break;
-            if (lane == 0) mbar_arrive(&b.raw_empty[praw.s]);
+            if (lane == 0) arrive(RZ_BAR(raw_empty) + 8 * praw.slot());
             use -= C::kUses;
-            h = (h + 1) % kHdr;
-            ring_add(praw, 2, C::kRingRaw);
+            ph.add(1);
+            praw.add(2);
         }
     } else {
         // ------------------------------------------------------------ sums
         if constexpr (C::kRegsSum) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSum ? C::kRegsSum : 24));
         const int dw = warp - C::kFirstSum, col0 = (dw >> 2) * C::kHalf, wrow = 32 * (dw & 3) + lane;
         const uint32_t at = tmem + (static_cast<uint32_t>(32 * (dw & 3)) << 16) + col0;
-        RingPos pd{0, 0}, ph{0, 0};
+        Ring<C::kBufD, N == 128> pd(0);
+        Ring<kHdr, N == 128> ph(0);
         bool ok = true;
         for (int item = 0; item < my_items && ok; ++item) {
             float sum[2][C::kHalf];
@@ -750,12 +816,16 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             for (int sb = 0; sb < nsb && ok; ++sb) {
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
-                    if (mt == 0 && !(ok = wait_warp(&b.h_full[ph.s], ph.par, b, g.err) && wait_warp(&b.cs_full[ph.s], ph.par, b, g.err))) break;
-                    if (!(ok = wait_warp(&b.d_full[pd.s], pd.par, b, g.err))) break;
+                    if (mt == 0) {
+                        ok = wait_warp(RZ_BAR(h_full) + 8 * ph.slot(), ph.par(), bars, g.err) &&
+                             wait_warp(RZ_BAR(cs_full) + 8 * ph.slot(), ph.par(), bars, g.err);
+                        if (!ok) break;
+                    }
+                    if (!(ok = wait_warp(RZ_BAR(d_full) + 8 * pd.slot(), pd.par(), bars, g.err))) break;
                     fence_after();
-                    const float gs = lds1f(sm32 + C::off_g + 4 * ((ph.s * 2 + mt) * 128 + wrow));
-                    const uint32_t cs = sm32 + C::off_cs + 4 * (ph.s * N + col0);
-                    const uint32_t from = at + pd.s * C::kColsD;
+                    const float gs = lds1f(sm32 + C::off_g + 4 * ((ph.slot() * 2 + mt) * 128 + wrow));
+                    const uint32_t cs = sm32 + C::off_cs + 4 * (ph.slot() * N + col0);
+                    const uint32_t from = at + pd.slot() * C::kColsD;
 #pragma unroll
                     for (int i = 0; i < C::kHalf; i += 8) {
                         float v[16];
@@ -775,12 +845,12 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     }
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&b.d_empty[pd.s]);
-                    ring_next(pd, C::kBufD);
+                    if (lane == 0) arrive(RZ_BAR(d_empty) + 8 * pd.slot());
+                    pd.add(1);
                 }
-                ring_next(ph, kHdr);
+                ph.add(1);
             }
-            if (!ok || *static_cast<volatile int *>(&b.gave_up)) break;
+            if (!ok || gave_up(bars)) break;
             // ---- outputs: a warp's 32 rows lie side by side in each column's row of y
             struct {
                 int row, m, rt;
