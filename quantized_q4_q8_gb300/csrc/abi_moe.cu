@@ -128,12 +128,14 @@ int64_t pack_bytes(int64_t n_pairs, int n_experts, int64_t in_dim)
     return moe_pack_bytes(moe_columns(n_pairs, n_experts), n_pairs, n_experts, in_dim);
 }
 
-// the rows' products, then B
+// the rows' products, in how many parts, then B
+int64_t down_products_bytes(int64_t pairs, int parts, int64_t out_dim) { return align256(parts * pairs * out_dim * 4) + (parts > 1 ? 256 : 0); }
+
 int64_t down_workspace_bytes(int64_t n_tokens, int n_experts, int top_k, int64_t out_dim, int64_t in_dim)
 {
     const int64_t pairs = n_tokens * top_k;
     if (moe_columns(pairs, n_experts) == 0) return 0;
-    return align256(pairs * out_dim * 4) + pack_bytes(pairs, n_experts, in_dim);
+    return down_products_bytes(pairs, moe_max_parts(pairs, n_experts, out_dim, in_dim), out_dim) + pack_bytes(pairs, n_experts, in_dim);
 }
 
 cudaError_t run_swiglu(const MoeGemvArgs &a, void *workspace, cudaStream_t s)
@@ -167,7 +169,10 @@ cudaError_t run_down(const void *w_down, const void *h_q8, const rz_moe_plan *p,
     c.err = a.err;
     const int columns = moe_columns(a.n_pairs, a.n_experts);
     if (columns == 0) return launch_moe_down_tokens(a, c, p->n_tokens, s);
-    const cudaError_t e = launch_moe_gemm_tc(a, columns, static_cast<uint8_t *>(workspace) + align256(a.n_pairs * out_dim * 4), s);
+    a.max_parts = moe_max_parts(a.n_pairs, a.n_experts, out_dim, in_dim);
+    uint8_t *pack = static_cast<uint8_t *>(workspace) + down_products_bytes(a.n_pairs, a.max_parts, out_dim);
+    if (a.max_parts > 1) c.parts = a.parts = reinterpret_cast<int32_t *>(pack - 256);
+    const cudaError_t e = launch_moe_gemm_tc(a, columns, pack, s);
     return e != cudaSuccess ? e : launch_moe_combine(c, p->n_tokens, s);
 }
 

@@ -217,8 +217,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_tokens_kernel(const MoeG
         for (int64_t z = a.out_dim + tid; z < b.out_pad; z += kThreads) b.y[t * b.out_pad + z] = 0.0f;
 }
 
-// y[t] = residual[t] + sum_j w_j o[place_j], zeros behind out_dim; a thread has kVec columns
-template <int kVec>
+// y[t] = residual[t] + sum_j w_j o[place_j], zeros behind out_dim; a thread has kVec columns.  kParts: o is the sum of its parts, in
+// order (a loop of one part for all would cost the large batches their loads side by side: 4095 tokens of 8, 366 to 399 us).
+template <int kVec, bool kParts>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeCombineArgs a)
 {
     pdl_launch_dependents();
@@ -226,6 +227,8 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeCombineArgs a
     const int64_t t = blockIdx.x;
     const int col = (blockIdx.y * 256 + threadIdx.x) * kVec;
     if (col >= a.out_pad) return;
+    const int parts = kParts ? *a.parts : 1;
+    const int64_t part = static_cast<int64_t>(a.n_pairs) * a.out_dim;
     float v[kVec];
     if (col < a.out_dim) {
 #pragma unroll
@@ -240,13 +243,19 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeCombineArgs a
             const float w = a.weights[t * a.top_k + j];
             const float *o = a.o + static_cast<int64_t>(place) * a.out_dim + col;
             if constexpr (kVec == 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4 *>(o));
+                float4 x = __ldg(reinterpret_cast<const float4 *>(o));
+                for (int p = 1; p < parts; ++p) {
+                    const float4 more = __ldg(reinterpret_cast<const float4 *>(o + p * part));
+                    x = make_float4(x.x + more.x, x.y + more.y, x.z + more.z, x.w + more.w);
+                }
                 v[0] = fmaf(w, x.x, v[0]);
                 v[1] = fmaf(w, x.y, v[1]);
                 v[2] = fmaf(w, x.z, v[2]);
                 v[3] = fmaf(w, x.w, v[3]);
             } else {
-                v[0] = fmaf(w, __ldg(o), v[0]);
+                float x = __ldg(o);
+                for (int p = 1; p < parts; ++p) x += __ldg(o + p * part);
+                v[0] = fmaf(w, x, v[0]);
             }
         }
     } else {
@@ -301,7 +310,8 @@ cudaError_t launch_moe_combine(const MoeCombineArgs &a, int64_t n_tokens, cudaSt
 {
     const int vec = a.out_dim % 4 == 0 && a.out_pad % 4 == 0 ? 4 : 1;
     const dim3 grid(static_cast<unsigned>(n_tokens), static_cast<unsigned>((a.out_pad + 256 * vec - 1) / (256 * vec)));
-    return vec == 4 ? launch(moe_combine_kernel<4>, grid, a, s) : launch(moe_combine_kernel<1>, grid, a, s);
+    if (a.parts) return vec == 4 ? launch(moe_combine_kernel<4, true>, grid, a, s) : launch(moe_combine_kernel<1, true>, grid, a, s);
+    return vec == 4 ? launch(moe_combine_kernel<4, false>, grid, a, s) : launch(moe_combine_kernel<1, false>, grid, a, s);
 }
 
 }  // namespace rz

@@ -351,6 +351,8 @@ struct MoeGemvArgs {
     float *yd, *ys;
     int64_t out_dim;
     int in_dim, n_experts, top_k, n_pairs;
+    int max_parts;   // tensor cores, w2 not given: in_dim in up to so many parts, sums of part p at y + p * n_pairs * out_dim
+    int32_t *parts;  // how many it took (not written with max_parts 1)
     unsigned *err;
 };
 cudaError_t launch_moe_swiglu(const MoeGemvArgs &a, cudaStream_t s);  // with integer dots (moe_gemv.cu), w2 given
@@ -360,9 +362,11 @@ cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &a, int columns, void *workspac
 int64_t moe_pack_bytes(int columns, int64_t n_pairs, int n_experts, int64_t in_dim);  // of its workspace
 
 int moe_columns(int64_t n_pairs, int n_experts);  // of the tiles for so many rows of so many experts; 0: integer dots
+int moe_max_parts(int64_t n_pairs, int n_experts, int64_t out_dim, int64_t in_dim);
 
 struct MoeCombineArgs {
-    const float *o;  // [n_pairs][out_dim]
+    const float *o;  // [*parts][n_pairs][out_dim]
+    const int32_t *parts;  // or nullptr: 1
     const int32_t *experts, *places;
     const float *weights, *residual;
     float *y;        // [n_tokens][out_pad]

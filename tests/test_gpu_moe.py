@@ -271,6 +271,35 @@ def test_down(rz, T, E, k, out_dim, in_dim):
     within(none, ref0, tol0, "y without a residual")
 
 
+PARTS = [  # few tiles and a long in_dim: 4 to 19 super-blocks, in parts of equal and unequal lengths
+    (9, 4, 2, 300, 1024), (33, 8, 2, 1000, 4864), (65, 16, 4, 130, 2304), (60, 2, 1, 257, 2816), (200, 1, 1, 700, 2560), (130, 1, 1, 1, 1280),
+    (12, 4, 1, 2049, 1792),
+]
+
+
+@pytest.mark.parametrize("T,E,k,out_dim,in_dim", PARTS)
+def test_down_in_parts(rz, T, E, k, out_dim, in_dim):
+    test_down(rz, T, E, k, out_dim, in_dim)
+
+
+def test_down_parts_workspace(rz):
+    """Nothing behind the workspace is written, nothing of an earlier call is read, and every call gives the same bits."""
+    rng = np.random.default_rng(77)
+    T, E, k, out_dim, in_dim = 33, 8, 2, 1000, 4864
+    plan, _ = make_plan(rz, rng, T, E, k)
+    args = (dev(q4k(rng, E, out_dim, in_dim=in_dim, spread=1.0)), dev(R.q8_buffer(*activations(rng, T * k, in_dim, 2.0))), plan, out_dim, in_dim)
+    size = rz.moe_down_workspace_bytes(T, E, k, out_dim, in_dim)
+    room = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+    first = rz.moe_down(*args, ws=room[:size])
+    for fill in (0, 127, 255):
+        room.fill_(fill)
+        assert torch.equal(rz.moe_down(*args, ws=room[:size]), first)
+        assert torch.all(room[size:] == fill)
+    res = torch.randn(T, out_dim, device="cuda")
+    rz.moe_route(torch.zeros(T, E, device="cuda"), plan, row_seq=torch.full((T,), -1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(rz.moe_down(*args, residual=res, ws=room[:size]), res)  # no row at all
+
+
 @pytest.mark.parametrize("T", [3, 90])
 def test_products_of_extreme_blocks(rz, T):
     """Super-blocks without a scale, without a min, with mins far above or below the scale; blocks of x far apart."""
