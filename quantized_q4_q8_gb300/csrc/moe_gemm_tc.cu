@@ -1036,21 +1036,30 @@ cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &g, int columns, void *workspac
     }
 }
 
-// By the rows that an expert has on average (us with integer dots, and in tiles of 16, 32 and 128 rows; gate and up):
-//   2 of 8 experts of 4096 > 14336:  1 row 74, 87, 94;  2 rows 126, 115, 128;  12 rows 632, 168, 152, 365;  40 rows 2081, 378, 270, 371;
-//                                    80 rows -, 693, 447, 453;  128 rows -, 1066, 635, 515
-//   8 of 64 experts of 2048 > 1024:  0.5 rows 21, 33, 36;  2 rows 55, 46, 51;  12 rows 239, 67, 64, 149;  96 rows -, 256, 171, 191;
-//                                    128 rows -, 334, 221, 217
-int moe_columns(int64_t n_pairs, int n_experts)
+// By the rows that an expert has on average (us in a graph; integer dots | tiles of 16 | 32 | 128 rows; experts chosen evenly, and
+// unevenly: logits with a normal part of their own for each expert).
+//   gate and up, 2 of 8 experts of 4096 > 14336
+//      1 row: 111, 98 | 104, 83;      1.5 rows: 142, 140 | 114, 93;      6 rows: - | 136, 135 | 149, 147;      8 rows: 136, 146 | 148, 147
+//      10 rows: 146, 167 | 149, 148;  75 rows: 415, 404 | 378, 490;     100 rows: 506, 520 | 382, 522;        128 rows: 621, 615 | 526, 554
+//   gate and up, 8 of 64 experts of 2048 > 1024 (integer dots: half unevenly)
+//      0.5 rows: 25 | 31;  1 row: 38 | 37;  1.5 rows: 50 | 43;  8 rows: 55, 55 | 63, 49;  12 rows: 56, 66 | 63, 62
+//      80 rows: 149, 149 | 151, 185;  96 rows: 166, 166 | 152, 187;     128 rows: 211, 216 | 199, 222
+//   down, half unevenly
+//      2 of 8, 14336 > 4096:  0.5 rows: 25 | 44;   1 row: 46 | 51;   1.5 rows: 66 | 64;   2 rows: 83 | 64
+//      8 of 64, 1024 > 2048:  0.5 rows: 20 | 25;   1 row: 37 | 28;   2 rows: 70 | 31;   64 rows: 74 | 93;   128 rows: 125 | 133;   512 rows: 436 | 370
+//      4 of 16, 4864 > 896:   1 row: 12 | 23;   2 rows: 18 | 27;   3 rows: 26 | 27
+// Under 2 rows an expert, fewer than 8 rows in all stay with the integer dots: with so few experts each one's weights are read about once.
+int moe_columns(int64_t n_pairs, int n_experts, bool gate_up)
 {
     const int64_t rows = n_pairs / n_experts;
-    return rows < 2 ? 0 : rows <= 10 ? 16 : rows < 96 ? 32 : 128;
+    if (rows < (gate_up ? 1 : 2) || (rows < 2 && n_pairs < 8)) return 0;
+    return rows <= 10 ? 16 : rows < (gate_up ? 96 : 160) ? 32 : 128;
 }
 
 // Parts of in_dim are for products that may come to fewer than two items an SM.
 int moe_max_parts(int64_t n_pairs, int n_experts, int64_t out_dim, int64_t in_dim)
 {
-    const int columns = moe_columns(n_pairs, n_experts);
+    const int columns = moe_columns(n_pairs, n_experts, false);
     if (columns == 0) return 1;
     const int64_t least = (n_pairs + columns - 1) / columns * ((out_dim + 255) / 256);
     return static_cast<int>(std::max<int64_t>(1, std::min({int64_t(8), in_dim / 512, 2 * 152 / least})));

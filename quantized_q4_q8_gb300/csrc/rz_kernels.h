@@ -361,7 +361,7 @@ cudaError_t launch_moe_swiglu(const MoeGemvArgs &a, cudaStream_t s);  // with in
 cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &a, int columns, void *workspace, cudaStream_t s);
 int64_t moe_pack_bytes(int columns, int64_t n_pairs, int n_experts, int64_t in_dim);  // of its workspace
 
-int moe_columns(int64_t n_pairs, int n_experts);  // of the tiles for so many rows of so many experts; 0: integer dots
+int moe_columns(int64_t n_pairs, int n_experts, bool gate_up);  // of the tiles for so many rows of so many experts; 0: integer dots
 int moe_max_parts(int64_t n_pairs, int n_experts, int64_t out_dim, int64_t in_dim);
 
 struct MoeCombineArgs {
