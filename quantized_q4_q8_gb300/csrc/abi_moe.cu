@@ -122,10 +122,10 @@ void swiglu_args(MoeGemvArgs &a, const void *w_gate, const void *w_up, const voi
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// the activations as the tensor-core kernel takes them; the integer kernel needs nothing
-int64_t pack_bytes(int64_t n_pairs, int n_experts, int64_t in_dim, bool gate_up)
+// the activations as the tensor-core kernel takes them, if that can be the one; the integer kernel needs nothing
+int64_t swiglu_pack_bytes(int64_t n_pairs, int n_experts, int64_t in_dim)
 {
-    return moe_pack_bytes(moe_columns(n_pairs, n_experts, gate_up), n_pairs, n_experts, in_dim);
+    return moe_pack_bytes(moe_tiles(n_pairs, n_experts, true), n_pairs, n_experts, in_dim);
 }
 
 // the rows' products, in how many parts, then B
@@ -134,13 +134,14 @@ int64_t down_products_bytes(int64_t pairs, int parts, int64_t out_dim) { return 
 int64_t down_workspace_bytes(int64_t n_tokens, int n_experts, int top_k, int64_t out_dim, int64_t in_dim)
 {
     const int64_t pairs = n_tokens * top_k;
-    if (moe_columns(pairs, n_experts, false) == 0) return 0;
-    return down_products_bytes(pairs, moe_max_parts(pairs, n_experts, out_dim, in_dim), out_dim) + pack_bytes(pairs, n_experts, in_dim, false);
+    const int columns = moe_columns(pairs, n_experts, top_k, out_dim, in_dim, false);
+    if (columns == 0) return 0;
+    return down_products_bytes(pairs, moe_max_parts(columns, pairs, out_dim, in_dim), out_dim) + moe_pack_bytes(columns, pairs, n_experts, in_dim);
 }
 
 cudaError_t run_swiglu(const MoeGemvArgs &a, void *workspace, cudaStream_t s)
 {
-    const int columns = moe_columns(a.n_pairs, a.n_experts, true);
+    const int columns = moe_columns(a.n_pairs, a.n_experts, a.top_k, a.out_dim, a.in_dim, true);
     return columns ? launch_moe_gemm_tc(a, columns, workspace, s) : launch_moe_swiglu(a, s);
 }
 
@@ -167,9 +168,9 @@ cudaError_t run_down(const void *w_down, const void *h_q8, const rz_moe_plan *p,
     c.top_k = p->top_k;
     c.n_pairs = a.n_pairs;
     c.err = a.err;
-    const int columns = moe_columns(a.n_pairs, a.n_experts, false);
+    const int columns = moe_columns(a.n_pairs, a.n_experts, a.top_k, out_dim, in_dim, false);
     if (columns == 0) return launch_moe_down_tokens(a, c, p->n_tokens, s);
-    a.max_parts = moe_max_parts(a.n_pairs, a.n_experts, out_dim, in_dim);
+    a.max_parts = moe_max_parts(columns, a.n_pairs, out_dim, in_dim);
     uint8_t *pack = static_cast<uint8_t *>(workspace) + down_products_bytes(a.n_pairs, a.max_parts, out_dim);
     if (a.max_parts > 1) c.parts = a.parts = reinterpret_cast<int32_t *>(pack - 256);
     const cudaError_t e = launch_moe_gemm_tc(a, columns, pack, s);
@@ -277,7 +278,7 @@ size_t rz_moe_swiglu_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_
     const char *fn = "rz_moe_swiglu_workspace_bytes";
     record_error(RZ_OK, "");
     if (check_counts(fn, n_tokens, n_experts, top_k) != RZ_OK || check_in_dim(fn, in_dim) != RZ_OK) return 0;
-    return pack_bytes(n_tokens * top_k, n_experts, in_dim, true);
+    return swiglu_pack_bytes(n_tokens * top_k, n_experts, in_dim);
 }
 
 rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, const rz_moe_plan *plan, int64_t inter, int64_t in_dim,
@@ -293,7 +294,7 @@ rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, 
     const void *bufs[] = {w_gate, w_up, x_q8, h, h_q8};
     for (const void *p : bufs)
         if (!aligned(p, 16)) return fail(RZ_ERR_ALIGN, "%s: buffers must be 16-byte aligned", fn);
-    RZ_TRY(check_workspace(fn, workspace, ws_bytes, pack_bytes(plan->n_tokens * plan->top_k, plan->n_experts, in_dim, true)));
+    RZ_TRY(check_workspace(fn, workspace, ws_bytes, swiglu_pack_bytes(plan->n_tokens * plan->top_k, plan->n_experts, in_dim)));
     RZ_TRY(ensure_device());
     MoeGemvArgs a{};
     swiglu_args(a, w_gate, w_up, x_q8, plan, inter, in_dim, h, h_q8);
@@ -327,7 +328,7 @@ rz_status rz_moe_down(const void *w_down, const void *h_q8, const rz_moe_plan *p
 static size_t ffn_h_bytes(int64_t n_tokens, int top_k, int64_t inter) { return align256(RZ_Q8_1_BYTES(n_tokens * top_k, inter)); }
 static size_t ffn_workspace_bytes(int64_t n_tokens, int n_experts, int top_k, int64_t hidden, int64_t hidden_pad, int64_t inter)
 {
-    const int64_t parts[] = {moe_route_workspace_bytes(n_tokens, n_experts), pack_bytes(n_tokens * top_k, n_experts, hidden_pad, true),
+    const int64_t parts[] = {moe_route_workspace_bytes(n_tokens, n_experts), swiglu_pack_bytes(n_tokens * top_k, n_experts, hidden_pad),
                              down_workspace_bytes(n_tokens, n_experts, top_k, hidden, inter)};
     return ffn_h_bytes(n_tokens, top_k, inter) + align256(std::max({parts[0], parts[1], parts[2]}));
 }

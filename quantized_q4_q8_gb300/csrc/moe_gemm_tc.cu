@@ -1036,30 +1036,42 @@ cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &g, int columns, void *workspac
     }
 }
 
-// By the rows that an expert has on average (us in a graph; integer dots | tiles of 16 | 32 | 128 rows; experts chosen evenly, and
-// unevenly: logits with a normal part of their own for each expert).
+// Tiles by the rows that an expert has on average (us in a graph, tiles of 16 | 32 | 128 rows; experts chosen evenly, and unevenly: logits
+// with a normal part of their own for each expert).  0: fewer rows than experts, which are for the integer dots.
 //   gate and up, 2 of 8 experts of 4096 > 14336
-//      1 row: 111, 98 | 104, 83;      1.5 rows: 142, 140 | 114, 93;      6 rows: - | 136, 135 | 149, 147;      8 rows: 136, 146 | 148, 147
-//      10 rows: 146, 167 | 149, 148;  75 rows: 415, 404 | 378, 490;     100 rows: 506, 520 | 382, 522;        128 rows: 621, 615 | 526, 554
-//   gate and up, 8 of 64 experts of 2048 > 1024 (integer dots: half unevenly)
-//      0.5 rows: 25 | 31;  1 row: 38 | 37;  1.5 rows: 50 | 43;  8 rows: 55, 55 | 63, 49;  12 rows: 56, 66 | 63, 62
-//      80 rows: 149, 149 | 151, 185;  96 rows: 166, 166 | 152, 187;     128 rows: 211, 216 | 199, 222
-//   down, half unevenly
-//      2 of 8, 14336 > 4096:  0.5 rows: 25 | 44;   1 row: 46 | 51;   1.5 rows: 66 | 64;   2 rows: 83 | 64
-//      8 of 64, 1024 > 2048:  0.5 rows: 20 | 25;   1 row: 37 | 28;   2 rows: 70 | 31;   64 rows: 74 | 93;   128 rows: 125 | 133;   512 rows: 436 | 370
-//      4 of 16, 4864 > 896:   1 row: 12 | 23;   2 rows: 18 | 27;   3 rows: 26 | 27
-// Under 2 rows an expert, fewer than 8 rows in all stay with the integer dots: with so few experts each one's weights are read about once.
-int moe_columns(int64_t n_pairs, int n_experts, bool gate_up)
+//      6 rows: 136, 135 | 149, 147;   8 rows: 136, 146 | 148, 147;   10 rows: 146, 167 | 149, 148
+//      75 rows: 415, 404 | 378, 490;  100 rows: 506, 520 | 382, 522;  128 rows: 621, 615 | 526, 554
+//   gate and up, 8 of 64 experts of 2048 > 1024
+//      8 rows: 55, 55 | 63, 49;  12 rows: 56, 66 | 63, 62;  80 rows: 149, 149 | 151, 185;  96 rows: 166, 166 | 152, 187;  128 rows: 211, 216 | 199, 222
+//   down, 8 of 64, 1024 > 2048, half unevenly:  8 rows: 37 | 41;  64 rows: 74 | 93;  128 rows: 125 | 133;  512 rows: 436 | 370
+int moe_tiles(int64_t n_pairs, int n_experts, bool gate_up)
 {
     const int64_t rows = n_pairs / n_experts;
-    if (rows < (gate_up ? 1 : 2) || (rows < 2 && n_pairs < 8)) return 0;
-    return rows <= 10 ? 16 : rows < (gate_up ? 96 : 160) ? 32 : 128;
+    return rows < 1 ? 0 : rows <= 10 ? 16 : rows < (gate_up ? 96 : 160) ? 32 : 128;
+}
+
+// The tiles, or 0, integer dots, where they would be tiles of 16 and rows and weights are so few that their time is less.  In us, of 304 CTAs side
+// by side, each a round of 8 super-blocks after the other; and of 152, by super-block, of the experts that are met if all
+// are as likely, after some 17 us for B's pieces, starts and ends.  Measured (dots | tiles of 16):
+//   gate and up, 2 of 8, 4096 > 14336:  1 row 88 | 104;  1.5 rows 126 | 114;  2 rows 165 | 124;   8 of 64, 2048 > 1024:  1 row 33 | 43;
+//   1.5 rows 46 | 43;  2 rows 60 | 46;   8 of 128, 2048 > 768:  1 row 46 | 47;  1.5 rows 67 | 58
+//   down, 2 of 8, 14336 > 4096:  1 row 46 | 51;  1.5 rows 66 | 64;  2 rows 83 | 64;   8 of 64, 1024 > 2048:  1 row 37 | 28;
+//   4 of 16, 4864 > 896:  1 row 12 | 23;  2 rows 18 | 27;  3 rows 26 | 27;   2 of 8, 512 > 1024:  2 rows 6 | 11;   1 of 4, 768 > 512:  3 rows 3 | 12
+int moe_columns(int64_t n_pairs, int n_experts, int top_k, int64_t out_dim, int64_t in_dim, bool gate_up)
+{
+    const int columns = moe_tiles(n_pairs, n_experts, gate_up);
+    if (columns != 16) return columns;
+    const double nsb = in_dim / 256, met = n_experts * (1.0 - pow(1.0 - 1.0 / n_experts, static_cast<double>(n_pairs)));
+    const int of_cta = gate_up ? 32 : 4 * moe_down_quads(top_k);
+    const double ctas = static_cast<double>(gate_up ? n_pairs : n_pairs / top_k) * ((out_dim + of_cta - 1) / of_cta);
+    const double dots = 3.0 + std::max(1.0, ctas / 304) * (gate_up ? 2 : 1) * (0.8 + 1.5 * ceil(nsb / 8));
+    const double items = met * ((out_dim + (gate_up ? 127 : 255)) / (gate_up ? 128 : 256));
+    return dots <= 17.0 + 1.2 * nsb * std::max(gate_up ? 1.0 : 0.25, items / 152) ? 0 : columns;
 }
 
 // Parts of in_dim are for products that may come to fewer than two items an SM.
-int moe_max_parts(int64_t n_pairs, int n_experts, int64_t out_dim, int64_t in_dim)
+int moe_max_parts(int columns, int64_t n_pairs, int64_t out_dim, int64_t in_dim)
 {
-    const int columns = moe_columns(n_pairs, n_experts, false);
     if (columns == 0) return 1;
     const int64_t least = (n_pairs + columns - 1) / columns * ((out_dim + 255) / 256);
     return static_cast<int>(std::max<int64_t>(1, std::min({int64_t(8), in_dim / 512, 2 * 152 / least})));

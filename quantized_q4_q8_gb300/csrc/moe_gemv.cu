@@ -6,9 +6,14 @@
 //   y[t][i] = residual[t][i] + sum_j weights[t][j] * o[places[t][j]][i]
 // with the product of rz_q4k_q8_gemv (exact integer dots of 32 codes, f32 sums).
 //
-// A CTA has 32 outputs and up to kTokens rows of one expert: 8 warps of 4 outputs, 4 lanes for a
-// super-block of 256 weights (64 each), 8 super-blocks side by side.  The weights come straight from
-// global memory, 12 loads of 16 bytes in flight for a lane.
+// A CTA has a row and 32 outputs: 8 warps of 4 outputs, 4 lanes for a super-block of 256 weights (64 each), 8 super-blocks side by
+// side.  The weights come straight from global memory, 12 loads of 16 bytes in flight for a lane; those of an expert with a
+// second row come from L2 again.  (Four rows of an expert at once took 170 registers, spilled, and 37.9 instead of 26.3 us for
+// one token of 2 of 8 experts, 4096 > 14336; 24.6 instead of 19.7 us for 4 tokens of 8 of 64, 2048 > 1024.)
+//
+// Bound: bytes where the weights are large (one token, 2 of 8 experts: gate and up 4096 > 14336 25.3 us, 5.2 TB/s; down 14336 >
+// 4096 13.8 us, 4.8 TB/s), else the latency of dependent loads behind a launch (one token, 8 of 64: gate and up 2048 > 1024 6.3 us,
+// 3.0 TB/s; down 1024 > 2048 6.7 us).
 #include <algorithm>
 
 #include "q4k_dot.cuh"
@@ -20,7 +25,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 32;    // outputs of a CTA
-constexpr int kTokens = 4;   // rows of one expert that share a load of its weights
 constexpr int kRows = 4;     // weight rows that a warp works at once
 
 struct Weights64 {  // a lane's 64 weights: a header and 32 bytes of codes
@@ -34,23 +38,22 @@ __device__ __forceinline__ int4 load_stream(const void *p)
     return v;
 }
 
-// The expert of row r (the CTA's first row), and the end of its rows; -1 where there is none.
-__device__ __forceinline__ int2 find_expert(const MoeGemvArgs &a, int r, int2 *found)
+// The expert of row r, -1 where there is none; by each warp for itself.
+__device__ __forceinline__ int find_expert(const MoeGemvArgs &a, int r, int lane)
 {
-    if (threadIdx.x == 0) *found = make_int2(-1, 0);
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.n_experts; e += kThreads) {
-        const int lo = a.offsets[e], hi = a.offsets[e + 1];
-        if (lo <= r && r < hi && lo >= 0 && hi <= a.n_pairs && (r - lo) % kTokens == 0) *found = make_int2(e, hi);
+    int found = -1;
+#pragma unroll 4
+    for (int e0 = 0; e0 < a.n_experts; e0 += 32) {
+        const int e = min(e0 + lane, a.n_experts - 1), lo = a.offsets[e], hi = a.offsets[e + 1];
+        const uint32_t here = __ballot_sync(0xffffffffu, lo <= r && r < hi && lo >= 0 && hi <= a.n_pairs);
+        if (here && found < 0) found = min(e0 + __ffs(here) - 1, a.n_experts - 1);
     }
-    __syncthreads();
-    return *found;
+    return found;
 }
 
-// acc[k][t] += the lane's share of weight row k times row src[t] of x, for m rows of x.
-template <int kT>
-__device__ __forceinline__ void dot_rows(const MoeGemvArgs &a, const uint8_t *const (&wr)[kRows], const int (&src)[kT], int m, int sub, int c,
-                                         const LaneConst &L, float (&acc)[kRows][kT])
+// acc[k] += the lane's share of weight row k times row src of x.
+__device__ __forceinline__ void dot_rows(const MoeGemvArgs &a, const uint8_t *const (&wr)[kRows], int src, int sub, int c, const LaneConst &L,
+                                         float (&acc)[kRows])
 {
     const int nsb = a.in_dim / 256, nb = a.in_dim / 32;
 #pragma unroll 1
@@ -77,36 +80,31 @@ __device__ __forceinline__ void dot_rows(const MoeGemvArgs &a, const uint8_t *co
             dm0[k] = dmin * static_cast<float>(mnp & 0xffu);
             dm1[k] = dmin * static_cast<float>((mnp >> 8) & 0xffu);
         }
+        const int64_t j = static_cast<int64_t>(src) * nb + sb * 8 + 2 * c;
+        const int4 *xp = reinterpret_cast<const int4 *>(a.xq + j * 32);
+        const int4 x0 = __ldg(xp), x1 = __ldg(xp + 1), x2 = __ldg(xp + 2), x3 = __ldg(xp + 3);
+        const float2 d8 = __ldg(reinterpret_cast<const float2 *>(a.xd + j)), s8 = __ldg(reinterpret_cast<const float2 *>(a.xs + j));
+        const int xa[16] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w, x2.x, x2.y, x2.z, x2.w, x3.x, x3.y, x3.z, x3.w};
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            if (t >= m) break;
-            const int64_t j = static_cast<int64_t>(src[t]) * nb + sb * 8 + 2 * c;
-            const int4 *xp = reinterpret_cast<const int4 *>(a.xq + j * 32);
-            const int4 x0 = __ldg(xp), x1 = __ldg(xp + 1), x2 = __ldg(xp + 2), x3 = __ldg(xp + 3);
-            const float2 d8 = __ldg(reinterpret_cast<const float2 *>(a.xd + j)), s8 = __ldg(reinterpret_cast<const float2 *>(a.xs + j));
-            const int xa[16] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w, x2.x, x2.y, x2.z, x2.w, x3.x, x3.y, x3.z, x3.w};
+        for (int k = 0; k < kRows; ++k) {
+            const int q[8] = {w[k].a.x, w[k].a.y, w[k].a.z, w[k].a.w, w[k].b.x, w[k].b.y, w[k].b.z, w[k].b.w};
+            int i0 = 0, i1 = 0;
 #pragma unroll
-            for (int k = 0; k < kRows; ++k) {
-                const int q[8] = {w[k].a.x, w[k].a.y, w[k].a.z, w[k].a.w, w[k].b.x, w[k].b.y, w[k].b.z, w[k].b.w};
-                int i0 = 0, i1 = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    i0 = __dp4a(q[i] & 0x0f0f0f0f, xa[i], i0);
-                    i1 = __dp4a((q[i] >> 4) & 0x0f0f0f0f, xa[8 + i], i1);
-                }
-                float v = fmaf(ds0[k], d8.x * static_cast<float>(i0), acc[k][t]);
-                v = fmaf(ds1[k], d8.y * static_cast<float>(i1), v);
-                v = fmaf(-dm0[k], s8.x, v);
-                acc[k][t] = fmaf(-dm1[k], s8.y, v);
+            for (int i = 0; i < 8; ++i) {
+                i0 = __dp4a(q[i] & 0x0f0f0f0f, xa[i], i0);
+                i1 = __dp4a((q[i] >> 4) & 0x0f0f0f0f, xa[8 + i], i1);
             }
+            float v = fmaf(ds0[k], d8.x * static_cast<float>(i0), acc[k]);
+            v = fmaf(ds1[k], d8.y * static_cast<float>(i1), v);
+            v = fmaf(-dm0[k], s8.x, v);
+            acc[k] = fmaf(-dm1[k], s8.y, v);
         }
     }
 }
 
 __global__ void __launch_bounds__(kThreads, 2) moe_swiglu_kernel(const MoeGemvArgs a)
 {
-    __shared__ int2 found;
-    __shared__ float out[kTokens][kTile];
+    __shared__ float out[kTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c = lane & 3, sub = lane >> 2;
     const int nsb = a.in_dim / 256;
@@ -114,25 +112,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_swiglu_kernel(const MoeGemvAr
     pdl_launch_dependents();
     pdl_wait();
     const int r = blockIdx.y;
-    const int2 ex = find_expert(a, r, &found);
-    if (ex.x < 0) return;
-    const int m = min(kTokens, ex.y - r);
-    int src[kTokens];  // the rows of x
-#pragma unroll
-    for (int t = 0; t < kTokens; ++t) {
-        int s = r + min(t, m - 1);
-        if (a.rows) {
-            const int pair = a.rows[s];
-            if (pair < 0 || pair >= a.n_pairs) {
-                if (tid == 0) set_error(a.err, DEV_BAD_LENGTH);
-                s = 0;
-            } else {
-                s = pair / a.top_k;
-            }
-        }
-        src[t] = s;
-    }
-    const int64_t wbase = static_cast<int64_t>(ex.x) * a.out_dim;
+    const int pair = a.rows[r], e = find_expert(a, r, lane);
+    if (e < 0) return;
+    const bool fine = pair >= 0 && pair < a.n_pairs;
+    if (!fine && tid == 0) set_error(a.err, DEV_BAD_LENGTH);
+    const int src = fine ? pair / a.top_k : 0;  // the row of x
+    const int64_t wbase = static_cast<int64_t>(e) * a.out_dim;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         // a warp's outputs 4 warp .. + 3, gate and up of two of them at once
@@ -143,23 +128,19 @@ __global__ void __launch_bounds__(kThreads, 2) moe_swiglu_kernel(const MoeGemvAr
             const int64_t o = min(static_cast<int64_t>(blockIdx.x) * kTile + o0 + (k >> 1), a.out_dim - 1);
             wr[k] = (k & 1 ? a.w2 : a.w1) + (wbase + o) * nsb * 144;
         }
-        float acc[kRows][kTokens] = {};
-        dot_rows(a, wr, src, m, sub, c, L, acc);
+        float acc[kRows] = {};
+        dot_rows(a, wr, src, sub, c, L, acc);
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) {
-            if (t >= m) break;
-#pragma unroll
-            for (int k = 0; k < kRows; ++k) acc[k][t] = warp_sum(acc[k][t]);
-            if (lane < 2) {
-                const float g = lane ? acc[2][t] : acc[0][t], u = lane ? acc[3][t] : acc[1][t];
-                out[t][o0 + lane] = g / (1.0f + expf(-g)) * u;
-            }
+        for (int k = 0; k < kRows; ++k) acc[k] = warp_sum(acc[k]);
+        if (lane < 2) {
+            const float g = lane ? acc[2] : acc[0], u = lane ? acc[3] : acc[1];
+            out[o0 + lane] = g / (1.0f + expf(-g)) * u;
         }
     }
     __syncthreads();
-    if (warp < m) {
-        const int64_t o = static_cast<int64_t>(blockIdx.x) * kTile + lane, at = static_cast<int64_t>(r + warp) * a.out_dim + o;
-        const float v = o < a.out_dim ? out[warp][lane] : 0.0f;
+    if (warp == 0) {
+        const int64_t o = static_cast<int64_t>(blockIdx.x) * kTile + lane, at = static_cast<int64_t>(r) * a.out_dim + o;
+        const float v = o < a.out_dim ? out[lane] : 0.0f;
         if (a.y && o < a.out_dim) a.y[at] = v;
         if (a.yq) {  // out_dim is a multiple of 32
             const float d = __fdiv_rn(warp_max(fabsf(v)), 127.0f);
@@ -195,12 +176,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_tokens_kernel(const MoeG
         const uint8_t *wr[kRows];
 #pragma unroll
         for (int k = 0; k < kRows; ++k) wr[k] = a.w1 + (e * a.out_dim + min(o0 + 4 * q + k, a.out_dim - 1)) * nsb * 144;
-        const int src[1] = {place};
-        float acc[kRows][1] = {};
-        dot_rows(a, wr, src, 1, sub, c, L, acc);
+        float acc[kRows] = {};
+        dot_rows(a, wr, place, sub, c, L, acc);
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) acc[k][0] = warp_sum(acc[k][0]);
-        if (lane < 4) out[j][4 * q + lane] = lane == 0 ? acc[0][0] : lane == 1 ? acc[1][0] : lane == 2 ? acc[2][0] : acc[3][0];
+        for (int k = 0; k < kRows; ++k) acc[k] = warp_sum(acc[k]);
+        if (lane < 4) out[j][4 * q + lane] = lane == 0 ? acc[0] : lane == 1 ? acc[1] : lane == 2 ? acc[2] : acc[3];
     }
     __syncthreads();
     const int64_t col = o0 + tid;
@@ -287,15 +267,15 @@ cudaError_t launch(K kernel, dim3 grid, const A &a, cudaStream_t s)
 
 cudaError_t launch_moe_swiglu(const MoeGemvArgs &a, cudaStream_t s)
 {
-    const dim3 grid(static_cast<unsigned>((a.out_dim + kTile - 1) / kTile), static_cast<unsigned>(a.n_pairs));  // fewer than 2 kMoeMaxExperts
+    const dim3 grid(static_cast<unsigned>((a.out_dim + kTile - 1) / kTile), static_cast<unsigned>(a.n_pairs));  // fewer than 11 kMoeMaxExperts
     return launch(moe_swiglu_kernel, grid, a, s);
 }
 
 cudaError_t launch_moe_down_tokens(const MoeGemvArgs &a, const MoeCombineArgs &b, int64_t n_tokens, cudaStream_t s)
 {
-    const int quads = a.top_k >= 8 ? 1 : 8 / a.top_k;
+    const int quads = moe_down_quads(a.top_k);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.out_dim + 4 * quads - 1) / (4 * quads)), static_cast<unsigned>(n_tokens));  // fewer than 2 kMoeMaxExperts
+    cfg.gridDim = dim3(static_cast<unsigned>((a.out_dim + 4 * quads - 1) / (4 * quads)), static_cast<unsigned>(n_tokens));  // fewer than 11 kMoeMaxExperts
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -12,6 +12,7 @@
 // before it wrote and places its own range.  Atomics only count and set bits, so that nothing depends on their order.
 //
 // Bound: latency, of the rounds and of two launches' trips to memory.  4 bytes a logit and 16 a row are read and written.
+// 1 token, 8 of 64 experts: 3.6 us; 4095 tokens, 8 of 128: 12.9 us.
 #include <math.h>
 
 #include "rz_common.cuh"

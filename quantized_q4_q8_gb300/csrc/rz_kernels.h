@@ -361,8 +361,10 @@ cudaError_t launch_moe_swiglu(const MoeGemvArgs &a, cudaStream_t s);  // with in
 cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &a, int columns, void *workspace, cudaStream_t s);
 int64_t moe_pack_bytes(int columns, int64_t n_pairs, int n_experts, int64_t in_dim);  // of its workspace
 
-int moe_columns(int64_t n_pairs, int n_experts, bool gate_up);  // of the tiles for so many rows of so many experts; 0: integer dots
-int moe_max_parts(int64_t n_pairs, int n_experts, int64_t out_dim, int64_t in_dim);
+int moe_tiles(int64_t n_pairs, int n_experts, bool gate_up);  // rows of the tiles that so many rows of so many experts may take, or 0
+int moe_columns(int64_t n_pairs, int n_experts, int top_k, int64_t out_dim, int64_t in_dim, bool gate_up);  // those that they take; 0: integer dots
+int moe_max_parts(int columns, int64_t n_pairs, int64_t out_dim, int64_t in_dim);
+constexpr int moe_down_quads(int top_k) { return top_k >= 8 ? 1 : 8 / top_k; }  // 4 outputs each, of a CTA of moe_down_tokens
 
 struct MoeCombineArgs {
     const float *o;  // [*parts][n_pairs][out_dim]

@@ -216,6 +216,7 @@ SHAPES = [  # T, E, k, inter, in
     (33, 4, 1, 129, 512), (40, 3, 3, 256, 1024), (130, 8, 2, 130, 256), (150, 2, 2, 320, 512), (300, 16, 4, 96, 256), (270, 1, 1, 200, 768),
     (64, 32, 2, 640, 256), (240, 8, 1, 2600, 256), (820, 8, 1, 2560, 512),  # more tiles than SMs, for each of the tiles' sizes
     (7, 8, 2, 65, 1280), (6, 16, 1, 40, 2560), (9, 256, 32, 32, 256),
+    (40, 8, 2, 2208, 512), (17, 2, 1, 3001, 1280), (100, 64, 2, 1024, 256), (10, 4, 4, 2000, 1536),  # tiles of 16 rows: many outputs
 ]
 
 
@@ -272,8 +273,8 @@ def test_down(rz, T, E, k, out_dim, in_dim):
 
 
 PARTS = [  # few tiles and a long in_dim: 4 to 19 super-blocks, in parts of equal and unequal lengths
-    (9, 4, 2, 300, 1024), (33, 8, 2, 1000, 4864), (65, 16, 4, 130, 2304), (60, 2, 1, 257, 2816), (200, 1, 1, 700, 2560), (130, 1, 1, 1, 1280),
-    (12, 4, 1, 2049, 1792),
+    (60, 4, 2, 300, 1024), (33, 8, 2, 1000, 4864), (65, 16, 4, 130, 2304), (60, 2, 1, 257, 2816), (200, 1, 1, 700, 2560), (130, 1, 1, 1, 1280),
+    (52, 4, 1, 2049, 1792),
 ]
 
 
@@ -300,11 +301,11 @@ def test_down_parts_workspace(rz):
     assert torch.equal(rz.moe_down(*args, residual=res, ws=room[:size]), res)  # no row at all
 
 
-@pytest.mark.parametrize("T", [3, 90])
-def test_products_of_extreme_blocks(rz, T):
+@pytest.mark.parametrize("T,inter", [(3, 64), (9, 2240), (90, 64), (200, 64)])  # integer dots, and tiles of 16, 32 and 128 rows
+def test_products_of_extreme_blocks(rz, T, inter):
     """Super-blocks without a scale, without a min, with mins far above or below the scale; blocks of x far apart."""
     rng = np.random.default_rng(T)
-    E, k, inter, in_dim = 2, 2, 64, 1024
+    E, k, in_dim = 2, 2, 1024
     plan, expert = make_plan(rz, rng, T, E, k, idle=0.0)
     w = q4k(rng, E, inter, in_dim=in_dim)
     d, dmin = w[..., 0:2].view(np.float16)[..., 0], w[..., 2:4].view(np.float16)[..., 0]
@@ -324,8 +325,8 @@ def test_products_of_extreme_blocks(rz, T):
 
 def test_values_that_are_no_numbers_stay_in_their_rows(rz):
     rng = np.random.default_rng(11)
-    for T in (4, 140):
-        E, k, out_dim, in_dim = 3, 1, 70, 512
+    for T, out_dim in ((4, 70), (31, 2600), (140, 70), (500, 70)):  # integer dots, and tiles of 16, 32 and 128 rows
+        E, k, in_dim = 3, 1, 512
         plan, expert = make_plan(rz, rng, T, E, k, idle=0.0)
         w = q4k(rng, E, out_dim, in_dim=in_dim)
         q, d, s = activations(rng, T, in_dim)
@@ -506,11 +507,11 @@ def test_block_in_a_graph_and_on_another_stream(rz):
     assert torch.equal(got, eager[1])
 
 
-@pytest.mark.parametrize("T,E", [(12, 4), (60, 4), (300, 2)])
-def test_wait_that_runs_out(rz, T, E):
+@pytest.mark.parametrize("T,E,out_dim", [(20, 4, 2304), (60, 4, 384), (300, 2, 384)])
+def test_wait_that_runs_out(rz, T, E, out_dim):
     """The first weights of CTA 0 are left uncopied: the product reports it, ends, and the next is as before."""
     rng = np.random.default_rng(T)
-    k, out_dim, in_dim = 2, 384, 1024
+    k, in_dim = 2, 1024
     plan, _ = make_plan(rz, rng, T, E, k, idle=0.0)
     w, x = dev(q4k(rng, E, out_dim, in_dim=in_dim)), dev(R.q8_buffer(*activations(rng, T, in_dim)))
     want = rz.moe_swiglu(w, w, x, plan, out_dim, in_dim)
