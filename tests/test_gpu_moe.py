@@ -507,6 +507,73 @@ def test_block_in_a_graph_and_on_another_stream(rz):
     assert torch.equal(got, eager[1])
 
 
+def test_two_streams_at_once(rz):
+    """Calls that share weights and input, each with its own plan, workspace and outputs."""
+    rng = np.random.default_rng(3)
+    T, E, k, n, inter = 33, 8, 2, 1024, 2048
+    gate, up, down = (dev(q4k(rng, E, *s, in_dim=i)) for s, i in (((inter,), n), ((inter,), n), ((n,), inter)))
+    x8, logits = dev(R.q8_buffer(*activations(rng, T, n))), torch.randn(4, T, E, device="cuda")
+    plans = [rz.MoePlan(T, E, k) for _ in logits]
+    run = lambda i: rz.moe_ffn(logits[i], x8, gate, up, down, plans[i], n, n, inter)
+    want = [run(i).clone() for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for i in range(4):
+            with torch.cuda.stream(streams[i % 2]):
+                got.append(run(i))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[j % 4]) for j, g in enumerate(got))
+    assert rz.check_device_error() == (0, 0)
+
+
+def test_two_graphs_share_a_workspace(rz):
+    """Replayed one after another; the smaller call leaves what the larger one must not read."""
+    rng = np.random.default_rng(4)
+    E, k, n, inter = 8, 2, 1024, 2048
+    gate, up, down = (dev(q4k(rng, E, *s, in_dim=i)) for s, i in (((inter,), n), ((inter,), n), ((n,), inter)))
+    sizes = (33, 3, 700)
+    ws = rz.workspace(max(rz.moe_ffn_workspace_bytes(T, E, k, n, n, inter) for T in sizes), "cuda")
+    graphs = []
+    for T in sizes:
+        args = torch.randn(T, E, device="cuda"), dev(R.q8_buffer(*activations(rng, T, n))), gate, up, down, rz.MoePlan(T, E, k), n, n, inter
+        want = rz.moe_ffn(*args, ws=ws).clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = rz.moe_ffn(*args, ws=ws)
+        graphs.append((g, out, want, args))
+    for i in (0, 1, 2, 1, 0, 2, 2, 0):
+        g, out, want, _ = graphs[i]
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    assert rz.check_device_error() == (0, 0)
+
+
+def test_more_than_2_31_values(rz):
+    rng = np.random.default_rng(5)
+    T, E, k, out_dim, in_dim = 74900, 4, 2, 14400, 256
+    plan, expert = make_plan(rz, rng, T, E, k, idle=0.0)
+    w = q4k(rng, E, out_dim, in_dim=in_dim, spread=1.0)
+    wv = R.weights(w)
+    q, d, s = activations(rng, T, in_dim)
+    d, s = (d * np.float32(0.01)).astype(np.float32), (s * np.float32(0.01)).astype(np.float32)
+    h = rz.moe_swiglu(dev(w), dev(w), dev(R.q8_buffer(q, d, s)), plan, out_dim, in_dim)
+    assert h.numel() > 2 ** 31 and expert[-1] >= 0
+    some = np.array([0, 1, 74901, T * k - 129, T * k - 1])
+    ref, tol = R.swiglu(wv, wv, R.q8_values(q, d), host(plan.rows)[some], expert[some], k)
+    within(host(h[torch.from_numpy(some).cuda()]), ref, 1.2 * tol, "h")
+    del h
+    q, d, s = activations(rng, T * k, in_dim)
+    y = rz.moe_down(dev(w), dev(R.q8_buffer(q, d, s)), plan, out_dim, in_dim)
+    places = host(plan.places).reshape(T, k)
+    some = np.array([0, T - 1, int(places.max(1).argmax()), 40000])
+    ref, tol = R.down(wv, R.q8_values(q, d), places[some].reshape(-1), expert, host(plan.weights)[some].astype(np.float64), None)
+    within(host(y[torch.from_numpy(some).cuda()]), ref, tol, "y")
+    assert rz.check_device_error() == (0, 0)
+
+
 @pytest.mark.parametrize("T,E,out_dim", [(20, 4, 2304), (60, 4, 384), (300, 2, 384)])
 def test_wait_that_runs_out(rz, T, E, out_dim):
     """The first weights of CTA 0 are left uncopied: the product reports it, ends, and the next is as before."""
