@@ -523,6 +523,23 @@ __device__ __forceinline__ void shrink8(uint32_t (&o)[8], uint32_t raw)
     for (int i = 0; i < 8; ++i) o[i] = hmul2u(o[i], by);
 }
 
+// What a super-block's mins are multiplied by, what the scales that centred codes leave out, and the scale of its row.
+struct Mins {
+    float by, f, g;
+    Mins() = default;
+    __device__ __forceinline__ Mins(const uint4 &hd, bool any_wide)
+    {
+        const Head head = head_of(hd.x);
+        const float ratio = head.wide ? 1.0f : head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
+        by = head.fine ? -0.125f * ratio : 0.0f;
+        f = any_wide ? head.shrink() : 1.0f;
+        g = !head.fine ? NAN : head.wide ? head.dmin : head.d;
+    }
+    // six-bit mins of sub-blocks 0-3 and 4-7
+    static __device__ __forceinline__ uint32_t low(const uint4 &hd) { return hd.z & 0x3f3f3f3fu; }
+    static __device__ __forceinline__ uint32_t high(const uint4 &hd) { return ((hd.w >> 4) & 0x0f0f0f0fu) | ((hd.z >> 2) & 0x30303030u); }
+};
+
 // Items in parts of in_dim, where whole ones leave SMs without work: the fewest super-blocks on an SM, with three more for each item's
 // start and end.  65 tokens of 4 in 16 experts, 4864 > 896: 39.8 to 30.6 us; 33 tokens of 2 in 8, 5632 > 2048: 39.3 to 27.7 us.
 __device__ __forceinline__ int parts_of(int64_t items, int nsb, int max_parts)
@@ -558,15 +575,15 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
     if (tid == 0) {
         for (int i = 0; i < 2 * C::kSlotsA; ++i) {
             mbar_init(&b.a_full[i & 1][i >> 1], 4);
-            mbar_init(&b.a_empty[i & 1][i >> 1], 1);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(&b.a_empty[i & 1][i >> 1], 1);
         for (int i = 0; i < C::kRingB; ++i) {
             mbar_init(&b.b_full[i], 1);
             mbar_init(&b.b_empty[i], 2);
         }
         for (int i = 0; i < C::kRingRaw; ++i) {
             mbar_init(&b.raw_full[i], 1);
-            mbar_init(&b.raw_empty[i], 4 * 2);
+            mbar_init(&b.raw_empty[i], C::kStack ? 4 : 4 * 2);
         }
         for (int i = 0; i < C::kBufD; ++i) {
             mbar_init(&b.d_full[i], 1);
@@ -661,7 +678,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
 #pragma unroll
                         for (int i = 0; i < 4; ++i) mma_ts(elected, d, ta + 8 * i, tb + 16 * i, operand_high(1024), idesc_f16(N), true);
                     }
-                    if (C::kStack || entry == 0 || again) commit(elected, RZ_BAR(a_empty) + 32 * mt + 8 * at.slot());
+                    // side by side: the other group writes this slot next, and waits at a barrier of its own
+                    const unsigned next = C::kStack ? at.slot() + (k & 1 ? 0 : 2) : at.slot();
+                    if (C::kStack || entry == 0 || again) commit(elected, RZ_BAR(a_empty) + 32 * mt + 8 * next);
                     commit(elected, RZ_BAR(b_empty) + 8 * pb.slot());
                     if (last) commit(elected, RZ_BAR(d_full) + 8 * pd.slot());
                     if (!again) pa.add(1);
@@ -742,28 +761,33 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         // group: matrix, and which of its steps
         const int cw = warp - C::kFirstUnpack, wrow = 32 * (cw & 3) + lane, mt = (cw >> 2) & 1, turn = cw >> 3;
         const uint32_t ta0 = tmem + (static_cast<uint32_t>(32 * (cw & 3)) << 16) + C::kColA + mt * C::kSlotsA * C::kWidthA;
-        Ring<C::kRingRaw, N == 128> praw(mt);
-        Ring<C::kSlotsA, N == 128> pa(turn);
-        Ring<kHdr, N == 128> ph(0);
-        int use = turn;  // this group's slots are every other one, over the super-blocks' ends
+        Ring<C::kRingRaw, N == 128> praw(C::kStack ? mt + 2 * turn : mt);
+        Ring<C::kSlotsA, N == 128> pa(C::kStack ? 0 : turn);
+        Ring<kHdr, N == 128> ph(C::kStack ? turn : 0);
+        // Side by side, a group has every other super-block; else every other slot, over the super-blocks' ends.
+        int use = C::kStack ? 0 : turn;
+        unsigned before = turn;  // side by side: parity of the phase in which the other group's use of a slot is read
         bool ok = true;
-        for (int64_t k = 0; k < blocks && ok; ++k) {
+        for (int64_t k = C::kStack ? turn : 0; k < blocks && ok; k += C::kStack ? 2 : 1) {
             if (!(ok = wait_warp(RZ_BAR(raw_full) + 8 * praw.slot(), praw.par(), bars, g.err))) break;
             const uint32_t raw = sm32 + C::off_raw + praw.slot() * kRawBytes + wrow * 144;
-            uint32_t sc0, sc1;  // six-bit scales, four to a word: sub-blocks 0-3 and 4-7
-            bool any_wide;
-            {
-                const uint4 hd = lds4(raw);
-                any_wide = __any_sync(0xffffffffu, mins_are_unit(hd.x));
-                sc0 = hd.y & 0x3f3f3f3fu;
-                sc1 = (hd.w & 0x0f0f0f0fu) | ((hd.y >> 2) & 0x30303030u);
-            }
+            const uint4 hd = lds4(raw);
+            const bool any_wide = __any_sync(0xffffffffu, mins_are_unit(hd.x));
+            // six-bit scales, four to a word: sub-blocks 0-3 and 4-7
+            const uint32_t sc0 = hd.y & 0x3f3f3f3fu, sc1 = (hd.w & 0x0f0f0f0fu) | ((hd.y >> 2) & 0x30303030u);
+            Mins mins_of;
+            if constexpr (C::kStack) mins_of = Mins(hd, any_wide);
 #pragma unroll 1
-            for (; use < C::kUses; use += 2) {
+            for (; use < C::kUses; use += C::kStack ? 1 : 2) {
                 const bool mins = !C::kStack && use == 0;  // the mins alone
-                if (!(ok = wait_warp(RZ_BAR(a_empty) + 32 * mt + 8 * pa.slot(), pa.par() ^ 1u, bars, g.err))) break;
+                if constexpr (C::kStack) {
+                    if (!(ok = wait_warp(RZ_BAR(a_empty) + 32 * mt + 8 * (use + 2 * turn), before ^ 1u, bars, g.err))) break;
+                } else {
+                    if (!(ok = wait_warp(RZ_BAR(a_empty) + 32 * mt + 8 * pa.slot(), pa.par() ^ 1u, bars, g.err))) break;
+                }
                 fence_after();
-                const uint32_t ta = ta0 + pa.slot() * C::kWidthA;
+                const unsigned slot = C::kStack ? use : pa.slot();
+                const uint32_t ta = ta0 + slot * C::kWidthA;
                 if (!mins) {
 #pragma unroll
                     for (int cc = 0; cc < C::kChunks; ++cc) {
@@ -797,21 +821,18 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     }
                 }
                 if (C::kStack || mins) {
-                    const uint4 hd = lds4(raw);
-                    const Head head = head_of(hd.x);
-                    const float ratio = head.wide ? 1.0f : head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
-                    const float by = head.fine ? -0.125f * ratio : 0.0f, f = any_wide ? head.shrink() : 1.0f;
-                    const uint32_t mn[2] = {hd.z & 0x3f3f3f3fu, ((hd.w >> 4) & 0x0f0f0f0fu) | ((hd.z >> 2) & 0x30303030u)};
+                    const uint4 h = C::kStack ? hd : lds4(raw);
+                    const Mins of = C::kStack ? mins_of : Mins(h, any_wide);
                     constexpr int kWords = C::kStack ? 2 : 4;  // of two sub-blocks: this slot's, or all
                     uint32_t hi[2 * kWords], lo[2 * kWords];   // high pieces, twice; low ones, twice
 #pragma unroll
                     for (int i = 0; i < kWords; ++i) {
                         // two mins, and the scales 8 of which centred codes leave out, as f16 (1024 + m is 0x64 m)
                         const int quad = C::kStack ? use : i >> 1;
-                        const uint32_t mm = C::kStack ? (use ? mn[1] : mn[0]) : mn[i >> 1], ss = quad ? sc1 : sc0;
+                        const uint32_t mm = quad ? Mins::high(h) : Mins::low(h), ss = quad ? sc1 : sc0;
                         const float2 m = unpack2(hsub2u(__byte_perm(mm, 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u));
                         const float2 sc = unpack2(hsub2u(__byte_perm(ss, 0x64646464u, i & 1 ? 0x4342 : 0x4140), 0x64006400u));
-                        const float r0 = C::kStack ? by * m.x : fmaf(by, m.x, any_wide ? f * sc.x : sc.x), r1 = fmaf(by, m.y, any_wide ? f * sc.y : sc.y);
+                        const float r0 = C::kStack ? of.by * m.x : fmaf(of.by, m.x, of.f * sc.x), r1 = fmaf(of.by, m.y, of.f * sc.y);
                         hi[i] = hi[kWords + i] = pack2(r0, r1);
                         const float2 t = unpack2(hi[i]);
                         lo[i] = lo[kWords + i] = pack2(r0 - t.x, r1 - t.y);
@@ -823,23 +844,23 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         tm_store8(ta, hi);
                         tm_store8(ta + 8, lo);
                     }
-                    if (!C::kStack || use == 1)
-                        sts1(sm32 + C::off_g + 4 * ((ph.slot() * 2 + mt) * 128 + wrow), __float_as_uint(!head.fine ? NAN : head.wide ? head.dmin : head.d));
+                    if (!C::kStack || use == 1) sts1(sm32 + C::off_g + 4 * ((ph.slot() * 2 + mt) * 128 + wrow), __float_as_uint(of.g));
                 }
                 tm_store_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    arrive(RZ_BAR(a_full) + 32 * mt + 8 * pa.slot());
+                    arrive(RZ_BAR(a_full) + 32 * mt + 8 * slot);
                     if (C::kStack ? use == 1 : mins) arrive(RZ_BAR(h_full) + 8 * ph.slot());
                 }
-                pa.add(2);
+                if constexpr (!C::kStack) pa.add(2);
             }
             if (!ok) break;
             if (lane == 0) arrive(RZ_BAR(raw_empty) + 8 * praw.slot());
             use -= C::kUses;
-            ph.add(1);
-            praw.add(2);
+            before ^= 1u;
+            ph.add(C::kStack ? 2 : 1);
+            praw.add(C::kStack ? 4 : 2);
         }
     } else {
         // ------------------------------------------------------------ sums
