@@ -32,12 +32,13 @@
 //                cycles each, so that one warp for both was the bottleneck)
 //   warp 2       copies B, bulk copies of tiles laid out as shared memory takes them (moe_pack_kernel, the launch before)
 //   warp 3       copies the raw weights, 128 rows x 144 bytes a box
-//   groups of 4  unpack A, a thread for a weight row, the groups taking the steps of both matrices in turn
+//   groups of 4  unpack A, a thread for a weight row, two groups for each matrix: every other super-block (kN <= 32; every other slot of each
+//                was 135 instead of 126 us, scales and mins looked up twice), or every other slot
 //   8 warps      add up: a thread has a weight row of both matrices and half of the columns
 // Few rows (kN <= 32): the two pieces of B stand side by side as 2 kN columns, which halves the instructions.
 //
-// Bound and measured.  Tiles of 16 and 32: issue slots, for unpacking (76% are taken; 16 tokens of 2 in 8 experts, gate and up 4096 > 14336:
-// 135 us, 3.9 TB/s; 129 of 8 in 128, 2048 > 768: 71 us, 3.2 TB/s).  Tiles of 128: the tensor cores, 61% of the time (1024 tokens) at 2.06 times
+// Bound and measured.  Tiles of 16 and 32: issue slots, for unpacking (72% are taken; 16 tokens of 2 in 8 experts, gate and up 4096 > 14336:
+// 126 us, 4.2 TB/s; 129 of 8 in 128, 2048 > 768: 69 us, 3.3 TB/s).  Tiles of 128: the tensor cores, 61% of the time (1024 tokens) at 2.06 times
 // the formula's products (4096 of 2 in 8, 4096 > 14336: 3016 us, 638 TFLOP/s of the formula's), and accumulators that are read before a matrix's
 // next super-block: tensor memory is full.
 //
@@ -71,7 +72,7 @@ struct Cfg {
     static constexpr int kEntries = kStack ? 2 : 9;
     static constexpr int kGroups = 4;                 // that unpack A: two for each matrix, taking its steps in turn
     static constexpr int kBufD = N == 128 ? 2 : 3;    // accumulators: one for each matrix, or three in turn
-    static constexpr int kSlotsA = N == 128 ? 4 : 2;  // of A for each matrix; its two groups fill them in turn
+    static constexpr int kSlotsA = N == 128 ? 4 : 2;  // of A for each matrix
     static constexpr int kMinsB = N * (kStack ? 32 : 64);
     static constexpr int kBytesB = N * (kStack ? 512 : 128);  // two pieces of 128 values, or one of 64
     static constexpr int kSlotB = kBytesB + (kStack ? kMinsB : 0);
@@ -1065,11 +1066,11 @@ cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &g, int columns, void *workspac
 // Tiles by the rows that an expert has on average (us in a graph, tiles of 16 | 32 | 128 rows; experts chosen evenly, and unevenly: logits
 // with a normal part of their own for each expert).  0: fewer rows than experts, which are for the integer dots.
 //   gate and up, 2 of 8 experts of 4096 > 14336
-//      6 rows: 136, 135 | 149, 147;   8 rows: 136, 146 | 148, 147;   10 rows: 146, 167 | 149, 148
-//      75 rows: 415, 404 | 378, 490;  100 rows: 506, 520 | 382, 522;  128 rows: 621, 615 | 526, 554
+//      6 rows: 128, 127 | 141, 139;   8 rows: 128, 138 | 141, 139;   10 rows: 138, 156 | 141, 141
+//      75 rows: 395, 384 | 376, 490;  100 rows: 481, 495 | 382, 520;  128 rows: 591, 585 | 526, 554
 //   gate and up, 8 of 64 experts of 2048 > 1024
-//      8 rows: 55, 55 | 63, 49;  12 rows: 56, 66 | 63, 62;  80 rows: 149, 149 | 151, 185;  96 rows: 166, 166 | 152, 187;  128 rows: 211, 216 | 199, 222
-//   down, 8 of 64, 1024 > 2048, half unevenly:  8 rows: 37 | 41;  64 rows: 74 | 93;  128 rows: 125 | 133;  512 rows: 436 | 370
+//      8 rows: 53, 53 | 61, 48;  12 rows: 53, 63 | 61, 60;  80 rows: 143, 143 | 151, 185;  96 rows: 159, 159 | 152, 187;  128 rows: 202, 207 | 199, 222
+//   down, 8 of 64, 1024 > 2048, half unevenly:  8 rows: 36 | 40;  64 rows: 71 | 93;  128 rows: 120 | 133;  160 rows: 147 | 152;  512 rows: 416 | 370
 int moe_tiles(int64_t n_pairs, int n_experts, bool gate_up)
 {
     const int64_t rows = n_pairs / n_experts;
@@ -1079,10 +1080,10 @@ int moe_tiles(int64_t n_pairs, int n_experts, bool gate_up)
 // The tiles, or 0, integer dots, where they would be tiles of 16 and rows and weights are so few that their time is less.  In us, of 304 CTAs side
 // by side, each a round of 8 super-blocks after the other; and of 152, by super-block, of the experts that are met if all
 // are as likely, after some 17 us for B's pieces, starts and ends.  Measured (dots | tiles of 16):
-//   gate and up, 2 of 8, 4096 > 14336:  1 row 88 | 104;  1.5 rows 126 | 114;  2 rows 165 | 124;   8 of 64, 2048 > 1024:  1 row 33 | 43;
-//   1.5 rows 46 | 43;  2 rows 60 | 46;   8 of 128, 2048 > 768:  1 row 46 | 47;  1.5 rows 67 | 58
-//   down, 2 of 8, 14336 > 4096:  1 row 46 | 51;  1.5 rows 66 | 64;  2 rows 83 | 64;   8 of 64, 1024 > 2048:  1 row 37 | 28;
-//   4 of 16, 4864 > 896:  1 row 12 | 23;  2 rows 18 | 27;  3 rows 26 | 27;   2 of 8, 512 > 1024:  2 rows 6 | 11;   1 of 4, 768 > 512:  3 rows 3 | 12
+//   gate and up, 2 of 8, 4096 > 14336:  1 row 86 | 79;  1.5 rows 126 | 98;  2 rows 165 | 108;   8 of 64, 2048 > 1024:  1 row 33 | 36;
+//   1.5 rows 46 | 41;  2 rows 59 | 41;   8 of 128, 2048 > 768:  1 row 46 | 46;  1.5 rows 67 | 55
+//   down, 2 of 8, 14336 > 4096:  1 row 46 | 50;  1.5 rows 66 | 61;  2 rows 84 | 62;   8 of 64, 1024 > 2048:  1 row 37 | 27;
+//   4 of 16, 4864 > 896:  1 row 12 | 23;  2 rows 18 | 26;  3 rows 26 | 26;   2 of 8, 512 > 1024:  2 rows 6 | 11;   1 of 4, 768 > 512:  3 rows 3 | 12
 int moe_columns(int64_t n_pairs, int n_experts, int top_k, int64_t out_dim, int64_t in_dim, bool gate_up)
 {
     const int columns = moe_tiles(n_pairs, n_experts, gate_up);

@@ -12,7 +12,7 @@
 //
 // Bound: bytes, 8 read and 9.25 written for each value.  A CTA has a row and holds it in
 // registers between the sum and the outputs, a float4 of each 4 * kThreads values for a thread;
-// eight threads hold a Q8_1 block.  4095 rows of 4096: 47.7 us, 6.07 TB/s, 89% of a copy's rate (issue slots 68%: the sums
+// eight threads hold a Q8_1 block.  4095 rows of 4096: 47.7 us, 6.07 TB/s, 89% of a copy's rate (issue slots 77%: the sums
 // of two f32).  Few rows are a launch and a row's latency: 33 of 2048 2.8 us, 1 of 896 2.0 us.
 #include "rz_common.cuh"
 #include "rz_kernels.h"
