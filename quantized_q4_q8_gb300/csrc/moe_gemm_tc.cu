@@ -514,14 +514,22 @@ __device__ __forceinline__ uint32_t low_codes(uint32_t v, uint32_t sc, uint32_t 
     return kPlain ? hfma2u(v, sc, add) : hmul2u(hsub2u(v, 0x64086408u), sc);
 }
 
-// Codes of the row at `raw` in the unit of its mins, where that is the unit.
-__device__ __forceinline__ float shrink_of(uint32_t raw) { return head_of(lds4(raw).x).shrink(); }
-__device__ __forceinline__ void shrink8(uint32_t (&o)[8], uint32_t raw)
+// A slot's codes in the unit of the mins, of the rows where that is the unit: read back and written again.  Rare, and so apart: beside each
+// store it took 6 to 7% of the time of all tiles of 16 and 32 rows (instructions that are fetched and not executed).
+template <int kCols>
+__device__ __forceinline__ void shrink_codes(uint32_t at, float by)
 {
-    const float f = shrink_of(raw);
-    const uint32_t by = pack2(f, f);
+    const uint32_t by2 = pack2(by, by);
+    tm_store_wait();
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 8) {
+        float v[16];
+        tm_load8(at + c, v);
+        uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = hmul2u(o[i], by);
+        for (int i = 0; i < 8; ++i) o[i] = hmul2u(__float_as_uint(v[i]), by2);
+        tm_store8(at + c, o);
+    }
 }
 
 // What a super-block's mins are multiplied by, what the scales that centred codes leave out, and the scale of its row.
@@ -812,14 +820,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                                 hi[2 * i] = hfma2u(lop_and_or(words[i], 0x00f000f0u, 0x64006400u), mul1, add1);
                                 hi[2 * i + 1] = hfma2u(lop_and_or(w8, 0x00f000f0u, 0x64006400u), mul1, add1);
                             }
-                            if (any_wide) {
-                                shrink8(lo, raw);
-                                shrink8(hi, raw);
-                            }
                             tm_store8(ta + 32 * cc + 8 * half, lo);
                             tm_store8(ta + 32 * cc + 16 + 8 * half, hi);
                         }
                     }
+                    if (any_wide) shrink_codes<32 * C::kChunks>(ta, head_of(lds4(raw).x).shrink());
                 }
                 if (C::kStack || mins) {
                     const uint4 h = C::kStack ? hd : lds4(raw);
