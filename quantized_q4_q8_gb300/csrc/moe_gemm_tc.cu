@@ -107,8 +107,8 @@ struct Cfg {
 
 struct Bars {
     uint64_t a_full[2][4], a_empty[2][4], b_full[8], b_empty[8], raw_full[8], raw_empty[8], d_full[3], d_empty[3], h_full[kHdr], cs_full[kHdr], done[2];
-    uint32_t tmem, limit;    // polls of a wait
-    int gave_up, parts;
+    uint32_t tmem, limit;    // polls of a wait; 0 once one has run out
+    int parts;
 };
 static_assert(sizeof(Bars) <= 768, "barriers");
 
@@ -277,28 +277,24 @@ __device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_
                  "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ bool gave_up(uint32_t bars) { return lds1i(RZ_BAR(gave_up)) != 0; }
+__device__ __forceinline__ bool gave_up(uint32_t bars) { return lds1i(RZ_BAR(limit)) == 0; }
 
-// Bounded waits; false after a timeout or when another role gave up.
-__device__ __forceinline__ bool wait_one(uint32_t bar, unsigned par, uint32_t bars, unsigned *err)
+// Bounded waits; false after a timeout or when another role gave up.  Short, as there are many of them.
+__device__ __forceinline__ bool wait_one(uint32_t bar, unsigned par, uint32_t bars)
 {
     for (uint32_t i = 0;; ++i) {
         if (try_phase(bar, par)) return true;
-        if ((i & 63u) == 63u) {
-            if (gave_up(bars)) return false;
-            if (i >= static_cast<uint32_t>(lds1i(RZ_BAR(limit)))) {
-                sts1(RZ_BAR(gave_up), 1);
-                set_error(err, DEV_TIMEOUT_MOE);
-                return false;
-            }
+        if ((i & 63u) == 63u && i >= static_cast<uint32_t>(lds1i(RZ_BAR(limit)))) {
+            sts1(RZ_BAR(limit), 0);
+            return false;
         }
     }
 }
-__device__ __forceinline__ bool wait_warp(uint32_t bar, unsigned par, uint32_t bars, unsigned *err)
+__device__ __forceinline__ bool wait_warp(uint32_t bar, unsigned par, uint32_t bars)
 {
     // All lanes wait for the same barrier: lanes that wait for different ones drift apart, and what follows (tcgen05.ld, products
     // issued for the warp) needs the warp together.
-    const bool ok = __all_sync(0xffffffffu, wait_one(bar, par, bars, err));
+    const bool ok = __all_sync(0xffffffffu, wait_one(bar, par, bars));
     __syncwarp();
     return ok;
 }
@@ -604,7 +600,6 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         }
         mbar_init(&b.done[0], 1);
         mbar_init(&b.done[1], 1);
-        b.gave_up = 0;
         b.limit = a.stall && blockIdx.x == 0 ? a.stall : kWaitLimit / 8;
         fence_mbar_init();
         tma_prefetch_desc(&a.map1);
@@ -667,9 +662,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     const bool rb = test_phase(RZ_BAR(b_full) + 8 * pb.slot(), pb.par());
                     const bool rd = entry > 0 || test_phase(RZ_BAR(d_empty) + 8 * pd.slot(), pd.par() ^ 1u);
                     if (!__all_sync(0xffffffffu, ra && rb && rd)) {
-                        if (entry == 0 && !(ok = wait_warp(RZ_BAR(d_empty) + 8 * pd.slot(), pd.par() ^ 1u, bars, g.err))) break;
-                        if (!(ok = wait_warp(RZ_BAR(b_full) + 8 * pb.slot(), pb.par(), bars, g.err))) break;
-                        if (!again && !(ok = wait_warp(RZ_BAR(a_full) + 32 * mt + 8 * at.slot(), at.par(), bars, g.err))) break;
+                        if (entry == 0 && !(ok = wait_warp(RZ_BAR(d_empty) + 8 * pd.slot(), pd.par() ^ 1u, bars))) break;
+                        if (!(ok = wait_warp(RZ_BAR(b_full) + 8 * pb.slot(), pb.par(), bars))) break;
+                        if (!again && !(ok = wait_warp(RZ_BAR(a_full) + 32 * mt + 8 * at.slot(), at.par(), bars))) break;
                     }
                     fence_after();
                     const uint32_t ta = tmem + C::kColA + (mt * C::kSlotsA + at.slot()) * C::kWidthA;
@@ -722,7 +717,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     const int y0 = static_cast<int>(e * g.out_dim + static_cast<int64_t>(rt) * (kSwiglu ? 128 : 256));
                     for (int sb = first; sb < end && ok; ++sb) {
                         for (int mt = 0; mt < 2; ++mt) {
-                            if (!(ok = wait_one(RZ_BAR(raw_empty) + 8 * p.s, p.par ^ 1u, bars, g.err))) break;
+                            if (!(ok = wait_one(RZ_BAR(raw_empty) + 8 * p.s, p.par ^ 1u, bars))) break;
                             if (!stalled || issued > 0) {
                                 expect_tx(RZ_BAR(raw_full) + 8 * p.s, kRawBytes);
                                 copy_box(sm32 + C::off_raw + p.s * kRawBytes, kSwiglu && mt ? &a.map2 : &a.map1, sb * 144,
@@ -737,7 +732,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                     for (int sb = first; sb < end && ok; ++sb) {
                         const uint8_t *from = a.pack + (cell0 + sb) * C::kCellB;
                         for (int entry = 0; entry < C::kEntries; ++entry) {
-                            if (!(ok = wait_one(RZ_BAR(b_empty) + 8 * p.s, p.par ^ 1u, bars, g.err))) break;
+                            if (!(ok = wait_one(RZ_BAR(b_empty) + 8 * p.s, p.par ^ 1u, bars))) break;
                             const uint32_t bytes = C::kStack ? C::kSlotB : entry == 0 ? C::kMinsB : C::kBytesB;
                             expect_tx(RZ_BAR(b_full) + 8 * p.s, bytes);
                             copy_bulk(sm32 + C::off_b + p.s * C::kSlotB, from, bytes, RZ_BAR(b_full) + 8 * p.s);
@@ -778,7 +773,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
         unsigned before = turn;  // side by side: parity of the phase in which the other group's use of a slot is read
         bool ok = true;
         for (int64_t k = C::kStack ? turn : 0; k < blocks && ok; k += C::kStack ? 2 : 1) {
-            if (!(ok = wait_warp(RZ_BAR(raw_full) + 8 * praw.slot(), praw.par(), bars, g.err))) break;
+            if (!(ok = wait_warp(RZ_BAR(raw_full) + 8 * praw.slot(), praw.par(), bars))) break;
             const uint32_t raw = sm32 + C::off_raw + praw.slot() * kRawBytes + wrow * 144;
             const uint4 hd = lds4(raw);
             const bool any_wide = __any_sync(0xffffffffu, mins_are_unit(hd.x));
@@ -790,9 +785,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             for (; use < C::kUses; use += C::kStack ? 1 : 2) {
                 const bool mins = !C::kStack && use == 0;  // the mins alone
                 if constexpr (C::kStack) {
-                    if (!(ok = wait_warp(RZ_BAR(a_empty) + 32 * mt + 8 * (use + 2 * turn), before ^ 1u, bars, g.err))) break;
+                    if (!(ok = wait_warp(RZ_BAR(a_empty) + 32 * mt + 8 * (use + 2 * turn), before ^ 1u, bars))) break;
                 } else {
-                    if (!(ok = wait_warp(RZ_BAR(a_empty) + 32 * mt + 8 * pa.slot(), pa.par() ^ 1u, bars, g.err))) break;
+                    if (!(ok = wait_warp(RZ_BAR(a_empty) + 32 * mt + 8 * pa.slot(), pa.par() ^ 1u, bars))) break;
                 }
                 fence_after();
                 const unsigned slot = C::kStack ? use : pa.slot();
@@ -824,7 +819,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                             tm_store8(ta + 32 * cc + 16 + 8 * half, hi);
                         }
                     }
-                    if (any_wide) shrink_codes<32 * C::kChunks>(ta, head_of(lds4(raw).x).shrink());
+                    if (any_wide) shrink_codes<32 * C::kChunks>(ta, C::kStack ? mins_of.f : head_of(lds4(raw).x).shrink());
                 }
                 if (C::kStack || mins) {
                     const uint4 h = C::kStack ? hd : lds4(raw);
@@ -884,11 +879,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     if (mt == 0) {
-                        ok = wait_warp(RZ_BAR(h_full) + 8 * ph.slot(), ph.par(), bars, g.err) &&
-                             wait_warp(RZ_BAR(cs_full) + 8 * ph.slot(), ph.par(), bars, g.err);
+                        ok = wait_warp(RZ_BAR(h_full) + 8 * ph.slot(), ph.par(), bars) &&
+                             wait_warp(RZ_BAR(cs_full) + 8 * ph.slot(), ph.par(), bars);
                         if (!ok) break;
                     }
-                    if (!(ok = wait_warp(RZ_BAR(d_full) + 8 * pd.slot(), pd.par(), bars, g.err))) break;
+                    if (!(ok = wait_warp(RZ_BAR(d_full) + 8 * pd.slot(), pd.par(), bars))) break;
                     fence_after();
                     const float gs = lds1f(sm32 + C::off_g + 4 * ((ph.slot() * 2 + mt) * 128 + wrow));
                     const uint32_t cs = sm32 + C::off_cs + 4 * (ph.slot() * N + col0);
@@ -982,7 +977,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
     }
     fence_before();
     __syncthreads();
+    if (tid == 0 && gave_up(bars)) set_error(g.err, DEV_TIMEOUT_MOE);
     if (warp == 0) {
+        __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(b.tmem) : "memory");
     }
