@@ -37,9 +37,10 @@
 //   8 warps      add up: a thread has a weight row of both matrices and half of the columns
 // Few rows (kN <= 32): the two pieces of B stand side by side as 2 kN columns, which halves the instructions.
 //
-// Bound and measured.  Tiles of 16 and 32: issue slots, for unpacking (72% are taken; 16 tokens of 2 in 8 experts, gate and up 4096 > 14336:
-// 126 us, 4.2 TB/s; 129 of 8 in 128, 2048 > 768: 69 us, 3.3 TB/s).  Tiles of 128: the tensor cores, 61% of the time (1024 tokens) at 2.06 times
-// the formula's products (4096 of 2 in 8, 4096 > 14336: 3016 us, 638 TFLOP/s of the formula's), and accumulators that are read before a matrix's
+// Bound and measured.  Tiles of 16 and 32: issue slots, for unpacking (77% are taken; 16 tokens of 2 in 8 experts, gate and up 4096 > 14336:
+// 114 us, 4.6 TB/s; 129 of 8 in 128, 2048 > 768: 63 us, 3.6 TB/s); code in those loops that is not even run costs (6% what stood there
+// for the rare unit of the mins, 4% longer waits).  Tiles of 128: the tensor cores, 63% of the time (1024 tokens) at 2.06 times
+// the formula's products (4096 of 2 in 8, 4096 > 14336: 2930 us, 657 TFLOP/s of the formula's), and accumulators that are read before a matrix's
 // next super-block: tensor memory is full.
 //
 // Every wait is bounded; after one that runs out every role stops, copies and products in flight
@@ -1068,24 +1069,24 @@ cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &g, int columns, void *workspac
 // Tiles by the rows that an expert has on average (us in a graph, tiles of 16 | 32 | 128 rows; experts chosen evenly, and unevenly: logits
 // with a normal part of their own for each expert).  0: fewer rows than experts, which are for the integer dots.
 //   gate and up, 2 of 8 experts of 4096 > 14336
-//      6 rows: 128, 127 | 141, 139;   8 rows: 128, 138 | 141, 139;   10 rows: 138, 156 | 141, 141
-//      75 rows: 395, 384 | 376, 490;  100 rows: 481, 495 | 382, 520;  128 rows: 591, 585 | 526, 554
+//      6 rows: 114, 114 | 128, 127;   8 rows: 115, 123 | 128, 127;   10 rows: 123, 140 | 128, 128
+//      75 rows: 355, 347 | 366, 476;  100 rows: 435, 447 | 371, 507;  128 rows: 535, 528 | 514, 541
 //   gate and up, 8 of 64 experts of 2048 > 1024
-//      8 rows: 53, 53 | 61, 48;  12 rows: 53, 63 | 61, 60;  80 rows: 143, 143 | 151, 185;  96 rows: 159, 159 | 152, 187;  128 rows: 202, 207 | 199, 222
-//   down, 8 of 64, 1024 > 2048, half unevenly:  8 rows: 36 | 40;  64 rows: 71 | 93;  128 rows: 120 | 133;  160 rows: 147 | 152;  512 rows: 416 | 370
+//      8 rows: 49, 48 | 57, 45;  12 rows: 49, 58 | 57, 56;  80 rows: 131, 131 | 146, 180;  96 rows: 146, 146 | 147, 183;  128 rows: 185, 190 | 194, 216
+//   down, 8 of 64, 1024 > 2048, half unevenly:  8 rows: 33 | 39;  64 rows: 68 | 89;  128 rows: 114 | 128;  160 rows: 139 | 147;  512 rows: 395 | 356
 int moe_tiles(int64_t n_pairs, int n_experts, bool gate_up)
 {
     const int64_t rows = n_pairs / n_experts;
-    return rows < 1 ? 0 : rows <= 10 ? 16 : rows < (gate_up ? 96 : 160) ? 32 : 128;
+    return rows < 1 ? 0 : rows <= 10 ? 16 : rows < (gate_up ? 128 : 192) ? 32 : 128;
 }
 
 // The tiles, or 0, integer dots, where they would be tiles of 16 and rows and weights are so few that their time is less.  In us, of 304 CTAs side
 // by side, each a round of 8 super-blocks after the other; and of 152, by super-block, of the experts that are met if all
 // are as likely, after some 17 us for B's pieces, starts and ends.  Measured (dots | tiles of 16):
-//   gate and up, 2 of 8, 4096 > 14336:  1 row 86 | 79;  1.5 rows 126 | 98;  2 rows 165 | 108;   8 of 64, 2048 > 1024:  1 row 33 | 36;
-//   1.5 rows 46 | 41;  2 rows 59 | 41;   8 of 128, 2048 > 768:  1 row 46 | 46;  1.5 rows 67 | 55
-//   down, 2 of 8, 14336 > 4096:  1 row 46 | 50;  1.5 rows 66 | 61;  2 rows 84 | 62;   8 of 64, 1024 > 2048:  1 row 37 | 27;
-//   4 of 16, 4864 > 896:  1 row 12 | 23;  2 rows 18 | 26;  3 rows 26 | 26;   2 of 8, 512 > 1024:  2 rows 6 | 11;   1 of 4, 768 > 512:  3 rows 3 | 12
+//   gate and up, 2 of 8, 4096 > 14336:  1 row 86 | 71;  1.5 rows 126 | 88;  2 rows 165 | 97;   8 of 64, 2048 > 1024:  1 row 32 | 33;
+//   1.5 rows 46 | 38;  2 rows 59 | 38;   8 of 128, 2048 > 768:  1 row 46 | 42;  1.5 rows 67 | 51
+//   down, 2 of 8, 14336 > 4096:  1 row 46 | 45;  1.5 rows 66 | 56;  2 rows 83 | 56;   8 of 64, 1024 > 2048:  1 row 37 | 26;
+//   4 of 16, 4864 > 896:  1 row 12 | 22;  2 rows 18 | 25;  3 rows 26 | 25;   2 of 8, 512 > 1024:  2 rows 6 | 11;   1 of 4, 768 > 512:  3 rows 3 | 11
 int moe_columns(int64_t n_pairs, int n_experts, int top_k, int64_t out_dim, int64_t in_dim, bool gate_up)
 {
     const int columns = moe_tiles(n_pairs, n_experts, gate_up);
@@ -1095,7 +1096,7 @@ int moe_columns(int64_t n_pairs, int n_experts, int top_k, int64_t out_dim, int6
     const double ctas = static_cast<double>(gate_up ? n_pairs : n_pairs / top_k) * ((out_dim + of_cta - 1) / of_cta);
     const double dots = 3.0 + std::max(1.0, ctas / 304) * (gate_up ? 2 : 1) * (0.8 + 1.5 * ceil(nsb / 8));
     const double items = met * ((out_dim + (gate_up ? 127 : 255)) / (gate_up ? 128 : 256));
-    return dots <= 17.0 + 1.2 * nsb * std::max(gate_up ? 1.0 : 0.25, items / 152) ? 0 : columns;
+    return dots <= 17.0 + nsb * std::max(gate_up ? 1.0 : 0.25, items / 152) ? 0 : columns;
 }
 
 // Parts of in_dim are for products that may come to fewer than two items an SM.
