@@ -51,6 +51,7 @@
 #include <algorithm>
 
 #include "mma_f16.cuh"
+#include "moe_tiles.h"
 #include "rz_common.cuh"
 #include "rz_kernels.h"
 
@@ -325,13 +326,6 @@ __device__ __forceinline__ bool mins_are_unit(uint32_t word)
     return __hgt(m, __hmul(d, __ushort_as_half(0x7000)));
 }
 
-// The most tiles that so many rows of so many experts can have.
-template <int N>
-__host__ __device__ constexpr int64_t max_tiles(int64_t n_pairs, int n_experts)
-{
-    return n_pairs / N + (n_pairs < n_experts ? n_pairs : n_experts);
-}
-
 // Whether a phase is complete, at once.
 __device__ __forceinline__ bool test_phase(uint32_t bar, unsigned par)
 {
@@ -346,44 +340,25 @@ __device__ __forceinline__ bool test_phase(uint32_t bar, unsigned par)
     return ok != 0;
 }
 
-// Tiles of kN rows before each expert, by one warp; returns how many there are.
+// Tiles of kN rows before each expert, cut to the workspace's (moe_tiles.h), by one warp.
 template <int N>
-__device__ __forceinline__ int tiles_before(const MoeGemvArgs &g, int *cum, int lane)
+__device__ __forceinline__ void tiles_before(const MoeGemvArgs &g, int *cum, int lane)
 {
+    const int most = static_cast<int>(moe_most_tiles(g.n_pairs, g.n_experts, N));
     int base = 0;
     for (int e0 = 0; e0 < g.n_experts; e0 += 32) {
         const int e = e0 + lane;
-        int own = 0;
-        if (e < g.n_experts) {
-            const int lo = g.offsets[e], hi = g.offsets[e + 1];
-            if (lo >= 0 && hi > lo && hi <= g.n_pairs) own = (hi - lo + N - 1) / N;
-        }
+        const int own = e < g.n_experts ? moe_expert_tiles(g.offsets[e], g.offsets[e + 1], g.n_pairs, N) : 0;
         int v = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += u;
         }
-        if (e < g.n_experts) cum[e] = base + v - own;
-        base += __shfl_sync(0xffffffffu, v, 31);
+        if (e < g.n_experts) cum[e] = moe_cut(base + v - own, most);
+        base = moe_cut(base + __shfl_sync(0xffffffffu, v, 31), most);
     }
-    // offsets that overlap could ask for more tiles than the workspace holds
-    base = min(base, static_cast<int>(max_tiles<N>(g.n_pairs, g.n_experts)));
     if (lane == 0) cum[g.n_experts] = base;
-    return base;
-}
-// The expert of tile i.
-__device__ __forceinline__ int expert_of(int i, const int *cum, int n_experts)
-{
-    int lo = 0, hi = n_experts;  // cum[lo] <= i < cum[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= i)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
 }
 
 // B: a CTA has a tile and some of its super-blocks, a warp a row's super-block at a time, a lane 8 codes.
@@ -400,7 +375,7 @@ __global__ void __launch_bounds__(kPackThreads) moe_pack_kernel(const MoeGemvArg
     __syncthreads();
     const int tile = blockIdx.x;
     if (tile >= cum[g.n_experts]) return;
-    const int e = expert_of(tile, cum, g.n_experts), first = g.offsets[e] + (tile - cum[e]) * N, end = g.offsets[e + 1];
+    const int e = moe_expert_of(tile, cum, g.n_experts), first = g.offsets[e] + (tile - cum[e]) * N, end = g.offsets[e + 1];
     for (int c = tid; c < N; c += kPackThreads) {
         int r = -1;  // the row of x, -1 beyond the expert's
         if (first + c < end) {
@@ -703,15 +678,12 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             int64_t issued = 0, issued_h = 0;
             bool ok = true;
             for (int i = 0; i < my_items && ok; ++i) {
-                // tiles of outputs after one another, the expert's tiles of rows within
                 int64_t it = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
                 const int part = parts > 1 ? static_cast<int>(it / whole) : 0;
                 it -= part * whole;
                 const int first = part * per, end = min(nsb, first + per);
-                const int e = expert_of(static_cast<int>(it / row_tiles), cum, g.n_experts);
-                const int tiles = cum[e + 1] - cum[e];
-                const int64_t at = it - static_cast<int64_t>(cum[e]) * row_tiles;
-                const int rt = static_cast<int>(at / tiles), tile = static_cast<int>(at - static_cast<int64_t>(rt) * tiles);
+                const MoeItem item = moe_item(it, row_tiles, cum, g.n_experts);
+                const int e = item.expert, rt = item.row_tile, tile = item.tile;
                 if (weights) {
                     const int row = g.offsets[e] + tile * N;
                     sts4(sm32 + C::off_item + 16 * (i % kItems), row, min(N, g.offsets[e + 1] - row), rt, part);
@@ -1011,7 +983,7 @@ namespace {
 template <int N>
 int64_t pack_bytes(int64_t n_pairs, int n_experts, int64_t in_dim)
 {
-    return max_tiles<N>(n_pairs, n_experts) * (in_dim / 256) * (Cfg<N>::kCellB + N * 4);
+    return moe_most_tiles(n_pairs, n_experts, N) * (in_dim / 256) * (Cfg<N>::kCellB + N * 4);
 }
 
 template <int N>
@@ -1021,7 +993,7 @@ cudaError_t launch_all(const MoeGemvArgs &g, void *workspace, cudaStream_t s)
     TcArgs a{};
     a.g = g;
     const int nsb = g.in_dim / 256;
-    const int64_t tiles = max_tiles<N>(g.n_pairs, g.n_experts);
+    const int64_t tiles = moe_most_tiles(g.n_pairs, g.n_experts, N);
     uint8_t *pack = static_cast<uint8_t *>(workspace);
     float *col_scale = reinterpret_cast<float *>(pack + tiles * nsb * C::kCellB);
     a.pack = pack;
