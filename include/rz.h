@@ -589,10 +589,11 @@ rz_status rz_decode_layer_paged(const float *input, const rz_layer_weights *w, c
  *
  * Row r of a plan is one (token, choice): the rows of expert e are offsets[e] .. offsets[e + 1], in
  * the order of their tokens.  All of a plan is in device memory, so that one captured graph serves every
- * step.  A plan may also come from elsewhere; offsets outside [0, n_tokens * top_k] make an expert have no
- * rows, a row or place outside it records RZ_ERR_DEVICE and reads row 0 or is left out, and offsets that
- * overlap or decrease give undefined values.  Calls that share a workspace or write one plan must not overlap on
- * the GPU, captured ones among them.
+ * step.  A plan may also come from elsewhere.  Offsets outside [0, n_tokens * top_k] or decreasing ones make an expert
+ * have no rows.  What is not in the plan's bounds records RZ_ERR_DEVICE: a row outside [0, n_tokens * top_k] reads
+ * row 0, a choice whose place is not among the rows of its expert is left out of the token's sum.  Offsets that
+ * overlap give undefined values.  Calls that share a workspace or write one plan must not overlap on the GPU,
+ * captured ones among them.
  * ---------------------------------------------------------------------------
  */
 typedef struct {

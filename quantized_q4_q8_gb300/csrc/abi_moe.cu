@@ -160,11 +160,13 @@ cudaError_t run_down(const void *w_down, const void *h_q8, const rz_moe_plan *p,
     c.o = a.y;
     c.experts = p->experts;
     c.places = p->places;
+    c.offsets = p->offsets;
     c.weights = p->weights;
     c.residual = residual;
     c.y = y;
     c.out_dim = static_cast<int>(out_dim);
     c.out_pad = static_cast<int>(out_pad);
+    c.n_experts = p->n_experts;
     c.top_k = p->top_k;
     c.n_pairs = a.n_pairs;
     c.err = a.err;

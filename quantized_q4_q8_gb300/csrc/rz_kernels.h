@@ -369,10 +369,10 @@ constexpr int moe_down_quads(int top_k) { return top_k >= 8 ? 1 : 8 / top_k; }  
 struct MoeCombineArgs {
     const float *o;  // [*parts][n_pairs][out_dim]
     const int32_t *parts;  // or nullptr: 1
-    const int32_t *experts, *places;
+    const int32_t *experts, *places, *offsets;
     const float *weights, *residual;
     float *y;        // [n_tokens][out_pad]
-    int out_dim, out_pad, top_k, n_pairs;
+    int out_dim, out_pad, n_experts, top_k, n_pairs;
     unsigned *err;
 };
 // Both in one launch, with integer dots (a.y is not used).

@@ -48,3 +48,55 @@ def test_overlapping_offsets(rz, n, E, out_dim):
         for r in (room, room2):
             assert bool((r[:4 << 20] == fill).all()) and bool((r[-(4 << 20):] == fill).all())
     assert rz.check_device_error() == (0, 0)
+
+
+# rows, experts, choices, outputs: integer dots, then tiles of 16, 32 and 128 rows (of in_dim 512; parts of in_dim are the next)
+DOWNS = [(5, 8, 2, 96, 512), (40, 8, 2, 2208, 512), (200, 8, 2, 640, 512), (800, 8, 2, 384, 512), (33, 8, 2, 1000, 4864)]
+
+
+@pytest.mark.parametrize("T,E,k,out_dim,in_dim", DOWNS)
+@pytest.mark.parametrize("bad", ["past the rows", "below 0", "decreasing", "a place of another expert", "no expert", "no place"])
+def test_down_of_bad_plans(rz, T, E, k, out_dim, in_dim, bad):
+    """An expert whose offsets are none has no rows, and a place that is not among its expert's is left out: both are reported, and
+    nothing of the workspace shows."""
+    rng = np.random.default_rng(T + 1)
+    plan, expert = make_plan(rz, rng, T, E, k, idle=0.2)
+    w = q4k(rng, E, out_dim, in_dim=in_dim)
+    q, d, s = activations(rng, T * k, in_dim)
+    res = rng.normal(size=(T, out_dim)).astype(np.float32)
+    off, ids, places = host(plan.offsets).copy(), host(plan.experts).copy().reshape(-1), host(plan.places).copy()
+    full = np.flatnonzero(np.diff(off))
+    last, some = int(full[-1]), int(full[len(full) // 2])
+    if bad == "past the rows":
+        off[last + 1:] = T * k + 3
+        lost = ids == last
+    elif bad == "below 0":
+        off[:full[0] + 1] = -1
+        lost = ids == full[0]
+    elif bad == "decreasing":
+        off[some + 1:] = off[some] - 1  # `some` ends before it starts, those behind it have none
+        lost = ids >= some
+    else:
+        lost = np.zeros(T * k, bool)
+        pair = int(np.flatnonzero(ids == last)[-1])
+        lost[pair] = True
+        if bad == "a place of another expert":
+            places[pair] = off[last] - 1
+        elif bad == "no expert":
+            ids[pair] = -1
+        else:
+            places[pair] = -1
+    plan.offsets.copy_(dev(off))
+    plan.experts.copy_(dev(ids).view(T, k))
+    plan.places.copy_(dev(places))
+    keep = np.where(lost, -1, host(plan.places))
+    ref, tol = R.down(R.weights(w), R.q8_values(q, d), keep, expert, host(plan.weights).astype(np.float64), res)
+    room, ws = in_the_middle(rz.moe_down_workspace_bytes(T, E, k, out_dim, in_dim))
+    args = dev(w), dev(R.q8_buffer(q, d, s)), plan, out_dim, in_dim
+    got = []
+    for fill in (0, 127, 255):
+        room.fill_(fill)
+        got.append(rz.moe_down(*args, residual=dev(res), ws=ws if ws.numel() else None))
+        assert rz.check_device_error() == (7, 0x203)
+    within(host(got[0]), ref, tol, "y")
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
