@@ -616,7 +616,8 @@ typedef struct {
  *   y         f32 [m][n_pad] output, or NULL.  May be x or delta (not sum).
  *   q8        Q8_1 of m rows of n_pad, of the y as it is rounded; or NULL.  (One of y, q8 is given.)  Its scales are
  *             max|y| times the f32 nearest to 1/127, at most an ulp from rz_q8_1_quantize's quotient; codes
- *             and sums follow from them as there.
+ *             and sums follow from them as there.  A block with a NaN has d = s = NaN (rz_q8_1_quantize leaves
+ *             it out of the largest value), so that what is made of it is NaN too.
  *   n_pad a multiple of 32 up to 16384; all buffers 16-byte aligned.
  * y is the f32 nearest to the formula's value of s but for about one value in 2^20 (sums and products are
  * carried as sums of two f32), so that codes do not depend on the order of a sum.  Squares of s stay in f32's range.
@@ -649,7 +650,7 @@ rz_status rz_moe_route(const float *logits, int64_t ld, const int32_t *row_seq, 
  *   w_gate, w_up  Q4_K [n_experts][inter][in_dim]     x_q8  Q8_1 of n_tokens rows of in_dim
  *   h         f32 [n_tokens * top_k][inter] output, in the plan's order of rows, or NULL
  *   h_q8      Q8_1 of n_tokens * top_k rows of inter (rz_moe_down's input): exactly the quantisation of
- *             h; or NULL (inter % 32 == 0)
+ *             h, but d = s = NaN for a block with a NaN; or NULL (inter % 32 == 0)
  *   workspace rz_moe_swiglu_workspace_bytes bytes; no initialisation; may be NULL where that is 0
  *   in_dim % 256 == 0; all 16-byte aligned.  Rows behind offsets[n_experts] stay as they were.
  * Sums are f32-accurate: exact integer dots for few rows of an expert, else the tensor cores, where

@@ -920,9 +920,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                         for (int i = 0; i < 8; ++i, to += g.out_dim) {
                             if (i0 + i >= m) break;
                             const float v = sum[0][i];
-                            const uint32_t key = isnan(v) ? 0u : __float_as_uint(fabsf(v)) + 1u;
-                            const uint32_t top = __reduce_max_sync(0xffffffffu, key);
-                            const float d = top ? __fdiv_rn(__uint_as_float(top - 1u), 127.0f) : NAN;
+                            // as in moe_gemv.cu: a block with a NaN has the scale NaN
+                            const float d = __fdiv_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v)))), 127.0f);
                             const int code = q8_code(v, q8_scale(d));
                             const int total = __reduce_add_sync(0xffffffffu, code);
                             g.yq[to] = static_cast<int8_t>(code);

@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_swiglu_kernel(const MoeGemvAr
         const float v = o < a.out_dim ? out[lane] : 0.0f;
         if (a.y && o < a.out_dim) a.y[at] = v;
         if (a.yq) {  // out_dim is a multiple of 32
-            const float d = __fdiv_rn(warp_max(fabsf(v)), 127.0f);
+            // as integers, which keep the order of the sizes and put NaN above them: a block with one has the scale NaN
+            const float d = __fdiv_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v)))), 127.0f);
             const int code = q8_code(v, q8_scale(d)), total = warp_sum_int(code);
             a.yq[at] = static_cast<int8_t>(code);
             if (lane == 0) {

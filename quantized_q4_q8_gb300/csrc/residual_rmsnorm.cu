@@ -61,6 +61,14 @@ __device__ __forceinline__ Two inverse_rms(Two sum, float n, float eps)
     return {r, __fmul_rn(0.5f * r, res)};
 }
 
+// The larger, NaN if one is: a block with a NaN has the scale NaN.
+__device__ __forceinline__ float max_or_nan(float a, float b)
+{
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
 template <int kThreads, int kVec>
 __global__ void __launch_bounds__(kThreads) residual_rmsnorm_kernel(const float *x, const float *delta, const float *__restrict__ gamma,
                                                                     float *sum, float *y, int8_t *__restrict__ q, float *__restrict__ qd,
@@ -127,9 +135,9 @@ __global__ void __launch_bounds__(kThreads) residual_rmsnorm_kernel(const float 
         if (in && sum) *reinterpret_cast<float4 *>(sum + at + i) = make_float4(s[k][0], s[k][1], s[k][2], s[k][3]);
         if (in && y) *reinterpret_cast<float4 *>(y + at + i) = make_float4(v[0], v[1], v[2], v[3]);
         if (q) {
-            float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+            float top = max_or_nan(max_or_nan(fabsf(v[0]), fabsf(v[1])), max_or_nan(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int o = 4; o > 0; o >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float d = __fmul_rn(top, 1.0f / 127.0f);  // within an ulp of the division that rz_q8_1_quantize makes
             const Q8Scale qsc = q8_scale(d);
             uint32_t word = 0;

@@ -100,3 +100,50 @@ def test_down_of_bad_plans(rz, T, E, k, out_dim, in_dim, bad):
         assert rz.check_device_error() == (7, 0x203)
     within(host(got[0]), ref, tol, "y")
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+# ---------------------------------------------------------------- values that are no numbers
+@pytest.mark.parametrize("T,inter", [(4, 256), (31, 2560), (140, 256), (620, 256)])  # integer dots, and tiles of 16, 32 and 128 rows
+def test_no_number_reaches_the_q8_of_its_block(rz, T, inter):
+    """One value of h is NaN: so are the scale and the sum of its block of 32, not those of the others, and what is made of it."""
+    rng = np.random.default_rng(T)
+    E, k, n = 3, 1, 512
+    plan, expert = make_plan(rz, rng, T, E, k, idle=0.0)
+    gate, up, down = q4k(rng, E, inter, in_dim=n), q4k(rng, E, inter, in_dim=n), q4k(rng, E, n, in_dim=inter)
+    x = dev(R.q8_buffer(*activations(rng, T, n)))
+    bad = gate.copy()
+    bad[1, 33, 0, 0:2] = np.float16(np.nan).reshape(1).view(np.uint8)
+    meets, block = expert == 1, np.arange(inter // 32) == 1
+    assert meets.any()
+    q8 = [torch.zeros(rz.q8_1_size(T, inter), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    h0 = host(rz.moe_swiglu(dev(gate), dev(up), x, plan, inter, n, out_q8=q8[0]))
+    h1 = host(rz.moe_swiglu(dev(bad), dev(up), x, plan, inter, n, out_q8=q8[1]))
+    keep = np.ones_like(h0, bool)
+    keep[meets, 33] = False
+    assert np.isnan(h1[~keep]).all() and np.array_equal(h1[keep], h0[keep])
+    (q0, d0, s0), (q1, d1, s1) = (R.q8_parts(host(b), T, inter) for b in q8)
+    hit = meets[:, None] & block
+    assert np.isnan(d1[hit]).all() and np.isnan(s1[hit]).all()
+    assert np.array_equal(d1[~hit], d0[~hit]) and np.array_equal(s1[~hit], s0[~hit])
+    same = np.repeat(~hit, 32, -1)
+    assert np.array_equal(q1[same], q0[same])
+    # through the whole FFN, its tokens and no other
+    logits = dev(np.where(np.arange(E) == host(plan.experts), 1, 0).astype(np.float32))
+    out = [host(rz.moe_ffn(logits, x, dev(g), dev(up), dev(down), rz.MoePlan(T, E, k), n, n, inter)) for g in (gate, bad)]
+    token = host(plan.experts)[:, 0] == 1
+    assert np.isfinite(out[0]).all() and np.isnan(out[1][token]).all() and np.array_equal(out[1][~token], out[0][~token])
+
+
+@pytest.mark.parametrize("m,n,n_pad", [(1, 96, 96), (3, 900, 1024), (2, 5000, 5120)])
+def test_no_number_reaches_the_norms_q8(rz, m, n, n_pad):
+    rng = np.random.default_rng(n)
+    x, gamma = rng.normal(size=(m, n_pad)).astype(np.float32), rng.uniform(0.5, 1.5, n).astype(np.float32)
+    bad = gamma.copy()
+    bad[70] = np.nan
+    (_, y0, b0), (_, y1, b1) = (rz.residual_rmsnorm(dev(x), None, dev(g), n, n_pad, 1e-6) for g in (gamma, bad))
+    y0, y1, hit = host(y0), host(y1), np.arange(n_pad // 32) == 2
+    assert np.isnan(y1[:, 70]).all() and np.array_equal(np.delete(y1, 70, 1), np.delete(y0, 70, 1))
+    (q0, d0, s0), (q1, d1, s1) = (R.q8_parts(host(b), m, n_pad) for b in (b0, b1))
+    assert np.isnan(d1[:, hit]).all() and np.isnan(s1[:, hit]).all()
+    assert np.array_equal(d1[:, ~hit], d0[:, ~hit]) and np.array_equal(s1[:, ~hit], s0[:, ~hit])
+    assert np.array_equal(q1[:, np.repeat(~hit, 32)], q0[:, np.repeat(~hit, 32)])
