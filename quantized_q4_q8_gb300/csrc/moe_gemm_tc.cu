@@ -22,8 +22,9 @@
 // sub-blocks come beside their codes and every other sub-block is centred, which costs nothing; in those of 128 the mins come first,
 // all codes are centred.  Off by 5.5 to 7e-7 of the values of a SwiGLU (1.2e-6 without either; the plain form in f32 0.6 to 1.7e-6).
 //
-// The scale g of a row is d.  Where dmin is over 2^13 times d (f16 would not hold r_j; d = 0 among them), g = dmin, and the codes are scaled by
-// d / dmin instead, rounded to f16: 2^-12 of codes that are less than an eighth of dmin.
+// The scale g of a row is d.  Where dmin is over 2^13 times d, f16 would not hold r_j: g = 2^p d, with p such that 2^12 <= dmin / g < 2^13, and codes
+// and r_j are scaled by 2^-p.  The least step of f16 is 2^-24, so that codes lose nothing up to p = 24, dmin = 2^37 d; beyond that (p is at
+// most 27, as f16 has no larger dmin and no smaller d) 36 d at most, 2^-33 of dmin.  With d = 0, g = dmin and the codes are 0.
 //
 // A super-block with a scale that is no number gives its row NaN (g), a block of x its column (B's pieces).
 //
@@ -307,11 +308,17 @@ __device__ __forceinline__ void wait_landed(uint32_t bar, unsigned par)
     }
 }
 
-// A super-block's two scales; wide: the mins' is the unit (see above).
+// A super-block's two scales; wide: the mins' is over 2^13 times the other (see above).
 struct Head {
     float d, dmin;
     bool wide, fine;
-    __device__ __forceinline__ float shrink() const { return wide && fine ? __half2float(__float2half_rn(__fdiv_rn(d, dmin))) : 1.0f; }
+    // 2^-p; 0 with d = 0
+    __device__ __forceinline__ float shrink() const
+    {
+        if (!wide || !fine) return 1.0f;
+        const uint32_t e = (__float_as_uint(__fdiv_rn(dmin, d)) >> 23) & 255u;  // 140 to 166
+        return d == 0.0f ? 0.0f : __uint_as_float((127u + 139u - e) << 23);
+    }
 };
 __device__ __forceinline__ Head head_of(uint32_t word)
 {
@@ -486,12 +493,13 @@ __device__ __forceinline__ uint32_t low_codes(uint32_t v, uint32_t sc, uint32_t 
     return kPlain ? hfma2u(v, sc, add) : hmul2u(hsub2u(v, 0x64086408u), sc);
 }
 
-// A slot's codes in the unit of the mins, of the rows where that is the unit: read back and written again.  Rare, and so apart: beside each
-// store it took 6 to 7% of the time of all tiles of 16 and 32 rows (instructions that are fetched and not executed).
+// A slot's codes times 2^-p, of the rows whose mins ask for it: read back and written again.  Rare, and so apart: beside each store it took
+// 6 to 7% of the time of all tiles of 16 and 32 rows (instructions that are fetched and not executed).  In two factors, as 2^-25 is none in f16.
 template <int kCols>
 __device__ __forceinline__ void shrink_codes(uint32_t at, float by)
 {
-    const uint32_t by2 = pack2(by, by);
+    const float first = fmaxf(by, 0x1p-14f), second = by < 0x1p-14f ? by * 0x1p14f : 1.0f;
+    const uint32_t first2 = pack2(first, first), second2 = pack2(second, second);
     tm_store_wait();
 #pragma unroll 1
     for (int c = 0; c < kCols; c += 8) {
@@ -499,7 +507,7 @@ __device__ __forceinline__ void shrink_codes(uint32_t at, float by)
         tm_load8(at + c, v);
         uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = hmul2u(__float_as_uint(v[i]), by2);
+        for (int i = 0; i < 8; ++i) o[i] = hmul2u(hmul2u(__float_as_uint(v[i]), first2), second2);
         tm_store8(at + c, o);
     }
 }
@@ -511,10 +519,16 @@ struct Mins {
     __device__ __forceinline__ Mins(const uint4 &hd, bool any_wide)
     {
         const Head head = head_of(hd.x);
-        const float ratio = head.wide ? 1.0f : head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
+        float ratio = head.d == 0.0f ? 0.0f : __fdiv_rn(head.dmin, head.d);
+        f = 1.0f;
+        g = head.d;
+        if (any_wide && head.wide) {
+            f = head.shrink();
+            ratio = head.d == 0.0f ? 1.0f : ratio * f;
+            g = head.d == 0.0f ? head.dmin : __fdiv_rn(head.d, f);
+        }
         by = head.fine ? -0.125f * ratio : 0.0f;
-        f = any_wide ? head.shrink() : 1.0f;
-        g = !head.fine ? NAN : head.wide ? head.dmin : head.d;
+        g = head.fine ? g : NAN;
     }
     // six-bit mins of sub-blocks 0-3 and 4-7
     static __device__ __forceinline__ uint32_t low(const uint4 &hd) { return hd.z & 0x3f3f3f3fu; }

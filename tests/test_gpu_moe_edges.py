@@ -147,3 +147,56 @@ def test_no_number_reaches_the_norms_q8(rz, m, n, n_pad):
     assert np.isnan(d1[:, hit]).all() and np.isnan(s1[:, hit]).all()
     assert np.array_equal(d1[:, ~hit], d0[:, ~hit]) and np.array_equal(s1[:, ~hit], s0[:, ~hit])
     assert np.array_equal(q1[:, np.repeat(~hit, 32)], q0[:, np.repeat(~hit, 32)])
+
+
+# ---------------------------------------------------------------- parts that are far apart
+@pytest.mark.parametrize("T,inter", [(3, 64), (31, 2560), (90, 64), (640, 64)])  # integer dots, and tiles of 16, 32 and 128 rows
+@pytest.mark.parametrize("d,dmin", [(2.0 ** -10, 9.0), (2.0 ** -14, 1.5), (3.1e-5, 33.0), (2.0 ** -14, 1000.0), (5e-7, 60.0), (1.2e-7, 8000.0),
+                                    (6e-8, 8000.0), (-3.1e-5, 33.0), (3.1e-5, -33.0)])
+@pytest.mark.parametrize("mins", ["none", "one", "all but one"])
+def test_codes_beside_a_large_scale_of_the_mins(rz, T, inter, d, dmin, mins):
+    """A scale of the mins 2^13 to 2^37 times the codes', where sub-blocks that x meets have no min: their codes are what a row is.  Usual
+    rows stand between."""
+    rng = np.random.default_rng(T + len(mins))
+    E, k, in_dim = 3, 1, 512
+    plan, expert = make_plan(rz, rng, T, E, k, idle=0.0)
+    w = q4k(rng, E, inter, in_dim=in_dim)
+    wide = np.arange(inter) % 5 != 4
+    w[..., 0:2] = np.float16(d).reshape(1).view(np.uint8)
+    w[..., 2:4] = w[..., 0:2]
+    w[:, wide, :, 2:4] = np.float16(dmin).reshape(1).view(np.uint8)
+    q, dd, _ = activations(rng, T, in_dim)
+    blocks = q.reshape(T, -1, 32)
+    at = np.arange(in_dim // 32)
+    if mins == "all but one":  # sub-block 1 has none, and x is 0 elsewhere
+        w[:, wide, :, 9] &= 0xc0
+        blocks[:, at % 8 != 1] = 0
+    else:  # the codes of the mins: bytes 8 to 11 and the upper halves of 12 to 15
+        w[:, wide, :, 8:12] = 0
+        w[:, wide, :, 12:16] &= 15
+        if mins == "one":  # the least there is, in sub-block 2 of the second super-block, where x is 0
+            w[:, wide, 1, 10] = 1
+            blocks[:, at == 10] = 0
+    dd = dd * np.float32(1 / (4000 * abs(float(np.float16(d)))))  # products of about 1
+    s = (dd * blocks.astype(np.float32).sum(-1)).astype(np.float32)
+    wv = R.weights(w)
+    h, tol = R.swiglu(wv, wv, R.q8_values(q, dd), host(plan.rows), expert, k)
+    out = host(rz.moe_swiglu(dev(w), dev(w), dev(R.q8_buffer(q, dd, s)), plan, inter, in_dim))
+    within(out, h, tol, "h")
+
+
+@pytest.mark.parametrize("n,E,out_dim", [(3, 8, 64)] + TILES)
+def test_codes_beside_the_largest_scale_of_the_mins(rz, n, E, out_dim):
+    """The least scale beside the largest: 2^40. What f16 steps cost is less than 2^-33 of the mins' scale for a weight."""
+    rng = np.random.default_rng(n)
+    in_dim, plan = 512, one_expert(rz, n, E, [0] + [n] * E)
+    for d, dmin in ((6e-8, 65504.0), (1.2e-7, 40000.0), (0.0, 65504.0)):
+        w = q4k(rng, 1, out_dim, in_dim=in_dim)
+        w[..., 0:2], w[..., 2:4] = (np.float16(v).reshape(1).view(np.uint8) for v in (d, dmin))
+        w[:, ::2, :, 8:12] = 0  # every other row without mins
+        w[:, ::2, :, 12:16] &= 15
+        q, dd, s = activations(rng, n, in_dim)
+        x = R.q8_values(q, dd)
+        ref, tol = R.down(R.weights(w), x, np.arange(n), np.zeros(n, int), np.ones((n, 1)), None)
+        y = host(rz.moe_down(dev(np.repeat(w, E, 0)), dev(R.q8_buffer(q, dd, s)), plan, out_dim, in_dim))
+        within(y, ref, tol + 2.0 ** -33 * dmin * np.abs(x).sum(-1, keepdims=True), (d, dmin))
