@@ -466,6 +466,15 @@ __global__ void __launch_bounds__(kPackThreads) moe_pack_kernel(const MoeGemvArg
     }
 }
 
+// silu(g) u without branches: e^-|g| <= 1 and a divisor of 1 .. 2, where the fast division is within 2 ulp.  Off by 11 half-ulps at most: 4 of
+// expf, 4 of the division, the roundings of g e, 1 + e and the product with u.  (g / (1 + e^-g), whose division has branches: 3145 instead of 2992 us,
+// 4096 tokens of 2 in 8 experts, 4096 > 14336; 89 instead of 77 us, 256 of 8 in 64, 2048 > 1024.)
+__device__ __forceinline__ float silu_mul_straight(float g, float u)
+{
+    const float e = expf(-fabsf(g));
+    return __fdividef(g >= 0.0f ? g : g * e, 1.0f + e) * u;
+}
+
 // A place in a ring of R slots and the parity of its phase.  kFew, where registers are short (tiles of 128 rows): one counter where
 // R is a power of two.  With barriers by 32-bit address 3198 to 3002 us (gate and up, 4096 tokens, 8 experts of 14336 x 4096, top 2);
 // tiles of 16 rows would lose 2% by the counter.
@@ -916,10 +925,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
             const int m = w.m - col0;
             int64_t to = static_cast<int64_t>(w.row + col0) * g.out_dim + o;
             if constexpr (kSwiglu) {
-                // In place first: half of the registers are free for what follows.  __expf is within 2 + 1.2 |g| ulp: 3% of the time less than
-                // expf at 4096 rows of 4096 > 14336, as this runs while no product does.
+                // in place first: half of the registers are free for what follows
 #pragma unroll
-                for (int i = 0; i < C::kHalf; ++i) sum[0][i] = in ? __fdividef(sum[0][i], 1.0f + __expf(-sum[0][i])) * sum[1][i] : 0.0f;
+                for (int i = 0; i < C::kHalf; ++i) sum[0][i] = in ? silu_mul_straight(sum[0][i], sum[1][i]) : 0.0f;
                 if (g.y && in) {
                     float *y = g.y + to;
 #pragma unroll

@@ -200,3 +200,33 @@ def test_codes_beside_the_largest_scale_of_the_mins(rz, n, E, out_dim):
         ref, tol = R.down(R.weights(w), x, np.arange(n), np.zeros(n, int), np.ones((n, 1)), None)
         y = host(rz.moe_down(dev(np.repeat(w, E, 0)), dev(R.q8_buffer(q, dd, s)), plan, out_dim, in_dim))
         within(y, ref, tol + 2.0 ** -33 * dmin * np.abs(x).sum(-1, keepdims=True), (d, dmin))
+
+
+def exact_gates(E, inter, in_dim):
+    """(gate, up, g): with x one code of 1 in front, gate row i gives g[i] <= 0 and up gives 1, both without any rounding."""
+    gate, up = np.zeros((2, E, inter, in_dim // 256, 144), np.uint8)
+    i = np.arange(inter)
+    sc, code = 1 + i % 63, 1 + i // 63 % 15
+    gate[:, :, 0, 0:2] = np.float16(-0.125).reshape(1).view(np.uint8)
+    up[:, :, 0, 0:2] = np.float16(1).reshape(1).view(np.uint8)
+    gate[:, :, 0, 4], gate[:, :, 0, 16] = sc, code
+    up[:, :, 0, 4], up[:, :, 0, 16] = 1, 1
+    return gate, up, -0.125 * (sc * code).astype(np.float64)
+
+
+def test_silu_of_exact_gates(rz):
+    """Gates that are exact, -0.125 to -118, so that only silu rounds.  In half-ulps, integer dots: e^-g within 2 ulp (4), an addition, a
+    division and the product with up (1 each); tensor cores: e^g within 2 ulp (4), its product with g and an addition (1 each), a division within
+    2 ulp (4), the product with up (1).  The same for every row."""
+    E, k, in_dim, inter = 3, 1, 256, 2560
+    gate, up, g = exact_gates(E, inter, in_dim)
+    with np.errstate(over="ignore"):
+        ref = g / (1 + np.exp(-g))
+    for T, half_ulps in ((2, 7), (31, 11), (90, 11), (640, 11)):  # integer dots, tiles of 16, 32 and 128 rows
+        tol = half_ulps * 2.0 ** -24 * np.abs(ref) + 2.7e-37  # e^88.73 and more is infinite in f32, where silu is 88.73 / 2^128
+        plan, _ = make_plan(rz, np.random.default_rng(T), T, E, k, idle=0.0)
+        q, d = np.zeros((T, in_dim), np.int8), np.zeros((T, in_dim // 32), np.float32)
+        q[:, 0], d[:, 0] = 1, 1
+        out = host(rz.moe_swiglu(dev(gate), dev(up), dev(R.q8_buffer(q, d, d)), plan, inter, in_dim))
+        assert np.array_equal(out, np.broadcast_to(out[0], out.shape))
+        within(out, np.broadcast_to(ref, out.shape), np.broadcast_to(tol, out.shape), T)
