@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) moe_gemm_tc_kernel(const 
                 }
                 ph.add(1);
             }
-            if (!ok || gave_up(bars)) break;
+            if (!ok) break;  // the same for the warp, as its lanes wait for one another below; else the sums are whole, whatever gave up since
             // ---- outputs: a warp's 32 rows lie side by side in each column's row of y
             struct {
                 int row, m, rt, part;

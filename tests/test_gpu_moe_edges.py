@@ -230,3 +230,32 @@ def test_silu_of_exact_gates(rz):
         out = host(rz.moe_swiglu(dev(gate), dev(up), dev(R.q8_buffer(q, d, d)), plan, inter, in_dim))
         assert np.array_equal(out, np.broadcast_to(out[0], out.shape))
         within(out, np.broadcast_to(ref, out.shape), np.broadcast_to(tol, out.shape), T)
+
+
+# ---------------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("T,E,out_dim", [(20, 4, 2304), (60, 4, 512), (300, 2, 512)])  # tiles of 16, 32 and 128 rows
+def test_waits_that_run_out_before_other_outputs(rz, T, E, out_dim):
+    """The same as with f32 outputs of gate and up, for their Q8_1 form and for the product back: reported, other CTAs' outputs whole, and
+    the next calls as before."""
+    rng = np.random.default_rng(T + 1)
+    k, in_dim = 2, 1024
+    plan, _ = make_plan(rz, rng, T, E, k, idle=0.0)
+    w, x = dev(q4k(rng, E, out_dim, in_dim=in_dim)), dev(R.q8_buffer(*activations(rng, T, in_dim)))
+    h8 = dev(R.q8_buffer(*activations(rng, T * k, in_dim)))
+    q8 = torch.zeros(rz.q8_1_size(T * k, out_dim), dtype=torch.uint8, device="cuda")
+
+    def gate_up():
+        rz.moe_swiglu(w, w, x, plan, out_dim, in_dim, out_q8=q8, want_h=False)
+        return q8[:T * k * out_dim].view(T * k, out_dim).clone()
+
+    for run, first in ((gate_up, 128), (lambda: rz.moe_down(w, h8, plan, out_dim, in_dim), 256)):
+        want = run()
+        assert rz.check_device_error() == (0, 0)
+        for limit in (1 << 10, 1 << 12, 1 << 14):
+            rz.rz_debug_stall_next_moe(limit)
+            got = run()
+            assert rz.check_device_error() == (5, 0x120)
+            assert torch.equal(got[:, first:], want[:, first:])
+            for _ in range(2):
+                assert torch.equal(run(), want)
+        assert rz.check_device_error() == (0, 0)
