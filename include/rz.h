@@ -653,8 +653,10 @@ rz_status rz_moe_route(const float *logits, int64_t ld, const int32_t *row_seq, 
  *             h, but d = s = NaN for a block with a NaN; or NULL (inter % 32 == 0)
  *   workspace rz_moe_swiglu_workspace_bytes bytes; no initialisation; may be NULL where that is 0
  *   in_dim % 256 == 0; all 16-byte aligned.  Rows behind offsets[n_experts] stay as they were.
- * Sums are f32-accurate: exact integer dots for few rows of an expert, else the tensor cores, where
- * activations enter with 22 bits and codes with every bit (where |dmin| is over 2^37 |d|, off by up to 2^-33 |dmin|).
+ * Sums are f32-accurate: exact integer dots for few rows of an expert, else the tensor cores.  There codes enter with
+ * every bit (where |dmin| is over 2^37 |d|, off by up to 2^-33 |dmin|), activations with 22 bits of the largest scale
+ * among the 256 values that share a super-block: where a block's scale is 2^-k of that, its values are off by up to
+ * 2^(k - 24) of its largest.  silu is within 11 half-ulps of the formula's.
  */
 size_t rz_moe_swiglu_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k, int64_t in_dim);
 rz_status rz_moe_swiglu(const void *w_gate, const void *w_up, const void *x_q8, const rz_moe_plan *plan, int64_t inter,

@@ -11,7 +11,10 @@
 // accumulation of 2 x 16 instructions of K = 16, and accumulators are read once for 256 weights:
 // products of the codes alone, exact in f16, would have to be read and scaled for each 32
 // (rz_q4k_q8_gemm: 344 TFLOP/s of the formula's operations).  A kernel before this one forms B's pieces,
-// once for a row of activations however many experts and tiles of outputs read it.
+// once for a (token, choice) row however many tiles of outputs read it: a token of k experts has its pieces formed and held k times.
+//
+// The pieces have 22 bits of the largest scale among the 256 values: with that between 1/2 and 1, f16 has steps of 2^-24, which a block whose scale
+// is 2^-k of it feels from k = 3 on (off by up to 2^(k - 24) of its largest value; the integer dots keep every bit).
 //
 // The rest of a weight, -dmin m or 8 d sc - dmin m, times the sum s of a block of x, goes into the same accumulators: A's
 // r_j = -m_j dmin / (8 d) (+ sc_j) and B's 8 s_j / 2^E, two f16 pieces each, all four products.
@@ -38,11 +41,11 @@
 //   8 warps      add up: a thread has a weight row of both matrices and half of the columns
 // Few rows (kN <= 32): the two pieces of B stand side by side as 2 kN columns, which halves the instructions.
 //
-// Bound and measured.  Tiles of 16 and 32: issue slots, for unpacking (77% are taken; 16 tokens of 2 in 8 experts, gate and up 4096 > 14336:
-// 114 us, 4.6 TB/s; 129 of 8 in 128, 2048 > 768: 63 us, 3.6 TB/s); code in those loops that is not even run costs (6% what stood there
-// for the rare unit of the mins, 4% longer waits).  Tiles of 128: the tensor cores, 63% of the time (1024 tokens) at 2.06 times
-// the formula's products (4096 of 2 in 8, 4096 > 14336: 2930 us, 657 TFLOP/s of the formula's), and accumulators that are read before a matrix's
-// next super-block: tensor memory is full.
+// Bound and measured, in a graph.  Tiles of 16 and 32: issue slots, for unpacking (over 70% are taken; 16 tokens of 2 in 8 experts, gate and up 4096 >
+// 14336: 113 us, 4.6 TB/s; 129 of 8 in 128, 2048 > 768: 63 us, 3.6 TB/s); code in those loops that is not even run costs (6% what stood there
+// for the rare scales of the mins, 4% longer waits).  Tiles of 128: the tensor cores, some 60% of the time (1024 tokens) at 34 instructions for the
+// formula's 16 (4096 of 2 in 8, 4096 > 14336: 2980 us, 645 TFLOP/s of the formula's; call by call 3300 us), and accumulators that are read before a
+// matrix's next super-block: tensor memory is full.  With the Q8_1 output, whose scales the warps that add up form: 119, 70 and 3670 us.
 //
 // Every wait is bounded; after one that runs out every role stops, copies and products in flight
 // are waited for, and tensor memory is freed.
@@ -1062,11 +1065,13 @@ cudaError_t launch_moe_gemm_tc(const MoeGemvArgs &g, int columns, void *workspac
 // Tiles by the rows that an expert has on average (us in a graph, tiles of 16 | 32 | 128 rows; experts chosen evenly, and unevenly: logits
 // with a normal part of their own for each expert).  0: fewer rows than experts, which are for the integer dots.
 //   gate and up, 2 of 8 experts of 4096 > 14336
-//      6 rows: 114, 114 | 128, 127;   8 rows: 115, 123 | 128, 127;   10 rows: 123, 140 | 128, 128
-//      75 rows: 355, 347 | 366, 476;  100 rows: 435, 447 | 371, 507;  128 rows: 535, 528 | 514, 541
+//      6 rows: 114, 114 | 127, 126;   8 rows: 115, 123 | 127, 126;   10 rows: 123, 140 | 127, 127
+//      75 rows: 354, 346 | 372, 482;  100 rows: 434, 444 | 375, 513;  128 rows: 533, 526 | 519, 547
 //   gate and up, 8 of 64 experts of 2048 > 1024
-//      8 rows: 49, 48 | 57, 45;  12 rows: 49, 58 | 57, 56;  80 rows: 131, 131 | 146, 180;  96 rows: 146, 146 | 147, 183;  128 rows: 185, 190 | 194, 216
-//   down, 8 of 64, 1024 > 2048, half unevenly:  8 rows: 33 | 39;  64 rows: 68 | 89;  128 rows: 114 | 128;  160 rows: 139 | 147;  512 rows: 395 | 356
+//      8 rows: 49, 48 | 56, 44;  12 rows: 49, 58 | 57, 56;  80 rows: 132, 132 | 149, 184;  96 rows: 147, 147 | 151, 186;  128 rows: 187, 191 | 198, 221
+//   down, 8 of 64, 1024 > 2048, half unevenly:  8 rows: 33 | 38;  64 rows: 67 | 90;  128 rows: 113 | 128;  160 rows: 137 | 146;  512 rows: 393 | 357
+// Which of the two a batch is, only the device knows: few large experts of some 100 rows, met evenly, would be 14% faster in tiles of 128; met
+// unevenly they are 13 to 16% faster as it is.
 int moe_tiles(int64_t n_pairs, int n_experts, bool gate_up)
 {
     const int64_t rows = n_pairs / n_experts;
@@ -1075,11 +1080,12 @@ int moe_tiles(int64_t n_pairs, int n_experts, bool gate_up)
 
 // The tiles, or 0, integer dots, where they would be tiles of 16 and rows and weights are so few that their time is less.  In us, of 304 CTAs side
 // by side, each a round of 8 super-blocks after the other; and of 152, by super-block, of the experts that are met if all
-// are as likely, after some 17 us for B's pieces, starts and ends.  Measured (dots | tiles of 16):
-//   gate and up, 2 of 8, 4096 > 14336:  1 row 86 | 71;  1.5 rows 126 | 88;  2 rows 165 | 97;   8 of 64, 2048 > 1024:  1 row 32 | 33;
+// are as likely, after some 17 us for B's pieces, starts and ends.  152 (and 304) are GB300's SMs: constants, as the queries of workspaces
+// make the same choice and ask no device.  Measured (dots | tiles of 16):
+//   gate and up, 2 of 8, 4096 > 14336:  1 row 86 | 70;  1.5 rows 126 | 88;  2 rows 165 | 97;   8 of 64, 2048 > 1024:  1 row 32 | 33;
 //   1.5 rows 46 | 38;  2 rows 59 | 38;   8 of 128, 2048 > 768:  1 row 46 | 42;  1.5 rows 67 | 51
-//   down, 2 of 8, 14336 > 4096:  1 row 46 | 45;  1.5 rows 66 | 56;  2 rows 83 | 56;   8 of 64, 1024 > 2048:  1 row 37 | 26;
-//   4 of 16, 4864 > 896:  1 row 12 | 22;  2 rows 18 | 25;  3 rows 26 | 25;   2 of 8, 512 > 1024:  2 rows 6 | 11;   1 of 4, 768 > 512:  3 rows 3 | 11
+//   down, 2 of 8, 14336 > 4096:  1 row 46 | 46;  1.5 rows 66 | 57;  2 rows 83 | 57;   8 of 64, 1024 > 2048:  1 row 37 | 27;
+//   4 of 16, 4864 > 896:  1 row 12 | 22;  2 rows 18 | 25;  3 rows 26 | 26;   2 of 8, 512 > 1024:  2 rows 6 | 11;   1 of 4, 768 > 512:  3 rows 3 | 11
 int moe_columns(int64_t n_pairs, int n_experts, int top_k, int64_t out_dim, int64_t in_dim, bool gate_up)
 {
     const int columns = moe_tiles(n_pairs, n_experts, gate_up);

@@ -259,3 +259,25 @@ def test_waits_that_run_out_before_other_outputs(rz, T, E, out_dim):
             for _ in range(2):
                 assert torch.equal(run(), want)
         assert rz.check_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("k", [1, 4, 8, 12, 16, 20])
+@pytest.mark.parametrize("n,E,out_dim", [(3, 8, 64)] + TILES)
+def test_small_blocks_beside_a_large_one(rz, n, E, out_dim, k):
+    """Block 0 of each super-block of x has a scale 2^k times the others', and meets weights of 0.  On the tensor cores a value of the others is off
+    by up to 2^(k - 24) of its block's largest: steps of 2^-24 where the largest scale is 1/2 .. 1."""
+    rng = np.random.default_rng(n + k)
+    in_dim, plan = 512, one_expert(rz, n, E, [0] + [n] * E)
+    w = q4k(rng, 1, out_dim, in_dim=in_dim)
+    w[..., 4] &= 0xc0
+    w[..., 8] &= 0xc0
+    q, d, _ = activations(rng, n, in_dim)
+    d[:] = rng.uniform(0.5, 1, d.shape) * 2.0 ** -k
+    d[:, ::8] = 1
+    s = (d * q.reshape(n, -1, 32).astype(np.float32).sum(-1)).astype(np.float32)
+    x, (wv, size) = R.q8_values(q, d), R.weights(w)
+    ref, tol = R.down((wv, size), x, np.arange(n), np.zeros(n, int), np.ones((n, 1)), None)
+    top = np.repeat(127 * d.astype(np.float64), 32, -1)  # of a block of 256 weights of 0 nothing counts
+    y = host(rz.moe_down(dev(np.repeat(w, E, 0)), dev(R.q8_buffer(q, d, s)), plan, out_dim, in_dim))
+    # the scale of a block may be half of 2^-k: once more
+    within(y, ref, tol + (0 if n == 3 else 2 * 1.02 * 2.0 ** (k - 24)) * (top @ size[0].T), "y")
